@@ -420,6 +420,173 @@ dartree_status dartree_accept(const int32_t *parent, const int32_t *token, const
                               int32_t *accept_len, int32_t *accept_nodes, int32_t *bonus,
                               void *stream);
 
+/* ------------------------------------------------------------------
+ * Paged key/value cache in 4 bits.  Context-free, asynchronous on `stream`,
+ * no allocation; errors are INVALID_ARG / UNSUPPORTED before any launch,
+ * dartree_last_error(NULL) has the text.  All arrays are device memory.
+ *
+ * A page holds page_tokens (16, 32, 64 or 128) consecutive tokens of one
+ * sequence, all key/value heads of one layer.  Per head it has one chunk of
+ * page_tokens * dh * 9 / 8 bytes (dh = 64 or 128):
+ *   key codes [page_tokens][dh/2], key scales [page_tokens][dh/16],
+ *   value codes [page_tokens][dh/2], value scales [page_tokens][dh/16].
+ * A code is e2m1 (0, .5, 1, 1.5, 2, 3, 4, 6 and the sign in bit 3), the even
+ * dimension in a byte's low half; a scale is an e4m3 byte for 16 dimensions.
+ * The value is code * scale * k_scale (v_scale for the values): exact in
+ * bf16 and in fp16 before k_scale.  k_scale and v_scale are powers of two
+ * from 2^-64 to 2^64 and move the scales' range (a block's largest magnitude
+ * should lie between 2^-6 and 2688 times it: larger ones saturate, smaller
+ * ones lose scale bits).
+ *
+ * pool [layers][pages] pages, 16-byte aligned; refs [pages] counts the table
+ * entries that hold a page (0 = free) and is the allocator's whole state: the
+ * free page with the lowest number is taken first.  refs may be NULL for
+ * append, read and attention.
+ *
+ * Sequences are rows of a page table [R][max_pages] (int32, token t of row r
+ * in page table[r][t / page_tokens]; a row's pages are its first entries,
+ * the rest is -1) with lens [R] tokens each.  A page that is held twice
+ * (dartree_cache_fork) is complete and is only read.
+ *
+ * err: optional device word; bad indices found on the device (a page number
+ * outside [0, pages), a token without a page, a row outside [0, R), ...) are
+ * skipped and OR 16 into it, a pipeline wait that ran out ORs 2. */
+typedef struct dartree_cache {
+  void *pool;
+  int32_t *refs;
+  int32_t layers, pages, page_tokens, Hkv, dh;
+  float k_scale, v_scale;
+} dartree_cache;
+
+/* Bytes of a page: Hkv * page_tokens * dh * 9 / 8 (0 for sizes outside the
+ * format's). */
+size_t dartree_cache_page_bytes(int32_t page_tokens, int32_t Hkv, int32_t dh);
+
+/* Quantises n tokens per request into layer `layer`: token i of request r
+ * goes to position lens[r] + offset + i.  K, V bf16 [R][n][Hkv][dh] with
+ * req_stride and token_stride elements between requests and tokens (multiples
+ * of 8, at least Hkv * dh for the tokens; K and V 16-byte aligned), so that
+ * slices of a fused projection's output are read in place.  count [R] (NULL:
+ * n for all): only the first count[r] tokens are written.  A row with
+ * lens[r] < 0 is skipped; lens is not changed.
+ * Per 16 dimensions: scale = e4m3(max|x| / 6), code = e2m1(x / scale), both
+ * to nearest even and saturating (x divided by k_scale or v_scale first);
+ * NaN counts as 0. */
+dartree_status dartree_cache_append(const dartree_cache *cache, int32_t layer, const void *K,
+                                    const void *V, int64_t req_stride, int64_t token_stride,
+                                    const int32_t *table, int32_t max_pages, const int32_t *lens,
+                                    int32_t offset, const int32_t *count, int32_t R, int32_t n,
+                                    int32_t *err, void *stream);
+
+/* The values of the tokens lens[r] + offset + i, i < min(n, count[r]), as
+ * bf16: K, V [R][n][Hkv][dh], dense, 16-byte aligned.  A token without a page
+ * reads as 0; tokens behind count[r] and rows with lens[r] < 0 are left as
+ * they were. */
+dartree_status dartree_cache_read(const dartree_cache *cache, int32_t layer, void *K, void *V,
+                                  const int32_t *table, int32_t max_pages, const int32_t *lens,
+                                  int32_t offset, const int32_t *count, int32_t R, int32_t n,
+                                  int32_t *err, void *stream);
+
+/* Attention of single tokens or draft trees over the cache, one layer:
+ *   Q    [R][B+1][Hq][dh] bf16, q_token_stride elements between the rows
+ *        (a multiple of 8, at least Hq * dh), requests (B+1) rows apart; row 0
+ *        is the root (the last verified token, at position lens[r] - 1), rows
+ *        1.. the tree nodes, node i at position lens[r] + i;
+ *   mask [R][B][ceil(B/32)] the build's ancestor mask (B > 0);
+ *   n_nodes [R] the trees' sizes (dartree_tree.n_out; NULL: B for all, or
+ *        with B = 0 nothing): rows behind them are left as they were;
+ *   max_len  an upper bound of lens[r] + n_nodes[r] (tokens behind it are
+ *        not read and flagged);
+ *   O    [R][B+1][Hq][dh] bf16, dense.
+ * Row 0 sees the lens[r] prefix tokens; node i the prefix and the nodes of
+ * its mask row.  Query head h reads key/value head h / (Hq / Hkv).
+ * O = softmax(scale * q.k) v; products and sums in fp32, the softmax weights
+ * in fp16 for the product with the values; O = 0 for a row that sees
+ * nothing.  Tokens without a page are not seen (and flagged).  A row with
+ * lens[r] < 0 is skipped.  B <= 1024, Hq % Hkv == 0; Q, O 16-byte aligned.
+ * work: dartree_cache_attention_workspace() bytes of scratch, 16-byte
+ * aligned, that overlapping calls must not share (its contents need no
+ * preparation; NULL when the size is 0). */
+dartree_status dartree_cache_attention(const dartree_cache *cache, int32_t layer, const void *Q,
+                                       int64_t q_token_stride, const uint32_t *mask,
+                                       const int32_t *n_nodes, const int32_t *table,
+                                       int32_t max_pages, const int32_t *lens, int32_t R, int32_t B,
+                                       int32_t max_len, int32_t Hq, float scale, void *O,
+                                       void *work, size_t work_bytes, int32_t *err, void *stream);
+size_t dartree_cache_attention_workspace(int32_t R, int32_t B, int32_t max_len, int32_t Hq,
+                                         int32_t Hkv, int32_t dh);
+
+/* Pages for want[r] more tokens per row: row r comes to hold at least
+ * ceil((lens[r] + want[r]) / page_tokens) pages; lens is not changed.  Rows
+ * are served in order; ok[r] = 0 for a row that needs more than max_pages or
+ * has lens[r] or want[r] < 0 (it gets none), and for the first row whose
+ * pages are not there and every later one that needs some.  R <= 4096. */
+dartree_status dartree_cache_reserve(const dartree_cache *cache, int32_t *table, int32_t max_pages,
+                                     const int32_t *lens, const int32_t *want, int32_t R,
+                                     int32_t *ok, void *stream);
+
+/* Continues sequences in several ways: for i < n, row dst[i] becomes a copy
+ * of row src[i].  Complete pages are shared; the last, partly filled page is
+ * copied in all layers, so that the page a row writes to is always its own.
+ * ok[i] = 0, and nothing done, when a row is outside [0, R), dst[i] holds
+ * pages, occurs earlier in dst or anywhere in src, lens[src[i]] < 0 or its
+ * pages are not there, or no free page is left (served in order, as
+ * dartree_cache_reserve).  n <= 1024. */
+dartree_status dartree_cache_fork(const dartree_cache *cache, int32_t *table, int32_t max_pages,
+                                  int32_t *lens, int32_t R, const int32_t *src, const int32_t *dst,
+                                  int32_t n, int32_t *ok, void *stream);
+
+/* After dartree_accept: the keys and values of the accepted tree nodes move,
+ * in all layers, to the end of the prefix -- node nodes[r][k] from position
+ * lens[r] + nodes[r][k] to lens[r] + k for k < m, m = min(len[r], max_len) --
+ * and lens[r] becomes lens[r] + m + extra (extra = 1 counts the bonus token,
+ * whose key and value the next step appends).  nodes, len as dartree_accept
+ * writes them (ranks rising in a row).  A row whose ranks do not rise, whose
+ * tokens have no page, or with lens[r] < 0 is left as it was (the former two
+ * are flagged). */
+dartree_status dartree_cache_commit(const dartree_cache *cache, const int32_t *table,
+                                    int32_t max_pages, int32_t *lens, const int32_t *nodes,
+                                    const int32_t *len, int32_t R, int32_t max_len, int32_t extra,
+                                    int32_t *err, void *stream);
+
+/* Rows rows[i], i < n, keep their first keep[i] tokens (0: the sequence
+ * ends): pages behind them are let go (free once no row holds them) and
+ * lens[rows[i]] = min(lens[rows[i]], keep[i]).  A row listed twice keeps the
+ * smaller number.  keep[i] < 0 and rows outside [0, R) are skipped. */
+dartree_status dartree_cache_release(const dartree_cache *cache, int32_t *table, int32_t max_pages,
+                                     int32_t *lens, int32_t R, const int32_t *rows,
+                                     const int32_t *keep, int32_t n, int32_t *err, void *stream);
+
+/* Copies the pages src[i] to dst[i], i < n, in all layers (table, lens and
+ * refs are the caller's).  A pair is skipped, and flagged, when a number is
+ * outside [0, pages), or dst[i] occurs earlier in dst or anywhere in src.
+ * n <= 65535. */
+dartree_status dartree_cache_copy_pages(const dartree_cache *cache, const int32_t *src,
+                                        const int32_t *dst, int32_t n, int32_t *err, void *stream);
+
+/* Tokens drawn from rows of logits with given random numbers -- the target's
+ * predictions that dartree_accept takes.
+ *   logits [rows][V], row_stride elements apart, fp32 or bf16 (`bf16`);
+ *   row i belongs to request i / rows_per_req, whose settings are
+ *   temperature, top_k, top_p, min_p [ceil(rows / rows_per_req)] (NULL: 1, 0,
+ *   1, 0 for all); u [rows] in [0, 1).
+ * The weights are w_i = exp((l_i - max) / temperature).  Tokens in order of
+ * (logit desc, index asc); kept are the first top_k (all if < 1), of those
+ * the ones with w_i >= min_p, and if top_p < 1 of those the fewest first
+ * whose weight is at least top_p of the whole's (one at least).  The token is
+ * the kept one with the lowest index whose running sum of weights (in index
+ * order) exceeds u times their total; prob its share of the total.
+ * temperature <= 0 (or NaN): the largest logit, lowest index.  NaN logits
+ * count as -inf; where +inf occur the tokens that have it share the weight;
+ * a row of -inf gives token -1, prob 0.
+ * The weights are rounded to multiples of 2^-44 of the largest and summed as
+ * integers, so a result does not depend on the order of the sums.
+ * V <= 2^18. */
+dartree_status dartree_sample(const void *logits, int32_t bf16, int64_t row_stride, int32_t V,
+                              int32_t rows, int32_t rows_per_req, const float *temperature,
+                              const int32_t *top_k, const float *top_p, const float *min_p,
+                              const float *u, int32_t *token, float *prob, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -53,6 +53,12 @@ class Tree(ctypes.Structure):
                 ("mask", _vp), ("n_out", _vp)]
 
 
+class Cache(ctypes.Structure):
+    _fields_ = [("pool", _vp), ("refs", _vp), ("layers", _i32), ("pages", _i32),
+                ("page_tokens", _i32), ("Hkv", _i32), ("dh", _i32),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
 class DartreeError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"dartree {STATUS.get(status, status)}: {msg}")
@@ -114,6 +120,25 @@ def load():
         "dartree_tree_attention_workspace": (ctypes.c_size_t, [_i32, _i32, _i32, _i32, _i32]),
         "dartree_accept": (st, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
     }
+    cache, i64 = ctypes.POINTER(Cache), ctypes.c_int64
+    sig.update({
+        "dartree_cache_page_bytes": (ctypes.c_size_t, [_i32, _i32, _i32]),
+        "dartree_cache_append": (st, [cache, _i32, _vp, _vp, i64, i64, _vp, _i32, _vp, _i32, _vp,
+                                      _i32, _i32, _vp, _vp]),
+        "dartree_cache_read": (st, [cache, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32,
+                                    _vp, _vp]),
+        "dartree_cache_attention": (st, [cache, _i32, _vp, i64, _vp, _vp, _vp, _i32, _vp, _i32,
+                                         _i32, _i32, _i32, ctypes.c_float, _vp, _vp,
+                                         ctypes.c_size_t, _vp, _vp]),
+        "dartree_cache_attention_workspace": (ctypes.c_size_t, [_i32] * 6),
+        "dartree_cache_reserve": (st, [cache, _vp, _i32, _vp, _vp, _i32, _vp, _vp]),
+        "dartree_cache_fork": (st, [cache, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp]),
+        "dartree_cache_commit": (st, [cache, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp]),
+        "dartree_cache_release": (st, [cache, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp]),
+        "dartree_cache_copy_pages": (st, [cache, _vp, _vp, _i32, _vp, _vp]),
+        "dartree_sample": (st, [_vp, _i32, i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                _vp, _vp]),
+    })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -469,3 +494,286 @@ def accept(parent, token, n_out, pred, *, max_len: int, stream=None) -> dict:
                                       max_len, _ptr(o["len"]), _ptr(o["nodes"]), _ptr(o["bonus"]),
                                       _stream(stream)))
     return o
+
+
+# ------------------------------------------------------- paged 4-bit cache
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def _ints(name: str, t: torch.Tensor, dev, shape) -> int:
+    """Address of a dense int32 tensor of that shape on that device."""
+    if t.dtype is not torch.int32 or t.device != dev or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 tensor on {dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _floats(name: str, t: torch.Tensor, dev, n: int) -> int:
+    if t.dtype is not torch.float32 or t.device != dev or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous fp32 tensor on {dev}")
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} entries, expected {n}")
+    return t.data_ptr()
+
+
+def _alloc(stream, shape, dtype, dev, zero: bool = False) -> torch.Tensor:
+    """A tensor whose memory belongs to the call's stream."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=dev)
+
+
+class _on:
+    """Runs a call with the tensors' device current and gives its stream."""
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream, self.back = dev, stream, None
+
+    def __enter__(self) -> int:
+        if torch.cuda.current_device() != self.dev.index:
+            self.back = torch.cuda.current_device()
+            torch.cuda.set_device(self.dev)
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.dev)
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+class KVCache:
+    """A paged key/value cache in 4 bits (dartree_cache): the pool of pages
+    and the pages' reference counts.  The sequences -- page tables [R,
+    max_pages] int32 (-1: no page) and lengths [R] int32 -- are the caller's
+    tensors.  ``pool`` (uint8 [layers, pages, page_bytes]) and ``refs`` (int32
+    [pages]) may be given; otherwise they are allocated, all pages free.
+    Bad indices found on the device gather in ``err`` until :meth:`check`."""
+
+    def __init__(self, layers: int, pages: int, *, page_tokens: int = 64, Hkv: int, dh: int,
+                 k_scale: float = 1.0, v_scale: float = 1.0, pool: torch.Tensor | None = None,
+                 refs: torch.Tensor | None = None, device="cuda"):
+        self._lib = load()
+        self.page_bytes = int(self._lib.dartree_cache_page_bytes(page_tokens, Hkv, dh))
+        if self.page_bytes == 0 or layers < 1 or pages < 1:
+            raise ValueError("page_tokens must be 16, 32, 64 or 128, dh 64 or 128, layers, pages "
+                             "and Hkv at least 1")
+        for s in (k_scale, v_scale):
+            if not (2.0 ** -64 <= s <= 2.0 ** 64 and np.frexp(s)[0] == 0.5):
+                raise ValueError("k_scale and v_scale must be powers of two from 2^-64 to 2^64")
+        if pool is None:
+            pool = torch.zeros(layers, pages, self.page_bytes, dtype=torch.uint8, device=device)
+        if not pool.is_cuda or pool.dtype is not torch.uint8 or not pool.is_contiguous():
+            raise TypeError("pool must be a contiguous uint8 CUDA tensor")
+        if pool.shape != (layers, pages, self.page_bytes):
+            raise ValueError(f"pool has shape {tuple(pool.shape)}, expected "
+                             f"{(layers, pages, self.page_bytes)}")
+        if refs is None:
+            refs = torch.zeros(pages, dtype=torch.int32, device=pool.device)
+        self.dev = pool.device
+        _ints("refs", refs, self.dev, (pages,))
+        self.pool, self.refs = pool, refs
+        self.layers, self.pages, self.page_tokens, self.Hkv, self.dh = (layers, pages, page_tokens,
+                                                                        Hkv, dh)
+        self.err = torch.zeros(1, dtype=torch.int32, device=self.dev)
+        self._c = Cache(pool.data_ptr(), refs.data_ptr(), layers, pages, page_tokens, Hkv, dh,
+                        k_scale, v_scale)
+        self._ref = ctypes.byref(self._c)
+        self._err = self.err.data_ptr()
+
+    def _seqs(self, table: torch.Tensor, lens: torch.Tensor):
+        if table.dim() != 2:
+            raise ValueError("table must be [R, max_pages]")
+        R, width = table.shape
+        return _ints("table", table, self.dev, (R, width)), width, \
+            _ints("lens", lens, self.dev, (R,)), R
+
+    def check(self) -> None:
+        """Synchronises and raises if a call since the last check met a bad
+        index (a token without a page, a row or page out of range)."""
+        e = int(self.err.item())
+        if e:
+            self.err.zero_()
+            raise DartreeError(5 if e & 2 else 4, f"cache: device check {e}")
+
+    def append(self, layer: int, K: torch.Tensor, V: torch.Tensor, table, lens, *, offset: int = 0,
+               count: torch.Tensor | None = None, stream=None) -> None:
+        """Quantise K, V [R, n, Hkv, dh] bf16 into positions lens[r] + offset
+        + i (dartree_cache_append); request and token strides are free, the
+        same in both."""
+        t, width, ln, R = self._seqs(table, lens)
+        for name, x in (("K", K), ("V", V)):
+            if x.dtype not in _BF16 or x.device != self.dev:
+                raise TypeError(f"{name} must be a bf16 tensor on {self.dev}")
+        n = K.shape[1]
+        if K.shape != (R, n, self.Hkv, self.dh) or V.shape != K.shape:
+            raise ValueError(f"K {tuple(K.shape)} / V {tuple(V.shape)} do not match R={R}, "
+                             f"Hkv={self.Hkv}, dh={self.dh}")
+        sr, sn, sh, sd = K.stride()
+        if V.stride() != K.stride() or (sd != 1 and self.dh > 1) or (sh != self.dh and self.Hkv > 1):
+            raise ValueError("K and V need equal strides, dense in heads and dims")
+        if n == 1:
+            sn = max(sn, self.Hkv * self.dh)
+        with _on(self.dev, stream) as st:
+            _check_free(self._lib.dartree_cache_append(
+                self._ref, layer, K.data_ptr(), V.data_ptr(), sr, sn, t, width, ln, offset,
+                None if count is None else _ints("count", count, self.dev, (R,)), R, n, self._err,
+                st))
+
+    def read(self, layer: int, table, lens, n: int, *, offset: int = 0,
+             count: torch.Tensor | None = None, out: tuple | None = None, stream=None) -> tuple:
+        """The values of the tokens lens[r] + offset + i, i < n, as bf16 (K,
+        V) [R, n, Hkv, dh] (dartree_cache_read).  Tokens behind count[r] keep
+        what ``out`` holds (zeros in a new one)."""
+        t, width, ln, R = self._seqs(table, lens)
+        shape = (R, n, self.Hkv, self.dh)
+        if out is None:
+            both = _alloc(stream, (2, *shape), torch.bfloat16, self.dev, count is not None)
+            out = (both[0], both[1])
+        for x in out:
+            if x.dtype not in _BF16 or x.device != self.dev or not x.is_contiguous():
+                raise TypeError(f"out must be contiguous bf16 tensors on {self.dev}")
+            if x.shape != shape:
+                raise ValueError(f"out has shape {tuple(x.shape)}, expected {shape}")
+        with _on(self.dev, stream) as st:
+            _check_free(self._lib.dartree_cache_read(
+                self._ref, layer, out[0].data_ptr(), out[1].data_ptr(), t, width, ln, offset,
+                None if count is None else _ints("count", count, self.dev, (R,)), R, n, self._err,
+                st))
+        return out
+
+    def attention(self, layer: int, Q: torch.Tensor, table, lens, *, max_len: int,
+                  mask: torch.Tensor | None = None, n_nodes: torch.Tensor | None = None,
+                  scale: float | None = None, out: torch.Tensor | None = None,
+                  work: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Attention of Q [R, B+1, Hq, dh] bf16 (row 0 the root, then the tree
+        nodes; B = 0: single tokens) over the cache (dartree_cache_attention)
+        -> O bf16 [R, B+1, Hq, dh].  ``max_len`` bounds lens[r] + n_nodes[r].
+        Rows behind n_nodes[r] keep what ``out`` holds (zeros in a new one)."""
+        t, width, ln, R = self._seqs(table, lens)
+        if Q.dtype not in _BF16 or Q.device != self.dev:
+            raise TypeError(f"Q must be a bf16 tensor on {self.dev}")
+        if Q.dim() != 4 or Q.shape[0] != R or Q.shape[1] < 1 or Q.shape[3] != self.dh:
+            raise ValueError(f"Q {tuple(Q.shape)} does not match R={R}, dh={self.dh}")
+        B, Hq = Q.shape[1] - 1, Q.shape[2]
+        if Hq % self.Hkv:
+            raise ValueError(f"{Hq} query heads are not a multiple of {self.Hkv}")
+        if Q.is_contiguous():
+            sq = Hq * self.dh
+        else:
+            sr, sq, sh, sd = Q.stride()
+            if B == 0:
+                sq = sr if R > 1 else max(sq, Hq * self.dh)
+            if (sr != (B + 1) * sq and R > 1) or sh != self.dh or sd != 1:
+                raise ValueError("Q needs one stride between rows, dense in heads and dims")
+        m = None
+        if B > 0:
+            if mask is None:
+                raise ValueError("a tree needs its mask")
+            m = _ints("mask", mask, self.dev, (R, B, (B + 31) // 32))
+        nn = None if n_nodes is None else _ints("n_nodes", n_nodes, self.dev, (R,))
+        if out is None:
+            out = _alloc(stream, (R, B + 1, Hq, self.dh), torch.bfloat16, self.dev,
+                         n_nodes is not None)
+        elif out.dtype not in _BF16 or out.device != self.dev or not out.is_contiguous():
+            raise TypeError(f"out must be a contiguous bf16 tensor on {self.dev}")
+        elif out.shape != (R, B + 1, Hq, self.dh):
+            raise ValueError(f"out has shape {tuple(out.shape)}")
+        need = self._lib.dartree_cache_attention_workspace(R, B, max_len, Hq, self.Hkv, self.dh)
+        if work is None and need:
+            work = _alloc(stream, (need,), torch.uint8, self.dev)
+        with _on(self.dev, stream) as st:
+            _check_free(self._lib.dartree_cache_attention(
+                self._ref, layer, Q.data_ptr(), sq, m, nn, t, width, ln, R, B, max_len, Hq,
+                float(scale) if scale is not None else self.dh ** -0.5, out.data_ptr(),
+                None if work is None else work.data_ptr(),
+                0 if work is None else work.numel() * work.element_size(), self._err, st))
+        return out
+
+    # ------------------------------------------------------ page operations
+    def reserve(self, table, lens, want, *, stream=None) -> torch.Tensor:
+        """Pages for want[r] more tokens per row -> ok [R] int32
+        (dartree_cache_reserve)."""
+        t, width, ln, R = self._seqs(table, lens)
+        w = _ints("want", want, self.dev, (R,))
+        ok = _alloc(stream, (R,), torch.int32, self.dev)
+        with _on(self.dev, stream) as st:
+            _check_free(self._lib.dartree_cache_reserve(self._ref, t, width, ln, w, R,
+                                                        ok.data_ptr(), st))
+        return ok
+
+    def fork(self, table, lens, src, dst, *, stream=None) -> torch.Tensor:
+        """Rows dst become copies of rows src -> ok [n] int32
+        (dartree_cache_fork)."""
+        t, width, ln, R = self._seqs(table, lens)
+        n = src.numel()
+        a, b = _ints("src", src, self.dev, (n,)), _ints("dst", dst, self.dev, (n,))
+        ok = _alloc(stream, (n,), torch.int32, self.dev)
+        with _on(self.dev, stream) as st:
+            _check_free(self._lib.dartree_cache_fork(self._ref, t, width, ln, R, a, b, n,
+                                                     ok.data_ptr(), st))
+        return ok
+
+    def commit(self, table, lens, nodes, length, *, extra: int = 0, stream=None) -> None:
+        """Moves the accepted nodes' tokens to the prefixes' ends and adds
+        length[r] + extra to lens (dartree_cache_commit); nodes [R, max_len]
+        and length [R] as :func:`accept` returns them."""
+        t, width, ln, R = self._seqs(table, lens)
+        if nodes.dim() != 2:
+            raise ValueError("nodes must be [R, max_len]")
+        most = nodes.shape[1]
+        a, b = _ints("nodes", nodes, self.dev, (R, most)), _ints("length", length, self.dev, (R,))
+        with _on(self.dev, stream) as st:
+            _check_free(self._lib.dartree_cache_commit(self._ref, t, width, ln, a, b, R, most,
+                                                       extra, self._err, st))
+
+    def release(self, table, lens, rows, keep, *, stream=None) -> None:
+        """Rows keep their first keep[i] tokens; pages behind them go back
+        (dartree_cache_release)."""
+        t, width, ln, R = self._seqs(table, lens)
+        n = rows.numel()
+        a, b = _ints("rows", rows, self.dev, (n,)), _ints("keep", keep, self.dev, (n,))
+        with _on(self.dev, stream) as st:
+            _check_free(self._lib.dartree_cache_release(self._ref, t, width, ln, R, a, b, n,
+                                                        self._err, st))
+
+    def copy_pages(self, src, dst, *, stream=None) -> None:
+        """Copies pages src[i] to dst[i] in all layers
+        (dartree_cache_copy_pages)."""
+        n = src.numel()
+        a, b = _ints("src", src, self.dev, (n,)), _ints("dst", dst, self.dev, (n,))
+        with _on(self.dev, stream) as st:
+            _check_free(self._lib.dartree_cache_copy_pages(self._ref, a, b, n, self._err, st))
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: torch.Tensor | None = None,
+           top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+           min_p: torch.Tensor | None = None, rows_per_req: int = 1, stream=None) -> dict:
+    """Tokens drawn from logits [rows, V] (fp32 or bf16) with the random
+    numbers u [rows] in [0, 1) (dartree_sample) -> {"token": int32 [rows],
+    "prob": fp32 [rows]}.  Row i uses entry i // rows_per_req of temperature,
+    top_p, min_p (fp32) and top_k (int32).  With rows_per_req = B + 1 the
+    tokens are :func:`accept`'s pred."""
+    if not logits.is_cuda or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits must be an fp32 or bf16 CUDA tensor")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [rows, V], dense in V")
+    rows, V = logits.shape
+    if rows < 1 or V < 1 or rows_per_req < 1:
+        raise ValueError("logits and rows_per_req must not be empty")
+    dev, n = logits.device, -(-rows // rows_per_req)
+    ptr = [None if t is None else
+           (_ints(name, t, dev, (n,)) if name == "top_k" else _floats(name, t, dev, n))
+           for name, t in (("temperature", temperature), ("top_k", top_k), ("top_p", top_p),
+                           ("min_p", min_p))]
+    up = _floats("u", u, dev, rows)
+    token = _alloc(stream, (rows,), torch.int32, dev)
+    prob = _alloc(stream, (rows,), torch.float32, dev)
+    with _on(dev, stream) as st:
+        _check_free(load().dartree_sample(
+            logits.data_ptr(), 1 if logits.dtype is torch.bfloat16 else 0,
+            logits.stride(0) if rows > 1 else max(V, logits.stride(0)), V, rows, rows_per_req,
+            *ptr, up, token.data_ptr(), prob.data_ptr(), st))
+    return {"token": token, "prob": prob}

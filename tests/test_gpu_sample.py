@@ -1,0 +1,192 @@
+"""Sampling on the GPU against the definition in 64 bits, row by row."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from speculative_decoding_draft_06_gb300 import dartree as dtl
+from tests import cache_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+
+def f32(x):
+    return torch.tensor(x, dtype=torch.float32, device="cuda")
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def check(logits, u, per, T, k, p, m):
+    """One call against the reference, every row.  prob is w / total rounded
+    to fp32 (2^-24), the weights being off by 2^-44 of the largest at most:
+    2^-25 of a weight above 2^-19; below, the difference is absolute."""
+    n = -(-len(u) // per)
+    got = dtl.sample(logits, torch.from_numpy(u).cuda(), rows_per_req=per, temperature=None if T is None else f32(T),
+                     top_k=None if k is None else i32(k), top_p=None if p is None else f32(p),
+                     min_p=None if m is None else f32(m))
+    tok, prob = got["token"].cpu().numpy(), got["prob"].cpu().numpy()
+    l = logits.float().cpu().numpy()
+    near = 0
+    f = lambda a, d, r: d if a is None else float(np.float32(a[r]))  # noqa: E731
+    for i in range(len(u)):
+        r = i // per
+        assert r < n
+        t, q, margin = ref.sample_row(l[i], f(T, 1.0, r), int(f(k, 0, r)), f(p, 1.0, r), f(m, 0.0, r), float(u[i]))
+        if margin < 2.0 ** -40:      # the border is where the value is: both sides' last bits decide
+            near += 1
+            continue
+        assert tok[i] == t, (i, tok[i], t, margin)
+        assert abs(prob[i] - q) <= 2.0 ** -23 * q + 2.0 ** -43, (i, prob[i], q)
+    assert near <= 0.02 * len(u) + 1
+    return tok, prob
+
+
+MIX = [("full", None, None, None, None), ("temperature", [0.3], None, None, None), ("hot", [50.0], None, [0.9], None),
+       ("k1", None, [1], None, None), ("k7", [0.8], [7], None, None), ("k1000", [1.0], [1000], [0.99], None),
+       ("p", [0.7], None, [0.9], None), ("p small", None, None, [1e-6], None), ("p0", None, None, [0.0], None),
+       ("m", [1.0], None, None, [0.05]), ("m1", None, None, None, [1.0]), ("all", [0.9], [50], [0.95], [0.02]),
+       ("m p", [1.2], None, [0.8], [0.01]), ("greedy", [0.0], [5], [0.5], None), ("huge k", None, [10 ** 9], [1.0], [0.0]),
+       ("negative", None, [-3], [2.0], [-1.0])]
+
+
+@pytest.mark.parametrize("V", [1, 2, 31, 1000, 4097, 32000, 151936])
+@pytest.mark.parametrize("mix", range(len(MIX)))
+def test_every_setting(V, mix):
+    """fp32 and bf16 logits of a vocabulary's usual shape, padding masked."""
+    _, T, k, p, m = MIX[mix]
+    g = np.random.default_rng(V + mix)
+    rows = 5 if V > 5000 else 24
+    x = g.standard_normal((rows, V)) * 2 - 1.1 * np.log(1 + g.permutation(V))[None] + 15
+    if V > 30:
+        x[:, -V // 50:] = -np.inf
+        x[1, g.random(V) < 0.99] = -np.inf
+    u = g.random(rows).astype(np.float32)
+    for dt in (torch.float32, torch.bfloat16):
+        check(torch.from_numpy(x).to(dt).cuda(), u, rows, T, k, p, m)
+
+
+def test_settings_of_each_request_and_strides():
+    g = np.random.default_rng(3)
+    R, per, V = 9, 13, 5000
+    x = torch.from_numpy(g.standard_normal((R * per - 4, V + 3)) * 3).float().cuda()[:, 1:V + 1]
+    assert x.stride(0) == V + 3
+    u = g.random(R * per - 4).astype(np.float32)       # (the last request has fewer rows)
+    check(x, u, per, g.choice([0.0, 0.5, 1.0, 2.0], R), g.choice([0, 1, 10, 300], R), g.choice([1.0, 0.9, 0.3], R),
+          g.choice([0.0, 0.1], R))
+    check(x[:, :777], u, 1, g.choice([0.0, 0.5, 1.0, 2.0], len(u)), None, g.choice([1.0, 0.9, 0.3], len(u)), None)
+
+
+@pytest.mark.parametrize("V", [7, 3000, 100000])
+def test_ties(V):
+    """Equal logits: the order is the index's; large classes of equal keys."""
+    g = np.random.default_rng(V)
+    for levels in (1, 2, 5):
+        x = g.integers(0, levels, (6, V)).astype(np.float32)
+        u = g.random(6).astype(np.float32)
+        for k, p in ((None, None), ([V // 2 + 1], None), (None, [0.37]), ([V - 1], [0.61]), ([1], None)):
+            check(torch.from_numpy(x).cuda(), u, 6, None, k, p, None)
+
+
+def test_exact_borders():
+    """Equal weights make the borders whole numbers: u and top_p that fall on
+    them are decided by 'exceeds u' and 'at least top_p'."""
+    V = 8
+    x = torch.zeros(9, V, device="cuda")
+    u = np.array([i / 8 for i in range(8)] + [np.nextafter(np.float32(1), np.float32(0))], np.float32)
+    tok = dtl.sample(x, torch.from_numpy(u).cuda())["token"].cpu().tolist()
+    assert tok == [0, 1, 2, 3, 4, 5, 6, 7, 7]
+    for p, n in ((0.125, 1), (0.25, 2), (0.5, 4), (0.5000001, 5), (0.875, 7)):
+        last = dtl.sample(x, torch.full((9,), 0.99999, device="cuda"), rows_per_req=9, top_p=f32([p]))
+        assert last["token"].cpu().tolist() == [n - 1] * 9
+        assert np.allclose(last["prob"].cpu().numpy(), 1 / n, rtol=2.0 ** -23)
+    # u outside [0, 1)
+    odd = dtl.sample(x[:4], f32([1.0, -0.5, 7.0, float("nan")]))["token"].cpu().tolist()
+    assert odd == [7, 0, 7, 0]
+
+
+def test_infinities_nan_and_empty_rows():
+    inf, nan = float("inf"), float("nan")
+    x = torch.zeros(8, 100, device="cuda")
+    x[0] = -inf
+    x[1] = nan
+    x[2] = nan
+    x[2, 40] = -5.0
+    x[3, 10], x[3, 20] = inf, inf
+    x[4] = -inf
+    x[4, 99] = -3.4e38
+    x[5] = -3.4028234663852886e38
+    x[5, 7] = 3.4028234663852886e38
+    x[6, ::2] = nan
+    x[7, 50] = inf
+    for T in (1.0, 0.0, 0.01, inf):
+        for p in (None, f32([0.9])):
+            out = dtl.sample(x, torch.full((8,), 0.75, device="cuda"), rows_per_req=8, temperature=f32([T]), top_p=p)
+            tok, prob = out["token"].cpu().tolist(), out["prob"].cpu().tolist()
+            assert tok[0] == tok[1] == -1 and prob[0] == prob[1] == 0.0
+            assert tok[2] == 40 and prob[2] == 1.0
+            assert tok[3] == (10 if T == 0.0 else 20)
+            assert tok[4] == 99 and prob[4] == 1.0
+            assert tok[5] == 7 or T == inf
+            assert tok[6] % 2 == 1 if T != 0.0 else tok[6] == 1
+            assert tok[7] == 50
+
+
+def test_results_do_not_depend_on_the_launch():
+    """A row alone, among few and among many rows (other cluster sizes), and
+    in a replayed graph: the same tokens and probabilities, bit for bit."""
+    g = np.random.default_rng(9)
+    x = torch.from_numpy(g.standard_normal((400, 20000)) * 2).float().cuda()
+    u = torch.from_numpy(g.random(400).astype(np.float32)).cuda()
+    kw = dict(rows_per_req=400, temperature=f32([0.9]), top_k=i32([3000]), top_p=f32([0.97]))
+    many = dtl.sample(x, u, **kw)
+    for n in (1, 20, 100):
+        few = dtl.sample(x[:n], u[:n], **kw)
+        assert torch.equal(few["token"], many["token"][:n]) and torch.equal(few["prob"], many["prob"][:n])
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = dtl.sample(x, u, **kw)
+    u.copy_(torch.flip(u, [0]))
+    gr.replay()
+    again = dtl.sample(x, u, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(out["token"], again["token"])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = dtl.sample(x, u, stream=s, **kw)
+    s.synchronize()
+    assert torch.equal(other["token"], again["token"])
+
+
+def test_draws_follow_the_distribution():
+    """40000 draws of one row: each kept token's count within 6 standard
+    deviations of its share, none of the others."""
+    g = np.random.default_rng(1)
+    l = g.standard_normal(50).astype(np.float32) * 2
+    n = 40000
+    x = torch.from_numpy(l).cuda().expand(n, 50).contiguous()
+    u = torch.from_numpy(g.random(n).astype(np.float32)).cuda()
+    tok = dtl.sample(x, u, rows_per_req=n, top_k=i32([12]))["token"].cpu().numpy()
+    w = np.exp(l.astype(np.float64))
+    w[np.argsort(-l)[12:]] = 0
+    w /= w.sum()
+    cnt = np.bincount(tok, minlength=50)
+    assert (np.abs(cnt - n * w) <= 6 * np.sqrt(n * w * (1 - w)) + 1e-9).all()
+
+
+def test_binding_refuses_bad_tensors():
+    x, u = torch.zeros(4, 10, device="cuda"), torch.zeros(4, device="cuda")
+    for bad in (x.half(), x.cpu()):
+        with pytest.raises(TypeError):
+            dtl.sample(bad, u)
+    with pytest.raises(ValueError):
+        dtl.sample(x.t().contiguous().t(), u)
+    with pytest.raises(ValueError):
+        dtl.sample(x, u[:3])
+    with pytest.raises(ValueError):
+        dtl.sample(x, u, rows_per_req=2, temperature=f32([1.0]))
+    with pytest.raises(TypeError):
+        dtl.sample(x, u, top_k=f32([1.0] * 4))
