@@ -1,10 +1,9 @@
 // Tokens drawn from rows of logits (dartree_sample).
 //
-// A row is the work of one thread-block cluster: CTA k, warp w reads the
-// (16 k + w)-th contiguous share of the vocabulary.  Every cut (top-k,
-// min-p, top-p) keeps a prefix of the order (logit desc, index asc), so the
-// kept tokens are those whose 50-bit key (ordered logit, inverted index) is
-// at least one threshold.
+// A row is the work of one thread-block cluster (one CTA where there are
+// many rows).  Every cut (top-k, min-p, top-p) keeps a prefix of the order
+// (logit desc, index asc), so the kept tokens are those whose 50-bit key
+// (ordered logit, inverted index) is at least one threshold.
 //
 // The weights w = 2^((l - max) log2(e) / T) are integers in units of 2^-44
 // (weight44): sums of them are exact whatever their order, so the shared
@@ -13,13 +12,22 @@
 // of 150 000 tokens has as many borders, and a running sum that is off by
 // 2^-20 of the total moves the draw over one of them every few rows.
 //
-// 1. the largest key (max, arg max);
-// 2. with top-k or top-p: a histogram of counts and masses over 1536 bins of
-//    -log2 w (1/32 each, monotone in the logit); the bin in which the cut
-//    falls is gathered (refined by digits of the key while it holds more
-//    than kList), sorted, and the cut element found in it;
-// 3. the kept tokens' sums per warp, the warp in which u Z falls, and in
-//    that warp the token.
+// Most rows are decided by about a thousand candidates (from_list):
+// 1. a sample of the row gives a bound that about that many tokens reach;
+// 2. one pass over the row notes the 16-byte units that hold such tokens and
+//    sums the weights of all others in fp32, with a bound of the sum's error;
+// 3. the candidates go to a list in shared memory; the cuts and the draw are
+//    made on it in integers.  The rest of the row only enters top-p's total:
+//    the row is decided if the crossing is the same at both ends of the
+//    total's interval.
+// A row that this does not decide (no cuts, a kept set beyond the list, a
+// border inside the interval, infinities, NaN) takes further passes over the
+// row itself, all in integers (whole_row).
+//
+// A cut: a histogram of counts and masses over 1024 classes of -log2 w
+// (monotone in the logit) gives the class in which it falls; the class is
+// gathered (refined by digits of the key while it is large), sorted, and the
+// cut's token found in it.
 #include <cuda_bf16.h>
 
 #include "block.cuh"
@@ -28,11 +36,14 @@
 namespace dt {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 1536;        // 48 powers of two, 32 bins each
-constexpr float kBinsPer2 = 32.f;
-constexpr int kList = 2048;
+constexpr int kBins = 1024;
+constexpr float kBinsPer2 = 20.f;    // classes per power of two
+constexpr int kList = 3072;          // candidates
+constexpr float kWant = 2000.f;      // candidates aimed at
+constexpr int kClass = 1024;         // members of a class that are sorted
+constexpr int kUnits = 4096;         // 16-byte units of a CTA that may hold candidates
 constexpr int kMaxCl = 8;
 constexpr int kIdxBits = 18;
 constexpr float kZeroBelow = -46.f;  // 2^-46 rounds to 0 in units of 2^-44
@@ -77,21 +88,39 @@ struct Ctl {             // the leader's decisions, read by the whole cluster
   unsigned long long prefix, mask;  // class within the bin
   unsigned long long keep;          // threshold key
   unsigned long long left, total;   // draw: mass before the token in the warp's share, whole mass
-  int bin;
+  float top;                        // the row's largest logit
+  int bin, last;
   int refine;            // 1: another digit, 0: gather
   int warp;              // draw: the warp (of the cluster)
+  int done;              // the list decided the row
+};
+
+struct Part {            // a CTA's share of the pass, for the leader
+  float top, sum, off;
+  int lost;              // more units than kUnits
 };
 
 struct Smem {
   float2 exp[1 << kExpBits];
-  unsigned long long mass[kBins];
+  unsigned mass_lo[kBins], mass_hi[kBins];
   unsigned count[kBins];
   unsigned long long list[kList];
-  unsigned long long wsum[kMaxCl * kWarps];
-  unsigned long long best[kMaxCl];
+  union {
+    unsigned long long cls[kClass];
+    uint16_t unit[kUnits];
+  };
+  unsigned long long wsum[kMaxCl * kWarps], wtot[kMaxCl * kWarps];
   unsigned long long scan_m[kWarps];
   unsigned scan_c[kWarps];
-  unsigned list_n;
+  float wmax[kWarps], wval[kWarps];
+  __align__(16) float sample[kThreads];
+  float2 bounds[kMaxCl];
+  float sbound, smax;
+  Part part[kMaxCl];
+  unsigned list_n, units_n, cls_n;
+  int picked;
+  unsigned picked_n, picked_c;
+  unsigned long long picked_m;
   Ctl ctl;
 };
 
@@ -132,26 +161,37 @@ struct Weights {
     float e = fmaf(s, ch, -p);
     e = fmaf(s, cl, e);
     e = fmaf(err, ch, e);
-    const float n = rintf(p * 1024.f);    // p = (n + f) / 1024, |f| <= 1/2, exact
-    const float t = fmaf(n, -1.f / 1024.f, p);
-    const int ni = static_cast<int>(n);
-    const float2 T = exp[ni & 1023];
-    const int sh = 44 + (ni >> 10);       // the integer part, up to the table's
+    // n = the nearest multiple of 1/1024 to p, by adding 1.5 2^13 (ulp 2^-10)
+    const float big = p + 12288.f;
+    const float t0 = p - (big - 12288.f);  // exact, |t0| <= 2^-11
+    const float t = t0 + e;
+    e -= t - t0;                          // t + e unchanged, |e| < 2^-35
+    const int n = __float_as_int(big) - __float_as_int(12288.f);  // 1024 n
+    const float2 T = exp[n & 1023];
     constexpr float kL1 = 0.693147182464599609375f;  // ln 2 = kL1 + kL1lo
     constexpr float kL1lo = -1.904654299957768e-9f;
     const float a = t * kL1;
     float b = fmaf(t, kL1, -a);
     b = fmaf(t, kL1lo, b);
-    b = fmaf(e * kL1, fmaf(t, kL1, 1.f), b);  // 2^(t+e) - 2^t
-    b = fmaf(t * t, fmaf(t, 0.05550410866f, 0.24022650696f), b);  // 2^t - 1 = a + b
-    const float m = T.x * a;
+    b = fmaf(e, kL1, b);
+    b = fmaf(t * t, fmaf(t, 0.05550410866f, 0.24022650696f), b);  // 2^(t+e) - 1 = a + b
+    const float m = T.x * a;              // |m| < 2^-10
     float lo = fmaf(T.x, a, -m);
     lo = fmaf(T.x, b, lo);
     lo = fmaf(T.y, a, lo);
-    lo += T.y;                            // T (1 + a + b) = T.x + m + lo
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);  // 2^sh, sh >= -2
-    const long long w = __float2ll_rn(T.x * up) + __float2ll_rn(m * up) + __float2ll_rn(lo * up);
-    return w > 0 ? static_cast<unsigned long long>(w) : 0ull;
+    lo += T.y;                            // T (1 + a + b) = T.x + m + lo, |lo| < 2^-22
+    // in units of 2^-45: T.x's mantissa, m in multiples of 2^-32 (the low bits
+    // of m + 1.5 2^-9, whose ulp that is), what m has left and lo (ulp 2^-44
+    // at 1.5 2^-21)
+    constexpr float kC1 = 1.5f / 512.f, kC2 = 1.5f / 2097152.f;
+    const float m1 = m + kC1;
+    const float rest = (m - (m1 - kC1)) + lo;
+    const float m2 = rest + kC2;
+    const int i1 = __float_as_int(m1) - __float_as_int(kC1), i2 = __float_as_int(m2) - __float_as_int(kC2);
+    const long long w45 = (static_cast<long long>((__float_as_int(T.x) & 0x7FFFFF) | 0x800000) << 22) +
+                          (static_cast<long long>(i1) << 13) + 2 * i2;
+    const int down = 1 - (n >> 10);       // 1 .. 47
+    return static_cast<unsigned long long>((w45 + (1ll << (down - 1))) >> down);
   }
 };
 
@@ -209,304 +249,576 @@ __device__ __forceinline__ unsigned long long ceil_share(float p, unsigned long 
   return c > 0ull ? c : 1ull;
 }
 
+
+// A row in 16-byte units: `head` logits before the first aligned address,
+// `units` units, the rest behind them.  Warp w of the cluster's n has the
+// units [w share, (w + 1) share), warp 0 the head too and warp n - 1 the
+// rest: the shares follow the index order.
 template <typename E>
-__global__ void __launch_bounds__(kThreads) k_sample(const SampleParams p) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  Smem& sm = *reinterpret_cast<Smem*>(raw);
-  unsigned cl_u, rank_u;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(cl_u));
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank_u));
-  const int cl = static_cast<int>(cl_u), rank = static_cast<int>(rank_u);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int row = blockIdx.x / cl, req = row / p.rows_per_req;
-  const E* src = static_cast<const E*>(p.logits) + static_cast<size_t>(row) * p.row_stride;
-  const bool lead = rank == 0;
-  Smem& ls = *at_rank(&sm, 0);  // the leader's
-
-  const int share = (p.V + cl * kWarps - 1) / (cl * kWarps);
-  const int begin = min(p.V, (rank * kWarps + warp) * share), end = min(p.V, begin + share);
-
-  // ---- 1. the largest key
-  unsigned long long best = 0;
-  for (int i = begin + lane; i < end; i += 32) {
-    const unsigned long long k = key50(logit<E>(src, i), i);
-    best = k > best ? k : best;
+struct Row {
+  static constexpr int kPer = 16 / static_cast<int>(sizeof(E));
+  const E* src;
+  int V, head, units;
+  __device__ __forceinline__ Row(const E* p, int v) : src(p), V(v) {
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
+    head = off == 0 ? 0 : (16 - off) / static_cast<int>(sizeof(E));
+    head = head < v ? head : v;
+    units = (v - head) / kPer;
   }
+  __device__ __forceinline__ uint4 load(int u) const {
+    return __ldg(reinterpret_cast<const uint4*>(src + head) + u);
+  }
+  __device__ __forceinline__ int index(int u) const { return head + u * kPer; }
+};
+
+template <typename E>
+__device__ __forceinline__ void unpack(uint4 v, float (&x)[16 / sizeof(E)]);
+template <>
+__device__ __forceinline__ void unpack<float>(uint4 v, float (&x)[4]) {
+  x[0] = __uint_as_float(v.x);
+  x[1] = __uint_as_float(v.y);
+  x[2] = __uint_as_float(v.z);
+  x[3] = __uint_as_float(v.w);
+}
+template <>
+__device__ __forceinline__ void unpack<uint16_t>(uint4 v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long y = __shfl_xor_sync(kFullMask, best, o);
-    best = y > best ? y : best;
+  for (int k = 0; k < 4; ++k) {
+    x[2 * k] = __uint_as_float(w[k] << 16);
+    x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
   }
-  if (lane == 0) sm.scan_m[warp] = best;
-  for (int i = tid; i < (1 << kExpBits); i += kThreads) sm.exp[i] = make_float2(g_exp.hi[i], g_exp.lo[i]);
-  for (int i = tid; i < kBins; i += kThreads) {
-    sm.mass[i] = 0;
+}
+
+// The largest of a unit's logits (fmaxf drops NaN; all NaN: NaN, which no
+// comparison takes).
+template <int N>
+__device__ __forceinline__ float max_of(const float (&x)[N]) {
+  float m = x[0];
+#pragma unroll
+  for (int k = 1; k < N; ++k) m = fmaxf(m, x[k]);
+  return m;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// What the cuts work on.  LIST: the leader's list of candidates, by the
+// leader's block alone; otherwise the whole row, by the cluster.
+template <bool LIST, typename E>
+struct Source {
+  Smem& sm;
+  Smem& ls;
+  Row<E> row;
+  int ub, ue;      // the warp's units (row)
+  int first, last; // 1: the warp has the head, the rest
+  int n;           // list entries
+  int cl;
+  bool lead;
+  int gw, share;   // the warp in the cluster, units per warp (row)
+  using Elem = E;
+  __device__ __forceinline__ void sync() const {
+    if constexpr (LIST) __syncthreads();
+    else cluster_sync();
+  }
+  // f(logit, index) for the row's logits above -inf, in no particular order
+  template <typename F>
+  __device__ __forceinline__ void each_value(F f) const {
+    const int lane = threadIdx.x & 31;
+    auto one = [&](float x, int i) {
+      if (x > -INFINITY) f(x, i);  // (not NaN either)
+    };
+    if (first && lane < row.head) one(logit<E>(row.src, lane), lane);
+    const int rest = row.index(row.units);
+    if (last && lane < row.V - rest) one(logit<E>(row.src, rest + lane), rest + lane);
+    uint4 next = ub + lane < ue ? row.load(ub + lane) : make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int u = ub + lane; u < ue; u += 32) {
+      const uint4 v = next;
+      if (u + 32 < ue) next = row.load(u + 32);
+      float x[Row<E>::kPer];
+      unpack<E>(v, x);
+#pragma unroll
+      for (int k = 0; k < Row<E>::kPer; ++k) one(x[k], row.index(u) + k);
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {  // f(logit, key)
+    if constexpr (LIST) {
+      for (int i = threadIdx.x; i < n; i += kThreads) {
+        const unsigned long long k = sm.list[i];
+        f(key50_value(k), k);
+      }
+    } else {
+      each_value([&](float x, int i) { f(x, key50(x, i)); });
+    }
+  }
+  // class b's sums over the cluster (leader)
+  __device__ __forceinline__ void sums(int b, unsigned* c, unsigned long long* m) const {
+    *c = 0;
+    *m = 0;
+    for (int q = 0; q < (LIST ? 1 : cl); ++q) {
+      const Smem* o = LIST ? &sm : at_rank(&sm, q);
+      *c += o->count[b];
+      *m += (static_cast<unsigned long long>(o->mass_hi[b]) << 32) + o->mass_lo[b];
+    }
+  }
+};
+
+// A 64-bit sum in shared memory from two 32-bit atomics (shared memory has
+// no 64-bit add): the low word's add that wraps carries.
+__device__ __forceinline__ void add_mass(Smem& sm, int b, unsigned long long w) {
+  const unsigned lo = static_cast<unsigned>(w);
+  const unsigned old = atomicAdd(&sm.mass_lo[b], lo);
+  const unsigned hi = static_cast<unsigned>(w >> 32) + (old + lo < old ? 1u : 0u);
+  if (hi) atomicAdd(&sm.mass_hi[b], hi);
+}
+
+__device__ __forceinline__ void clear_classes(Smem& sm) {
+  for (int i = threadIdx.x; i < kBins; i += kThreads) {
+    sm.mass_lo[i] = 0;
+    sm.mass_hi[i] = 0;
     sm.count[i] = 0;
   }
-  if (tid == 0) sm.list_n = 0;
+}
+
+// Among the classes (ascending class = descending order) finds the one in
+// which the running count or mass reaches `target`; the leader's block.
+// c_before, m_before: what lies before the first class, then before the one
+// found.  Returns the class; *members: its count.
+template <typename S>
+__device__ __forceinline__ int pick_class(const S& s, bool by_count, unsigned long long target, unsigned& c_before,
+                                          unsigned long long& m_before, unsigned* members) {
+  constexpr int kPer = kBins / kThreads;
+  Smem& sm = s.sm;
+  unsigned cs[kPer], c = 0;
+  unsigned long long ms[kPer], m = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    s.sums(threadIdx.x * kPer + j, &cs[j], &ms[j]);
+    c += cs[j];
+    m += ms[j];
+  }
+  unsigned bc = c_before - c;
+  unsigned long long bm = m_before - m;
+  block_scan(sm, c, m);
+  bc += c;
+  bm += m;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    if (by_count ? (bc < target && target <= bc + cs[j]) : (bm < target && target <= bm + ms[j])) {
+      sm.picked = threadIdx.x * kPer + j;
+      sm.picked_n = cs[j];
+      sm.picked_c = bc;
+      sm.picked_m = bm;
+    }
+    bc += cs[j];
+    bm += ms[j];
+  }
   __syncthreads();
-  if (warp == 0) {
-    best = lane < kWarps ? sm.scan_m[lane] : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long y = __shfl_xor_sync(kFullMask, best, o);
-      best = y > best ? y : best;
-    }
-    if (lane < cl) at_rank(&sm, lane)->best[rank] = best;
-  }
-  cluster_sync();
-  best = sm.best[0];
-  for (int k = 1; k < cl; ++k) best = sm.best[k] > best ? sm.best[k] : best;
-  const float top = key50_value(best);
-  const float T = p.temperature ? p.temperature[req] : 1.f;
-  const bool greedy = !(T > 0.f);
-  if (top == -INFINITY || greedy) {  // (the same in the whole cluster)
-    if (lead && tid == 0) {
-      const bool none = top == -INFINITY;
-      p.token[row] = none ? -1 : (1 << kIdxBits) - 1 - static_cast<int>(best & ((1u << kIdxBits) - 1));
-      p.prob[row] = none ? 0.f : 1.f;
-    }
-    return;  // (no CTA reads another's memory after the barrier above)
-  }
-  const double c2 = 1.4426950408889634074 / static_cast<double>(T);
-  Weights wt;
-  wt.top = top;
-  wt.ch = static_cast<float>(c2);
-  wt.cl = isinf(wt.ch) ? 0.f : static_cast<float>(c2 - static_cast<double>(wt.ch));
-  wt.exp = sm.exp;
-  const int k = p.top_k ? p.top_k[req] : 0;
-  const float tp = p.top_p ? p.top_p[req] : 1.f;
-  const float mp = p.min_p ? fminf(p.min_p[req], 1.f) : 0.f;
-  const bool use_k = k >= 1 && k < p.V, use_p = tp < 1.f;
-  unsigned long long keep = 0;  // threshold key so far
+  c_before = sm.picked_c;
+  m_before = sm.picked_m;
+  *members = sm.picked_n;
+  const int k = sm.picked;
+  __syncthreads();
+  return k;
+}
 
-  // ---- 2. the cuts
-  if (mp > 0.f) {
-    // the smallest ordered logit whose weight is at least min_p: 32 probes a
-    // round (every warp finds the same)
-    const unsigned long long need = static_cast<unsigned long long>(ceil(ldexp(static_cast<double>(mp), 44)));
-    unsigned lo = 0, hi = float_order(top);  // the answer lies in (lo, hi]
-    while (hi - lo > 1) {
-      const unsigned step = (hi - lo + 31) / 32;
-      const unsigned long long at = static_cast<unsigned long long>(lo) + static_cast<unsigned long long>(lane + 1) * step;
-      const bool in = at >= hi || wt.weight44(order_float(static_cast<unsigned>(at))) >= need;
-      const int f = __ffs(__ballot_sync(kFullMask, in)) - 1;  // (the last probe is at or behind hi)
-      const unsigned long long nhi = static_cast<unsigned long long>(lo) + static_cast<unsigned long long>(f + 1) * step;
-      lo += static_cast<unsigned>(f) * step;
-      hi = nhi < hi ? static_cast<unsigned>(nhi) : hi;
+// The classes of the cuts: -log2 w in steps of 1 / kBinsPer2.
+__device__ __forceinline__ int bin_of(const Weights& wt, float x) {
+  return min(kBins - 1, static_cast<int>(wt.log2w(x) * -kBinsPer2));
+}
+
+// The element at which the running count (by_count) or mass in the order
+// reaches `target`: its key becomes `keep`; the mass up to and with it is
+// left in the leader's *upto.  The bins' sums are in place.  All threads of
+// the source call it.
+template <typename S>
+__device__ void cut(const S& s, const Weights& wt, bool by_count, unsigned long long target,
+                    unsigned long long& keep, unsigned long long* upto) {
+  Smem& sm = s.sm;
+  Ctl& ctl = s.ls.ctl;
+  unsigned c_before = 0, members = 0;
+  unsigned long long m_before = 0;
+  if (s.lead) {
+    const int b = pick_class(s, by_count, target, c_before, m_before, &members);
+    if (threadIdx.x == 0) {
+      ctl.bin = b;
+      ctl.prefix = ctl.mask = 0;
+      ctl.refine = members > kClass;
     }
-    keep = static_cast<unsigned long long>(hi) << kIdxBits;
   }
-  if (use_k || use_p) {
-    auto bin_of = [&](float x) { return min(kBins - 1, static_cast<int>(wt.log2w(x) * -kBinsPer2)); };
-    for (int i = begin + lane; i < end; i += 32) {
-      const float x = logit<E>(src, i);
-      if (key50(x, i) < keep) continue;
+  s.sync();
+  // a class too large to be gathered: by digits of its keys, 10 bits each
+  for (int shift = 40; ctl.refine; shift -= 10) {
+    const int bin = ctl.bin;
+    const unsigned long long pre = ctl.prefix, msk = ctl.mask;
+    clear_classes(sm);
+    __syncthreads();
+    s.each([&](float x, unsigned long long key) {
+      if (key < keep || (key & msk) != pre || bin_of(wt, x) != bin) return;
       const unsigned long long w = wt.weight44(x);
-      if (w == 0) continue;
-      const int b = bin_of(x);
-      atomicAdd(&sm.count[b], 1u);
-      atomicAdd(&sm.mass[b], w);
-    }
-    cluster_sync();
-    // the leader keeps the bins' sums of the whole row
-    constexpr int kPer = kBins / kThreads;
-    unsigned row_c[kPer];
-    unsigned long long row_m[kPer];
-    if (lead) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        row_c[j] = 0;
-        row_m[j] = 0;
-        for (int q = 0; q < cl; ++q) {
-          const Smem* o = at_rank(&sm, q);
-          row_c[j] += o->count[tid * kPer + j];
-          row_m[j] += o->mass[tid * kPer + j];
-        }
+      if (w == 0) return;
+      const int d = 1023 - static_cast<int>((key >> shift) & 1023);
+      atomicAdd(&sm.count[d], 1u);
+      add_mass(sm, d, w);
+    });
+    s.sync();
+    if (s.lead) {
+      const int d = pick_class(s, by_count, target, c_before, m_before, &members);
+      if (threadIdx.x == 0) {
+        ctl.prefix |= static_cast<unsigned long long>(1023 - d) << shift;
+        ctl.mask |= 1023ull << shift;
+        ctl.refine = members > kClass;
       }
     }
-    unsigned long long Z = 0;  // mass of what is kept so far (leader)
-    // find the element at which the running count (by_count) or mass reaches
-    // `target`; what lies before it counts.  All CTAs call it together; on
-    // return sm.ctl.keep of the leader is its key, and in the leader `got`
-    // the mass up to and with it.
-    auto cut = [&](bool by_count, unsigned long long target, unsigned long long* got) {
-      unsigned c_before = 0;
-      unsigned long long m_before = 0;
-      // the class that holds the element among n_cls = kPer * kThreads (or
-      // 1024) classes whose sums the leader's threads hold
-      auto pick = [&](int per, const unsigned* cs, const unsigned long long* ms, int shift) {
-        unsigned c = 0;
-        unsigned long long m = 0;
-        for (int j = 0; j < per; ++j) {
-          c += cs[j];
-          m += ms[j];
-        }
-        const unsigned c0 = c;
-        const unsigned long long m0 = m;
-        block_scan(sm, c, m);
-        unsigned bc = c_before + c - c0;
-        unsigned long long bm = m_before + m - m0;
-        for (int j = 0; j < per; ++j) {
-          const bool here = by_count ? (bc < target && target <= bc + cs[j]) : (bm < target && target <= bm + ms[j]);
-          if (here) {
-            if (shift < 0) {
-              sm.ctl.bin = tid * per + j;
-              sm.ctl.prefix = sm.ctl.mask = 0;
-            } else {  // digits run from the largest
-              sm.ctl.prefix |= static_cast<unsigned long long>(1023 - (tid * per + j)) << shift;
-              sm.ctl.mask |= 1023ull << shift;
-            }
-            sm.ctl.refine = cs[j] > kList;
-            sm.scan_c[0] = bc;
-            sm.scan_m[0] = bm;
-          }
-          bc += cs[j];
-          bm += ms[j];
-        }
-        __syncthreads();
-        c_before = sm.scan_c[0];
-        m_before = sm.scan_m[0];
-        __syncthreads();
-      };
-      if (lead) pick(kPer, row_c, row_m, -1);
-      cluster_sync();
-      for (int shift = 40; ls.ctl.refine; shift -= 10) {
-        for (int i = tid; i < 1024; i += kThreads) {
-          sm.mass[i] = 0;
-          sm.count[i] = 0;
-        }
-        const int bin = ls.ctl.bin;
-        const unsigned long long pre = ls.ctl.prefix, msk = ls.ctl.mask;
-        __syncthreads();
-        for (int i = begin + lane; i < end; i += 32) {
-          const float x = logit<E>(src, i);
-          const unsigned long long key = key50(x, i);
-          if (key < keep || (key & msk) != pre) continue;
-          const unsigned long long w = wt.weight44(x);
-          if (w == 0 || bin_of(x) != bin) continue;
-          const int d = 1023 - static_cast<int>((key >> shift) & 1023);
-          atomicAdd(&sm.count[d], 1u);
-          atomicAdd(&sm.mass[d], w);
-        }
-        cluster_sync();
-        if (lead) {
-          unsigned cs[2];
-          unsigned long long ms[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            cs[j] = 0;
-            ms[j] = 0;
-            for (int q = 0; q < cl; ++q) {
-              const Smem* o = at_rank(&sm, q);
-              cs[j] += o->count[tid * 2 + j];
-              ms[j] += o->mass[tid * 2 + j];
-            }
-          }
-          pick(2, cs, ms, shift);
-        }
-        cluster_sync();
-      }
-      // the class's members to the leader
-      {
-        const int bin = ls.ctl.bin;
-        const unsigned long long pre = ls.ctl.prefix, msk = ls.ctl.mask;
-        for (int i = begin + lane; i < end; i += 32) {
-          const float x = logit<E>(src, i);
-          const unsigned long long key = key50(x, i);
-          if (key < keep || (key & msk) != pre || bin_of(x) != bin || wt.weight44(x) == 0) continue;
-          const unsigned at = atomicAdd(&ls.list_n, 1u);
-          if (at < kList) ls.list[at] = key;
-        }
-      }
-      cluster_sync();
-      if (lead) {
-        const int n = min(static_cast<int>(sm.list_n), kList);
-        const int n2 = pow2_at_least(n);
-        for (int i = n + tid; i < n2; i += kThreads) sm.list[i] = 0;
-        __syncthreads();
-        block_sort_desc(reinterpret_cast<uint64_t*>(sm.list), n2);
-        constexpr int kQ = kList / kThreads;
-        unsigned cs[kQ];
-        unsigned long long ms[kQ];
-        unsigned c = 0;
-        unsigned long long m = 0;
-#pragma unroll
-        for (int j = 0; j < kQ; ++j) {
-          const int i = tid * kQ + j;
-          cs[j] = i < n ? 1u : 0u;
-          ms[j] = i < n ? wt.weight44(key50_value(sm.list[i])) : 0ull;
-          c += cs[j];
-          m += ms[j];
-        }
-        const unsigned c0 = c;
-        const unsigned long long m0 = m;
-        block_scan(sm, c, m);
-        unsigned bc = c_before + c - c0;
-        unsigned long long bm = m_before + m - m0;
-#pragma unroll
-        for (int j = 0; j < kQ; ++j) {
-          if (cs[j] && (by_count ? bc + 1 == target : (bm < target && target <= bm + ms[j]))) {
-            sm.ctl.keep = sm.list[tid * kQ + j];
-            sm.ctl.left = bm + ms[j];
-          }
-          bc += cs[j];
-          bm += ms[j];
-        }
-        if (tid == 0) sm.list_n = 0;
-        __syncthreads();
-        *got = sm.ctl.left;
-      }
-      cluster_sync();
-      keep = ls.ctl.keep;
-    };
-    // the leader tells whether each cut is needed
-    if (lead) {
-      unsigned c = 0;
-      unsigned long long m = 0;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        c += row_c[j];
-        m += row_m[j];
-      }
-      block_scan(sm, c, m);
-      if (tid == kThreads - 1) {
-        sm.ctl.total = m;
-        sm.ctl.warp = use_k && c > static_cast<unsigned>(k);
-      }
-      __syncthreads();
-      Z = sm.ctl.total;
-    }
-    cluster_sync();
-    if (ls.ctl.warp) cut(true, static_cast<unsigned long long>(k), &Z);
-    if (use_p) {
-      unsigned long long got;
-      cut(false, tp > 0.f && lead ? ceil_share(tp, Z) : 1ull, &got);
-    }
+    s.sync();
   }
+  {
+    const int bin = ctl.bin;
+    const unsigned long long pre = ctl.prefix, msk = ctl.mask;
+    s.each([&](float x, unsigned long long key) {
+      if (key < keep || (key & msk) != pre || bin_of(wt, x) != bin || wt.weight44(x) == 0) return;
+      const unsigned at = atomicAdd(&s.ls.cls_n, 1u);
+      if (at < kClass) s.ls.cls[at] = key;
+    });
+  }
+  s.sync();
+  if (s.lead) {
+    const int n = min(static_cast<int>(sm.cls_n), kClass);
+    const int n2 = pow2_at_least(n);
+    for (int i = n + threadIdx.x; i < n2; i += kThreads) sm.cls[i] = 0;
+    __syncthreads();
+    block_sort_desc(reinterpret_cast<uint64_t*>(sm.cls), n2);
+    constexpr int kQ = kClass / kThreads;
+    unsigned long long ms[kQ], m = 0;
+    unsigned c = 0;
+#pragma unroll
+    for (int j = 0; j < kQ; ++j) {
+      const int i = threadIdx.x * kQ + j;
+      ms[j] = i < n ? wt.weight44(key50_value(sm.cls[i])) : 0ull;
+      c += i < n ? 1u : 0u;
+      m += ms[j];
+    }
+    unsigned bc = c_before - c;
+    unsigned long long bm = m_before - m;
+    block_scan(sm, c, m);
+    bc += c;
+    bm += m;
+#pragma unroll
+    for (int j = 0; j < kQ; ++j) {
+      const int i = threadIdx.x * kQ + j;
+      if (i < n && (by_count ? bc + 1 == target : (bm < target && target <= bm + ms[j]))) {
+        ctl.keep = sm.cls[i];
+        sm.picked_m = bm + ms[j];
+      }
+      bc += i < n ? 1u : 0u;
+      bm += ms[j];
+    }
+    if (threadIdx.x == 0) sm.cls_n = 0;
+    __syncthreads();
+    *upto = sm.picked_m;
+  }
+  s.sync();
+  keep = ctl.keep;
+}
 
-  // ---- 3. the kept tokens' mass per warp, and the draw
-  unsigned long long sum = 0;
-  for (int i = begin + lane; i < end; i += 32) {
-    const float x = logit<E>(src, i);
-    if (key50(x, i) >= keep) sum += wt.weight44(x);
+// A request's settings for a row.
+struct Rule {
+  float tp, mp;
+  int k;
+  bool use_k, use_p;
+};
+
+// Smallest key whose weight is at least min_p: 32 probes a round over the
+// ordered logits (every warp finds the same).
+__device__ unsigned long long min_p_key(const Weights& wt, float mp) {
+  const int lane = threadIdx.x & 31;
+  const unsigned long long need = static_cast<unsigned long long>(ceil(ldexp(static_cast<double>(mp), 44)));
+  unsigned lo = 0, hi = float_order(wt.top);  // the answer lies in (lo, hi]
+  while (hi - lo > 1) {
+    const unsigned step = (hi - lo + 31) / 32;
+    const unsigned long long at = static_cast<unsigned long long>(lo) + static_cast<unsigned long long>(lane + 1) * step;
+    const bool in = at >= hi || wt.weight44(order_float(static_cast<unsigned>(at))) >= need;
+    const int f = __ffs(__ballot_sync(kFullMask, in)) - 1;  // (the last probe is at or behind hi)
+    const unsigned long long nhi = static_cast<unsigned long long>(lo) + static_cast<unsigned long long>(f + 1) * step;
+    lo += static_cast<unsigned>(f) * step;
+    hi = nhi < hi ? static_cast<unsigned>(nhi) : hi;
   }
+  return static_cast<unsigned long long>(hi) << kIdxBits;
+}
+
+// floor(u total) for the draw, below total.
+__device__ __forceinline__ unsigned long long draw_mark(float u, unsigned long long total) {
+  unsigned long long t = 0;
+  if (u > 0.f)
+    t = u >= 1.f ? total : __umul64hi(static_cast<unsigned long long>(ldexp(static_cast<double>(u), 64)), total);
+  return t < total ? t : total - 1;
+}
+
+// The row's classes: counts and masses of what is above `keep`.
+template <typename S>
+__device__ void fill_bins(const S& s, const Weights& wt, unsigned long long keep) {
+  clear_classes(s.sm);
+  __syncthreads();
+  s.each([&](float x, unsigned long long key) {
+    if (key < keep) return;
+    const unsigned long long w = wt.weight44(x);
+    if (w == 0) return;
+    const int b = bin_of(wt, x);
+    atomicAdd(&s.sm.count[b], 1u);
+    add_mass(s.sm, b, w);
+  });
+  s.sync();
+}
+
+// Count and mass over all classes (leader's block).
+template <typename S>
+__device__ void all_classes(const S& s, unsigned* count, unsigned long long* mass) {
+  constexpr int kPer = kBins / kThreads;
+  unsigned c = 0, cj;
+  unsigned long long m = 0, mj;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    s.sums(threadIdx.x * kPer + j, &cj, &mj);
+    c += cj;
+    m += mj;
+  }
+  block_scan(s.sm, c, m);
+  if (threadIdx.x == kThreads - 1) {
+    s.sm.picked_c = c;
+    s.sm.picked_m = m;
+  }
+  __syncthreads();
+  *count = s.sm.picked_c;
+  *mass = s.sm.picked_m;
+  __syncthreads();
+}
+
+// The kept tokens' mass per warp, left in the leader's wsum.
+template <typename S>
+__device__ void whole_sums(const S& s, const Weights& wt, unsigned long long keep) {
+  unsigned long long sum = 0;
+  const float kx = key50_value(keep);
+  const bool any = keep == 0;
+  s.each([&](float x, unsigned long long key) {
+    if (any || (x >= kx && key >= keep)) sum += wt.weight44(x);
+  });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
-  if (lane == 0) ls.wsum[rank * kWarps + warp] = sum;
+  if ((threadIdx.x & 31) == 0) s.ls.wsum[s.gw] = sum;
+}
+
+// top-p alone, or no cut: one exact pass over the row.
+// A histogram of approximate class masses (a count, and in units of 2^-18 how
+// far the class's weights lie below its largest possible one: two 32-bit
+// sums) tells the classes [c1, c2] in which the running mass passes top_p of
+// the whole, with room for the masses' error.  The exact pass then sums all
+// weights and those of the classes before c1, and gathers the tokens of c1 ..
+// c2, among which the cut falls.  False if it does not, or if they are too
+// many; else the kept tokens' mass per warp is in wsum.
+template <typename S>
+__device__ bool nucleus(const S& s, const Weights& wt, const Rule& rule, unsigned long long& keep) {
+  Smem& sm = s.sm;
+  Ctl& ctl = s.ls.ctl;
+  const int tid = threadIdx.x, lane = tid & 31;
+  keep = 0;
+  if (!rule.use_p) {
+    whole_sums(s, wt, keep);
+    return true;
+  }
+  clear_classes(sm);
+  if (s.lead && tid == 0) sm.list_n = 0;
+  __syncthreads();
+  s.each_value([&](float x, int) {
+    const float y = wt.log2w(x);
+    if (!(y >= kZeroBelow)) return;
+    const int b = min(kBins - 1, static_cast<int>(y * -kBinsPer2));
+    const float w = ex2(fmaf(static_cast<float>(b), 1.f / kBinsPer2, y));  // 2^(-1/20) .. 1
+    atomicAdd(&sm.count[b], 1u);
+    atomicAdd(&sm.mass_lo[b], static_cast<unsigned>(fmaxf((1.f - w) * 262144.f, 0.f)));
+  });
+  s.sync();
+  if (s.lead) {
+    constexpr int kPer = kBins / kThreads;
+    float ms[kPer], m = 0.f;
+    unsigned cs[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      unsigned long long low;
+      s.sums(tid * kPer + j, &cs[j], &low);
+      const float d = static_cast<float>(static_cast<double>(low) * (1.0 / 262144.0));
+      ms[j] = (static_cast<float>(cs[j]) - d) * ex2(static_cast<float>(tid * kPer + j) * (-1.f / kBinsPer2));
+      m += ms[j];
+    }
+    float inc = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float y = __shfl_up_sync(kFullMask, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) sm.wval[tid >> 5] = inc;
+    if (tid == 0) {
+      ctl.bin = kBins;
+      ctl.last = kBins;
+    }
+    __syncthreads();
+    float before = inc - m, all = 0.f;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < (tid >> 5)) before += sm.wval[w];
+      all += sm.wval[w];
+    }
+    // (the fp32 sums and the classes' masses are good to 2^-15 of the whole)
+    const float t1 = fmaxf(rule.tp, 0.f) * all - all * (1.f / 16384.f), t2 = t1 + all * (2.f / 16384.f);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int c = tid * kPer + j;
+      const float after = before + ms[j];
+      if (cs[j] > 0 && after >= t1) atomicMin(&ctl.bin, c);
+      if (cs[j] > 0 && after >= t2) atomicMin(&ctl.last, c);
+      before = after;
+    }
+    __syncthreads();
+    unsigned members = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int c = tid * kPer + j;
+      if (c >= ctl.bin && c <= ctl.last) members += cs[j];
+    }
+    atomicAdd(&sm.list_n, members);
+    __syncthreads();
+    if (tid == 0) {
+      ctl.refine = sm.list_n > kList ? 1 : 0;
+      sm.list_n = 0;
+    }
+  }
+  s.sync();
+  if (ctl.refine) return false;
+  const int c1 = ctl.bin, c2 = ctl.last;
+  unsigned long long above = 0, total = 0;
+  s.each_value([&](float x, int i) {
+    const int b = bin_of(wt, x);
+    const unsigned long long w = wt.weight44(x);
+    total += w;
+    if (b < c1) above += w;
+    else if (b <= c2 && w != 0) {
+      const unsigned at = atomicAdd(&s.ls.list_n, 1u);
+      if (at < kList) s.ls.list[at] = key50(x, i);
+    }
+  });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    above += __shfl_xor_sync(kFullMask, above, o);
+    total += __shfl_xor_sync(kFullMask, total, o);
+  }
+  if (lane == 0) {
+    s.ls.wsum[s.gw] = above;
+    s.ls.wtot[s.gw] = total;
+  }
+  s.sync();
+  if (s.lead) {
+    const int n = static_cast<int>(sm.list_n), warps = s.cl * kWarps;
+    unsigned long long A = 0, Z = 0;
+    for (int w = 0; w < warps; ++w) {
+      A += sm.wsum[w];
+      Z += sm.wtot[w];
+    }
+    const unsigned long long target = rule.tp > 0.f ? ceil_share(rule.tp, Z) : 1ull;
+    const Source<true, typename S::Elem> l{sm, sm, s.row, 0, 0, 0, 0, n, 1, true, 0, 1};
+    bool ok = n <= kList && target > A;
+    if (ok) {
+      fill_bins(l, wt, 0);
+      unsigned count;
+      unsigned long long in;
+      all_classes(l, &count, &in);
+      ok = target - A <= in;
+      if (ok) {
+        unsigned long long upto;
+        cut(l, wt, false, target - A, keep, &upto);
+        // the kept ones among them to their warps' masses
+        clear_classes(sm);
+        __syncthreads();
+        l.each([&](float x, unsigned long long key) {
+          if (key < keep) return;
+          const int i = (1 << kIdxBits) - 1 - static_cast<int>(static_cast<unsigned>(key) & ((1u << kIdxBits) - 1));
+          const int u = (i - s.row.head) / Row<typename S::Elem>::kPer;
+          const int w = i < s.row.head ? 0 : u >= s.row.units ? warps - 1 : u / s.share;
+          add_mass(sm, w, wt.weight44(x));
+        });
+        __syncthreads();
+        for (int w = tid; w < warps; w += kThreads)
+          sm.wsum[w] += (static_cast<unsigned long long>(sm.mass_hi[w]) << 32) + sm.mass_lo[w];
+      }
+    }
+    __syncthreads();
+    if (tid == 0) {
+      ctl.keep = keep;
+      ctl.refine = ok ? 0 : 1;
+    }
+  }
+  s.sync();
+  keep = ctl.keep;
+  return ctl.refine == 0;
+}
+
+// The whole row, every decision on integer sums over it.
+template <typename E>
+__device__ void whole_row(const SampleParams& p, Smem& sm, Smem& ls, const E* src, int row, int cl, int rank,
+                          const Weights& wt, const Rule& rule, bool greedy) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Row<E> rw(src, p.V);
+  const int gw = rank * kWarps + warp, gn = cl * kWarps;
+  const int share = (rw.units + gn - 1) / gn;
+  const int ub = min(rw.units, gw * share), ue = min(rw.units, ub + share);
+  const Source<false, E> s{sm, ls, rw, ub, ue, gw == 0, gw == gn - 1, 0, cl, rank == 0, gw, max(share, 1)};
+  if (greedy) {  // the lowest index of the largest logit
+    unsigned long long best = 0;
+    s.each([&](float x, unsigned long long key) { best = max(best, key); });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(kFullMask, best, o));
+    if (lane == 0) ls.wsum[rank * kWarps + warp] = best;
+    cluster_sync();
+    if (s.lead && tid == 0) {
+      for (int w = 0; w < cl * kWarps; ++w) best = max(best, sm.wsum[w]);
+      p.token[row] = (1 << kIdxBits) - 1 - static_cast<int>(best & ((1u << kIdxBits) - 1));
+      p.prob[row] = 1.f;
+    }
+    return;
+  }
+  unsigned long long keep = 0;
+  const bool quick = !rule.use_k && !(rule.mp > 0.f) && nucleus(s, wt, rule, keep);
+  if (!quick) {
+    keep = rule.mp > 0.f ? min_p_key(wt, rule.mp) : 0;
+    if (rule.use_k || rule.use_p) {
+      fill_bins(s, wt, keep);
+      unsigned count = 0;
+      unsigned long long Z = 0;
+      if (s.lead) {
+        all_classes(s, &count, &Z);
+        if (tid == 0) ls.ctl.warp = rule.use_k && count > static_cast<unsigned>(rule.k);
+      }
+      cluster_sync();
+      if (ls.ctl.warp) cut(s, wt, true, static_cast<unsigned long long>(rule.k), keep, &Z);
+      if (rule.use_p) {
+        unsigned long long upto;
+        if (ls.ctl.warp) fill_bins(s, wt, keep);  // (the digits' passes used the classes)
+        cut(s, wt, false, rule.tp > 0.f && s.lead ? ceil_share(rule.tp, Z) : 1ull, keep, &upto);
+      }
+    }
+    whole_sums(s, wt, keep);
+  }
   cluster_sync();
-  if (lead && warp == 0) {
+  if (s.lead && warp == 0) {
     const int n = cl * kWarps;
     unsigned long long total = 0;
     for (int i = lane; i < n; i += 32) total += sm.wsum[i];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFullMask, total, o);
     if (lane == 0) {
-      const float u = p.u[row];
-      unsigned long long t = 0;
-      if (u > 0.f)
-        t = u >= 1.f ? total : __umul64hi(static_cast<unsigned long long>(ldexp(static_cast<double>(u), 64)), total);
-      t = t < total ? t : total - 1;
+      unsigned long long t = draw_mark(p.u[row], total);
       int w = 0;
       while (w < n - 1 && t >= sm.wsum[w]) t -= sm.wsum[w++];
       sm.ctl.warp = w;
@@ -515,35 +827,378 @@ __global__ void __launch_bounds__(kThreads) k_sample(const SampleParams p) {
     }
   }
   cluster_sync();
-  const int win = ls.ctl.warp;
-  if (win == rank * kWarps + warp) {
+  if (ls.ctl.warp == rank * kWarps + warp) {
+    // the warp's tokens in index order: the head, units of kPer tokens by the
+    // lanes, the rest
     const unsigned long long t = ls.ctl.left, total = ls.ctl.total;
     unsigned long long before = 0;
-    for (int b = begin; b < end; b += 32) {
-      const int i = b + lane;
-      unsigned long long w = 0;
-      if (i < end) {
-        const float x = logit<E>(src, i);
-        if (key50(x, i) >= keep) w = wt.weight44(x);
+    constexpr int kPer = Row<E>::kPer;
+    auto step = [&](const float (&x)[kPer], int i0, int n) {  // the lane's n tokens from i0; true: found
+      unsigned long long w[kPer], sum = 0;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        w[k] = k < n && x[k] > -INFINITY && key50(x[k], i0 + k) >= keep ? wt.weight44(x[k]) : 0ull;
+        sum += w[k];
       }
-      unsigned long long inc = w;
+      unsigned long long inc = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const unsigned long long y = __shfl_up_sync(kFullMask, inc, o);
         if (lane >= o) inc += y;
       }
       const unsigned hit = __ballot_sync(kFullMask, before + inc > t);
-      if (hit) {
-        if (lane == __ffs(hit) - 1) {
-          p.token[row] = i;
-          p.prob[row] = static_cast<float>(static_cast<double>(w) / static_cast<double>(total));
+      if (hit && lane == __ffs(hit) - 1) {
+        unsigned long long c = before + inc - sum;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          if (c <= t && c + w[k] > t) {
+            p.token[row] = i0 + k;
+            p.prob[row] = static_cast<float>(static_cast<double>(w[k]) / static_cast<double>(total));
+          }
+          c += w[k];
         }
-        break;
       }
       before += __shfl_sync(kFullMask, inc, 31);
+      return hit != 0;
+    };
+    bool found = false;
+    float x[kPer];
+    if (gw == 0 && rw.head > 0) {
+      x[0] = lane < rw.head ? logit<E>(src, lane) : -INFINITY;
+      found = step(x, lane, lane < rw.head ? 1 : 0);
+    }
+    for (int b = ub; b < ue && !found; b += 32) {
+      const int u = b + lane;
+      if (u < ue) unpack<E>(rw.load(u), x);
+      found = step(x, rw.index(u), u < ue ? kPer : 0);
+    }
+    const int rest = rw.index(rw.units);
+    if (!found && gw == gn - 1 && rest < p.V) {
+      x[0] = rest + lane < p.V ? logit<E>(src, rest + lane) : -INFINITY;
+      step(x, rest + lane, rest + lane < p.V ? 1 : 0);
     }
   }
-  cluster_sync();  // (no CTA leaves while another reads the leader's memory)
+}
+
+// The candidates in the leader's list (its block): all tokens whose logit is
+// at least the bound's; the other tokens weigh `tail` together, at most
+// tail_err off (units of 2^-44).  False where they do not decide the row.
+template <typename E>
+__device__ bool from_list(const SampleParams& p, Smem& sm, int row, int n, unsigned long long bound_key,
+                          unsigned long long tail, unsigned long long tail_err, const Weights& wt, const Rule& rule) {
+  const int tid = threadIdx.x;
+  const Source<true, E> s{sm, sm, Row<E>(nullptr, 0), 0, 0, 0, 0, n, 1, true, 0, 1};
+  unsigned long long keep = bound_key;
+  bool all = false;  // nothing below `keep` is kept
+  if (rule.mp > 0.f) {
+    const unsigned long long mk = min_p_key(wt, rule.mp);
+    if (mk >= bound_key) {
+      keep = mk;
+      all = true;
+    }
+  }
+  fill_bins(s, wt, keep);
+  unsigned count;
+  unsigned long long Z;
+  all_classes(s, &count, &Z);
+  if (rule.use_k && count >= static_cast<unsigned>(rule.k)) {
+    if (count > static_cast<unsigned>(rule.k)) {
+      cut(s, wt, true, static_cast<unsigned long long>(rule.k), keep, &Z);
+      if (rule.use_p) fill_bins(s, wt, keep);
+    }
+    all = true;
+  }
+  // (top-k or min-p beyond the candidates, or nothing cut but the tail)
+  if (!all && (rule.use_k || rule.mp > 0.f || !rule.use_p)) return false;
+  if (all) tail = tail_err = 0;
+  if (rule.use_p) {
+    const unsigned long long lo = rule.tp > 0.f ? ceil_share(rule.tp, Z + tail - tail_err) : 1ull;
+    const unsigned long long hi = rule.tp > 0.f ? ceil_share(rule.tp, Z + tail + tail_err) : 1ull;
+    if (hi > Z) return false;
+    cut(s, wt, false, lo, keep, &Z);
+    if (hi > Z) return false;  // (the interval's other end falls on a later token)
+  }
+  // the draw: masses by index (256 to a class), then the class's tokens
+  const unsigned long long t = draw_mark(p.u[row], Z);
+  clear_classes(sm);
+  __syncthreads();
+  auto inverted = [](unsigned long long key) { return static_cast<unsigned>(key) & ((1u << kIdxBits) - 1); };
+  s.each([&](float x, unsigned long long key) {
+    if (key >= keep) add_mass(sm, 1023 - static_cast<int>(inverted(key) >> 8), wt.weight44(x));  // ascending index
+  });
+  __syncthreads();
+  unsigned c0 = 0, members;
+  unsigned long long before = 0;
+  const unsigned c = pick_class(s, false, t + 1, c0, before, &members);
+  s.each([&](float x, unsigned long long key) {
+    if (key < keep || 1023 - (inverted(key) >> 8) != c) return;
+    const unsigned at = atomicAdd(&sm.cls_n, 1u);  // (at most 256)
+    sm.cls[at] = (static_cast<unsigned long long>(inverted(key)) << 32) | (key >> kIdxBits);
+  });
+  __syncthreads();
+  const int m = static_cast<int>(sm.cls_n), m2 = pow2_at_least(m);
+  for (int i = m + tid; i < m2; i += kThreads) sm.cls[i] = 0;
+  __syncthreads();
+  block_sort_desc(reinterpret_cast<uint64_t*>(sm.cls), m2);  // ascending index
+  const unsigned long long w = tid < m ? wt.weight44(order_float(static_cast<uint32_t>(sm.cls[tid]))) : 0ull;
+  unsigned one = 0;
+  unsigned long long inc = w;
+  block_scan(sm, one, inc);
+  inc += before;
+  if (tid < m && inc > t && inc - w <= t) {
+    p.token[row] = (1 << kIdxBits) - 1 - static_cast<int>(sm.cls[tid] >> 32);
+    p.prob[row] = static_cast<float>(static_cast<double>(w) / static_cast<double>(Z));
+  }
+  return true;
+}
+
+template <typename E>
+__global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
+  constexpr int kPer = Row<E>::kPer;
+  extern __shared__ __align__(16) uint8_t raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(raw);
+  unsigned cl_u, rank_u;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(cl_u));
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank_u));
+  const int cl = static_cast<int>(cl_u), rank = static_cast<int>(rank_u);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (waited on before the first access to another CTA's memory)
+  if (cl > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int row = blockIdx.x / cl, req = row / p.rows_per_req;
+  const E* src = static_cast<const E*>(p.logits) + static_cast<size_t>(row) * p.row_stride;
+  const bool lead = rank == 0;
+  Smem& ls = *at_rank(&sm, 0);  // the leader's
+  const Row<E> rw(src, p.V);
+  const int gw = rank * kWarps + warp, gn = cl * kWarps;
+  const int share = (rw.units + gn - 1) / gn;
+  const int ub = min(rw.units, gw * share), ue = min(rw.units, ub + share);
+
+  const float T = p.temperature ? p.temperature[req] : 1.f;
+  Rule rule;
+  rule.k = p.top_k ? p.top_k[req] : 0;
+  rule.tp = p.top_p ? p.top_p[req] : 1.f;
+  rule.mp = p.min_p ? fminf(p.min_p[req], 1.f) : 0.f;
+  rule.use_k = rule.k >= 1 && rule.k < p.V;
+  rule.use_p = rule.tp < 1.f;
+  const bool greedy = !(T > 0.f);
+  const float ch = static_cast<float>(1.4426950408889634074 / static_cast<double>(T));
+
+  // (with no cut every token is in the draw, and the row's sums are needed)
+  bool listed = greedy || rule.use_k || rule.use_p || rule.mp > 0.f;
+  float bound = -INFINITY, off = 0.f;
+  for (int i = tid; i < (1 << kExpBits); i += kThreads) sm.exp[i] = make_float2(g_exp.hi[i], g_exp.lo[i]);
+  if (tid == 0) {
+    sm.list_n = 0;
+    sm.units_n = 0;
+    sm.cls_n = 0;
+    sm.ctl.done = 0;
+  }
+  if (listed) {
+    // ---- 1. a sample: every thread one unit, evenly spread over the row.
+    // the bound is the r-th largest of the CTA's units' maxima (a cluster
+    // takes the mean), with r / 256 the share of units that hold one of the
+    // candidates wanted: 256 (1 - (1 - want / V)^kPer)
+    float m = -INFINITY;
+    if (rw.units > 0) {
+      float x[kPer];
+      const long long at = (static_cast<long long>(rank) * kThreads + tid) * rw.units / (cl * kThreads);
+      unpack<E>(rw.load(static_cast<int>(at)), x);
+      m = fmaxf(max_of(x), -INFINITY);
+    }
+    sm.sample[tid] = m;
+    __syncthreads();
+    const float want = rule.use_k ? fminf(fmaxf(1.6f * rule.k + 300.f, 0.5f * kWant), kWant) : kWant;
+    const float share_out = fminf(want / static_cast<float>(p.V), 1.f);
+    const int r = greedy ? 1 : max(1, static_cast<int>(kThreads * (1.f - __powf(1.f - share_out, kPer)) + 0.5f));
+    int above = 0, equal = 0;
+    for (int q = 0; q < kThreads; q += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(&sm.sample[q]);
+      above += (o.x > m) + (o.y > m) + (o.z > m) + (o.w > m);
+      equal += (o.x == m) + (o.y == m) + (o.z == m) + (o.w == m);
+    }
+    if (above == 0) sm.smax = m;                          // (all that write write the same)
+    if (above < r && r <= above + equal) sm.sbound = m;
+    __syncthreads();
+    float lo = sm.sbound, hi = sm.smax;
+    if (cl > 1) {
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      if (tid < cl) at_rank(&sm, tid)->bounds[rank] = make_float2(lo, hi);
+      cluster_sync();
+      float mean = 0.f;
+      for (int q = 0; q < cl; ++q) {
+        mean += sm.bounds[q].x;
+        hi = fmaxf(hi, sm.bounds[q].y);
+      }
+      lo = mean / static_cast<float>(cl);                 // (-inf where one of them is)
+    }
+    bound = greedy ? hi : lo;
+    off = hi * ch;  // the reference of the sums: the sample's largest logit
+    if (!isfinite(off)) off = 0.f;
+  } else if (cl > 1) {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    cluster_sync();  // (the leader's counters)
+  } else {
+    __syncthreads();
+  }
+
+  // ---- 2. one pass: units that reach the bound are noted; the weights of
+  // the other tokens, 2^(x ch - off) <= 1, are summed where top-p needs them.
+  // NaN makes the sum NaN, which sends the row to the whole-row path.
+  float top = -INFINITY, sum = 0.f;
+  const bool sums = rule.use_p && !rule.use_k && !greedy;
+  auto pass = [&](auto mode) {
+    constexpr int kMode = decltype(mode)::value;  // 0: largest logit, 1: and candidates, 2: and sums
+    constexpr int kAhead = 4;
+    auto take = [&](uint4 v, int u) {
+      float x[kPer];
+      unpack<E>(v, x);
+      const float m = max_of(x);
+      if constexpr (kMode == 0) {
+        top = fmaxf(top, m);
+        return 0.f;
+      }
+      if (m >= bound && m > -INFINITY) {
+        top = fmaxf(top, m);
+        const unsigned at = atomicAdd(&sm.units_n, 1u);
+        if (at < kUnits) sm.unit[at] = static_cast<uint16_t>(u);
+        return 0.f;
+      }
+      float w = 0.f;
+      if constexpr (kMode == 2) {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) w += ex2(fmaf(x[k], ch, -off));
+      }
+      return w;
+    };
+    int u = ub + lane;
+    for (; u + 32 * (kAhead - 1) < ue; u += 32 * kAhead) {
+      uint4 v[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) v[a] = rw.load(u + 32 * a);
+      float w = 0.f;
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) w += take(v[a], u + 32 * a);
+      sum += w;
+    }
+    for (; u < ue; u += 32) sum += take(rw.load(u), u);
+  };
+  if (!listed) pass(IntC<0>{});
+  else if (!sums) pass(IntC<1>{});
+  else pass(IntC<2>{});
+  __syncthreads();
+  // one token: to the leader's list, or into the sum
+  auto token = [&](float x, int i) {
+    if (!(x > -INFINITY)) return;  // (NaN, -inf)
+    top = fmaxf(top, x);
+    if (!listed) return;
+    if (x >= bound) {
+      const unsigned at = atomicAdd(&ls.list_n, 1u);
+      if (at < kList) ls.list[at] = key50(x, i);
+    } else {
+      sum += ex2(fmaf(x, ch, -off));
+    }
+  };
+  if (listed) {
+    const int n = min(static_cast<int>(sm.units_n), kUnits);
+    for (int i = tid; i < n; i += kThreads) {
+      const int un = sm.unit[i];
+      float x[kPer];
+      unpack<E>(rw.load(un), x);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) token(x[k], rw.index(un) + k);
+    }
+  }
+  if (lead) {
+    const int rest = rw.index(rw.units);
+    if (tid < rw.head) token(logit<E>(src, tid), tid);
+    if (tid < p.V - rest) token(logit<E>(src, rest + tid), rest + tid);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+    sum += __shfl_xor_sync(kFullMask, sum, o);
+  }
+  if (lane == 0) {
+    sm.wmax[warp] = top;
+    sm.wval[warp] = sum;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    float t = sm.wmax[0], w = sm.wval[0];
+    for (int k = 1; k < kWarps; ++k) {
+      t = fmaxf(t, sm.wmax[k]);
+      w += sm.wval[k];
+    }
+    ls.part[rank] = Part{t, w, off, sm.units_n > kUnits ? 1 : 0};
+  }
+  if (cl > 1) cluster_sync();
+  else __syncthreads();
+
+  // ---- 3. the leader decides the row by the list, or the cluster by the row
+  Weights wt;
+  wt.exp = sm.exp;
+  wt.ch = ch;
+  wt.cl = 0.f;
+  if (!isinf(ch))
+    wt.cl = static_cast<float>(1.4426950408889634074 / static_cast<double>(T) - static_cast<double>(ch));
+  if (lead) {
+    float all = 0.f;
+    bool lost = false;
+    top = -INFINITY;
+    for (int q = 0; q < cl; ++q) {
+      top = fmaxf(top, sm.part[q].top);
+      all += sm.part[q].sum;
+      lost |= sm.part[q].lost != 0;
+    }
+    wt.top = top;
+    const int n = static_cast<int>(sm.list_n);
+    bool done = false;
+    if (top == -INFINITY) {
+      if (tid == 0) {
+        p.token[row] = -1;
+        p.prob[row] = 0.f;
+      }
+      done = true;
+    } else if (greedy) {
+      if (!lost && n <= kList) {
+        unsigned long long best = 0;
+        for (int i = tid; i < n; i += kThreads) best = max(best, sm.list[i]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(kFullMask, best, o));
+        if (lane == 0) sm.scan_m[warp] = best;
+        __syncthreads();
+        if (tid == 0) {
+          for (int w = 1; w < kWarps; ++w) best = max(best, sm.scan_m[w]);
+          p.token[row] = (1 << kIdxBits) - 1 - static_cast<int>(best & ((1u << kIdxBits) - 1));
+          p.prob[row] = 1.f;
+        }
+        done = true;
+      }
+    } else if (listed && !lost && n <= kList && isfinite(top) && isfinite(all) && isfinite(top * ch)) {
+      // the sums, relative to the largest logit: 2^(off - top ch) of what
+      // they are, off by (|x ch - off| <= 46 where a weight counts) 2^-19 for
+      // the argument's rounding, 2^-20 for ch's, 2^-22 for ex2 and 2^-17 for
+      // some 100 additions: below 2^-16; the weights' own rounding to whole
+      // units is half a unit per token
+      const double scaled = ldexp(static_cast<double>(all) * exp2(static_cast<double>(off) -
+                                                                   static_cast<double>(top) * static_cast<double>(ch)), 44);
+      const unsigned long long tail = static_cast<unsigned long long>(scaled);
+      done = from_list<E>(p, sm, row, n, static_cast<unsigned long long>(float_order(bound)) << kIdxBits, tail,
+                          (tail >> 16) + static_cast<unsigned long long>(p.V), wt, rule);
+    }
+    if (tid == 0) {
+      sm.ctl.done = done ? 1 : 0;
+      sm.ctl.top = top;
+      sm.cls_n = 0;
+    }
+  }
+  if (cl > 1) cluster_sync();
+  else __syncthreads();
+  if (!ls.ctl.done) {
+    wt.top = ls.ctl.top;
+    whole_row<E>(p, sm, ls, src, row, cl, rank, wt, rule, greedy);
+  }
+  if (cl > 1) cluster_sync();  // (no CTA leaves while another reads the leader's memory)
 }
 
 }  // namespace
@@ -559,9 +1214,9 @@ extern "C" dartree_status dartree_sample(const void* logits, int32_t bf16, int64
     return cache_fail(DARTREE_ERR_INVALID_ARG, "bad V, rows, rows_per_req or row_stride");
   if (V > (1 << kIdxBits)) return cache_fail(DARTREE_ERR_UNSUPPORTED, "V must be at most 2^18");
   const SampleParams p{logits, row_stride, V, rows, rows_per_req, temperature, top_k, top_p, min_p, u, token, prob};
-  // one cluster per row: as many CTAs as fill the SMs twice over
+  // one cluster per row: as many CTAs as the SMs hold (four each)
   int cl = 1;
-  while (cl < kMaxCl && static_cast<long long>(rows) * cl < 304 && V / cl > 4096) cl *= 2;
+  while (cl < kMaxCl && static_cast<long long>(rows) * cl < 304 && V / cl > 8192) cl *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (static_cast<long long>(rows) * cl > 0x7FFFFFFFll) return cache_fail(DARTREE_ERR_UNSUPPORTED, "too many rows");
   const dim3 grid(static_cast<unsigned>(rows) * cl);
