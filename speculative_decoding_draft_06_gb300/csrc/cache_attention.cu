@@ -23,8 +23,7 @@
 // [c dh/4, (c + 1) dh/4) of its key: one 16-byte (dh = 128) load.  In O, the
 // n index r of n-tile j is dim r dh/8 + j: a lane holds dh/8 dims of four
 // keys, and an output lane the dims [c dh/4, (c + 1) dh/4) of its rows.
-#include "cache.cuh"
-#include "ptx.cuh"
+#include "cache_attn.cuh"
 
 namespace dt {
 namespace {
@@ -34,47 +33,8 @@ constexpr int kStages = 4;
 constexpr int kWarps = 4;                      // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kRows = 16;                      // query rows per CTA
-constexpr float kBias = 6.f;                   // the reference maximum's weight is 2^kBias
-constexpr float kRaise = 8.f;                  // the reference rises when a score passes it by this
 
 __device__ int g_cache_err;  // error word when the caller passes none
-
-struct CacheAttnParams {
-  CacheView c;              // the layer
-  const uint16_t* Q;
-  long long q_stride;       // elements between rows (nodes)
-  const uint32_t* mask;     // [R][B][words]
-  const int32_t *n_nodes, *table, *lens;
-  int max_pages, R, B, max_len, Hq, g, words, rows, m_tiles;
-  int n_split, split_tiles;  // key tiles per split
-  float scale_log2;          // scale * log2(e) * k_scale
-  uint16_t* O;               // [R][B+1][Hq][dh]
-  float* part;               // [R][Hkv][m_tiles][n_split][16][dh + 2] (n_split > 1)
-  int* err;
-};
-
-// A request's keys: its prefix and nodes, cut at max_len.
-struct Span {
-  int Lp, n, L;  // prefix, nodes, keys
-};
-
-__device__ __forceinline__ bool request_span(const CacheAttnParams& p, int r, Span* s) {
-  const int len = p.lens[r];
-  int n = p.n_nodes ? min(p.n_nodes[r], p.B) : p.B;
-  if (len < 0 || n < 0) return false;
-  s->Lp = min(len, p.max_len);
-  s->n = n;
-  s->L = static_cast<int>(min(static_cast<long long>(len) + n, static_cast<long long>(p.max_len)));
-  return true;
-}
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -82,24 +42,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
 }
 
 // Bytes of one tile in shared memory: key codes, key scales, value codes,
@@ -213,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_attention(const CacheAttnPar
   const int q0 = mt * kRows;
   const int live = min((sp.n + 1) * p.g - q0, kRows);  // rows of this tile
   if (live <= 0) return;
-  const int t_all = (sp.L + kTileKeys - 1) / kTileKeys;
+  const int t_all = row_tile_keys(p, sp, mt);
   const int t_beg = split * p.split_tiles;
   const int nt = min(t_all, t_beg + p.split_tiles) - t_beg;
   if (nt <= 0 && !(split == 0 && p.n_split == 1)) return;  // (one split: rows without keys are written as 0)
@@ -464,17 +406,14 @@ __global__ void __launch_bounds__(kThreads) k_cache_attention(const CacheAttnPar
       for (int w = 0; w < kWarps; ++w) v[e] += sm.red[w][row][lane * kE + e] * f[w];
     }
     if (p.n_split > 1) {
-      float* dst = p.part + (((static_cast<size_t>(r) * p.c.Hkv + hk) * p.m_tiles + mt) * p.n_split + split) *
-                                (kRows * (DH + 2)) + row * (DH + 2);
+      float* dst = cache_part_row(p, r, hk, mt, split, row);
 #pragma unroll
       for (int e = 0; e < kE; e += 2)
         *reinterpret_cast<float2*>(dst + 2 + lane * kE + e) = make_float2(v[e], v[e + 1]);
       if (lane == 0) *reinterpret_cast<float2*>(dst) = make_float2(M, L);
     } else {
       const float inv = L > 0.f ? out_scale / L : 0.f;
-      const int q = q0 + row, nd = q / p.g;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(
-          p.O + ((static_cast<size_t>(r) * (p.B + 1) + nd) * p.Hq + hk * p.g + (q - nd * p.g)) * DH + lane * kE);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row(p, r, hk, q0 + row) + lane * kE);
 #pragma unroll
       for (int e = 0; e < kE; e += 2) dst[e / 2] = pack_bf16(v[e] * inv, v[e + 1] * inv);
     }
@@ -491,12 +430,11 @@ __global__ void __launch_bounds__(256) k_cache_attention_join(const CacheAttnPar
   pdl_wait();
   Span sp;
   if (!request_span(p, r, &sp) || q >= (sp.n + 1) * p.g) return;
-  const int tiles = (sp.L + kTileKeys - 1) / kTileKeys;
-  const int ns = (tiles + p.split_tiles - 1) / p.split_tiles;  // splits that had keys
+  const int mt = q / p.tile_rows;
+  const int ns = (row_tile_keys(p, sp, mt) + p.split_tiles - 1) / p.split_tiles;  // splits that had keys
   constexpr int kE = DH / 32;
-  const size_t step = kRows * (DH + 2);
-  const float* src = p.part + (((static_cast<size_t>(r) * p.c.Hkv + hk) * p.m_tiles + q / kRows) * p.n_split) * step +
-                     (q % kRows) * (DH + 2);
+  const size_t step = static_cast<size_t>(p.tile_rows) * (DH + 2);
+  const float* src = cache_part_row(p, r, hk, mt, 0, q - mt * p.tile_rows);
   float M = -INFINITY;
   for (int s = lane; s < ns; s += 32) M = fmaxf(M, src[s * step]);
 #pragma unroll
@@ -516,34 +454,39 @@ __global__ void __launch_bounds__(256) k_cache_attention_join(const CacheAttnPar
     }
   }
   const float inv = L > 0.f ? p.c.v_scale / L : 0.f;
-  const int nd = q / p.g;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(
-      p.O + ((static_cast<size_t>(r) * (p.B + 1) + nd) * p.Hq + hk * p.g + (q - nd * p.g)) * DH + lane * kE);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row(p, r, hk, q) + lane * kE);
 #pragma unroll
   for (int e = 0; e < kE; e += 2) dst[e / 2] = pack_bf16(v[e] * inv, v[e + 1] * inv);
 }
 
-// Key splits: enough CTAs to fill the SMs about three times over (three are
-// resident per SM), each with two tiles at least.
+// How a call is cut: up to kTreeRows rows per key/value head by the kernel
+// above, in tiles of 16 rows and 64 keys; more by the tensor-core kernel in
+// tiles of 128 rows and 128 keys.  The keys are split until the GPU is full:
+// here enough CTAs for about three waves of the three that an SM holds, two
+// tiles each at least; there one wave of one CTA per SM.
+constexpr int kTreeRows = 16;
+
 struct Plan {
-  int m_tiles, n_split, split_tiles;
+  int tile_rows, tile_keys, m_tiles, n_split, split_tiles;
   size_t work;
 };
 
 Plan plan_of(int R, int B, int max_len, int Hq, int Hkv, int dh) {
   Plan pl;
-  const int g = Hq / Hkv;
-  pl.m_tiles = static_cast<int>((static_cast<long long>(B + 1) * g + kRows - 1) / kRows);
-  const int tiles = max_len < 1 ? 1 : (max_len - 1) / kTileKeys + 1;
+  const long long rows = static_cast<long long>(B + 1) * (Hq / Hkv);
+  const bool tree = rows > kTreeRows;
+  pl.tile_rows = tree ? 128 : kRows;
+  pl.tile_keys = tree ? 128 : kTileKeys;
+  pl.m_tiles = static_cast<int>((rows + pl.tile_rows - 1) / pl.tile_rows);
+  const int tiles = max_len < 1 ? 1 : (max_len - 1) / pl.tile_keys + 1;
   const long long ctas = static_cast<long long>(R) * Hkv * pl.m_tiles;
-  const long long want = 152 * 6;
-  long long n = (want + ctas - 1) / ctas;
+  long long n = tree ? 152 / ctas : (152 * 6 + ctas - 1) / ctas;
   const long long most = (tiles + 1) / 2;
   n = n < most ? n : most;
   n = n < 1 ? 1 : n;
   pl.split_tiles = static_cast<int>((tiles + n - 1) / n);
   pl.n_split = (tiles + pl.split_tiles - 1) / pl.split_tiles;
-  pl.work = pl.n_split > 1 ? static_cast<size_t>(ctas) * pl.n_split * kRows * (dh + 2) * sizeof(float) : 0;
+  pl.work = pl.n_split > 1 ? static_cast<size_t>(ctas) * pl.n_split * pl.tile_rows * (dh + 2) * sizeof(float) : 0;
   return pl;
 }
 
@@ -599,6 +542,8 @@ extern "C" dartree_status dartree_cache_attention(const dartree_cache* cache, in
   p.Hq = Hq;
   p.words = (B + 31) / 32;
   p.rows = (B + 1) * p.g;
+  p.tile_rows = pl.tile_rows;
+  p.tile_keys = pl.tile_keys;
   p.m_tiles = pl.m_tiles;
   p.n_split = pl.n_split;
   p.split_tiles = pl.split_tiles;
@@ -611,7 +556,9 @@ extern "C" dartree_status dartree_cache_attention(const dartree_cache* cache, in
   cudaError_t e = cudaSuccess;
   if (!p.err) e = cudaGetSymbolAddress(reinterpret_cast<void**>(&p.err), g_cache_err);
   if (e != cudaSuccess) return cache_launched(e);
-  if (dh == 128) {
+  if (pl.tile_rows == 128) {
+    e = launch_cache_tree(p, st);
+  } else if (dh == 128) {
     e = set_max_dynamic_smem(k_cache_attention<128>);
     if (e == cudaSuccess)
       e = launch_kernel(k_cache_attention<128>, grid, dim3(kThreads), sizeof(AttnSmem<128>), st, false, p);

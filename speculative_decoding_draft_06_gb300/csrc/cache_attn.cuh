@@ -1,0 +1,96 @@
+// What the attention kernels over the 4-bit cache share: their parameters, a
+// request's keys, and the rows' way out (directly, or as shares of several
+// key splits in the workspace, which a join kernel brings together).
+#pragma once
+#include "cache.cuh"
+#include "ptx.cuh"
+
+namespace dt {
+
+constexpr float kBias = 6.f;   // the reference maximum's weight is 2^kBias
+constexpr float kRaise = 8.f;  // the reference rises when a score passes it by this
+
+struct CacheAttnParams {
+  CacheView c;              // the layer
+  const uint16_t* Q;
+  long long q_stride;       // elements between rows (nodes)
+  const uint32_t* mask;     // [R][B][words]
+  const int32_t *n_nodes, *table, *lens;
+  int max_pages, R, B, max_len, Hq, g, words, rows;
+  int tile_rows, tile_keys;  // of the kernel: 16 x 64 or 128 x 128
+  int m_tiles;               // row tiles
+  int n_split, split_tiles;  // key tiles per split
+  float scale_log2;          // scale * log2(e) * k_scale
+  uint16_t* O;               // [R][B+1][Hq][dh]
+  float* part;               // [R][Hkv][m_tiles][n_split][tile_rows][dh + 2] (n_split > 1)
+  int* err;
+};
+
+// A request's keys: its prefix and nodes, cut at max_len.
+struct Span {
+  int Lp, n, L;  // prefix, nodes, keys
+};
+
+__device__ __forceinline__ bool request_span(const CacheAttnParams& p, int r, Span* s) {
+  const int len = p.lens[r];
+  int n = p.n_nodes ? min(p.n_nodes[r], p.B) : p.B;
+  if (len < 0 || n < 0) return false;
+  s->Lp = min(len, p.max_len);
+  s->n = n;
+  s->L = static_cast<int>(min(static_cast<long long>(len) + n, static_cast<long long>(p.max_len)));
+  return true;
+}
+
+
+// Key tiles that the rows of row tile mt can see: the prefix and the nodes
+// up to the tile's last row's.
+__device__ __forceinline__ int row_tile_keys(const CacheAttnParams& p, const Span& s, int mt) {
+  const int last = min(s.n, (mt * p.tile_rows + p.tile_rows - 1) / p.g);
+  const int keys = min(s.L, s.Lp + last);
+  return (keys + p.tile_keys - 1) / p.tile_keys;
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+
+// Row q of a key/value head in the output (node q / g, query head hk g + q % g).
+__device__ __forceinline__ size_t cache_out_row(const CacheAttnParams& p, int r, int hk, int q) {
+  const int nd = q / p.g;
+  return ((static_cast<size_t>(r) * (p.B + 1) + nd) * p.Hq + hk * p.g + (q - nd * p.g)) * p.c.dh;
+}
+
+// Row `row` of row tile mt and one split in the workspace: (m, l) and dh
+// unnormalised outputs.
+__device__ __forceinline__ float* cache_part_row(const CacheAttnParams& p, int r, int hk, int mt, int split, int row) {
+  const size_t tile = ((static_cast<size_t>(r) * p.c.Hkv + hk) * p.m_tiles + mt) * p.n_split + split;
+  return p.part + (tile * p.tile_rows + row) * (p.c.dh + 2);
+}
+
+// The tensor-core kernel of many rows (cache_tree.cu).
+cudaError_t launch_cache_tree(const CacheAttnParams& p, cudaStream_t st);
+
+}  // namespace dt
