@@ -124,10 +124,12 @@ __global__ void __launch_bounds__(256) k_cache_append(const TokenParams p) {
 // 8 bytes of codes and a scale byte -> 16 bf16 (exact).
 __device__ __forceinline__ void values16(uint2 codes, uint32_t scale, float mul, uint4 (&out)[2]) {
   const uint32_t s2 = e4m3x2_to_f16x2(scale | (scale << 8));
-  uint32_t o[8];
+  uint32_t o[8], lo[4], hi[4];
+  e2m1x8_to_f16(codes.x, lo);
+  e2m1x8_to_f16(codes.y, hi);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const uint32_t x = h2mul(e2m1x2_to_f16x2(((k < 4 ? codes.x : codes.y) >> (8 * (k & 3))) & 0xFFu), s2);
+    const uint32_t x = h2mul(k < 4 ? lo[k] : hi[k - 4], s2);
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
     const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * mul, f.y * mul);
     o[k] = *reinterpret_cast<const uint32_t*>(&b);

@@ -74,14 +74,17 @@ inline dartree_status cache_launched(cudaError_t e) {
   return e == cudaSuccess ? DARTREE_OK : cache_fail(DARTREE_ERR_CUDA, cudaGetErrorString(e));
 }
 
-// Two e2m1 codes of a byte -> fp16 pair (low nibble in the low half), exact.
-__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
-  uint32_t d;
-  asm("{\n\t.reg .b8 b;\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.u8.u16 b, h;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
-      : "=r"(d)
-      : "r"(byte));
-  return d;
+// The eight e2m1 codes of a word -> four fp16 pairs, byte by byte (low nibble
+// in the low half), exact.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
 }
 
 // Two e4m3 bytes (low 16 bits) -> fp16 pair, exact.

@@ -239,15 +239,17 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
         }
       }
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        uint32_t a[4];
+      for (int k2 = 0; k2 < kSteps / 2; ++k2) {  // a word: two k-steps
+        uint32_t x[2][4];
+        e2m1x8_to_f16(w[0][k2], x[0]);
+        e2m1x8_to_f16(w[1][k2], x[1]);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          a[t] = h2mul(e2m1x2_to_f16x2((w[t][k >> 1] >> (16 * (k & 1))) & 0xFFu), sc[t][k >> 2]);
-          a[2 + t] = h2mul(e2m1x2_to_f16x2((w[t][k >> 1] >> (16 * (k & 1) + 8)) & 0xFFu), sc[t][k >> 2]);
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t a[4] = {h2mul(x[0][2 * k], sc[0][k2 >> 1]), h2mul(x[1][2 * k], sc[1][k2 >> 1]),
+                                 h2mul(x[0][2 * k + 1], sc[0][k2 >> 1]), h2mul(x[1][2 * k + 1], sc[1][k2 >> 1])};
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) mma_f16(s[h][n], a, qb[n][2 * k2 + k][0], qb[n][2 * k2 + k][1]);
         }
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) mma_f16(s[h][n], a, qb[n][k][0], qb[n][k][1]);
       }
     }
     // ---- scores in base 2; x = 2 t + i: key 16 h + 8 t + perm(rr), row 8 n + 2 c + i
@@ -347,19 +349,17 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
       }
 #pragma unroll
       for (int w = 0; w < DH / 64; ++w) {
-        uint32_t ev[2], od[2];  // bytes: (first key's, second key's) codes of the even, odd dims
+        uint32_t ev[2][4], od[2][4];  // (first key's, second key's) codes of the even, odd dims
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const uint32_t x = vw[t][0][w], y = vw[t][1][w];
-          ev[t] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
-          od[t] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
+          e2m1x8_to_f16((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), ev[t]);
+          e2m1x8_to_f16(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), od[t]);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t a[4] = {h2mul(e2m1x2_to_f16x2((ev[0] >> (8 * k)) & 0xFFu), vs[0]),
-                                 h2mul(e2m1x2_to_f16x2((od[0] >> (8 * k)) & 0xFFu), vs[0]),
-                                 h2mul(e2m1x2_to_f16x2((ev[1] >> (8 * k)) & 0xFFu), vs[1]),
-                                 h2mul(e2m1x2_to_f16x2((od[1] >> (8 * k)) & 0xFFu), vs[1])};
+          const uint32_t a[4] = {h2mul(ev[0][k], vs[0]), h2mul(od[0][k], vs[0]), h2mul(ev[1][k], vs[1]),
+                                 h2mul(od[1][k], vs[1])};
 #pragma unroll
           for (int n = 0; n < NQ; ++n) mma_f16(o[n][4 * w + k], a, pb[h][n][0], pb[h][n][1]);
         }
@@ -435,43 +435,79 @@ cudaError_t launch_rows(const CacheAttnParams& p, cudaStream_t st) {
                        sizeof(AttnSmem<DH, NQ>), st, false, p);
 }
 
-// The shares of each row over the key splits, joined in split order:
-// M = max m_s, O = sum O_s 2^(m_s - M) / sum l_s 2^(m_s - M).  One warp per
-// row; grid (rows / 8, Hkv, R).
-template <int DH>
+// The shares of each row over the key splits, joined in a fixed order: M =
+// max m_s, O = sum O_s 2^(m_s - M) / sum l_s 2^(m_s - M).  W warps per row
+// take every W-th split and meet in shared memory; grid (rows / (8 / W), Hkv,
+// R).
+template <int DH, int W>
 __global__ void __launch_bounds__(256) k_cache_attention_join(const CacheAttnParams p) {
-  const int lane = threadIdx.x & 31;
-  const int q = blockIdx.x * 8 + (threadIdx.x >> 5), hk = blockIdx.y, r = blockIdx.z;
+  constexpr int kE = DH / 32, kPerBlock = 8 / W;
+  __shared__ float s_v[W > 1 ? 8 : 1][DH];
+  __shared__ float2 s_ml[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % W;
+  const int q = blockIdx.x * kPerBlock + warp / W, hk = blockIdx.y, r = blockIdx.z;
   pdl_wait();
   Span sp;
-  if (!request_span(p, r, &sp) || q >= (sp.n + 1) * p.g) return;
-  const int mt = q / p.tile_rows;
-  const int ns = (row_tile_keys(p, sp, mt) + p.split_tiles - 1) / p.split_tiles;  // splits that had keys
-  constexpr int kE = DH / 32;
-  const size_t step = static_cast<size_t>(p.tile_rows) * (DH + 2);
-  const float* src = cache_part_row(p, r, hk, mt, 0, q - mt * p.tile_rows);
-  float M = -INFINITY;
-  for (int s = lane; s < ns; s += 32) M = fmaxf(M, src[s * step]);
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, x));
-  float L = 0.f, v[kE];
+  const bool on = request_span(p, r, &sp) && q < (sp.n + 1) * p.g;
+  if (W == 1 && !on) return;
+  float M = -INFINITY, L = 0.f, v[kE];
 #pragma unroll
   for (int e = 0; e < kE; ++e) v[e] = 0.f;
-  for (int s = 0; s < ns; ++s) {
-    const float2 ml = *reinterpret_cast<const float2*>(src + s * step);
-    const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-    L += ml.y * f;
+  if (on) {
+    const int mt = q / p.tile_rows;
+    const int ns = (row_tile_keys(p, sp, mt) + p.split_tiles - 1) / p.split_tiles;  // splits that had keys
+    const size_t step = static_cast<size_t>(p.tile_rows) * (DH + 2);
+    const float* src = cache_part_row(p, r, hk, mt, 0, q - mt * p.tile_rows);
+    for (int s = w + lane * W; s < ns; s += 32 * W) M = fmaxf(M, src[s * step]);
 #pragma unroll
-    for (int e = 0; e < kE; e += 2) {
-      const float2 x = *reinterpret_cast<const float2*>(src + s * step + 2 + lane * kE + e);
-      v[e] += x.x * f;
-      v[e + 1] += x.y * f;
+    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, x));
+#pragma unroll 4
+    for (int s = w; s < ns; s += W) {
+      const float2 ml = *reinterpret_cast<const float2*>(src + s * step);
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+      L += ml.y * f;
+#pragma unroll
+      for (int e = 0; e < kE; e += 2) {
+        const float2 x = *reinterpret_cast<const float2*>(src + s * step + 2 + lane * kE + e);
+        v[e] += x.x * f;
+        v[e + 1] += x.y * f;
+      }
+    }
+  }
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int e = 0; e < kE; ++e) s_v[warp][lane * kE + e] = v[e];
+    if (lane == 0) s_ml[warp] = make_float2(M, L);
+    __syncthreads();
+    if (w != 0 || !on) return;
+    float T = M;
+#pragma unroll
+    for (int k = 1; k < W; ++k) T = fmaxf(T, s_ml[warp + k].x);
+    L = 0.f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) v[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const float2 ml = s_ml[warp + k];
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - T);
+      L += ml.y * f;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) v[e] += s_v[warp + k][lane * kE + e] * f;
     }
   }
   const float inv = L > 0.f ? p.c.v_scale / L : 0.f;
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row(p, r, hk, q) + lane * kE);
 #pragma unroll
   for (int e = 0; e < kE; e += 2) dst[e / 2] = pack_bf16(v[e] * inv, v[e + 1] * inv);
+}
+
+template <int DH>
+cudaError_t launch_join(const CacheAttnParams& p, cudaStream_t st) {
+  // eight warps per row where a row has many shares (or few rows would leave
+  // the GPU to a handful of blocks), one warp where it has a few
+  if (p.n_split > 8)
+    return launch_kernel(k_cache_attention_join<DH, 8>, dim3(p.rows, p.c.Hkv, p.R), dim3(256), 0, st, true, p);
+  return launch_kernel(k_cache_attention_join<DH, 1>, dim3((p.rows + 7) / 8, p.c.Hkv, p.R), dim3(256), 0, st, true, p);
 }
 
 // How a call is cut: up to kTreeRows rows per key/value head by the kernel
@@ -578,10 +614,6 @@ extern "C" dartree_status dartree_cache_attention(const dartree_cache* cache, in
   } else {
     e = dh == 128 ? launch_rows<128, 2>(p, st) : launch_rows<64, 2>(p, st);
   }
-  if (e == cudaSuccess && pl.n_split > 1) {
-    const dim3 jgrid((p.rows + 7) / 8, p.c.Hkv, R);
-    e = launch_kernel(dh == 128 ? k_cache_attention_join<128> : k_cache_attention_join<64>, jgrid, dim3(256), 0,
-                      st, true, p);
-  }
+  if (e == cudaSuccess && pl.n_split > 1) e = dh == 128 ? launch_join<128>(p, st) : launch_join<64>(p, st);
   return cache_launched(e);
 }

@@ -302,9 +302,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
               scl = sc[(i ^ 2) >> 1];
             }
             uint32_t y[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] = h2mul(e2m1x2_to_f16x2((word >> (8 * k)) & 0xFFu), scl);
-            *reinterpret_cast<uint4*>(line + sw128(key, g + ii)) = make_uint4(y[0], y[1], y[2], y[3]);
+            e2m1x8_to_f16(word, y);
+            *reinterpret_cast<uint4*>(line + sw128(key, g + ii)) =
+                make_uint4(h2mul(y[0], scl), h2mul(y[1], scl), h2mul(y[2], scl), h2mul(y[3], scl));
           }
         }
         fence_async_smem();
