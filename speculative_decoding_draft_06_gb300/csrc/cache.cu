@@ -420,6 +420,7 @@ __device__ __forceinline__ void piece(size_t page_bytes, int* begin, int* end) {
 // The partly filled page of each fork, grid (pieces, layers, forks).
 __global__ void __launch_bounds__(256) k_cache_fork_copy(const ForkParams p) {
   const int i = blockIdx.z;
+  pdl_wait();
   if (!p.ok[i]) return;
   const int s = p.src[i], d = p.dst[i], len = p.lens[d];
   if ((len & ((1 << p.log_page) - 1)) == 0) return;
@@ -497,7 +498,7 @@ struct CommitParams {
   const int32_t* table;
   int32_t* lens;
   const int32_t *nodes, *len;
-  int pages, log_page, max_pages, Hkv, chunk, R, max_len, extra;
+  int pages, log_page, max_pages, layers, Hkv, chunk, R, max_len, extra;
   int* err;
 };
 
@@ -526,62 +527,62 @@ __device__ __forceinline__ int commit_count(const CommitParams& p, int r, int* b
   return *bad ? -1 : m;
 }
 
-// Grid (rows, layers).  A token of one head is 18 units of dh / 16 bytes (8 +
-// 1 of keys, 8 + 1 of values).  Ranks rise, so token k's source is at or
-// behind position k: a chunk of tokens is read whole before it is written,
-// and no later chunk reads what an earlier one wrote.
+// A cluster per row, its CTAs share the layers.  A token of one head is 18
+// units of dh / 16 bytes (8 + 1 of keys, 8 + 1 of values).  Ranks rise, so
+// token k's source is at or behind position k: a chunk of tokens is read whole
+// before it is written, and no later chunk reads what an earlier one wrote.
+// The row's length changes once every CTA of its cluster has read it.
 template <typename U>
 __global__ void __launch_bounds__(256) k_cache_commit(const CommitParams p) {
   constexpr int kU = 8;
-  const int r = blockIdx.x;
+  unsigned cl, rank;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(cl));
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int r = blockIdx.x / cl;
   int bad;
   const int m = commit_count(p, r, &bad);
-  if (m <= 0) return;
   const int len = p.lens[r], P = 1 << p.log_page;
   const int32_t* nodes = p.nodes + static_cast<size_t>(r) * p.max_len;
   const int32_t* row = p.table + static_cast<size_t>(r) * p.max_pages;
-  uint8_t* layer = p.pool + static_cast<size_t>(blockIdx.y) * p.layer_bytes;
   const int per = p.Hkv * 18;  // units per token
-  const long long units = static_cast<long long>(m) * per;
-  auto address = [&](int pos, int h, int u) -> U* {
-    const int page = row[pos >> p.log_page], t = pos & (P - 1);
-    const int w = u < 9 ? u : u - 9;
-    const int at = (u < 9 ? 0 : p.chunk >> 1) +
-                   (w < 8 ? (t * 8 + w) : (P * 8 + t)) * static_cast<int>(sizeof(U));
-    return reinterpret_cast<U*>(layer + static_cast<size_t>(page) * p.page_bytes +
-                                static_cast<size_t>(h) * p.chunk + at);
-  };
-  // (a chunk is whole units, not whole tokens: a unit of token k is only
-  // overwritten by the same unit of a token before k)
-  for (long long b = 0; b < units; b += kU * 256) {
-    U v[kU];
+  const long long units = m > 0 ? static_cast<long long>(m) * per : 0;
+  cluster_arrive();
+  for (int y = rank; y < p.layers; y += cl) {
+    uint8_t* layer = p.pool + static_cast<size_t>(y) * p.layer_bytes;
+    auto address = [&](int pos, int h, int u) -> U* {
+      const int page = row[pos >> p.log_page], t = pos & (P - 1);
+      const int w = u < 9 ? u : u - 9;
+      const int at = (u < 9 ? 0 : p.chunk >> 1) + (w < 8 ? (t * 8 + w) : (P * 8 + t)) * static_cast<int>(sizeof(U));
+      return reinterpret_cast<U*>(layer + static_cast<size_t>(page) * p.page_bytes + static_cast<size_t>(h) * p.chunk +
+                                  at);
+    };
+    // (a chunk is whole units, not whole tokens: a unit of token k is only
+    // overwritten by the same unit of a token before k)
+    for (long long b = 0; b < units; b += kU * 256) {
+      U v[kU];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const long long at = b + u * 256 + threadIdx.x;
-      if (at < units) {
-        const int k = static_cast<int>(at / per), rest = static_cast<int>(at % per);
-        v[u] = *address(len + nodes[k], rest / 18, rest % 18);
+      for (int u = 0; u < kU; ++u) {
+        const long long at = b + u * 256 + threadIdx.x;
+        if (at < units) {
+          const int k = static_cast<int>(at / per), rest = static_cast<int>(at % per);
+          v[u] = *address(len + nodes[k], rest / 18, rest % 18);
+        }
       }
-    }
-    __syncthreads();
+      __syncthreads();
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const long long at = b + u * 256 + threadIdx.x;
-      if (at < units) {
-        const int k = static_cast<int>(at / per), rest = static_cast<int>(at % per);
-        *address(len + k, rest / 18, rest % 18) = v[u];
+      for (int u = 0; u < kU; ++u) {
+        const long long at = b + u * 256 + threadIdx.x;
+        if (at < units) {
+          const int k = static_cast<int>(at / per), rest = static_cast<int>(at % per);
+          *address(len + k, rest / 18, rest % 18) = v[u];
+        }
       }
+      __syncthreads();
     }
-    __syncthreads();
   }
-}
-
-__global__ void __launch_bounds__(64) k_cache_commit_lens(const CommitParams p) {
-  const int r = blockIdx.x;
-  int bad;
-  const int m = commit_count(p, r, &bad);
-  if (threadIdx.x == 0) {
-    if (m >= 0) p.lens[r] += m + p.extra;
+  cluster_wait();
+  if (rank == 0 && threadIdx.x == 0) {
+    if (m >= 0) p.lens[r] = len + m + p.extra;
     if (bad && p.err) atomicOr(p.err, DT_ERR_BAD_INDEX);
   }
 }
@@ -709,7 +710,7 @@ extern "C" dartree_status dartree_cache_fork(const dartree_cache* cache, int32_t
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_kernel(k_cache_fork, dim3(1), dim3(kPlanThreads), 0, st, false, p);
   if (e == cudaSuccess)
-    e = launch_kernel(k_cache_fork_copy, dim3(copy_pieces(v.page_bytes), v.layers, n), dim3(256), 0, st, false, p);
+    e = launch_kernel(k_cache_fork_copy, dim3(copy_pieces(v.page_bytes), v.layers, n), dim3(256), 0, st, true, p);
   return cache_launched(e);
 }
 
@@ -723,14 +724,14 @@ extern "C" dartree_status dartree_cache_commit(const dartree_cache* cache, const
   if (s != DARTREE_OK) return s;
   if (!nodes || !len) return cache_fail(DARTREE_ERR_INVALID_ARG, "null pointer argument");
   if (max_len < 1 || extra < 0) return cache_fail(DARTREE_ERR_INVALID_ARG, "bad max_len or extra");
-  if (v.layers > 65535) return cache_fail(DARTREE_ERR_UNSUPPORTED, "commit takes at most 65535 layers");
-  const CommitParams p{v.pool,     v.page_bytes, v.layer_bytes, table,   lens, nodes,   len,   v.pages,
-                       v.log_page, max_pages,    v.Hkv,         v.chunk, R,    max_len, extra, err};
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_kernel(v.dh == 128 ? k_cache_commit<uint2> : k_cache_commit<uint32_t>,
-                                dim3(R, v.layers), dim3(256), 0, st, false, p);
-  if (e == cudaSuccess) e = launch_kernel(k_cache_commit_lens, dim3(R), dim3(64), 0, st, false, p);
-  return cache_launched(e);
+  if (R > (1 << 24)) return cache_fail(DARTREE_ERR_UNSUPPORTED, "commit takes at most 2^24 rows");
+  const CommitParams p{v.pool,     v.page_bytes, v.layer_bytes, table,   lens, nodes, len,     v.pages,
+                       v.log_page, max_pages,    v.layers,      v.Hkv,   v.chunk, R,  max_len, extra, err};
+  int cl = 1;  // CTAs per row: about one per layer, up to a cluster
+  while (cl < 8 && cl < v.layers) cl *= 2;
+  return cache_launched(launch_kernel_cluster(v.dh == 128 ? k_cache_commit<uint2> : k_cache_commit<uint32_t>,
+                                              dim3(static_cast<unsigned>(R) * cl), dim3(256), 0,
+                                              static_cast<cudaStream_t>(stream), false, cl, p));
 }
 
 extern "C" dartree_status dartree_cache_release(const dartree_cache* cache, int32_t* table, int32_t max_pages,

@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <string>
 
@@ -74,6 +75,20 @@ inline dartree_status cache_launched(cudaError_t e) {
   return e == cudaSuccess ? DARTREE_OK : cache_fail(DARTREE_ERR_CUDA, cudaGetErrorString(e));
 }
 
+// Opts a kernel into its dynamic shared memory, once per device (the calls
+// cost as much as a launch).
+template <typename Kern>
+inline cudaError_t opt_in_smem(Kern* k, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = set_max_dynamic_smem(k);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 // The eight e2m1 codes of a word -> four fp16 pairs, byte by byte (low nibble
 // in the low half), exact.
 __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
@@ -108,6 +123,26 @@ __device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The same object in CTA `rank` of the cluster.
+template <typename T>
+__device__ __forceinline__ T* at_rank(T* p, int rank) {
+  uint64_t out;
+  asm volatile("mapa.u64 %0, %1, %2;" : "=l"(out) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+  return reinterpret_cast<T*>(out);
 }
 
 }  // namespace dt

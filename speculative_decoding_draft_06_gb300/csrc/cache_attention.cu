@@ -5,10 +5,10 @@
 // group, g = Hq / Hkv.  A CTA takes up to 16 rows of one request and one
 // key/value head and a share of its keys (the keys are split over CTAs until
 // the GPU is full; a second kernel joins the shares).  Its four warps are
-// independent: each takes every fourth 32-key tile of the share, brings the
-// tile's codes and scales into its own ring of three stages in shared memory
-// with bulk copies, and has a softmax state and an output of its own until
-// the end.
+// independent: each takes every fourth 64-key tile of the share, brings the
+// tile's codes and scales into its own two stages in shared memory with bulk
+// copies (one for a 64-token page), and has a softmax state and an output of
+// its own until the end.
 //
 // Both products are mma m16n8k16 in fp16 with fp32 sums and the keys' side as
 // the 16-row operand: S^T = K Q^T (16 keys x 8 rows x 16 dims), O^T += V^T
@@ -32,8 +32,10 @@
 namespace dt {
 namespace {
 
-constexpr int kTileKeys = 32;
-constexpr int kStages = 3;
+constexpr int kTileKeys = 64;   // keys of a stage
+constexpr int kStep = 32;       // keys between two looks at the maximum
+constexpr int kStages = 2;
+constexpr int kMaxCluster = 8;  // splits that join in a cluster's shared memory
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 
@@ -55,8 +57,15 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
+// Bits of x where the mask has ones, of y where it has zeros.
+__device__ __forceinline__ uint32_t bit_select(uint32_t mask, uint32_t x, uint32_t y) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xCA;" : "=r"(d) : "r"(mask), "r"(x), "r"(y));
+  return d;
+}
+
 // Bytes of one tile in shared memory: key codes, key scales, value codes,
-// value scales of 32 tokens.
+// value scales of 64 tokens (a 64-token page's chunk, byte for byte).
 template <int DH>
 struct Tile {
   static constexpr int kCodes = kTileKeys * DH / 2, kScales = kTileKeys * DH / 16;
@@ -68,15 +77,19 @@ template <int DH, int NQ>
 struct __align__(128) AttnSmem {
   union {
     uint8_t stage[kWarps][kStages][Tile<DH>::kBytes];
-    float red[kWarps][8 * NQ][DH + 4];
+    struct {
+      float red[kWarps][8 * NQ][DH + 4];
+      float recv[8 * NQ + kMaxCluster][DH + 4];  // a cluster's shares of the rows that this CTA joins
+    };
   };
   uint64_t full[kWarps][kStages];
-  uint32_t valid[kWarps][kStages];  // bit k: key k of the tile is there
+  uint64_t valid[kWarps][kStages];  // bit k: key k of the tile is there
   float2 ml[kWarps][8 * NQ];
+  float2 recv_ml[8 * NQ + kMaxCluster];
 };
 
 template <int DH, int NQ>
-__global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(const CacheAttnParams p) {
+__global__ void __launch_bounds__(kThreads, 3) k_cache_attention(const CacheAttnParams p) {
   constexpr int kSteps = DH / 16;   // k-steps of S^T, dim tiles of O^T
   constexpr int kRows = 8 * NQ;
   using T = Tile<DH>;
@@ -90,7 +103,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
   const int t_all = row_tile_keys(p, sp, 0);
   const int t_beg = split * p.split_tiles;
   const int nt = min(t_all, t_beg + p.split_tiles) - t_beg;
-  if (nt <= 0 && !(split == 0 && p.n_split == 1)) return;  // (one split: rows without keys are written as 0)
+  // (one split: rows without keys are written as 0; a cluster's CTAs all stay)
+  if (nt <= 0 && !p.cluster && !(split == 0 && p.n_split == 1)) return;
   const int mine = nt > warp ? (nt - warp + kWarps - 1) / kWarps : 0;  // the warp's tiles
 
   if (lane < kStages) mbar_init(&sm.full[warp][lane], 1);
@@ -100,19 +114,23 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
     atomicOr(p.err, DT_ERR_BAD_INDEX);
 
   // ---- the warp's copies: lane (piece, segment) has one of a tile's (a
-  // piece: min(page, 32) tokens; segments: key codes, key scales, values')
+  // piece: min(page, 64) tokens; segments: key codes, key scales, values', or
+  // all of a 64-token page at once)
   const int P = 1 << p.c.log_page;
   const int piece = P < kTileKeys ? P : kTileKeys;
-  const int pieces = kTileKeys / piece;
-  const int pc = lane >> 2, seg = lane & 3;
+  const int pieces = kTileKeys / piece, segs = P == kTileKeys ? 1 : 4;
+  const int pc = lane / segs, seg = lane % segs;
+  const bool copies = pc < pieces;
   const int32_t* trow = p.table + static_cast<size_t>(r) * p.max_pages;
   const int unit = (seg & 1) ? DH / 16 : DH / 2;  // bytes of a token in the segment
-  const int seg_page = (seg >> 1) * (p.c.chunk >> 1) + ((seg & 1) ? P * DH / 2 : 0);
-  const int seg_tile = (seg >> 1) * T::kV + ((seg & 1) ? T::kCodes : 0) + pc * piece * unit;
+  const uint32_t bytes = static_cast<uint32_t>(segs == 1 ? T::kBytes : piece * unit);
+  const int seg_tile = (seg >> 1) * T::kV + ((seg & 1) ? T::kCodes : 0) + (segs == 1 ? 0 : pc * piece * unit);
+  const uint8_t* seg_base = p.c.pool + static_cast<size_t>(hk) * p.c.chunk + (seg >> 1) * (p.c.chunk >> 1) +
+                            ((seg & 1) ? P * DH / 2 : 0);
   auto first_key = [&](int i) { return (t_beg + warp + i * kWarps) * kTileKeys; };
   auto page_of = [&](int i) {  // the lane's piece's page: -1 none, -2 bad
     const int key = first_key(i) + pc * piece;
-    if (i >= mine || pc >= pieces || key >= sp.L) return -1;
+    if (i >= mine || !copies || key >= sp.L) return -1;
     const int slot = key >> p.c.log_page;
     const int page = slot < p.max_pages ? trow[slot] : -2;
     return page < 0 || page >= p.c.pages ? -2 : page;
@@ -123,21 +141,22 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
     const unsigned got = __ballot_sync(kFullMask, page >= 0);
     if (page == -2 && seg == 0) atomicOr(p.err, DT_ERR_BAD_INDEX);
     if (lane == 0) {
-      uint32_t v = 0;
-      for (int k = 0; k < pieces; ++k)
-        if ((got >> (4 * k)) & 1u) v |= (piece == 32 ? ~0u : ((1u << piece) - 1u) << (k * piece));
+      uint64_t v = ~0ull;
+      if (got != (segs == 1 ? 1u : (pieces == 1 ? 0xFu : pieces == 2 ? 0xFFu : 0xFFFFu))) {
+        v = 0;
+        for (int k = 0; k < pieces; ++k)
+          if ((got >> (segs * k)) & 1u) v |= (piece == 64 ? ~0ull : ((1ull << piece) - 1ull) << (k * piece));
+      }
       const int left = sp.L - key0;
-      if (left < kTileKeys) v &= (1u << left) - 1u;
+      if (left < kTileKeys) v &= (1ull << left) - 1ull;
       sm.valid[warp][st] = v;
-      mbar_arrive_expect_tx(&sm.full[warp][st], static_cast<uint32_t>(__popc(got) / 4 * piece * (DH / 8 * 9)));
+      mbar_arrive_expect_tx(&sm.full[warp][st], static_cast<uint32_t>(__popc(got) / segs * piece * (DH / 8 * 9)));
     }
     __syncwarp();
     if (page >= 0) {
       const int tok = (key0 + pc * piece) & (P - 1);
-      bulk_load(&sm.stage[warp][st][seg_tile],
-                p.c.pool + static_cast<size_t>(page) * p.c.page_bytes + static_cast<size_t>(hk) * p.c.chunk +
-                    seg_page + tok * unit,
-                static_cast<uint32_t>(piece * unit), &sm.full[warp][st]);
+      bulk_load(&sm.stage[warp][st][seg_tile], seg_base + static_cast<size_t>(page) * p.c.page_bytes + tok * unit, bytes,
+                &sm.full[warp][st]);
     }
   };
   int page[kStages];
@@ -193,25 +212,21 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
     }
   }
   float o[NQ][kSteps][4];           // dim tile j: dims rr DH/8 + 2 j, + 1 of rows 8 n + 2 c, + 1
-  float m[NQ][2], l[NQ][2];
+  float m[NQ][2], l[NQ][2];         // reference maximum (base 2), sum
+  float limit[NQ][2];               // the unscaled score above which m rises
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    m[n][0] = m[n][1] = -INFINITY;
+    m[n][0] = m[n][1] = limit[n][0] = limit[n][1] = -INFINITY;
     l[n][0] = l[n][1] = 0.f;
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
   }
 
-  int done = 0;
-  for (int i = 0; i < mine; ++i) {
-    const int st = i % kStages;
-    if (!__all_sync(kFullMask, mbar_wait(&sm.full[warp][st], static_cast<uint32_t>((i / kStages) & 1), p.err))) break;
-    done = i + 1;
-    const uint8_t* tile = sm.stage[warp][st];
-    const int key0 = first_key(i);
-    const uint32_t valid = sm.valid[warp][st];
-    const bool plain = valid == ~0u && key0 + kTileKeys <= sp.Lp;  // all seen by every row
-    // ---- S^T of the tile's two halves of 16 keys
+  // One step of 32 keys: `at` their first in the tile, key0 its position,
+  // valid their bits.  kAll: every row sees every key.
+  auto step = [&](auto all_seen, const uint8_t* tile, int at, int key0, uint32_t valid) {
+    constexpr bool kAll = decltype(all_seen)::value != 0;
+    // ---- S^T of the two halves of 16 keys
     float s[2][NQ][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -220,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
       uint32_t w[2][DH / 32], sc[2][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int key = 16 * h + 8 * t + (rr >> 1) + 4 * (rr & 1);
+        const int key = at + 16 * h + 8 * t + (rr >> 1) + 4 * (rr & 1);
         if constexpr (DH == 128) {
           const uint4 x = *reinterpret_cast<const uint4*>(tile + key * 64 + c * 16);
           w[t][0] = x.x;
@@ -252,20 +267,19 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
         }
       }
     }
-    // ---- scores in base 2; x = 2 t + i: key 16 h + 8 t + perm(rr), row 8 n + 2 c + i
+    // ---- x = 2 t + i: key 16 h + 8 t + perm(rr), row 8 n + 2 c + i.  The
+    // scores stay as they are (a row's factor to base 2 comes with the
+    // exponent); the reference rises where one passes `limit`
     bool up = false;
     float top[NQ][2];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
+      if constexpr (!kAll) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int i2 = x & 1;
-          if (plain) {
-            s[h][n][x] *= fac[n][i2];
-          } else {
-            const int kk = 16 * h + 8 * (x >> 1) + (rr >> 1) + 4 * (rr & 1), pos = key0 + kk;
+          for (int x = 0; x < 4; ++x) {
+            const int i2 = x & 1, kk = 16 * h + 8 * (x >> 1) + (rr >> 1) + 4 * (rr & 1), pos = key0 + kk;
             bool seen = (valid >> kk) & 1u;
             if (seen && pos >= sp.Lp) {
               const int j = pos - sp.Lp;
@@ -273,13 +287,13 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
                      ((__ldg(p.mask + (static_cast<size_t>(r) * p.B + node[n][i2] - 1) * p.words + (j >> 5)) >>
                        (j & 31)) & 1u);
             }
-            s[h][n][x] = seen ? s[h][n][x] * fac[n][i2] : -INFINITY;
+            if (!seen) s[h][n][x] = -INFINITY;
           }
-        }
+      }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         top[n][x] = fmaxf(fmaxf(s[0][n][x], s[0][n][x + 2]), fmaxf(s[1][n][x], s[1][n][x + 2]));
-        up |= top[n][x] > m[n][x] + kRaise;
+        up |= top[n][x] > limit[n][x];
       }
     }
     if (__any_sync(kFullMask, up)) {
@@ -292,9 +306,11 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
 #pragma unroll
           for (int d = 4; d < 32; d *= 2) t = fmaxf(t, __shfl_xor_sync(kFullMask, t, d));
           al[x] = 1.f;
-          if (t > m[n][x] + kRaise) {
+          if (t > limit[n][x]) {
+            t *= fac[n][x];
             al[x] = ex2(m[n][x] - t);  // (0 from -inf)
             m[n][x] = t;
+            limit[n][x] = __fdividef(t + kRaise, fac[n][x]);
             l[n][x] *= al[x];
           }
         }
@@ -310,13 +326,13 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
     uint32_t pb[2][NQ][2];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      const float sub0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - kBias;
-      const float sub1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - kBias;
+      const float sub0 = m[n][0] == -INFINITY ? 0.f : kBias - m[n][0];
+      const float sub1 = m[n][1] == -INFINITY ? 0.f : kBias - m[n][1];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const float p0 = ex2(s[h][n][2 * t] - sub0), p1 = ex2(s[h][n][2 * t + 1] - sub1);
+          const float p0 = ex2(fmaf(s[h][n][2 * t], fac[n][0], sub0)), p1 = ex2(fmaf(s[h][n][2 * t + 1], fac[n][1], sub1));
           l[n][0] += p0;
           l[n][1] += p1;
           pb[h][n][t] = transpose8x8(pack_f16(p0, p1));
@@ -332,18 +348,19 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
         uint32_t b[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int kk = 16 * h + 8 * t + c + 4 * x;
+          const int kk = 16 * h + 8 * t + c + 4 * x, key = at + kk;
           if constexpr (DH == 128) {
-            const uint2 y = *reinterpret_cast<const uint2*>(vt + kk * 64 + rr * 8);
+            const uint2 y = *reinterpret_cast<const uint2*>(vt + key * 64 + rr * 8);
             vw[t][x][0] = y.x;
             vw[t][x][1] = y.y;
-            b[x] = vt[T::kCodes + kk * 8 + rr];
+            b[x] = vt[T::kCodes + key * 8 + rr];
           } else {
-            vw[t][x][0] = *reinterpret_cast<const uint32_t*>(vt + kk * 32 + rr * 4);
-            b[x] = vt[T::kCodes + kk * 4 + (rr >> 1)];
+            vw[t][x][0] = *reinterpret_cast<const uint32_t*>(vt + key * 32 + rr * 4);
+            b[x] = vt[T::kCodes + key * 4 + (rr >> 1)];
           }
           // what lies behind the keys may be anything: a zero weight needs a finite value
-          if (!plain && !((valid >> kk) & 1u)) b[x] = 0;
+          if constexpr (!kAll)
+            if (!((valid >> kk) & 1u)) b[x] = 0;
         }
         vs[t] = e4m3x2_to_f16x2(b[0] | (b[1] << 8));
       }
@@ -353,8 +370,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const uint32_t x = vw[t][0][w], y = vw[t][1][w];
-          e2m1x8_to_f16((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), ev[t]);
-          e2m1x8_to_f16(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), od[t]);
+          e2m1x8_to_f16(bit_select(0x0F0F0F0Fu, x, y << 4), ev[t]);
+          e2m1x8_to_f16(bit_select(0x0F0F0F0Fu, x >> 4, y), od[t]);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -365,8 +382,26 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
         }
       }
     }
-    // the stage is free: the tile three on goes there, and its successor's
-    // page is looked up
+  };
+
+  int done = 0;
+  for (int i = 0; i < mine; ++i) {
+    const int st = i % kStages;
+    if (!__all_sync(kFullMask, mbar_wait(&sm.full[warp][st], static_cast<uint32_t>((i / kStages) & 1), p.err))) break;
+    done = i + 1;
+    const uint8_t* tile = sm.stage[warp][st];
+    const int key0 = first_key(i);
+    const uint64_t valid = sm.valid[warp][st];
+    if (valid == ~0ull && key0 + kTileKeys <= sp.Lp) {
+#pragma unroll 1
+      for (int at = 0; at < kTileKeys; at += kStep) step(IntC<1>{}, tile, at, key0 + at, ~0u);
+    } else {
+#pragma unroll 1
+      for (int at = 0; at < kTileKeys; at += kStep)
+        if (static_cast<uint32_t>(valid >> at)) step(IntC<0>{}, tile, at, key0 + at, static_cast<uint32_t>(valid >> at));
+    }
+    // the stage is free: the tile after the next goes there, and its
+    // successor's page is looked up
     __syncwarp();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     issue(i + kStages, next_page);
@@ -392,7 +427,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
         *reinterpret_cast<float4*>(dst + 2 * j) =
             make_float4(o[n][j][x], o[n][j][x + 2], o[n][j + 1][x], o[n][j + 1][x + 2]);
     }
-  __syncthreads();
+  if (p.cluster) cluster_sync();  // (every CTA's stages are free: the rows may be sent)
+  else __syncthreads();
   // ---- the four warps' shares of each row, joined in warp order
   for (int row = warp; row < min(live, kRows); row += kWarps) {
     float M = -INFINITY;
@@ -412,7 +448,14 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) v[e] += sm.red[w][row][lane * kE + e] * f[w];
     }
-    if (p.n_split > 1) {
+    if (p.cluster) {
+      // row i is the (i / n)-th that CTA i % n joins
+      const int owner = row % p.n_split, at = split * ((kRows + p.n_split - 1) / p.n_split) + row / p.n_split;
+      float* dst = at_rank(&sm.recv[at][0], owner);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) dst[lane * kE + e] = v[e];
+      if (lane == 0) *at_rank(&sm.recv_ml[at], owner) = make_float2(M, L);
+    } else if (p.n_split > 1) {
       float* dst = cache_part_row(p, r, hk, 0, split, row);
 #pragma unroll
       for (int e = 0; e < kE; e += 2)
@@ -425,14 +468,42 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 4 : 3) k_cache_attention(c
       for (int e = 0; e < kE; e += 2) dst[e / 2] = pack_bf16(v[e] * inv, v[e + 1] * inv);
     }
   }
+  if (!p.cluster) return;
+  cluster_sync();
+  // ---- the rows this CTA joins, in split order
+  const int each = (kRows + p.n_split - 1) / p.n_split;
+  for (int row = split + warp * p.n_split; row < min(live, kRows); row += kWarps * p.n_split) {
+    const int at = row / p.n_split;
+    float M = -INFINITY, L = 0.f;
+    for (int k = 0; k < p.n_split; ++k) M = fmaxf(M, sm.recv_ml[k * each + at].x);
+    constexpr int kE = DH / 32;
+    float v[kE];
+#pragma unroll
+    for (int e = 0; e < kE; ++e) v[e] = 0.f;
+    for (int k = 0; k < p.n_split; ++k) {
+      const float2 ml = sm.recv_ml[k * each + at];
+      const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+      L += ml.y * f;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) v[e] += sm.recv[k * each + at][lane * kE + e] * f;
+    }
+    const float inv = L > 0.f ? p.c.v_scale / L : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row(p, r, hk, row) + lane * kE);
+#pragma unroll
+    for (int e = 0; e < kE; e += 2) dst[e / 2] = pack_bf16(v[e] * inv, v[e + 1] * inv);
+  }
 }
 
 template <int DH, int NQ>
 cudaError_t launch_rows(const CacheAttnParams& p, cudaStream_t st) {
-  cudaError_t e = set_max_dynamic_smem(k_cache_attention<DH, NQ>);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = opt_in_smem(k_cache_attention<DH, NQ>, &done);
   if (e != cudaSuccess) return e;
-  return launch_kernel(k_cache_attention<DH, NQ>, dim3(p.n_split, p.c.Hkv, p.R), dim3(kThreads),
-                       sizeof(AttnSmem<DH, NQ>), st, false, p);
+  const dim3 grid(p.n_split, p.c.Hkv, p.R);
+  if (p.cluster)
+    return launch_kernel_cluster(k_cache_attention<DH, NQ>, grid, dim3(kThreads), sizeof(AttnSmem<DH, NQ>), st, false,
+                                 p.n_split, p);
+  return launch_kernel(k_cache_attention<DH, NQ>, grid, dim3(kThreads), sizeof(AttnSmem<DH, NQ>), st, false, p);
 }
 
 // The shares of each row over the key splits, joined in a fixed order: M =
@@ -511,14 +582,18 @@ cudaError_t launch_join(const CacheAttnParams& p, cudaStream_t st) {
 }
 
 // How a call is cut: up to kTreeRows rows per key/value head by the kernel
-// above, in tiles of 32 keys, four warps a tile each; more by the tensor-core
+// above, in tiles of 64 keys, four warps a tile each; more by the tensor-core
 // kernel in tiles of 128 rows and 128 keys.  The keys are split until the GPU
-// is full: here two waves of the four CTAs that an SM holds, a tile per warp
-// at least; there one wave of one CTA per SM.
+// is full: here once over (three CTAs per SM), a tile per warp at least, and
+// at the latest every 2048 keys, so that sequences of different lengths share
+// the SMs evenly; there one wave of one CTA per SM.  Up to eight splits that
+// are all resident at once are a thread-block cluster each and join in shared
+// memory: no second kernel and no workspace for short sequences.
 constexpr int kTreeRows = 16;
+constexpr int kSplitTiles = 32;  // 2048 keys
 
 struct Plan {
-  int tile_rows, tile_keys, m_tiles, n_split, split_tiles;
+  int tile_rows, tile_keys, m_tiles, n_split, split_tiles, cluster;
   size_t work;
 };
 
@@ -531,14 +606,16 @@ Plan plan_of(int R, int B, int max_len, int Hq, int Hkv, int dh) {
   pl.m_tiles = static_cast<int>((rows + pl.tile_rows - 1) / pl.tile_rows);
   const int tiles = max_len < 1 ? 1 : (max_len - 1) / pl.tile_keys + 1;
   const long long ctas = static_cast<long long>(R) * Hkv * pl.m_tiles;
-  long long n = tree ? 152 / ctas : (152 * 8 + ctas - 1) / ctas;
+  long long n = tree ? 152 / ctas : (152 * 3 + ctas - 1) / ctas;
+  if (!tree && n < (tiles + kSplitTiles - 1) / kSplitTiles) n = (tiles + kSplitTiles - 1) / kSplitTiles;
   const long long most = tree ? (tiles + 1) / 2 : (tiles + kWarps - 1) / kWarps;
   n = n < most ? n : most;
   n = n < 1 ? 1 : n;
   pl.split_tiles = static_cast<int>((tiles + n - 1) / n);
   if (!tree) pl.split_tiles = (pl.split_tiles + kWarps - 1) / kWarps * kWarps;
   pl.n_split = (tiles + pl.split_tiles - 1) / pl.split_tiles;
-  pl.work = pl.n_split > 1 ? static_cast<size_t>(ctas) * pl.n_split * pl.tile_rows * (dh + 2) * sizeof(float) : 0;
+  pl.cluster = !tree && pl.n_split > 1 && pl.n_split <= kMaxCluster && ctas * pl.n_split <= 152 * 2;
+  pl.work = pl.n_split > 1 && !pl.cluster ? static_cast<size_t>(ctas) * pl.n_split * pl.tile_rows * (dh + 2) * sizeof(float) : 0;
   return pl;
 }
 
@@ -599,6 +676,7 @@ extern "C" dartree_status dartree_cache_attention(const dartree_cache* cache, in
   p.m_tiles = pl.m_tiles;
   p.n_split = pl.n_split;
   p.split_tiles = pl.split_tiles;
+  p.cluster = pl.cluster;
   p.scale_log2 = scale * 1.4426950408889634f * p.c.k_scale;
   p.O = static_cast<uint16_t*>(O);
   p.part = static_cast<float*>(work);
@@ -614,6 +692,6 @@ extern "C" dartree_status dartree_cache_attention(const dartree_cache* cache, in
   } else {
     e = dh == 128 ? launch_rows<128, 2>(p, st) : launch_rows<64, 2>(p, st);
   }
-  if (e == cudaSuccess && pl.n_split > 1) e = dh == 128 ? launch_join<128>(p, st) : launch_join<64>(p, st);
+  if (e == cudaSuccess && pl.n_split > 1 && !pl.cluster) e = dh == 128 ? launch_join<128>(p, st) : launch_join<64>(p, st);
   return cache_launched(e);
 }

@@ -20,6 +20,7 @@ struct CacheAttnParams {
   int tile_rows, tile_keys;  // of the kernel: 16 x 64 or 128 x 128
   int m_tiles;               // row tiles
   int n_split, split_tiles;  // key tiles per split
+  int cluster;               // the splits are one cluster and join there
   float scale_log2;          // scale * log2(e) * k_scale
   uint16_t* O;               // [R][B+1][Hq][dh]
   float* part;               // [R][Hkv][m_tiles][n_split][tile_rows][dh + 2] (n_split > 1)

@@ -549,14 +549,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
 
 cudaError_t launch_cache_tree(const CacheAttnParams& p, cudaStream_t st) {
   const dim3 grid(p.m_tiles * p.n_split, p.c.Hkv, p.R);
-  if (p.c.dh == 128) {
-    cudaError_t e = set_max_dynamic_smem(k_cache_tree<128>);
-    if (e != cudaSuccess) return e;
-    return launch_kernel(k_cache_tree<128>, grid, dim3(kTreeThreads), TreeSmem<128>::kTotal + 1024, st, false, p);
-  }
-  cudaError_t e = set_max_dynamic_smem(k_cache_tree<64>);
+  static std::atomic<uint64_t> done128{0}, done64{0};
+  cudaError_t e = p.c.dh == 128 ? opt_in_smem(k_cache_tree<128>, &done128) : opt_in_smem(k_cache_tree<64>, &done64);
   if (e != cudaSuccess) return e;
-  return launch_kernel(k_cache_tree<64>, grid, dim3(kTreeThreads), TreeSmem<64>::kTotal + 1024, st, false, p);
+  return launch_kernel(p.c.dh == 128 ? k_cache_tree<128> : k_cache_tree<64>, grid, dim3(kTreeThreads),
+                       (p.c.dh == 128 ? TreeSmem<128>::kTotal : TreeSmem<64>::kTotal) + 1024, st, false, p);
 }
 
 }  // namespace dt

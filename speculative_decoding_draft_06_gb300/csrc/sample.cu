@@ -124,19 +124,6 @@ struct Smem {
   Ctl ctl;
 };
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// The same object in CTA `rank` of the cluster.
-template <typename T>
-__device__ __forceinline__ T* at_rank(T* p, int rank) {
-  uint64_t out;
-  asm volatile("mapa.u64 %0, %1, %2;" : "=l"(out) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
-  return reinterpret_cast<T*>(out);
-}
-
 // One row's weights.
 struct Weights {
   float top;      // the largest logit
@@ -1220,7 +1207,8 @@ extern "C" dartree_status dartree_sample(const void* logits, int32_t bf16, int64
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (static_cast<long long>(rows) * cl > 0x7FFFFFFFll) return cache_fail(DARTREE_ERR_UNSUPPORTED, "too many rows");
   const dim3 grid(static_cast<unsigned>(rows) * cl);
-  cudaError_t e = set_max_dynamic_smem(bf16 ? k_sample<uint16_t> : k_sample<float>);
+  static std::atomic<uint64_t> done_bf16{0}, done_f32{0};
+  cudaError_t e = bf16 ? opt_in_smem(k_sample<uint16_t>, &done_bf16) : opt_in_smem(k_sample<float>, &done_f32);
   if (e == cudaSuccess)
     e = launch_kernel_cluster(bf16 ? k_sample<uint16_t> : k_sample<float>, grid, dim3(kThreads), sizeof(Smem), st,
                               false, cl, p);

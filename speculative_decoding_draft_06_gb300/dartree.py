@@ -498,20 +498,21 @@ def accept(parent, token, n_out, pred, *, max_len: int, stream=None) -> dict:
 
 # ------------------------------------------------------- paged 4-bit cache
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_I32 = torch.int32
 
 
-def _ints(name: str, t: torch.Tensor, dev, shape) -> int:
-    """Address of a dense int32 tensor of that shape on that device."""
-    if t.dtype is not torch.int32 or t.device != dev or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous int32 tensor on {dev}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t.data_ptr()
+def _ints(name: str, t: torch.Tensor, idx: int, n: int) -> int:
+    """Address of a dense int32 tensor of n entries on CUDA device idx."""
+    if t.dtype is _I32 and t.numel() == n and t.is_contiguous() and t.get_device() == idx:
+        return t.data_ptr()
+    if t.dtype is not _I32 or not t.is_contiguous() or t.get_device() != idx:
+        raise TypeError(f"{name} must be a contiguous int32 tensor on cuda:{idx}")
+    raise ValueError(f"{name} has {t.numel()} entries, expected {n}")
 
 
-def _floats(name: str, t: torch.Tensor, dev, n: int) -> int:
-    if t.dtype is not torch.float32 or t.device != dev or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous fp32 tensor on {dev}")
+def _floats(name: str, t: torch.Tensor, idx: int, n: int) -> int:
+    if t.dtype is not torch.float32 or not t.is_contiguous() or t.get_device() != idx:
+        raise TypeError(f"{name} must be a contiguous fp32 tensor on cuda:{idx}")
     if t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} entries, expected {n}")
     return t.data_ptr()
@@ -526,22 +527,23 @@ def _alloc(stream, shape, dtype, dev, zero: bool = False) -> torch.Tensor:
         return make(shape, dtype=dtype, device=dev)
 
 
-class _on:
-    """Runs a call with the tensors' device current and gives its stream."""
+# the current stream's handle without a Stream object (which costs as much as
+# the rest of a call), where PyTorch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda idx: torch.cuda.current_stream(idx).cuda_stream)
 
-    def __init__(self, dev, stream):
-        self.dev, self.stream, self.back = dev, stream, None
 
-    def __enter__(self) -> int:
-        if torch.cuda.current_device() != self.dev.index:
-            self.back = torch.cuda.current_device()
-            torch.cuda.set_device(self.dev)
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.dev)
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+def _launch(fn, idx: int, stream, *args) -> None:
+    """Calls fn(*args, stream) with the tensors' device current; raises on an
+    error."""
+    st = _raw_stream(idx) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == idx:
+        s = fn(*args, st)
+    else:
+        with torch.cuda.device(idx):
+            s = fn(*args, st)
+    if s != 0:
+        _check_free(s)
 
 
 class KVCache:
@@ -572,8 +574,8 @@ class KVCache:
                              f"{(layers, pages, self.page_bytes)}")
         if refs is None:
             refs = torch.zeros(pages, dtype=torch.int32, device=pool.device)
-        self.dev = pool.device
-        _ints("refs", refs, self.dev, (pages,))
+        self.dev, self._idx = pool.device, pool.get_device()
+        _ints("refs", refs, self._idx, pages)
         self.pool, self.refs = pool, refs
         self.layers, self.pages, self.page_tokens, self.Hkv, self.dh = (layers, pages, page_tokens,
                                                                         Hkv, dh)
@@ -582,13 +584,13 @@ class KVCache:
                         k_scale, v_scale)
         self._ref = ctypes.byref(self._c)
         self._err = self.err.data_ptr()
+        self._work_bytes: dict = {}  # workspace sizes by (R, B, max_len, Hq)
 
     def _seqs(self, table: torch.Tensor, lens: torch.Tensor):
-        if table.dim() != 2:
-            raise ValueError("table must be [R, max_pages]")
+        """Addresses and sizes of a page table and its lengths."""
         R, width = table.shape
-        return _ints("table", table, self.dev, (R, width)), width, \
-            _ints("lens", lens, self.dev, (R,)), R
+        idx = self._idx
+        return _ints("table", table, idx, R * width), width, _ints("lens", lens, idx, R), R
 
     def check(self) -> None:
         """Synchronises and raises if a call since the last check met a bad
@@ -604,23 +606,22 @@ class KVCache:
         + i (dartree_cache_append); request and token strides are free, the
         same in both."""
         t, width, ln, R = self._seqs(table, lens)
+        idx, Hkv, dh = self._idx, self.Hkv, self.dh
         for name, x in (("K", K), ("V", V)):
-            if x.dtype not in _BF16 or x.device != self.dev:
+            if x.dtype not in _BF16 or x.get_device() != idx:
                 raise TypeError(f"{name} must be a bf16 tensor on {self.dev}")
         n = K.shape[1]
-        if K.shape != (R, n, self.Hkv, self.dh) or V.shape != K.shape:
+        if K.shape != (R, n, Hkv, dh) or V.shape != K.shape:
             raise ValueError(f"K {tuple(K.shape)} / V {tuple(V.shape)} do not match R={R}, "
-                             f"Hkv={self.Hkv}, dh={self.dh}")
+                             f"Hkv={Hkv}, dh={dh}")
         sr, sn, sh, sd = K.stride()
-        if V.stride() != K.stride() or (sd != 1 and self.dh > 1) or (sh != self.dh and self.Hkv > 1):
+        if V.stride() != (sr, sn, sh, sd) or sd != 1 or (sh != dh and Hkv > 1):
             raise ValueError("K and V need equal strides, dense in heads and dims")
-        if n == 1:
-            sn = max(sn, self.Hkv * self.dh)
-        with _on(self.dev, stream) as st:
-            _check_free(self._lib.dartree_cache_append(
-                self._ref, layer, K.data_ptr(), V.data_ptr(), sr, sn, t, width, ln, offset,
-                None if count is None else _ints("count", count, self.dev, (R,)), R, n, self._err,
-                st))
+        if n == 1 and sn < Hkv * dh:
+            sn = Hkv * dh
+        _launch(self._lib.dartree_cache_append, idx, stream, self._ref, layer, K.data_ptr(),
+                V.data_ptr(), sr, sn, t, width, ln, offset,
+                None if count is None else _ints("count", count, idx, R), R, n, self._err)
 
     def read(self, layer: int, table, lens, n: int, *, offset: int = 0,
              count: torch.Tensor | None = None, out: tuple | None = None, stream=None) -> tuple:
@@ -633,15 +634,13 @@ class KVCache:
             both = _alloc(stream, (2, *shape), torch.bfloat16, self.dev, count is not None)
             out = (both[0], both[1])
         for x in out:
-            if x.dtype not in _BF16 or x.device != self.dev or not x.is_contiguous():
+            if x.dtype not in _BF16 or x.get_device() != self._idx or not x.is_contiguous():
                 raise TypeError(f"out must be contiguous bf16 tensors on {self.dev}")
             if x.shape != shape:
                 raise ValueError(f"out has shape {tuple(x.shape)}, expected {shape}")
-        with _on(self.dev, stream) as st:
-            _check_free(self._lib.dartree_cache_read(
-                self._ref, layer, out[0].data_ptr(), out[1].data_ptr(), t, width, ln, offset,
-                None if count is None else _ints("count", count, self.dev, (R,)), R, n, self._err,
-                st))
+        _launch(self._lib.dartree_cache_read, self._idx, stream, self._ref, layer,
+                out[0].data_ptr(), out[1].data_ptr(), t, width, ln, offset,
+                None if count is None else _ints("count", count, self._idx, R), R, n, self._err)
         return out
 
     def attention(self, layer: int, Q: torch.Tensor, table, lens, *, max_len: int,
@@ -653,43 +652,50 @@ class KVCache:
         -> O bf16 [R, B+1, Hq, dh].  ``max_len`` bounds lens[r] + n_nodes[r].
         Rows behind n_nodes[r] keep what ``out`` holds (zeros in a new one)."""
         t, width, ln, R = self._seqs(table, lens)
-        if Q.dtype not in _BF16 or Q.device != self.dev:
+        idx, dh = self._idx, self.dh
+        if Q.dtype not in _BF16 or Q.get_device() != idx:
             raise TypeError(f"Q must be a bf16 tensor on {self.dev}")
-        if Q.dim() != 4 or Q.shape[0] != R or Q.shape[1] < 1 or Q.shape[3] != self.dh:
-            raise ValueError(f"Q {tuple(Q.shape)} does not match R={R}, dh={self.dh}")
-        B, Hq = Q.shape[1] - 1, Q.shape[2]
+        r, rows, Hq, d = Q.shape
+        if r != R or rows < 1 or d != dh:
+            raise ValueError(f"Q {tuple(Q.shape)} does not match R={R}, dh={dh}")
+        B, sq = rows - 1, Hq * dh
         if Hq % self.Hkv:
             raise ValueError(f"{Hq} query heads are not a multiple of {self.Hkv}")
-        if Q.is_contiguous():
-            sq = Hq * self.dh
-        else:
-            sr, sq, sh, sd = Q.stride()
-            if B == 0:
-                sq = sr if R > 1 else max(sq, Hq * self.dh)
-            if (sr != (B + 1) * sq and R > 1) or sh != self.dh or sd != 1:
+        if not Q.is_contiguous():
+            sr, s1, sh, sd = Q.stride()
+            sq = s1 if B else max(sr, sq)
+            if (sr != rows * sq and R > 1) or (sh != dh and Hq > 1) or sd != 1:
                 raise ValueError("Q needs one stride between rows, dense in heads and dims")
         m = None
         if B > 0:
             if mask is None:
                 raise ValueError("a tree needs its mask")
-            m = _ints("mask", mask, self.dev, (R, B, (B + 31) // 32))
-        nn = None if n_nodes is None else _ints("n_nodes", n_nodes, self.dev, (R,))
+            m = _ints("mask", mask, idx, R * B * ((B + 31) // 32))
+        nn = None if n_nodes is None else _ints("n_nodes", n_nodes, idx, R)
         if out is None:
-            out = _alloc(stream, (R, B + 1, Hq, self.dh), torch.bfloat16, self.dev,
-                         n_nodes is not None)
-        elif out.dtype not in _BF16 or out.device != self.dev or not out.is_contiguous():
+            out = _alloc(stream, (R, rows, Hq, dh), torch.bfloat16, self.dev, n_nodes is not None)
+        elif out.dtype not in _BF16 or out.get_device() != idx or not out.is_contiguous():
             raise TypeError(f"out must be a contiguous bf16 tensor on {self.dev}")
-        elif out.shape != (R, B + 1, Hq, self.dh):
+        elif out.shape != (R, rows, Hq, dh):
             raise ValueError(f"out has shape {tuple(out.shape)}")
-        need = self._lib.dartree_cache_attention_workspace(R, B, max_len, Hq, self.Hkv, self.dh)
-        if work is None and need:
+        key = (R, B, max_len, Hq)
+        need = self._work_bytes.get(key)
+        if need is None:
+            if len(self._work_bytes) > 4096:
+                self._work_bytes.clear()
+            need = self._work_bytes[key] = int(
+                self._lib.dartree_cache_attention_workspace(R, B, max_len, Hq, self.Hkv, dh))
+        wp, wb = None, 0
+        if work is not None:
+            if not work.is_contiguous() or work.get_device() != idx:
+                raise TypeError(f"work must be a contiguous tensor on {self.dev}")
+            wp, wb = work.data_ptr(), work.numel() * work.element_size()
+        elif need:
             work = _alloc(stream, (need,), torch.uint8, self.dev)
-        with _on(self.dev, stream) as st:
-            _check_free(self._lib.dartree_cache_attention(
-                self._ref, layer, Q.data_ptr(), sq, m, nn, t, width, ln, R, B, max_len, Hq,
-                float(scale) if scale is not None else self.dh ** -0.5, out.data_ptr(),
-                None if work is None else work.data_ptr(),
-                0 if work is None else work.numel() * work.element_size(), self._err, st))
+            wp, wb = work.data_ptr(), need
+        _launch(self._lib.dartree_cache_attention, idx, stream, self._ref, layer, Q.data_ptr(), sq, m,
+                nn, t, width, ln, R, B, max_len, Hq, dh ** -0.5 if scale is None else scale,
+                out.data_ptr(), wp, wb, self._err)
         return out
 
     # ------------------------------------------------------ page operations
@@ -697,11 +703,9 @@ class KVCache:
         """Pages for want[r] more tokens per row -> ok [R] int32
         (dartree_cache_reserve)."""
         t, width, ln, R = self._seqs(table, lens)
-        w = _ints("want", want, self.dev, (R,))
-        ok = _alloc(stream, (R,), torch.int32, self.dev)
-        with _on(self.dev, stream) as st:
-            _check_free(self._lib.dartree_cache_reserve(self._ref, t, width, ln, w, R,
-                                                        ok.data_ptr(), st))
+        ok = _alloc(stream, (R,), _I32, self.dev)
+        _launch(self._lib.dartree_cache_reserve, self._idx, stream, self._ref, t, width, ln,
+                _ints("want", want, self._idx, R), R, ok.data_ptr())
         return ok
 
     def fork(self, table, lens, src, dst, *, stream=None) -> torch.Tensor:
@@ -709,11 +713,9 @@ class KVCache:
         (dartree_cache_fork)."""
         t, width, ln, R = self._seqs(table, lens)
         n = src.numel()
-        a, b = _ints("src", src, self.dev, (n,)), _ints("dst", dst, self.dev, (n,))
-        ok = _alloc(stream, (n,), torch.int32, self.dev)
-        with _on(self.dev, stream) as st:
-            _check_free(self._lib.dartree_cache_fork(self._ref, t, width, ln, R, a, b, n,
-                                                     ok.data_ptr(), st))
+        ok = _alloc(stream, (n,), _I32, self.dev)
+        _launch(self._lib.dartree_cache_fork, self._idx, stream, self._ref, t, width, ln, R,
+                _ints("src", src, self._idx, n), _ints("dst", dst, self._idx, n), n, ok.data_ptr())
         return ok
 
     def commit(self, table, lens, nodes, length, *, extra: int = 0, stream=None) -> None:
@@ -721,31 +723,25 @@ class KVCache:
         length[r] + extra to lens (dartree_cache_commit); nodes [R, max_len]
         and length [R] as :func:`accept` returns them."""
         t, width, ln, R = self._seqs(table, lens)
-        if nodes.dim() != 2:
-            raise ValueError("nodes must be [R, max_len]")
-        most = nodes.shape[1]
-        a, b = _ints("nodes", nodes, self.dev, (R, most)), _ints("length", length, self.dev, (R,))
-        with _on(self.dev, stream) as st:
-            _check_free(self._lib.dartree_cache_commit(self._ref, t, width, ln, a, b, R, most,
-                                                       extra, self._err, st))
+        r, most = nodes.shape
+        _launch(self._lib.dartree_cache_commit, self._idx, stream, self._ref, t, width, ln,
+                _ints("nodes", nodes, self._idx, R * most), _ints("length", length, self._idx, R), R,
+                most, extra, self._err)
 
     def release(self, table, lens, rows, keep, *, stream=None) -> None:
         """Rows keep their first keep[i] tokens; pages behind them go back
         (dartree_cache_release)."""
         t, width, ln, R = self._seqs(table, lens)
         n = rows.numel()
-        a, b = _ints("rows", rows, self.dev, (n,)), _ints("keep", keep, self.dev, (n,))
-        with _on(self.dev, stream) as st:
-            _check_free(self._lib.dartree_cache_release(self._ref, t, width, ln, R, a, b, n,
-                                                        self._err, st))
+        _launch(self._lib.dartree_cache_release, self._idx, stream, self._ref, t, width, ln, R,
+                _ints("rows", rows, self._idx, n), _ints("keep", keep, self._idx, n), n, self._err)
 
     def copy_pages(self, src, dst, *, stream=None) -> None:
         """Copies pages src[i] to dst[i] in all layers
         (dartree_cache_copy_pages)."""
         n = src.numel()
-        a, b = _ints("src", src, self.dev, (n,)), _ints("dst", dst, self.dev, (n,))
-        with _on(self.dev, stream) as st:
-            _check_free(self._lib.dartree_cache_copy_pages(self._ref, a, b, n, self._err, st))
+        _launch(self._lib.dartree_cache_copy_pages, self._idx, stream, self._ref,
+                _ints("src", src, self._idx, n), _ints("dst", dst, self._idx, n), n, self._err)
 
 
 def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: torch.Tensor | None = None,
@@ -763,17 +759,16 @@ def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: torch.Tensor |
     rows, V = logits.shape
     if rows < 1 or V < 1 or rows_per_req < 1:
         raise ValueError("logits and rows_per_req must not be empty")
-    dev, n = logits.device, -(-rows // rows_per_req)
-    ptr = [None if t is None else
-           (_ints(name, t, dev, (n,)) if name == "top_k" else _floats(name, t, dev, n))
-           for name, t in (("temperature", temperature), ("top_k", top_k), ("top_p", top_p),
-                           ("min_p", min_p))]
-    up = _floats("u", u, dev, rows)
-    token = _alloc(stream, (rows,), torch.int32, dev)
-    prob = _alloc(stream, (rows,), torch.float32, dev)
-    with _on(dev, stream) as st:
-        _check_free(load().dartree_sample(
-            logits.data_ptr(), 1 if logits.dtype is torch.bfloat16 else 0,
-            logits.stride(0) if rows > 1 else max(V, logits.stride(0)), V, rows, rows_per_req,
-            *ptr, up, token.data_ptr(), prob.data_ptr(), st))
+    idx, n = logits.get_device(), -(-rows // rows_per_req)
+    T = None if temperature is None else _floats("temperature", temperature, idx, n)
+    k = None if top_k is None else _ints("top_k", top_k, idx, n)
+    p = None if top_p is None else _floats("top_p", top_p, idx, n)
+    m = None if min_p is None else _floats("min_p", min_p, idx, n)
+    up = _floats("u", u, idx, rows)
+    token = _alloc(stream, (rows,), _I32, logits.device)
+    prob = _alloc(stream, (rows,), torch.float32, logits.device)
+    _launch(load().dartree_sample, idx, stream, logits.data_ptr(),
+            1 if logits.dtype is torch.bfloat16 else 0,
+            logits.stride(0) if rows > 1 else max(V, logits.stride(0)), V, rows, rows_per_req, T, k,
+            p, m, up, token.data_ptr(), prob.data_ptr())
     return {"token": token, "prob": prob}
