@@ -41,22 +41,6 @@ constexpr int kThreads = kWarps * 32;
 
 __device__ int g_cache_err;  // error word when the caller passes none
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// A 16x8 block of fp16 pairs, rows to columns: lane (r, c)'s pair (row r,
-// columns 2c, 2c + 1) of an 8x8 matrix becomes (column r, rows 2c, 2c + 1).
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t y;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-
 // Bits of x where the mask has ones, of y where it has zeros.
 __device__ __forceinline__ uint32_t bit_select(uint32_t mask, uint32_t x, uint32_t y) {
   uint32_t d;
@@ -525,9 +509,11 @@ __global__ void __launch_bounds__(256) k_cache_attention_join(const CacheAttnPar
 #pragma unroll
   for (int e = 0; e < kE; ++e) v[e] = 0.f;
   if (on) {
-    const int mt = q / p.tile_rows;
+    // (the rows behind a request's last whole tile may be that tile's tail)
+    int mt = q / p.tile_rows;
+    if (p.part_rows > p.tile_rows && mt > 0 && (sp.n + 1) * p.g - mt * p.tile_rows <= kTreeTail) --mt;
     const int ns = (row_tile_keys(p, sp, mt) + p.split_tiles - 1) / p.split_tiles;  // splits that had keys
-    const size_t step = static_cast<size_t>(p.tile_rows) * (DH + 2);
+    const size_t step = static_cast<size_t>(p.part_rows) * (DH + 2);
     const float* src = cache_part_row(p, r, hk, mt, 0, q - mt * p.tile_rows);
     for (int s = w + lane * W; s < ns; s += 32 * W) M = fmaxf(M, src[s * step]);
 #pragma unroll
@@ -583,7 +569,7 @@ cudaError_t launch_join(const CacheAttnParams& p, cudaStream_t st) {
 
 // How a call is cut: up to kTreeRows rows per key/value head by the kernel
 // above, in tiles of 64 keys, four warps a tile each; more by the tensor-core
-// kernel in tiles of 128 rows and 128 keys.  The keys are split until the GPU
+// kernel in tiles of 256 rows and 128 keys.  The keys are split until the GPU
 // is full: here once over (three CTAs per SM), a tile per warp at least, and
 // at the latest every 2048 keys, so that sequences of different lengths share
 // the SMs evenly; there one wave of one CTA per SM.  Up to eight splits that
@@ -593,7 +579,7 @@ constexpr int kTreeRows = 16;
 constexpr int kSplitTiles = 32;  // 2048 keys
 
 struct Plan {
-  int tile_rows, tile_keys, m_tiles, n_split, split_tiles, cluster;
+  int tile_rows, part_rows, tile_keys, m_tiles, n_split, split_tiles, cluster;
   size_t work;
 };
 
@@ -601,21 +587,24 @@ Plan plan_of(int R, int B, int max_len, int Hq, int Hkv, int dh) {
   Plan pl;
   const long long rows = static_cast<long long>(B + 1) * (Hq / Hkv);
   const bool tree = rows > kTreeRows;
-  pl.tile_rows = tree ? 128 : rows > 8 ? 16 : 8;
+  pl.tile_rows = tree ? kTreeRowsCta : rows > 8 ? 16 : 8;
+  pl.part_rows = tree ? kTreeRowsCta + kTreeTail : pl.tile_rows;
   pl.tile_keys = tree ? 128 : kTileKeys;
+  // (a request with fewer nodes than B may end in any tile)
   pl.m_tiles = static_cast<int>((rows + pl.tile_rows - 1) / pl.tile_rows);
+  if (tree && pl.m_tiles > 1 && rows % kTreeRowsCta != 0 && rows % kTreeRowsCta <= kTreeTail) --pl.m_tiles;
   const int tiles = max_len < 1 ? 1 : (max_len - 1) / pl.tile_keys + 1;
   const long long ctas = static_cast<long long>(R) * Hkv * pl.m_tiles;
   long long n = tree ? 152 / ctas : (152 * 3 + ctas - 1) / ctas;
   if (!tree && n < (tiles + kSplitTiles - 1) / kSplitTiles) n = (tiles + kSplitTiles - 1) / kSplitTiles;
-  const long long most = tree ? (tiles + 1) / 2 : (tiles + kWarps - 1) / kWarps;
+  const long long most = tree ? (tiles + 3) / 4 : (tiles + kWarps - 1) / kWarps;
   n = n < most ? n : most;
   n = n < 1 ? 1 : n;
   pl.split_tiles = static_cast<int>((tiles + n - 1) / n);
   if (!tree) pl.split_tiles = (pl.split_tiles + kWarps - 1) / kWarps * kWarps;
   pl.n_split = (tiles + pl.split_tiles - 1) / pl.split_tiles;
   pl.cluster = !tree && pl.n_split > 1 && pl.n_split <= kMaxCluster && ctas * pl.n_split <= 152 * 2;
-  pl.work = pl.n_split > 1 && !pl.cluster ? static_cast<size_t>(ctas) * pl.n_split * pl.tile_rows * (dh + 2) * sizeof(float) : 0;
+  pl.work = pl.n_split > 1 && !pl.cluster ? static_cast<size_t>(ctas) * pl.n_split * pl.part_rows * (dh + 2) * sizeof(float) : 0;
   return pl;
 }
 
@@ -672,6 +661,7 @@ extern "C" dartree_status dartree_cache_attention(const dartree_cache* cache, in
   p.words = (B + 31) / 32;
   p.rows = (B + 1) * p.g;
   p.tile_rows = pl.tile_rows;
+  p.part_rows = pl.part_rows;
   p.tile_keys = pl.tile_keys;
   p.m_tiles = pl.m_tiles;
   p.n_split = pl.n_split;
@@ -685,7 +675,7 @@ extern "C" dartree_status dartree_cache_attention(const dartree_cache* cache, in
   cudaError_t e = cudaSuccess;
   if (!p.err) e = cudaGetSymbolAddress(reinterpret_cast<void**>(&p.err), g_cache_err);
   if (e != cudaSuccess) return cache_launched(e);
-  if (pl.tile_rows == 128) {
+  if (pl.tile_rows == kTreeRowsCta) {
     e = launch_cache_tree(p, st);
   } else if (pl.tile_rows == 8) {
     e = dh == 128 ? launch_rows<128, 1>(p, st) : launch_rows<64, 1>(p, st);

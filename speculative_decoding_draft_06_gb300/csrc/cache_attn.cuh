@@ -10,6 +10,10 @@ namespace dt {
 constexpr float kBias = 6.f;   // the reference maximum's weight is 2^kBias
 constexpr float kRaise = 8.f;  // the reference rises when a score passes it by this
 
+// Rows of a CTA of the tensor-core kernel: two tiles of 128, and up to
+// kTreeTail more in the last.
+constexpr int kTreeRowsCta = 256, kTreeTail = 8;
+
 struct CacheAttnParams {
   CacheView c;              // the layer
   const uint16_t* Q;
@@ -17,13 +21,14 @@ struct CacheAttnParams {
   const uint32_t* mask;     // [R][B][words]
   const int32_t *n_nodes, *table, *lens;
   int max_pages, R, B, max_len, Hq, g, words, rows;
-  int tile_rows, tile_keys;  // of the kernel: 16 x 64 or 128 x 128
+  int tile_rows, tile_keys;  // of the kernel: 8 or 16 x 64, 256 x 128
+  int part_rows;             // rows of a row tile in the workspace
   int m_tiles;               // row tiles
   int n_split, split_tiles;  // key tiles per split
   int cluster;               // the splits are one cluster and join there
   float scale_log2;          // scale * log2(e) * k_scale
   uint16_t* O;               // [R][B+1][Hq][dh]
-  float* part;               // [R][Hkv][m_tiles][n_split][tile_rows][dh + 2] (n_split > 1)
+  float* part;               // [R][Hkv][m_tiles][n_split][part_rows][dh + 2] (n_split > 1)
   int* err;
 };
 
@@ -43,10 +48,10 @@ __device__ __forceinline__ bool request_span(const CacheAttnParams& p, int r, Sp
 }
 
 
-// Key tiles that the rows of row tile mt can see: the prefix and the nodes
-// up to the tile's last row's.
+// Key tiles that the rows of row tile mt (and its tail) can see: the prefix
+// and the nodes up to the tile's last row's.
 __device__ __forceinline__ int row_tile_keys(const CacheAttnParams& p, const Span& s, int mt) {
-  const int last = min(s.n, (mt * p.tile_rows + p.tile_rows - 1) / p.g);
+  const int last = min(s.n, (mt * p.tile_rows + p.part_rows - 1) / p.g);
   const int keys = min(s.L, s.Lp + last);
   return (keys + p.tile_keys - 1) / p.tile_keys;
 }
@@ -78,6 +83,23 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 
+// D (16x8, fp32) += A (16x16) B (16x8), fp16.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A 16x8 block of fp16 pairs, rows to columns: lane (r, c)'s pair (row r,
+// columns 2c, 2c + 1) of an 8x8 matrix becomes (column r, rows 2c, 2c + 1).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // Row q of a key/value head in the output (node q / g, query head hk g + q % g).
 __device__ __forceinline__ size_t cache_out_row(const CacheAttnParams& p, int r, int hk, int q) {
   const int nd = q / p.g;
@@ -88,7 +110,7 @@ __device__ __forceinline__ size_t cache_out_row(const CacheAttnParams& p, int r,
 // unnormalised outputs.
 __device__ __forceinline__ float* cache_part_row(const CacheAttnParams& p, int r, int hk, int mt, int split, int row) {
   const size_t tile = ((static_cast<size_t>(r) * p.c.Hkv + hk) * p.m_tiles + mt) * p.n_split + split;
-  return p.part + (tile * p.tile_rows + row) * (p.c.dh + 2);
+  return p.part + (tile * p.part_rows + row) * (p.c.dh + 2);
 }
 
 // The tensor-core kernel of many rows (cache_tree.cu).

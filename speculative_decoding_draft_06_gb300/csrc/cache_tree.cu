@@ -1,49 +1,51 @@
 // Attention of draft trees over the paged 4-bit cache on the 5th-generation
-// tensor cores (dartree_cache_attention with more than a few query rows per
+// tensor cores (dartree_cache_attention with more than 16 query rows per
 // key/value head).
 //
-// A CTA owns 128 query rows (one TMEM lane each) of one request and one
-// key/value head and a share of the key range, in tiles of 128 keys.  Warp
-// roles (448 threads):
-//   0-7   softmax: two warpgroups, a thread owns a row and half of each
-//         tile's keys and of the head dimensions of O;
-//   8-11  expand the tiles: codes and scales to fp16 keys and values (exact);
-//   12    producer: bulk copies of the pages' codes and scales, kRaw tiles
-//         ahead;
-//   13    TMEM owner, issues the MMAs.
-// S = Q K^T (M 128, N 128, fp16, fp32 sums) into double-buffered TMEM; P =
-// 2^(s - m + kBias) in fp16 to TMEM; O += P V with P from TMEM.  Keys and
-// values lie in shared memory in the same layout (a token's row of 64 head
-// dimensions is a 128-byte swizzled line): for S it is a K-major operand, for
-// O the same lines are MN-major (the transposed read is the tensor core's).
+// A CTA owns up to 256 query rows of one request and one key/value head, as
+// two tiles of 128 (a TMEM lane each), up to 8 more ("tail": a tree of 2^k
+// nodes and its root are a few rows more than whole tiles), and a share of
+// the key range in tiles of 128 keys.  Warp roles (480 threads):
+//   0-3, 4-7  softmax of the two row tiles: a thread owns a row;
+//   8-11      expand: codes and scales from memory to fp16 keys and values in
+//             shared memory (exact), a tile ahead in registers;
+//   12        TMEM owner, issues the MMAs;
+//   13        the tail rows, by mma.sync on the same fp16 tiles;
+//   14        (fills the warpgroup).
+// S = Q K^T (M 128, N 128, fp16, fp32 sums) into TMEM, P = 2^(s - m + kBias)
+// in fp16 over the S columns it came from, O += P V with P from TMEM.  While
+// one row tile's scores are in the softmax, the tensor cores work for the
+// other.  Keys and values lie in shared memory in the same layout (a token's
+// row of 64 head dimensions is a 128-byte swizzled line): for S it is a
+// K-major operand, for O the same lines are MN-major (the transposed read is
+// the tensor core's).
 // The running maximum is a reference that rises only when a score passes it
-// by kRaise, which rescales O in TMEM.
+// by kRaise: a row's weights are computed with the reference as it is, and
+// once more where that happens (O in TMEM is rescaled then; S(j) is issued
+// after P V(j - 1), so its arrival says that O is at rest).
+#include <type_traits>
+
 #include "cache_attn.cuh"
 
 namespace dt {
 namespace {
 
-constexpr int kRowsQ = 128, kKeys = 128, kHalf = kKeys / 2;
-constexpr int kSoftmaxWarps = 8, kExpandWarps = 4;
-constexpr int kExpandWarp0 = 8, kProducerWarp = 12, kMmaWarp = 13;
-constexpr int kTreeThreads = 14 * 32;
-constexpr int kStages = 2, kRaw = 3;
-constexpr int kValid = kRaw + 5;     // tiles from a raw tile's copy to the end of its softmax
-constexpr uint32_t kTmemCols = 512;  // S0 [0,128) S1 [128,256) O [256,256+dh) P0 [384,448) P1 [448,512)
-constexpr uint32_t kColO = 256, kColP = 384;
+constexpr int kMRows = 128, kKeys = 128;
+constexpr int kExpandWarp0 = 8, kExpandWarps = 4, kMmaWarp = 12, kTailWarp = 13;
+constexpr int kTreeThreads = 15 * 32;
+constexpr int kStages = 2;
+constexpr int kValid = 4;  // a tile's keys are expanded after the scores of two before: the softmax of three before is done
+constexpr int kTail = kTreeTail;
+constexpr uint32_t kTmemCols = 512;  // S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512); P over S
+constexpr uint32_t kColO = 256;
 
 template <int DH>
 struct TreeSmem {
   static constexpr int kTile = kKeys * DH * 2;           // fp16 keys or values of a tile
-  static constexpr int kCodes = kKeys * DH / 2, kScales = kKeys * DH / 16;
-  static constexpr int kV = kCodes + kScales, kRawBytes = 2 * kV;
-  static constexpr int kQ = 0;
-  static constexpr int kStage = kQ + kRowsQ * DH * 2;    // stage s: keys, values
-  static constexpr int kRaw0 = kStage + kStages * 2 * kTile;
-  static constexpr int kBars = kRaw0 + kRaw * kRawBytes;
-  static constexpr int kTotal = kBars + 512;
-  static constexpr int kOPitch = DH + 4;                 // floats per staged row of O
-  static_assert(kRowsQ * kOPitch * 4 <= kStages * 2 * kTile + kRaw * kRawBytes, "O is staged over the tiles");
+  static constexpr int kQTile = kMRows * DH * 2;
+  static constexpr int kStage = 2 * kQTile;              // stage s: keys, values
+  static constexpr int kBars = kStage + kStages * 2 * kTile;
+  static constexpr int kTotal = kBars + 256;
 };
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -71,66 +73,118 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t lead) 
   return d;
 }
 
+// 32 consecutive columns of the thread's lane (no wait: tmem_wait_ld).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// Codes and scales are read once: past L1.
+__device__ __forceinline__ uint4 ld_once16(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_once8(const uint8_t* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
+// Which of the 32 keys from position pos on a row sees: the prefix, and the
+// nodes of its mask row (null: none), before the keys' own bits.
+__device__ __forceinline__ uint32_t row_sees(int pos, int Lp, const uint32_t* mrow, int words) {
+  if (pos + 32 <= Lp) return ~0u;
+  const int np = pos < Lp ? Lp - pos : 0, tf = pos > Lp ? pos - Lp : 0;
+  uint32_t w0 = 0, w1 = 0;
+  if (mrow) {
+    const int wb = tf >> 5;
+    if (wb < words) w0 = __ldg(mrow + wb);
+    if (wb + 1 < words) w1 = __ldg(mrow + wb + 1);
+  }
+  const uint32_t nodes = __funnelshift_r(w0, w1, tf & 31);
+  return (nodes << np) | ((1u << np) - 1u);
+}
+
+// A query row: its factor to base 2 and its power of two (bf16 words w).
+__device__ __forceinline__ float row_exponent(float top, float scale_log2, float* down) {
+  int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+  e = top > 0.f ? max(-100, min(e, 100)) : 0;
+  *down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  return scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
+
 template <int DH>
 __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnParams p) {
   using L = TreeSmem<DH>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* sQ = smem + L::kQ;
   uint8_t* sStage = smem + L::kStage;
-  uint8_t* sRaw = smem + L::kRaw0;
-  uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L::kBars);
-  uint64_t* raw_empty = raw_full + kRaw;
-  uint64_t* k_full = raw_empty + kRaw;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint64_t* k_empty = k_full + kStages;
   uint64_t* v_full = k_empty + kStages;
   uint64_t* v_empty = v_full + kStages;
-  uint64_t* s_full = v_empty + kStages;
-  uint64_t* s_empty = s_full + 2;
-  uint64_t* p_full = s_empty + 2;
-  uint64_t* p_empty = p_full + 2;
-  uint64_t* o_done = p_empty + 2;
+  uint64_t* s_full = v_empty + kStages;  // [2] row tiles
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_done = p_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  // bit k of a tile's 128: key k is there.  Tile f's copy starts after tile
-  // f - 3 (kRaw) is expanded, its keys after the scores of f - 5 (kStages),
-  // they after the softmax of f - 7 (two buffers) has begun: that of f - 8 is
-  // done, so eight slots do.
-  __shared__ uint32_t s_valid[kValid][4];
-  __shared__ float s_fac[kRowsQ];
-  __shared__ float2 s_ml[kRowsQ];
+  __shared__ __align__(16) uint8_t s_valid[kValid][kKeys / 8];  // bit k of a tile: key k is there
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = blockIdx.z, hk = blockIdx.y;
   const int mt = blockIdx.x / p.n_split, split = blockIdx.x % p.n_split;
   Span sp;
   if (!request_span(p, r, &sp)) return;
-  const int q0 = mt * kRowsQ;
-  const int live = min((sp.n + 1) * p.g - q0, kRowsQ);
-  if (live <= 0) return;
+  const int q0 = mt * kTreeRowsCta;
+  int live = (sp.n + 1) * p.g - q0;              // rows of this CTA: 256, and the tail in the last
+  if (live > kTreeRowsCta + kTail) live = kTreeRowsCta;
+  if (live <= 0 || (mt > 0 && live <= kTail)) return;  // (the tile before has them as its tail)
   const int t_all = row_tile_keys(p, sp, mt);
   const int t_beg = split * p.split_tiles;
   const int nt = min(t_all, t_beg + p.split_tiles) - t_beg;
   if (nt <= 0 && !(split == 0 && p.n_split == 1)) return;
+  const int odd = live % kMRows;
+  const int tail = live > kMRows && odd <= kTail ? odd : 0;
+  const int rows = live - tail;                  // by the tensor cores' two tiles
+  const int two = rows > kMRows ? 2 : 1;
 
   if (warp == kMmaWarp) tmem_alloc<kTmemCols>(tmem_slot);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kRaw; ++s) {
-      mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], kExpandWarps);
-    }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&k_full[s], kExpandWarps);
-      mbar_init(&k_empty[s], 1);
+      mbar_init(&k_empty[s], tail ? 2 : 1);
       mbar_init(&v_full[s], kExpandWarps);
-      mbar_init(&v_empty[s], 1);
+      mbar_init(&v_empty[s], tail ? 2 : 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&s_full[b], 1);
-      mbar_init(&s_empty[b], kSoftmaxWarps);
-      mbar_init(&p_full[b], kSoftmaxWarps);
-      mbar_init(&p_empty[b], 1);
+    for (int i = 0; i < 2; ++i) {
+      const int n = min(rows - i * kMRows, kMRows);  // one arrival per warp with rows
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], n > 0 ? (n + 31) / 32 : 1);
     }
     mbar_init(o_done, 1);
     *abort_flag = 0;
@@ -139,9 +193,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
       atomicOr(p.err, DT_ERR_BAD_INDEX);
   }
   // the queries, as fp16 rows scaled by a power of two to at most 2 each
-  if (threadIdx.x < kRowsQ) {
+  float fac = 1.f;
+  if (threadIdx.x < 2 * kMRows && threadIdx.x < two * kMRows) {
     const int row = threadIdx.x, q = q0 + row;
-    const bool on = row < live;
+    const bool on = row < rows;
     const int node = on ? q / p.g : 0;
     const uint4* src = reinterpret_cast<const uint4*>(
         p.Q + (static_cast<size_t>(r) * (p.B + 1) + node) * p.q_stride +
@@ -156,10 +211,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
       for (int j = 0; j < 4; ++j)
         top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[j] << 16)), fabsf(__uint_as_float(x[j] & 0xFFFF0000u))));
     }
-    int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-    e = top > 0.f ? max(-100, min(e, 100)) : 0;
-    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    s_fac[row] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    float down;
+    fac = row_exponent(top, p.scale_log2, &down);
+    uint8_t* dst = smem + (row >> 7) * L::kQTile;
 #pragma unroll
     for (int k = 0; k < DH / 8; ++k) {
       const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
@@ -167,7 +221,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         y[j] = pack_f16(__uint_as_float(x[j] << 16) * down, __uint_as_float(x[j] & 0xFFFF0000u) * down);
-      *reinterpret_cast<uint4*>(sQ + (k >> 3) * (kRowsQ * 128) + sw128(row, k & 7)) =
+      *reinterpret_cast<uint4*>(dst + (k >> 3) * (kMRows * 128) + sw128(row & 127, k & 7)) =
           make_uint4(y[0], y[1], y[2], y[3]);
     }
     fence_async_smem();
@@ -181,146 +235,141 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   auto wait_w = [&](uint64_t* bar, uint32_t par) {
     int ok = 0;
     if (lane == 0) ok = !*abort_flag && mbar_wait(bar, par, p.err) ? 1 : 0;
-    return __shfl_sync(kFullMask, ok, 0) != 0;
+    ok = __shfl_sync(kFullMask, ok, 0);
+    __syncwarp();  // (what lane 0 has seen, the warp sees)
+    return ok != 0;
   };
-
-  if (warp == kProducerWarp) {
-    // ------------------------------------------------------------ producer
-    const int P = 1 << p.c.log_page;
-    const int pieces = kKeys / P;                  // 8, 4, 2, 1
-    const int segs = pieces == 1 ? 1 : 4;          // copies per piece (a 128-token page's chunk is a raw tile)
-    const int32_t* row = p.table + static_cast<size_t>(r) * p.max_pages;
-    const int pc = lane / segs, seg = lane % segs;
-    const uint32_t piece_bytes = static_cast<uint32_t>(P * DH / 8 * 9);
-    int issued = 0;
-    bool flagged = false;
-    for (int f = 0; f < nt; ++f) {
-      const int st = f % kRaw;
-      if (f >= kRaw && !wait_w(&raw_empty[st], static_cast<uint32_t>((f / kRaw) & 1) ^ 1u)) {
-        if (lane == 0) *abort_flag = 1;
-        break;
-      }
-      const int key0 = (t_beg + f) * kKeys;
-      const bool mine = lane < pieces * segs && key0 + pc * P < sp.L;
-      int page = -1;
-      if (mine) {
-        const int slot = (key0 >> p.c.log_page) + pc;
-        if (slot < p.max_pages) page = row[slot];
-        if (page >= p.c.pages) page = -1;
-      }
-      const bool there = mine && page >= 0;
-      if (mine && !there && !flagged) {
-        flagged = true;
-        atomicOr(p.err, DT_ERR_BAD_INDEX);
-      }
-      const unsigned got = __ballot_sync(kFullMask, there);
-      if (lane < 4) {  // keys 32 lane .. 32 lane + 31
-        uint32_t v = 0;
-        for (int k = 0; k < pieces; ++k) {
-          if (!((got >> (k * segs)) & 1u)) continue;
-          const int a = max(k * P - 32 * lane, 0), b = min(min((k + 1) * P, sp.L - key0) - 32 * lane, 32);
-          if (b > a) v |= (b == 32 ? 0xFFFFFFFFu : (1u << b) - 1u) & ~((1u << a) - 1u);
-        }
-        s_valid[f % kValid][lane] = v;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], __popc(got) / segs * piece_bytes);
-      __syncwarp();
-      if (there) {
-        const uint8_t* chunk = p.c.pool + static_cast<size_t>(page) * p.c.page_bytes +
-                               static_cast<size_t>(hk) * p.c.chunk;
-        uint8_t* dst = sRaw + st * L::kRawBytes;
-        if (segs == 1) {
-          bulk_load(dst, chunk, piece_bytes, &raw_full[st]);
-        } else {
-          const bool codes = (seg & 1) == 0;
-          const int unit = codes ? DH / 2 : DH / 16;
-          bulk_load(dst + (seg >> 1) * L::kV + (codes ? 0 : L::kCodes) + pc * P * unit,
-                    chunk + (seg >> 1) * (p.c.chunk >> 1) + (codes ? 0 : P * DH / 2),
-                    static_cast<uint32_t>(P * unit), &raw_full[st]);
-        }
-      }
-      issued = f + 1;
-    }
-    if (lane == 0)  // every copy must have landed before the block may end
-      for (int f = issued > kRaw ? issued - kRaw : 0; f < issued; ++f)
-        mbar_wait(&raw_full[f % kRaw], static_cast<uint32_t>((f / kRaw) & 1), p.err);
-  } else if (warp >= kExpandWarp0 && warp < kProducerWarp) {
+  if (warp >= kExpandWarp0 && warp < kMmaWarp) {
     // ------------------------------------------------- codes to fp16 tiles
     // Lane (key = lane / 4, c = lane % 4) of a warp's 8 keys takes the dims
     // [c DH/4, (c+1) DH/4): one load of codes, two (one) scales, DH/32 lines
     // of 16 bytes.  The lanes of c >= 2 write theirs in another order: the
     // eight lanes of a store's phase then lie in eight different 16-byte
-    // columns.
+    // columns.  A tile's codes are loaded while the one before is expanded,
+    // its pages' numbers a tile earlier still.
+    constexpr int kIt = kKeys / (kExpandWarps * 8);
     const int ew = warp - kExpandWarp0, kl = lane >> 2, c = lane & 3;
+    const int P = 1 << p.c.log_page;
+    const int32_t* trow = p.table + static_cast<size_t>(r) * p.max_pages;
+    const uint8_t* head = p.c.pool + static_cast<size_t>(hk) * p.c.chunk;
+    const int half = p.c.chunk >> 1;
+    using Codes = typename std::conditional<DH == 128, uint4, uint2>::type;
+    Codes code[2][kIt];
+    uint32_t scl[2][kIt];
+    int page[kIt];
+    bool flagged = false;
+    auto key_of = [&](int f, int it) { return (t_beg + f) * kKeys + (it * kExpandWarps + ew) * 8 + kl; };
+    auto look_up = [&](int f) {
+#pragma unroll
+      for (int it = 0; it < kIt; ++it) {
+        const int key = key_of(f, it), slot = key >> p.c.log_page;
+        page[it] = -1;
+        if (f < nt && key < sp.L) {
+          if (slot < p.max_pages) page[it] = trow[slot];
+          if (page[it] < 0 || page[it] >= p.c.pages) {
+            page[it] = -1;
+            if (!flagged) atomicOr(p.err, DT_ERR_BAD_INDEX);
+            flagged = true;
+          }
+        }
+      }
+    };
+    auto fetch = [&](int f, int kv) {
+#pragma unroll
+      for (int it = 0; it < kIt; ++it) {
+        scl[kv][it] = 0;
+        code[kv][it] = Codes{};
+        if (page[it] >= 0) {
+          const int t = key_of(f, it) & (P - 1);
+          const uint8_t* chunk = head + static_cast<size_t>(page[it]) * p.c.page_bytes + kv * half;
+          if constexpr (DH == 128) {
+            code[kv][it] = ld_once16(chunk + t * 64 + c * 16);
+            scl[kv][it] = *reinterpret_cast<const uint16_t*>(chunk + P * 64 + t * 8 + c * 2);
+          } else {
+            code[kv][it] = ld_once8(chunk + t * 32 + c * 8);
+            scl[kv][it] = chunk[P * 32 + t * 4 + c];
+          }
+        }
+      }
+    };
+    uint8_t there[2];  // bits of the warp's groups of 8 keys: this tile's (lane it), the next one's
+    auto note = [&](int slot) {
+#pragma unroll
+      for (int it = 0; it < kIt; ++it) {
+        uint32_t x = __ballot_sync(kFullMask, page[it] >= 0) & 0x11111111u;  // (lane 4 k: key k)
+        x = (x | x >> 3) & 0x03030303u;
+        x = (x | x >> 6) & 0x000F000Fu;
+        x = (x | x >> 12) & 0xFFu;
+        if (lane == it) there[slot] = static_cast<uint8_t>(x);
+      }
+    };
+    look_up(0);
+    fetch(0, 0);
+    fetch(0, 1);
+    note(0);
+    look_up(1);
     bool go = true;
     for (int f = 0; f < nt && go; ++f) {
-      const int st = f % kStages, rs = f % kRaw;
+      const int st = f % kStages;
       const uint32_t ph = static_cast<uint32_t>((f / kStages) & 1);
-      go = wait_w(&raw_full[rs], static_cast<uint32_t>((f / kRaw) & 1));
-      if (!go) break;
-      mbar_try_wait(smem_u32(&raw_full[rs]), static_cast<uint32_t>((f / kRaw) & 1));
-#pragma unroll 1
+      note(1);  // (of tile f + 1)
+#pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         if (f >= kStages && !wait_w(kv == 0 ? &k_empty[st] : &v_empty[st], ph ^ 1u)) {
           go = false;
           break;
         }
-        const uint8_t* raw = sRaw + rs * L::kRawBytes + kv * L::kV;
+        if (kv == 0 && lane < kIt) s_valid[f % kValid][lane * kExpandWarps + ew] = there[0];
         uint8_t* dst = sStage + st * 2 * L::kTile + kv * L::kTile;
 #pragma unroll
-        for (int it = 0; it < kKeys / (kExpandWarps * 8); ++it) {
+        for (int it = 0; it < kIt; ++it) {
           const int key = (it * kExpandWarps + ew) * 8 + kl;
-          const bool there = (s_valid[f % kValid][key >> 5] >> (key & 31)) & 1u;
           uint32_t w[DH / 32], sc[2];
+          const uint32_t* cw = reinterpret_cast<const uint32_t*>(&code[kv][it]);
+#pragma unroll
+          for (int i = 0; i < DH / 32; ++i) w[i] = cw[i];
           if constexpr (DH == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(raw + key * 64 + c * 16);
-            w[0] = x.x;
-            w[1] = x.y;
-            w[2] = x.z;
-            w[3] = x.w;
-            uint32_t two = *reinterpret_cast<const uint16_t*>(raw + L::kCodes + key * 8 + c * 2);
-            two = e4m3x2_to_f16x2(there ? two : 0u);
-            sc[0] = __byte_perm(two, two, 0x1010);
-            sc[1] = __byte_perm(two, two, 0x3232);
+            const uint32_t s2 = e4m3x2_to_f16x2(scl[kv][it]);
+            sc[0] = __byte_perm(s2, s2, 0x1010);
+            sc[1] = __byte_perm(s2, s2, 0x3232);
+            if (c & 2) {  // the lines in the order 2, 3, 0, 1
+              uint32_t x = w[0];
+              w[0] = w[2];
+              w[2] = x;
+              x = w[1];
+              w[1] = w[3];
+              w[3] = x;
+              x = sc[0];
+              sc[0] = sc[1];
+              sc[1] = x;
+            }
           } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(raw + key * 32 + c * 8);
-            w[0] = x.x;
-            w[1] = x.y;
-            const uint32_t b = there ? raw[L::kCodes + key * 4 + c] : 0u;
-            sc[0] = sc[1] = e4m3x2_to_f16x2(b | (b << 8));
+            sc[0] = sc[1] = e4m3x2_to_f16x2(scl[kv][it] | (scl[kv][it] << 8));
           }
           uint8_t* line = dst + (DH == 128 ? (c >> 1) * (kKeys * 128) : 0);
 #pragma unroll
           for (int i = 0; i < DH / 32; ++i) {
-            const int g = DH == 128 ? ((c & 1) << 2) : (c << 1);
-            const int ii = DH == 128 ? i ^ (c & 2) : i;     // (which of the lane's lines)
-            uint32_t word = w[i];
-            uint32_t scl = sc[DH == 128 ? i >> 1 : 0];
-            if (DH == 128 && (c & 2)) {                      // i ^ 2
-              word = w[i ^ 2];
-              scl = sc[(i ^ 2) >> 1];
-            }
+            const int gr = DH == 128 ? ((c & 1) << 2) + (i ^ (c & 2)) : (c << 1) + i;
             uint32_t y[4];
-            e2m1x8_to_f16(word, y);
-            *reinterpret_cast<uint4*>(line + sw128(key, g + ii)) =
-                make_uint4(h2mul(y[0], scl), h2mul(y[1], scl), h2mul(y[2], scl), h2mul(y[3], scl));
+            e2m1x8_to_f16(w[i], y);
+            const uint32_t s2 = sc[DH == 128 ? i >> 1 : 0];
+            *reinterpret_cast<uint4*>(line + sw128(key, gr)) =
+                make_uint4(h2mul(y[0], s2), h2mul(y[1], s2), h2mul(y[2], s2), h2mul(y[3], s2));
           }
         }
+        fetch(f + 1, kv);
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(kv == 0 ? &k_full[st] : &v_full[st]);
-          if (kv == 1) mbar_arrive(&raw_empty[rs]);
-        }
+        if (lane == 0) mbar_arrive(kv == 0 ? &k_full[st] : &v_full[st]);
       }
+      there[0] = there[1];
+      look_up(f + 2);
     }
     if (!go && lane == 0) *abort_flag = 1;
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------- MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_f16(kKeys, false), idesc_o = idesc_f16(DH, true);
-      const uint32_t q_addr = smem_u32(sQ);
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t par) {
         if (ok && !*abort_flag && mbar_wait(bar, par, p.err)) return true;
@@ -328,212 +377,318 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
         *abort_flag = 1;
         return false;
       };
-      auto issue_s = [&](int j) {
-        const int b = j & 1, st = j % kStages;
-        if (!wait(&s_empty[b], (static_cast<uint32_t>(j >> 1) & 1u) ^ 1u)) return;
-        if (!wait(&k_full[st], static_cast<uint32_t>((j / kStages) & 1))) return;
+      // S_i of tile j (over P_i(j - 1), which P V(j - 1), issued before, has read)
+      auto issue_s = [&](int i, int j) {
+        const int st = j % kStages;
+        if (i == 0 && !wait(&k_full[st], static_cast<uint32_t>((j / kStages) & 1))) return;
         tc_fence_after();
-        const uint32_t k_addr = smem_u32(sStage + st * 2 * L::kTile);
+        const uint32_t q_addr = smem_u32(smem + i * L::kQTile), k_addr = smem_u32(sStage + st * 2 * L::kTile);
 #pragma unroll
         for (int kk = 0; kk < DH / 16; ++kk) {
           const uint32_t off = (kk & 3) * 32u;
-          tc_mma_bf16(tmem_base + static_cast<uint32_t>(b * kKeys),
-                      smem_desc_sw128(q_addr + (kk >> 2) * (kRowsQ * 128) + off),
+          tc_mma_bf16(tmem_base + static_cast<uint32_t>(i * kKeys),
+                      smem_desc_sw128(q_addr + (kk >> 2) * (kMRows * 128) + off),
                       smem_desc_sw128(k_addr + (kk >> 2) * (kKeys * 128) + off), idesc_s, kk != 0 ? 1u : 0u);
         }
-        tc_commit(&s_full[b]);
-        tc_commit(&k_empty[st]);
+        tc_commit(&s_full[i]);
+        if (i == two - 1) tc_commit(&k_empty[st]);
       };
-      auto issue_o = [&](int j) {
-        const int st = j % kStages, pb = j & 1;
-        if (!wait(&p_full[pb], static_cast<uint32_t>(j >> 1) & 1u)) return;
-        if (!wait(&v_full[st], static_cast<uint32_t>((j / kStages) & 1))) return;
+      auto issue_o = [&](int i, int j) {
+        const int st = j % kStages;
+        if (!wait(&p_full[i], static_cast<uint32_t>(j) & 1u)) return;
+        if (i == 0 && !wait(&v_full[st], static_cast<uint32_t>((j / kStages) & 1))) return;
         tc_fence_after();
         const uint32_t v_addr = smem_u32(sStage + st * 2 * L::kTile + L::kTile);
-        const uint32_t pa = tmem_base + kColP + static_cast<uint32_t>(pb * (kKeys / 2));
+        const uint32_t pa = tmem_base + static_cast<uint32_t>(i * kKeys);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)  // 16 keys: two atoms of 8 lines
-          tc_mma_bf16_ta(tmem_base + kColO, pa + static_cast<uint32_t>(kk * 8),
+          tc_mma_bf16_ta(tmem_base + kColO + static_cast<uint32_t>(i * 128), pa + static_cast<uint32_t>(kk * 8),
                          smem_desc_mn(v_addr + kk * 2048, kKeys * 128), idesc_o, (j != 0 || kk != 0) ? 1u : 0u);
-        tc_commit(&p_empty[pb]);
-        tc_commit(&v_empty[st]);
+        if (i == two - 1) tc_commit(&v_empty[st]);
       };
-      for (int j = 0; j < nt && ok; ++j) {
-        issue_s(j);
-        if (ok && j > 0) issue_o(j - 1);
-      }
-      if (ok && nt > 0) issue_o(nt - 1);
+      for (int i = 0; i < two && ok && nt > 0; ++i) issue_s(i, 0);
+      for (int j = 0; j < nt && ok; ++j)
+        for (int i = 0; i < two && ok; ++i) {
+          issue_o(i, j);
+          if (ok && j + 1 < nt) issue_s(i, j + 1);
+        }
       tc_commit(o_done);
       mbar_wait(o_done, 0, p.err);
     }
-  } else {
+  } else if (warp < kExpandWarp0 && warp * 32 < rows) {
     // ------------------------------------------------------------- softmax
-    __shared__ float red[2][kRowsQ];
-    __shared__ float red2[2][2][kRowsQ];
-    __shared__ int stop_slot[2][kSoftmaxWarps];
-    const int wg = warp >> 2, wq = warp & 3;
-    const int row = wq * 32 + lane, q = q0 + row;
-    const int node = row < live ? q / p.g : 0;
-    const uint32_t* mrow =
-        node >= 1 ? p.mask + (static_cast<size_t>(r) * p.B + node - 1) * p.words : nullptr;
-    const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-    const int col0 = wg * kHalf;
-    const float fac = s_fac[row];
-    const bool idle = wq * 32 >= live;  // none of the warp's rows exists
-    constexpr int kOH = DH / 2;
+    const int i = warp >> 2, row = threadIdx.x, q = q0 + row;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem_base + lane_base + static_cast<uint32_t>(i * kKeys);
+    const uint32_t o_addr = tmem_base + lane_base + kColO + static_cast<uint32_t>(i * 128);
+    const int node = row < rows ? q / p.g : 0;
+    const uint32_t* mrow = node >= 1 ? p.mask + (static_cast<size_t>(r) * p.B + node - 1) * p.words : nullptr;
     float m = -INFINITY, l = 0.f;
+    float limit = -INFINITY;  // the unscaled score above which the reference rises
     bool go = true;
     for (int j = 0; j < nt; ++j) {
-      const int key0 = (t_beg + j) * kKeys + col0;
-      // the mask words of this group's half of the tile (three from the one
-      // that holds its first node)
-      uint32_t mw[3] = {0u, 0u, 0u};
-      if (mrow && key0 + kHalf > sp.Lp) {
-        const int wb = (key0 > sp.Lp ? key0 - sp.Lp : 0) >> 5;
+      const int key0 = (t_beg + j) * kKeys;
+      if (!(go = wait_w(&s_full[i], static_cast<uint32_t>(j) & 1u))) break;
+      tc_fence_after();
+      const uint4 there = *reinterpret_cast<const uint4*>(s_valid[j % kValid]);
+      const bool plain = key0 + kKeys <= sp.Lp && (there.x & there.y & there.z & there.w) == ~0u;
+      uint32_t pk[kKeys / 2];
+      float add;
+      // the row's weights with the reference as it is; false: it has to rise
+      auto weigh = [&]() {
+        const float sub = m == -INFINITY ? 0.f : kBias - m;
+        float top = -INFINITY;
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < 3; ++k)
-          if (wb + k < p.words) mw[k] = __ldg(mrow + wb + k);
-      }
-      const bool okw = go && wait_w(&s_full[j & 1], static_cast<uint32_t>(j >> 1) & 1u);
-      float s[kHalf];
-      float mh = -INFINITY;
-      if (okw) {
-        tc_fence_after();
-        const uint32_t taddr = tmem_base + lane_base + static_cast<uint32_t>((j & 1) * kKeys + col0);
-        if (!idle) {
+        for (int ch = 0; ch < kKeys / 32; ++ch) {
+          uint32_t x[32];
+          tmem_ld32(s_addr + ch * 32, x);
+          tmem_wait_ld();
+          if (!plain) {
+            const uint32_t w = ch == 0 ? there.x : ch == 1 ? there.y : ch == 2 ? there.z : there.w;
+            const uint32_t see = row_sees(key0 + 32 * ch, sp.Lp, mrow, p.words) & w;
 #pragma unroll
-          for (int c = 0; c < kHalf; c += 16) {
+            for (int k = 0; k < 32; ++k)
+              if (!((see >> k) & 1u)) x[k] = 0xFF800000u;  // -inf
+          }
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const float a = __uint_as_float(x[k]), b = __uint_as_float(x[k + 1]);
+            top = fmaxf(top, fmaxf(a, b));
+            const float pa = ex2(fmaf(a, fac, sub)), pb = ex2(fmaf(b, fac, sub));
+            part[(k >> 1) & 3] += pa + pb;
+            pk[ch * 16 + k / 2] = pack_f16(pa, pb);
+          }
+        }
+        add = (part[0] + part[1]) + (part[2] + part[3]);
+        if (!__any_sync(kFullMask, top > limit)) return true;
+        if (top > limit) {
+          const float t = top * fac, alpha = ex2(m - t);  // (0 from -inf)
+          m = t;
+          limit = __fdividef(t + kRaise, fac);
+          l *= alpha;
+          part[0] = alpha;
+        } else {
+          part[0] = 1.f;
+        }
+        if (j > 0) {  // O holds the products of the tiles before
+#pragma unroll
+          for (int ch = 0; ch < DH / 16; ++ch) {
             float x[16];
-            tmem_ld16(taddr + c, x);
+            tmem_ld16(o_addr + ch * 16, x);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[c + i] = x[i];
+            for (int k = 0; k < 16; ++k) x[k] *= part[0];
+            tmem_st16(o_addr + ch * 16, x);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_empty[j & 1]);
-        if (!idle) {
-          const uint32_t va = s_valid[j % kValid][2 * wg], vb = s_valid[j % kValid][2 * wg + 1];
-          if (key0 + kHalf <= sp.Lp && (va & vb) == 0xFFFFFFFFu) {
+        return false;
+      };
+      if (!weigh()) weigh();  // (the second time no score passes the limit)
+      l += add;
+      uint32_t half[32];
 #pragma unroll
-            for (int c = 0; c < kHalf; ++c) s[c] *= fac;
-          } else {
-            const int np = sp.Lp > key0 ? sp.Lp - key0 : 0;  // prefix keys of the window
-            const int tf = key0 > sp.Lp ? key0 - sp.Lp : 0;  // its first node
-            const uint32_t lo = __funnelshift_r(mw[0], mw[1], tf & 31);
-            const uint32_t hi = __funnelshift_r(mw[1], mw[2], tf & 31);
-            uint64_t vis = (static_cast<uint64_t>(hi) << 32) | lo;
-            vis = np >= 64 ? ~0ull : (vis << np) | ((1ull << np) - 1);
-            const uint32_t v0 = static_cast<uint32_t>(vis) & va, v1 = static_cast<uint32_t>(vis >> 32) & vb;
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int c = 0; c < kHalf; ++c) {
-              const bool seen = (((c < 32 ? v0 : v1) >> (c & 31)) & 1u) != 0u;
-              s[c] = seen ? s[c] * fac : -INFINITY;
-            }
-          }
-#pragma unroll
-          for (int c = 0; c < kHalf; ++c) mh = fmaxf(mh, s[c]);
-        }
+        for (int k = 0; k < 32; ++k) half[k] = pk[32 * h + k];
+        tmem_st32(s_addr + 32 * h, half);
       }
-      red2[j & 1][wg][row] = mh;
-      if (lane == 0) stop_slot[j & 1][warp] = okw ? 0 : 1;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      int stop = 0;
-#pragma unroll
-      for (int w = 0; w < kSoftmaxWarps; ++w) stop |= stop_slot[j & 1][w];
-      if (stop) {  // the same for all 256 threads
-        go = false;
-        *abort_flag = 1;
-        break;
-      }
-      const float mx = fmaxf(red2[j & 1][0][row], red2[j & 1][1][row]);
-      const bool raise = mx > m + kRaise;  // the same in both groups
-      bool failed = false;
-      if (__any_sync(kFullMask, raise)) {
-        const float m_new = raise ? mx : m;
-        const float alpha = raise ? ex2(m - m_new) : 1.f;
-        l *= alpha;
-        m = m_new;
-        if (j > 0) {
-          failed = !wait_w(&p_empty[(j - 1) & 1], static_cast<uint32_t>((j - 1) >> 1) & 1u);
-          if (!failed) {
-            tc_fence_after();
-            const uint32_t oaddr = tmem_base + lane_base + kColO + wg * kOH;
-#pragma unroll
-            for (int c = 0; c < kOH; c += 16) {
-              float x[16];
-              tmem_ld16(oaddr + c, x);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] *= alpha;
-              tmem_st16(oaddr + c, x);
-            }
-            tmem_wait_st();
-          }
-        }
-      }
-      const float sub = m == -INFINITY ? 0.f : m - kBias;
-      uint32_t pk[kHalf / 2];
-      if (!idle) {
-#pragma unroll
-        for (int c = 0; c < kHalf; c += 2) {
-          const float a = ex2(s[c] - sub), b = ex2(s[c + 1] - sub);
-          l += a + b;
-          pk[c / 2] = pack_f16(a, b);
-        }
-      }
-      if (!failed && j > 1) failed = !wait_w(&p_empty[j & 1], (static_cast<uint32_t>(j >> 1) & 1u) ^ 1u);
-      if (failed) {
-        go = false;
-        *abort_flag = 1;
-        continue;
-      }
-      if (!idle) {
-        tmem_st32(tmem_base + lane_base + kColP + static_cast<uint32_t>((j & 1) * (kKeys / 2) + wg * 32), pk);
-        tmem_wait_st();
-      }
+      tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[j & 1]);
+      if (lane == 0) mbar_arrive(&p_full[i]);
     }
-    red[wg][row] = l;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    l = red[0][row] + red[1][row];
-    float* sO = reinterpret_cast<float*>(sStage);
+    if (!go && lane == 0) *abort_flag = 1;
     const bool have = go && nt > 0 && wait_w(o_done, 0);
     if (have) tc_fence_after();
-    if (!idle) {
-      float* dst = sO + row * L::kOPitch + wg * kOH;
+    else l = 0.f;
+    const bool on = row < rows;
+    const float inv = l > 0.f ? p.c.v_scale / l : 0.f;
+    float* part = p.n_split > 1 && on ? cache_part_row(p, r, hk, mt, split, row) : nullptr;
+    uint4* out = p.n_split > 1 || !on ? nullptr : reinterpret_cast<uint4*>(p.O + cache_out_row(p, r, hk, q));
+    if (part) *reinterpret_cast<float2*>(part) = make_float2(m, l);
 #pragma unroll
-      for (int c = 0; c < kOH; c += 16) {
-        float x[16];
-        if (have) {
-          tmem_ld16(tmem_base + lane_base + kColO + wg * kOH + c, x);
-        } else {
+    for (int ch = 0; ch < DH / 32; ++ch) {
+      uint32_t x[32];
+      if (have) {
+        tmem_ld32(o_addr + ch * 32, x);
+        tmem_wait_ld();
+      } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = 0.f;
+        for (int k = 0; k < 32; ++k) x[k] = 0u;
+      }
+      if (part) {
+#pragma unroll
+        for (int k = 0; k < 32; k += 2)
+          *reinterpret_cast<float2*>(part + 2 + ch * 32 + k) =
+              make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+      }
+      if (out) {
+#pragma unroll
+        for (int k = 0; k < 32; k += 8) {
+          uint32_t y[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            y[u] = pack_bf16(__uint_as_float(x[k + 2 * u]) * inv, __uint_as_float(x[k + 2 * u + 1]) * inv);
+          out[ch * 4 + k / 8] = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      }
+    }
+  } else if (warp == kTailWarp && tail > 0) {
+    // ------------------------------------------------------------ tail rows
+    // S^T = K Q^T and O^T += V^T P^T by mma m16n8k16 with the tiles' keys as
+    // the 16-row operand (as the kernel of few rows does from the codes).
+    const int rr = lane >> 2, c = lane & 3;
+    constexpr int kSteps = DH / 16, kGroups = kKeys / 16;
+    uint32_t qb[kSteps][2];
+    float tf[2];
+    int nd[2];
+    {
+      const bool on = rr < tail;
+      const int q = q0 + rows + (on ? rr : 0), n = q / p.g;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(
+          p.Q + (static_cast<size_t>(r) * (p.B + 1) + n) * p.q_stride +
+          static_cast<size_t>(hk * p.g + (q - n * p.g)) * DH);
+      float top = 0.f;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          qb[s][h] = on ? __ldg(src + 8 * s + 4 * h + c) : 0u;  // dims 16 s + 8 h + 2 c, + 1
+          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qb[s][h] << 16)), fabsf(__uint_as_float(qb[s][h] & 0xFFFF0000u))));
+        }
+      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
+      float down;
+      const float f = row_exponent(top, p.scale_log2, &down);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          qb[s][h] = pack_f16(__uint_as_float(qb[s][h] << 16) * down, __uint_as_float(qb[s][h] & 0xFFFF0000u) * down);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        tf[x] = __shfl_sync(kFullMask, f, (2 * c + x) * 4);
+        nd[x] = __shfl_sync(kFullMask, n, (2 * c + x) * 4);
+      }
+    }
+    float o[kSteps][4];  // dims 16 s + rr, + 8 of rows 2 c, 2 c + 1
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) o[s][0] = o[s][1] = o[s][2] = o[s][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, limit[2] = {-INFINITY, -INFINITY};
+    const int lr = lane & 7, lm = lane >> 3;  // ldmatrix: row lr of matrix lm
+    bool go = true;
+    for (int j = 0; j < nt; ++j) {
+      const int st = j % kStages, key0 = (t_beg + j) * kKeys;
+      const uint32_t ph = static_cast<uint32_t>((j / kStages) & 1);
+      if (!(go = wait_w(&k_full[st], ph))) break;
+      const uint32_t k_addr = smem_u32(sStage + st * 2 * L::kTile), v_addr = k_addr + L::kTile;
+      const uint4 there = *reinterpret_cast<const uint4*>(s_valid[j % kValid]);
+      const bool plain = key0 + kKeys <= sp.Lp && (there.x & there.y & there.z & there.w) == ~0u;
+      float s[kGroups][4];
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        s[g][0] = s[g][1] = s[g][2] = s[g][3] = 0.f;
+        const int key = 16 * g + lr + 8 * (lm & 1);  // matrices: keys 0-7 | 8-15, dims 0-7; the same, dims 8-15
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          uint32_t a[4];
+          const int gr = 2 * k + (lm >> 1);
+          ldmatrix_x4(k_addr + (gr >> 3) * (kKeys * 128) + sw128(key, gr & 7), a);
+          mma_f16(s[g], a, qb[k][0], qb[k][1]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_empty[st]);
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (!plain) {
+            const int kk = 16 * g + 8 * (x >> 1) + rr, pos = key0 + kk;
+            const uint32_t w = g < 2 ? there.x : g < 4 ? there.y : g < 6 ? there.z : there.w;
+            bool seen = (w >> (kk & 31)) & 1u;
+            if (seen && pos >= sp.Lp) {
+              const int t = pos - sp.Lp, n = nd[x & 1];
+              seen = n > 0 &&
+                     ((__ldg(p.mask + (static_cast<size_t>(r) * p.B + n - 1) * p.words + (t >> 5)) >> (t & 31)) & 1u);
+            }
+            if (!seen) s[g][x] = -INFINITY;
+          }
+          top[x & 1] = fmaxf(top[x & 1], s[g][x]);
+        }
+      if (__any_sync(kFullMask, top[0] > limit[0] || top[1] > limit[1])) {
+        float al[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float t = top[x];
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) t = fmaxf(t, __shfl_xor_sync(kFullMask, t, d));
+          al[x] = 1.f;
+          if (t > limit[x]) {
+            t *= tf[x];
+            al[x] = ex2(m[x] - t);
+            m[x] = t;
+            limit[x] = __fdividef(t + kRaise, tf[x]);
+            l[x] *= al[x];
+          }
         }
 #pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<float4*>(dst + c + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        for (int k = 0; k < kSteps; ++k) {
+          o[k][0] *= al[0];
+          o[k][1] *= al[1];
+          o[k][2] *= al[0];
+          o[k][3] *= al[1];
+        }
       }
-      if (wg == 0) s_ml[row] = make_float2(m, have ? l : 0.f);
+      const float sub0 = m[0] == -INFINITY ? 0.f : kBias - m[0], sub1 = m[1] == -INFINITY ? 0.f : kBias - m[1];
+      uint32_t pb[kGroups][2];
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float p0 = ex2(fmaf(s[g][2 * t], tf[0], sub0)), p1 = ex2(fmaf(s[g][2 * t + 1], tf[1], sub1));
+          l[0] += p0;
+          l[1] += p1;
+          pb[g][t] = transpose8x8(pack_f16(p0, p1));
+        }
+      if (!(go = wait_w(&v_full[st], ph))) break;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        const int gr = 2 * k + (lm & 1);  // matrices: dims 0-7 | 8-15, keys 0-7; the same, keys 8-15
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          uint32_t a[4];
+          ldmatrix_x4_trans(v_addr + (gr >> 3) * (kKeys * 128) + sw128(16 * g + lr + 8 * (lm >> 1), gr & 7), a);
+          mma_f16(o[k], a, pb[g][0], pb[g][1]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&v_empty[st]);
     }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    constexpr int kE = DH / 32;
-    for (int rr = warp; rr < live; rr += kSoftmaxWarps) {
-      const float2 ml = s_ml[rr];
-      const float* v = sO + rr * L::kOPitch + lane * kE;
+    if (!go && lane == 0) *abort_flag = 1;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+      for (int d = 4; d < 32; d *= 2) l[x] += __shfl_xor_sync(kFullMask, l[x], d);
+      const int row = 2 * c + x;
+      if (row >= tail) continue;
       if (p.n_split > 1) {
-        float* dst = cache_part_row(p, r, hk, mt, split, rr);
+        float* dst = cache_part_row(p, r, hk, mt, split, rows + row);
+        if (rr == 0) *reinterpret_cast<float2*>(dst) = make_float2(m[x], l[x]);
 #pragma unroll
-        for (int e = 0; e < kE; e += 2)
-          *reinterpret_cast<float2*>(dst + 2 + lane * kE + e) = make_float2(v[e], v[e + 1]);
-        if (lane == 0) *reinterpret_cast<float2*>(dst) = ml;
+        for (int k = 0; k < kSteps; ++k) {
+          dst[2 + 16 * k + rr] = o[k][x];
+          dst[2 + 16 * k + 8 + rr] = o[k][2 + x];
+        }
       } else {
-        const float inv = ml.y > 0.f ? p.c.v_scale / ml.y : 0.f;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row(p, r, hk, q0 + rr) + lane * kE);
+        const float inv = l[x] > 0.f ? p.c.v_scale / l[x] : 0.f;
+        uint16_t* dst = p.O + cache_out_row(p, r, hk, q0 + rows + row);
 #pragma unroll
-        for (int e = 0; e < kE; e += 2) dst[e / 2] = pack_bf16(v[e] * inv, v[e + 1] * inv);
+        for (int k = 0; k < kSteps; ++k) {
+          dst[16 * k + rr] = float_to_bf16_bits(o[k][x] * inv);
+          dst[16 * k + 8 + rr] = float_to_bf16_bits(o[k][2 + x] * inv);
+        }
       }
     }
   }
