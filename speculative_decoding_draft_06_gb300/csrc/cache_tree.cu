@@ -5,24 +5,25 @@
 // A CTA owns up to 256 query rows of one request and one key/value head, as
 // two tiles of 128 (a TMEM lane each), up to 8 more ("tail": a tree of 2^k
 // nodes and its root are a few rows more than whole tiles), and a share of
-// the key range in tiles of 128 keys.  Warp roles (480 threads):
+// the key range in tiles of 128 keys.  Warp roles (512 threads):
 //   0-3, 4-7  softmax of the two row tiles: a thread owns a row;
 //   8-11      expand: codes and scales from memory to fp16 keys and values in
 //             shared memory (exact), a tile ahead in registers;
-//   12        TMEM owner, issues the MMAs;
-//   13        the tail rows, by mma.sync on the same fp16 tiles;
-//   14        (fills the warpgroup).
-// S = Q K^T (M 128, N 128, fp16, fp32 sums) into TMEM, P = 2^(s - m + kBias)
-// in fp16 over the S columns it came from, O += P V with P from TMEM.  While
-// one row tile's scores are in the softmax, the tensor cores work for the
-// other.  Keys and values lie in shared memory in the same layout (a token's
+//   12-13     the tail rows, by mma.sync on the same fp16 tiles, half of a
+//             tile's keys each;
+//   14, 15    issue the MMAs of one row tile each (14 owns the TMEM): what
+//             waits on the issue all wait for, and two warps issue twice as fast.
+// In steps of 64 keys: S = Q K^T (M 128, N 64, fp16, fp32 sums) into TMEM,
+// double-buffered per row tile, P = 2^(s - m + kBias) in fp16 over the S
+// columns it came from, O += P V with P from TMEM; S runs a step ahead of P.
+// Keys and values lie in shared memory in the same layout (a token's
 // row of 64 head dimensions is a 128-byte swizzled line): for S it is a
 // K-major operand, for O the same lines are MN-major (the transposed read is
 // the tensor core's).
 // The running maximum is a reference that rises only when a score passes it
-// by kRaise: a row's weights are computed with the reference as it is, and
-// once more where that happens (O in TMEM is rescaled then; S(j) is issued
-// after P V(j - 1), so its arrival says that O is at rest).
+// by kRaise, which rescales O in TMEM.
+// Requests go to the SMs longest first (the CTA's request is the z-th
+// longest), so that the last ones to start are the short ones.
 #include <type_traits>
 
 #include "cache_attn.cuh"
@@ -30,13 +31,16 @@
 namespace dt {
 namespace {
 
-constexpr int kMRows = 128, kKeys = 128;
-constexpr int kExpandWarp0 = 8, kExpandWarps = 4, kMmaWarp = 12, kTailWarp = 13;
-constexpr int kTreeThreads = 15 * 32;
+constexpr int kMRows = 128, kKeys = 128, kStepKeys = 64;
+constexpr int kExpandWarp0 = 8, kExpandWarps = 4, kTailWarp0 = 12, kMmaWarp0 = 14;
+constexpr int kTreeThreads = 16 * 32;
 constexpr int kStages = 2;
-constexpr int kValid = 4;  // a tile's keys are expanded after the scores of two before: the softmax of three before is done
+// (a tile's keys are expanded after all scores of the tile two before are
+// issued, and they after the weights of the tile three before are there)
+constexpr int kValid = 4;
 constexpr int kTail = kTreeTail;
-constexpr uint32_t kTmemCols = 512;  // S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512); P over S
+constexpr int kTreeSorted = 256;  // requests that are taken longest first (each CTA ranks them: R^2 / 512 steps)
+constexpr uint32_t kTmemCols = 512;  // S of row tile i, buffer b: 128 i + 64 b; O of row tile i: 256 + 128 i; P over S
 constexpr uint32_t kColO = 256;
 
 template <int DH>
@@ -49,6 +53,13 @@ struct TreeSmem {
 };
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// One lane of a converged warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 
 __device__ __forceinline__ uint32_t sw128(int r, int gr) {
   return static_cast<uint32_t>(r * 128 + ((gr ^ (r & 7)) << 4));
@@ -85,6 +96,44 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr));
+}
+
+// Pairs of fp32 in one operand (two lanes of the fp32 pipe per instruction).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -148,16 +197,32 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   uint64_t* k_empty = k_full + kStages;
   uint64_t* v_full = k_empty + kStages;
   uint64_t* v_empty = v_full + kStages;
-  uint64_t* s_full = v_empty + kStages;  // [2] row tiles
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_done = p_full + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 1);
+  uint64_t* s_full = v_empty + kStages;  // [row tile][buffer]
+  uint64_t* p_full = s_full + 4;         // [row tile][buffer]
+  uint64_t* o_full = p_full + 4;         // [row tile][buffer]: P V of a step has landed
+  uint64_t* mma_done = o_full + 4;       // [row tile]: everything issued has
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ __align__(16) uint8_t s_valid[kValid][kKeys / 8];  // bit k of a tile: key k is there
+  __shared__ float s_tail[kTail][DH + 2];                       // the second tail warp's rows
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.z, hk = blockIdx.y;
+  const int hk = blockIdx.y;
   const int mt = blockIdx.x / p.n_split, split = blockIdx.x % p.n_split;
+  __shared__ int s_r;
+  if (p.R > 1 && p.R <= kTreeSorted) {  // the z-th longest request
+    for (int a = threadIdx.x; a < p.R; a += kTreeThreads) {
+      const int len = p.lens[a];
+      int before = 0;
+      for (int b = 0; b < p.R; ++b) {
+        const int other = __ldg(p.lens + b);
+        before += other > len || (other == len && b < a);
+      }
+      if (before == static_cast<int>(blockIdx.z)) s_r = a;
+    }
+    __syncthreads();
+  }
+  const int r = p.R > 1 && p.R <= kTreeSorted ? s_r : blockIdx.z;
   Span sp;
   if (!request_span(p, r, &sp)) return;
   const int q0 = mt * kTreeRowsCta;
@@ -168,25 +233,30 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   const int t_beg = split * p.split_tiles;
   const int nt = min(t_all, t_beg + p.split_tiles) - t_beg;
   if (nt <= 0 && !(split == 0 && p.n_split == 1)) return;
+  // steps of 64 keys (the last tile may need one only)
+  const int steps = nt > 0 ? min(2 * nt, (sp.L - t_beg * kKeys + kStepKeys - 1) / kStepKeys) : 0;
   const int odd = live % kMRows;
   const int tail = live > kMRows && odd <= kTail ? odd : 0;
   const int rows = live - tail;                  // by the tensor cores' two tiles
   const int two = rows > kMRows ? 2 : 1;
 
-  if (warp == kMmaWarp) tmem_alloc<kTmemCols>(tmem_slot);
+  if (warp == kMmaWarp0) tmem_alloc<kTmemCols>(tmem_slot);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&k_full[s], kExpandWarps);
-      mbar_init(&k_empty[s], tail ? 2 : 1);
+      mbar_init(&k_empty[s], two + (tail ? 2 : 0));
       mbar_init(&v_full[s], kExpandWarps);
-      mbar_init(&v_empty[s], tail ? 2 : 1);
+      mbar_init(&v_empty[s], two + (tail ? 2 : 0));
     }
     for (int i = 0; i < 2; ++i) {
       const int n = min(rows - i * kMRows, kMRows);  // one arrival per warp with rows
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], n > 0 ? (n + 31) / 32 : 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&s_full[2 * i + b], 1);
+        mbar_init(&p_full[2 * i + b], n > 0 ? (n + 31) / 32 : 1);
+        mbar_init(&o_full[2 * i + b], 1);
+      }
+      mbar_init(&mma_done[i], 1);
     }
-    mbar_init(o_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
     if (split == 0 && hk == 0 && mt == 0 && static_cast<long long>(p.lens[r]) + sp.n > p.max_len)
@@ -231,15 +301,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  // a warp-uniform bounded wait (lane 0 polls); false: give up
+  // a bounded wait of the whole warp; false: give up (another warp has, or
+  // the time is over)
   auto wait_w = [&](uint64_t* bar, uint32_t par) {
-    int ok = 0;
-    if (lane == 0) ok = !*abort_flag && mbar_wait(bar, par, p.err) ? 1 : 0;
-    ok = __shfl_sync(kFullMask, ok, 0);
-    __syncwarp();  // (what lane 0 has seen, the warp sees)
-    return ok != 0;
+    const uint32_t addr = smem_u32(bar);
+    bool ok = mbar_try_wait(addr, par);
+    if (!ok) {
+      const long long t0 = clock64();
+      while (!(ok = mbar_try_wait(addr, par)) && !*abort_flag)
+        if (clock64() - t0 > kWaitLimitCycles) {
+          atomicOr(p.err, DT_ERR_TIMEOUT);
+          break;
+        }
+    }
+    return __all_sync(kFullMask, ok) != 0;
   };
-  if (warp >= kExpandWarp0 && warp < kMmaWarp) {
+
+  if (warp >= kExpandWarp0 && warp < kTailWarp0) {
     // ------------------------------------------------- codes to fp16 tiles
     // Lane (key = lane / 4, c = lane % 4) of a warp's 8 keys takes the dims
     // [c DH/4, (c+1) DH/4): one load of codes, two (one) scales, DH/32 lines
@@ -366,55 +444,62 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
       look_up(f + 2);
     }
     if (!go && lane == 0) *abort_flag = 1;
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_f16(kKeys, false), idesc_o = idesc_f16(DH, true);
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t par) {
-        if (ok && !*abort_flag && mbar_wait(bar, par, p.err)) return true;
-        ok = false;
-        *abort_flag = 1;
-        return false;
-      };
-      // S_i of tile j (over P_i(j - 1), which P V(j - 1), issued before, has read)
-      auto issue_s = [&](int i, int j) {
-        const int st = j % kStages;
-        if (i == 0 && !wait(&k_full[st], static_cast<uint32_t>((j / kStages) & 1))) return;
+  } else if (warp >= kMmaWarp0 && warp - kMmaWarp0 < two) {
+    // --------------------------------------------------------- MMA issuers
+    constexpr uint32_t idesc_s = idesc_f16(kStepKeys, false), idesc_o = idesc_f16(DH, true);
+    const int i = warp - kMmaWarp0;
+    const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + i * L::kQTile));
+    const uint64_t k_desc = smem_desc_sw128(smem_u32(sStage));
+    const uint64_t v_desc = smem_desc_mn(smem_u32(sStage + L::kTile), kKeys * 128);
+    const uint32_t s_col = tmem_base + static_cast<uint32_t>(i * kKeys);
+    const uint32_t o_col = tmem_base + kColO + static_cast<uint32_t>(i * 128);
+    const bool elected = elect_one();
+    bool go = true;
+    for (int u = -2; u < steps; ++u) {  // (a step's scores two steps ahead of its products)
+      if (u >= 0) {  // O += P V of step u
+        const int f = u >> 1, st = f % kStages, b = u & 1;
+        if (!(go = wait_w(&p_full[2 * i + b], static_cast<uint32_t>(f) & 1u))) break;
+        if (b == 0 && !(go = wait_w(&v_full[st], static_cast<uint32_t>((f / kStages) & 1)))) break;
         tc_fence_after();
-        const uint32_t q_addr = smem_u32(smem + i * L::kQTile), k_addr = smem_u32(sStage + st * 2 * L::kTile);
+        if (elected) {
+          const uint64_t vd = v_desc + static_cast<uint64_t>(st * (2 * L::kTile >> 4) + b * (kStepKeys * 128 >> 4));
+          const uint32_t pa = s_col + static_cast<uint32_t>(b * kStepKeys);
 #pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk) {
-          const uint32_t off = (kk & 3) * 32u;
-          tc_mma_bf16(tmem_base + static_cast<uint32_t>(i * kKeys),
-                      smem_desc_sw128(q_addr + (kk >> 2) * (kMRows * 128) + off),
-                      smem_desc_sw128(k_addr + (kk >> 2) * (kKeys * 128) + off), idesc_s, kk != 0 ? 1u : 0u);
+          for (int kk = 0; kk < kStepKeys / 16; ++kk)  // 16 keys: two atoms of 8 lines
+            tc_mma_bf16_ta(o_col, pa + static_cast<uint32_t>(kk * 8), vd + static_cast<uint64_t>(kk * (2048 >> 4)),
+                           idesc_o, (u != 0 || kk != 0) ? 1u : 0u);
+          tc_commit(&o_full[2 * i + b]);
+          if (b == 1 || u == steps - 1) tc_commit(&v_empty[st]);
         }
-        tc_commit(&s_full[i]);
-        if (i == two - 1) tc_commit(&k_empty[st]);
-      };
-      auto issue_o = [&](int i, int j) {
-        const int st = j % kStages;
-        if (!wait(&p_full[i], static_cast<uint32_t>(j) & 1u)) return;
-        if (i == 0 && !wait(&v_full[st], static_cast<uint32_t>((j / kStages) & 1))) return;
+        __syncwarp();
+      }
+      if (u + 2 < steps) {  // S of step u + 2, over P(u), which the product just issued has read
+        const int f = (u + 2) >> 1, st = f % kStages, b = u & 1;
+        if (b == 0 && !(go = wait_w(&k_full[st], static_cast<uint32_t>((f / kStages) & 1)))) break;
         tc_fence_after();
-        const uint32_t v_addr = smem_u32(sStage + st * 2 * L::kTile + L::kTile);
-        const uint32_t pa = tmem_base + static_cast<uint32_t>(i * kKeys);
+        if (elected) {
+          // (descriptors count in 16 bytes: 16 dims are 2, the next 64 dims a
+          // tile's lines, 64 keys half of them)
+          const uint64_t kd = k_desc + static_cast<uint64_t>(st * (2 * L::kTile >> 4) + b * (kStepKeys * 128 >> 4));
+          const uint32_t col = s_col + static_cast<uint32_t>(b * kStepKeys);
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)  // 16 keys: two atoms of 8 lines
-          tc_mma_bf16_ta(tmem_base + kColO + static_cast<uint32_t>(i * 128), pa + static_cast<uint32_t>(kk * 8),
-                         smem_desc_mn(v_addr + kk * 2048, kKeys * 128), idesc_o, (j != 0 || kk != 0) ? 1u : 0u);
-        if (i == two - 1) tc_commit(&v_empty[st]);
-      };
-      for (int i = 0; i < two && ok && nt > 0; ++i) issue_s(i, 0);
-      for (int j = 0; j < nt && ok; ++j)
-        for (int i = 0; i < two && ok; ++i) {
-          issue_o(i, j);
-          if (ok && j + 1 < nt) issue_s(i, j + 1);
+          for (int kk = 0; kk < DH / 16; ++kk) {
+            constexpr uint64_t kAtom = kKeys * 128 >> 4;
+            const uint64_t off = (kk & 3) * 2 + (kk >> 2) * kAtom;
+            tc_mma_bf16(col, q_desc + off, kd + off, idesc_s, kk != 0 ? 1u : 0u);
+          }
+          tc_commit(&s_full[2 * i + b]);
+          if (b == 1 || u + 2 == steps - 1) tc_commit(&k_empty[st]);
         }
-      tc_commit(o_done);
-      mbar_wait(o_done, 0, p.err);
+        __syncwarp();
+      }
     }
+    if (!go && lane == 0) *abort_flag = 1;
+    if (elected) {  // what was issued has landed before the block may end
+      tc_commit(&mma_done[i]);
+      mbar_wait(&mma_done[i], 0, p.err);
+    }
+    __syncwarp();
   } else if (warp < kExpandWarp0 && warp * 32 < rows) {
     // ------------------------------------------------------------- softmax
     const int i = warp >> 2, row = threadIdx.x, q = q0 + row;
@@ -426,79 +511,78 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     float m = -INFINITY, l = 0.f;
     float limit = -INFINITY;  // the unscaled score above which the reference rises
     bool go = true;
-    for (int j = 0; j < nt; ++j) {
-      const int key0 = (t_beg + j) * kKeys;
-      if (!(go = wait_w(&s_full[i], static_cast<uint32_t>(j) & 1u))) break;
+    for (int u = 0; u < steps; ++u) {
+      const int f = u >> 1, b = u & 1, key0 = t_beg * kKeys + u * kStepKeys;
+      if (!(go = wait_w(&s_full[2 * i + b], static_cast<uint32_t>(f) & 1u))) break;
       tc_fence_after();
-      const uint4 there = *reinterpret_cast<const uint4*>(s_valid[j % kValid]);
-      const bool plain = key0 + kKeys <= sp.Lp && (there.x & there.y & there.z & there.w) == ~0u;
-      uint32_t pk[kKeys / 2];
-      float add;
-      // the row's weights with the reference as it is; false: it has to rise
-      auto weigh = [&]() {
-        const float sub = m == -INFINITY ? 0.f : kBias - m;
-        float top = -INFINITY;
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t x[kStepKeys];
+      tmem_ld64(s_addr + b * kStepKeys, x);
+      const uint2 there = *reinterpret_cast<const uint2*>(&s_valid[f % kValid][b * (kStepKeys / 8)]);
+      tmem_wait_ld();
+      if (key0 + kStepKeys > sp.Lp || (there.x & there.y) != ~0u) {  // -inf where not seen
+        const uint32_t lo = row_sees(key0, sp.Lp, mrow, p.words) & there.x;
+        const uint32_t hi = row_sees(key0 + 32, sp.Lp, mrow, p.words) & there.y;
 #pragma unroll
-        for (int ch = 0; ch < kKeys / 32; ++ch) {
-          uint32_t x[32];
-          tmem_ld32(s_addr + ch * 32, x);
-          tmem_wait_ld();
-          if (!plain) {
-            const uint32_t w = ch == 0 ? there.x : ch == 1 ? there.y : ch == 2 ? there.z : there.w;
-            const uint32_t see = row_sees(key0 + 32 * ch, sp.Lp, mrow, p.words) & w;
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (!((see >> k) & 1u)) x[k] = 0xFF800000u;  // -inf
-          }
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            const float a = __uint_as_float(x[k]), b = __uint_as_float(x[k + 1]);
-            top = fmaxf(top, fmaxf(a, b));
-            const float pa = ex2(fmaf(a, fac, sub)), pb = ex2(fmaf(b, fac, sub));
-            part[(k >> 1) & 3] += pa + pb;
-            pk[ch * 16 + k / 2] = pack_f16(pa, pb);
-          }
+        for (int k = 0; k < 32; ++k) {
+          if (!((lo >> k) & 1u)) x[k] = 0xFF800000u;
+          if (!((hi >> k) & 1u)) x[32 + k] = 0xFF800000u;
         }
-        add = (part[0] + part[1]) + (part[2] + part[3]);
-        if (!__any_sync(kFullMask, top > limit)) return true;
-        if (top > limit) {
-          const float t = top * fac, alpha = ex2(m - t);  // (0 from -inf)
-          m = t;
-          limit = __fdividef(t + kRaise, fac);
-          l *= alpha;
-          part[0] = alpha;
-        } else {
-          part[0] = 1.f;
-        }
-        if (j > 0) {  // O holds the products of the tiles before
-#pragma unroll
-          for (int ch = 0; ch < DH / 16; ++ch) {
-            float x[16];
-            tmem_ld16(o_addr + ch * 16, x);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] *= part[0];
-            tmem_st16(o_addr + ch * 16, x);
-          }
-        }
-        return false;
-      };
-      if (!weigh()) weigh();  // (the second time no score passes the limit)
-      l += add;
-      uint32_t half[32];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k) half[k] = pk[32 * h + k];
-        tmem_st32(s_addr + 32 * h, half);
       }
+      float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < kStepKeys; k += 2)
+        t[(k >> 1) & 3] = fmaxf(t[(k >> 1) & 3], fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
+      const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+      if (__any_sync(kFullMask, top > limit)) {
+        float alpha = 1.f;
+        if (top > limit) {
+          const float y = top * fac;
+          alpha = ex2(m - y);  // (0 from -inf)
+          m = y;
+          limit = __fdividef(y + kRaise, fac);
+          l *= alpha;
+        }
+        if (u > 0) {
+          // O holds the products of the steps before, once the last has landed
+          // (the scores of this step came after the one of u - 2, and the
+          // barrier of u - 1 is that of u - 3: its parity is certain)
+          if (!(go = wait_w(&o_full[2 * i + (b ^ 1)], static_cast<uint32_t>((u - 1) >> 1) & 1u))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int ch = 0; ch < DH / 16; ++ch) {
+            float y[16];
+            tmem_ld16(o_addr + ch * 16, y);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) y[k] *= alpha;
+            tmem_st16(o_addr + ch * 16, y);
+          }
+        }
+      }
+      // the weights, over the columns their scores came from
+      const float sub = m == -INFINITY ? 0.f : kBias - m;
+      const uint64_t fac2 = pack2(fac, fac), sub2 = pack2(sub, sub);
+      uint64_t sum[2] = {0ull, 0ull};
+      uint32_t pk[kStepKeys / 2];
+#pragma unroll
+      for (int k = 0; k < kStepKeys; k += 2) {
+        float a, c;
+        unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), fac2, sub2), a, c);
+        a = ex2(a);
+        c = ex2(c);
+        sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, c));
+        pk[k / 2] = pack_f16(a, c);
+      }
+      tmem_st32(s_addr + b * kStepKeys, pk);
+      float a, c;
+      unpack2(add2(sum[0], sum[1]), a, c);
+      l += a + c;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[i]);
+      if (lane == 0) mbar_arrive(&p_full[2 * i + b]);
     }
     if (!go && lane == 0) *abort_flag = 1;
-    const bool have = go && nt > 0 && wait_w(o_done, 0);
+    const bool have = go && steps > 0 && wait_w(&mma_done[i], 0);
     if (have) tc_fence_after();
     else l = 0.f;
     const bool on = row < rows;
@@ -533,12 +617,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
         }
       }
     }
-  } else if (warp == kTailWarp && tail > 0) {
+  } else if ((warp == kTailWarp0 || warp == kTailWarp0 + 1) && tail > 0) {
     // ------------------------------------------------------------ tail rows
     // S^T = K Q^T and O^T += V^T P^T by mma m16n8k16 with the tiles' keys as
-    // the 16-row operand (as the kernel of few rows does from the codes).
-    const int rr = lane >> 2, c = lane & 3;
-    constexpr int kSteps = DH / 16, kGroups = kKeys / 16;
+    // the 16-row operand (as the kernel of few rows does from the codes).  The
+    // loops run over independent sums inside.
+    const int rr = lane >> 2, c = lane & 3, tw = warp - kTailWarp0;
+    constexpr int kSteps = DH / 16, kGroups = kKeys / 32;  // 16-key groups of this warp
     uint32_t qb[kSteps][2];
     float tf[2];
     int nd[2];
@@ -578,21 +663,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     const int lr = lane & 7, lm = lane >> 3;  // ldmatrix: row lr of matrix lm
     bool go = true;
     for (int j = 0; j < nt; ++j) {
-      const int st = j % kStages, key0 = (t_beg + j) * kKeys;
+      const int st = j % kStages, key0 = (t_beg + j) * kKeys + tw * (kKeys / 2);
       const uint32_t ph = static_cast<uint32_t>((j / kStages) & 1);
       if (!(go = wait_w(&k_full[st], ph))) break;
       const uint32_t k_addr = smem_u32(sStage + st * 2 * L::kTile), v_addr = k_addr + L::kTile;
-      const uint4 there = *reinterpret_cast<const uint4*>(s_valid[j % kValid]);
-      const bool plain = key0 + kKeys <= sp.Lp && (there.x & there.y & there.z & there.w) == ~0u;
+      const uint2 there = *reinterpret_cast<const uint2*>(&s_valid[j % kValid][tw * (kKeys / 16)]);
+      const bool plain = key0 + kKeys / 2 <= sp.Lp && (there.x & there.y) == ~0u;
       float s[kGroups][4];
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        s[g][0] = s[g][1] = s[g][2] = s[g][3] = 0.f;
-        const int key = 16 * g + lr + 8 * (lm & 1);  // matrices: keys 0-7 | 8-15, dims 0-7; the same, dims 8-15
+      for (int g = 0; g < kGroups; ++g) s[g][0] = s[g][1] = s[g][2] = s[g][3] = 0.f;
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
+      for (int k = 0; k < kSteps; ++k) {
+        const int gr = 2 * k + (lm >> 1);  // matrices: keys 0-7 | 8-15, dims 0-7; the same, dims 8-15
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
           uint32_t a[4];
-          const int gr = 2 * k + (lm >> 1);
+          const int key = tw * (kKeys / 2) + 16 * g + lr + 8 * (lm & 1);
           ldmatrix_x4(k_addr + (gr >> 3) * (kKeys * 128) + sw128(key, gr & 7), a);
           mma_f16(s[g], a, qb[k][0], qb[k][1]);
         }
@@ -606,8 +692,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
         for (int x = 0; x < 4; ++x) {
           if (!plain) {
             const int kk = 16 * g + 8 * (x >> 1) + rr, pos = key0 + kk;
-            const uint32_t w = g < 2 ? there.x : g < 4 ? there.y : g < 6 ? there.z : there.w;
-            bool seen = (w >> (kk & 31)) & 1u;
+            bool seen = ((g < 2 ? there.x : there.y) >> (kk & 31)) & 1u;
             if (seen && pos >= sp.Lp) {
               const int t = pos - sp.Lp, n = nd[x & 1];
               seen = n > 0 &&
@@ -654,12 +739,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
         }
       if (!(go = wait_w(&v_full[st], ph))) break;
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        const int gr = 2 * k + (lm & 1);  // matrices: dims 0-7 | 8-15, keys 0-7; the same, keys 8-15
+      for (int g = 0; g < kGroups; ++g) {
+        const int key = tw * (kKeys / 2) + 16 * g + lr + 8 * (lm >> 1);
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
+        for (int k = 0; k < kSteps; ++k) {
           uint32_t a[4];
-          ldmatrix_x4_trans(v_addr + (gr >> 3) * (kKeys * 128) + sw128(16 * g + lr + 8 * (lm >> 1), gr & 7), a);
+          const int gr = 2 * k + (lm & 1);  // matrices: dims 0-7 | 8-15, keys 0-7; the same, keys 8-15
+          ldmatrix_x4_trans(v_addr + (gr >> 3) * (kKeys * 128) + sw128(key, gr & 7), a);
           mma_f16(o[k], a, pb[g][0], pb[g][1]);
         }
       }
@@ -667,22 +753,48 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
       if (lane == 0) mbar_arrive(&v_empty[st]);
     }
     if (!go && lane == 0) *abort_flag = 1;
+    // the second warp's rows to the first, which joins them
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
 #pragma unroll
       for (int d = 4; d < 32; d *= 2) l[x] += __shfl_xor_sync(kFullMask, l[x], d);
+      if (tw == 1) {
+        float* dst = s_tail[2 * c + x];
+        if (rr == 0) {
+          dst[DH] = m[x];
+          dst[DH + 1] = l[x];
+        }
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          dst[16 * k + rr] = o[k][x];
+          dst[16 * k + 8 + rr] = o[k][2 + x];
+        }
+      }
+    }
+    asm volatile("bar.sync 1, 64;" ::: "memory");
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
       const int row = 2 * c + x;
-      if (row >= tail) continue;
+      if (tw == 1 || row >= tail) continue;
+      const float* other = s_tail[row];
+      const float M = fmaxf(m[x], other[DH]);
+      const float f0 = m[x] == -INFINITY ? 0.f : ex2(m[x] - M), f1 = other[DH] == -INFINITY ? 0.f : ex2(other[DH] - M);
+      const float Lr = l[x] * f0 + other[DH + 1] * f1;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        o[k][x] = o[k][x] * f0 + other[16 * k + rr] * f1;
+        o[k][2 + x] = o[k][2 + x] * f0 + other[16 * k + 8 + rr] * f1;
+      }
       if (p.n_split > 1) {
         float* dst = cache_part_row(p, r, hk, mt, split, rows + row);
-        if (rr == 0) *reinterpret_cast<float2*>(dst) = make_float2(m[x], l[x]);
+        if (rr == 0) *reinterpret_cast<float2*>(dst) = make_float2(M, Lr);
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
           dst[2 + 16 * k + rr] = o[k][x];
           dst[2 + 16 * k + 8 + rr] = o[k][2 + x];
         }
       } else {
-        const float inv = l[x] > 0.f ? p.c.v_scale / l[x] : 0.f;
+        const float inv = Lr > 0.f ? p.c.v_scale / Lr : 0.f;
         uint16_t* dst = p.O + cache_out_row(p, r, hk, q0 + rows + row);
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
@@ -694,7 +806,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kMmaWarp0) {
     tc_fence_after();
     tmem_dealloc<kTmemCols>(tmem_base);
   }
