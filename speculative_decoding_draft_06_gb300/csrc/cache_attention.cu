@@ -73,7 +73,7 @@ struct __align__(128) AttnSmem {
 };
 
 template <int DH, int NQ>
-__global__ void __launch_bounds__(kThreads, 3) k_cache_attention(const CacheAttnParams p) {
+__device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
   constexpr int kSteps = DH / 16;   // k-steps of S^T, dim tiles of O^T
   constexpr int kRows = 8 * NQ;
   using T = Tile<DH>;
@@ -83,7 +83,14 @@ __global__ void __launch_bounds__(kThreads, 3) k_cache_attention(const CacheAttn
   const int split = blockIdx.x, hk = blockIdx.y, r = blockIdx.z;
   Span sp;
   if (!request_span(p, r, &sp)) return;
-  const int live = (sp.n + 1) * p.g;  // rows (one row tile)
+  // rows q0 .. q0 + live - 1
+  int q0 = 0, live = (sp.n + 1) * p.g;
+  if (p.tail) {
+    q0 = live;
+    live = tail_rows(live);
+    if (live == 0) return;
+    q0 -= live;
+  }
   const int t_all = row_tile_keys(p, sp, 0);
   const int t_beg = split * p.split_tiles;
   const int nt = min(t_all, t_beg + p.split_tiles) - t_beg;
@@ -94,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_cache_attention(const CacheAttn
   if (lane < kStages) mbar_init(&sm.full[warp][lane], 1);
   fence_mbar_init();
   __syncwarp();
-  if (threadIdx.x == 0 && split == 0 && hk == 0 && static_cast<long long>(p.lens[r]) + sp.n > p.max_len)
+  if (threadIdx.x == 0 && split == 0 && hk == 0 && !p.tail && static_cast<long long>(p.lens[r]) + sp.n > p.max_len)
     atomicOr(p.err, DT_ERR_BAD_INDEX);
 
   // ---- the warp's copies: lane (piece, segment) has one of a tile's (a
@@ -157,9 +164,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_cache_attention(const CacheAttn
   int node[NQ][2];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    const int q = 8 * n + rr;
-    const bool on = q < live;
-    const int nd = on ? q / p.g : 0;
+    const bool on = 8 * n + rr < live;
+    const int q = on ? q0 + 8 * n + rr : 0, nd = q / p.g;
     uint32_t w[DH / 8];
     const uint4* src = reinterpret_cast<const uint4*>(
         p.Q + (static_cast<size_t>(r) * (p.B + 1) + nd) * p.q_stride +
@@ -447,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_cache_attention(const CacheAttn
       if (lane == 0) *reinterpret_cast<float2*>(dst) = make_float2(M, L);
     } else {
       const float inv = L > 0.f ? p.c.v_scale / L : 0.f;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row(p, r, hk, row) + lane * kE);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row(p, r, hk, q0 + row) + lane * kE);
 #pragma unroll
       for (int e = 0; e < kE; e += 2) dst[e / 2] = pack_bf16(v[e] * inv, v[e + 1] * inv);
     }
@@ -472,10 +478,19 @@ __global__ void __launch_bounds__(kThreads, 3) k_cache_attention(const CacheAttn
       for (int e = 0; e < kE; ++e) v[e] += sm.recv[k * each + at][lane * kE + e] * f;
     }
     const float inv = L > 0.f ? p.c.v_scale / L : 0.f;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row(p, r, hk, row) + lane * kE);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row(p, r, hk, q0 + row) + lane * kE);
 #pragma unroll
     for (int e = 0; e < kE; e += 2) dst[e / 2] = pack_bf16(v[e] * inv, v[e + 1] * inv);
   }
+}
+
+template <int DH, int NQ>
+__global__ void __launch_bounds__(kThreads, 3) k_cache_attention(const CacheAttnParams p) {
+  attend_rows<DH, NQ>(p);
+  // The rows left over by the tensor-core kernel: launched while that one
+  // runs, whose outputs these are not; one CTA sees it complete, so that what
+  // follows this launch follows both.
+  if (p.tail && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) pdl_wait();
 }
 
 template <int DH, int NQ>
@@ -485,9 +500,9 @@ cudaError_t launch_rows(const CacheAttnParams& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const dim3 grid(p.n_split, p.c.Hkv, p.R);
   if (p.cluster)
-    return launch_kernel_cluster(k_cache_attention<DH, NQ>, grid, dim3(kThreads), sizeof(AttnSmem<DH, NQ>), st, false,
-                                 p.n_split, p);
-  return launch_kernel(k_cache_attention<DH, NQ>, grid, dim3(kThreads), sizeof(AttnSmem<DH, NQ>), st, false, p);
+    return launch_kernel_cluster(k_cache_attention<DH, NQ>, grid, dim3(kThreads), sizeof(AttnSmem<DH, NQ>), st,
+                                 p.tail != 0, p.n_split, p);
+  return launch_kernel(k_cache_attention<DH, NQ>, grid, dim3(kThreads), sizeof(AttnSmem<DH, NQ>), st, p.tail != 0, p);
 }
 
 // The shares of each row over the key splits, joined in a fixed order: M =
@@ -503,17 +518,21 @@ __global__ void __launch_bounds__(256) k_cache_attention_join(const CacheAttnPar
   const int q = blockIdx.x * kPerBlock + warp / W, hk = blockIdx.y, r = blockIdx.z;
   pdl_wait();
   Span sp;
-  const bool on = request_span(p, r, &sp) && q < (sp.n + 1) * p.g;
+  bool on = request_span(p, r, &sp);
+  int q0 = 0;  // the launch's first row
+  if (on) {
+    const int all = (sp.n + 1) * p.g, tail = p.tile_rows == kTreeRowsCta || p.tail ? tail_rows(all) : 0;
+    q0 = p.tail ? all - tail : 0;
+    on = q < (p.tail ? tail : all - tail);
+  }
   if (W == 1 && !on) return;
   float M = -INFINITY, L = 0.f, v[kE];
 #pragma unroll
   for (int e = 0; e < kE; ++e) v[e] = 0.f;
   if (on) {
-    // (the rows behind a request's last whole tile may be that tile's tail)
-    int mt = q / p.tile_rows;
-    if (p.part_rows > p.tile_rows && mt > 0 && (sp.n + 1) * p.g - mt * p.tile_rows <= kTreeTail) --mt;
+    const int mt = q / p.tile_rows;
     const int ns = (row_tile_keys(p, sp, mt) + p.split_tiles - 1) / p.split_tiles;  // splits that had keys
-    const size_t step = static_cast<size_t>(p.part_rows) * (DH + 2);
+    const size_t step = static_cast<size_t>(p.tile_rows) * (DH + 2);
     const float* src = cache_part_row(p, r, hk, mt, 0, q - mt * p.tile_rows);
     for (int s = w + lane * W; s < ns; s += 32 * W) M = fmaxf(M, src[s * step]);
 #pragma unroll
@@ -553,16 +572,16 @@ __global__ void __launch_bounds__(256) k_cache_attention_join(const CacheAttnPar
     }
   }
   const float inv = L > 0.f ? p.c.v_scale / L : 0.f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row(p, r, hk, q) + lane * kE);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row(p, r, hk, q0 + q) + lane * kE);
 #pragma unroll
   for (int e = 0; e < kE; e += 2) dst[e / 2] = pack_bf16(v[e] * inv, v[e + 1] * inv);
 }
 
 template <int DH>
 cudaError_t launch_join(const CacheAttnParams& p, cudaStream_t st) {
-  // eight warps per row where a row has many shares (or few rows would leave
-  // the GPU to a handful of blocks), one warp where it has a few
-  if (p.n_split > 8)
+  // eight warps per row where a row has many shares and few rows would leave
+  // the GPU to a handful of blocks
+  if (p.n_split > 8 && static_cast<long long>(p.R) * p.c.Hkv * p.rows < 152 * 16)
     return launch_kernel(k_cache_attention_join<DH, 8>, dim3(p.rows, p.c.Hkv, p.R), dim3(256), 0, st, true, p);
   return launch_kernel(k_cache_attention_join<DH, 1>, dim3((p.rows + 7) / 8, p.c.Hkv, p.R), dim3(256), 0, st, true, p);
 }
@@ -579,33 +598,48 @@ constexpr int kTreeRows = 16;
 constexpr int kSplitTiles = 32;  // 2048 keys
 
 struct Plan {
-  int tile_rows, part_rows, tile_keys, m_tiles, n_split, split_tiles, cluster;
+  int rows, tile_rows, tile_keys, m_tiles, n_split, split_tiles, cluster;
   size_t work;
 };
 
-Plan plan_of(int R, int B, int max_len, int Hq, int Hkv, int dh) {
+Plan plan_rows(bool tree, long long rows, int R, int max_len, int Hkv, int dh, int most_splits) {
   Plan pl;
-  const long long rows = static_cast<long long>(B + 1) * (Hq / Hkv);
-  const bool tree = rows > kTreeRows;
+  pl.rows = static_cast<int>(rows);
   pl.tile_rows = tree ? kTreeRowsCta : rows > 8 ? 16 : 8;
-  pl.part_rows = tree ? kTreeRowsCta + kTreeTail : pl.tile_rows;
   pl.tile_keys = tree ? 128 : kTileKeys;
-  // (a request with fewer nodes than B may end in any tile)
-  pl.m_tiles = static_cast<int>((rows + pl.tile_rows - 1) / pl.tile_rows);
-  if (tree && pl.m_tiles > 1 && rows % kTreeRowsCta != 0 && rows % kTreeRowsCta <= kTreeTail) --pl.m_tiles;
+  // (a tree's rows behind its last whole tile of 128 are planned by themselves)
+  const int odd = static_cast<int>(rows % kTreeTile);
+  const long long mine = tree && rows > kTreeTile && odd <= kTreeTail ? rows - odd : rows;
+  pl.m_tiles = static_cast<int>((mine + pl.tile_rows - 1) / pl.tile_rows);
   const int tiles = max_len < 1 ? 1 : (max_len - 1) / pl.tile_keys + 1;
   const long long ctas = static_cast<long long>(R) * Hkv * pl.m_tiles;
   long long n = tree ? 152 / ctas : (152 * 3 + ctas - 1) / ctas;
   if (!tree && n < (tiles + kSplitTiles - 1) / kSplitTiles) n = (tiles + kSplitTiles - 1) / kSplitTiles;
   const long long most = tree ? (tiles + 3) / 4 : (tiles + kWarps - 1) / kWarps;
   n = n < most ? n : most;
+  n = n < most_splits ? n : most_splits;
   n = n < 1 ? 1 : n;
   pl.split_tiles = static_cast<int>((tiles + n - 1) / n);
   if (!tree) pl.split_tiles = (pl.split_tiles + kWarps - 1) / kWarps * kWarps;
   pl.n_split = (tiles + pl.split_tiles - 1) / pl.split_tiles;
-  pl.cluster = !tree && pl.n_split > 1 && pl.n_split <= kMaxCluster && ctas * pl.n_split <= 152 * 2;
-  pl.work = pl.n_split > 1 && !pl.cluster ? static_cast<size_t>(ctas) * pl.n_split * pl.part_rows * (dh + 2) * sizeof(float) : 0;
+  pl.cluster = !tree && pl.n_split > 1 && pl.n_split <= kMaxCluster &&
+               (ctas * pl.n_split <= 152 * 6 || most_splits == kMaxCluster);
+  pl.work = pl.n_split > 1 && !pl.cluster
+                ? static_cast<size_t>(ctas) * pl.n_split * pl.tile_rows * (dh + 2) * sizeof(float)
+                : 0;
   return pl;
+}
+
+// The launches of a call: [0] all rows, or those of whole tiles; [1] (tree
+// only) the rows behind them, where a request may have some.
+int plan_of(int R, int B, int max_len, int Hq, int Hkv, int dh, Plan (&pl)[2]) {
+  const long long rows = static_cast<long long>(B + 1) * (Hq / Hkv);
+  const bool tree = rows > kTreeRows;
+  pl[0] = plan_rows(tree, rows, R, max_len, Hkv, dh, 1 << 30);
+  if (!tree || rows <= kTreeTile) return 1;
+  // (up to a cluster: they run beside the others and need no launch more)
+  pl[1] = plan_rows(false, kTreeTail, R, max_len, Hkv, dh, kMaxCluster);
+  return 2;
 }
 
 }  // namespace
@@ -616,7 +650,9 @@ extern "C" size_t dartree_cache_attention_workspace(int32_t R, int32_t B, int32_
   if (R < 1 || B < 0 || B > DARTREE_MAX_B || max_len < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 ||
       (dh != 64 && dh != 128))
     return 0;
-  return dt::plan_of(R, B, max_len, Hq, Hkv, dh).work;
+  dt::Plan pl[2];
+  dt::plan_of(R, B, max_len, Hq, Hkv, dh, pl);
+  return pl[0].work;
 }
 
 extern "C" dartree_status dartree_cache_attention(const dartree_cache* cache, int32_t layer, const void* Q,
@@ -640,11 +676,12 @@ extern "C" dartree_status dartree_cache_attention(const dartree_cache* cache, in
     return cache_fail(DARTREE_ERR_INVALID_ARG, "q_token_stride must be a multiple of 8, at least Hq * dh");
   if ((reinterpret_cast<uintptr_t>(Q) | reinterpret_cast<uintptr_t>(O) | reinterpret_cast<uintptr_t>(work)) & 15)
     return cache_fail(DARTREE_ERR_INVALID_ARG, "Q, O and work must be 16-byte aligned");
-  const Plan pl = plan_of(R, B, max_len, Hq, p.c.Hkv, dh);
-  if (pl.work > 0 && (!work || work_bytes < pl.work))
+  Plan pl[2];
+  const int launches = plan_of(R, B, max_len, Hq, p.c.Hkv, dh, pl);
+  if (pl[0].work > 0 && (!work || work_bytes < pl[0].work))
     return cache_fail(DARTREE_ERR_INVALID_ARG, "work is smaller than dartree_cache_attention_workspace()");
   p.g = Hq / p.c.Hkv;
-  if (R > 65535 || static_cast<long long>(p.c.Hkv) * pl.m_tiles > 65535 || max_len > (1 << 30))
+  if (R > 65535 || static_cast<long long>(p.c.Hkv) * pl[0].m_tiles > 65535 || max_len > (1 << 30))
     return cache_fail(DARTREE_ERR_UNSUPPORTED, "too many requests, heads or keys");
   p.c.pool += static_cast<size_t>(layer) * p.c.layer_bytes;
   p.Q = static_cast<const uint16_t*>(Q);
@@ -659,29 +696,34 @@ extern "C" dartree_status dartree_cache_attention(const dartree_cache* cache, in
   p.max_len = max_len;
   p.Hq = Hq;
   p.words = (B + 31) / 32;
-  p.rows = (B + 1) * p.g;
-  p.tile_rows = pl.tile_rows;
-  p.part_rows = pl.part_rows;
-  p.tile_keys = pl.tile_keys;
-  p.m_tiles = pl.m_tiles;
-  p.n_split = pl.n_split;
-  p.split_tiles = pl.split_tiles;
-  p.cluster = pl.cluster;
   p.scale_log2 = scale * 1.4426950408889634f * p.c.k_scale;
   p.O = static_cast<uint16_t*>(O);
-  p.part = static_cast<float*>(work);
   p.err = err;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (!p.err) e = cudaGetSymbolAddress(reinterpret_cast<void**>(&p.err), g_cache_err);
   if (e != cudaSuccess) return cache_launched(e);
-  if (pl.tile_rows == kTreeRowsCta) {
-    e = launch_cache_tree(p, st);
-  } else if (pl.tile_rows == 8) {
-    e = dh == 128 ? launch_rows<128, 1>(p, st) : launch_rows<64, 1>(p, st);
-  } else {
-    e = dh == 128 ? launch_rows<128, 2>(p, st) : launch_rows<64, 2>(p, st);
+  // (without n_nodes it is known here whether rows are left over)
+  const int odd = pl[0].rows % kTreeTile;
+  const int run = launches > 1 && !n_nodes && (odd == 0 || odd > kTreeTail) ? 1 : launches;
+  CacheAttnParams first = p;
+  for (int k = 0; k < run && e == cudaSuccess; ++k) {
+    p.rows = pl[k].rows;
+    p.tile_rows = pl[k].tile_rows;
+    p.tile_keys = pl[k].tile_keys;
+    p.m_tiles = pl[k].m_tiles;
+    p.n_split = pl[k].n_split;
+    p.split_tiles = pl[k].split_tiles;
+    p.cluster = pl[k].cluster;
+    p.tail = k;
+    p.part = static_cast<float*>(work);
+    if (k == 0) first = p;
+    if (p.tile_rows == kTreeRowsCta) e = launch_cache_tree(p, st);
+    else if (p.tile_rows == 8) e = dh == 128 ? launch_rows<128, 1>(p, st) : launch_rows<64, 1>(p, st);
+    else e = dh == 128 ? launch_rows<128, 2>(p, st) : launch_rows<64, 2>(p, st);
   }
-  if (e == cudaSuccess && pl.n_split > 1 && !pl.cluster) e = dh == 128 ? launch_join<128>(p, st) : launch_join<64>(p, st);
+  // (the rows left over have joined in their cluster)
+  if (e == cudaSuccess && first.n_split > 1 && !first.cluster)
+    e = dh == 128 ? launch_join<128>(first, st) : launch_join<64>(first, st);
   return cache_launched(e);
 }

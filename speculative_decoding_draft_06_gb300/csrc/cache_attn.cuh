@@ -10,9 +10,11 @@ namespace dt {
 constexpr float kBias = 6.f;   // the reference maximum's weight is 2^kBias
 constexpr float kRaise = 8.f;  // the reference rises when a score passes it by this
 
-// Rows of a CTA of the tensor-core kernel: two tiles of 128, and up to
-// kTreeTail more in the last.
-constexpr int kTreeRowsCta = 256, kTreeTail = 8;
+// Rows of a CTA of the tensor-core kernel: two tiles of 128.  Up to kTreeTail
+// rows that a request has behind its last whole tile of 128 (a tree of 2^k
+// nodes and its root: the root's) are the few-rows kernel's, in a launch of
+// their own.
+constexpr int kTreeRowsCta = 256, kTreeTile = 128, kTreeTail = 8;
 
 struct CacheAttnParams {
   CacheView c;              // the layer
@@ -22,13 +24,13 @@ struct CacheAttnParams {
   const int32_t *n_nodes, *table, *lens;
   int max_pages, R, B, max_len, Hq, g, words, rows;
   int tile_rows, tile_keys;  // of the kernel: 8 or 16 x 64, 256 x 128
-  int part_rows;             // rows of a row tile in the workspace
   int m_tiles;               // row tiles
   int n_split, split_tiles;  // key tiles per split
   int cluster;               // the splits are one cluster and join there
+  int tail;                  // the few-rows kernel works on the rows behind the whole tiles
   float scale_log2;          // scale * log2(e) * k_scale
   uint16_t* O;               // [R][B+1][Hq][dh]
-  float* part;               // [R][Hkv][m_tiles][n_split][part_rows][dh + 2] (n_split > 1)
+  float* part;               // [R][Hkv][m_tiles][n_split][tile_rows][dh + 2] (n_split > 1)
   int* err;
 };
 
@@ -48,10 +50,17 @@ __device__ __forceinline__ bool request_span(const CacheAttnParams& p, int r, Sp
 }
 
 
-// Key tiles that the rows of row tile mt (and its tail) can see: the prefix
+// The rows behind a request's whole tiles of 128 that are the few-rows
+// kernel's (of `rows` in all).
+__device__ __forceinline__ int tail_rows(int rows) {
+  const int odd = rows % kTreeTile;
+  return rows > kTreeTile && odd <= kTreeTail ? odd : 0;
+}
+
+// Key tiles that the rows of row tile mt can see: the prefix
 // and the nodes up to the tile's last row's.
 __device__ __forceinline__ int row_tile_keys(const CacheAttnParams& p, const Span& s, int mt) {
-  const int last = min(s.n, (mt * p.tile_rows + p.part_rows - 1) / p.g);
+  const int last = p.tail ? s.n : min(s.n, (mt * p.tile_rows + p.tile_rows - 1) / p.g);
   const int keys = min(s.L, s.Lp + last);
   return (keys + p.tile_keys - 1) / p.tile_keys;
 }
@@ -110,7 +119,7 @@ __device__ __forceinline__ size_t cache_out_row(const CacheAttnParams& p, int r,
 // unnormalised outputs.
 __device__ __forceinline__ float* cache_part_row(const CacheAttnParams& p, int r, int hk, int mt, int split, int row) {
   const size_t tile = ((static_cast<size_t>(r) * p.c.Hkv + hk) * p.m_tiles + mt) * p.n_split + split;
-  return p.part + (tile * p.part_rows + row) * (p.c.dh + 2);
+  return p.part + (tile * p.tile_rows + row) * (p.c.dh + 2);
 }
 
 // The tensor-core kernel of many rows (cache_tree.cu).

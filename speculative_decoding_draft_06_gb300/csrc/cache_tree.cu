@@ -3,15 +3,13 @@
 // key/value head).
 //
 // A CTA owns up to 256 query rows of one request and one key/value head, as
-// two tiles of 128 (a TMEM lane each), up to 8 more ("tail": a tree of 2^k
-// nodes and its root are a few rows more than whole tiles), and a share of
-// the key range in tiles of 128 keys.  Warp roles (512 threads):
+// two tiles of 128 (a TMEM lane each), and a share of the key range in tiles
+// of 128 keys.  Warp roles (576 threads):
 //   0-3, 4-7  softmax of the two row tiles: a thread owns a row;
-//   8-11      expand: codes and scales from memory to fp16 keys and values in
-//             shared memory (exact), a tile ahead in registers;
-//   12-13     the tail rows, by mma.sync on the same fp16 tiles, half of a
-//             tile's keys each;
-//   14, 15    issue the MMAs of one row tile each (14 owns the TMEM): what
+//   8-15      expand: codes and scales from memory to fp16 keys (8-11) and
+//             values (12-15) in shared memory (exact), a tile ahead in
+//             registers;
+//   16, 17    issue the MMAs of one row tile each (16 owns the TMEM): what
 //             waits on the issue all wait for, and two warps issue twice as fast.
 // In steps of 64 keys: S = Q K^T (M 128, N 64, fp16, fp32 sums) into TMEM,
 // double-buffered per row tile, P = 2^(s - m + kBias) in fp16 over the S
@@ -32,16 +30,35 @@ namespace dt {
 namespace {
 
 constexpr int kMRows = 128, kKeys = 128, kStepKeys = 64;
-constexpr int kExpandWarp0 = 8, kExpandWarps = 4, kTailWarp0 = 12, kMmaWarp0 = 14;
-constexpr int kTreeThreads = 16 * 32;
+constexpr int kExpandWarp0 = 8, kExpandWarps = 8, kMmaWarp0 = 16;
+constexpr int kTreeThreads = 18 * 32;
 constexpr int kStages = 2;
 // (a tile's keys are expanded after all scores of the tile two before are
 // issued, and they after the weights of the tile three before are there)
 constexpr int kValid = 4;
-constexpr int kTail = kTreeTail;
-constexpr int kTreeSorted = 256;  // requests that are taken longest first (each CTA ranks them: R^2 / 512 steps)
+constexpr int kTreeSorted = 256;  // requests that are taken longest first (each CTA ranks them: R^2 / 576 steps)
 constexpr uint32_t kTmemCols = 512;  // S of row tile i, buffer b: 128 i + 64 b; O of row tile i: 256 + 128 i; P over S
 constexpr uint32_t kColO = 256;
+
+// Pairs of fp32 in one operand (two lanes of the fp32 pipe per instruction).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 
 template <int DH>
 struct TreeSmem {
@@ -84,25 +101,16 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t lead) 
   return d;
 }
 
-// 32 consecutive columns of the thread's lane (no wait: tmem_wait_ld).
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
+// 64 consecutive columns of the thread's lane (one statement with its wait: no
+// use of a value can come before it).
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
       "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
@@ -111,42 +119,8 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
         "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
         "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
         "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-      : "r"(taddr));
-}
-
-// Pairs of fp32 in one operand (two lanes of the fp32 pipe per instruction).
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-  return d;
-}
-__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+      : "r"(taddr)
+      : "memory");
 }
 
 // Codes and scales are read once: past L1.
@@ -204,11 +178,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ __align__(16) uint8_t s_valid[kValid][kKeys / 8];  // bit k of a tile: key k is there
-  __shared__ float s_tail[kTail][DH + 2];                       // the second tail warp's rows
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hk = blockIdx.y;
   const int mt = blockIdx.x / p.n_split, split = blockIdx.x % p.n_split;
+  pdl_trigger();  // (the launch of the rows left over may fill the SMs that come free)
   __shared__ int s_r;
   if (p.R > 1 && p.R <= kTreeSorted) {  // the z-th longest request
     for (int a = threadIdx.x; a < p.R; a += kTreeThreads) {
@@ -226,27 +200,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   Span sp;
   if (!request_span(p, r, &sp)) return;
   const int q0 = mt * kTreeRowsCta;
-  int live = (sp.n + 1) * p.g - q0;              // rows of this CTA: 256, and the tail in the last
-  if (live > kTreeRowsCta + kTail) live = kTreeRowsCta;
-  if (live <= 0 || (mt > 0 && live <= kTail)) return;  // (the tile before has them as its tail)
+  // rows of this CTA, without the few behind the request's last whole tile
+  const int all = (sp.n + 1) * p.g;
+  const int rows = min(all - tail_rows(all) - q0, kTreeRowsCta);
+  if (rows <= 0) return;
   const int t_all = row_tile_keys(p, sp, mt);
   const int t_beg = split * p.split_tiles;
   const int nt = min(t_all, t_beg + p.split_tiles) - t_beg;
   if (nt <= 0 && !(split == 0 && p.n_split == 1)) return;
   // steps of 64 keys (the last tile may need one only)
   const int steps = nt > 0 ? min(2 * nt, (sp.L - t_beg * kKeys + kStepKeys - 1) / kStepKeys) : 0;
-  const int odd = live % kMRows;
-  const int tail = live > kMRows && odd <= kTail ? odd : 0;
-  const int rows = live - tail;                  // by the tensor cores' two tiles
   const int two = rows > kMRows ? 2 : 1;
 
   if (warp == kMmaWarp0) tmem_alloc<kTmemCols>(tmem_slot);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&k_full[s], kExpandWarps);
-      mbar_init(&k_empty[s], two + (tail ? 2 : 0));
-      mbar_init(&v_full[s], kExpandWarps);
-      mbar_init(&v_empty[s], two + (tail ? 2 : 0));
+      mbar_init(&k_full[s], kExpandWarps / 2);
+      mbar_init(&k_empty[s], two);
+      mbar_init(&v_full[s], kExpandWarps / 2);
+      mbar_init(&v_empty[s], two);
     }
     for (int i = 0; i < 2; ++i) {
       const int n = min(rows - i * kMRows, kMRows);  // one arrival per warp with rows
@@ -271,12 +243,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     const uint4* src = reinterpret_cast<const uint4*>(
         p.Q + (static_cast<size_t>(r) * (p.B + 1) + node) * p.q_stride +
         static_cast<size_t>(hk * p.g + (on ? q - node * p.g : 0)) * DH);
-    uint4 w[DH / 8];
     float top = 0.f;
-#pragma unroll
+#pragma unroll 4
     for (int k = 0; k < DH / 8; ++k) {
-      w[k] = on ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-      const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+      const uint4 w = on ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[j] << 16)), fabsf(__uint_as_float(x[j] & 0xFFFF0000u))));
@@ -284,9 +255,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     float down;
     fac = row_exponent(top, p.scale_log2, &down);
     uint8_t* dst = smem + (row >> 7) * L::kQTile;
-#pragma unroll
-    for (int k = 0; k < DH / 8; ++k) {
-      const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll 4
+    for (int k = 0; k < DH / 8; ++k) {  // (once more: the row is in L1)
+      const uint4 w = on ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
       uint32_t y[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -317,131 +289,104 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     return __all_sync(kFullMask, ok) != 0;
   };
 
-  if (warp >= kExpandWarp0 && warp < kTailWarp0) {
+  if (warp >= kExpandWarp0 && warp < kMmaWarp0) {
     // ------------------------------------------------- codes to fp16 tiles
-    // Lane (key = lane / 4, c = lane % 4) of a warp's 8 keys takes the dims
-    // [c DH/4, (c+1) DH/4): one load of codes, two (one) scales, DH/32 lines
-    // of 16 bytes.  The lanes of c >= 2 write theirs in another order: the
-    // eight lanes of a store's phase then lie in eight different 16-byte
-    // columns.  A tile's codes are loaded while the one before is expanded,
-    // its pages' numbers a tile earlier still.
-    constexpr int kIt = kKeys / (kExpandWarps * 8);
-    const int ew = warp - kExpandWarp0, kl = lane >> 2, c = lane & 3;
+    // Four warps take the keys, four the values; a warp's it-th group is 8
+    // tokens (of one page).  Lane (r = lane / 4, c = lane % 4) takes the dims
+    // [c DH/4, (c+1) DH/4) of one of the 8: one load of codes, two (one)
+    // scales, DH/32 lines of 16 bytes.  The lanes of c >= 2 take token r ^ 2
+    // instead of r: the eight lanes of a store's phase then lie in eight
+    // different 16-byte columns.  A group's codes are loaded when the same
+    // group of the tile before has been expanded, the pages' numbers (lane
+    // `it` has group it's) a tile earlier still.
+    constexpr int kSub = kExpandWarps / 2, kIt = kKeys / (8 * kSub);
+    const int ew = warp - kExpandWarp0, kv = ew / kSub, sub = ew % kSub;
+    const int c = lane & 3, kl = (lane >> 2) ^ (c & 2);
     const int P = 1 << p.c.log_page;
     const int32_t* trow = p.table + static_cast<size_t>(r) * p.max_pages;
-    const uint8_t* head = p.c.pool + static_cast<size_t>(hk) * p.c.chunk;
-    const int half = p.c.chunk >> 1;
+    const uint8_t* head = p.c.pool + static_cast<size_t>(hk) * p.c.chunk + kv * (p.c.chunk >> 1) + c * (DH / 8);
+    const uint8_t* head_sc = head - c * (DH / 8) + P * (DH / 2) + c * (DH / 64);
     using Codes = typename std::conditional<DH == 128, uint4, uint2>::type;
-    Codes code[2][kIt];
-    uint32_t scl[2][kIt];
-    int page[kIt];
-    bool flagged = false;
-    auto key_of = [&](int f, int it) { return (t_beg + f) * kKeys + (it * kExpandWarps + ew) * 8 + kl; };
+    Codes code[kIt];
+    uint32_t scl[kIt];
+    auto group = [&](int f, int it) { return (t_beg + f) * kKeys + (it * kSub + sub) * 8; };  // its first token
+    // lane it's page of tile f (not looked at before the next tile)
     auto look_up = [&](int f) {
-#pragma unroll
-      for (int it = 0; it < kIt; ++it) {
-        const int key = key_of(f, it), slot = key >> p.c.log_page;
-        page[it] = -1;
-        if (f < nt && key < sp.L) {
-          if (slot < p.max_pages) page[it] = trow[slot];
-          if (page[it] < 0 || page[it] >= p.c.pages) {
-            page[it] = -1;
-            if (!flagged) atomicOr(p.err, DT_ERR_BAD_INDEX);
-            flagged = true;
-          }
+      const int slot = group(f, lane) >> p.c.log_page;
+      return lane < kIt && f < nt && slot < p.max_pages ? trow[slot] : -1;
+    };
+    // the page, or -1; the bits of the group's tokens that are there
+    auto check = [&](int f, int raw, uint32_t* bits) {
+      const int left = sp.L - group(f, lane);
+      *bits = 0;
+      if (lane >= kIt || f >= nt || left <= 0) return -1;
+      if (raw < 0 || raw >= p.c.pages) {
+        atomicOr(p.err, DT_ERR_BAD_INDEX);
+        return -1;
+      }
+      *bits = left >= 8 ? 0xFFu : (1u << left) - 1u;
+      return raw;
+    };
+    auto load = [&](int f, int page_of_lane, int it) {
+      const int page = __shfl_sync(kFullMask, page_of_lane, it);
+      scl[it] = 0;
+      code[it] = Codes{};
+      const int key = group(f, it) + kl;
+      if (page >= 0 && key < sp.L) {
+        const size_t at = static_cast<size_t>(page) * p.c.page_bytes;
+        const int t = key & (P - 1);
+        if constexpr (DH == 128) {
+          code[it] = ld_once16(head + at + t * 64);
+          scl[it] = *reinterpret_cast<const uint16_t*>(head_sc + at + t * 8);
+        } else {
+          code[it] = ld_once8(head + at + t * 32);
+          scl[it] = head_sc[at + t * 4];
         }
       }
     };
-    auto fetch = [&](int f, int kv) {
+    uint32_t bits, next_bits;
+    int page = check(0, look_up(0), &bits);
 #pragma unroll
-      for (int it = 0; it < kIt; ++it) {
-        scl[kv][it] = 0;
-        code[kv][it] = Codes{};
-        if (page[it] >= 0) {
-          const int t = key_of(f, it) & (P - 1);
-          const uint8_t* chunk = head + static_cast<size_t>(page[it]) * p.c.page_bytes + kv * half;
-          if constexpr (DH == 128) {
-            code[kv][it] = ld_once16(chunk + t * 64 + c * 16);
-            scl[kv][it] = *reinterpret_cast<const uint16_t*>(chunk + P * 64 + t * 8 + c * 2);
-          } else {
-            code[kv][it] = ld_once8(chunk + t * 32 + c * 8);
-            scl[kv][it] = chunk[P * 32 + t * 4 + c];
-          }
-        }
-      }
-    };
-    uint8_t there[2];  // bits of the warp's groups of 8 keys: this tile's (lane it), the next one's
-    auto note = [&](int slot) {
-#pragma unroll
-      for (int it = 0; it < kIt; ++it) {
-        uint32_t x = __ballot_sync(kFullMask, page[it] >= 0) & 0x11111111u;  // (lane 4 k: key k)
-        x = (x | x >> 3) & 0x03030303u;
-        x = (x | x >> 6) & 0x000F000Fu;
-        x = (x | x >> 12) & 0xFFu;
-        if (lane == it) there[slot] = static_cast<uint8_t>(x);
-      }
-    };
-    look_up(0);
-    fetch(0, 0);
-    fetch(0, 1);
-    note(0);
-    look_up(1);
+    for (int it = 0; it < kIt; ++it) load(0, page, it);
+    int raw = look_up(1);
+    uint64_t* full = kv ? v_full : k_full;
+    uint64_t* empty = kv ? v_empty : k_empty;
     bool go = true;
-    for (int f = 0; f < nt && go; ++f) {
+#pragma unroll 1
+    for (int f = 0; f < nt; ++f) {
       const int st = f % kStages;
-      const uint32_t ph = static_cast<uint32_t>((f / kStages) & 1);
-      note(1);  // (of tile f + 1)
+      if (f >= kStages && !(go = wait_w(&empty[st], static_cast<uint32_t>((f / kStages) & 1) ^ 1u))) break;
+      if (kv == 0 && lane < kIt) s_valid[f % kValid][lane * kSub + sub] = static_cast<uint8_t>(bits);
+      page = check(f + 1, raw, &next_bits);
+      bits = next_bits;
+      raw = look_up(f + 2);
+      uint8_t* dst = sStage + (st * 2 + kv) * L::kTile + (DH == 128 ? (c >> 1) * (kKeys * 128) : 0);
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        if (f >= kStages && !wait_w(kv == 0 ? &k_empty[st] : &v_empty[st], ph ^ 1u)) {
-          go = false;
-          break;
+      for (int it = 0; it < kIt; ++it) {
+        const int key = (it * kSub + sub) * 8 + kl;
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&code[it]);
+        uint32_t sc[2];
+        if constexpr (DH == 128) {
+          const uint32_t s2 = e4m3x2_to_f16x2(scl[it]);
+          sc[0] = __byte_perm(s2, s2, 0x1010);
+          sc[1] = __byte_perm(s2, s2, 0x3232);
+        } else {
+          sc[0] = sc[1] = e4m3x2_to_f16x2(scl[it] | (scl[it] << 8));
         }
-        if (kv == 0 && lane < kIt) s_valid[f % kValid][lane * kExpandWarps + ew] = there[0];
-        uint8_t* dst = sStage + st * 2 * L::kTile + kv * L::kTile;
 #pragma unroll
-        for (int it = 0; it < kIt; ++it) {
-          const int key = (it * kExpandWarps + ew) * 8 + kl;
-          uint32_t w[DH / 32], sc[2];
-          const uint32_t* cw = reinterpret_cast<const uint32_t*>(&code[kv][it]);
-#pragma unroll
-          for (int i = 0; i < DH / 32; ++i) w[i] = cw[i];
-          if constexpr (DH == 128) {
-            const uint32_t s2 = e4m3x2_to_f16x2(scl[kv][it]);
-            sc[0] = __byte_perm(s2, s2, 0x1010);
-            sc[1] = __byte_perm(s2, s2, 0x3232);
-            if (c & 2) {  // the lines in the order 2, 3, 0, 1
-              uint32_t x = w[0];
-              w[0] = w[2];
-              w[2] = x;
-              x = w[1];
-              w[1] = w[3];
-              w[3] = x;
-              x = sc[0];
-              sc[0] = sc[1];
-              sc[1] = x;
-            }
-          } else {
-            sc[0] = sc[1] = e4m3x2_to_f16x2(scl[kv][it] | (scl[kv][it] << 8));
-          }
-          uint8_t* line = dst + (DH == 128 ? (c >> 1) * (kKeys * 128) : 0);
-#pragma unroll
-          for (int i = 0; i < DH / 32; ++i) {
-            const int gr = DH == 128 ? ((c & 1) << 2) + (i ^ (c & 2)) : (c << 1) + i;
-            uint32_t y[4];
-            e2m1x8_to_f16(w[i], y);
-            const uint32_t s2 = sc[DH == 128 ? i >> 1 : 0];
-            *reinterpret_cast<uint4*>(line + sw128(key, gr)) =
-                make_uint4(h2mul(y[0], s2), h2mul(y[1], s2), h2mul(y[2], s2), h2mul(y[3], s2));
-          }
+        for (int i = 0; i < DH / 32; ++i) {
+          const int gr = DH == 128 ? ((c & 1) << 2) + i : (c << 1) + i;
+          uint32_t y[4];
+          e2m1x8_to_f16(w[i], y);
+          const uint32_t s2 = sc[DH == 128 ? i >> 1 : 0];
+          *reinterpret_cast<uint4*>(dst + sw128(key, gr)) =
+              make_uint4(h2mul(y[0], s2), h2mul(y[1], s2), h2mul(y[2], s2), h2mul(y[3], s2));
         }
-        fetch(f + 1, kv);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(kv == 0 ? &k_full[st] : &v_full[st]);
+        load(f + 1, page, it);
       }
-      there[0] = there[1];
-      look_up(f + 2);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[st]);
     }
     if (!go && lane == 0) *abort_flag = 1;
   } else if (warp >= kMmaWarp0 && warp - kMmaWarp0 < two) {
@@ -455,26 +400,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     const uint32_t o_col = tmem_base + kColO + static_cast<uint32_t>(i * 128);
     const bool elected = elect_one();
     bool go = true;
-    for (int u = -2; u < steps; ++u) {  // (a step's scores two steps ahead of its products)
-      if (u >= 0) {  // O += P V of step u
-        const int f = u >> 1, st = f % kStages, b = u & 1;
-        if (!(go = wait_w(&p_full[2 * i + b], static_cast<uint32_t>(f) & 1u))) break;
-        if (b == 0 && !(go = wait_w(&v_full[st], static_cast<uint32_t>((f / kStages) & 1)))) break;
-        tc_fence_after();
-        if (elected) {
-          const uint64_t vd = v_desc + static_cast<uint64_t>(st * (2 * L::kTile >> 4) + b * (kStepKeys * 128 >> 4));
-          const uint32_t pa = s_col + static_cast<uint32_t>(b * kStepKeys);
-#pragma unroll
-          for (int kk = 0; kk < kStepKeys / 16; ++kk)  // 16 keys: two atoms of 8 lines
-            tc_mma_bf16_ta(o_col, pa + static_cast<uint32_t>(kk * 8), vd + static_cast<uint64_t>(kk * (2048 >> 4)),
-                           idesc_o, (u != 0 || kk != 0) ? 1u : 0u);
-          tc_commit(&o_full[2 * i + b]);
-          if (b == 1 || u == steps - 1) tc_commit(&v_empty[st]);
-        }
-        __syncwarp();
-      }
-      if (u + 2 < steps) {  // S of step u + 2, over P(u), which the product just issued has read
-        const int f = (u + 2) >> 1, st = f % kStages, b = u & 1;
+    for (int u = -1; u < steps; ++u) {
+      if (u + 1 < steps) {  // S of step u + 1, over P(u - 1) once its product has landed
+        const int f = (u + 1) >> 1, st = f % kStages, b = (u + 1) & 1;
+        if (u >= 1 && !(go = wait_w(&o_full[2 * i + b], static_cast<uint32_t>((u - 1) >> 1) & 1u))) break;
         if (b == 0 && !(go = wait_w(&k_full[st], static_cast<uint32_t>((f / kStages) & 1)))) break;
         tc_fence_after();
         if (elected) {
@@ -489,7 +418,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
             tc_mma_bf16(col, q_desc + off, kd + off, idesc_s, kk != 0 ? 1u : 0u);
           }
           tc_commit(&s_full[2 * i + b]);
-          if (b == 1 || u + 2 == steps - 1) tc_commit(&k_empty[st]);
+          if (b == 1 || u + 1 == steps - 1) tc_commit(&k_empty[st]);
+        }
+        __syncwarp();
+      }
+      if (u >= 0) {  // O += P V of step u
+        const int f = u >> 1, st = f % kStages, b = u & 1;
+        if (!(go = wait_w(&p_full[2 * i + b], static_cast<uint32_t>(f) & 1u))) break;
+        if (b == 0 && !(go = wait_w(&v_full[st], static_cast<uint32_t>((f / kStages) & 1)))) break;
+        tc_fence_after();
+        if (elected) {
+          const uint64_t vd = v_desc + static_cast<uint64_t>(st * (2 * L::kTile >> 4) + b * (kStepKeys * 128 >> 4));
+          const uint32_t pa = s_col + static_cast<uint32_t>(b * kStepKeys);
+#pragma unroll
+          for (int kk = 0; kk < kStepKeys / 16; ++kk)  // 16 keys: two atoms of 8 lines
+            tc_mma_bf16_ta(o_col, pa + static_cast<uint32_t>(kk * 8), vd + static_cast<uint64_t>(kk * (2048 >> 4)),
+                           idesc_o, (u != 0 || kk != 0) ? 1u : 0u);
+          tc_commit(&o_full[2 * i + b]);
+          if (b == 1 || u == steps - 1) tc_commit(&v_empty[st]);
         }
         __syncwarp();
       }
@@ -515,25 +461,47 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
       const int f = u >> 1, b = u & 1, key0 = t_beg * kKeys + u * kStepKeys;
       if (!(go = wait_w(&s_full[2 * i + b], static_cast<uint32_t>(f) & 1u))) break;
       tc_fence_after();
-      uint32_t x[kStepKeys];
-      tmem_ld64(s_addr + b * kStepKeys, x);
       const uint2 there = *reinterpret_cast<const uint2*>(&s_valid[f % kValid][b * (kStepKeys / 8)]);
-      tmem_wait_ld();
-      if (key0 + kStepKeys > sp.Lp || (there.x & there.y) != ~0u) {  // -inf where not seen
-        const uint32_t lo = row_sees(key0, sp.Lp, mrow, p.words) & there.x;
-        const uint32_t hi = row_sees(key0 + 32, sp.Lp, mrow, p.words) & there.y;
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          if (!((lo >> k) & 1u)) x[k] = 0xFF800000u;
-          if (!((hi >> k) & 1u)) x[32 + k] = 0xFF800000u;
-        }
+      uint32_t see[2] = {~0u, ~0u};
+      const bool masked = key0 + kStepKeys > sp.Lp || (there.x & there.y) != ~0u;
+      if (masked) {
+        see[0] = row_sees(key0, sp.Lp, mrow, p.words) & there.x;
+        see[1] = row_sees(key0 + 32, sp.Lp, mrow, p.words) & there.y;
       }
-      float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      // the weights with the reference as it is; where a score passes the
+      // limit the reference rises and they are computed once more
+      uint32_t pk[kStepKeys / 2];
+      float add;
+      for (int round = 0;; ++round) {
+        const float sub = m == -INFINITY ? 0.f : kBias - m;
+        const uint64_t fac2 = pack2(fac, fac), sub2 = pack2(sub, sub);
+        uint64_t sum[2] = {0ull, 0ull};
+        float t[2] = {-INFINITY, -INFINITY};
+        uint32_t x[kStepKeys];
+        tmem_ld64(s_addr + b * kStepKeys, x);
 #pragma unroll
-      for (int k = 0; k < kStepKeys; k += 2)
-        t[(k >> 1) & 3] = fmaxf(t[(k >> 1) & 3], fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
-      const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-      if (__any_sync(kFullMask, top > limit)) {
+        for (int ch = 0; ch < 2; ++ch) {
+          if (masked) {  // -inf where not seen
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (!((see[ch] >> k) & 1u)) x[32 * ch + k] = 0xFF800000u;
+          }
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            float a = __uint_as_float(x[32 * ch + k]), c = __uint_as_float(x[32 * ch + k + 1]);
+            t[(k >> 1) & 1] = fmaxf(t[(k >> 1) & 1], fmaxf(a, c));
+            unpack2(fma2(pack2(a, c), fac2, sub2), a, c);
+            a = ex2(a);
+            c = ex2(c);
+            sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, c));
+            pk[ch * 16 + k / 2] = pack_f16(a, c);
+          }
+        }
+        float a, c;
+        unpack2(add2(sum[0], sum[1]), a, c);
+        add = a + c;
+        const float top = fmaxf(t[0], t[1]);
+        if (round > 0 || !__any_sync(kFullMask, top > limit)) break;
         float alpha = 1.f;
         if (top > limit) {
           const float y = top * fac;
@@ -558,24 +526,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
           }
         }
       }
-      // the weights, over the columns their scores came from
-      const float sub = m == -INFINITY ? 0.f : kBias - m;
-      const uint64_t fac2 = pack2(fac, fac), sub2 = pack2(sub, sub);
-      uint64_t sum[2] = {0ull, 0ull};
-      uint32_t pk[kStepKeys / 2];
-#pragma unroll
-      for (int k = 0; k < kStepKeys; k += 2) {
-        float a, c;
-        unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), fac2, sub2), a, c);
-        a = ex2(a);
-        c = ex2(c);
-        sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, c));
-        pk[k / 2] = pack_f16(a, c);
-      }
+      if (!go) break;
+      l += add;
       tmem_st32(s_addr + b * kStepKeys, pk);
-      float a, c;
-      unpack2(add2(sum[0], sum[1]), a, c);
-      l += a + c;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -584,224 +537,48 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     if (!go && lane == 0) *abort_flag = 1;
     const bool have = go && steps > 0 && wait_w(&mma_done[i], 0);
     if (have) tc_fence_after();
-    else l = 0.f;
-    const bool on = row < rows;
+    if (!have || m == -INFINITY) l = 0.f;
     const float inv = l > 0.f ? p.c.v_scale / l : 0.f;
-    float* part = p.n_split > 1 && on ? cache_part_row(p, r, hk, mt, split, row) : nullptr;
-    uint4* out = p.n_split > 1 || !on ? nullptr : reinterpret_cast<uint4*>(p.O + cache_out_row(p, r, hk, q));
-    if (part) *reinterpret_cast<float2*>(part) = make_float2(m, l);
+    if (p.n_split > 1 && row < rows)
+      *reinterpret_cast<float2*>(cache_part_row(p, r, hk, mt, split, row)) = make_float2(m, l);
+    // O by way of the row tile's queries' place in shared memory (the scores
+    // are done), a quarter of the dims at a time, so that a warp's accesses
+    // are whole rows: kC dims of a row by kC / 4 lanes
+    constexpr int kC = DH / 4, kPitch = kC + 4, kLanes = kC / 4;
+    float* stage = reinterpret_cast<float*>(smem + i * L::kQTile) + (warp & 3) * 32 * kPitch;
+    static_assert(4 * 32 * kPitch * 4 <= L::kQTile, "the staged rows fit");
+#pragma unroll 1
+    for (int ch = 0; ch < 4; ++ch) {
 #pragma unroll
-    for (int ch = 0; ch < DH / 32; ++ch) {
-      uint32_t x[32];
-      if (have) {
-        tmem_ld32(o_addr + ch * 32, x);
-        tmem_wait_ld();
-      } else {
+      for (int h = 0; h < kC; h += 16) {
+        float x[16];
+        if (have) {
+          tmem_ld16(o_addr + ch * kC + h, x);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = 0u;
-      }
-      if (part) {
-#pragma unroll
-        for (int k = 0; k < 32; k += 2)
-          *reinterpret_cast<float2*>(part + 2 + ch * 32 + k) =
-              make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-      }
-      if (out) {
-#pragma unroll
-        for (int k = 0; k < 32; k += 8) {
-          uint32_t y[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            y[u] = pack_bf16(__uint_as_float(x[k + 2 * u]) * inv, __uint_as_float(x[k + 2 * u + 1]) * inv);
-          out[ch * 4 + k / 8] = make_uint4(y[0], y[1], y[2], y[3]);
+          for (int k = 0; k < 16; ++k) x[k] = 0.f;
         }
+#pragma unroll
+        for (int k = 0; k < 16; k += 4)
+          *reinterpret_cast<float4*>(stage + lane * kPitch + h + k) =
+              make_float4(p.n_split > 1 ? x[k] : x[k] * inv, p.n_split > 1 ? x[k + 1] : x[k + 1] * inv,
+                          p.n_split > 1 ? x[k + 2] : x[k + 2] * inv, p.n_split > 1 ? x[k + 3] : x[k + 3] * inv);
       }
-    }
-  } else if ((warp == kTailWarp0 || warp == kTailWarp0 + 1) && tail > 0) {
-    // ------------------------------------------------------------ tail rows
-    // S^T = K Q^T and O^T += V^T P^T by mma m16n8k16 with the tiles' keys as
-    // the 16-row operand (as the kernel of few rows does from the codes).  The
-    // loops run over independent sums inside.
-    const int rr = lane >> 2, c = lane & 3, tw = warp - kTailWarp0;
-    constexpr int kSteps = DH / 16, kGroups = kKeys / 32;  // 16-key groups of this warp
-    uint32_t qb[kSteps][2];
-    float tf[2];
-    int nd[2];
-    {
-      const bool on = rr < tail;
-      const int q = q0 + rows + (on ? rr : 0), n = q / p.g;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(
-          p.Q + (static_cast<size_t>(r) * (p.B + 1) + n) * p.q_stride +
-          static_cast<size_t>(hk * p.g + (q - n * p.g)) * DH);
-      float top = 0.f;
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          qb[s][h] = on ? __ldg(src + 8 * s + 4 * h + c) : 0u;  // dims 16 s + 8 h + 2 c, + 1
-          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qb[s][h] << 16)), fabsf(__uint_as_float(qb[s][h] & 0xFFFF0000u))));
-        }
-      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
-      float down;
-      const float f = row_exponent(top, p.scale_log2, &down);
-#pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          qb[s][h] = pack_f16(__uint_as_float(qb[s][h] << 16) * down, __uint_as_float(qb[s][h] & 0xFFFF0000u) * down);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        tf[x] = __shfl_sync(kFullMask, f, (2 * c + x) * 4);
-        nd[x] = __shfl_sync(kFullMask, n, (2 * c + x) * 4);
-      }
-    }
-    float o[kSteps][4];  // dims 16 s + rr, + 8 of rows 2 c, 2 c + 1
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) o[s][0] = o[s][1] = o[s][2] = o[s][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, limit[2] = {-INFINITY, -INFINITY};
-    const int lr = lane & 7, lm = lane >> 3;  // ldmatrix: row lr of matrix lm
-    bool go = true;
-    for (int j = 0; j < nt; ++j) {
-      const int st = j % kStages, key0 = (t_beg + j) * kKeys + tw * (kKeys / 2);
-      const uint32_t ph = static_cast<uint32_t>((j / kStages) & 1);
-      if (!(go = wait_w(&k_full[st], ph))) break;
-      const uint32_t k_addr = smem_u32(sStage + st * 2 * L::kTile), v_addr = k_addr + L::kTile;
-      const uint2 there = *reinterpret_cast<const uint2*>(&s_valid[j % kValid][tw * (kKeys / 16)]);
-      const bool plain = key0 + kKeys / 2 <= sp.Lp && (there.x & there.y) == ~0u;
-      float s[kGroups][4];
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) s[g][0] = s[g][1] = s[g][2] = s[g][3] = 0.f;
-#pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        const int gr = 2 * k + (lm >> 1);  // matrices: keys 0-7 | 8-15, dims 0-7; the same, dims 8-15
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          uint32_t a[4];
-          const int key = tw * (kKeys / 2) + 16 * g + lr + 8 * (lm & 1);
-          ldmatrix_x4(k_addr + (gr >> 3) * (kKeys * 128) + sw128(key, gr & 7), a);
-          mma_f16(s[g], a, qb[k][0], qb[k][1]);
+      __syncwarp();
+      for (int k = lane / kLanes; k < 32; k += 32 / kLanes) {
+        const int rr = (threadIdx.x & ~31) + k, d = ch * kC + (lane % kLanes) * 4;
+        if (rr >= rows) break;
+        const float4 v = *reinterpret_cast<const float4*>(stage + k * kPitch + (lane % kLanes) * 4);
+        if (p.n_split > 1) {
+          float* dst = cache_part_row(p, r, hk, mt, split, rr) + 2 + d;
+          *reinterpret_cast<float2*>(dst) = make_float2(v.x, v.y);
+          *reinterpret_cast<float2*>(dst + 2) = make_float2(v.z, v.w);
+        } else {
+          *reinterpret_cast<uint2*>(p.O + cache_out_row(p, r, hk, q0 + rr) + d) =
+              make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&k_empty[st]);
-      float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if (!plain) {
-            const int kk = 16 * g + 8 * (x >> 1) + rr, pos = key0 + kk;
-            bool seen = ((g < 2 ? there.x : there.y) >> (kk & 31)) & 1u;
-            if (seen && pos >= sp.Lp) {
-              const int t = pos - sp.Lp, n = nd[x & 1];
-              seen = n > 0 &&
-                     ((__ldg(p.mask + (static_cast<size_t>(r) * p.B + n - 1) * p.words + (t >> 5)) >> (t & 31)) & 1u);
-            }
-            if (!seen) s[g][x] = -INFINITY;
-          }
-          top[x & 1] = fmaxf(top[x & 1], s[g][x]);
-        }
-      if (__any_sync(kFullMask, top[0] > limit[0] || top[1] > limit[1])) {
-        float al[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float t = top[x];
-#pragma unroll
-          for (int d = 4; d < 32; d *= 2) t = fmaxf(t, __shfl_xor_sync(kFullMask, t, d));
-          al[x] = 1.f;
-          if (t > limit[x]) {
-            t *= tf[x];
-            al[x] = ex2(m[x] - t);
-            m[x] = t;
-            limit[x] = __fdividef(t + kRaise, tf[x]);
-            l[x] *= al[x];
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          o[k][0] *= al[0];
-          o[k][1] *= al[1];
-          o[k][2] *= al[0];
-          o[k][3] *= al[1];
-        }
-      }
-      const float sub0 = m[0] == -INFINITY ? 0.f : kBias - m[0], sub1 = m[1] == -INFINITY ? 0.f : kBias - m[1];
-      uint32_t pb[kGroups][2];
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const float p0 = ex2(fmaf(s[g][2 * t], tf[0], sub0)), p1 = ex2(fmaf(s[g][2 * t + 1], tf[1], sub1));
-          l[0] += p0;
-          l[1] += p1;
-          pb[g][t] = transpose8x8(pack_f16(p0, p1));
-        }
-      if (!(go = wait_w(&v_full[st], ph))) break;
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        const int key = tw * (kKeys / 2) + 16 * g + lr + 8 * (lm >> 1);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          uint32_t a[4];
-          const int gr = 2 * k + (lm & 1);  // matrices: dims 0-7 | 8-15, keys 0-7; the same, keys 8-15
-          ldmatrix_x4_trans(v_addr + (gr >> 3) * (kKeys * 128) + sw128(key, gr & 7), a);
-          mma_f16(o[k], a, pb[g][0], pb[g][1]);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&v_empty[st]);
-    }
-    if (!go && lane == 0) *abort_flag = 1;
-    // the second warp's rows to the first, which joins them
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-#pragma unroll
-      for (int d = 4; d < 32; d *= 2) l[x] += __shfl_xor_sync(kFullMask, l[x], d);
-      if (tw == 1) {
-        float* dst = s_tail[2 * c + x];
-        if (rr == 0) {
-          dst[DH] = m[x];
-          dst[DH + 1] = l[x];
-        }
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          dst[16 * k + rr] = o[k][x];
-          dst[16 * k + 8 + rr] = o[k][2 + x];
-        }
-      }
-    }
-    asm volatile("bar.sync 1, 64;" ::: "memory");
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int row = 2 * c + x;
-      if (tw == 1 || row >= tail) continue;
-      const float* other = s_tail[row];
-      const float M = fmaxf(m[x], other[DH]);
-      const float f0 = m[x] == -INFINITY ? 0.f : ex2(m[x] - M), f1 = other[DH] == -INFINITY ? 0.f : ex2(other[DH] - M);
-      const float Lr = l[x] * f0 + other[DH + 1] * f1;
-#pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        o[k][x] = o[k][x] * f0 + other[16 * k + rr] * f1;
-        o[k][2 + x] = o[k][2 + x] * f0 + other[16 * k + 8 + rr] * f1;
-      }
-      if (p.n_split > 1) {
-        float* dst = cache_part_row(p, r, hk, mt, split, rows + row);
-        if (rr == 0) *reinterpret_cast<float2*>(dst) = make_float2(M, Lr);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          dst[2 + 16 * k + rr] = o[k][x];
-          dst[2 + 16 * k + 8 + rr] = o[k][2 + x];
-        }
-      } else {
-        const float inv = Lr > 0.f ? p.c.v_scale / Lr : 0.f;
-        uint16_t* dst = p.O + cache_out_row(p, r, hk, q0 + rows + row);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          dst[16 * k + rr] = float_to_bf16_bits(o[k][x] * inv);
-          dst[16 * k + 8 + rr] = float_to_bf16_bits(o[k][2 + x] * inv);
-        }
-      }
     }
   }
   tc_fence_before();
