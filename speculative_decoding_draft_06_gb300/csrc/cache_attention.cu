@@ -602,7 +602,7 @@ struct Plan {
   size_t work;
 };
 
-Plan plan_rows(bool tree, long long rows, int R, int max_len, int Hkv, int dh, int most_splits) {
+Plan plan_rows(bool tree, long long rows, int R, int max_len, int Hkv, int dh, int most_splits, int sms) {
   Plan pl;
   pl.rows = static_cast<int>(rows);
   pl.tile_rows = tree ? kTreeRowsCta : rows > 8 ? 16 : 8;
@@ -613,7 +613,7 @@ Plan plan_rows(bool tree, long long rows, int R, int max_len, int Hkv, int dh, i
   pl.m_tiles = static_cast<int>((mine + pl.tile_rows - 1) / pl.tile_rows);
   const int tiles = max_len < 1 ? 1 : (max_len - 1) / pl.tile_keys + 1;
   const long long ctas = static_cast<long long>(R) * Hkv * pl.m_tiles;
-  long long n = tree ? 152 / ctas : (152 * 3 + ctas - 1) / ctas;
+  long long n = tree ? sms / ctas : (sms * 3 + ctas - 1) / ctas;
   if (!tree && n < (tiles + kSplitTiles - 1) / kSplitTiles) n = (tiles + kSplitTiles - 1) / kSplitTiles;
   const long long most = tree ? (tiles + 3) / 4 : (tiles + kWarps - 1) / kWarps;
   n = n < most ? n : most;
@@ -623,7 +623,7 @@ Plan plan_rows(bool tree, long long rows, int R, int max_len, int Hkv, int dh, i
   if (!tree) pl.split_tiles = (pl.split_tiles + kWarps - 1) / kWarps * kWarps;
   pl.n_split = (tiles + pl.split_tiles - 1) / pl.split_tiles;
   pl.cluster = !tree && pl.n_split > 1 && pl.n_split <= kMaxCluster &&
-               (ctas * pl.n_split <= 152 * 6 || most_splits == kMaxCluster);
+               (ctas * pl.n_split <= sms * 6 || most_splits == kMaxCluster);
   pl.work = pl.n_split > 1 && !pl.cluster
                 ? static_cast<size_t>(ctas) * pl.n_split * pl.tile_rows * (dh + 2) * sizeof(float)
                 : 0;
@@ -634,12 +634,18 @@ Plan plan_rows(bool tree, long long rows, int R, int max_len, int Hkv, int dh, i
 // only) the rows behind them, where a request may have some.
 int plan_of(int R, int B, int max_len, int Hq, int Hkv, int dh, Plan (&pl)[2]) {
   const long long rows = static_cast<long long>(B + 1) * (Hq / Hkv);
-  const bool tree = rows > kTreeRows;
-  pl[0] = plan_rows(tree, rows, R, max_len, Hkv, dh, 1 << 30);
-  if (!tree || rows <= kTreeTile) return 1;
-  // (up to a cluster: they run beside the others and need no launch more)
-  pl[1] = plan_rows(false, kTreeTail, R, max_len, Hkv, dh, kMaxCluster);
-  return 2;
+  const bool tree = rows > kTreeRows, left = tree && rows > kTreeTile;
+  int sms = 152;
+  if (left) {
+    // the rows left over: up to a cluster's splits (they run beside the others
+    // and need no launch more), three CTAs to an SM, which the splits of the
+    // others leave free
+    pl[1] = plan_rows(false, kTreeTail, R, max_len, Hkv, dh, kMaxCluster, sms);
+    const long long theirs = (static_cast<long long>(R) * Hkv * pl[1].n_split + 2) / 3;
+    sms -= static_cast<int>(theirs < 40 ? theirs : 40);
+  }
+  pl[0] = plan_rows(tree, rows, R, max_len, Hkv, dh, 1 << 30, sms);
+  return left ? 2 : 1;
 }
 
 }  // namespace

@@ -4,13 +4,15 @@
 //
 // A CTA owns up to 256 query rows of one request and one key/value head, as
 // two tiles of 128 (a TMEM lane each), and a share of the key range in tiles
-// of 128 keys.  Warp roles (576 threads):
-//   0-3, 4-7  softmax of the two row tiles: a thread owns a row;
-//   8-15      expand: codes and scales from memory to fp16 keys (8-11) and
-//             values (12-15) in shared memory (exact), a tile ahead in
-//             registers;
-//   16, 17    issue the MMAs of one row tile each (16 owns the TMEM): what
-//             waits on the issue all wait for, and two warps issue twice as fast.
+// of 128 keys.  Warp roles (832 threads):
+//   0-7, 8-15  softmax of the two row tiles: two threads share a row, each
+//              has half of a step's keys and of the head dimensions of O;
+//   16-23      expand: codes and scales from memory to fp16 keys (16-19) and
+//              values (20-23) in shared memory (exact), a tile ahead in
+//              registers;
+//   24, 25     issue the MMAs of one row tile each (24 owns the TMEM): what
+//              waits on the issue all wait for, and two warps issue twice as
+//              fast.
 // In steps of 64 keys: S = Q K^T (M 128, N 64, fp16, fp32 sums) into TMEM,
 // double-buffered per row tile, P = 2^(s - m + kBias) in fp16 over the S
 // columns it came from, O += P V with P from TMEM; S runs a step ahead of P.
@@ -30,13 +32,13 @@ namespace dt {
 namespace {
 
 constexpr int kMRows = 128, kKeys = 128, kStepKeys = 64;
-constexpr int kExpandWarp0 = 8, kExpandWarps = 8, kMmaWarp0 = 16;
-constexpr int kTreeThreads = 18 * 32;
+constexpr int kExpandWarp0 = 16, kExpandWarps = 8, kMmaWarp0 = 24;
+constexpr int kTreeThreads = 26 * 32;
 constexpr int kStages = 2;
 // (a tile's keys are expanded after all scores of the tile two before are
 // issued, and they after the weights of the tile three before are there)
 constexpr int kValid = 4;
-constexpr int kTreeSorted = 256;  // requests that are taken longest first (each CTA ranks them: R^2 / 576 steps)
+constexpr int kTreeSorted = 256;  // requests that are taken longest first (each CTA ranks them: R^2 / 832 steps)
 constexpr uint32_t kTmemCols = 512;  // S of row tile i, buffer b: 128 i + 64 b; O of row tile i: 256 + 128 i; P over S
 constexpr uint32_t kColO = 256;
 
@@ -101,26 +103,44 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t lead) 
   return d;
 }
 
-// 64 consecutive columns of the thread's lane (one statement with its wait: no
+// 32 consecutive columns of the thread's lane (one statement with its wait: no
 // use of a value can come before it).
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
         "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// A barrier of 64 threads that gives the OR of their predicates.
+__device__ __forceinline__ bool barrier_or(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.aligned.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
 }
 
 // Codes and scales are read once: past L1.
@@ -177,6 +197,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   uint64_t* mma_done = o_full + 4;       // [row tile]: everything issued has
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  __shared__ float s_fac[2 * kMRows], s_top[2][2 * kMRows];  // of the rows: factor; by half: maximum, sum
   __shared__ __align__(16) uint8_t s_valid[kValid][kKeys / 8];  // bit k of a tile: key k is there
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -224,7 +245,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
       const int n = min(rows - i * kMRows, kMRows);  // one arrival per warp with rows
       for (int b = 0; b < 2; ++b) {
         mbar_init(&s_full[2 * i + b], 1);
-        mbar_init(&p_full[2 * i + b], n > 0 ? (n + 31) / 32 : 1);
+        mbar_init(&p_full[2 * i + b], n > 0 ? 2 * ((n + 31) / 32) : 1);
         mbar_init(&o_full[2 * i + b], 1);
       }
       mbar_init(&mma_done[i], 1);
@@ -235,8 +256,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
       atomicOr(p.err, DT_ERR_BAD_INDEX);
   }
   // the queries, as fp16 rows scaled by a power of two to at most 2 each
-  float fac = 1.f;
-  if (threadIdx.x < 2 * kMRows && threadIdx.x < two * kMRows) {
+  if (threadIdx.x < two * kMRows) {
     const int row = threadIdx.x, q = q0 + row;
     const bool on = row < rows;
     const int node = on ? q / p.g : 0;
@@ -253,7 +273,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
         top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[j] << 16)), fabsf(__uint_as_float(x[j] & 0xFFFF0000u))));
     }
     float down;
-    fac = row_exponent(top, p.scale_log2, &down);
+    s_fac[row] = row_exponent(top, p.scale_log2, &down);
     uint8_t* dst = smem + (row >> 7) * L::kQTile;
 #pragma unroll 4
     for (int k = 0; k < DH / 8; ++k) {  // (once more: the row is in L1)
@@ -446,62 +466,73 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
       mbar_wait(&mma_done[i], 0, p.err);
     }
     __syncwarp();
-  } else if (warp < kExpandWarp0 && warp * 32 < rows) {
+  } else if (warp < kExpandWarp0 && (warp >> 3) * kMRows + (warp & 3) * 32 < rows) {
     // ------------------------------------------------------------- softmax
-    const int i = warp >> 2, row = threadIdx.x, q = q0 + row;
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int i = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+    const int row = i * kMRows + quarter * 32 + lane, q = q0 + row;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_addr = tmem_base + lane_base + static_cast<uint32_t>(i * kKeys);
-    const uint32_t o_addr = tmem_base + lane_base + kColO + static_cast<uint32_t>(i * 128);
+    const uint32_t o_addr = tmem_base + lane_base + kColO + static_cast<uint32_t>(i * 128 + half * (DH / 2));
+    const int pair = 1 + i * 4 + quarter;  // the barrier of the two warps that share rows
     const int node = row < rows ? q / p.g : 0;
     const uint32_t* mrow = node >= 1 ? p.mask + (static_cast<size_t>(r) * p.B + node - 1) * p.words : nullptr;
-    float m = -INFINITY, l = 0.f;
-    float limit = -INFINITY;  // the unscaled score above which the reference rises
-    bool go = true;
+    const float fac = s_fac[row];
+    float m = -INFINITY, l = 0.f;  // the row's reference (the same in both threads), this half's sum
+    float limit = -INFINITY;       // the unscaled score above which the reference rises
+    bool go = true;                // (the same in both warps after every barrier)
     for (int u = 0; u < steps; ++u) {
-      const int f = u >> 1, b = u & 1, key0 = t_beg * kKeys + u * kStepKeys;
-      if (!(go = wait_w(&s_full[2 * i + b], static_cast<uint32_t>(f) & 1u))) break;
+      const int f = u >> 1, b = u & 1, key0 = t_beg * kKeys + u * kStepKeys + half * (kStepKeys / 2);
+      go = wait_w(&s_full[2 * i + b], static_cast<uint32_t>(f) & 1u);
       tc_fence_after();
-      const uint2 there = *reinterpret_cast<const uint2*>(&s_valid[f % kValid][b * (kStepKeys / 8)]);
-      uint32_t see[2] = {~0u, ~0u};
-      const bool masked = key0 + kStepKeys > sp.Lp || (there.x & there.y) != ~0u;
-      if (masked) {
-        see[0] = row_sees(key0, sp.Lp, mrow, p.words) & there.x;
-        see[1] = row_sees(key0 + 32, sp.Lp, mrow, p.words) & there.y;
-      }
+      const uint32_t there = *reinterpret_cast<const uint32_t*>(&s_valid[f % kValid][(2 * b + half) * 4]);
+      uint32_t see = ~0u;
+      if (key0 + 32 > sp.Lp || there != ~0u) see = row_sees(key0, sp.Lp, mrow, p.words) & there;
       // the weights with the reference as it is; where a score passes the
       // limit the reference rises and they are computed once more
-      uint32_t pk[kStepKeys / 2];
-      float add;
+      uint32_t pk[16];
+      float add = 0.f;
       for (int round = 0;; ++round) {
-        const float sub = m == -INFINITY ? 0.f : kBias - m;
-        const uint64_t fac2 = pack2(fac, fac), sub2 = pack2(sub, sub);
-        uint64_t sum[2] = {0ull, 0ull};
-        float t[2] = {-INFINITY, -INFINITY};
-        uint32_t x[kStepKeys];
-        tmem_ld64(s_addr + b * kStepKeys, x);
-#pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
-          if (masked) {  // -inf where not seen
+        float top = -INFINITY;
+        if (go) {
+          uint32_t x[32];
+          tmem_ld32(s_addr + b * kStepKeys + half * 32, x);
+          if (__any_sync(kFullMask, see != ~0u)) {  // -inf where not seen
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              if (!((see[ch] >> k) & 1u)) x[32 * ch + k] = 0xFF800000u;
+              if (!((see >> k) & 1u)) x[k] = 0xFF800000u;
           }
+          const float sub = m == -INFINITY ? 0.f : kBias - m;
+          const uint64_t fac2 = pack2(fac, fac), sub2 = pack2(sub, sub);
+          uint64_t sum[2] = {0ull, 0ull};
+          float t[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
-            float a = __uint_as_float(x[32 * ch + k]), c = __uint_as_float(x[32 * ch + k + 1]);
+            float a = __uint_as_float(x[k]), c = __uint_as_float(x[k + 1]);
             t[(k >> 1) & 1] = fmaxf(t[(k >> 1) & 1], fmaxf(a, c));
             unpack2(fma2(pack2(a, c), fac2, sub2), a, c);
             a = ex2(a);
             c = ex2(c);
             sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pack2(a, c));
-            pk[ch * 16 + k / 2] = pack_f16(a, c);
+            pk[k / 2] = pack_f16(a, c);
           }
+          float a, c;
+          unpack2(add2(sum[0], sum[1]), a, c);
+          add = a + c;
+          top = fmaxf(t[0], t[1]);
         }
-        float a, c;
-        unpack2(add2(sum[0], sum[1]), a, c);
-        add = a + c;
-        const float top = fmaxf(t[0], t[1]);
-        if (round > 0 || !__any_sync(kFullMask, top > limit)) break;
+        // (every way on from here: both halves' scores are read, their columns
+        // may be written)
+        if (round > 0) {
+          barrier_or(pair, false);
+          break;
+        }
+        if (!barrier_or(pair, !go || top > limit)) break;
+        s_top[half][row] = top;
+        if (barrier_or(pair, !go)) {
+          go = false;
+          break;
+        }
+        top = fmaxf(s_top[0][row], s_top[1][row]);
         float alpha = 1.f;
         if (top > limit) {
           const float y = top * fac;
@@ -510,63 +541,71 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
           limit = __fdividef(y + kRaise, fac);
           l *= alpha;
         }
+        bool landed = true;
         if (u > 0) {
           // O holds the products of the steps before, once the last has landed
           // (the scores of this step came after the one of u - 2, and the
           // barrier of u - 1 is that of u - 3: its parity is certain)
-          if (!(go = wait_w(&o_full[2 * i + (b ^ 1)], static_cast<uint32_t>((u - 1) >> 1) & 1u))) break;
+          landed = wait_w(&o_full[2 * i + (b ^ 1)], static_cast<uint32_t>((u - 1) >> 1) & 1u);
           tc_fence_after();
+          if (landed) {
 #pragma unroll 1
-          for (int ch = 0; ch < DH / 16; ++ch) {
-            float y[16];
-            tmem_ld16(o_addr + ch * 16, y);
+            for (int ch = 0; ch < DH / 32; ++ch) {
+              float y[16];
+              tmem_ld16(o_addr + ch * 16, y);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) y[k] *= alpha;
-            tmem_st16(o_addr + ch * 16, y);
+              for (int k = 0; k < 16; ++k) y[k] *= alpha;
+              tmem_st16(o_addr + ch * 16, y);
+            }
           }
+        }
+        if (barrier_or(pair, !landed)) {  // (also: s_top may be written again)
+          go = false;
+          break;
         }
       }
       if (!go) break;
       l += add;
-      tmem_st32(s_addr + b * kStepKeys, pk);
+      tmem_st16(s_addr + b * kStepKeys + half * 16, reinterpret_cast<const float(&)[16]>(pk));
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[2 * i + b]);
     }
     if (!go && lane == 0) *abort_flag = 1;
+    s_top[half][row] = l;
+    barrier_or(pair, false);
+    l = s_top[0][row] + s_top[1][row];
     const bool have = go && steps > 0 && wait_w(&mma_done[i], 0);
     if (have) tc_fence_after();
     if (!have || m == -INFINITY) l = 0.f;
     const float inv = l > 0.f ? p.c.v_scale / l : 0.f;
-    if (p.n_split > 1 && row < rows)
+    if (half == 0 && p.n_split > 1 && row < rows)
       *reinterpret_cast<float2*>(cache_part_row(p, r, hk, mt, split, row)) = make_float2(m, l);
     // O by way of the row tile's queries' place in shared memory (the scores
-    // are done), a quarter of the dims at a time, so that a warp's accesses
-    // are whole rows: kC dims of a row by kC / 4 lanes
-    constexpr int kC = DH / 4, kPitch = kC + 4, kLanes = kC / 4;
-    float* stage = reinterpret_cast<float*>(smem + i * L::kQTile) + (warp & 3) * 32 * kPitch;
-    static_assert(4 * 32 * kPitch * 4 <= L::kQTile, "the staged rows fit");
+    // are done), an eighth of the dims at a time, so that a warp's accesses are
+    // whole pieces of rows: kC dims of a row by kC / 4 lanes
+    constexpr int kC = DH / 8, kPitch = kC + 4, kLanes = kC / 4;
+    float* stage = reinterpret_cast<float*>(smem + i * L::kQTile) + (warp & 7) * 32 * kPitch;
+    static_assert(8 * 32 * kPitch * 4 <= L::kQTile, "the staged rows fit");
+    const float mul = p.n_split > 1 ? 1.f : inv;
 #pragma unroll 1
     for (int ch = 0; ch < 4; ++ch) {
+      float x[kC];
+      if (have) {
+        if constexpr (kC == 16) tmem_ld16(o_addr + ch * kC, x);
+        else tmem_ld8(o_addr + ch * kC, x);
+      } else {
 #pragma unroll
-      for (int h = 0; h < kC; h += 16) {
-        float x[16];
-        if (have) {
-          tmem_ld16(o_addr + ch * kC + h, x);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) x[k] = 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < 16; k += 4)
-          *reinterpret_cast<float4*>(stage + lane * kPitch + h + k) =
-              make_float4(p.n_split > 1 ? x[k] : x[k] * inv, p.n_split > 1 ? x[k + 1] : x[k + 1] * inv,
-                          p.n_split > 1 ? x[k + 2] : x[k + 2] * inv, p.n_split > 1 ? x[k + 3] : x[k + 3] * inv);
+        for (int k = 0; k < kC; ++k) x[k] = 0.f;
       }
+#pragma unroll
+      for (int k = 0; k < kC; k += 4)
+        *reinterpret_cast<float4*>(stage + lane * kPitch + k) =
+            make_float4(x[k] * mul, x[k + 1] * mul, x[k + 2] * mul, x[k + 3] * mul);
       __syncwarp();
       for (int k = lane / kLanes; k < 32; k += 32 / kLanes) {
-        const int rr = (threadIdx.x & ~31) + k, d = ch * kC + (lane % kLanes) * 4;
+        const int rr = i * kMRows + quarter * 32 + k, d = half * (DH / 2) + ch * kC + (lane % kLanes) * 4;
         if (rr >= rows) break;
         const float4 v = *reinterpret_cast<const float4*>(stage + k * kPitch + (lane % kLanes) * 4);
         if (p.n_split > 1) {
