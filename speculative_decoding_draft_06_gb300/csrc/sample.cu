@@ -40,8 +40,10 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr float kBinsPer2 = 20.f;    // classes per power of two
-constexpr int kList = 3072;          // candidates
-constexpr float kWant = 2000.f;      // candidates aimed at
+constexpr float kMassUnit = 16000.f; // 2^18 2^(1/40) units fit 32 bits
+constexpr int kTable = 768;          // bf16 logits of a sign whose weights are tabled
+constexpr int kList = 2944;          // candidates
+constexpr float kWant = 1800.f;      // candidates aimed at
 constexpr int kClass = 1024;         // members of a class that are sorted
 constexpr int kUnits = 4096;         // 16-byte units of a CTA that may hold candidates
 constexpr int kMaxCl = 8;
@@ -102,8 +104,13 @@ struct Part {            // a CTA's share of the pass, for the leader
 
 struct Smem {
   float2 exp[1 << kExpBits];
-  unsigned mass_lo[kBins], mass_hi[kBins];
-  unsigned count[kBins];
+  union {
+    struct {
+      unsigned mass_lo[kBins], mass_hi[kBins];
+      unsigned count[kBins];
+    };
+    unsigned long long weight[2 * kTable];
+  };
   unsigned long long list[kList];
   union {
     unsigned long long cls[kClass];
@@ -114,8 +121,8 @@ struct Smem {
   unsigned scan_c[kWarps];
   float wmax[kWarps], wval[kWarps];
   __align__(16) float sample[kThreads];
-  float2 bounds[kMaxCl];
-  float sbound, smax;
+  float4 bounds[kMaxCl];
+  float sbound, sbound2, smax;
   Part part[kMaxCl];
   unsigned list_n, units_n, cls_n;
   int picked;
@@ -236,7 +243,6 @@ __device__ __forceinline__ unsigned long long ceil_share(float p, unsigned long 
   return c > 0ull ? c : 1ull;
 }
 
-
 // A row in 16-byte units: `head` logits before the first aligned address,
 // `units` units, the rest behind them.  Warp w of the cluster's n has the
 // units [w share, (w + 1) share), warp 0 the head too and warp n - 1 the
@@ -293,6 +299,21 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// f(unit, its number) for the lane's units of a warp's [ub, ue), with a load
+// in flight ahead (three: 4% to 7% slower by their moves).
+template <typename E, typename F>
+__device__ __forceinline__ void each_unit(const Row<E>& row, int ub, int ue, F f) {
+  int u = ub + (threadIdx.x & 31);
+  auto at = [&](int q) { return q < ue ? row.load(q) : make_uint4(0, 0, 0, 0); };
+  uint4 next = at(u);
+#pragma unroll 1
+  for (; u < ue; u += 32) {
+    const uint4 v = next;
+    next = at(u + 32);
+    f(v, u);
+  }
+}
+
 // What the cuts work on.  LIST: the leader's list of candidates, by the
 // leader's block alone; otherwise the whole row, by the cluster.
 template <bool LIST, typename E>
@@ -321,16 +342,12 @@ struct Source {
     if (first && lane < row.head) one(logit<E>(row.src, lane), lane);
     const int rest = row.index(row.units);
     if (last && lane < row.V - rest) one(logit<E>(row.src, rest + lane), rest + lane);
-    uint4 next = ub + lane < ue ? row.load(ub + lane) : make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-    for (int u = ub + lane; u < ue; u += 32) {
-      const uint4 v = next;
-      if (u + 32 < ue) next = row.load(u + 32);
+    each_unit(row, ub, ue, [&](uint4 v, int u) {
       float x[Row<E>::kPer];
       unpack<E>(v, x);
 #pragma unroll
       for (int k = 0; k < Row<E>::kPer; ++k) one(x[k], row.index(u) + k);
-    }
+    });
   }
   template <typename F>
   __device__ __forceinline__ void each(F f) const {  // f(logit, key)
@@ -414,17 +431,21 @@ __device__ __forceinline__ int pick_class(const S& s, bool by_count, unsigned lo
   return k;
 }
 
-// The classes of the cuts: -log2 w in steps of 1 / kBinsPer2.
-__device__ __forceinline__ int bin_of(const Weights& wt, float x) {
-  return min(kBins - 1, static_cast<int>(wt.log2w(x) * -kBinsPer2));
+// The classes of the cuts: -log2 w in steps of 1 / kBinsPer2, to the nearest
+// (by adding 1.5 2^23, whose ulp is 1).
+__device__ __forceinline__ int bin_of_log2(float y) {
+  constexpr float kBig = 12582912.f;
+  return min(kBins - 1, __float_as_int(fmaf(y, -kBinsPer2, kBig)) - __float_as_int(kBig));
 }
+__device__ __forceinline__ int bin_of(const Weights& wt, float x) { return bin_of_log2(wt.log2w(x)); }
 
 // The element at which the running count (by_count) or mass in the order
 // reaches `target`: its key becomes `keep`; the mass up to and with it is
 // left in the leader's *upto.  The bins' sums are in place.  All threads of
-// the source call it.
+// the source call it.  Returns whether the bins' sums were used for digits
+// (else those before the cut's bin still hold).
 template <typename S>
-__device__ void cut(const S& s, const Weights& wt, bool by_count, unsigned long long target,
+__device__ bool cut(const S& s, const Weights& wt, bool by_count, unsigned long long target,
                     unsigned long long& keep, unsigned long long* upto) {
   Smem& sm = s.sm;
   Ctl& ctl = s.ls.ctl;
@@ -440,7 +461,9 @@ __device__ void cut(const S& s, const Weights& wt, bool by_count, unsigned long 
   }
   s.sync();
   // a class too large to be gathered: by digits of its keys, 10 bits each
+  bool refined = false;
   for (int shift = 40; ctl.refine; shift -= 10) {
+    refined = true;
     const int bin = ctl.bin;
     const unsigned long long pre = ctl.prefix, msk = ctl.mask;
     clear_classes(sm);
@@ -511,6 +534,7 @@ __device__ void cut(const S& s, const Weights& wt, bool by_count, unsigned long 
   }
   s.sync();
   keep = ctl.keep;
+  return refined;
 }
 
 // A request's settings for a row.
@@ -585,14 +609,66 @@ __device__ void all_classes(const S& s, unsigned* count, unsigned long long* mas
   __syncthreads();
 }
 
+// f(logit, index, weight) for the row's logits above -inf, in no particular
+// order; the classes' memory is used.  bf16 logits near the largest are few
+// different values: the weights of kTable codes downward from it, and of
+// kTable negative ones from -1/4 (or from it, if that is negative), come from
+// a table (weight44 is some 70 instructions: 2064 rows of 151936 without cuts
+// take 610 us, 1050 without the table).
+template <typename S, typename F>
+__device__ __forceinline__ void each_weight(const S& s, const Weights& wt, F f) {
+  using E = typename S::Elem;
+  if constexpr (sizeof(E) == 4) {
+    s.each_value([&](float x, int i) { f(x, i, wt.weight44(x)); });
+  } else {
+    const int top = __float_as_int(wt.top) >> 16, neg0 = max(0x3E80, top < 0 ? top & 0x7FFF : 0);
+    for (int j = threadIdx.x; j < 2 * kTable; j += kThreads) {
+      const int code = j < kTable ? max(top - j, 0) : (neg0 + j - kTable) | 0x8000;
+      const float x = bf16_bits_to_float(static_cast<uint16_t>(code));
+      s.sm.weight[j] = x > -INFINITY ? wt.weight44(x) : 0ull;
+    }
+    __syncthreads();
+    // the table's entry or -1
+    auto entry = [&](float x) {
+      const int b = __float_as_int(x) >> 16;
+      const int j = b < 0 ? (b & 0x7FFF) - neg0 : top - b;
+      return static_cast<unsigned>(j) < kTable ? j + (b < 0 ? kTable : 0) : -1;
+    };
+    constexpr int kPer = Row<E>::kPer;
+    const int lane = threadIdx.x & 31;
+    auto one = [&](float x, int i) {
+      if (x > -INFINITY) f(x, i, wt.weight44(x));
+    };
+    if (s.first && lane < s.row.head) one(logit<E>(s.row.src, lane), lane);
+    const int rest = s.row.index(s.row.units);
+    if (s.last && lane < s.row.V - rest) one(logit<E>(s.row.src, rest + lane), rest + lane);
+    each_unit(s.row, s.ub, s.ue, [&](uint4 v, int u) {
+      float x[kPer];
+      unpack<E>(v, x);
+      unsigned others = 0;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int j = entry(x[k]);
+        if (j >= 0) f(x[k], s.row.index(u) + k, s.sm.weight[j]);
+        else if (x[k] > -INFINITY) others |= 1u << k;
+      }
+      for (; others; others &= others - 1) {
+        const int k = __ffs(others) - 1;
+        const uint32_t pair = k < 4 ? (k < 2 ? v.x : v.y) : (k < 6 ? v.z : v.w);
+        one(__uint_as_float(k & 1 ? pair & 0xFFFF0000u : pair << 16), s.row.index(u) + k);
+      }
+    });
+  }
+}
+
 // The kept tokens' mass per warp, left in the leader's wsum.
 template <typename S>
 __device__ void whole_sums(const S& s, const Weights& wt, unsigned long long keep) {
   unsigned long long sum = 0;
   const float kx = key50_value(keep);
   const bool any = keep == 0;
-  s.each([&](float x, unsigned long long key) {
-    if (any || (x >= kx && key >= keep)) sum += wt.weight44(x);
+  each_weight(s, wt, [&](float x, int i, unsigned long long w) {
+    if (any || (x >= kx && key50(x, i) >= keep)) sum += w;
   });
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
@@ -600,10 +676,10 @@ __device__ void whole_sums(const S& s, const Weights& wt, unsigned long long kee
 }
 
 // top-p alone, or no cut: one exact pass over the row.
-// A histogram of approximate class masses (a count, and in units of 2^-18 how
-// far the class's weights lie below its largest possible one: two 32-bit
-// sums) tells the classes [c1, c2] in which the running mass passes top_p of
-// the whole, with room for the masses' error.  The exact pass then sums all
+// A histogram of approximate class masses (in units of kMassUnit of the
+// class's middle weight, one 32-bit sum: 2^18 tokens fit) tells the classes
+// [c1, c2] in which the running mass passes top_p of the whole, with room for
+// the masses' error.  The exact pass then sums all
 // weights and those of the classes before c1, and gathers the tokens of c1 ..
 // c2, among which the cut falls.  False if it does not, or if they are too
 // many; else the kept tokens' mass per warp is in wsum.
@@ -623,22 +699,22 @@ __device__ bool nucleus(const S& s, const Weights& wt, const Rule& rule, unsigne
   s.each_value([&](float x, int) {
     const float y = wt.log2w(x);
     if (!(y >= kZeroBelow)) return;
-    const int b = min(kBins - 1, static_cast<int>(y * -kBinsPer2));
-    const float w = ex2(fmaf(static_cast<float>(b), 1.f / kBinsPer2, y));  // 2^(-1/20) .. 1
-    atomicAdd(&sm.count[b], 1u);
-    atomicAdd(&sm.mass_lo[b], static_cast<unsigned>(fmaxf((1.f - w) * 262144.f, 0.f)));
+    const int b = bin_of_log2(y);
+    const float w = ex2(fmaf(static_cast<float>(b), 1.f / kBinsPer2, y));  // 2^(-1/40) .. 2^(1/40)
+    atomicAdd(&sm.mass_lo[b], static_cast<unsigned>(fmaf(w, kMassUnit, 0.5f)));
   });
   s.sync();
   if (s.lead) {
     constexpr int kPer = kBins / kThreads;
     float ms[kPer], m = 0.f;
-    unsigned cs[kPer];
+    float cs[kPer];  // tokens, about
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      unsigned long long low;
-      s.sums(tid * kPer + j, &cs[j], &low);
-      const float d = static_cast<float>(static_cast<double>(low) * (1.0 / 262144.0));
-      ms[j] = (static_cast<float>(cs[j]) - d) * ex2(static_cast<float>(tid * kPer + j) * (-1.f / kBinsPer2));
+      unsigned none;
+      unsigned long long units;
+      s.sums(tid * kPer + j, &none, &units);
+      cs[j] = static_cast<float>(units) * (1.f / kMassUnit);
+      ms[j] = cs[j] * ex2(static_cast<float>(tid * kPer + j) * (-1.f / kBinsPer2));
       m += ms[j];
     }
     float inc = m;
@@ -658,14 +734,15 @@ __device__ bool nucleus(const S& s, const Weights& wt, const Rule& rule, unsigne
       if (w < (tid >> 5)) before += sm.wval[w];
       all += sm.wval[w];
     }
-    // (the fp32 sums and the classes' masses are good to 2^-15 of the whole)
+    // (a token's mass is rounded by 2^-15 of itself, the fp32 sums add 2^-18 of
+    // the whole)
     const float t1 = fmaxf(rule.tp, 0.f) * all - all * (1.f / 16384.f), t2 = t1 + all * (2.f / 16384.f);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int c = tid * kPer + j;
       const float after = before + ms[j];
-      if (cs[j] > 0 && after >= t1) atomicMin(&ctl.bin, c);
-      if (cs[j] > 0 && after >= t2) atomicMin(&ctl.last, c);
+      if (cs[j] > 0.f && after >= t1) atomicMin(&ctl.bin, c);
+      if (cs[j] > 0.f && after >= t2) atomicMin(&ctl.last, c);
       before = after;
     }
     __syncthreads();
@@ -673,7 +750,7 @@ __device__ bool nucleus(const S& s, const Weights& wt, const Rule& rule, unsigne
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int c = tid * kPer + j;
-      if (c >= ctl.bin && c <= ctl.last) members += cs[j];
+      if (c >= ctl.bin && c <= ctl.last) members += static_cast<unsigned>(cs[j]);
     }
     atomicAdd(&sm.list_n, members);
     __syncthreads();
@@ -686,9 +763,8 @@ __device__ bool nucleus(const S& s, const Weights& wt, const Rule& rule, unsigne
   if (ctl.refine) return false;
   const int c1 = ctl.bin, c2 = ctl.last;
   unsigned long long above = 0, total = 0;
-  s.each_value([&](float x, int i) {
+  each_weight(s, wt, [&](float x, int i, unsigned long long w) {
     const int b = bin_of(wt, x);
-    const unsigned long long w = wt.weight44(x);
     total += w;
     if (b < c1) above += w;
     else if (b <= c2 && w != 0) {
@@ -751,6 +827,60 @@ __device__ bool nucleus(const S& s, const Weights& wt, const Rule& rule, unsigne
   return ctl.refine == 0;
 }
 
+template <typename E>
+__device__ bool from_list(const SampleParams& p, Smem& sm, int row, int n, unsigned long long bound_key,
+                          unsigned long long tail, unsigned long long tail_err, const Weights& wt, const Rule& rule);
+
+// top-k that the candidates did not decide (too many or fewer than k): a
+// histogram of counts gives the class in which the k-th falls, and the tokens
+// up to that class are the candidates.  False where they do not fit the list.
+template <typename S>
+__device__ bool k_list(const S& s, const SampleParams& p, int row, const Weights& wt, const Rule& rule) {
+  Smem& sm = s.sm;
+  Ctl& ctl = s.ls.ctl;
+  clear_classes(sm);
+  if (s.lead && threadIdx.x == 0) sm.list_n = 0;
+  __syncthreads();
+  s.each_value([&](float x, int) { atomicAdd(&sm.count[bin_of(wt, x)], 1u); });
+  s.sync();
+  if (s.lead) {
+    unsigned total, c = 0, members = 0;
+    unsigned long long none = 0;
+    all_classes(s, &total, &none);
+    const unsigned k = static_cast<unsigned>(rule.k);
+    const int b = total > k ? pick_class(s, true, k, c, none, &members) : kBins;
+    if (threadIdx.x == 0) {
+      ctl.bin = b;
+      ctl.refine = (total > k ? c + members : total) > kList;
+    }
+  }
+  s.sync();
+  if (ctl.refine) return false;
+  const int b = ctl.bin;
+  s.each_value([&](float x, int i) {
+    if (bin_of(wt, x) <= b) s.ls.list[atomicAdd(&s.ls.list_n, 1u)] = key50(x, i);
+  });
+  s.sync();
+  if (s.lead) {
+    const int n = static_cast<int>(sm.list_n);
+    unsigned long long least = ~0ull;
+    for (int i = threadIdx.x; i < n; i += kThreads) least = min(least, sm.list[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(kFullMask, least, o));
+    if ((threadIdx.x & 31) == 0) sm.scan_m[threadIdx.x >> 5] = least;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) least = min(least, sm.scan_m[w]);
+    __syncthreads();
+    const bool ok = from_list<typename S::Elem>(p, sm, row, n, least, 0, 0, wt, rule);
+    if (threadIdx.x == 0) {
+      ctl.refine = ok ? 0 : 1;
+      sm.cls_n = 0;
+    }
+  }
+  s.sync();
+  return ctl.refine == 0;
+}
+
 // The whole row, every decision on integer sums over it.
 template <typename E>
 __device__ void whole_row(const SampleParams& p, Smem& sm, Smem& ls, const E* src, int row, int cl, int rank,
@@ -775,6 +905,7 @@ __device__ void whole_row(const SampleParams& p, Smem& sm, Smem& ls, const E* sr
     }
     return;
   }
+  if (rule.use_k && k_list(s, p, row, wt, rule)) return;
   unsigned long long keep = 0;
   const bool quick = !rule.use_k && !(rule.mp > 0.f) && nucleus(s, wt, rule, keep);
   if (!quick) {
@@ -788,10 +919,10 @@ __device__ void whole_row(const SampleParams& p, Smem& sm, Smem& ls, const E* sr
         if (tid == 0) ls.ctl.warp = rule.use_k && count > static_cast<unsigned>(rule.k);
       }
       cluster_sync();
-      if (ls.ctl.warp) cut(s, wt, true, static_cast<unsigned long long>(rule.k), keep, &Z);
+      const bool refined = ls.ctl.warp && cut(s, wt, true, static_cast<unsigned long long>(rule.k), keep, &Z);
       if (rule.use_p) {
         unsigned long long upto;
-        if (ls.ctl.warp) fill_bins(s, wt, keep);  // (the digits' passes used the classes)
+        if (refined) fill_bins(s, wt, keep);
         cut(s, wt, false, rule.tp > 0.f && s.lead ? ceil_share(rule.tp, Z) : 1ull, keep, &upto);
       }
     }
@@ -876,12 +1007,14 @@ __device__ bool from_list(const SampleParams& p, Smem& sm, int row, int n, unsig
   const int tid = threadIdx.x;
   const Source<true, E> s{sm, sm, Row<E>(nullptr, 0), 0, 0, 0, 0, n, 1, true, 0, 1};
   unsigned long long keep = bound_key;
-  bool all = false;  // nothing below `keep` is kept
+  bool all = key50_value(bound_key) == -INFINITY;  // nothing below `keep` is kept (the list has every token)
   if (rule.mp > 0.f) {
     const unsigned long long mk = min_p_key(wt, rule.mp);
     if (mk >= bound_key) {
       keep = mk;
       all = true;
+    } else if (all) {
+      keep = mk;
     }
   }
   fill_bins(s, wt, keep);
@@ -890,8 +1023,7 @@ __device__ bool from_list(const SampleParams& p, Smem& sm, int row, int n, unsig
   all_classes(s, &count, &Z);
   if (rule.use_k && count >= static_cast<unsigned>(rule.k)) {
     if (count > static_cast<unsigned>(rule.k)) {
-      cut(s, wt, true, static_cast<unsigned long long>(rule.k), keep, &Z);
-      if (rule.use_p) fill_bins(s, wt, keep);
+      if (cut(s, wt, true, static_cast<unsigned long long>(rule.k), keep, &Z) && rule.use_p) fill_bins(s, wt, keep);
     }
     all = true;
   }
@@ -939,6 +1071,16 @@ __device__ bool from_list(const SampleParams& p, Smem& sm, int row, int n, unsig
   return true;
 }
 
+// How long a request's rows take, roughly: 2 all weights exactly, 1 all
+// weights, 0 the candidates'.
+__device__ __forceinline__ int request_cost(const SampleParams& p, int req) {
+  const float T = p.temperature ? p.temperature[req] : 1.f, tp = p.top_p ? p.top_p[req] : 1.f;
+  const int k = p.top_k ? p.top_k[req] : 0;
+  if (!(T > 0.f) || (k >= 1 && k < p.V)) return 0;
+  if (p.min_p && p.min_p[req] > 0.f) return 0;
+  return tp < 1.f && T < 0.9f ? 1 : 2;
+}
+
 template <typename E>
 __global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
   constexpr int kPer = Row<E>::kPer;
@@ -951,7 +1093,32 @@ __global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // (waited on before the first access to another CTA's memory)
   if (cl > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  const int row = blockIdx.x / cl, req = row / p.rows_per_req;
+  // requests that need their whole rows' weights first: their rows take several
+  // times as long as the others', which then fill the SMs (2064 rows of 151936
+  // in 129 requests of all kinds: an eighth to a third less time than in the rows' order)
+  int row = blockIdx.x / cl;
+  const int requests = p.rows / p.rows_per_req;
+  if (requests > 1 && requests <= kBins && requests * p.rows_per_req == p.rows) {
+    for (int a = tid; a < requests; a += kThreads) sm.count[a] = request_cost(p, a);
+    __syncthreads();
+    if (warp == 0) {
+      auto with = [&](int b, unsigned cost) {
+        return __ballot_sync(kFullMask, b + lane < requests && sm.count[b + lane] == cost);
+      };
+      int place = row / p.rows_per_req;
+      for (int cost = 2; cost >= 0; --cost) {
+        for (int b = 0; b < requests; b += 32) {
+          const unsigned in = with(b, cost);
+          if (place >= 0 && place < __popc(in) && (in >> lane & 1) && __popc(in & ((1u << lane) - 1)) == place)
+            sm.picked = b + lane;
+          place -= __popc(in);
+        }
+      }
+    }
+    __syncthreads();
+    row = sm.picked * p.rows_per_req + row % p.rows_per_req;
+  }
+  const int req = row / p.rows_per_req;
   const E* src = static_cast<const E*>(p.logits) + static_cast<size_t>(row) * p.row_stride;
   const bool lead = rank == 0;
   Smem& ls = *at_rank(&sm, 0);  // the leader's
@@ -972,7 +1139,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
 
   // (with no cut every token is in the draw, and the row's sums are needed)
   bool listed = greedy || rule.use_k || rule.use_p || rule.mp > 0.f;
-  float bound = -INFINITY, off = 0.f;
+  float bound = -INFINITY, bound2 = -INFINITY, off = 0.f;
   for (int i = tid; i < (1 << kExpBits); i += kThreads) sm.exp[i] = make_float2(g_exp.hi[i], g_exp.lo[i]);
   if (tid == 0) {
     sm.list_n = 0;
@@ -994,7 +1161,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
     }
     sm.sample[tid] = m;
     __syncthreads();
-    const float want = rule.use_k ? fminf(fmaxf(1.6f * rule.k + 300.f, 0.5f * kWant), kWant) : kWant;
+    const float want = rule.use_k ? fminf(fmaxf(2.f * rule.k, 0.5f * kWant), 1.2f * kWant) : kWant;
     const float share_out = fminf(want / static_cast<float>(p.V), 1.f);
     const int r = greedy ? 1 : max(1, static_cast<int>(kThreads * (1.f - __powf(1.f - share_out, kPer)) + 0.5f));
     int above = 0, equal = 0;
@@ -1005,20 +1172,25 @@ __global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
     }
     if (above == 0) sm.smax = m;                          // (all that write write the same)
     if (above < r && r <= above + equal) sm.sbound = m;
+    const int r2 = rule.use_k ? (2 * r + 2) / 3 : (r + 1) / 2;  // (should the list overflow)
+    if (above < r2 && r2 <= above + equal) sm.sbound2 = m;
     __syncthreads();
-    float lo = sm.sbound, hi = sm.smax;
+    float lo = sm.sbound, lo2 = sm.sbound2, hi = sm.smax;
     if (cl > 1) {
       asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-      if (tid < cl) at_rank(&sm, tid)->bounds[rank] = make_float2(lo, hi);
+      if (tid < cl) at_rank(&sm, tid)->bounds[rank] = make_float4(lo, lo2, hi, 0.f);
       cluster_sync();
-      float mean = 0.f;
+      lo = lo2 = 0.f;
       for (int q = 0; q < cl; ++q) {
-        mean += sm.bounds[q].x;
-        hi = fmaxf(hi, sm.bounds[q].y);
+        lo += sm.bounds[q].x;
+        lo2 += sm.bounds[q].y;
+        hi = fmaxf(hi, sm.bounds[q].z);
       }
-      lo = mean / static_cast<float>(cl);                 // (-inf where one of them is)
+      lo /= static_cast<float>(cl);                       // (-inf where one of them is)
+      lo2 /= static_cast<float>(cl);
     }
     bound = greedy ? hi : lo;
+    bound2 = greedy ? hi : lo2;
     off = hi * ch;  // the reference of the sums: the sample's largest logit
     if (!isfinite(off)) off = 0.f;
   } else if (cl > 1) {
@@ -1058,13 +1230,21 @@ __global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
       return w;
     };
     int u = ub + lane;
-    for (; u + 32 * (kAhead - 1) < ue; u += 32 * kAhead) {
-      uint4 v[kAhead];
+    uint4 v[kAhead];
+    auto full = [&](int at) { return at + 32 * (kAhead - 1) < ue; };
+    if (full(u)) {
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) v[a] = rw.load(u + 32 * a);
+    }
+    for (; full(u); u += 32 * kAhead) {
       float w = 0.f;
+      const bool more = full(u + 32 * kAhead);
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) w += take(v[a], u + 32 * a);
+      for (int a = 0; a < kAhead; ++a) {
+        const uint4 now = v[a];
+        if (more) v[a] = rw.load(u + 32 * (kAhead + a));
+        w += take(now, u + 32 * a);
+      }
       sum += w;
     }
     for (; u < ue; u += 32) sum += take(rw.load(u), u);
@@ -1085,41 +1265,53 @@ __global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
       sum += ex2(fmaf(x, ch, -off));
     }
   };
-  if (listed) {
-    const int n = min(static_cast<int>(sm.units_n), kUnits);
-    for (int i = tid; i < n; i += kThreads) {
-      const int un = sm.unit[i];
-      float x[kPer];
-      unpack<E>(rw.load(un), x);
+  const float rest_sum = sum;
+  for (;;) {
+    if (listed) {
+      const int n = min(static_cast<int>(sm.units_n), kUnits);
+      for (int i = tid; i < n; i += kThreads) {
+        const int un = sm.unit[i];
+        float x[kPer];
+        unpack<E>(rw.load(un), x);
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) token(x[k], rw.index(un) + k);
+        for (int k = 0; k < kPer; ++k) token(x[k], rw.index(un) + k);
+      }
     }
-  }
-  if (lead) {
-    const int rest = rw.index(rw.units);
-    if (tid < rw.head) token(logit<E>(src, tid), tid);
-    if (tid < p.V - rest) token(logit<E>(src, rest + tid), rest + tid);
-  }
+    if (lead) {
+      const int rest = rw.index(rw.units);
+      if (tid < rw.head) token(logit<E>(src, tid), tid);
+      if (tid < p.V - rest) token(logit<E>(src, rest + tid), rest + tid);
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
-    sum += __shfl_xor_sync(kFullMask, sum, o);
-  }
-  if (lane == 0) {
-    sm.wmax[warp] = top;
-    sm.wval[warp] = sum;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    float t = sm.wmax[0], w = sm.wval[0];
-    for (int k = 1; k < kWarps; ++k) {
-      t = fmaxf(t, sm.wmax[k]);
-      w += sm.wval[k];
+    for (int o = 16; o > 0; o >>= 1) {
+      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+      sum += __shfl_xor_sync(kFullMask, sum, o);
     }
-    ls.part[rank] = Part{t, w, off, sm.units_n > kUnits ? 1 : 0};
+    if (lane == 0) {
+      sm.wmax[warp] = top;
+      sm.wval[warp] = sum;
+    }
+    __syncthreads();
+    if (tid == 0) {
+      float t = sm.wmax[0], w = sm.wval[0];
+      for (int k = 1; k < kWarps; ++k) {
+        t = fmaxf(t, sm.wmax[k]);
+        w += sm.wval[k];
+      }
+      ls.part[rank] = Part{t, w, off, sm.units_n > kUnits ? 1 : 0};
+    }
+    if (cl > 1) cluster_sync();
+    else __syncthreads();
+    // too many candidates: once more among the noted units, with the higher bound
+    if (!(ls.list_n > kList && bound2 > bound)) break;
+    if (cl > 1) cluster_sync();
+    else __syncthreads();
+    bound = bound2;
+    sum = rest_sum;
+    if (tid == 0) sm.list_n = 0;
+    if (cl > 1) cluster_sync();
+    else __syncthreads();
   }
-  if (cl > 1) cluster_sync();
-  else __syncthreads();
 
   // ---- 3. the leader decides the row by the list, or the cluster by the row
   Weights wt;
@@ -1203,7 +1395,7 @@ extern "C" dartree_status dartree_sample(const void* logits, int32_t bf16, int64
   const SampleParams p{logits, row_stride, V, rows, rows_per_req, temperature, top_k, top_p, min_p, u, token, prob};
   // one cluster per row: as many CTAs as the SMs hold (four each)
   int cl = 1;
-  while (cl < kMaxCl && static_cast<long long>(rows) * cl < 304 && V / cl > 8192) cl *= 2;
+  while (cl < kMaxCl && static_cast<long long>(rows) * cl * 2 <= 608 && V / cl > 8192) cl *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (static_cast<long long>(rows) * cl > 0x7FFFFFFFll) return cache_fail(DARTREE_ERR_UNSUPPORTED, "too many rows");
   const dim3 grid(static_cast<unsigned>(rows) * cl);
