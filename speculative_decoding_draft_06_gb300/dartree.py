@@ -607,11 +607,12 @@ class KVCache:
         same in both."""
         t, width, ln, R = self._seqs(table, lens)
         idx, Hkv, dh = self._idx, self.Hkv, self.dh
-        for name, x in (("K", K), ("V", V)):
-            if x.dtype not in _BF16 or x.get_device() != idx:
-                raise TypeError(f"{name} must be a bf16 tensor on {self.dev}")
-        n = K.shape[1]
-        if K.shape != (R, n, Hkv, dh) or V.shape != K.shape:
+        if K.dtype not in _BF16 or K.get_device() != idx:
+            raise TypeError(f"K must be a bf16 tensor on {self.dev}")
+        if V.dtype not in _BF16 or V.get_device() != idx:
+            raise TypeError(f"V must be a bf16 tensor on {self.dev}")
+        n, want = K.shape[1], (R, K.shape[1], Hkv, dh)
+        if K.shape != want or V.shape != want:
             raise ValueError(f"K {tuple(K.shape)} / V {tuple(V.shape)} do not match R={R}, "
                              f"Hkv={Hkv}, dh={dh}")
         sr, sn, sh, sd = K.stride()
@@ -631,13 +632,14 @@ class KVCache:
         t, width, ln, R = self._seqs(table, lens)
         shape = (R, n, self.Hkv, self.dh)
         if out is None:
-            both = _alloc(stream, (2, *shape), torch.bfloat16, self.dev, count is not None)
-            out = (both[0], both[1])
-        for x in out:
-            if x.dtype not in _BF16 or x.get_device() != self._idx or not x.is_contiguous():
-                raise TypeError(f"out must be contiguous bf16 tensors on {self.dev}")
-            if x.shape != shape:
-                raise ValueError(f"out has shape {tuple(x.shape)}, expected {shape}")
+            # (two calls: halves of one tensor cost 10 us more)
+            out = tuple(_alloc(stream, shape, torch.bfloat16, self.dev, count is not None) for _ in "kv")
+        else:
+            for x in out:
+                if x.dtype not in _BF16 or x.get_device() != self._idx or not x.is_contiguous():
+                    raise TypeError(f"out must be contiguous bf16 tensors on {self.dev}")
+                if x.shape != shape:
+                    raise ValueError(f"out has shape {tuple(x.shape)}, expected {shape}")
         _launch(self._lib.dartree_cache_read, self._idx, stream, self._ref, layer,
                 out[0].data_ptr(), out[1].data_ptr(), t, width, ln, offset,
                 None if count is None else _ints("count", count, self._idx, R), R, n, self._err)
