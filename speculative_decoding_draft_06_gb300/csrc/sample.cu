@@ -32,6 +32,7 @@
 
 #include "block.cuh"
 #include "cache.cuh"
+#include "ptx.cuh"
 
 namespace dt {
 namespace {
@@ -45,6 +46,7 @@ constexpr int kTable = 768;          // bf16 logits of a sign whose weights are 
 constexpr int kList = 2944;          // candidates
 constexpr float kWant = 1800.f;      // candidates aimed at
 constexpr int kClass = 1024;         // members of a class that are sorted
+constexpr int kRanked = 128;         // members of a class that are ranked by comparisons
 constexpr int kUnits = 4096;         // 16-byte units of a CTA that may hold candidates
 constexpr int kMaxCl = 8;
 constexpr int kIdxBits = 18;
@@ -52,8 +54,8 @@ constexpr float kZeroBelow = -46.f;  // 2^-46 rounds to 0 in units of 2^-44
 constexpr int kExpBits = 10;
 
 // 2^(j / 1024) as the sum of two floats.
-struct ExpTable {
-  float hi[1 << kExpBits], lo[1 << kExpBits];
+struct alignas(16) ExpTable {
+  float v[2 << kExpBits];  // hi, lo
 };
 constexpr double exp2_fraction(double x) {  // x in [0, 1): the exponential series of x ln 2
   const double t = x * 0.69314718055994530941723212145818;
@@ -68,8 +70,8 @@ constexpr ExpTable make_exp_table() {
   ExpTable t{};
   for (int j = 0; j < (1 << kExpBits); ++j) {
     const double x = exp2_fraction(static_cast<double>(j) / (1 << kExpBits));
-    t.hi[j] = static_cast<float>(x);
-    t.lo[j] = static_cast<float>(x - static_cast<double>(t.hi[j]));
+    t.v[2 * j] = static_cast<float>(x);
+    t.v[2 * j + 1] = static_cast<float>(x - static_cast<double>(t.v[2 * j]));
   }
   return t;
 }
@@ -103,7 +105,7 @@ struct Part {            // a CTA's share of the pass, for the leader
 };
 
 struct Smem {
-  float2 exp[1 << kExpBits];
+  __align__(16) float2 exp[1 << kExpBits];
   union {
     struct {
       unsigned mass_lo[kBins], mass_hi[kBins];
@@ -120,8 +122,7 @@ struct Smem {
   unsigned long long scan_m[kWarps];
   unsigned scan_c[kWarps];
   float wmax[kWarps], wval[kWarps];
-  __align__(16) float sample[kThreads];
-  float4 bounds[kMaxCl];
+  __align__(16) unsigned sample[kThreads];
   float sbound, sbound2, smax;
   Part part[kMaxCl];
   unsigned list_n, units_n, cls_n;
@@ -234,9 +235,28 @@ __device__ __forceinline__ float logit<uint16_t>(const uint16_t* row, int i) {
   return x == x ? x : -INFINITY;
 }
 
+// floor(x 2^64) for x in (0, 1).
+__device__ __forceinline__ unsigned long long fraction64(float x) {
+  const unsigned b = __float_as_uint(x);
+  const int e = static_cast<int>(b >> 23);  // x = m 2^(e - 150), subnormals as if e were 1
+  const unsigned long long m = (b & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+  const int up = max(e, 1) - 86;
+  return up >= 0 ? m << up : up > -24 ? m >> -up : 0ull;
+}
+
+// w / z to fp32, for w <= z: both as sums of two floats (49 bits or more), the
+// quotient of the upper ones corrected once.  (An fp64 division: 0.7 us.)
+__device__ __forceinline__ float share_of(unsigned long long w, unsigned long long z) {
+  const float wh = __ull2float_rn(w), zh = __ull2float_rn(z);
+  const float wl = __ll2float_rn(static_cast<long long>(w - __float2ull_rn(wh)));
+  const float zl = __ll2float_rn(static_cast<long long>(z - __float2ull_rn(zh)));
+  const float q = __fdiv_rn(wh, zh);
+  return q + __fdiv_rn(fmaf(-q, zh, wh) + fmaf(-q, zl, wl), zh);
+}
+
 // ceil(p z) for p in (0, 1) (fp32) and z < 2^63, at least 1.
 __device__ __forceinline__ unsigned long long ceil_share(float p, unsigned long long z) {
-  const unsigned long long f = static_cast<unsigned long long>(ldexp(static_cast<double>(p), 63));
+  const unsigned long long f = fraction64(p) >> 1;
   const unsigned long long hi = __umul64hi(f, z), lo = f * z;
   const unsigned long long q = (hi << 1) | (lo >> 63);
   const unsigned long long c = q + ((lo << 1) != 0ull ? 1ull : 0ull);
@@ -499,34 +519,60 @@ __device__ bool cut(const S& s, const Weights& wt, bool by_count, unsigned long 
   s.sync();
   if (s.lead) {
     const int n = min(static_cast<int>(sm.cls_n), kClass);
-    const int n2 = pow2_at_least(n);
-    for (int i = n + threadIdx.x; i < n2; i += kThreads) sm.cls[i] = 0;
-    __syncthreads();
-    block_sort_desc(reinterpret_cast<uint64_t*>(sm.cls), n2);
-    constexpr int kQ = kClass / kThreads;
-    unsigned long long ms[kQ], m = 0;
-    unsigned c = 0;
-#pragma unroll
-    for (int j = 0; j < kQ; ++j) {
-      const int i = threadIdx.x * kQ + j;
-      ms[j] = i < n ? wt.weight44(key50_value(sm.cls[i])) : 0ull;
-      c += i < n ? 1u : 0u;
-      m += ms[j];
-    }
-    unsigned bc = c_before - c;
-    unsigned long long bm = m_before - m;
-    block_scan(sm, c, m);
-    bc += c;
-    bm += m;
-#pragma unroll
-    for (int j = 0; j < kQ; ++j) {
-      const int i = threadIdx.x * kQ + j;
-      if (i < n && (by_count ? bc + 1 == target : (bm < target && target <= bm + ms[j]))) {
-        ctl.keep = sm.cls[i];
-        sm.picked_m = bm + ms[j];
+    if (n <= kRanked) {
+      // few: each thread adds up what precedes its member
+      const int i = threadIdx.x;
+      unsigned long long key = 0, w = 0;
+      if (i < n) {
+        key = sm.cls[i];
+        w = wt.weight44(key50_value(key));
+        sm.cls[kRanked + i] = w;
       }
-      bc += i < n ? 1u : 0u;
-      bm += ms[j];
+      __syncthreads();
+      if (i < n) {
+        unsigned bc = c_before;
+        unsigned long long bm = m_before;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+          const bool before = sm.cls[j] > key;
+          bc += before;
+          bm += before ? sm.cls[kRanked + j] : 0ull;
+        }
+        if (by_count ? bc + 1 == target : (bm < target && target <= bm + w)) {
+          ctl.keep = key;
+          sm.picked_m = bm + w;
+        }
+      }
+    } else {
+      const int n2 = pow2_at_least(n);
+      for (int i = n + threadIdx.x; i < n2; i += kThreads) sm.cls[i] = 0;
+      __syncthreads();
+      block_sort_desc(reinterpret_cast<uint64_t*>(sm.cls), n2);
+      constexpr int kQ = kClass / kThreads;
+      unsigned long long ms[kQ], m = 0;
+      unsigned c = 0;
+#pragma unroll
+      for (int j = 0; j < kQ; ++j) {
+        const int i = threadIdx.x * kQ + j;
+        ms[j] = i < n ? wt.weight44(key50_value(sm.cls[i])) : 0ull;
+        c += i < n ? 1u : 0u;
+        m += ms[j];
+      }
+      unsigned bc = c_before - c;
+      unsigned long long bm = m_before - m;
+      block_scan(sm, c, m);
+      bc += c;
+      bm += m;
+#pragma unroll
+      for (int j = 0; j < kQ; ++j) {
+        const int i = threadIdx.x * kQ + j;
+        if (i < n && (by_count ? bc + 1 == target : (bm < target && target <= bm + ms[j]))) {
+          ctl.keep = sm.cls[i];
+          sm.picked_m = bm + ms[j];
+        }
+        bc += i < n ? 1u : 0u;
+        bm += ms[j];
+      }
     }
     if (threadIdx.x == 0) sm.cls_n = 0;
     __syncthreads();
@@ -566,7 +612,7 @@ __device__ unsigned long long min_p_key(const Weights& wt, float mp) {
 __device__ __forceinline__ unsigned long long draw_mark(float u, unsigned long long total) {
   unsigned long long t = 0;
   if (u > 0.f)
-    t = u >= 1.f ? total : __umul64hi(static_cast<unsigned long long>(ldexp(static_cast<double>(u), 64)), total);
+    t = u >= 1.f ? total : __umul64hi(fraction64(u), total);
   return t < total ? t : total - 1;
 }
 
@@ -971,7 +1017,7 @@ __device__ void whole_row(const SampleParams& p, Smem& sm, Smem& ls, const E* sr
         for (int k = 0; k < kPer; ++k) {
           if (c <= t && c + w[k] > t) {
             p.token[row] = i0 + k;
-            p.prob[row] = static_cast<float>(static_cast<double>(w[k]) / static_cast<double>(total));
+            p.prob[row] = share_of(w[k], total);
           }
           c += w[k];
         }
@@ -1055,18 +1101,21 @@ __device__ bool from_list(const SampleParams& p, Smem& sm, int row, int n, unsig
     sm.cls[at] = (static_cast<unsigned long long>(inverted(key)) << 32) | (key >> kIdxBits);
   });
   __syncthreads();
-  const int m = static_cast<int>(sm.cls_n), m2 = pow2_at_least(m);
-  for (int i = m + tid; i < m2; i += kThreads) sm.cls[i] = 0;
+  const int m = static_cast<int>(sm.cls_n);  // (256 at most)
+  unsigned long long mine = 0, w = 0;
+  if (tid < m) {
+    mine = sm.cls[tid];
+    w = wt.weight44(order_float(static_cast<uint32_t>(mine)));
+    sm.cls[kThreads + tid] = w;
+  }
   __syncthreads();
-  block_sort_desc(reinterpret_cast<uint64_t*>(sm.cls), m2);  // ascending index
-  const unsigned long long w = tid < m ? wt.weight44(order_float(static_cast<uint32_t>(sm.cls[tid]))) : 0ull;
-  unsigned one = 0;
-  unsigned long long inc = w;
-  block_scan(sm, one, inc);
-  inc += before;
-  if (tid < m && inc > t && inc - w <= t) {
-    p.token[row] = (1 << kIdxBits) - 1 - static_cast<int>(sm.cls[tid] >> 32);
-    p.prob[row] = static_cast<float>(static_cast<double>(w) / static_cast<double>(Z));
+  if (tid < m) {
+#pragma unroll 4
+    for (int j = 0; j < m; ++j) before += sm.cls[j] > mine ? sm.cls[kThreads + j] : 0ull;  // (lower indices)
+    if (before <= t && before + w > t) {
+      p.token[row] = (1 << kIdxBits) - 1 - static_cast<int>(mine >> 32);
+      p.prob[row] = share_of(w, Z);
+    }
   }
   return true;
 }
@@ -1091,8 +1140,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank_u));
   const int cl = static_cast<int>(cl_u), rank = static_cast<int>(rank_u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // (waited on before the first access to another CTA's memory)
-  if (cl > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   // requests that need their whole rows' weights first: their rows take several
   // times as long as the others', which then fill the SMs (2064 rows of 151936
   // in 129 requests of all kinds: an eighth to a third less time than in the rows' order)
@@ -1135,67 +1182,60 @@ __global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
   rule.use_k = rule.k >= 1 && rule.k < p.V;
   rule.use_p = rule.tp < 1.f;
   const bool greedy = !(T > 0.f);
-  const float ch = static_cast<float>(1.4426950408889634074 / static_cast<double>(T));
+  // log2(e) / T as a sum of two floats (fp64 divisions take a microsecond)
+  constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLo = 1.9259629911266175e-8f;
+  const float ch = __fdiv_rn(kLog2e, T);
+  const float ch_lo = isfinite(ch) ? __fdiv_rn(fmaf(-ch, T, kLog2e) + kLog2eLo, T) : 0.f;
 
   // (with no cut every token is in the draw, and the row's sums are needed)
   bool listed = greedy || rule.use_k || rule.use_p || rule.mp > 0.f;
   float bound = -INFINITY, bound2 = -INFINITY, off = 0.f;
-  for (int i = tid; i < (1 << kExpBits); i += kThreads) sm.exp[i] = make_float2(g_exp.hi[i], g_exp.lo[i]);
+  // (the table is waited for in front of the list)
+  for (int i = tid; i < (1 << kExpBits) / 2; i += kThreads)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&sm.exp[2 * i])), "l"(g_exp.v + 4 * i)
+                 : "memory");
   if (tid == 0) {
     sm.list_n = 0;
     sm.units_n = 0;
     sm.cls_n = 0;
     sm.ctl.done = 0;
   }
+  // (waited for before the first access to another CTA's memory)
+  if (cl > 1) cluster_arrive();
   if (listed) {
-    // ---- 1. a sample: every thread one unit, evenly spread over the row.
-    // the bound is the r-th largest of the CTA's units' maxima (a cluster
-    // takes the mean), with r / 256 the share of units that hold one of the
-    // candidates wanted: 256 (1 - (1 - want / V)^kPer)
+    // ---- 1. a sample: every thread one unit, evenly spread over the row (the
+    // same in all of a cluster's CTAs: exchanging bounds of several samples
+    // costs more than their better bound gives).  The bound is the r-th largest
+    // of the units' maxima, with r / 256 the share of units that hold one of
+    // the candidates wanted: 256 (1 - (1 - want / V)^kPer).  The order is that
+    // of the maxima's upper 24 bits: any bound near it does.
     float m = -INFINITY;
     if (rw.units > 0) {
       float x[kPer];
-      const long long at = (static_cast<long long>(rank) * kThreads + tid) * rw.units / (cl * kThreads);
-      unpack<E>(rw.load(static_cast<int>(at)), x);
+      unpack<E>(rw.load(static_cast<int>(static_cast<long long>(tid) * rw.units / kThreads)), x);
       m = fmaxf(max_of(x), -INFINITY);
     }
-    sm.sample[tid] = m;
+    const unsigned mine = (float_order(m) & ~255u) | tid;
+    sm.sample[tid] = mine;
     __syncthreads();
     const float want = rule.use_k ? fminf(fmaxf(2.f * rule.k, 0.5f * kWant), 1.2f * kWant) : kWant;
     const float share_out = fminf(want / static_cast<float>(p.V), 1.f);
-    const int r = greedy ? 1 : max(1, static_cast<int>(kThreads * (1.f - __powf(1.f - share_out, kPer)) + 0.5f));
-    int above = 0, equal = 0;
-    for (int q = 0; q < kThreads; q += 4) {
-      const float4 o = *reinterpret_cast<const float4*>(&sm.sample[q]);
-      above += (o.x > m) + (o.y > m) + (o.z > m) + (o.w > m);
-      equal += (o.x == m) + (o.y == m) + (o.z == m) + (o.w == m);
-    }
-    if (above == 0) sm.smax = m;                          // (all that write write the same)
-    if (above < r && r <= above + equal) sm.sbound = m;
+    const int r = max(1, static_cast<int>(kThreads * (1.f - __powf(1.f - share_out, kPer)) + 0.5f));
     const int r2 = rule.use_k ? (2 * r + 2) / 3 : (r + 1) / 2;  // (should the list overflow)
-    if (above < r2 && r2 <= above + equal) sm.sbound2 = m;
-    __syncthreads();
-    float lo = sm.sbound, lo2 = sm.sbound2, hi = sm.smax;
-    if (cl > 1) {
-      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-      if (tid < cl) at_rank(&sm, tid)->bounds[rank] = make_float4(lo, lo2, hi, 0.f);
-      cluster_sync();
-      lo = lo2 = 0.f;
-      for (int q = 0; q < cl; ++q) {
-        lo += sm.bounds[q].x;
-        lo2 += sm.bounds[q].y;
-        hi = fmaxf(hi, sm.bounds[q].z);
-      }
-      lo /= static_cast<float>(cl);                       // (-inf where one of them is)
-      lo2 /= static_cast<float>(cl);
+    int above = 0;
+    for (int q = 0; q < kThreads; q += 4) {
+      const uint4 o = *reinterpret_cast<const uint4*>(&sm.sample[q]);
+      above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
     }
-    bound = greedy ? hi : lo;
-    bound2 = greedy ? hi : lo2;
-    off = hi * ch;  // the reference of the sums: the sample's largest logit
+    if (above == 0) sm.smax = m;
+    if (above == r - 1) sm.sbound = m;
+    if (above == r2 - 1) sm.sbound2 = m;
+    __syncthreads();
+    const float hi = sm.smax;
+    bound = greedy ? hi : sm.sbound;
+    bound2 = greedy ? hi : sm.sbound2;
+    off = hi * ch;  // the reference of the sums
     if (!isfinite(off)) off = 0.f;
-  } else if (cl > 1) {
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    cluster_sync();  // (the leader's counters)
   } else {
     __syncthreads();
   }
@@ -1252,6 +1292,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
   if (!listed) pass(IntC<0>{});
   else if (!sums) pass(IntC<1>{});
   else pass(IntC<2>{});
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (cl > 1) cluster_wait();
   __syncthreads();
   // one token: to the leader's list, or into the sum
   auto token = [&](float x, int i) {
@@ -1269,12 +1311,36 @@ __global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
   for (;;) {
     if (listed) {
       const int n = min(static_cast<int>(sm.units_n), kUnits);
-      for (int i = tid; i < n; i += kThreads) {
-        const int un = sm.unit[i];
+      for (int b = warp * 32; b < n; b += kThreads) {
+        const int un = b + lane < n ? sm.unit[b + lane] : -1;
+        unsigned in = 0;
         float x[kPer];
-        unpack<E>(rw.load(un), x);
+        if (un >= 0) {
+          unpack<E>(rw.load(un), x);
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) token(x[k], rw.index(un) + k);
+          for (int k = 0; k < kPer; ++k) {
+            if (!(x[k] > -INFINITY)) continue;  // (NaN, -inf)
+            top = fmaxf(top, x[k]);
+            if (x[k] >= bound) in |= 1u << k;
+            else sum += ex2(fmaf(x[k], ch, -off));
+          }
+        }
+        // the warp's candidates take their places by one addition
+        int at = __popc(in);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(kFullMask, at, o);
+          if (lane >= o) at += y;
+        }
+        unsigned base = 0;
+        if (lane == 31) base = atomicAdd(&ls.list_n, static_cast<unsigned>(at));
+        at += static_cast<int>(__shfl_sync(kFullMask, base, 31)) - __popc(in);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          if (!(in >> k & 1)) continue;
+          if (at < kList) ls.list[at] = key50(x[k], rw.index(un) + k);
+          ++at;
+        }
       }
     }
     if (lead) {
@@ -1317,9 +1383,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
   Weights wt;
   wt.exp = sm.exp;
   wt.ch = ch;
-  wt.cl = 0.f;
-  if (!isinf(ch))
-    wt.cl = static_cast<float>(1.4426950408889634074 / static_cast<double>(T) - static_cast<double>(ch));
+  wt.cl = ch_lo;
   if (lead) {
     float all = 0.f;
     bool lost = false;
@@ -1355,13 +1419,13 @@ __global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
       }
     } else if (listed && !lost && n <= kList && isfinite(top) && isfinite(all) && isfinite(top * ch)) {
       // the sums, relative to the largest logit: 2^(off - top ch) of what
-      // they are, off by (|x ch - off| <= 46 where a weight counts) 2^-19 for
-      // the argument's rounding, 2^-20 for ch's, 2^-22 for ex2 and 2^-17 for
-      // some 100 additions: below 2^-16; the weights' own rounding to whole
-      // units is half a unit per token
-      const double scaled = ldexp(static_cast<double>(all) * exp2(static_cast<double>(off) -
-                                                                   static_cast<double>(top) * static_cast<double>(ch)), 44);
-      const unsigned long long tail = static_cast<unsigned long long>(scaled);
+      // they are, off by (|x ch - off| <= 46 where a weight counts, and so
+      // is |off - top ch|) 2^-19 for each argument's rounding, 2^-19 for
+      // ch's, 2^-21 for two ex2 and 2^-17 for some 100 additions: below
+      // 2^-16; the weights' own rounding to whole units is half a unit per
+      // token
+      const unsigned long long tail =
+          static_cast<unsigned long long>(all * ex2(fmaf(-top, ch, off)) * 17592186044416.f);
       done = from_list<E>(p, sm, row, n, static_cast<unsigned long long>(float_order(bound)) << kIdxBits, tail,
                           (tail >> 16) + static_cast<unsigned long long>(p.V), wt, rule);
     }
