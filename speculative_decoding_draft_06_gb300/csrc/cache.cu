@@ -38,11 +38,11 @@ __device__ __forceinline__ TokenSlot token_slot(const TokenParams& p) {
   constexpr int kBlk = DH / 16, kTok = 32 / kBlk;
   TokenSlot s;
   const int lane = threadIdx.x & 31;
-  const long long w = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  s.h = static_cast<int>(w % p.c.Hkv);
-  const long long rest = w / p.c.Hkv;
-  s.r = static_cast<int>(rest / p.groups);
-  s.i = static_cast<int>(rest % p.groups) * kTok + lane / kBlk;
+  const unsigned w = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const unsigned rest = w / static_cast<unsigned>(p.c.Hkv);
+  s.h = static_cast<int>(w - rest * p.c.Hkv);
+  s.r = static_cast<int>(rest / static_cast<unsigned>(p.groups));
+  s.i = static_cast<int>(rest - static_cast<unsigned>(s.r) * p.groups) * kTok + lane / kBlk;
   s.blk = lane % kBlk;
   s.live = s.paged = false;
   s.base = nullptr;
@@ -616,7 +616,7 @@ dartree_status token_params(const dartree_cache* cache, int32_t layer, const voi
   p->groups = (n + tok - 1) / tok;
   p->err = err;
   const long long warps = static_cast<long long>(R) * p->groups * p->c.Hkv;
-  if (warps > (1ll << 33)) return cache_fail(DARTREE_ERR_UNSUPPORTED, "too many tokens in one call");
+  if (warps > 0x7FFFFFF0ll) return cache_fail(DARTREE_ERR_UNSUPPORTED, "too many tokens in one call");
   *blocks = static_cast<unsigned>((warps + 7) / 8);
   return DARTREE_OK;
 }

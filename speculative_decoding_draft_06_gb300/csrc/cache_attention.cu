@@ -590,8 +590,9 @@ cudaError_t launch_join(const CacheAttnParams& p, cudaStream_t st) {
 // above, in tiles of 64 keys, four warps a tile each; more by the tensor-core
 // kernel in tiles of 256 rows and 128 keys.  The keys are split until the GPU
 // is full: here once over (three CTAs per SM), a tile per warp at least, and
-// at the latest every 2048 keys, so that sequences of different lengths share
-// the SMs evenly; there one wave of one CTA per SM.  Up to eight splits that
+// with several requests at the latest every 2048 keys, so that sequences of
+// different lengths share the SMs evenly (a single one of 131072 tokens: one
+// wave 36 us, in 2048 keys, a wave and an eighth, 46); there one wave of one CTA per SM.  Up to eight splits that
 // are all resident at once are a thread-block cluster each and join in shared
 // memory: no second kernel and no workspace for short sequences.
 constexpr int kTreeRows = 16;
@@ -614,7 +615,7 @@ Plan plan_rows(bool tree, long long rows, int R, int max_len, int Hkv, int dh, i
   const int tiles = max_len < 1 ? 1 : (max_len - 1) / pl.tile_keys + 1;
   const long long ctas = static_cast<long long>(R) * Hkv * pl.m_tiles;
   long long n = tree ? sms / ctas : (sms * 3 + ctas - 1) / ctas;
-  if (!tree && n < (tiles + kSplitTiles - 1) / kSplitTiles) n = (tiles + kSplitTiles - 1) / kSplitTiles;
+  if (!tree && R > 1 && n < (tiles + kSplitTiles - 1) / kSplitTiles) n = (tiles + kSplitTiles - 1) / kSplitTiles;
   const long long most = tree ? (tiles + 3) / 4 : (tiles + kWarps - 1) / kWarps;
   n = n < most ? n : most;
   n = n < most_splits ? n : most_splits;
