@@ -33,8 +33,17 @@ struct TokenSlot {
   bool paged;
 };
 
+// Data that is read once (issued here, whatever the compiler would move).
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 template <int DH>
-__device__ __forceinline__ TokenSlot token_slot(const TokenParams& p) {
+__device__ __forceinline__ TokenSlot token_of(const TokenParams& p) {
   constexpr int kBlk = DH / 16, kTok = 32 / kBlk;
   TokenSlot s;
   const int lane = threadIdx.x & 31;
@@ -47,11 +56,15 @@ __device__ __forceinline__ TokenSlot token_slot(const TokenParams& p) {
   s.live = s.paged = false;
   s.base = nullptr;
   s.t = 0;
-  if (s.r >= p.R) return s;
+  return s;
+}
+
+// The token's page and place in it, if it has them (r < R).
+__device__ __forceinline__ void find_slot(const TokenParams& p, TokenSlot& s) {
   const int len = p.lens[s.r];
   const int n = p.count ? min(p.n, p.count[s.r]) : p.n;
   s.live = len >= 0 && s.i < n;
-  if (!s.live) return s;
+  if (!s.live) return;
   const long long pos = static_cast<long long>(len) + p.offset + s.i;
   const long long slot = pos >> p.c.log_page;
   if (pos >= 0 && slot < p.max_pages) {
@@ -63,7 +76,6 @@ __device__ __forceinline__ TokenSlot token_slot(const TokenParams& p) {
     }
   }
   if (!s.paged && s.blk == 0 && s.h == 0 && p.err) atomicOr(p.err, DT_ERR_BAD_INDEX);
-  return s;
 }
 
 // One block of 16 bf16 -> 8 bytes of codes and the scale byte.
@@ -101,14 +113,17 @@ __device__ __forceinline__ uint2 quantise16(const uint4 (&in)[2], float inv_scal
 
 template <int DH>
 __global__ void __launch_bounds__(256) k_cache_append(const TokenParams p) {
-  const TokenSlot s = token_slot<DH>(p);
-  if (!s.live || !s.paged) return;
+  TokenSlot s = token_of<DH>(p);
+  if (s.r >= p.R || s.i >= p.n) return;
   const size_t at = static_cast<size_t>(s.r) * p.req_stride + static_cast<size_t>(s.i) * p.token_stride +
                     s.h * DH + s.blk * 16;
   const uint4* k = reinterpret_cast<const uint4*>(p.K + at);
   const uint4* v = reinterpret_cast<const uint4*>(p.V + at);
-  const uint4 kin[2] = {__ldg(k), __ldg(k + 1)};
-  const uint4 vin[2] = {__ldg(v), __ldg(v + 1)};
+  // (on their way while the page is looked up)
+  const uint4 kin[2] = {load_once(k), load_once(k + 1)};
+  const uint4 vin[2] = {load_once(v), load_once(v + 1)};
+  find_slot(p, s);
+  if (!s.live || !s.paged) return;
   uint8_t* base = const_cast<uint8_t*>(s.base);
   const int codes = (DH / 2) << p.c.log_page;  // bytes of a chunk's key codes
   const int half = p.c.chunk >> 1;
@@ -140,7 +155,9 @@ __device__ __forceinline__ void values16(uint2 codes, uint32_t scale, float mul,
 
 template <int DH>
 __global__ void __launch_bounds__(256) k_cache_read(const TokenParams p) {
-  const TokenSlot s = token_slot<DH>(p);
+  TokenSlot s = token_of<DH>(p);
+  if (s.r >= p.R) return;
+  find_slot(p, s);
   if (!s.live) return;
   const size_t at = ((static_cast<size_t>(s.r) * p.n + s.i) * p.c.Hkv + s.h) * DH + s.blk * 16;
   uint4* k = reinterpret_cast<uint4*>(p.Ko + at);
@@ -156,10 +173,10 @@ __global__ void __launch_bounds__(256) k_cache_read(const TokenParams p) {
     values16(ck, sk, p.c.k_scale, ko);
     values16(cv, sv, p.c.v_scale, vo);
   }
-  k[0] = ko[0];
-  k[1] = ko[1];
-  v[0] = vo[0];
-  v[1] = vo[1];
+  __stcs(k, ko[0]);
+  __stcs(k + 1, ko[1]);
+  __stcs(v, vo[0]);
+  __stcs(v + 1, vo[1]);
 }
 
 // --------------------------------------------------------- page operations
