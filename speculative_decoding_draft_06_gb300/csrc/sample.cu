@@ -190,8 +190,9 @@ struct Weights {
   }
 };
 
+// (-0 + 0 = 0: the two zeros are one logit)
 __device__ __forceinline__ unsigned long long key50(float x, int idx) {
-  return (static_cast<unsigned long long>(float_order(x)) << kIdxBits) |
+  return (static_cast<unsigned long long>(float_order(x + 0.f)) << kIdxBits) |
          static_cast<unsigned>((1 << kIdxBits) - 1 - idx);
 }
 __device__ __forceinline__ float key50_value(unsigned long long k) {

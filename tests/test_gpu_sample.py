@@ -91,6 +91,18 @@ def test_ties(V):
             check(torch.from_numpy(x).cuda(), u, 6, None, k, p, None)
 
 
+@pytest.mark.parametrize("V", [9, 20000, 100000])
+def test_the_two_zeros_are_equal(V):
+    g = np.random.default_rng(V)
+    x = np.where(g.random((6, V)) < 0.5, np.float32(-0.0), np.float32(0.0))
+    x[3:, V // 2:] = -1.0
+    u = g.random(6).astype(np.float32)
+    for dt in (torch.float32, torch.bfloat16):
+        t = torch.from_numpy(x).to(dt).cuda()
+        for T, k, p in ((0.0, 0, 1.0), (1.0, 1, 1.0), (1.0, V // 3, 1.0), (1.0, 0, 0.4), (0.7, 5, 0.5)):
+            check(t, u, 6, [T], [k], [p], None)
+
+
 def test_exact_borders():
     """Equal weights make the borders whole numbers: u and top_p that fall on
     them are decided by 'exceeds u' and 'at least top_p'."""
@@ -159,6 +171,55 @@ def test_results_do_not_depend_on_the_launch():
     other = dtl.sample(x, u, stream=s, **kw)
     s.synchronize()
     assert torch.equal(other["token"], again["token"])
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("shift", [-6.0, 6.0])
+def test_rows_whose_spread_out_units_mislead(bf16, shift):
+    """256 evenly spread units of 16 bytes lie far below or above the rest of
+    the row: a bound that is taken from them lets nearly all tokens pass, or
+    almost none."""
+    V, rows = 40008, 4
+    g = np.random.default_rng(5)
+    x = g.standard_normal((rows, V)).astype(np.float32)
+    per = 8 if bf16 else 4
+    units = V // per
+    for t in range(256):
+        at = t * units // 256 * per
+        x[:, at:at + per] += shift
+    x = torch.from_numpy(x).to(torch.bfloat16 if bf16 else torch.float32).cuda()
+    u = g.random(rows).astype(np.float32)
+    for T, k, p, m in ((1.0, 20, 1.0, 0.0), (1.0, 1000, 1.0, 0.0), (0.5, 1000, 0.9, 0.0), (1.0, 2500, 1.0, 0.0),
+                       (1.0, 2500, 0.8, 0.01), (1.0, 9000, 0.999, 0.0), (1.0, 30000, 1.0, 0.0), (0.3, 0, 0.5, 0.0),
+                       (1.0, 0, 0.99, 0.0), (1.0, 0, 1.0, 0.2), (1.0, 0, 0.9, 1e-4), (0.0, 0, 1.0, 0.0), (3.0, 0, 0.3, 0.0)):
+        check(x, u, rows, [T], [k], [p], [m])
+
+
+@pytest.mark.parametrize("V", [300, 60000])
+@pytest.mark.parametrize("low,high", [(-0.3, 0.3), (-30.0, -0.05), (-9.0, 5.0), (1e-38, 1e-30), (-3e4, -2e4), (-1.0, 0.0)])
+def test_bf16_logits_of_all_sizes(low, high, V):
+    """Whole rows of bf16 logits, most of them on either side of zero, at
+    zero, subnormal or far from it."""
+    g = np.random.default_rng(V)
+    x = torch.from_numpy(g.uniform(low, high, (4, V))).to(torch.bfloat16)
+    x[1, ::3] = 0.0
+    x[1, 1::3] = -0.0
+    x[2, ::2] = high
+    u = g.random(4).astype(np.float32)
+    for T in (1.0, 0.1, 20.0):
+        for p in (1.0, 0.95, 0.4):
+            check(x.cuda(), u, 4, [T], None, [p], None)
+
+
+@pytest.mark.parametrize("R,per,last", [(300, 3, 3), (300, 3, 1), (1024, 1, 1), (1030, 1, 1), (33, 2, 2)])
+def test_many_requests_of_all_kinds(R, per, last):
+    """Rows that need their whole row's weights among rows that do not."""
+    g = np.random.default_rng(R)
+    V, rows = 700, R * per - (per - last)
+    x = torch.from_numpy(g.standard_normal((rows, V)).astype(np.float32) * 2).cuda()
+    u = g.random(rows).astype(np.float32)
+    check(x, u, per, g.choice([0.0, 0.5, 1.0, 2.0], R), g.choice([0, 0, 1, 10, 300], R),
+          g.choice([1.0, 0.9, 0.3], R), g.choice([0.0, 0.0, 0.1], R))
 
 
 def test_draws_follow_the_distribution():
