@@ -452,11 +452,12 @@ __device__ __forceinline__ int pick_class(const S& s, bool by_count, unsigned lo
   return k;
 }
 
+constexpr float kBinBig = 12582912.f;
+
 // The classes of the cuts: -log2 w in steps of 1 / kBinsPer2, to the nearest
 // (by adding 1.5 2^23, whose ulp is 1).
 __device__ __forceinline__ int bin_of_log2(float y) {
-  constexpr float kBig = 12582912.f;
-  return min(kBins - 1, __float_as_int(fmaf(y, -kBinsPer2, kBig)) - __float_as_int(kBig));
+  return min(kBins - 1, __float_as_int(fmaf(y, -kBinsPer2, kBinBig)) - __float_as_int(kBinBig));
 }
 __device__ __forceinline__ int bin_of(const Weights& wt, float x) { return bin_of_log2(wt.log2w(x)); }
 
@@ -746,9 +747,12 @@ __device__ bool nucleus(const S& s, const Weights& wt, const Rule& rule, unsigne
   s.each_value([&](float x, int) {
     const float y = wt.log2w(x);
     if (!(y >= kZeroBelow)) return;
-    const int b = bin_of_log2(y);
-    const float w = ex2(fmaf(static_cast<float>(b), 1.f / kBinsPer2, y));  // 2^(-1/40) .. 2^(1/40)
-    atomicAdd(&sm.mass_lo[b], static_cast<unsigned>(fmaf(w, kMassUnit, 0.5f)));
+    // (bin_of_log2's class, at most 920, and the mass by additions of 1.5 2^23
+    // and 2^23: conversions are slower)
+    const float z = fmaf(y, -kBinsPer2, kBinBig);
+    const float w = ex2(fmaf(z - kBinBig, 1.f / kBinsPer2, y));  // 2^(-1/40) .. 2^(1/40)
+    atomicAdd(&sm.mass_lo[__float_as_int(z) - __float_as_int(kBinBig)],
+              __float_as_uint(fmaf(w, kMassUnit, 8388608.f)) & 0x7FFFFFu);
   });
   s.sync();
   if (s.lead) {
