@@ -531,13 +531,14 @@ def _alloc(stream, shape, dtype, dev, zero: bool = False) -> torch.Tensor:
 # the rest of a call), where PyTorch has it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda idx: torch.cuda.current_stream(idx).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _launch(fn, idx: int, stream, *args) -> None:
     """Calls fn(*args, stream) with the tensors' device current; raises on an
     error."""
     st = _raw_stream(idx) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == idx:
+    if _device() == idx:
         s = fn(*args, st)
     else:
         with torch.cuda.device(idx):
@@ -633,7 +634,9 @@ class KVCache:
         shape = (R, n, self.Hkv, self.dh)
         if out is None:
             # (two calls: halves of one tensor cost 10 us more)
-            out = tuple(_alloc(stream, shape, torch.bfloat16, self.dev, count is not None) for _ in "kv")
+            zero = count is not None
+            out = (_alloc(stream, shape, torch.bfloat16, self.dev, zero),
+                   _alloc(stream, shape, torch.bfloat16, self.dev, zero))
         else:
             for x in out:
                 if x.dtype not in _BF16 or x.get_device() != self._idx or not x.is_contiguous():
