@@ -15,6 +15,12 @@ namespace {
 // other.  Consecutive warps take consecutive heads, so that the bf16 rows
 // are touched in their order and the codes of a warp's tokens are one
 // contiguous piece.
+// Bound by memory and, in append, by issue as well (0.83 instructions a cycle
+// and scheduler): 2 x 16000 tokens of 8 heads of 128 take 31 us in and 32 us
+// out, 168 MB each, 81% of a copy's rate together (71 us together with loads
+// behind the page lookup and plain stores; several heads per warp, one lookup
+// for all, 66 to 70: fewer loads in flight).  A step's 8 x 129 tokens: 6.2 us
+// in and out.
 struct TokenParams {
   CacheView c;
   const uint16_t *K, *V;   // append: input rows
@@ -272,6 +278,7 @@ struct ReserveParams {
 
 // One block: what each row lacks, the rows' first ranks among the free
 // pages (prefix sums), then the free pages go to the row their rank falls in.
+// Latency: 4.5 us alone with cold caches.
 __global__ void __launch_bounds__(kPlanThreads) k_cache_reserve(const ReserveParams p) {
   __shared__ int s_first[kMaxReserveRows + 1], s_held[kMaxReserveRows];
   __shared__ int sh[33];
@@ -434,7 +441,9 @@ __device__ __forceinline__ void piece(size_t page_bytes, int* begin, int* end) {
   *end = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
 }
 
-// The partly filled page of each fork, grid (pieces, layers, forks).
+// The partly filled page of each fork, grid (pieces, layers, forks).  Bound by
+// memory: 32 forks, 32 layers, pages of 64 tokens of 8 heads of 128: 151 MB
+// with the release and the plan in front of it in 24 us, 6.3 TB/s.
 __global__ void __launch_bounds__(256) k_cache_fork_copy(const ForkParams p) {
   const int i = blockIdx.z;
   pdl_wait();
@@ -549,6 +558,8 @@ __device__ __forceinline__ int commit_count(const CommitParams& p, int r, int* b
 // token k's source is at or behind position k: a chunk of tokens is read whole
 // before it is written, and no later chunk reads what an earlier one wrote.
 // The row's length changes once every CTA of its cluster has read it.
+// Latency of a read behind a lookup behind a read: release, reserve and commit
+// of a path of 8 tokens in 32 layers take 13.8 us, of 32 paths 18.3.
 template <typename U>
 __global__ void __launch_bounds__(256) k_cache_commit(const CommitParams p) {
   constexpr int kU = 8;

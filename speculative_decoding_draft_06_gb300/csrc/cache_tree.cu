@@ -24,6 +24,16 @@
 // by kRaise, which rescales O in TMEM.
 // Requests go to the SMs longest first (the CTA's request is the z-th
 // longest), so that the last ones to start are the short ones.
+//
+// Bound by the latency of a step's chain (scores, maximum, weights, product)
+// at two row tiles per SM: 32 trees of 65 rows over up to 2500 tokens, 32 heads
+// over 8 of 128: 83 us, 640 TFLOP/s, the tensor pipe active 33% of the time,
+// issue 0.55 (the exponentials and the conversions of the codes alone would
+// take 29 us); one of 129 rows over 4099 tokens: 32 us.  Steps for the 32 (the
+// one): one row tile 181 us (41); two, and codes expanded from registers 121
+// (53); scores a step of 64 keys ahead and two issuers 85 (47); leftover rows in
+// a launch beside 89 (43); two threads per row 83 (35).  A polynomial for part
+// of the exponentials and row tiles that take turns were slower.
 #include <type_traits>
 
 #include "cache_attn.cuh"

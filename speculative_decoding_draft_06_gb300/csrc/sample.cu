@@ -24,6 +24,13 @@
 // border inside the interval, infinities, NaN) takes further passes over the
 // row itself, all in integers (whole_row).
 //
+// Bound, in rows that the candidates decide, by the passes' instructions (6 a
+// token) and the list's chain of steps; in the others by 35 to 100 a token.
+// 2064 rows of 151936 bf16 logits: greedy 153 us (4.1 TB/s, 61% of a copy),
+// top-k 50 213, top-p 0.9 at T = 0.7 390, top-p 0.95 at T = 1 (85% of these
+// rows by whole rows) 1300, no cut 620; 129 rows in fp32: 24, 37, 46, 193, 108;
+// 17 rows of 32000 20 us, latency.
+//
 // A cut: a histogram of counts and masses over 1024 classes of -log2 w
 // (monotone in the logit) gives the class in which it falls; the class is
 // gathered (refined by digits of the key while it is large), sorted, and the
