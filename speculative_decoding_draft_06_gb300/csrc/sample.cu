@@ -1190,14 +1190,14 @@ __global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
   Rule rule;
   rule.k = p.top_k ? p.top_k[req] : 0;
   rule.tp = p.top_p ? p.top_p[req] : 1.f;
-  rule.mp = p.min_p ? fminf(p.min_p[req], 1.f) : 0.f;
+  rule.mp = p.min_p && p.min_p[req] > 0.f ? fminf(p.min_p[req], 1.f) : 0.f;
   rule.use_k = rule.k >= 1 && rule.k < p.V;
   rule.use_p = rule.tp < 1.f;
   const bool greedy = !(T > 0.f);
   // log2(e) / T as a sum of two floats (fp64 divisions take a microsecond)
   constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLo = 1.9259629911266175e-8f;
   const float ch = __fdiv_rn(kLog2e, T);
-  const float ch_lo = isfinite(ch) ? __fdiv_rn(fmaf(-ch, T, kLog2e) + kLog2eLo, T) : 0.f;
+  const float ch_lo = isfinite(ch) && isfinite(T) ? __fdiv_rn(fmaf(-ch, T, kLog2e) + kLog2eLo, T) : 0.f;
 
   // (with no cut every token is in the draw, and the row's sums are needed)
   bool listed = greedy || rule.use_k || rule.use_p || rule.mp > 0.f;

@@ -20,10 +20,12 @@ def i32(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
-def check(logits, u, per, T, k, p, m):
+def check(logits, u, per, T, k, p, m, exact=False):
     """One call against the reference, every row.  prob is w / total rounded
     to fp32 (2^-24), the weights being off by 2^-44 of the largest at most:
-    2^-25 of a weight above 2^-19; below, the difference is absolute."""
+    2^-25 of a weight above 2^-19; below, the difference is absolute.  exact:
+    the weights are whole numbers on both sides, and so are values on a
+    border."""
     n = -(-len(u) // per)
     got = dtl.sample(logits, torch.from_numpy(u).cuda(), rows_per_req=per, temperature=None if T is None else f32(T),
                      top_k=None if k is None else i32(k), top_p=None if p is None else f32(p),
@@ -36,7 +38,7 @@ def check(logits, u, per, T, k, p, m):
         r = i // per
         assert r < n
         t, q, margin = ref.sample_row(l[i], f(T, 1.0, r), int(f(k, 0, r)), f(p, 1.0, r), f(m, 0.0, r), float(u[i]))
-        if margin < 2.0 ** -40:      # the border is where the value is: both sides' last bits decide
+        if margin < 2.0 ** -40 and not exact:      # the border is where the value is: both sides' last bits decide
             near += 1
             continue
         assert tok[i] == t, (i, tok[i], t, margin)
@@ -101,6 +103,25 @@ def test_the_two_zeros_are_equal(V):
         t = torch.from_numpy(x).to(dt).cuda()
         for T, k, p in ((0.0, 0, 1.0), (1.0, 1, 1.0), (1.0, V // 3, 1.0), (1.0, 0, 0.4), (0.7, 5, 0.5)):
             check(t, u, 6, [T], [k], [p], None)
+
+
+@pytest.mark.parametrize("V", [50, 3001, 60000])
+def test_extreme_settings(V):
+    """Temperatures from the smallest to infinity; NaN settings cut nothing (a
+    temperature: the largest logit)."""
+    g = np.random.default_rng(V)
+    x = torch.from_numpy(g.standard_normal((5, V)).astype(np.float32) * 3)
+    u = g.random(5).astype(np.float32)
+    big = float(np.finfo(np.float32).max)
+    for t in (x.cuda(), x.to(torch.bfloat16).cuda()):
+        for T in (float("inf"), big, 1e30, 1e5, 1e-5, 1e-30, 1e-38):
+            for k, p, m in ((0, 1.0, 0.0), (7, 1.0, 0.0), (0, 0.5, 0.0), (0, 1.0, 0.5), (V // 2, 0.9, 0.1)):
+                check(t, u, 5, [T], [k], [p], [m], exact=T >= 1e30)  # (there all weights are 1)
+        nan = dtl.sample(t, torch.from_numpy(u).cuda(), rows_per_req=5, top_p=f32([float("nan")]), min_p=f32([float("nan")]))
+        none = dtl.sample(t, torch.from_numpy(u).cuda())
+        assert torch.equal(nan["token"], none["token"]) and torch.equal(nan["prob"], none["prob"])
+        cold = dtl.sample(t, torch.from_numpy(u).cuda(), rows_per_req=5, temperature=f32([float("nan")]))
+        assert torch.equal(cold["token"], t.float().argmax(1).int())
 
 
 def test_exact_borders():
