@@ -519,8 +519,11 @@ size_t dartree_cache_attention_workspace(int32_t R, int32_t B, int32_t max_len, 
 /* Pages for want[r] more tokens per row: row r comes to hold at least
  * ceil((lens[r] + want[r]) / page_tokens) pages; lens is not changed.  Rows
  * are served in order; ok[r] = 0 for a row that needs more than max_pages or
- * has lens[r] or want[r] < 0 (it gets none), and for the first row whose
- * pages are not there and every later one that needs some.  R <= 4096. */
+ * has lens[r] or want[r] < 0 (it gets none), or whose last page is partly
+ * filled and held by another row too (a forked row that was cut within a
+ * complete page: fork it, the copy has a page of its own), and for the first
+ * row whose pages are not there and every later one that needs some.
+ * R <= 4096, R * max_pages < 2^31. */
 dartree_status dartree_cache_reserve(const dartree_cache *cache, int32_t *table, int32_t max_pages,
                                      const int32_t *lens, const int32_t *want, int32_t R,
                                      int32_t *ok, void *stream);

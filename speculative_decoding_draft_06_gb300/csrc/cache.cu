@@ -290,6 +290,15 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_reserve(const ReservePar
     if (len >= 0 && want >= 0 && need <= p.max_pages) {
       held = held_pages(p.table + static_cast<size_t>(r) * p.max_pages, p.max_pages);
       lack = need > held ? static_cast<int>(need) - held : 0;
+      // its next token would go into a page that another row reads
+      const long long at = len >> p.log_page;
+      if (want > 0 && (len & ((1 << p.log_page) - 1)) != 0 && at < held) {
+        const int page = p.table[static_cast<size_t>(r) * p.max_pages + at];
+        if (page < p.pages && p.refs[page] > 1) {
+          held = -1;
+          lack = 0;
+        }
+      }
     }
     if (lane == 0) {
       s_held[r] = held;
@@ -297,7 +306,6 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_reserve(const ReservePar
     }
   }
   __syncthreads();
-  // ranks saturate at the page count (more cannot be met anyway)
   int total = 0;
   {
     int v[4], sum = 0;

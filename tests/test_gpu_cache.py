@@ -297,6 +297,28 @@ def test_commit(case):
     assert int(cache.err.item()) == (BAD if flagged else 0)
 
 
+def test_a_row_cut_within_a_shared_page_does_not_grow():
+    """Its next token would go into a page that the other row reads: reserve
+    refuses it until the row is forked or the page is its own."""
+    c = dtl.KVCache(2, 12, page_tokens=16, Hkv=1, dh=64)
+    table, lens = cu(np.full((3, 6), -1)), cu([0, 0, 0])
+    assert host(c.reserve(table, lens, cu([40, 0, 0]))).tolist() == [1, 1, 1]
+    lens[0] = 40
+    assert host(c.fork(table, lens, cu([0]), cu([1]))).tolist() == [1]
+    c.release(table, lens, cu([1]), cu([20]))
+    before = host(table)
+    assert host(c.reserve(table, lens, cu([1, 1, 0]))).tolist() == [1, 0, 1]
+    assert host(c.reserve(table, lens, cu([1, 0, 0]))).tolist() == [1, 1, 1]
+    assert (host(table) == before).all()
+    assert host(c.fork(table, lens, cu([1]), cu([2]))).tolist() == [1]
+    assert host(c.reserve(table, lens, cu([0, 1, 30]))).tolist() == [1, 0, 1]
+    t = host(table)
+    assert t[2, 0] == t[0, 0] and t[2, 1] not in (t[0, 1], -1) and (t[2, 2:4] >= 0).all()
+    c.release(table, lens, cu([0]), cu([0]))
+    assert host(c.reserve(table, lens, cu([0, 1, 0]))).tolist() == [1, 1, 1]
+    c.check()
+
+
 def test_copy_pages():
     g = np.random.default_rng(7)
     Hkv, dh, P, layers, pages = 3, 64, 32, 2, 40
