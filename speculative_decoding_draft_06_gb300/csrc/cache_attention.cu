@@ -715,6 +715,7 @@ extern "C" dartree_status dartree_cache_attention(const dartree_cache* cache, in
   p.scale_log2 = scale * 1.4426950408889634f * p.c.k_scale;
   p.O = static_cast<uint16_t*>(O);
   p.err = err;
+  if (!(p.scale_log2 <= 3.0e38f)) return cache_fail(DARTREE_ERR_INVALID_ARG, "scale times k_scale is too large");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (!p.err) e = cudaGetSymbolAddress(reinterpret_cast<void**>(&p.err), g_cache_err);

@@ -227,6 +227,81 @@ def test_captured_calls_and_other_streams():
     cache.check()
 
 
+def tree_call(g, lens, n, B, Hq, Hkv, dh, P):
+    """A cache, queries and masks of trees of n nodes: what attention takes."""
+    trees = [I.random_tree(g, B, max(1, int(k))) for k in n]
+    masks = np.stack([ancestor_mask(t["parent"], int(k), B) for t, k in zip(trees, n)])
+    cache, table, vals = filled(g, lens, n, P, Hkv, dh)
+    q = torch.from_numpy(g.standard_normal((len(lens), B + 1, Hq, dh)) * 2).to(torch.bfloat16).cuda()
+    return cache, table, vals, masks, torch.from_numpy(masks.view(np.int32)).cuda(), q
+
+
+@pytest.mark.parametrize("Hq,Hkv,dh", [(8, 2, 128), (3, 1, 64), (8, 1, 128)])
+def test_rows_behind_whole_tiles(Hq, Hkv, dh):
+    """Trees whose rows end around multiples of 128, some with up to eight rows
+    left over, of different lengths in one call and each alone without sizes."""
+    g, gr, P, B = np.random.default_rng(Hq + dh), Hq // Hkv, 32, 170
+    n = sorted({max(0, min(B, t * 128 // gr + d - 1)) for t in (1, 2, 4) for d in (-1, 0, 1, 2, 3, 5, 9)})
+    lens = g.integers(0, 700, len(n))
+    lens[::5] = 0
+    n = np.array(n)
+    cache, table, vals, masks, m, q = tree_call(g, lens, n, B, Hq, Hkv, dh, P)
+    out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    cache.attention(0, q, cu(table), cu(lens), mask=m, n_nodes=cu(n), max_len=int((lens + n).max()), out=out)
+    cache.check()
+    O = host(out.double())
+    check_rows(O, host(q.double()), lens, n, masks, vals, dh ** -0.5)
+    for r in range(len(n)):
+        assert (O[r, n[r] + 1:] == 5.0).all()
+        if n[r] > 0 and n[r] % 32 == 0:
+            k = int(n[r])
+            alone = cache.attention(0, q[r:r + 1, :k + 1].contiguous(), cu(table[r:r + 1]), cu(lens[r:r + 1]),
+                                    mask=m[r:r + 1, :k, :k // 32].contiguous(), max_len=int(lens[r]) + k)
+            check_rows(host(alone.double()), host(q[r:r + 1].double()), lens[r:r + 1], n[r:r + 1], masks[r:r + 1],
+                       vals[r:r + 1], dh ** -0.5)
+    cache.check()
+
+
+@pytest.mark.parametrize("R", [255, 257, 300])
+def test_trees_of_many_requests(R):
+    g = np.random.default_rng(R)
+    B, Hq, Hkv, dh, P = 5, 4, 1, 64, 16
+    lens, n = g.integers(-1, 150, R), g.integers(0, B + 1, R)
+    cache, table, vals, masks, m, q = tree_call(g, lens, n, B, Hq, Hkv, dh, P)
+    out = cache.attention(0, q, cu(table), cu(lens), mask=m, n_nodes=cu(n), max_len=160)
+    cache.check()
+    check_rows(host(out.double()), host(q.double()), lens, n, masks, vals, dh ** -0.5)
+
+
+def test_trees_on_two_streams_and_in_graphs():
+    """Two streams and two graphs, each call with its own workspace: the same
+    bits as alone."""
+    g = np.random.default_rng(12)
+    lens, n = np.array([2500]), np.array([64])
+    cache, table, vals, masks, m, q = tree_call(g, lens, n, 64, 16, 4, 128, 64)
+    t, ln, nn = cu(table), cu(lens), cu(n)
+    call = lambda s=None: cache.attention(0, q, t, ln, mask=m, n_nodes=nn, max_len=2564, stream=s)  # noqa: E731
+    want = call()
+    check_rows(host(want.double()), host(q.double()), lens, n, masks, vals, 128 ** -0.5)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [call(s) for _ in range(20) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for gr in graphs:
+        with torch.cuda.graph(gr):
+            outs.append(call())
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, gr in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                gr.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    cache.check()
+
+
 def test_verification_steps_over_the_cache():
     """Three steps of one layer, as a user runs them: build a tree, reserve
     pages, append the root's and the nodes' keys and values, attend, sample
