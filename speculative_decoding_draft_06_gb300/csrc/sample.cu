@@ -27,8 +27,8 @@
 // Bound, in rows that the candidates decide, by the passes' instructions (6 a
 // token) and the list's chain of steps; in the others by 35 to 100 a token.
 // 2064 rows of 151936 bf16 logits: greedy 153 us (4.1 TB/s, 61% of a copy),
-// top-k 50 213, top-p 0.9 at T = 0.7 390, top-p 0.95 at T = 1 (85% of these
-// rows by whole rows) 1300, no cut 620; 129 rows in fp32: 24, 37, 46, 193, 108;
+// top-k 50 215, top-p 0.9 at T = 0.7 360, top-p 0.95 at T = 1 (85% of these
+// rows by whole rows) 1090, no cut 670; 129 rows in fp32: 24, 37, 46, 193, 112;
 // 17 rows of 32000 20 us, latency.
 //
 // A cut: a histogram of counts and masses over 1024 classes of -log2 w
@@ -119,6 +119,7 @@ struct Smem {
       unsigned count[kBins];
     };
     unsigned long long weight[2 * kTable];
+    unsigned codes[2 * kTable];
   };
   unsigned long long list[kList];
   union {
@@ -664,56 +665,243 @@ __device__ void all_classes(const S& s, unsigned* count, unsigned long long* mas
   __syncthreads();
 }
 
-// f(logit, index, weight) for the row's logits above -inf, in no particular
-// order; the classes' memory is used.  bf16 logits near the largest are few
-// different values: the weights of kTable codes downward from it, and of
-// kTable negative ones from -1/4 (or from it, if that is negative), come from
-// a table (weight44 is some 70 instructions: 2064 rows of 151936 without cuts
-// take 610 us, 1050 without the table).
+// bf16 logits near the largest are few different values: kTable codes downward
+// from it and kTable negative ones from -1/4 (or from it, if that is lower)
+// have places, in descending order.  What lies between the two and what lies
+// below them has none.
+// (Behind the last place of an extreme largest logit lies -inf: weight 0.)
+struct Codes {
+  int top, neg0;
+  __device__ __forceinline__ explicit Codes(float t) {
+    top = __float_as_int(t) >> 16;
+    neg0 = max(0x3E80, top < 0 ? top & 0x7FFF : 0);
+  }
+  // the place or -1
+  __device__ __forceinline__ int place(float x) const {
+    const int b = __float_as_int(x) >> 16;
+    const int j = b < 0 ? (b & 0x7FFF) - neg0 : top - b;
+    return static_cast<unsigned>(j) < kTable ? j + (b < 0 ? kTable : 0) : -1;
+  }
+  // x without a place: whether it lies below them all
+  __device__ __forceinline__ bool below(float x) const {
+    const int b = __float_as_int(x) >> 16;
+    return b < 0 && (b & 0x7FFF) >= neg0;
+  }
+  // whether zero has no place (its two codes would be two logits)
+  __device__ __forceinline__ bool sound() const { return top >= kTable || top < 0; }
+  __device__ __forceinline__ float value(int j) const {  // (-inf behind the last)
+    const int code = j < kTable ? max(top - j, 0) : 0x8000 | min(neg0 + j - kTable, 0x7F80);
+    return bf16_bits_to_float(static_cast<uint16_t>(code));
+  }
+  __device__ __forceinline__ unsigned long long weight(const Weights& wt, int j) const {
+    const float x = value(j);
+    return x > -INFINITY && x <= wt.top ? wt.weight44(x) : 0ull;
+  }
+};
+
+// coded(x, index, place) and other(x, index) for the row's bf16 logits, in no
+// particular order, but for -inf and NaN without a place.
+template <typename S, typename F, typename G>
+__device__ __forceinline__ void each_code(const S& s, const Codes& c, F coded, G other) {
+  using E = typename S::Elem;
+  constexpr int kPer = Row<E>::kPer;
+  const int lane = threadIdx.x & 31;
+  auto one = [&](float x, int i) {
+    const int j = c.place(x);
+    if (j >= 0) coded(x, i, j);
+    else if (x > -INFINITY) other(x, i);
+  };
+  if (s.first && lane < s.row.head) one(logit<E>(s.row.src, lane), lane);
+  const int rest = s.row.index(s.row.units);
+  if (s.last && lane < s.row.V - rest) one(logit<E>(s.row.src, rest + lane), rest + lane);
+  each_unit(s.row, s.ub, s.ue, [&](uint4 v, int u) {
+    float x[kPer];
+    unpack<E>(v, x);
+    unsigned others = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int j = c.place(x[k]);
+      if (j >= 0) coded(x[k], s.row.index(u) + k, j);
+      else others |= 1u << k;
+    }
+    for (; others; others &= others - 1) {
+      const int k = __ffs(others) - 1;
+      const uint32_t pair = k < 4 ? (k < 2 ? v.x : v.y) : (k < 6 ? v.z : v.w);
+      const float y = __uint_as_float(k & 1 ? pair & 0xFFFF0000u : pair << 16);
+      if (y > -INFINITY) other(y, s.row.index(u) + k);
+    }
+  });
+}
+
+// f(logit, index, weight) for the row's logits that have a weight (and some
+// without), in no particular order; the classes' memory is used.  The weights of the codes that have
+// places come from a table (weight44 is some 70 instructions: 2064 rows of
+// 151936 without cuts take 670 us, 1050 without the table).
 template <typename S, typename F>
 __device__ __forceinline__ void each_weight(const S& s, const Weights& wt, F f) {
-  using E = typename S::Elem;
-  if constexpr (sizeof(E) == 4) {
+  if constexpr (sizeof(typename S::Elem) == 4) {
     s.each_value([&](float x, int i) { f(x, i, wt.weight44(x)); });
   } else {
-    const int top = __float_as_int(wt.top) >> 16, neg0 = max(0x3E80, top < 0 ? top & 0x7FFF : 0);
-    for (int j = threadIdx.x; j < 2 * kTable; j += kThreads) {
-      const int code = j < kTable ? max(top - j, 0) : (neg0 + j - kTable) | 0x8000;
-      const float x = bf16_bits_to_float(static_cast<uint16_t>(code));
-      s.sm.weight[j] = x > -INFINITY ? wt.weight44(x) : 0ull;
-    }
+    const Codes c(wt.top);
+    for (int j = threadIdx.x; j < 2 * kTable; j += kThreads) s.sm.weight[j] = c.weight(wt, j);
     __syncthreads();
-    // the table's entry or -1
-    auto entry = [&](float x) {
-      const int b = __float_as_int(x) >> 16;
-      const int j = b < 0 ? (b & 0x7FFF) - neg0 : top - b;
-      return static_cast<unsigned>(j) < kTable ? j + (b < 0 ? kTable : 0) : -1;
-    };
-    constexpr int kPer = Row<E>::kPer;
-    const int lane = threadIdx.x & 31;
-    auto one = [&](float x, int i) {
-      if (x > -INFINITY) f(x, i, wt.weight44(x));
-    };
-    if (s.first && lane < s.row.head) one(logit<E>(s.row.src, lane), lane);
-    const int rest = s.row.index(s.row.units);
-    if (s.last && lane < s.row.V - rest) one(logit<E>(s.row.src, rest + lane), rest + lane);
-    each_unit(s.row, s.ub, s.ue, [&](uint4 v, int u) {
-      float x[kPer];
-      unpack<E>(v, x);
-      unsigned others = 0;
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int j = entry(x[k]);
-        if (j >= 0) f(x[k], s.row.index(u) + k, s.sm.weight[j]);
-        else if (x[k] > -INFINITY) others |= 1u << k;
-      }
-      for (; others; others &= others - 1) {
-        const int k = __ffs(others) - 1;
-        const uint32_t pair = k < 4 ? (k < 2 ? v.x : v.y) : (k < 6 ? v.z : v.w);
-        one(__uint_as_float(k & 1 ? pair & 0xFFFF0000u : pair << 16), s.row.index(u) + k);
-      }
-    });
+    each_code(s, c, [&](float x, int i, int j) { f(x, i, s.sm.weight[j]); },
+              [&](float x, int i) { f(x, i, wt.weight44(x)); });
   }
+}
+
+// top-k and top-p of a bf16 row by counts of its codes: they and the codes'
+// weights give the running counts and masses exactly, so a cut falls on a code
+// and a number of its ties, the first in index order.  Left are that value
+// (*value), the kept tokens' mass per warp in wsum and the number of ties a
+// warp keeps in wtot.  False where a cut falls on a logit without a place.
+// (2064 rows of 151936, top-p 0.95: at T = 1 1090 us, with the approximate
+// classes below 1300; at T = 1.3 1110 and 2120, where many rows had more tied
+// tokens about the cut than the list holds.)
+template <typename S>
+__device__ bool code_cuts(const S& s, const Weights& wt, const Rule& rule, float* value) {
+  Smem& sm = s.sm;
+  Ctl& ctl = s.ls.ctl;
+  const int tid = threadIdx.x, lane = tid & 31, warps = s.cl * kWarps;
+  constexpr int kN = 2 * kTable + 2, kPer = (kN + kThreads - 1) / kThreads;
+  const Codes code(wt.top);
+  if (!code.sound()) return false;
+  float v = -INFINITY;
+  {
+    for (int j = tid; j < 2 * kTable; j += kThreads) sm.codes[j] = 0;
+    __syncthreads();
+    unsigned between = 0, below = 0;
+    unsigned long long between_m = 0, below_m = 0;
+    each_code(s, code, [&](float, int, int j) { atomicAdd(&sm.codes[j], 1u); },
+              [&](float x, int) {
+                const unsigned long long w = wt.weight44(x);
+                const bool low = code.below(x);
+                between += !low;
+                below += low;
+                between_m += low ? 0ull : w;
+                below_m += low ? w : 0ull;
+              });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      between += __shfl_xor_sync(kFullMask, between, o);
+      below += __shfl_xor_sync(kFullMask, below, o);
+      between_m += __shfl_xor_sync(kFullMask, between_m, o);
+      below_m += __shfl_xor_sync(kFullMask, below_m, o);
+    }
+    if (lane == 0) {  // (the list is not in use)
+      unsigned long long* to = &s.ls.list[4 * s.gw];
+      to[0] = between;
+      to[1] = between_m;
+      to[2] = below;
+      to[3] = below_m;
+    }
+    s.sync();
+    if (s.lead) {
+      // entries in order: the positive codes, what lies between, the negative
+      // codes, what lies below
+      unsigned cs[kPer], c = 0;
+      unsigned long long ms[kPer], m = 0;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        const int e = tid * kPer + q;
+        cs[q] = 0;
+        ms[q] = 0;
+        if (e == kTable || e == kN - 1) {
+          for (int w = 0; w < warps; ++w) {
+            cs[q] += static_cast<unsigned>(sm.list[4 * w + (e == kN - 1 ? 2 : 0)]);
+            ms[q] += sm.list[4 * w + (e == kN - 1 ? 3 : 1)];
+          }
+        } else if (e < kN) {
+          const int j = e < kTable ? e : e - 1;
+          for (int r = 0; r < s.cl; ++r) cs[q] += at_rank(&sm, r)->codes[j];
+          ms[q] = cs[q] ? cs[q] * code.weight(wt, j) : 0ull;
+        }
+        c += cs[q];
+        m += ms[q];
+      }
+      unsigned c0 = 0u - c;
+      unsigned long long m0 = 0ull - m;
+      block_scan(sm, c, m);
+      c0 += c;
+      m0 += m;  // what lies before the thread's entries
+      if (tid == kThreads - 1) {
+        sm.picked = -1;
+        sm.picked_c = c;
+        sm.picked_m = m;
+      }
+      __syncthreads();
+      unsigned long long Z = sm.picked_m;
+      bool ok = true;
+      // the entry that a cut falls on, and how many of its tokens are kept
+      auto fall = [&](bool by_count, unsigned long long target) {
+        unsigned bc = c0;
+        unsigned long long bm = m0;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+          if (by_count ? (bc < target && target <= bc + cs[q]) : (bm < target && target <= bm + ms[q])) {
+            const int e = tid * kPer + q;
+            const unsigned long long w = max(ms[q] / cs[q], 1ull);
+            const unsigned n = by_count ? static_cast<unsigned>(target - bc)
+                                        : static_cast<unsigned>((target - bm + w - 1) / w);
+            sm.picked = e == kTable || e == kN - 1 ? -2 : e < kTable ? e : e - 1;
+            sm.picked_n = n;
+            sm.picked_m = ms[q] ? bm + n * w : bm;  // (an entry without a place: not used)
+          }
+          bc += cs[q];
+          bm += ms[q];
+        }
+        __syncthreads();
+        if (sm.picked == -2) ok = false;
+        Z = sm.picked_m;
+        __syncthreads();
+      };
+      const unsigned all = sm.picked_c;
+      __syncthreads();
+      if (rule.use_k && all > static_cast<unsigned>(rule.k)) fall(true, static_cast<unsigned long long>(rule.k));
+      if (rule.use_p && ok && Z > 0) fall(false, rule.tp > 0.f ? ceil_share(rule.tp, Z) : 1ull);
+      if (tid == 0) {
+        ctl.bin = sm.picked;
+        ctl.left = sm.picked < 0 ? 0 : sm.picked_n;
+        ctl.refine = ok ? 0 : 1;
+      }
+    }
+    s.sync();
+    if (ctl.refine) return false;
+    if (ctl.bin >= 0) v = code.value(ctl.bin);
+  }
+  // the weights of what is above the cut's code, and its ties
+  for (int j = tid; j < 2 * kTable; j += kThreads) sm.weight[j] = code.value(j) > v ? code.weight(wt, j) : 0ull;
+  __syncthreads();
+  unsigned long long sum = 0;
+  unsigned ties = 0;
+  each_code(s, code,
+            [&](float x, int, int j) {
+              sum += sm.weight[j];
+              ties += x == v;
+            },
+            [&](float x, int) { sum += x > v ? wt.weight44(x) : 0ull; });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(kFullMask, sum, o);
+    ties += __shfl_xor_sync(kFullMask, ties, o);
+  }
+  if (lane == 0) {
+    s.ls.wsum[s.gw] = sum;
+    s.ls.wtot[s.gw] = ties;
+  }
+  s.sync();
+  if (s.lead && tid == 0 && v > -INFINITY) {
+    const unsigned long long w = wt.weight44(v);
+    unsigned long long left = ctl.left;
+    for (int k = 0; k < warps; ++k) {
+      const unsigned long long n = min(left, sm.wtot[k]);
+      sm.wsum[k] += n * w;
+      sm.wtot[k] = n;
+      left -= n;
+    }
+  }
+  *value = v;
+  return true;
 }
 
 // The kept tokens' mass per warp, left in the leader's wsum.
@@ -963,9 +1151,13 @@ __device__ void whole_row(const SampleParams& p, Smem& sm, Smem& ls, const E* sr
     }
     return;
   }
-  if (rule.use_k && k_list(s, p, row, wt, rule)) return;
   unsigned long long keep = 0;
-  const bool quick = !rule.use_k && !(rule.mp > 0.f) && nucleus(s, wt, rule, keep);
+  float value = 0.f;
+  bool coded = false;  // kept are the logits above `value` and the first of its ties
+  if (rule.use_k && rule.k <= kList && k_list(s, p, row, wt, rule)) return;
+  if constexpr (sizeof(E) == 2)
+    coded = (rule.use_k || rule.use_p) && !(rule.mp > 0.f) && isfinite(wt.top) && code_cuts(s, wt, rule, &value);
+  const bool quick = coded || (!rule.use_k && !(rule.mp > 0.f) && nucleus(s, wt, rule, keep));
   if (!quick) {
     keep = rule.mp > 0.f ? min_p_key(wt, rule.mp) : 0;
     if (rule.use_k || rule.use_p) {
@@ -1008,12 +1200,30 @@ __device__ void whole_row(const SampleParams& p, Smem& sm, Smem& ls, const E* sr
     // lanes, the rest
     const unsigned long long t = ls.ctl.left, total = ls.ctl.total;
     unsigned long long before = 0;
+    int ties = coded ? static_cast<int>(ls.wtot[gw]) : 0;  // that are still kept
     constexpr int kPer = Row<E>::kPer;
     auto step = [&](const float (&x)[kPer], int i0, int n) {  // the lane's n tokens from i0; true: found
       unsigned long long w[kPer], sum = 0;
+      int tie = ties;  // that are still kept from the lane's first on
+      if (coded) {
+        int own = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) own += k < n && x[k] == value;
+        int inc = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(kFullMask, inc, o);
+          if (lane >= o) inc += y;
+        }
+        tie -= inc - own;
+        ties -= __shfl_sync(kFullMask, inc, 31);
+      }
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
-        w[k] = k < n && x[k] > -INFINITY && key50(x[k], i0 + k) >= keep ? wt.weight44(x[k]) : 0ull;
+        bool in = k < n && x[k] > -INFINITY;
+        if (coded) in = in && (x[k] > value || (x[k] == value && tie-- > 0));
+        else in = in && key50(x[k], i0 + k) >= keep;
+        w[k] = in ? wt.weight44(x[k]) : 0ull;
         sum += w[k];
       }
       unsigned long long inc = sum;
@@ -1154,7 +1364,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // requests that need their whole rows' weights first: their rows take several
   // times as long as the others', which then fill the SMs (2064 rows of 151936
-  // in 129 requests of all kinds: an eighth to a third less time than in the rows' order)
+  // in 16 requests of all kinds: an eighth to a third less time than in the rows'
+  // order)
   int row = blockIdx.x / cl;
   const int requests = p.rows / p.rows_per_req;
   if (requests > 1 && requests <= kBins && requests * p.rows_per_req == p.rows) {

@@ -93,6 +93,25 @@ def test_ties(V):
             check(torch.from_numpy(x).cuda(), u, 6, None, k, p, None)
 
 
+@pytest.mark.parametrize("V", [40, 5000, 70001])
+@pytest.mark.parametrize("centre,spread", [(0.0, 0.5), (12.0, 3.0), (-8.0, 2.0), (-0.01, 0.005), (300.0, 100.0)])
+def test_bf16_cuts_among_ties(V, centre, spread):
+    """Top-k and top-p of whole rows that fall among many equal logits, rows
+    that start at any address."""
+    g = np.random.default_rng(V)
+    x = torch.from_numpy(g.standard_normal((4, V + 5)) * spread + centre).to(torch.bfloat16)
+    x[1] = (x[1].float() * 4).round().to(torch.bfloat16) / 4
+    x[2, ::7] = x[2, 3]
+    x[3, ::5] = float("nan")
+    x[3, 1::5] = -float("inf")
+    u = g.random(4).astype(np.float32)
+    for off in (0, 1, 5):
+        t = x.cuda()[:, off:off + V]
+        for T in (1.0, 5.0):
+            for k, p in ((V // 3, 1.0), (V - 2, 0.97), (V // 2, 0.6), (0, 0.9), (0, 0.999), (0, 1.0)):
+                check(t, u, 4, [T], [k], [p], None)
+
+
 @pytest.mark.parametrize("V", [9, 20000, 100000])
 def test_the_two_zeros_are_equal(V):
     g = np.random.default_rng(V)
