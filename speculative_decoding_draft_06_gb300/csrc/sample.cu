@@ -1117,6 +1117,8 @@ __device__ bool k_list(const S& s, const SampleParams& p, int row, const Weights
     __syncthreads();
     for (int w = 0; w < kWarps; ++w) least = min(least, sm.scan_m[w]);
     __syncthreads();
+    // (all of the row's tokens, or the first k and some: nothing else is kept)
+    if (b == kBins) least = static_cast<unsigned long long>(float_order(-INFINITY)) << kIdxBits;
     const bool ok = from_list<typename S::Elem>(p, sm, row, n, least, 0, 0, wt, rule);
     if (threadIdx.x == 0) {
       ctl.refine = ok ? 0 : 1;
@@ -1289,7 +1291,8 @@ __device__ bool from_list(const SampleParams& p, Smem& sm, int row, int n, unsig
   unsigned count;
   unsigned long long Z;
   all_classes(s, &count, &Z);
-  if (rule.use_k && count >= static_cast<unsigned>(rule.k)) {
+  // (count is that of the tokens with a weight; the list may hold k with fewer)
+  if (rule.use_k && n >= rule.k) {
     if (count > static_cast<unsigned>(rule.k)) {
       if (cut(s, wt, true, static_cast<unsigned long long>(rule.k), keep, &Z) && rule.use_p) fill_bins(s, wt, keep);
     }
