@@ -802,19 +802,27 @@ __device__ bool code_cuts(const S& s, const Weights& wt, const Rule& rule, float
       unsigned cs[kPer], c = 0;
       unsigned long long ms[kPer], m = 0;
 #pragma unroll
+      for (int q = 0; q < kPer; ++q) cs[q] = 0;
+      for (int r = 0; r < s.cl; ++r) {
+        const unsigned* from = at_rank(&sm, r)->codes;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+          const int e = tid * kPer + q;
+          if (e < kN - 1 && e != kTable) cs[q] += from[e < kTable ? e : e - 1];
+        }
+      }
+#pragma unroll
       for (int q = 0; q < kPer; ++q) {
         const int e = tid * kPer + q;
-        cs[q] = 0;
         ms[q] = 0;
         if (e == kTable || e == kN - 1) {
+#pragma unroll 8
           for (int w = 0; w < warps; ++w) {
             cs[q] += static_cast<unsigned>(sm.list[4 * w + (e == kN - 1 ? 2 : 0)]);
             ms[q] += sm.list[4 * w + (e == kN - 1 ? 3 : 1)];
           }
-        } else if (e < kN) {
-          const int j = e < kTable ? e : e - 1;
-          for (int r = 0; r < s.cl; ++r) cs[q] += at_rank(&sm, r)->codes[j];
-          ms[q] = cs[q] ? cs[q] * code.weight(wt, j) : 0ull;
+        } else if (cs[q]) {
+          ms[q] = cs[q] * code.weight(wt, e < kTable ? e : e - 1);
         }
         c += cs[q];
         m += ms[q];
@@ -954,12 +962,20 @@ __device__ bool nucleus(const S& s, const Weights& wt, const Rule& rule, unsigne
     constexpr int kPer = kBins / kThreads;
     float ms[kPer], m = 0.f;
     float cs[kPer];  // tokens, about
+    static_assert(kPer == 4, "a thread's classes are one 16-byte load");
+    unsigned units[kPer] = {0, 0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < kMaxCl; ++q) {  // (the CTAs' loads together)
+      if (q >= s.cl) continue;
+      const uint4 x = *reinterpret_cast<const uint4*>(&at_rank(&sm, q)->mass_lo[tid * kPer]);
+      units[0] += x.x;
+      units[1] += x.y;
+      units[2] += x.z;
+      units[3] += x.w;
+    }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      unsigned none;
-      unsigned long long units;
-      s.sums(tid * kPer + j, &none, &units);
-      cs[j] = static_cast<float>(units) * (1.f / kMassUnit);
+      cs[j] = static_cast<float>(units[j]) * (1.f / kMassUnit);
       ms[j] = cs[j] * ex2(static_cast<float>(tid * kPer + j) * (-1.f / kBinsPer2));
       m += ms[j];
     }
@@ -1685,7 +1701,7 @@ extern "C" dartree_status dartree_sample(const void* logits, int32_t bf16, int64
   const SampleParams p{logits, row_stride, V, rows, rows_per_req, temperature, top_k, top_p, min_p, u, token, prob};
   // one cluster per row: as many CTAs as the SMs hold (four each)
   int cl = 1;
-  while (cl < kMaxCl && static_cast<long long>(rows) * cl * 2 <= 608 && V / cl > 8192) cl *= 2;
+  while (cl < kMaxCl && static_cast<long long>(rows) * cl * 2 <= 608 && V / cl > 4096) cl *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (static_cast<long long>(rows) * cl > 0x7FFFFFFFll) return cache_fail(DARTREE_ERR_UNSUPPORTED, "too many rows");
   const dim3 grid(static_cast<unsigned>(rows) * cl);
