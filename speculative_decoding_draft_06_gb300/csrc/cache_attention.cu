@@ -457,7 +457,7 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
       float* dst = cache_part_row(p, r, hk, 0, split, row);
 #pragma unroll
       for (int e = 0; e < kE; e += 2)
-        *reinterpret_cast<float2*>(dst + 2 + lane * kE + e) = make_float2(v[e], v[e + 1]);
+        *reinterpret_cast<float2*>(dst + kPartHead + lane * kE + e) = make_float2(v[e], v[e + 1]);
       if (lane == 0) *reinterpret_cast<float2*>(dst) = make_float2(M, L);
     } else {
       const float inv = L > 0.f ? p.c.v_scale / L : 0.f;
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(256) k_cache_attention_join(const CacheAttnPar
   if (on) {
     const int mt = q / p.tile_rows;
     const int ns = (row_tile_keys(p, sp, mt) + p.split_tiles - 1) / p.split_tiles;  // splits that had keys
-    const size_t step = static_cast<size_t>(p.tile_rows) * (DH + 2);
+    const size_t step = static_cast<size_t>(p.tile_rows) * (DH + kPartHead);
     const float* src = cache_part_row(p, r, hk, mt, 0, q - mt * p.tile_rows);
     for (int s = w + lane * W; s < ns; s += 32 * W) M = fmaxf(M, src[s * step]);
 #pragma unroll
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(256) k_cache_attention_join(const CacheAttnPar
       L += ml.y * f;
 #pragma unroll
       for (int e = 0; e < kE; e += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(src + s * step + 2 + lane * kE + e);
+        const float2 x = *reinterpret_cast<const float2*>(src + s * step + kPartHead + lane * kE + e);
         v[e] += x.x * f;
         v[e + 1] += x.y * f;
       }
@@ -635,7 +635,7 @@ Plan plan_rows(bool tree, long long rows, int R, int max_len, int Hkv, int dh, i
   pl.cluster = !tree && pl.n_split > 1 && pl.n_split <= kMaxCluster &&
                (ctas * pl.n_split <= sms * 6 || most_splits == kMaxCluster);
   pl.work = pl.n_split > 1 && !pl.cluster
-                ? static_cast<size_t>(ctas) * pl.n_split * pl.tile_rows * (dh + 2) * sizeof(float)
+                ? static_cast<size_t>(ctas) * pl.n_split * pl.tile_rows * (dh + kPartHead) * sizeof(float)
                 : 0;
   return pl;
 }

@@ -30,7 +30,7 @@ struct CacheAttnParams {
   int tail;                  // the few-rows kernel works on the rows behind the whole tiles
   float scale_log2;          // scale * log2(e) * k_scale
   uint16_t* O;               // [R][B+1][Hq][dh]
-  float* part;               // [R][Hkv][m_tiles][n_split][tile_rows][dh + 2] (n_split > 1)
+  float* part;               // [R][Hkv][m_tiles][n_split][tile_rows][dh + kPartHead] (n_split > 1)
   int* err;
 };
 
@@ -115,11 +115,12 @@ __device__ __forceinline__ size_t cache_out_row(const CacheAttnParams& p, int r,
   return ((static_cast<size_t>(r) * (p.B + 1) + nd) * p.Hq + hk * p.g + (q - nd * p.g)) * p.c.dh;
 }
 
-// Row `row` of row tile mt and one split in the workspace: (m, l) and dh
-// unnormalised outputs.
+// Row `row` of row tile mt and one split in the workspace: (m, l), and behind
+// kPartHead the dh unnormalised outputs (rows of 16-byte pieces).
+constexpr int kPartHead = 4;
 __device__ __forceinline__ float* cache_part_row(const CacheAttnParams& p, int r, int hk, int mt, int split, int row) {
   const size_t tile = ((static_cast<size_t>(r) * p.c.Hkv + hk) * p.m_tiles + mt) * p.n_split + split;
-  return p.part + (tile * p.tile_rows + row) * (p.c.dh + 2);
+  return p.part + (tile * p.tile_rows + row) * (p.c.dh + kPartHead);
 }
 
 // The tensor-core kernel of many rows (cache_tree.cu).

@@ -27,12 +27,13 @@
 //
 // Bound by the latency of a step's chain (scores, maximum, weights, product)
 // at two row tiles per SM: 32 trees of 65 rows over up to 2500 tokens, 32 heads
-// over 8 of 128: 83 us, 640 TFLOP/s, the tensor pipe active 33% of the time,
+// over 8 of 128: 76 us, 700 TFLOP/s, the tensor pipe active 33% of the time,
 // issue 0.55 (the exponentials and the conversions of the codes alone would
-// take 29 us); one of 129 rows over 4099 tokens: 32 us.  Steps for the 32 (the
+// take 29 us); one of 129 rows over 4099 tokens: 28 us.  Steps for the 32 (the
 // one): one row tile 181 us (41); two, and codes expanded from registers 121
 // (53); scores a step of 64 keys ahead and two issuers 85 (47); leftover rows in
-// a launch beside 89 (43); two threads per row 83 (35).  A polynomial for part
+// a launch beside 89 (43); two threads per row 83 (35); queries loaded by the
+// softmax warps beside the first codes, output addresses out of the loop 77 (31).  A polynomial for part
 // of the exponentials and row tiles that take turns were slower.
 #include <type_traits>
 
@@ -43,6 +44,7 @@ namespace {
 
 constexpr int kMRows = 128, kKeys = 128, kStepKeys = 64;
 constexpr int kExpandWarp0 = 16, kExpandWarps = 8, kMmaWarp0 = 24;
+constexpr int kLoadWarps = 8;  // that load a row tile's queries: its softmax warps
 constexpr int kTreeThreads = 26 * 32;
 constexpr int kStages = 2;
 // (a tile's keys are expanded after all scores of the tile two before are
@@ -205,7 +207,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   uint64_t* p_full = s_full + 4;         // [row tile][buffer]
   uint64_t* o_full = p_full + 4;         // [row tile][buffer]: P V of a step has landed
   uint64_t* mma_done = o_full + 4;       // [row tile]: everything issued has
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 2);
+  uint64_t* q_full = mma_done + 2;       // [row tile]: the queries are there
+  constexpr int kBarriers = 4 * kStages + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ float s_fac[2 * kMRows], s_top[2][2 * kMRows];  // of the rows: factor; by half: maximum, sum
   __shared__ __align__(16) uint8_t s_valid[kValid][kKeys / 8];  // bit k of a tile: key k is there
@@ -244,59 +248,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   const int two = rows > kMRows ? 2 : 1;
 
   if (warp == kMmaWarp0) tmem_alloc<kTmemCols>(tmem_slot);
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&k_full[s], kExpandWarps / 2);
-      mbar_init(&k_empty[s], two);
-      mbar_init(&v_full[s], kExpandWarps / 2);
-      mbar_init(&v_empty[s], two);
-    }
-    for (int i = 0; i < 2; ++i) {
-      const int n = min(rows - i * kMRows, kMRows);  // one arrival per warp with rows
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(&s_full[2 * i + b], 1);
-        mbar_init(&p_full[2 * i + b], n > 0 ? 2 * ((n + 31) / 32) : 1);
-        mbar_init(&o_full[2 * i + b], 1);
+  if (warp == 0) {
+    static_assert(kStages == 2 && kBarriers <= 32, "a lane per barrier");
+    if (lane < kBarriers) {
+      int count = 1;                                      // s_full, o_full, mma_done
+      if (lane < 8) count = lane & 2 ? two : kExpandWarps / 2;  // k_full, k_empty, v_full, v_empty
+      if (lane >= 12 && lane < 16) {                      // p_full: one arrival per warp with rows
+        const int n = min(rows - ((lane - 12) >> 1) * kMRows, kMRows);
+        if (n > 0) count = 2 * ((n + 31) / 32);
       }
-      mbar_init(&mma_done[i], 1);
+      if (lane >= 22) count = kLoadWarps;                 // q_full
+      mbar_init(&k_full[lane], count);
+      fence_mbar_init();
     }
-    *abort_flag = 0;
-    fence_mbar_init();
-    if (split == 0 && hk == 0 && mt == 0 && static_cast<long long>(p.lens[r]) + sp.n > p.max_len)
-      atomicOr(p.err, DT_ERR_BAD_INDEX);
-  }
-  // the queries, as fp16 rows scaled by a power of two to at most 2 each
-  if (threadIdx.x < two * kMRows) {
-    const int row = threadIdx.x, q = q0 + row;
-    const bool on = row < rows;
-    const int node = on ? q / p.g : 0;
-    const uint4* src = reinterpret_cast<const uint4*>(
-        p.Q + (static_cast<size_t>(r) * (p.B + 1) + node) * p.q_stride +
-        static_cast<size_t>(hk * p.g + (on ? q - node * p.g : 0)) * DH);
-    float top = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < DH / 8; ++k) {
-      const uint4 w = on ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[j] << 16)), fabsf(__uint_as_float(x[j] & 0xFFFF0000u))));
-    }
-    float down;
-    s_fac[row] = row_exponent(top, p.scale_log2, &down);
-    uint8_t* dst = smem + (row >> 7) * L::kQTile;
-#pragma unroll 4
-    for (int k = 0; k < DH / 8; ++k) {  // (once more: the row is in L1)
-      const uint4 w = on ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-      uint32_t y[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        y[j] = pack_f16(__uint_as_float(x[j] << 16) * down, __uint_as_float(x[j] & 0xFFFF0000u) * down);
-      *reinterpret_cast<uint4*>(dst + (k >> 3) * (kMRows * 128) + sw128(row & 127, k & 7)) =
-          make_uint4(y[0], y[1], y[2], y[3]);
-    }
-    fence_async_smem();
+    if (lane == 0) *abort_flag = 0;
   }
   tc_fence_before();
   __syncthreads();
@@ -318,6 +283,47 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     }
     return __all_sync(kFullMask, ok) != 0;
   };
+
+  if (warp < two * kLoadWarps) {
+    // the queries, as fp16 rows scaled by a power of two to at most 2 each: a
+    // warp takes 16 rows, DH / 8 lanes a row, all loads before their use (a
+    // thread per row: 9400 cycles)
+    constexpr int kRowLanes = DH / 8, kRowsIt = 32 / kRowLanes, kIts = kMRows / kLoadWarps / kRowsIt;
+    const int k = lane % kRowLanes, first = warp * (kMRows / kLoadWarps) + lane / kRowLanes;
+    uint4 w[kIts];
+#pragma unroll
+    for (int j = 0; j < kIts; ++j) {
+      const int row = first + j * kRowsIt, q = q0 + row, node = row < rows ? q / p.g : 0;
+      w[j] = make_uint4(0, 0, 0, 0);
+      if (row < rows)
+        w[j] = __ldg(reinterpret_cast<const uint4*>(
+                         p.Q + (static_cast<size_t>(r) * (p.B + 1) + node) * p.q_stride +
+                         static_cast<size_t>(hk * p.g + (q - node * p.g)) * DH) + k);
+    }
+    uint8_t* dst = smem + (warp / kLoadWarps) * L::kQTile + (k >> 3) * (kMRows * 128);
+#pragma unroll
+    for (int j = 0; j < kIts; ++j) {
+      const int row = first + j * kRowsIt;
+      const uint32_t x[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+      float top = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xFFFF0000u))));
+#pragma unroll
+      for (int o = 1; o < kRowLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+      float down;
+      const float fac = row_exponent(top, p.scale_log2, &down);
+      if (k == 0) s_fac[row] = fac;
+      uint32_t y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        y[e] = pack_f16(__uint_as_float(x[e] << 16) * down, __uint_as_float(x[e] & 0xFFFF0000u) * down);
+      *reinterpret_cast<uint4*>(dst + sw128(row & 127, k & 7)) = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&q_full[warp / kLoadWarps]);
+  }
 
   if (warp >= kExpandWarp0 && warp < kMmaWarp0) {
     // ------------------------------------------------- codes to fp16 tiles
@@ -429,8 +435,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     const uint32_t s_col = tmem_base + static_cast<uint32_t>(i * kKeys);
     const uint32_t o_col = tmem_base + kColO + static_cast<uint32_t>(i * 128);
     const bool elected = elect_one();
-    bool go = true;
-    for (int u = -1; u < steps; ++u) {
+    bool go = wait_w(&q_full[i], 0);
+    for (int u = -1; go && u < steps; ++u) {
       if (u + 1 < steps) {  // S of step u + 1, over P(u - 1) once its product has landed
         const int f = (u + 1) >> 1, st = f % kStages, b = (u + 1) & 1;
         if (u >= 1 && !(go = wait_w(&o_full[2 * i + b], static_cast<uint32_t>((u - 1) >> 1) & 1u))) break;
@@ -486,13 +492,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     const int pair = 1 + i * 4 + quarter;  // the barrier of the two warps that share rows
     const int node = row < rows ? q / p.g : 0;
     const uint32_t* mrow = node >= 1 ? p.mask + (static_cast<size_t>(r) * p.B + node - 1) * p.words : nullptr;
+    bool go = wait_w(&q_full[i], 0);  // (the same in both warps after every barrier)
     const float fac = s_fac[row];
     float m = -INFINITY, l = 0.f;  // the row's reference (the same in both threads), this half's sum
     float limit = -INFINITY;       // the unscaled score above which the reference rises
-    bool go = true;                // (the same in both warps after every barrier)
     for (int u = 0; u < steps; ++u) {
       const int f = u >> 1, b = u & 1, key0 = t_beg * kKeys + u * kStepKeys + half * (kStepKeys / 2);
-      go = wait_w(&s_full[2 * i + b], static_cast<uint32_t>(f) & 1u);
+      go = go && wait_w(&s_full[2 * i + b], static_cast<uint32_t>(f) & 1u);
       tc_fence_after();
       const uint32_t there = *reinterpret_cast<const uint32_t*>(&s_valid[f % kValid][(2 * b + half) * 4]);
       uint32_t see = ~0u;
@@ -599,6 +605,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     float* stage = reinterpret_cast<float*>(smem + i * L::kQTile) + (warp & 7) * 32 * kPitch;
     static_assert(8 * 32 * kPitch * 4 <= L::kQTile, "the staged rows fit");
     const float mul = p.n_split > 1 ? 1.f : inv;
+    // the lane's pieces of rows k = lane / kLanes, + 32 / kLanes, ..: where they
+    // go, a chunk's step on (looked up once: in the loop 3000 cycles)
+    uint8_t* to[kLanes];
+#pragma unroll
+    for (int j = 0; j < kLanes; ++j) {
+      const int rr = i * kMRows + quarter * 32 + lane / kLanes + j * (32 / kLanes);
+      const int d = half * (DH / 2) + (lane % kLanes) * 4;
+      to[j] = nullptr;
+      if (rr < rows)
+        to[j] = p.n_split > 1 ? reinterpret_cast<uint8_t*>(cache_part_row(p, r, hk, mt, split, rr) + kPartHead + d)
+                              : reinterpret_cast<uint8_t*>(p.O + cache_out_row(p, r, hk, q0 + rr) + d);
+    }
 #pragma unroll 1
     for (int ch = 0; ch < 4; ++ch) {
       float x[kC];
@@ -614,22 +632,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
         *reinterpret_cast<float4*>(stage + lane * kPitch + k) =
             make_float4(x[k] * mul, x[k + 1] * mul, x[k + 2] * mul, x[k + 3] * mul);
       __syncwarp();
-      for (int k = lane / kLanes; k < 32; k += 32 / kLanes) {
-        const int rr = i * kMRows + quarter * 32 + k, d = half * (DH / 2) + ch * kC + (lane % kLanes) * 4;
-        if (rr >= rows) break;
-        const float4 v = *reinterpret_cast<const float4*>(stage + k * kPitch + (lane % kLanes) * 4);
+#pragma unroll
+      for (int j = 0; j < kLanes; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(stage + (lane / kLanes + j * (32 / kLanes)) * kPitch +
+                                                          (lane % kLanes) * 4);
+        if (!to[j]) continue;
         if (p.n_split > 1) {
-          float* dst = cache_part_row(p, r, hk, mt, split, rr) + 2 + d;
-          *reinterpret_cast<float2*>(dst) = make_float2(v.x, v.y);
-          *reinterpret_cast<float2*>(dst + 2) = make_float2(v.z, v.w);
+          *reinterpret_cast<float4*>(to[j]) = v;
+          to[j] += kC * 4;
         } else {
-          *reinterpret_cast<uint2*>(p.O + cache_out_row(p, r, hk, q0 + rr) + d) =
-              make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+          *reinterpret_cast<uint2*>(to[j]) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+          to[j] += kC * 2;
         }
       }
       __syncwarp();
     }
   }
+  if (threadIdx.x == kMmaWarp0 * 32 && split == 0 && hk == 0 && mt == 0 &&
+      static_cast<long long>(p.lens[r]) + sp.n > p.max_len)
+    atomicOr(p.err, DT_ERR_BAD_INDEX);
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp0) {
