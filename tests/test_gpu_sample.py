@@ -251,6 +251,24 @@ def test_bf16_logits_of_all_sizes(low, high, V):
             check(x.cuda(), u, 4, [T], None, [p], None)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_the_largest_vocabulary(bf16):
+    """2^18 tokens: all equal (sums of 2^62), two values, the usual shape, and
+    the type's extremes."""
+    V = 1 << 18
+    g = np.random.default_rng(18)
+    x = np.zeros((5, V), np.float32)
+    x[1] = g.integers(0, 2, V)
+    x[2] = g.standard_normal(V) * 2 - 1.1 * np.log(1 + g.permutation(V)) + 15
+    x[3] = g.uniform(-3.3e38, -1e38, V)
+    x[4] = g.uniform(1e38, 3.3e38, V)
+    t = torch.from_numpy(x).to(torch.bfloat16 if bf16 else torch.float32).cuda()
+    u = np.array([0.3, 0.999, 0.5, 0.2, 0.8], np.float32)
+    for T, k, p in ((1.0, 0, 1.0), (1.0, V - 1, 0.7), (2.0, 0, 0.97), (1.0, 5, 1.0), (0.0, 0, 1.0)):
+        check(t, u, 5, [T], [k], [p], None)
+    assert dtl.sample(t[:1], torch.tensor([1.0], device="cuda"))["token"].item() == V - 1
+
+
 @pytest.mark.parametrize("R,per,last", [(300, 3, 3), (300, 3, 1), (1024, 1, 1), (1030, 1, 1), (33, 2, 2)])
 def test_many_requests_of_all_kinds(R, per, last):
     """Rows that need their whole row's weights among rows that do not."""
