@@ -273,6 +273,41 @@ def test_trees_of_many_requests(R):
     check_rows(host(out.double()), host(q.double()), lens, n, masks, vals, dh ** -0.5)
 
 
+def test_pages_behind_the_first_4_gb():
+    """Attention of both kinds, commit and fork over far pages: the same bits
+    as over near ones with the same bytes."""
+    g = np.random.default_rng(21)
+    Hkv, dh, P, Hq, B = 8, 128, 128, 16, 64
+    cache = dtl.KVCache(2, 20000, page_tokens=P, Hkv=Hkv, dh=dh)       # 5.9 GB
+    near, far = np.arange(6), np.array([19999, 14600, 19998, 16000, 15001, 18000])
+    K = torch.randn(1, 6 * P, Hkv, dh, device="cuda").to(torch.bfloat16)
+    for layer in range(2):
+        cache.append(layer, K * (layer + 1), -K, cu(near[None]), cu([0]))
+    cache.copy_pages(cu(near), cu(far))
+    lens, n = np.array([650]), np.array([B])
+    m = torch.from_numpy(ancestor_mask(I.random_tree(g, B, B)["parent"], B, B)[None].view(np.int32)).cuda()
+    q = torch.randn(1, B + 1, Hq, dh, device="cuda").to(torch.bfloat16)
+    for rows in (1, B + 1):
+        kw = dict(mask=m, n_nodes=cu(n)) if rows > 1 else {}
+        out = [cache.attention(1, q[:, :rows].contiguous(), cu(t[None]), cu(lens), max_len=720, **kw) for t in (near, far)]
+        assert torch.equal(*out)
+    nodes, length = cu([[3, 9, 40]]), cu([3])
+    read = []
+    for t in (near, far):
+        ln = cu(lens)
+        cache.commit(cu(t[None]), ln, nodes, length)
+        assert host(ln).tolist() == [653]
+        read.append(cache.read(1, cu(t[None]), cu([0]), 653))
+    assert torch.equal(read[0][0], read[1][0]) and torch.equal(read[0][1], read[1][1])
+    cache.refs[torch.from_numpy(far).cuda()] = 1
+    cache.refs[:6] = 1
+    table, ln = cu(np.stack([far, np.full(6, -1)])), cu([653, 0])
+    assert host(cache.fork(table, ln, cu([0]), cu([1]))).tolist() == [1]
+    k, v = cache.read(1, table[1:].contiguous(), cu([0]), 653)
+    cache.check()
+    assert torch.equal(k, read[0][0]) and torch.equal(v, read[0][1])
+
+
 def test_trees_on_two_streams_and_in_graphs():
     """Two streams and two graphs, each call with its own workspace: the same
     bits as alone."""
