@@ -16,11 +16,10 @@ namespace {
 // are touched in their order and the codes of a warp's tokens are one
 // contiguous piece.
 // Bound by memory and, in append, by issue as well (0.83 instructions a cycle
-// and scheduler): 2 x 16000 tokens of 8 heads of 128 take 31 us in and 32 us
-// out, 168 MB each, 81% of a copy's rate together (71 us together with loads
-// behind the page lookup and plain stores; several heads per warp, one lookup
-// for all, 66 to 70: fewer loads in flight).  A step's 8 x 129 tokens: 6.2 us
-// in and out.
+// and scheduler): 2 x 16000 tokens of 8 heads of 128 take 58 us in and out,
+// 336 MB, 87% of a copy's rate (9 us more with loads behind the page lookup and
+// plain stores; several heads per warp, one lookup for all, 4 to 8 more: fewer
+// loads in flight).  A step's 8 x 129 tokens: 5.4 us in and out.
 struct TokenParams {
   CacheView c;
   const uint16_t *K, *V;   // append: input rows
@@ -119,6 +118,8 @@ __device__ __forceinline__ uint2 quantise16(const uint4 (&in)[2], float inv_scal
 
 template <int DH>
 __global__ void __launch_bounds__(256) k_cache_append(const TokenParams p) {
+  pdl_wait();
+  pdl_trigger();
   TokenSlot s = token_of<DH>(p);
   if (s.r >= p.R || s.i >= p.n) return;
   const size_t at = static_cast<size_t>(s.r) * p.req_stride + static_cast<size_t>(s.i) * p.token_stride +
@@ -161,6 +162,8 @@ __device__ __forceinline__ void values16(uint2 codes, uint32_t scale, float mul,
 
 template <int DH>
 __global__ void __launch_bounds__(256) k_cache_read(const TokenParams p) {
+  pdl_wait();
+  pdl_trigger();
   TokenSlot s = token_of<DH>(p);
   if (s.r >= p.R) return;
   find_slot(p, s);
@@ -280,6 +283,8 @@ struct ReserveParams {
 // pages (prefix sums), then the free pages go to the row their rank falls in.
 // Latency: 4.5 us alone with cold caches.
 __global__ void __launch_bounds__(kPlanThreads) k_cache_reserve(const ReserveParams p) {
+  pdl_wait();
+  pdl_trigger();
   __shared__ int s_first[kMaxReserveRows + 1], s_held[kMaxReserveRows];
   __shared__ int sh[33];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -361,6 +366,8 @@ struct ForkParams {
 };
 
 __global__ void __launch_bounds__(kPlanThreads) k_cache_fork(const ForkParams p) {
+  pdl_wait();
+  pdl_trigger();
   __shared__ int s_src[kMaxForks], s_dst[kMaxForks], s_page[kMaxForks], s_len[kMaxForks];
   __shared__ int sh[33];
   const int i = threadIdx.x;
@@ -479,6 +486,8 @@ struct CopyParams {
 // among the sources and the earlier destinations: such a pair is skipped, so
 // that the result does not depend on the blocks' order.
 __global__ void __launch_bounds__(256) k_cache_copy(const CopyParams p) {
+  pdl_wait();
+  pdl_trigger();
   const int i = blockIdx.z;
   const int s = p.src[i], d = p.dst[i];
   bool bad = s < 0 || s >= p.pages || d < 0 || d >= p.pages;
@@ -505,6 +514,8 @@ struct ReleaseParams {
 // A block per listed row.  An entry is taken by an exchange with -1, so a
 // row listed twice lets each page go once.
 __global__ void __launch_bounds__(128) k_cache_release(const ReleaseParams p) {
+  pdl_wait();
+  pdl_trigger();
   const int r = p.rows[blockIdx.x], keep = p.keep[blockIdx.x];
   if (r < 0 || r >= p.R || keep < 0) {
     if (threadIdx.x == 0 && p.err) atomicOr(p.err, DT_ERR_BAD_INDEX);
@@ -570,6 +581,8 @@ __device__ __forceinline__ int commit_count(const CommitParams& p, int r, int* b
 // of a path of 8 tokens in 32 layers take 13.8 us, of 32 paths 18.3.
 template <typename U>
 __global__ void __launch_bounds__(256) k_cache_commit(const CommitParams p) {
+  pdl_wait();
+  pdl_trigger();
   constexpr int kU = 8;
   unsigned cl, rank;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(cl));
@@ -694,7 +707,7 @@ extern "C" dartree_status dartree_cache_append(const dartree_cache* cache, int32
   p.req_stride = req_stride;
   p.token_stride = token_stride;
   return cache_launched(launch_kernel(p.c.dh == 128 ? k_cache_append<128> : k_cache_append<64>, dim3(blocks),
-                                      dim3(256), 0, static_cast<cudaStream_t>(stream), false, p));
+                                      dim3(256), 0, static_cast<cudaStream_t>(stream), true, p));
 }
 
 extern "C" dartree_status dartree_cache_read(const dartree_cache* cache, int32_t layer, void* K, void* V,
@@ -710,7 +723,7 @@ extern "C" dartree_status dartree_cache_read(const dartree_cache* cache, int32_t
   p.Ko = static_cast<uint16_t*>(K);
   p.Vo = static_cast<uint16_t*>(V);
   return cache_launched(launch_kernel(p.c.dh == 128 ? k_cache_read<128> : k_cache_read<64>, dim3(blocks),
-                                      dim3(256), 0, static_cast<cudaStream_t>(stream), false, p));
+                                      dim3(256), 0, static_cast<cudaStream_t>(stream), true, p));
 }
 
 extern "C" dartree_status dartree_cache_reserve(const dartree_cache* cache, int32_t* table, int32_t max_pages,
@@ -726,7 +739,7 @@ extern "C" dartree_status dartree_cache_reserve(const dartree_cache* cache, int3
     return cache_fail(DARTREE_ERR_UNSUPPORTED, "R * max_pages must be below 2^31");
   const ReserveParams p{cache->refs, table, lens, want, ok, v.pages, v.log_page, max_pages, R};
   return cache_launched(launch_kernel(k_cache_reserve, dim3(1), dim3(kPlanThreads), 0,
-                                      static_cast<cudaStream_t>(stream), false, p));
+                                      static_cast<cudaStream_t>(stream), true, p));
 }
 
 extern "C" dartree_status dartree_cache_fork(const dartree_cache* cache, int32_t* table, int32_t max_pages,
@@ -744,7 +757,7 @@ extern "C" dartree_status dartree_cache_fork(const dartree_cache* cache, int32_t
   const ForkParams p{cache->refs, table,      lens, src, dst, ok, v.pages, v.log_page,
                      max_pages,   R,          n,    v.pool, v.page_bytes, v.layer_bytes};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_kernel(k_cache_fork, dim3(1), dim3(kPlanThreads), 0, st, false, p);
+  cudaError_t e = launch_kernel(k_cache_fork, dim3(1), dim3(kPlanThreads), 0, st, true, p);
   if (e == cudaSuccess)
     e = launch_kernel(k_cache_fork_copy, dim3(copy_pieces(v.page_bytes), v.layers, n), dim3(256), 0, st, true, p);
   return cache_launched(e);
@@ -767,7 +780,7 @@ extern "C" dartree_status dartree_cache_commit(const dartree_cache* cache, const
   while (cl < 8 && cl < v.layers) cl *= 2;
   return cache_launched(launch_kernel_cluster(v.dh == 128 ? k_cache_commit<uint2> : k_cache_commit<uint32_t>,
                                               dim3(static_cast<unsigned>(R) * cl), dim3(256), 0,
-                                              static_cast<cudaStream_t>(stream), false, cl, p));
+                                              static_cast<cudaStream_t>(stream), true, cl, p));
 }
 
 extern "C" dartree_status dartree_cache_release(const dartree_cache* cache, int32_t* table, int32_t max_pages,
@@ -782,7 +795,7 @@ extern "C" dartree_status dartree_cache_release(const dartree_cache* cache, int3
   if (!rows || !keep) return cache_fail(DARTREE_ERR_INVALID_ARG, "null pointer argument");
   const ReleaseParams p{cache->refs, table, lens, rows, keep, v.pages, v.log_page, max_pages, R, err};
   return cache_launched(launch_kernel(k_cache_release, dim3(n), dim3(128), 0, static_cast<cudaStream_t>(stream),
-                                      false, p));
+                                      true, p));
 }
 
 extern "C" dartree_status dartree_cache_copy_pages(const dartree_cache* cache, const int32_t* src,
@@ -797,5 +810,5 @@ extern "C" dartree_status dartree_cache_copy_pages(const dartree_cache* cache, c
     return cache_fail(DARTREE_ERR_UNSUPPORTED, "copy_pages takes at most 65535 pages and layers");
   const CopyParams p{v.pool, v.page_bytes, v.layer_bytes, src, dst, n, v.pages, err};
   return cache_launched(launch_kernel(k_cache_copy, dim3(copy_pieces(v.page_bytes), v.layers, n), dim3(256), 0,
-                                      static_cast<cudaStream_t>(stream), false, p));
+                                      static_cast<cudaStream_t>(stream), true, p));
 }

@@ -494,6 +494,11 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
 
 template <int DH, int NQ>
 __global__ void __launch_bounds__(kThreads, 3) k_cache_attention(const CacheAttnParams p) {
+  if (!p.tail) {
+    pdl_wait();
+    // (not ahead of a join: its blocks would take the place of these)
+    if (p.cluster || p.n_split == 1) pdl_trigger();
+  }
   attend_rows<DH, NQ>(p);
   // The rows left over by the tensor-core kernel: launched while that one
   // runs, whose outputs these are not; one CTA sees it complete, so that what
@@ -509,8 +514,8 @@ cudaError_t launch_rows(const CacheAttnParams& p, cudaStream_t st) {
   const dim3 grid(p.n_split, p.c.Hkv, p.R);
   if (p.cluster)
     return launch_kernel_cluster(k_cache_attention<DH, NQ>, grid, dim3(kThreads), sizeof(AttnSmem<DH, NQ>), st,
-                                 p.tail != 0, p.n_split, p);
-  return launch_kernel(k_cache_attention<DH, NQ>, grid, dim3(kThreads), sizeof(AttnSmem<DH, NQ>), st, p.tail != 0, p);
+                                 true, p.n_split, p);
+  return launch_kernel(k_cache_attention<DH, NQ>, grid, dim3(kThreads), sizeof(AttnSmem<DH, NQ>), st, true, p);
 }
 
 // The shares of each row over the key splits, joined in a fixed order: M =

@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hk = blockIdx.y;
   const int mt = blockIdx.x / p.n_split, split = blockIdx.x % p.n_split;
+  pdl_wait();
   pdl_trigger();  // (the launch of the rows left over may fill the SMs that come free)
   __shared__ int s_r;
   if (p.R > 1 && p.R <= kTreeSorted) {  // the z-th longest request
@@ -668,7 +669,7 @@ cudaError_t launch_cache_tree(const CacheAttnParams& p, cudaStream_t st) {
   cudaError_t e = p.c.dh == 128 ? opt_in_smem(k_cache_tree<128>, &done128) : opt_in_smem(k_cache_tree<64>, &done64);
   if (e != cudaSuccess) return e;
   return launch_kernel(p.c.dh == 128 ? k_cache_tree<128> : k_cache_tree<64>, grid, dim3(kTreeThreads),
-                       (p.c.dh == 128 ? TreeSmem<128>::kTotal : TreeSmem<64>::kTotal) + 1024, st, false, p);
+                       (p.c.dh == 128 ? TreeSmem<128>::kTotal : TreeSmem<64>::kTotal) + 1024, st, true, p);
 }
 
 }  // namespace dt

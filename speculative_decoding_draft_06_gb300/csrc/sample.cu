@@ -1376,6 +1376,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_sample(const SampleParams p) {
   constexpr int kPer = Row<E>::kPer;
   extern __shared__ __align__(16) uint8_t raw[];
   Smem& sm = *reinterpret_cast<Smem*>(raw);
+  pdl_wait();
+  pdl_trigger();
   unsigned cl_u, rank_u;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(cl_u));
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank_u));
@@ -1709,6 +1711,6 @@ extern "C" dartree_status dartree_sample(const void* logits, int32_t bf16, int64
   cudaError_t e = bf16 ? opt_in_smem(k_sample<uint16_t>, &done_bf16) : opt_in_smem(k_sample<float>, &done_f32);
   if (e == cudaSuccess)
     e = launch_kernel_cluster(bf16 ? k_sample<uint16_t> : k_sample<float>, grid, dim3(kThreads), sizeof(Smem), st,
-                              false, cl, p);
+                              true, cl, p);
   return cache_launched(e);
 }
