@@ -546,7 +546,7 @@ dartree_status dartree_cache_fork(const dartree_cache *cache, int32_t *table, in
  * whose key and value the next step appends).  nodes, len as dartree_accept
  * writes them (ranks rising in a row).  A row whose ranks do not rise, whose
  * tokens have no page, or with lens[r] < 0 is left as it was (the former two
- * are flagged). */
+ * are flagged).  R <= 2^24, max_len * Hkv * layers < 2^25. */
 dartree_status dartree_cache_commit(const dartree_cache *cache, const int32_t *table,
                                     int32_t max_pages, int32_t *lens, const int32_t *nodes,
                                     const int32_t *len, int32_t R, int32_t max_len, int32_t extra,

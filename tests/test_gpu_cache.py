@@ -256,7 +256,8 @@ def test_release(seed):
     assert not host(cache.refs).any() and (host(table) == -1).all() and not host(lens).any()
 
 
-COMMITS = [(64, 128, 8, 4, 7), (16, 64, 3, 2, 16), (128, 128, 1, 1, 1), (32, 64, 2, 3, 40), (16, 128, 8, 1, 130)]
+COMMITS = [(64, 128, 8, 4, 7), (16, 64, 3, 2, 16), (128, 128, 1, 1, 1), (32, 64, 2, 3, 40), (16, 128, 8, 1, 130),
+           (64, 128, 2, 20, 9), (16, 64, 3, 9, 33), (32, 128, 8, 17, 60)]
 
 
 @pytest.mark.parametrize("case", range(len(COMMITS)))
