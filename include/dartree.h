@@ -427,7 +427,7 @@ dartree_status dartree_accept(const int32_t *parent, const int32_t *token, const
  *
  * A page holds page_tokens (16, 32, 64 or 128) consecutive tokens of one
  * sequence, all key/value heads of one layer.  Per head it has one chunk of
- * page_tokens * dh * 9 / 8 bytes (dh = 64 or 128):
+ * page_tokens * dh * 9 / 8 bytes (dh = 64 or 128, at most 65535 heads):
  *   key codes [page_tokens][dh/2], key scales [page_tokens][dh/16],
  *   value codes [page_tokens][dh/2], value scales [page_tokens][dh/16].
  * A code is e2m1 (0, .5, 1, 1.5, 2, 3, 4, 6 and the sign in bit 3), the even

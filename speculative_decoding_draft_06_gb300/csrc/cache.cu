@@ -681,7 +681,7 @@ dartree_status page_check(const dartree_cache* cache, const void* table, const v
 }  // namespace dt
 
 extern "C" size_t dartree_cache_page_bytes(int32_t page_tokens, int32_t Hkv, int32_t dh) {
-  if (dt::cache_log_page(page_tokens) < 0 || Hkv < 1 || (dh != 64 && dh != 128)) return 0;
+  if (dt::cache_log_page(page_tokens) < 0 || Hkv < 1 || Hkv > 65535 || (dh != 64 && dh != 128)) return 0;
   return static_cast<size_t>(Hkv) * (page_tokens * dh / 8) * 9;
 }
 

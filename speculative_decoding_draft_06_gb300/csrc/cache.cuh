@@ -42,7 +42,7 @@ inline bool cache_pow2(float x) {
 // (*unsupported: outside the format's sizes).
 inline const char* cache_view(const dartree_cache* c, CacheView* v) {
   if (!c || !c->pool) return "null cache or pool";
-  if (c->layers < 1 || c->pages < 1 || c->Hkv < 1) return "bad cache layers, pages or Hkv";
+  if (c->layers < 1 || c->pages < 1 || c->Hkv < 1 || c->Hkv > 65535) return "bad cache layers, pages or Hkv";
   const int lp = cache_log_page(c->page_tokens);
   if (lp < 0) return "page_tokens must be 16, 32, 64 or 128";
   if (c->dh != 64 && c->dh != 128) return "the cache's head dimension must be 64 or 128";

@@ -562,7 +562,7 @@ class KVCache:
         self.page_bytes = int(self._lib.dartree_cache_page_bytes(page_tokens, Hkv, dh))
         if self.page_bytes == 0 or layers < 1 or pages < 1:
             raise ValueError("page_tokens must be 16, 32, 64 or 128, dh 64 or 128, layers, pages "
-                             "and Hkv at least 1")
+                             "and Hkv at least 1 (65535 at most)")
         for s in (k_scale, v_scale):
             if not (2.0 ** -64 <= s <= 2.0 ** 64 and np.frexp(s)[0] == 0.5):
                 raise ValueError("k_scale and v_scale must be powers of two from 2^-64 to 2^64")

@@ -28,7 +28,7 @@ def desc(**over):
     return ctypes.byref(dtl.Cache(*(d[n] for n, _ in dtl.Cache._fields_)))
 
 
-BAD_DESC = [dict(pool=None), dict(pool=A + 8), dict(layers=0), dict(pages=0), dict(Hkv=0), dict(page_tokens=48),
+BAD_DESC = [dict(Hkv=65536), dict(pool=None), dict(pool=A + 8), dict(layers=0), dict(pages=0), dict(Hkv=0), dict(page_tokens=48),
             dict(page_tokens=256), dict(dh=96), dict(dh=256), dict(k_scale=3.0), dict(v_scale=0.0),
             dict(v_scale=-1.0), dict(k_scale=2.0 ** 65), dict(k_scale=float("nan")), dict(v_scale=float("inf"))]
 
@@ -69,7 +69,8 @@ REFUSED = [
     ("attention", dict(max_len=-1), INVALID), ("attention", dict(layer=2), INVALID),
     ("attention", dict(max_len=100000, work=None), INVALID),
     ("attention", dict(max_len=100000, work_bytes=100), INVALID),
-    ("attention", dict(R=70000), UNSUPPORTED),
+    ("attention", dict(R=70000), UNSUPPORTED), ("attention", dict(scale=-0.1), INVALID),
+    ("commit", dict(R=(1 << 24) + 1), UNSUPPORTED), ("commit", dict(max_len=1 << 30), UNSUPPORTED),
     ("reserve", dict(want=None), INVALID), ("reserve", dict(ok=None), INVALID), ("reserve", dict(R=0), INVALID),
     ("reserve", dict(R=4097), UNSUPPORTED), ("reserve", dict(R=4096, width=1 << 20), UNSUPPORTED),
     ("fork", dict(src=None), INVALID), ("fork", dict(n=-1), INVALID), ("fork", dict(n=1025), UNSUPPORTED),
@@ -99,6 +100,11 @@ def test_bad_descriptors_are_refused(lib, name, case):
 @pytest.mark.parametrize("name", ["reserve", "fork", "release"])
 def test_the_allocator_needs_refs(lib, name):
     assert call(lib, name, desc(refs=None)) == INVALID
+
+
+def test_a_scale_that_overflows_with_the_keys_unit_is_refused(lib):
+    assert call(lib, "attention", desc(k_scale=2.0 ** 64), scale=1e20) == INVALID
+    assert call(lib, "attention", desc(k_scale=2.0 ** -64), scale=3.1e38) == INVALID
 
 
 def test_page_bytes(lib):
