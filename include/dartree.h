@@ -446,7 +446,9 @@ dartree_status dartree_accept(const int32_t *parent, const int32_t *token, const
  * Sequences are rows of a page table [R][max_pages] (int32, token t of row r
  * in page table[r][t / page_tokens]; a row's pages are its first entries,
  * the rest is -1) with lens [R] tokens each.  A page that is held twice
- * (dartree_cache_fork) is complete and is only read.
+ * (dartree_cache_fork) is complete and is only read: its tokens are written.
+ * Where the last tokens of lens are counted before they are written (extra of
+ * dartree_cache_commit), the _ex forms of fork and reserve are told so.
  *
  * err: optional device word; bad indices found on the device (a page number
  * outside [0, pages), a token without a page, a row outside [0, R), ...) are
@@ -519,14 +521,22 @@ size_t dartree_cache_attention_workspace(int32_t R, int32_t B, int32_t max_len, 
 /* Pages for want[r] more tokens per row: row r comes to hold at least
  * ceil((lens[r] + want[r]) / page_tokens) pages; lens is not changed.  Rows
  * are served in order; ok[r] = 0 for a row that needs more than max_pages or
- * has lens[r] or want[r] < 0 (it gets none), or whose last page is partly
- * filled and held by another row too (a forked row that was cut within a
- * complete page: fork it, the copy has a page of its own), and for the first
- * row whose pages are not there and every later one that needs some.
- * R <= 4096, R * max_pages < 2^31. */
+ * has lens[r] or want[r] < 0 (it gets none), or that wants tokens and would
+ * write them to a page that another row holds too (a forked row that was cut
+ * within a complete page: fork it, the copy has a page of its own), and for
+ * the first row whose pages are not there and every later one that needs some.
+ * R <= 4096, R * max_pages < 2^31.
+ * _ex: the last `pending` >= 0 tokens of every row are counted but not
+ * written (1 behind a commit with extra = 1), so the first token to be
+ * written is at position lens[r] - pending, wanted or not;
+ * dartree_cache_reserve: none. */
 dartree_status dartree_cache_reserve(const dartree_cache *cache, int32_t *table, int32_t max_pages,
                                      const int32_t *lens, const int32_t *want, int32_t R,
                                      int32_t *ok, void *stream);
+dartree_status dartree_cache_reserve_ex(const dartree_cache *cache, int32_t *table,
+                                        int32_t max_pages, const int32_t *lens,
+                                        const int32_t *want, int32_t R, int32_t pending,
+                                        int32_t *ok, void *stream);
 
 /* Continues sequences in several ways: for i < n, row dst[i] becomes a copy
  * of row src[i].  Complete pages are shared; the last, partly filled page is
@@ -534,16 +544,28 @@ dartree_status dartree_cache_reserve(const dartree_cache *cache, int32_t *table,
  * ok[i] = 0, and nothing done, when a row is outside [0, R), dst[i] holds
  * pages, occurs earlier in dst or anywhere in src, lens[src[i]] < 0 or its
  * pages are not there, or no free page is left (served in order, as
- * dartree_cache_reserve).  n <= 1024. */
+ * dartree_cache_reserve).  n <= 1024.
+ * _ex: the last `pending` >= 0 tokens of lens[src[i]] are counted but not
+ * written (1 behind a commit with extra = 1: without it both rows would write
+ * their bonus tokens to one shared page where lens[src[i]] is a multiple of
+ * page_tokens).  Shared are the pages whose tokens are all written; the page
+ * in which the written ones end is copied, and the copy gets pages of its own
+ * for the pending ones too (the source needs none for them).
+ * n * max_pages < 2^31 with pending tokens.  dartree_cache_fork: none. */
 dartree_status dartree_cache_fork(const dartree_cache *cache, int32_t *table, int32_t max_pages,
                                   int32_t *lens, int32_t R, const int32_t *src, const int32_t *dst,
                                   int32_t n, int32_t *ok, void *stream);
+dartree_status dartree_cache_fork_ex(const dartree_cache *cache, int32_t *table, int32_t max_pages,
+                                     int32_t *lens, int32_t R, const int32_t *src,
+                                     const int32_t *dst, int32_t n, int32_t pending, int32_t *ok,
+                                     void *stream);
 
 /* After dartree_accept: the keys and values of the accepted tree nodes move,
  * in all layers, to the end of the prefix -- node nodes[r][k] from position
  * lens[r] + nodes[r][k] to lens[r] + k for k < m, m = min(len[r], max_len) --
  * and lens[r] becomes lens[r] + m + extra (extra = 1 counts the bonus token,
- * whose key and value the next step appends).  nodes, len as dartree_accept
+ * whose key and value the next step appends; until then it is pending for
+ * dartree_cache_fork_ex and _reserve_ex).  nodes, len as dartree_accept
  * writes them (ranks rising in a row).  A row whose ranks do not rise, whose
  * tokens have no page, or with lens[r] < 0 is left as it was (the former two
  * are flagged).  R <= 2^24, max_len * Hkv * layers < 2^25. */

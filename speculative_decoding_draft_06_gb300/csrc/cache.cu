@@ -276,7 +276,7 @@ struct ReserveParams {
   int32_t* table;
   const int32_t *lens, *want;
   int32_t* ok;
-  int pages, log_page, max_pages, R;
+  int pages, log_page, max_pages, R, pending;
 };
 
 // One block: what each row lacks, the rows' first ranks among the free
@@ -295,14 +295,16 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_reserve(const ReservePar
     if (len >= 0 && want >= 0 && need <= p.max_pages) {
       held = held_pages(p.table + static_cast<size_t>(r) * p.max_pages, p.max_pages);
       lack = need > held ? static_cast<int>(need) - held : 0;
-      // its next token would go into a page that another row reads
-      const long long at = len >> p.log_page;
-      if (want > 0 && (len & ((1 << p.log_page) - 1)) != 0 && at < held) {
-        const int page = p.table[static_cast<size_t>(r) * p.max_pages + at];
-        if (page < p.pages && p.refs[page] > 1) {
-          held = -1;
-          lack = 0;
+      // tokens would go into a page that another row reads
+      bool shared = false;
+      if (want > 0 || p.pending > 0)
+        for (long long at = (max(len - p.pending, 0ll) >> p.log_page) + lane; at < need && at < held; at += 32) {
+          const int page = p.table[static_cast<size_t>(r) * p.max_pages + at];
+          shared |= page < p.pages && p.refs[page] > 1;
         }
+      if (__any_sync(kFullMask, shared)) {
+        held = -1;
+        lack = 0;
       }
     }
     if (lane == 0) {
@@ -359,16 +361,23 @@ struct ForkParams {
   int32_t *table, *lens;
   const int32_t *src, *dst;
   int32_t* ok;
-  int pages, log_page, max_pages, R, n;
+  int pages, log_page, max_pages, R, n, pending;
   // the copy
   uint8_t* pool;
   size_t page_bytes, layer_bytes;
 };
 
+// Tokens of a row of len that are written: behind them `pending` are only
+// counted, and their places are still to be written.
+__device__ __forceinline__ int written(int len, int pending) { return max(len - pending, 0); }
+
+// Pages of written tokens only are shared; those behind are the copy's own:
+// the one in which the written tokens end (copied below) and, with more
+// pending tokens, fresh ones.
 __global__ void __launch_bounds__(kPlanThreads) k_cache_fork(const ForkParams p) {
   pdl_wait();
   pdl_trigger();
-  __shared__ int s_src[kMaxForks], s_dst[kMaxForks], s_page[kMaxForks], s_len[kMaxForks];
+  __shared__ int s_src[kMaxForks], s_dst[kMaxForks], s_len[kMaxForks], s_first[kMaxForks + 1];
   __shared__ int sh[33];
   const int i = threadIdx.x;
   const int P = 1 << p.log_page;
@@ -377,8 +386,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_fork(const ForkParams p)
     s_dst[i] = p.dst[i];
   }
   __syncthreads();
-  bool valid = false, part = false;
-  int len = 0;
+  bool valid = false;
+  int len = -1, own = 0;  // own: pages that are not shared
   if (i < p.n) {
     const int s = s_src[i], d = s_dst[i];
     valid = s >= 0 && s < p.R && d >= 0 && d < p.R;
@@ -386,32 +395,55 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_fork(const ForkParams p)
       if (s_src[j] == d || (j < i && s_dst[j] == d)) valid = false;
     if (valid) {
       len = p.lens[s];
+      const int done = len < 0 ? 0 : written(len, p.pending);
       const int need = len < 0 ? 0 : static_cast<int>((static_cast<long long>(len) + P - 1) >> p.log_page);
+      const int there = static_cast<int>((static_cast<long long>(done) + P - 1) >> p.log_page);
       valid = len >= 0 && need <= p.max_pages && p.table[static_cast<size_t>(d) * p.max_pages] < 0;
-      if (valid && need > 0) {
-        const int last = p.table[static_cast<size_t>(s) * p.max_pages + need - 1];
+      if (valid && there > 0) {
+        const int last = p.table[static_cast<size_t>(s) * p.max_pages + there - 1];
         valid = last >= 0 && last < p.pages;
       }
+      if (valid) own = need - (done >> p.log_page);
     }
-    part = valid && (len & (P - 1)) != 0;
   }
   int total;
-  const int rank = block_exclusive(part ? 1 : 0, sh, &total);
-  const int found = find_free(p.refs, p.pages, total, sh, [&](int k, int page) { s_page[k] = page; });
+  const int first = block_exclusive(own, sh, &total);
+  if (i < p.n) {
+    s_len[i] = len;
+    s_first[i] = first;
+  }
+  if (i == 0) s_first[p.n] = total;
   __syncthreads();
-  const int mine = part && rank < found ? s_page[rank] : -1;
+  // (the last row whose first rank is <= rank: refused ones have no ranks)
+  const int found = find_free(p.refs, p.pages, total, sh, [&](int rank, int page) {
+    int lo = 0, hi = p.n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_first[mid] <= rank) lo = mid;
+      else hi = mid;
+    }
+    p.table[static_cast<size_t>(s_dst[lo]) * p.max_pages + (written(s_len[lo], p.pending) >> p.log_page) + rank -
+            s_first[lo]] = page;
+    p.refs[page] = 1;
+  });
   __syncthreads();
   if (i < p.n) {
-    const bool ok = valid && (!part || mine >= 0);
+    const bool ok = valid && (own == 0 || first + own <= found);
     p.ok[i] = ok ? 1 : 0;
-    s_len[i] = ok ? len : -1;
-    s_page[i] = mine;
+    if (!ok) {
+      for (int k = 0; k < min(own, found - first); ++k) {  // the row the pages ran out in
+        int32_t* e = p.table + static_cast<size_t>(s_dst[i]) * p.max_pages + (written(len, p.pending) >> p.log_page) + k;
+        p.refs[*e] = 0;
+        *e = -1;
+      }
+      s_len[i] = -1;
+    }
   }
   __syncthreads();
   const int warp = i >> 5, lane = i & 31;
   for (int f = warp; f < p.n; f += kPlanThreads / 32) {
     if (s_len[f] < 0) continue;
-    const int whole = s_len[f] >> p.log_page;
+    const int whole = written(s_len[f], p.pending) >> p.log_page;
     const int32_t* from = p.table + static_cast<size_t>(s_src[f]) * p.max_pages;
     int32_t* to = p.table + static_cast<size_t>(s_dst[f]) * p.max_pages;
     for (int j = lane; j < whole; j += 32) {
@@ -419,13 +451,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_fork(const ForkParams p)
       to[j] = page;
       if (page >= 0 && page < p.pages) atomicAdd(&p.refs[page], 1);
     }
-    if (lane == 0) {
-      if (s_page[f] >= 0) {
-        to[whole] = s_page[f];
-        p.refs[s_page[f]] = 1;
-      }
-      p.lens[s_dst[f]] = s_len[f];
-    }
+    if (lane == 0) p.lens[s_dst[f]] = s_len[f];
   }
 }
 
@@ -458,15 +484,15 @@ __device__ __forceinline__ void piece(size_t page_bytes, int* begin, int* end) {
 
 // The partly filled page of each fork, grid (pieces, layers, forks).  Bound by
 // memory: 32 forks, 32 layers, pages of 64 tokens of 8 heads of 128: 151 MB
-// with the release and the plan in front of it in 24 us, 6.3 TB/s.
+// with the release and the plan in front of it in 24 us, 6.3 TB/s (a graph's).
 __global__ void __launch_bounds__(256) k_cache_fork_copy(const ForkParams p) {
   const int i = blockIdx.z;
   pdl_wait();
   if (!p.ok[i]) return;
-  const int s = p.src[i], d = p.dst[i], len = p.lens[d];
-  if ((len & ((1 << p.log_page) - 1)) == 0) return;
-  const int from = p.table[static_cast<size_t>(s) * p.max_pages + (len >> p.log_page)];
-  const int to = p.table[static_cast<size_t>(d) * p.max_pages + (len >> p.log_page)];
+  const int s = p.src[i], d = p.dst[i], done = written(p.lens[d], p.pending);
+  if ((done & ((1 << p.log_page) - 1)) == 0) return;
+  const int from = p.table[static_cast<size_t>(s) * p.max_pages + (done >> p.log_page)];
+  const int to = p.table[static_cast<size_t>(d) * p.max_pages + (done >> p.log_page)];
   uint8_t* layer = p.pool + static_cast<size_t>(blockIdx.y) * p.layer_bytes;
   int b, e;
   piece(p.page_bytes, &b, &e);
@@ -723,41 +749,57 @@ extern "C" dartree_status dartree_cache_read(const dartree_cache* cache, int32_t
                                       dim3(256), 0, static_cast<cudaStream_t>(stream), true, p));
 }
 
-extern "C" dartree_status dartree_cache_reserve(const dartree_cache* cache, int32_t* table, int32_t max_pages,
-                                                const int32_t* lens, const int32_t* want, int32_t R,
-                                                int32_t* ok, void* stream) {
+extern "C" dartree_status dartree_cache_reserve_ex(const dartree_cache* cache, int32_t* table, int32_t max_pages,
+                                                   const int32_t* lens, const int32_t* want, int32_t R,
+                                                   int32_t pending, int32_t* ok, void* stream) {
   using namespace dt;
   CacheView v;
   const dartree_status s = page_check(cache, table, lens, max_pages, R, true, &v);
   if (s != DARTREE_OK) return s;
   if (!want || !ok) return cache_fail(DARTREE_ERR_INVALID_ARG, "null pointer argument");
+  if (pending < 0) return cache_fail(DARTREE_ERR_INVALID_ARG, "bad pending");
   if (R > kMaxReserveRows) return cache_fail(DARTREE_ERR_UNSUPPORTED, "reserve takes at most 4096 rows");
   if (static_cast<long long>(R) * max_pages > 0x7FFFFFFFll)  // (what the rows lack is summed in 32 bits)
     return cache_fail(DARTREE_ERR_UNSUPPORTED, "R * max_pages must be below 2^31");
-  const ReserveParams p{cache->refs, table, lens, want, ok, v.pages, v.log_page, max_pages, R};
+  const ReserveParams p{cache->refs, table, lens, want, ok, v.pages, v.log_page, max_pages, R, pending};
   return cache_launched(launch_kernel(k_cache_reserve, dim3(1), dim3(kPlanThreads), 0,
                                       static_cast<cudaStream_t>(stream), true, p));
 }
 
-extern "C" dartree_status dartree_cache_fork(const dartree_cache* cache, int32_t* table, int32_t max_pages,
-                                             int32_t* lens, int32_t R, const int32_t* src,
-                                             const int32_t* dst, int32_t n, int32_t* ok, void* stream) {
+extern "C" dartree_status dartree_cache_reserve(const dartree_cache* cache, int32_t* table, int32_t max_pages,
+                                                const int32_t* lens, const int32_t* want, int32_t R,
+                                                int32_t* ok, void* stream) {
+  return dartree_cache_reserve_ex(cache, table, max_pages, lens, want, R, 0, ok, stream);
+}
+
+extern "C" dartree_status dartree_cache_fork_ex(const dartree_cache* cache, int32_t* table, int32_t max_pages,
+                                                int32_t* lens, int32_t R, const int32_t* src,
+                                                const int32_t* dst, int32_t n, int32_t pending, int32_t* ok,
+                                                void* stream) {
   using namespace dt;
   CacheView v;
   const dartree_status s = page_check(cache, table, lens, max_pages, R, true, &v);
   if (s != DARTREE_OK) return s;
-  if (n < 0) return cache_fail(DARTREE_ERR_INVALID_ARG, "bad n");
+  if (n < 0 || pending < 0) return cache_fail(DARTREE_ERR_INVALID_ARG, "bad n or pending");
   if (n == 0) return DARTREE_OK;
   if (!src || !dst || !ok) return cache_fail(DARTREE_ERR_INVALID_ARG, "null pointer argument");
   if (n > kMaxForks || v.layers > 65535)
     return cache_fail(DARTREE_ERR_UNSUPPORTED, "fork takes at most 1024 rows and 65535 layers");
-  const ForkParams p{cache->refs, table,      lens, src, dst, ok, v.pages, v.log_page,
-                     max_pages,   R,          n,    v.pool, v.page_bytes, v.layer_bytes};
+  if (pending > 0 && static_cast<long long>(n) * max_pages > 0x7FFFFFFFll)  // (the rows' pages are summed in 32 bits)
+    return cache_fail(DARTREE_ERR_UNSUPPORTED, "n * max_pages must be below 2^31");
+  const ForkParams p{cache->refs, table, lens, src,     dst,    ok,           v.pages,      v.log_page,
+                     max_pages,   R,     n,    pending, v.pool, v.page_bytes, v.layer_bytes};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_kernel(k_cache_fork, dim3(1), dim3(kPlanThreads), 0, st, true, p);
   if (e == cudaSuccess)
     e = launch_kernel(k_cache_fork_copy, dim3(copy_pieces(v.page_bytes), v.layers, n), dim3(256), 0, st, true, p);
   return cache_launched(e);
+}
+
+extern "C" dartree_status dartree_cache_fork(const dartree_cache* cache, int32_t* table, int32_t max_pages,
+                                             int32_t* lens, int32_t R, const int32_t* src,
+                                             const int32_t* dst, int32_t n, int32_t* ok, void* stream) {
+  return dartree_cache_fork_ex(cache, table, max_pages, lens, R, src, dst, n, 0, ok, stream);
 }
 
 extern "C" dartree_status dartree_cache_commit(const dartree_cache* cache, const int32_t* table,

@@ -132,7 +132,9 @@ def load():
                                          ctypes.c_size_t, _vp, _vp]),
         "dartree_cache_attention_workspace": (ctypes.c_size_t, [_i32] * 6),
         "dartree_cache_reserve": (st, [cache, _vp, _i32, _vp, _vp, _i32, _vp, _vp]),
+        "dartree_cache_reserve_ex": (st, [cache, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp]),
         "dartree_cache_fork": (st, [cache, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp]),
+        "dartree_cache_fork_ex": (st, [cache, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp]),
         "dartree_cache_commit": (st, [cache, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp]),
         "dartree_cache_release": (st, [cache, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp]),
         "dartree_cache_copy_pages": (st, [cache, _vp, _vp, _i32, _vp, _vp]),
@@ -704,29 +706,34 @@ class KVCache:
         return out
 
     # ------------------------------------------------------ page operations
-    def reserve(self, table, lens, want, *, stream=None) -> torch.Tensor:
+    def reserve(self, table, lens, want, *, pending: int = 0, stream=None) -> torch.Tensor:
         """Pages for want[r] more tokens per row -> ok [R] int32
-        (dartree_cache_reserve)."""
+        (dartree_cache_reserve_ex).  ``pending``: how many of the last tokens of
+        lens are counted but not written yet (commit's ``extra``)."""
         t, width, ln, R = self._seqs(table, lens)
         ok = _alloc(stream, (R,), _I32, self.dev)
-        _launch(self._lib.dartree_cache_reserve, self._idx, stream, self._ref, t, width, ln,
-                _ints("want", want, self._idx, R), R, ok.data_ptr())
+        _launch(self._lib.dartree_cache_reserve_ex, self._idx, stream, self._ref, t, width, ln,
+                _ints("want", want, self._idx, R), R, pending, ok.data_ptr())
         return ok
 
-    def fork(self, table, lens, src, dst, *, stream=None) -> torch.Tensor:
+    def fork(self, table, lens, src, dst, *, pending: int = 0, stream=None) -> torch.Tensor:
         """Rows dst become copies of rows src -> ok [n] int32
-        (dartree_cache_fork)."""
+        (dartree_cache_fork_ex).  ``pending``: how many of the last tokens of
+        lens are counted but not written yet (commit's ``extra``): the pages
+        they go to are not shared."""
         t, width, ln, R = self._seqs(table, lens)
         n = src.numel()
         ok = _alloc(stream, (n,), _I32, self.dev)
-        _launch(self._lib.dartree_cache_fork, self._idx, stream, self._ref, t, width, ln, R,
-                _ints("src", src, self._idx, n), _ints("dst", dst, self._idx, n), n, ok.data_ptr())
+        _launch(self._lib.dartree_cache_fork_ex, self._idx, stream, self._ref, t, width, ln, R,
+                _ints("src", src, self._idx, n), _ints("dst", dst, self._idx, n), n, pending,
+                ok.data_ptr())
         return ok
 
     def commit(self, table, lens, nodes, length, *, extra: int = 0, stream=None) -> None:
         """Moves the accepted nodes' tokens to the prefixes' ends and adds
         length[r] + extra to lens (dartree_cache_commit); nodes [R, max_len]
-        and length [R] as :func:`accept` returns them."""
+        and length [R] as :func:`accept` returns them.  The ``extra`` tokens are
+        pending (see :meth:`fork`, :meth:`reserve`) until they are appended."""
         t, width, ln, R = self._seqs(table, lens)
         r, most = nodes.shape
         _launch(self._lib.dartree_cache_commit, self._idx, stream, self._ref, t, width, ln,
