@@ -470,7 +470,8 @@ size_t dartree_cache_page_bytes(int32_t page_tokens, int32_t Hkv, int32_t dh);
  * of 8, at least Hkv * dh for the tokens; K and V 16-byte aligned), so that
  * slices of a fused projection's output are read in place.  count [R] (NULL:
  * n for all): only the first count[r] tokens are written.  A row with
- * lens[r] < 0 is skipped; lens is not changed.
+ * lens[r] < 0 is skipped; lens is not changed.  A token whose page another
+ * row holds too (refs above 1) is not written, and flagged.
  * Per 16 dimensions: scale = e4m3(max|x| / 6), code = e2m1(x / scale), both
  * to nearest even and saturating (x divided by k_scale or v_scale first);
  * NaN counts as 0. */

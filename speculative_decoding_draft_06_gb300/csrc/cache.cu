@@ -16,16 +16,17 @@ namespace {
 // are touched in their order and the codes of a warp's tokens are one
 // contiguous piece.
 // Bound by memory and, in append, by issue as well (0.83 instructions a cycle
-// and scheduler): 2 x 16000 tokens of 8 heads of 128 take 58 us in and out,
-// 336 MB, 87% of a copy's rate (9 us more with loads behind the page lookup and
+// and scheduler): 2 x 16000 tokens of 8 heads of 128 take 59 us in and out (the
+// look at a page's holders 1 of them), 336 MB, 86% of a copy's rate (9 us more with loads behind the page lookup and
 // plain stores; several heads per warp, one lookup for all, 4 to 8 more: fewer
-// loads in flight).  A step's 8 x 129 tokens: 5.4 us in and out.
+// loads in flight).  A step's 8 x 129 tokens: 5.7 us in and out.
 struct TokenParams {
   CacheView c;
   const uint16_t *K, *V;   // append: input rows
   uint16_t *Ko, *Vo;       // read: output rows
   long long req_stride, token_stride;
   const int32_t *table, *lens, *count;
+  const int32_t* refs;     // append: the pages' holders (or null)
   int max_pages, offset, R, n, groups;  // groups: ceil(n / tokens per warp)
   int* err;
 };
@@ -36,6 +37,7 @@ struct TokenSlot {
   const uint8_t* base;  // the token's page's chunk of head h (live and *paged)
   int t;                // token within the page
   bool paged;
+  int page;
 };
 
 // Data that is read once (issued here, whatever the compiler would move).
@@ -76,6 +78,7 @@ __device__ __forceinline__ void find_slot(const TokenParams& p, TokenSlot& s) {
     const int page = p.table[static_cast<size_t>(s.r) * p.max_pages + slot];
     if (page >= 0 && page < p.c.pages) {
       s.paged = true;
+      s.page = page;
       s.base = p.c.pool + static_cast<size_t>(page) * p.c.page_bytes + static_cast<size_t>(s.h) * p.c.chunk;
       s.t = static_cast<int>(pos & ((1 << p.c.log_page) - 1));
     }
@@ -131,12 +134,17 @@ __global__ void __launch_bounds__(256) k_cache_append(const TokenParams p) {
   const uint4 vin[2] = {load_once(v), load_once(v + 1)};
   find_slot(p, s);
   if (!s.live || !s.paged) return;
+  const int holders = p.refs ? p.refs[s.page] : 1;  // (on its way during the arithmetic)
   uint8_t* base = const_cast<uint8_t*>(s.base);
   const int codes = (DH / 2) << p.c.log_page;  // bytes of a chunk's key codes
   const int half = p.c.chunk >> 1;
   uint32_t sk, sv;
   const uint2 ck = quantise16(kin, 1.f / p.c.k_scale, &sk);
   const uint2 cv = quantise16(vin, 1.f / p.c.v_scale, &sv);
+  if (holders > 1) {  // other rows read it
+    if (s.blk == 0 && s.h == 0 && p.err) atomicOr(p.err, DT_ERR_BAD_INDEX);
+    return;
+  }
   *reinterpret_cast<uint2*>(base + s.t * (DH / 2) + s.blk * 8) = ck;
   base[codes + s.t * (DH / 16) + s.blk] = static_cast<uint8_t>(sk);
   *reinterpret_cast<uint2*>(base + half + s.t * (DH / 2) + s.blk * 8) = cv;
@@ -727,6 +735,7 @@ extern "C" dartree_status dartree_cache_append(const dartree_cache* cache, int32
     return cache_fail(DARTREE_ERR_INVALID_ARG, "strides must be multiples of 8 elements, tokens not overlapping");
   p.K = static_cast<const uint16_t*>(K);
   p.V = static_cast<const uint16_t*>(V);
+  p.refs = cache->refs;
   p.req_stride = req_stride;
   p.token_stride = token_stride;
   return cache_launched(launch_kernel(p.c.dh == 128 ? k_cache_append<128> : k_cache_append<64>, dim3(blocks),

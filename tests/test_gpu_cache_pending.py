@@ -167,3 +167,33 @@ def test_fork_and_reserve_with_pending_tokens(seed):
         same(cache, want, table, lens)
         pending = 0
     cache.check()
+
+
+def test_a_shared_page_is_not_written():
+    """append leaves a page that two rows hold as it is and flags the token;
+    tokens of the row's own pages are written."""
+    P, Hkv, dh = 16, 3, 128
+    cache = dtl.KVCache(1, 8, page_tokens=P, Hkv=Hkv, dh=dh)
+    table, lens = cu(np.full((2, 4), -1)), cu([0, 0])
+    assert host(cache.reserve(table, lens, cu([32, 0]))).tolist() == [1, 1]
+    K = torch.randn(2, 20, Hkv, dh, device="cuda").to(torch.bfloat16)
+    cache.append(0, K, K, table, lens, count=cu([20, 0]))
+    lens[0] = 32
+    assert host(cache.fork(table, lens, cu([0]), cu([1]))).tolist() == [1]
+    assert host(cache.reserve(table, lens, cu([20, 20]))).tolist() == [1, 1]
+    cache.check()
+    pool = cache.pool.clone()
+    cache.append(0, -K, -K, table, lens, offset=-4)          # positions 28 .. 47: 28 .. 31 are shared
+    with pytest.raises(dtl.DartreeError):
+        cache.check()
+    t = host(table)
+    assert torch.equal(cache.pool[0, t[0, :2]], pool[0, t[0, :2]])
+    k, _ = cache.read(0, table, lens, 16)
+    assert np.array_equal(host(k.double()), -ref.values(*ref.quantise(host(K[:, 4:].double()))))
+    cache.append(0, -K, -K, table, lens)                     # their own pages alone
+    cache.check()
+    cache.release(table, lens, cu([1]), cu([0]))
+    cache.append(0, -K, -K, table, lens, offset=-4, count=cu([20, 0]))
+    cache.check()
+    k, _ = cache.read(0, table, lens, 20, offset=-4)
+    assert np.array_equal(host(k[0].double()), -ref.values(*ref.quantise(host(K[0].double()))))
