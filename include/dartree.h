@@ -484,11 +484,15 @@ dartree_status dartree_cache_append(const dartree_cache *cache, int32_t layer, c
 /* The values of the tokens lens[r] + offset + i, i < min(n, count[r]), as
  * bf16: K, V [R][n][Hkv][dh], dense, 16-byte aligned.  A token without a page
  * reads as 0; tokens behind count[r] and rows with lens[r] < 0 are left as
- * they were. */
+ * they were (_ex: with zero_rest != 0 they are written as 0). */
 dartree_status dartree_cache_read(const dartree_cache *cache, int32_t layer, void *K, void *V,
                                   const int32_t *table, int32_t max_pages, const int32_t *lens,
                                   int32_t offset, const int32_t *count, int32_t R, int32_t n,
                                   int32_t *err, void *stream);
+dartree_status dartree_cache_read_ex(const dartree_cache *cache, int32_t layer, void *K, void *V,
+                                     const int32_t *table, int32_t max_pages, const int32_t *lens,
+                                     int32_t offset, const int32_t *count, int32_t R, int32_t n,
+                                     int32_t zero_rest, int32_t *err, void *stream);
 
 /* Attention of single tokens or draft trees over the cache, one layer:
  *   Q    [R][B+1][Hq][dh] bf16, q_token_stride elements between the rows
@@ -506,7 +510,9 @@ dartree_status dartree_cache_read(const dartree_cache *cache, int32_t layer, voi
  * O = softmax(scale * q.k) v; products and sums in fp32, the softmax weights
  * in fp16 for the product with the values; O = 0 for a row that sees
  * nothing.  Tokens without a page are not seen (and flagged).  A row with
- * lens[r] < 0 is skipped.  B <= 1024, Hq % Hkv == 0; Q, O 16-byte aligned.
+ * lens[r] < 0 is skipped (with n_nodes[r] < 0, too): left as it was.  _ex:
+ * with zero_rest != 0 the rows that are left otherwise are written as 0.
+ * B <= 1024, Hq % Hkv == 0; Q, O 16-byte aligned.
  * work: dartree_cache_attention_workspace() bytes of scratch, 16-byte
  * aligned, that overlapping calls must not share (its contents need no
  * preparation; NULL when the size is 0). */
@@ -516,6 +522,13 @@ dartree_status dartree_cache_attention(const dartree_cache *cache, int32_t layer
                                        int32_t max_pages, const int32_t *lens, int32_t R, int32_t B,
                                        int32_t max_len, int32_t Hq, float scale, void *O,
                                        void *work, size_t work_bytes, int32_t *err, void *stream);
+dartree_status dartree_cache_attention_ex(const dartree_cache *cache, int32_t layer, const void *Q,
+                                          int64_t q_token_stride, const uint32_t *mask,
+                                          const int32_t *n_nodes, const int32_t *table,
+                                          int32_t max_pages, const int32_t *lens, int32_t R,
+                                          int32_t B, int32_t max_len, int32_t Hq, float scale,
+                                          int32_t zero_rest, void *O, void *work,
+                                          size_t work_bytes, int32_t *err, void *stream);
 size_t dartree_cache_attention_workspace(int32_t R, int32_t B, int32_t max_len, int32_t Hq,
                                          int32_t Hkv, int32_t dh);
 

@@ -28,6 +28,7 @@ struct TokenParams {
   const int32_t *table, *lens, *count;
   const int32_t* refs;     // append: the pages' holders (or null)
   int max_pages, offset, R, n, groups;  // groups: ceil(n / tokens per warp)
+  int zero_rest;           // read: tokens that no row has are written as 0
   int* err;
 };
 
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(256) k_cache_read(const TokenParams p) {
   TokenSlot s = token_of<DH>(p);
   if (s.r >= p.R) return;
   find_slot(p, s);
-  if (!s.live) return;
+  if (!s.live && !(p.zero_rest && s.i < p.n)) return;
   const size_t at = ((static_cast<size_t>(s.r) * p.n + s.i) * p.c.Hkv + s.h) * DH + s.blk * 16;
   uint4* k = reinterpret_cast<uint4*>(p.Ko + at);
   uint4* v = reinterpret_cast<uint4*>(p.Vo + at);
@@ -742,10 +743,10 @@ extern "C" dartree_status dartree_cache_append(const dartree_cache* cache, int32
                                       dim3(256), 0, static_cast<cudaStream_t>(stream), true, p));
 }
 
-extern "C" dartree_status dartree_cache_read(const dartree_cache* cache, int32_t layer, void* K, void* V,
-                                             const int32_t* table, int32_t max_pages, const int32_t* lens,
-                                             int32_t offset, const int32_t* count, int32_t R, int32_t n,
-                                             int32_t* err, void* stream) {
+extern "C" dartree_status dartree_cache_read_ex(const dartree_cache* cache, int32_t layer, void* K, void* V,
+                                                const int32_t* table, int32_t max_pages, const int32_t* lens,
+                                                int32_t offset, const int32_t* count, int32_t R, int32_t n,
+                                                int32_t zero_rest, int32_t* err, void* stream) {
   using namespace dt;
   TokenParams p{};
   unsigned blocks = 0;
@@ -754,8 +755,16 @@ extern "C" dartree_status dartree_cache_read(const dartree_cache* cache, int32_t
   if (s != DARTREE_OK) return s;
   p.Ko = static_cast<uint16_t*>(K);
   p.Vo = static_cast<uint16_t*>(V);
+  p.zero_rest = zero_rest != 0;
   return cache_launched(launch_kernel(p.c.dh == 128 ? k_cache_read<128> : k_cache_read<64>, dim3(blocks),
                                       dim3(256), 0, static_cast<cudaStream_t>(stream), true, p));
+}
+
+extern "C" dartree_status dartree_cache_read(const dartree_cache* cache, int32_t layer, void* K, void* V,
+                                             const int32_t* table, int32_t max_pages, const int32_t* lens,
+                                             int32_t offset, const int32_t* count, int32_t R, int32_t n,
+                                             int32_t* err, void* stream) {
+  return dartree_cache_read_ex(cache, layer, K, V, table, max_pages, lens, offset, count, R, n, 0, err, stream);
 }
 
 extern "C" dartree_status dartree_cache_reserve_ex(const dartree_cache* cache, int32_t* table, int32_t max_pages,

@@ -599,6 +599,20 @@ cudaError_t launch_join(const CacheAttnParams& p, cudaStream_t st) {
   return launch_kernel(k_cache_attention_join<DH, 1>, dim3((p.rows + 7) / 8, p.c.Hkv, p.R), dim3(256), 0, st, true, p);
 }
 
+// Zeros in the rows that a call leaves as they were: those behind a request's
+// tree, all of a skipped one.  Grid (R).  (Where it is asked for, a launch of
+// its own, 0.6 to 3 us: in the attention kernels its code made 32 trees 5% slower.)
+__global__ void __launch_bounds__(256) k_cache_zero_rest(const CacheAttnParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int r = blockIdx.x;
+  Span sp;
+  const int first = request_span(p, r, &sp) ? sp.n + 1 : 0;
+  const size_t per = static_cast<size_t>(p.Hq) * p.c.dh / 8;  // 16-byte units of a node
+  uint4* o = reinterpret_cast<uint4*>(p.O) + static_cast<size_t>(r) * (p.B + 1) * per;
+  for (size_t i = first * per + threadIdx.x; i < (p.B + 1) * per; i += 256) o[i] = make_uint4(0, 0, 0, 0);
+}
+
 // How a call is cut: up to kTreeRows rows per key/value head by the kernel
 // above, in tiles of 64 keys, four warps a tile each; more by the tensor-core
 // kernel in tiles of 256 rows and 128 keys.  The keys are split until the GPU
@@ -676,13 +690,13 @@ extern "C" size_t dartree_cache_attention_workspace(int32_t R, int32_t B, int32_
   return pl[0].work;
 }
 
-extern "C" dartree_status dartree_cache_attention(const dartree_cache* cache, int32_t layer, const void* Q,
-                                                  int64_t q_token_stride, const uint32_t* mask,
-                                                  const int32_t* n_nodes, const int32_t* table,
-                                                  int32_t max_pages, const int32_t* lens, int32_t R,
-                                                  int32_t B, int32_t max_len, int32_t Hq, float scale,
-                                                  void* O, void* work, size_t work_bytes, int32_t* err,
-                                                  void* stream) {
+extern "C" dartree_status dartree_cache_attention_ex(const dartree_cache* cache, int32_t layer, const void* Q,
+                                                     int64_t q_token_stride, const uint32_t* mask,
+                                                     const int32_t* n_nodes, const int32_t* table,
+                                                     int32_t max_pages, const int32_t* lens, int32_t R,
+                                                     int32_t B, int32_t max_len, int32_t Hq, float scale,
+                                                     int32_t zero_rest, void* O, void* work, size_t work_bytes,
+                                                     int32_t* err, void* stream) {
   using namespace dt;
   CacheAttnParams p{};
   if (const char* why = cache_view(cache, &p.c)) return cache_fail(DARTREE_ERR_INVALID_ARG, why);
@@ -725,6 +739,7 @@ extern "C" dartree_status dartree_cache_attention(const dartree_cache* cache, in
   cudaError_t e = cudaSuccess;
   if (!p.err) e = cudaGetSymbolAddress(reinterpret_cast<void**>(&p.err), g_cache_err);
   if (e != cudaSuccess) return cache_launched(e);
+  if (zero_rest) e = launch_kernel(k_cache_zero_rest, dim3(R), dim3(256), 0, st, true, p);
   // (without n_nodes it is known here whether rows are left over)
   const int odd = pl[0].rows % kTreeTile;
   const int run = launches > 1 && !n_nodes && (odd == 0 || odd > kTreeTail) ? 1 : launches;
@@ -748,4 +763,15 @@ extern "C" dartree_status dartree_cache_attention(const dartree_cache* cache, in
   if (e == cudaSuccess && first.n_split > 1 && !first.cluster)
     e = dh == 128 ? launch_join<128>(first, st) : launch_join<64>(first, st);
   return cache_launched(e);
+}
+
+extern "C" dartree_status dartree_cache_attention(const dartree_cache* cache, int32_t layer, const void* Q,
+                                                  int64_t q_token_stride, const uint32_t* mask,
+                                                  const int32_t* n_nodes, const int32_t* table,
+                                                  int32_t max_pages, const int32_t* lens, int32_t R,
+                                                  int32_t B, int32_t max_len, int32_t Hq, float scale,
+                                                  void* O, void* work, size_t work_bytes, int32_t* err,
+                                                  void* stream) {
+  return dartree_cache_attention_ex(cache, layer, Q, q_token_stride, mask, n_nodes, table, max_pages, lens, R, B,
+                                    max_len, Hq, scale, 0, O, work, work_bytes, err, stream);
 }

@@ -127,9 +127,14 @@ def load():
                                       _i32, _i32, _vp, _vp]),
         "dartree_cache_read": (st, [cache, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32,
                                     _vp, _vp]),
+        "dartree_cache_read_ex": (st, [cache, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32,
+                                       _i32, _vp, _vp]),
         "dartree_cache_attention": (st, [cache, _i32, _vp, i64, _vp, _vp, _vp, _i32, _vp, _i32,
                                          _i32, _i32, _i32, ctypes.c_float, _vp, _vp,
                                          ctypes.c_size_t, _vp, _vp]),
+        "dartree_cache_attention_ex": (st, [cache, _i32, _vp, i64, _vp, _vp, _vp, _i32, _vp, _i32,
+                                            _i32, _i32, _i32, ctypes.c_float, _i32, _vp, _vp,
+                                            ctypes.c_size_t, _vp, _vp]),
         "dartree_cache_attention_workspace": (ctypes.c_size_t, [_i32] * 6),
         "dartree_cache_reserve": (st, [cache, _vp, _i32, _vp, _vp, _i32, _vp, _vp]),
         "dartree_cache_reserve_ex": (st, [cache, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp]),
@@ -520,13 +525,12 @@ def _floats(name: str, t: torch.Tensor, idx: int, n: int) -> int:
     return t.data_ptr()
 
 
-def _alloc(stream, shape, dtype, dev, zero: bool = False) -> torch.Tensor:
+def _alloc(stream, shape, dtype, dev) -> torch.Tensor:
     """A tensor whose memory belongs to the call's stream."""
-    make = torch.zeros if zero else torch.empty
     if stream is None:
-        return make(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 # the current stream's handle without a Stream object (which costs as much as
@@ -630,24 +634,24 @@ class KVCache:
     def read(self, layer: int, table, lens, n: int, *, offset: int = 0,
              count: torch.Tensor | None = None, out: tuple | None = None, stream=None) -> tuple:
         """The values of the tokens lens[r] + offset + i, i < n, as bf16 (K,
-        V) [R, n, Hkv, dh] (dartree_cache_read).  Tokens behind count[r] keep
-        what ``out`` holds (zeros in a new one)."""
+        V) [R, n, Hkv, dh] (dartree_cache_read_ex).  Tokens behind count[r] and
+        rows with lens[r] < 0 keep what ``out`` holds (zeros in a new one)."""
         t, width, ln, R = self._seqs(table, lens)
         shape = (R, n, self.Hkv, self.dh)
-        if out is None:
+        new = out is None
+        if new:
             # (two calls: halves of one tensor cost 10 us more)
-            zero = count is not None
-            out = (_alloc(stream, shape, torch.bfloat16, self.dev, zero),
-                   _alloc(stream, shape, torch.bfloat16, self.dev, zero))
+            out = (_alloc(stream, shape, torch.bfloat16, self.dev),
+                   _alloc(stream, shape, torch.bfloat16, self.dev))
         else:
             for x in out:
                 if x.dtype not in _BF16 or x.get_device() != self._idx or not x.is_contiguous():
                     raise TypeError(f"out must be contiguous bf16 tensors on {self.dev}")
                 if x.shape != shape:
                     raise ValueError(f"out has shape {tuple(x.shape)}, expected {shape}")
-        _launch(self._lib.dartree_cache_read, self._idx, stream, self._ref, layer,
+        _launch(self._lib.dartree_cache_read_ex, self._idx, stream, self._ref, layer,
                 out[0].data_ptr(), out[1].data_ptr(), t, width, ln, offset,
-                None if count is None else _ints("count", count, self._idx, R), R, n, self._err)
+                None if count is None else _ints("count", count, self._idx, R), R, n, new, self._err)
         return out
 
     def attention(self, layer: int, Q: torch.Tensor, table, lens, *, max_len: int,
@@ -655,9 +659,10 @@ class KVCache:
                   scale: float | None = None, out: torch.Tensor | None = None,
                   work: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Attention of Q [R, B+1, Hq, dh] bf16 (row 0 the root, then the tree
-        nodes; B = 0: single tokens) over the cache (dartree_cache_attention)
+        nodes; B = 0: single tokens) over the cache (dartree_cache_attention_ex)
         -> O bf16 [R, B+1, Hq, dh].  ``max_len`` bounds lens[r] + n_nodes[r].
-        Rows behind n_nodes[r] keep what ``out`` holds (zeros in a new one)."""
+        Rows behind n_nodes[r] and requests with lens[r] < 0 keep what ``out``
+        holds (zeros in a new one)."""
         t, width, ln, R = self._seqs(table, lens)
         idx, dh = self._idx, self.dh
         if Q.dtype not in _BF16 or Q.get_device() != idx:
@@ -679,8 +684,9 @@ class KVCache:
                 raise ValueError("a tree needs its mask")
             m = _ints("mask", mask, idx, R * B * ((B + 31) // 32))
         nn = None if n_nodes is None else _ints("n_nodes", n_nodes, idx, R)
-        if out is None:
-            out = _alloc(stream, (R, rows, Hq, dh), torch.bfloat16, self.dev, n_nodes is not None)
+        new = out is None
+        if new:
+            out = _alloc(stream, (R, rows, Hq, dh), torch.bfloat16, self.dev)
         elif out.dtype not in _BF16 or out.get_device() != idx or not out.is_contiguous():
             raise TypeError(f"out must be a contiguous bf16 tensor on {self.dev}")
         elif out.shape != (R, rows, Hq, dh):
@@ -700,9 +706,9 @@ class KVCache:
         elif need:
             work = _alloc(stream, (need,), torch.uint8, self.dev)
             wp, wb = work.data_ptr(), need
-        _launch(self._lib.dartree_cache_attention, idx, stream, self._ref, layer, Q.data_ptr(), sq, m,
+        _launch(self._lib.dartree_cache_attention_ex, idx, stream, self._ref, layer, Q.data_ptr(), sq, m,
                 nn, t, width, ln, R, B, max_len, Hq, dh ** -0.5 if scale is None else scale,
-                out.data_ptr(), wp, wb, self._err)
+                new, out.data_ptr(), wp, wb, self._err)
         return out
 
     # ------------------------------------------------------ page operations
