@@ -192,11 +192,8 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
       top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
     top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
     top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
-    // 2^-e with 2^e <= top < 2^(e+1) (e within what the factors can be)
-    int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-    e = top > 0.f ? max(-100, min(e, 100)) : 0;
-    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    const float f = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    float down;
+    const float f = row_exponent(p, top, &down);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       fac[n][i] = __shfl_sync(kFullMask, f, (2 * c + i) * 4);
@@ -731,10 +728,10 @@ extern "C" dartree_status dartree_cache_attention_ex(const dartree_cache* cache,
   p.max_len = max_len;
   p.Hq = Hq;
   p.words = (B + 31) / 32;
-  p.scale_log2 = scale * 1.4426950408889634f * p.c.k_scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
   p.O = static_cast<uint16_t*>(O);
   p.err = err;
-  if (!(p.scale_log2 <= 3.0e38f)) return cache_fail(DARTREE_ERR_INVALID_ARG, "scale times k_scale is too large");
+  if (!(p.scale_log2 * p.c.k_scale <= 3.0e38f)) return cache_fail(DARTREE_ERR_INVALID_ARG, "scale times k_scale is too large");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (!p.err) e = cudaGetSymbolAddress(reinterpret_cast<void**>(&p.err), g_cache_err);

@@ -28,7 +28,7 @@ struct CacheAttnParams {
   int n_split, split_tiles;  // key tiles per split
   int cluster;               // the splits are one cluster and join there
   int tail;                  // the few-rows kernel works on the rows behind the whole tiles
-  float scale_log2;          // scale * log2(e) * k_scale
+  float scale_log2;          // scale * log2(e)
   uint16_t* O;               // [R][B+1][Hq][dh]
   float* part;               // [R][Hkv][m_tiles][n_split][tile_rows][dh + kPartHead] (n_split > 1)
   int* err;
@@ -107,6 +107,19 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+
+// A query row becomes fp16 as multiples of 2^e, its largest magnitude (`top`)
+// in [1, 2) of them, or below 4 and above 2^-8 at the ends of bf16's range.
+// *down: 2^-e.  Returns the factor of its scores to base 2, 2^e scale log2(e)
+// k_scale, held between 2^-126 (0 would make NaN of the keys that are not seen)
+// and 2^100 (a score is below 2^21, so no product overflows): scores, whose
+// unit is 2^-34 or more, weigh the same beyond either end.
+__device__ __forceinline__ float row_exponent(const CacheAttnParams& p, float top, float* down) {
+  const int e = top > 0.f ? max(-126, min(static_cast<int>(__float_as_uint(top) >> 23) - 127, 126)) : 0;
+  *down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  const float f = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.c.k_scale;
+  return fmaxf(fminf(f, 0x1p100f), 0x1p-126f);
 }
 
 // Row q of a key/value head in the output (node q / g, query head hk g + q % g).

@@ -185,14 +185,6 @@ __device__ __forceinline__ uint32_t row_sees(int pos, int Lp, const uint32_t* mr
   return (nodes << np) | ((1u << np) - 1u);
 }
 
-// A query row: its factor to base 2 and its power of two (bf16 words w).
-__device__ __forceinline__ float row_exponent(float top, float scale_log2, float* down) {
-  int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-  e = top > 0.f ? max(-100, min(e, 100)) : 0;
-  *down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-  return scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-}
-
 template <int DH>
 __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnParams p) {
   using L = TreeSmem<DH>;
@@ -314,7 +306,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
 #pragma unroll
       for (int o = 1; o < kRowLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
       float down;
-      const float fac = row_exponent(top, p.scale_log2, &down);
+      const float fac = row_exponent(p, top, &down);
       if (k == 0) s_fac[row] = fac;
       uint32_t y[4];
 #pragma unroll
