@@ -207,8 +207,8 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
     }
   }
   float o[NQ][kSteps][4];           // dim tile j: dims rr DH/8 + 2 j, + 1 of rows 8 n + 2 c, + 1
-  float m[NQ][2], l[NQ][2];         // reference maximum (base 2), sum
-  float limit[NQ][2];               // the unscaled score above which m rises
+  float m[NQ][2], l[NQ][2];         // reference maximum (a score, before its factor), sum
+  float limit[NQ][2];               // the score above which m rises
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     m[n][0] = m[n][1] = limit[n][0] = limit[n][1] = -INFINITY;
@@ -263,8 +263,8 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
       }
     }
     // ---- x = 2 t + i: key 16 h + 8 t + perm(rr), row 8 n + 2 c + i.  The
-    // scores stay as they are (a row's factor to base 2 comes with the
-    // exponent); the reference rises where one passes `limit`
+    // scores stay as they are (a row's factor to base 2 multiplies their
+    // distance from the reference); the reference rises where one passes `limit`
     bool up = false;
     float top[NQ][2];
 #pragma unroll
@@ -302,10 +302,9 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
           for (int d = 4; d < 32; d *= 2) t = fmaxf(t, __shfl_xor_sync(kFullMask, t, d));
           al[x] = 1.f;
           if (t > limit[n][x]) {
-            t *= fac[n][x];
-            al[x] = ex2(m[n][x] - t);  // (0 from -inf)
+            al[x] = ex2((m[n][x] - t) * fac[n][x]);  // (0 from -inf)
             m[n][x] = t;
-            limit[n][x] = __fdividef(t + kRaise, fac[n][x]);
+            limit[n][x] = rise_limit(t, fac[n][x]);
             l[n][x] *= al[x];
           }
         }
@@ -318,16 +317,18 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
         }
       }
     }
+    // the weights: 2^((s - m) fac + kBias) (s fac - m fac would be off by 2^-24 of
+    // m fac, which from 2^27 on is more than fp16 holds)
     uint32_t pb[2][NQ][2];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      const float sub0 = m[n][0] == -INFINITY ? 0.f : kBias - m[n][0];
-      const float sub1 = m[n][1] == -INFINITY ? 0.f : kBias - m[n][1];
+      const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const float p0 = ex2(fmaf(s[h][n][2 * t], fac[n][0], sub0)), p1 = ex2(fmaf(s[h][n][2 * t + 1], fac[n][1], sub1));
+          const float p0 = ex2(fmaf(s[h][n][2 * t] - m0, fac[n][0], kBias));
+          const float p1 = ex2(fmaf(s[h][n][2 * t + 1] - m1, fac[n][1], kBias));
           l[n][0] += p0;
           l[n][1] += p1;
           pb[h][n][t] = transpose8x8(pack_f16(p0, p1));
@@ -415,7 +416,7 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
 #pragma unroll
       for (int d = 4; d < 32; d *= 2) l[n][x] += __shfl_xor_sync(kFullMask, l[n][x], d);
       const int row = 8 * n + 2 * c + x;
-      if (rr == 0) sm.ml[warp][row] = make_float2(m[n][x], l[n][x]);
+      if (rr == 0) sm.ml[warp][row] = make_float2(m[n][x] * fac[n][x], l[n][x]);
       float* dst = &sm.red[warp][row][rr * (DH / 8)];
 #pragma unroll
       for (int j = 0; j < kSteps; j += 2)

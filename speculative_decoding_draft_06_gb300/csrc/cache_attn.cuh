@@ -122,6 +122,10 @@ __device__ __forceinline__ float row_exponent(const CacheAttnParams& p, float to
   return fmaxf(fminf(f, 0x1p100f), 0x1p-126f);
 }
 
+// The score above which a reference m rises: kRaise behind it in the exponent
+// (rounded down: no weight passes 2^(kBias + kRaise) and fp16's range).
+__device__ __forceinline__ float rise_limit(float m, float fac) { return __fadd_rd(m, __fdividef(kRaise, fac)); }
+
 // Row q of a key/value head in the output (node q / g, query head hk g + q % g).
 __device__ __forceinline__ size_t cache_out_row(const CacheAttnParams& p, int r, int hk, int q) {
   const int nd = q / p.g;

@@ -52,6 +52,13 @@ constexpr int kStages = 2;
 // issued, and they after the weights of the tile three before are there)
 constexpr int kValid = 4;
 constexpr int kTreeSorted = 256;  // requests that are taken longest first (each CTA ranks them: R^2 / 832 steps)
+// A weight is 2^(s fac - m + kBias) with m = ref fac rounded, off by 2^-24 of
+// itself.  Where it would pass kFar, whose unit is 1/2, the row goes on with the
+// factor that puts it there: the weights of scores within 2^-18 of the largest
+// then differ by less than they should, those of all others are 0 either way (a
+// score's own sum in fp32 is off by as much).  Without it a weight passes fp16's
+// range from 2^27 on; taking the distance s - ref first costs 4% of the time.
+constexpr float kFar = 4194304.f;
 constexpr uint32_t kTmemCols = 512;  // S of row tile i, buffer b: 128 i + 64 b; O of row tile i: 256 + 128 i; P over S
 constexpr uint32_t kColO = 256;
 
@@ -205,6 +212,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ float s_fac[2 * kMRows], s_top[2][2 * kMRows];  // of the rows: factor; by half: maximum, sum
+  __shared__ float s_ref[2][2 * kMRows];                     // by half: the reference as a score
   __shared__ __align__(16) uint8_t s_valid[kValid][kKeys / 8];  // bit k of a tile: key k is there
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -487,9 +495,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     const int node = row < rows ? q / p.g : 0;
     const uint32_t* mrow = node >= 1 ? p.mask + (static_cast<size_t>(r) * p.B + node - 1) * p.words : nullptr;
     bool go = wait_w(&q_full[i], 0);  // (the same in both warps after every barrier)
-    const float fac = s_fac[row];
+    float fac = s_fac[row];
     float m = -INFINITY, l = 0.f;  // the row's reference (the same in both threads), this half's sum
-    float limit = -INFINITY;       // the unscaled score above which the reference rises
+    float& ref = s_ref[half][row]; // the reference as a score
+    float limit = -INFINITY;       // the score above which the reference rises
+    ref = -INFINITY;
     for (int u = 0; u < steps; ++u) {
       const int f = u >> 1, b = u & 1, key0 = t_beg * kKeys + u * kStepKeys + half * (kStepKeys / 2);
       go = go && wait_w(&s_full[2 * i + b], static_cast<uint32_t>(f) & 1u);
@@ -545,10 +555,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
         top = fmaxf(s_top[0][row], s_top[1][row]);
         float alpha = 1.f;
         if (top > limit) {
-          const float y = top * fac;
-          alpha = ex2(m - y);  // (0 from -inf)
-          m = y;
-          limit = __fdividef(y + kRaise, fac);
+          const float full = s_fac[row], y = top * full;
+          alpha = ex2((ref - top) * full);  // (0 from -inf)
+          ref = top;
+          fac = fabsf(y) > kFar ? full * __fdividef(kFar, fabsf(y)) : full;
+          m = top * fac;
+          limit = rise_limit(top, fac);
           l *= alpha;
         }
         bool landed = true;
@@ -591,7 +603,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     if (!have || m == -INFINITY) l = 0.f;
     const float inv = l > 0.f ? p.c.v_scale / l : 0.f;
     if (half == 0 && p.n_split > 1 && row < rows)
-      *reinterpret_cast<float2*>(cache_part_row(p, r, hk, mt, split, row)) = make_float2(m, l);
+      *reinterpret_cast<float2*>(cache_part_row(p, r, hk, mt, split, row)) = make_float2(ref * s_fac[row], l);
     // O by way of the row tile's queries' place in shared memory (the scores
     // are done), an eighth of the dims at a time, so that a warp's accesses are
     // whole pieces of rows: kC dims of a row by kC / 4 lanes
