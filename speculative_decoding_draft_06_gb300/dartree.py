@@ -610,8 +610,8 @@ class KVCache:
     def append(self, layer: int, K: torch.Tensor, V: torch.Tensor, table, lens, *, offset: int = 0,
                count: torch.Tensor | None = None, stream=None) -> None:
         """Quantise K, V [R, n, Hkv, dh] bf16 into positions lens[r] + offset
-        + i (dartree_cache_append); request and token strides are free, the
-        same in both."""
+        + i (dartree_cache_append); request and token strides are multiples of
+        8, the same in both."""
         t, width, ln, R = self._seqs(table, lens)
         idx, Hkv, dh = self._idx, self.Hkv, self.dh
         if K.dtype not in _BF16 or K.get_device() != idx:
@@ -622,11 +622,15 @@ class KVCache:
         if K.shape != want or V.shape != want:
             raise ValueError(f"K {tuple(K.shape)} / V {tuple(V.shape)} do not match R={R}, "
                              f"Hkv={Hkv}, dh={dh}")
-        sr, sn, sh, sd = K.stride()
-        if V.stride() != (sr, sn, sh, sd) or sd != 1 or (sh != dh and Hkv > 1):
+        (sr, sn, sh, sd), (vr, vn, vh, vd) = K.stride(), V.stride()
+        if R == 1:  # (a dimension of one has no stride)
+            sr = vr = 0
+        if n == 1:
+            sn = vn = Hkv * dh
+        if Hkv == 1:
+            sh = vh = dh
+        if (sr, sn, sh, sd) != (vr, vn, vh, vd) or sd != 1 or sh != dh:
             raise ValueError("K and V need equal strides, dense in heads and dims")
-        if n == 1 and sn < Hkv * dh:
-            sn = Hkv * dh
         _launch(self._lib.dartree_cache_append, idx, stream, self._ref, layer, K.data_ptr(),
                 V.data_ptr(), sr, sn, t, width, ln, offset,
                 None if count is None else _ints("count", count, idx, R), R, n, self._err)
