@@ -600,8 +600,10 @@ class KVCache:
         return _ints("table", table, idx, R * width), width, _ints("lens", lens, idx, R), R
 
     def check(self) -> None:
-        """Synchronises and raises if a call since the last check met a bad
-        index (a token without a page, a row or page out of range)."""
+        """Synchronises the device and raises if a call since the last check, on
+        any stream, met a bad index (a token without a page, a row or page out
+        of range)."""
+        torch.cuda.synchronize(self.dev)
         e = int(self.err.item())
         if e:
             self.err.zero_()
