@@ -581,8 +581,9 @@ dartree_status dartree_cache_fork_ex(const dartree_cache *cache, int32_t *table,
  * whose key and value the next step appends; until then it is pending for
  * dartree_cache_fork_ex and _reserve_ex).  nodes, len as dartree_accept
  * writes them (ranks rising in a row).  A row whose ranks do not rise, whose
- * tokens have no page, or with lens[r] < 0 is left as it was (the former two
- * are flagged).  R <= 2^24, max_len * Hkv * layers < 2^25. */
+ * tokens have no page, whose length or positions would pass 2^31 - 1, or with
+ * lens[r] < 0 is left as it was (all but the last are flagged).  R <= 2^24,
+ * 18 * max_len * Hkv * (ceil(layers / 8) + 1) <= 2^31. */
 dartree_status dartree_cache_commit(const dartree_cache *cache, const int32_t *table,
                                     int32_t max_pages, int32_t *lens, const int32_t *nodes,
                                     const int32_t *len, int32_t R, int32_t max_len, int32_t extra,

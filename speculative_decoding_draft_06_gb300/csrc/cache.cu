@@ -591,10 +591,10 @@ __device__ __forceinline__ int commit_count(const CommitParams& p, int r, int* b
   const int m = max(0, min(p.len[r], p.max_len));
   const int32_t* nodes = p.nodes + static_cast<size_t>(r) * p.max_len;
   const int32_t* row = p.table + static_cast<size_t>(r) * p.max_pages;
-  bool b = false;
+  bool b = static_cast<long long>(len) + m + p.extra > INT32_MAX;  // (lengths and positions are 32 bits)
   for (int k = threadIdx.x; k < m; k += blockDim.x) {
     const int node = nodes[k];
-    b |= node < 0 || (k > 0 && node <= nodes[k - 1]);
+    b |= node < 0 || (k > 0 && node <= nodes[k - 1]) || static_cast<long long>(len) + node > INT32_MAX;
     if (b) break;
     const long long from = (static_cast<long long>(len) + node) >> p.log_page;
     const long long to = (static_cast<long long>(len) + k) >> p.log_page;
