@@ -35,6 +35,8 @@
 // a producer warp and rows as the 16-row operand 315 us for the 64; warps with
 // rings of their own and keys as that operand 246; four code bytes to a
 // conversion 198; stages of 64 keys and no scaling in front 145.
+#include <cstdlib>
+
 #include "cache_attn.cuh"
 
 namespace dt {
@@ -380,10 +382,20 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
     }
   };
 
+  auto landed = [&](uint64_t* bar, uint32_t par) {
+    if (p.wait_limit >= kWaitLimitCycles) return mbar_wait(bar, par, p.err);
+    const long long t0 = clock64();
+    while (!poll<true>(smem_u32(bar), par))
+      if (clock64() - t0 > p.wait_limit) {
+        atomicOr(p.err, DT_ERR_TIMEOUT);
+        return false;
+      }
+    return true;
+  };
   int done = 0;
   for (int i = 0; i < mine; ++i) {
     const int st = i % kStages;
-    if (!__all_sync(kFullMask, mbar_wait(&sm.full[warp][st], static_cast<uint32_t>((i / kStages) & 1), p.err))) break;
+    if (!__all_sync(kFullMask, landed(&sm.full[warp][st], static_cast<uint32_t>((i / kStages) & 1)))) break;
     done = i + 1;
     const uint8_t* tile = sm.stage[warp][st];
     const int key0 = first_key(i);
@@ -405,8 +417,7 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
   }
   // (a wait that ran out: every copy must have landed before the block may end)
   for (int i = done; i < min(mine, done + kStages); ++i)
-    if (i < kStages || i - kStages < done)
-      mbar_wait(&sm.full[warp][i % kStages], static_cast<uint32_t>((i / kStages) & 1), p.err);
+    mbar_wait(&sm.full[warp][i % kStages], static_cast<uint32_t>((i / kStages) & 1), p.err);
   __syncthreads();
   // ---- the warp's rows into shared memory
 #pragma unroll
@@ -732,6 +743,10 @@ extern "C" dartree_status dartree_cache_attention_ex(const dartree_cache* cache,
   p.scale_log2 = scale * 1.4426950408889634f;
   p.O = static_cast<uint16_t*>(O);
   p.err = err;
+  p.wait_limit = kWaitLimitCycles;
+  // test knob (as for contexts): shorten the pipeline waits to provoke TIMEOUT
+  if (const char* v = getenv("DARTREE_WAIT_LIMIT_CYCLES"))
+    if (const long long c = atoll(v); c > 0) p.wait_limit = c;
   if (!(p.scale_log2 * p.c.k_scale <= 3.0e38f)) return cache_fail(DARTREE_ERR_INVALID_ARG, "scale times k_scale is too large");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;

@@ -32,6 +32,7 @@ struct CacheAttnParams {
   uint16_t* O;               // [R][B+1][Hq][dh]
   float* part;               // [R][Hkv][m_tiles][n_split][tile_rows][dh + kPartHead] (n_split > 1)
   int* err;
+  long long wait_limit;      // cycles that a pipeline wait may take
 };
 
 // A request's keys: its prefix and nodes, cut at max_len.
@@ -71,6 +72,22 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
           smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
+}
+
+// Whether a phase is complete.  try_wait waits itself for longer than any wait
+// of these kernels lasts, so a short limit needs the poll that does not.
+template <bool SHORT>
+__device__ __forceinline__ bool poll(uint32_t addr, uint32_t parity) {
+  if constexpr (!SHORT) return mbar_try_wait(addr, parity);
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(addr), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 __device__ __forceinline__ float ex2(float x) {

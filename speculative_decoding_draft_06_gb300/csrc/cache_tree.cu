@@ -192,7 +192,8 @@ __device__ __forceinline__ uint32_t row_sees(int pos, int Lp, const uint32_t* mr
   return (nodes << np) | ((1u << np) - 1u);
 }
 
-template <int DH>
+// SHORT: with a limit of the waits (the form that a wait that runs out is tested with).
+template <int DH, bool SHORT>
 __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnParams p) {
   using L = TreeSmem<DH>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -274,11 +275,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   // the time is over)
   auto wait_w = [&](uint64_t* bar, uint32_t par) {
     const uint32_t addr = smem_u32(bar);
-    bool ok = mbar_try_wait(addr, par);
+    bool ok = poll<SHORT>(addr, par);
     if (!ok) {
-      const long long t0 = clock64();
-      while (!(ok = mbar_try_wait(addr, par)) && !*abort_flag)
-        if (clock64() - t0 > kWaitLimitCycles) {
+      const long long t0 = clock64(), limit = SHORT ? p.wait_limit : kWaitLimitCycles;
+      while (!(ok = poll<SHORT>(addr, par)) && !*abort_flag)
+        if (clock64() - t0 > limit) {
           atomicOr(p.err, DT_ERR_TIMEOUT);
           break;
         }
@@ -594,7 +595,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[2 * i + b]);
     }
-    if (!go && lane == 0) *abort_flag = 1;
+    if (!go) {  // (a rescaled output's stores end before the TMEM goes)
+      if (lane == 0) *abort_flag = 1;
+      tmem_wait_st();
+    }
     s_top[half][row] = l;
     barrier_or(pair, false);
     l = s_top[0][row] + s_top[1][row];
@@ -603,7 +607,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     if (!have || m == -INFINITY) l = 0.f;
     const float inv = l > 0.f ? p.c.v_scale / l : 0.f;
     if (half == 0 && p.n_split > 1 && row < rows)
-      *reinterpret_cast<float2*>(cache_part_row(p, r, hk, mt, split, row)) = make_float2(ref * s_fac[row], l);
+      *reinterpret_cast<float2*>(cache_part_row(p, r, hk, mt, split, row)) = make_float2(have ? ref * s_fac[row] : -INFINITY, l);
     // O by way of the row tile's queries' place in shared memory (the scores
     // are done), an eighth of the dims at a time, so that a warp's accesses are
     // whole pieces of rows: kC dims of a row by kC / 4 lanes
@@ -665,15 +669,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   }
 }
 
+template <int DH, bool SHORT>
+cudaError_t launch_tree(const CacheAttnParams& p, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = opt_in_smem(k_cache_tree<DH, SHORT>, &done);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(k_cache_tree<DH, SHORT>, dim3(p.m_tiles * p.n_split, p.c.Hkv, p.R), dim3(kTreeThreads),
+                       TreeSmem<DH>::kTotal + 1024, st, true, p);
+}
+
 }  // namespace
 
 cudaError_t launch_cache_tree(const CacheAttnParams& p, cudaStream_t st) {
-  const dim3 grid(p.m_tiles * p.n_split, p.c.Hkv, p.R);
-  static std::atomic<uint64_t> done128{0}, done64{0};
-  cudaError_t e = p.c.dh == 128 ? opt_in_smem(k_cache_tree<128>, &done128) : opt_in_smem(k_cache_tree<64>, &done64);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(p.c.dh == 128 ? k_cache_tree<128> : k_cache_tree<64>, grid, dim3(kTreeThreads),
-                       (p.c.dh == 128 ? TreeSmem<128>::kTotal : TreeSmem<64>::kTotal) + 1024, st, true, p);
+  if (p.wait_limit < kWaitLimitCycles) return p.c.dh == 128 ? launch_tree<128, true>(p, st) : launch_tree<64, true>(p, st);
+  return p.c.dh == 128 ? launch_tree<128, false>(p, st) : launch_tree<64, false>(p, st);
 }
 
 }  // namespace dt
