@@ -29,7 +29,7 @@
 // transposed within the warp (movmatrix).
 //
 // Bound by memory where there are many keys: 64 single tokens over 1 to 16001
-// tokens, 32 heads over 8 of 128: 143 us, 5.2 TB/s, 78% of a copy's rate; one
+// tokens, 32 heads over 8 of 128: 145 us, 5.2 TB/s, 79% of a copy's rate; one
 // over 131072 tokens 36 us, 4.2 TB/s (the join and the ramp: a warp has 9
 // tiles); over 1000 tokens 6.9 us, latency.  Steps:
 // a producer warp and rows as the 16-row operand 315 us for the 64; warps with
@@ -626,14 +626,14 @@ __global__ void __launch_bounds__(256) k_cache_zero_rest(const CacheAttnParams p
 // above, in tiles of 64 keys, four warps a tile each; more by the tensor-core
 // kernel in tiles of 256 rows and 128 keys.  The keys are split until the GPU
 // is full: here once over (three CTAs per SM), a tile per warp at least, and
-// with several requests at the latest every 4096 keys, so that sequences of
-// different lengths share the SMs evenly (64 of up to 16001: 2048 keys 1% to 2%
-// more time, 1024 11%, 8192 11%; a single one of 131072: one wave 36 us, cut
-// into a wave and an eighth 46); there one wave of one CTA per SM.  Up to eight
-// splits that are all resident at once are a thread-block cluster each and join
-// in shared memory: no second kernel and no workspace for short sequences.
+// with several requests at the latest every 2048 keys, so that sequences of
+// different lengths share the SMs evenly (a single one of 131072 tokens: one
+// wave 36 us, in 2048 keys, a wave and an eighth, 46); there one wave of one
+// CTA per SM.  Up to eight splits that are all resident at once are a
+// thread-block cluster each and join in shared memory: no second kernel and no
+// workspace for short sequences.
 constexpr int kTreeRows = 16;
-constexpr int kSplitTiles = 64;  // 4096 keys
+constexpr int kSplitTiles = 32;  // 2048 keys
 
 struct Plan {
   int rows, tile_rows, tile_keys, m_tiles, n_split, split_tiles, cluster;
