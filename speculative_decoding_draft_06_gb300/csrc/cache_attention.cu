@@ -627,11 +627,16 @@ __global__ void __launch_bounds__(256) k_cache_zero_rest(const CacheAttnParams p
 // kernel in tiles of 256 rows and 128 keys.  The keys are split until the GPU
 // is full: here once over (three CTAs per SM), a tile per warp at least, and
 // with several requests at the latest every 2048 keys, so that sequences of
-// different lengths share the SMs evenly (a single one of 131072 tokens: one
-// wave 36 us, in 2048 keys, a wave and an eighth, 46); there one wave of one
-// CTA per SM.  Up to eight splits that are all resident at once are a
-// thread-block cluster each and join in shared memory: no second kernel and no
-// workspace for short sequences.
+// different lengths share the SMs evenly (8 key/value heads, times against
+// every 4096: 32 requests of up to 8000 keys 52 us and 67, 48 of 6000 54 and
+// 69, 16 of 16001 53 and 75, but 64 of 16001 141 and 138, 128 of 2500 64 and
+// 59; a single one of 131072: one wave 36 us, in 2048 keys, a wave and an
+// eighth, 46); there one wave of one CTA per SM.  Up to eight splits are a
+// thread-block cluster each and join in shared memory, without a second kernel
+// and a workspace, where the whole grid is resident at once.  Beyond that whole
+// clusters wait for room: with up to two waves of clusters 16 requests of 4100
+// keys took 32 us (21 by way of the workspace), 32 of 1000 19 (13), 8 of 16001
+// 43 (31); with more waves a third to a half more.
 constexpr int kTreeRows = 16;
 constexpr int kSplitTiles = 32;  // 2048 keys
 
@@ -661,7 +666,7 @@ Plan plan_rows(bool tree, long long rows, int R, int max_len, int Hkv, int dh, i
   if (!tree) pl.split_tiles = (pl.split_tiles + kWarps - 1) / kWarps * kWarps;
   pl.n_split = (tiles + pl.split_tiles - 1) / pl.split_tiles;
   pl.cluster = !tree && pl.n_split > 1 && pl.n_split <= kMaxCluster &&
-               (ctas * pl.n_split <= sms * 6 || most_splits == kMaxCluster);
+               (ctas * pl.n_split <= sms * 3 || most_splits == kMaxCluster);
   pl.work = pl.n_split > 1 && !pl.cluster
                 ? static_cast<size_t>(ctas) * pl.n_split * pl.tile_rows * (dh + kPartHead) * sizeof(float)
                 : 0;

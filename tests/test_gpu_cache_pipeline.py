@@ -48,14 +48,14 @@ def check_request(O, q, K, V, see, scale, keys):
 
 
 CASES = [  # R, Hq, Hkv, dh, P, lengths (from, to), long ones, B, bound beyond them
-    (58, 32, 8, 128, 64, (1500, 2500), (), 0, 0),        # one split, ten tiles a warp
-    (230, 16, 2, 64, 16, (600, 1200), (), 0, 0),
-    (120, 64, 4, 128, 128, (900, 1500), (), 0, 0),       # sixteen rows
+    (58, 32, 8, 128, 64, (1500, 2500), (), 0, 0),        # two splits, five tiles a warp, through the workspace
+    (230, 16, 2, 64, 16, (600, 1200), (), 0, 0),        # one split
+    (120, 64, 4, 128, 128, (900, 1500), (), 0, 0),       # one, sixteen rows
     (58, 96, 8, 64, 32, (700, 1300), (1, 64), 0, 0),
     (58, 24, 8, 128, 16, (1000, 1700), (0, 63, 65), 0, 0),
-    (64, 32, 8, 128, 64, (1, 700), (13000, 4096, 4097, 8192, 12288), 0, 0),  # four splits, joined by a warp a row
+    (64, 32, 8, 128, 64, (1, 700), (13000, 4096, 4097, 8192, 12288), 0, 0),  # seven splits, joined by a warp a row
     (64, 64, 4, 64, 16, (1, 500), (13001, 9000), 0, 0),
-    (58, 32, 8, 128, 128, (300, 2500), (), 0, 17500),    # a loose bound: five splits, most without keys
+    (58, 32, 8, 128, 128, (300, 2500), (), 0, 17500),    # a loose bound: nine splits, most without keys
     (1, 32, 8, 128, 64, (41003, 41003), (), 0, 0),       # 53 splits, three tiles a warp, joined by eight warps
     (1, 128, 8, 64, 128, (40500, 40500), (), 0, 0),
     (2, 8, 1, 128, 16, (70001, 70001), (33333,), 0, 0),
@@ -64,6 +64,8 @@ CASES = [  # R, Hq, Hkv, dh, P, lengths (from, to), long ones, B, bound beyond t
     (2, 32, 8, 128, 64, (6000, 6100), (), 128, 0),       # four rows behind whole tiles: three tiles a warp
     (30, 32, 8, 128, 32, (2500, 3000), (5,), 32, 0),     # six
     (12, 8, 8, 64, 16, (3000, 4000), (), 130, 0),
+    (8, 32, 8, 128, 64, (4000, 4100), (100,), 0, 0),     # six splits in a cluster, three tiles a warp
+    (19, 64, 8, 64, 32, (1000, 1700), (0,), 0, 0),       # three
 ]
 
 
