@@ -668,8 +668,8 @@ __global__ void __launch_bounds__(256) k_cache_commit(const CommitParams p) {
   }
 }
 
-// Blocks per page copy: about 8 KB each, so that a page of a layer is spread
-// over SMs while every thread still has several loads in flight.
+// Blocks per page copy: about 32 KB each, a thread's eight 16-byte loads once,
+// so that a page of a layer is spread over SMs.
 int copy_pieces(size_t page_bytes) {
   const size_t k = (page_bytes + 32767) / 32768;
   return static_cast<int>(k < 1 ? 1 : k > 1024 ? 1024 : k);

@@ -38,8 +38,7 @@ inline bool cache_pow2(float x) {
   return (b & 0x807FFFFFu) == 0 && e >= -64 && e <= 64;
 }
 
-// Checks the descriptor and fills the view; nullptr, or why it is bad
-// (*unsupported: outside the format's sizes).
+// Checks the descriptor and fills the view; nullptr, or why it is bad.
 inline const char* cache_view(const dartree_cache* c, CacheView* v) {
   if (!c || !c->pool) return "null cache or pool";
   if (c->layers < 1 || c->pages < 1 || c->Hkv < 1 || c->Hkv > 65535) return "bad cache layers, pages or Hkv";
@@ -121,6 +120,12 @@ __device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
       : "=r"(d)
       : "f"(lo), "f"(hi));
   return d;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ uint32_t h2mul(uint32_t a, uint32_t b) {

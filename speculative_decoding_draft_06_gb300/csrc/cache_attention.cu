@@ -15,9 +15,10 @@
 // P^T (16 dims x 8 rows x 16 keys).  A code times its scale has 6 significant
 // bits and lies between 2^-10 and 2688: exact in fp16.  The queries are
 // scaled per row by a power of two to at most 2 before they become fp16, so
-// all that rounds is fp32 sums, P (2^-11, with its reference maximum at 2^6 so
-// that weights down to 2^-20 of the largest keep all their bits) and the
-// output.
+// all that rounds is fp32 sums, P (2^-12 of a weight, with its reference maximum
+// at 2^6 so that weights down to 2^-20 of the largest keep all their bits; the
+// normaliser sums them before they are rounded, in fp32) and the output, whose
+// rounding to bf16 (2^-9) is the largest.
 //
 // The k index of a product may run over the dims (or keys) in any order, and
 // so may the row index: the orders are chosen so that a lane's codes lie
@@ -682,7 +683,8 @@ int plan_of(int R, int B, int max_len, int Hq, int Hkv, int dh, Plan (&pl)[2]) {
   if (left) {
     // the rows left over: up to a cluster's splits (they run beside the others
     // and need no launch more), three CTAs to an SM, which the splits of the
-    // others leave free
+    // others leave free (40 SMs at most: half of them cost one tree of 129 rows
+    // 42 us, 32 with these)
     pl[1] = plan_rows(false, kTreeTail, R, max_len, Hkv, dh, kMaxCluster, sms);
     const long long theirs = (static_cast<long long>(R) * Hkv * pl[1].n_split + 2) / 3;
     sms -= static_cast<int>(theirs < 40 ? theirs : 40);

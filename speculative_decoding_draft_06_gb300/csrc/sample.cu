@@ -322,12 +322,6 @@ __device__ __forceinline__ float max_of(const float (&x)[N]) {
   return m;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // f(unit, its number) for the lane's units of a warp's [ub, ue), with a load
 // in flight ahead (three: 4% to 7% slower by their moves).
 template <typename E, typename F>
@@ -1362,7 +1356,11 @@ __device__ bool from_list(const SampleParams& p, Smem& sm, int row, int n, unsig
 }
 
 // How long a request's rows take, roughly: 2 all weights exactly, 1 all
-// weights, 0 the candidates'.
+// weights, 0 the candidates'.  Only the rows' order depends on it.  (Whether
+// top-p is decided by the candidates depends on the logits' spread over T, which
+// is not known here: 0.9 stands for the spread that language models' logits
+// have, where at T = 0.7 a few percent and at T = 1 most rows take whole-row
+// passes.)
 __device__ __forceinline__ int request_cost(const SampleParams& p, int req) {
   const float T = p.temperature ? p.temperature[req] : 1.f, tp = p.top_p ? p.top_p[req] : 1.f;
   const int k = p.top_k ? p.top_k[req] : 0;
