@@ -290,7 +290,8 @@ struct ReserveParams {
 
 // One block: what each row lacks, the rows' first ranks among the free
 // pages (prefix sums), then the free pages go to the row their rank falls in.
-// Latency: 4.5 us alone with cold caches.
+// Latency: 4.5 us alone with cold caches; the search is one block's and starts at
+// page 0: behind 100000 pages in use 27 us, behind 500000 120.
 __global__ void __launch_bounds__(kPlanThreads) k_cache_reserve(const ReserveParams p) {
   pdl_wait();
   pdl_trigger();
@@ -519,7 +520,9 @@ struct CopyParams {
 
 // Grid (pieces, layers, pairs).  Every block looks for its own destination
 // among the sources and the earlier destinations: such a pair is skipped, so
-// that the result does not depend on the blocks' order.
+// that the result does not depend on the blocks' order.  Memory's while the pairs
+// are few: pages of 64 tokens of 8 heads of 128 in 8 layers, 1024 pairs 177 us (6.8
+// TB/s), 4096 801 us (6.0); the looks grow with their square.
 __global__ void __launch_bounds__(256) k_cache_copy(const CopyParams p) {
   pdl_wait();
   pdl_trigger();
@@ -613,7 +616,7 @@ __device__ __forceinline__ int commit_count(const CommitParams& p, int r, int* b
 // before it is written, and no later chunk reads what an earlier one wrote.
 // The row's length changes once every CTA of its cluster has read it.
 // Latency of a read behind a lookup behind a read: release, reserve and commit
-// of a path of 8 tokens in 32 layers take 11.0 us, of 32 paths 15.6.
+// of a path of 8 tokens in 32 layers take 10.8 us, of 32 paths 16.2.
 template <typename U>
 __global__ void __launch_bounds__(256) k_cache_commit(const CommitParams p) {
   pdl_wait();

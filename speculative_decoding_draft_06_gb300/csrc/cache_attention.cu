@@ -30,7 +30,7 @@
 // transposed within the warp (movmatrix).
 //
 // Bound by memory where there are many keys: 64 single tokens over 1 to 16001
-// tokens, 32 heads over 8 of 128: 145 us, 5.2 TB/s, 79% of a copy's rate; one
+// tokens, 32 heads over 8 of 128: 144 us, 5.1 TB/s, 77% of a copy's rate; one
 // over 131072 tokens 36 us, 4.2 TB/s (the join and the ramp: a warp has 9
 // tiles); over 1000 tokens 6.9 us, latency.  Steps:
 // a producer warp and rows as the 16-row operand 315 us for the 64; warps with

@@ -27,7 +27,7 @@
 //
 // Bound by the latency of a step's chain (scores, maximum, weights, product)
 // at two row tiles per SM: 32 trees of 65 rows over up to 2500 tokens, 32 heads
-// over 8 of 128: 76 us, 700 TFLOP/s, the tensor pipe active 37% of the time,
+// over 8 of 128: 73 us (76 in a graph), 730 TFLOP/s, the tensor pipe active 37% of the time,
 // issue 0.62 (the exponentials and the conversions of the codes alone would
 // take 29 us); one of 129 rows over 4099 tokens: 28 us.  Steps for the 32 (the
 // one): one row tile 181 us (41); two, and codes expanded from registers 121
@@ -35,7 +35,7 @@
 // a launch beside 89 (43); two threads per row 83 (35); queries loaded by the
 // softmax warps beside the first codes, output addresses out of the loop 77
 // (31).  A polynomial for part of the exponentials and row tiles that take
-// turns were slower.
+// turns were slower (no figures kept).
 #include <type_traits>
 
 #include "cache_attn.cuh"

@@ -24,12 +24,16 @@
 // border inside the interval, infinities, NaN) takes further passes over the
 // row itself, all in integers (whole_row).
 //
-// Bound, in rows that the candidates decide, by the passes' instructions (6 a
-// token) and the list's chain of steps; in the others by 35 to 100 a token.
-// 2064 rows of 151936 bf16 logits: greedy 153 us (4.1 TB/s, 61% of a copy),
-// top-k 50 215, top-p 0.9 at T = 0.7 360, top-p 0.95 at T = 1 (85% of these
-// rows by whole rows) 1090, no cut 670; 129 rows in fp32: 24, 37, 46, 193, 112;
-// 17 rows of 32000 20 us, latency.
+// Bound, in rows that the candidates decide, by latency: a block's steps (sample,
+// pass, list, cut, draw) wait for one another, and four blocks to an SM (by
+// registers and shared memory) do not cover it: greedy issues 0.34 a cycle with
+// DRAM at half its rate, 6 instructions a token.  Of the rows that they do not
+// decide each stays with the one block that found out, 35 to 100 instructions a
+// token, and the last of them set the end of the launch.
+// 2064 rows of 151936 bf16 logits: greedy 149 us (4.2 TB/s, 63% of a copy),
+// top-k 20 218, top-p 0.9 at T = 0.7 357 to 375, top-p 0.95 at T = 1 (85% of
+// these rows by whole rows) 1065, no cut 660; 129 rows in fp32: 23, 36, 42, 188,
+// 112; 17 rows of 32000 17 to 21 us, latency.
 //
 // A cut: a histogram of counts and masses over 1024 classes of -log2 w
 // (monotone in the logit) gives the class in which it falls; the class is
