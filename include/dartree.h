@@ -218,8 +218,8 @@ dartree_status dartree_build_host(dartree_ctx *ctx, const float *base_logits_hos
  * gathered since the last such report, cleared on read; OK when no call has
  * run on the device (reason text in dartree_last_error(NULL)).
  * Test knob: DARTREE_WAIT_LIMIT_CYCLES (read at dartree_create, and at every
- * dartree_state_step_noalloc and dartree_cache_attention call) shortens the kernels' pipeline waits to
- * provoke the TIMEOUT path. */
+ * dartree_state_step_noalloc and dartree_cache_attention call) shortens the
+ * kernels' pipeline waits to provoke the TIMEOUT path. */
 dartree_status dartree_sync_status(dartree_ctx *ctx, void *stream);
 
 /* Number of head calls made by the last build: D for a depth-wise build,
