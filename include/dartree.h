@@ -509,7 +509,8 @@ dartree_status dartree_cache_read_ex(const dartree_cache *cache, int32_t layer, 
  * its mask row.  Query head h reads key/value head h / (Hq / Hkv).
  * O = softmax(scale * q.k) v; products and sums in fp32, the softmax weights
  * in fp16 for the product with the values; O = 0 for a row that sees
- * nothing.  Tokens without a page are not seen (and flagged).  A row with
+ * nothing.  Tokens without a page are not seen (and flagged); nodes that no
+ * row sees need not be written.  A row with
  * lens[r] < 0 is skipped (with n_nodes[r] < 0, too): left as it was.  _ex:
  * with zero_rest != 0 the rows that are left otherwise are written as 0.
  * B <= 1024, Hq % Hkv == 0; Q, O 16-byte aligned.

@@ -347,7 +347,7 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
         uint32_t b[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int kk = 16 * h + 8 * t + c + 4 * x, key = at + kk;
+          const int key = at + 16 * h + 8 * t + c + 4 * x;
           if constexpr (DH == 128) {
             const uint2 y = *reinterpret_cast<const uint2*>(vt + key * 64 + rr * 8);
             vw[t][x][0] = y.x;
@@ -357,11 +357,9 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
             vw[t][x][0] = *reinterpret_cast<const uint32_t*>(vt + key * 32 + rr * 4);
             b[x] = vt[T::kCodes + key * 4 + (rr >> 1)];
           }
-          // what lies behind the keys may be anything: a zero weight needs a finite value
-          if constexpr (!kAll)
-            if (!((valid >> kk) & 1u)) b[x] = 0;
         }
         vs[t] = e4m3x2_to_f16x2(b[0] | (b[1] << 8));
+        if constexpr (!kAll) vs[t] = finite_scales(vs[t]);
       }
 #pragma unroll
       for (int w = 0; w < DH / 64; ++w) {

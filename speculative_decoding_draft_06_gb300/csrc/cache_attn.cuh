@@ -90,6 +90,15 @@ __device__ __forceinline__ bool poll(uint32_t addr, uint32_t parity) {
   return ok != 0;
 }
 
+// Scales as the products with weights take them: what nothing has written may
+// be e4m3's NaN, which a weight of zero does not cancel.  (max takes the other
+// operand of a NaN; scales are not negative.)
+__device__ __forceinline__ uint32_t finite_scales(uint32_t s2) {
+  uint32_t d;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(s2), "r"(0u));
+  return d;
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));

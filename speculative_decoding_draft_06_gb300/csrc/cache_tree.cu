@@ -406,11 +406,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
         const uint32_t* w = reinterpret_cast<const uint32_t*>(&code[it]);
         uint32_t sc[2];
         if constexpr (DH == 128) {
-          const uint32_t s2 = e4m3x2_to_f16x2(scl[it]);
+          const uint32_t s2 = finite_scales(e4m3x2_to_f16x2(scl[it]));
           sc[0] = __byte_perm(s2, s2, 0x1010);
           sc[1] = __byte_perm(s2, s2, 0x3232);
         } else {
-          sc[0] = sc[1] = e4m3x2_to_f16x2(scl[it] | (scl[it] << 8));
+          sc[0] = sc[1] = finite_scales(e4m3x2_to_f16x2(scl[it] | (scl[it] << 8)));
         }
 #pragma unroll
         for (int i = 0; i < DH / 32; ++i) {
