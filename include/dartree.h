@@ -533,6 +533,45 @@ dartree_status dartree_cache_attention_ex(const dartree_cache *cache, int32_t la
 size_t dartree_cache_attention_workspace(int32_t R, int32_t B, int32_t max_len, int32_t Hq,
                                          int32_t Hkv, int32_t dh);
 
+/* Attention with a sliding window and a few first tokens that stay visible
+ * (sinks) over the cache, one layer, for single tokens, draft trees and chains
+ * (drafted ones, or a prompt's tokens) of any length, whose keys and values are
+ * in the cache:
+ *   row i of request r is at place lens[r] + offset + i of its sequence.  Row 0
+ *        is the root, at that position (offset -1: the last token that lens
+ *        counts, as in dartree_cache_attention);
+ *   mask NULL: the rows are a chain, row i at position lens[r] + offset + i; it
+ *        sees the tokens up to its own.  B is then bounded by (B + 1) Hq / Hkv <=
+ *        2^30 alone;
+ *   mask [R][B][ceil(B/32)]: the rows behind the root are tree nodes (B <= 1024).
+ *        A node's position is the root's and the number of nodes that its mask
+ *        row names, its depth; it sees the prefix up to the root and those nodes;
+ *   window (0: none) and sinks: of the tokens that it sees otherwise, a row at
+ *        position q sees those at positions k < sinks or k > q - window;
+ *   Q    rows of Hq dh bf16, q_token_stride elements apart (as above), q_rows of
+ *        them in all, and O as many, dense.  start NULL: request r has the rows r
+ *        (B + 1) .. of which n_nodes[r] + 1 (NULL: all) count.  start [R + 1]
+ *        (dartree_cache_plan's): its rows are start[r] .. start[r + 1] - 1, at
+ *        most B + 1; n_nodes is NULL;
+ *   max_len  an upper bound of lens[r] + offset + 1 + n, n + 1 the rows of r
+ *        (tokens behind it are not read and flagged).
+ * Only pages that hold a token which a row may see need to be there (a tree's
+ * rows: within the root's window); others may have been let go.  Arithmetic,
+ * alignment, work, zero_rest, err and rows without a visible token are those of
+ * dartree_cache_attention_ex.  A request with lens[r] < 0 or lens[r] + offset <
+ * -1 is skipped (at -1 row 0 stands before the first token), and one whose rows lie outside [0, q_rows) is, too, and flagged.
+ * work: dartree_cache_window_attention_workspace() bytes (chain: whether mask is
+ * NULL). */
+dartree_status dartree_cache_window_attention(
+    const dartree_cache *cache, int32_t layer, const void *Q, int64_t q_token_stride,
+    int64_t q_rows, const int32_t *start, const uint32_t *mask, const int32_t *n_nodes,
+    const int32_t *table, int32_t max_pages, const int32_t *lens, int32_t R, int32_t B,
+    int32_t max_len, int32_t offset, int32_t window, int32_t sinks, int32_t Hq, float scale,
+    int32_t zero_rest, void *O, void *work, size_t work_bytes, int32_t *err, void *stream);
+size_t dartree_cache_window_attention_workspace(int32_t R, int32_t B, int32_t max_len,
+                                                int32_t window, int32_t sinks, int32_t chain,
+                                                int32_t Hq, int32_t Hkv, int32_t dh);
+
 /* Pages for want[r] more tokens per row: row r comes to hold at least
  * ceil((lens[r] + want[r]) / page_tokens) pages; lens is not changed.  Rows
  * are served in order; ok[r] = 0 for a row that needs more than max_pages or

@@ -52,6 +52,11 @@ constexpr int kThreads = kWarps * 32;
 
 __device__ int g_cache_err;  // error word when the caller passes none
 
+#ifndef DT_WINDOW
+#define DT_WINDOW 0  // 1: the forms with a sliding window (an object of their own)
+#endif
+constexpr bool kWin = DT_WINDOW != 0;
+
 // Bits of x where the mask has ones, of y where it has zeros.
 __device__ __forceinline__ uint32_t bit_select(uint32_t mask, uint32_t x, uint32_t y) {
   uint32_t d;
@@ -83,7 +88,7 @@ struct __align__(128) AttnSmem {
   float2 recv_ml[8 * NQ + kMaxCluster];
 };
 
-template <int DH, int NQ>
+template <int DH, int NQ, bool kWin>
 __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
   constexpr int kSteps = DH / 16;   // k-steps of S^T, dim tiles of O^T
   constexpr int kRows = 8 * NQ;
@@ -93,18 +98,20 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x, hk = blockIdx.y, r = blockIdx.z;
   Span sp;
-  if (!request_span(p, r, &sp)) return;
+  if (kWin && threadIdx.x == 0 && split == 0 && hk == 0 && !p.tail && span_flag<kWin>(p, r))
+    atomicOr(p.err, DT_ERR_BAD_INDEX);
+  if (!request_span<kWin>(p, r, &sp)) return;
   // rows q0 .. q0 + live - 1
   int q0 = 0, live = (sp.n + 1) * p.g;
   if (p.tail) {
     q0 = live;
-    live = tail_rows(live);
+    live = tail_rows<kWin>(p, live);
     if (live == 0) return;
     q0 -= live;
   }
-  const int t_all = row_tile_keys(p, sp, 0);
+  const KeyTiles<kWin> tl = row_key_tiles<kWin>(p, sp, 0, q0);
   const int t_beg = split * p.split_tiles;
-  const int nt = min(t_all, t_beg + p.split_tiles) - t_beg;
+  const int nt = min(tl.n, t_beg + p.split_tiles) - t_beg;
   // (one split: rows without keys are written as 0; a cluster's CTAs all stay)
   if (nt <= 0 && !p.cluster && !(split == 0 && p.n_split == 1)) return;
   const int mine = nt > warp ? (nt - warp + kWarps - 1) / kWarps : 0;  // the warp's tiles
@@ -112,7 +119,7 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
   if (lane < kStages) mbar_init(&sm.full[warp][lane], 1);
   fence_mbar_init();
   __syncwarp();
-  if (threadIdx.x == 0 && split == 0 && hk == 0 && !p.tail && static_cast<long long>(p.lens[r]) + sp.n > p.max_len)
+  if (!kWin && threadIdx.x == 0 && split == 0 && hk == 0 && !p.tail && static_cast<long long>(p.lens[r]) + sp.n > p.max_len)
     atomicOr(p.err, DT_ERR_BAD_INDEX);
 
   // ---- the warp's copies: lane (piece, segment) has one of a tile's (a
@@ -129,10 +136,10 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
   const int seg_tile = (seg >> 1) * T::kV + ((seg & 1) ? T::kCodes : 0) + (segs == 1 ? 0 : pc * piece * unit);
   const uint8_t* seg_base = p.c.pool + static_cast<size_t>(hk) * p.c.chunk + (seg >> 1) * (p.c.chunk >> 1) +
                             ((seg & 1) ? P * DH / 2 : 0);
-  auto first_key = [&](int i) { return (t_beg + warp + i * kWarps) * kTileKeys; };
+  auto first_key = [&](int i) { return tl.at(t_beg + warp + i * kWarps) * kTileKeys; };
   auto page_of = [&](int i) {  // the lane's piece's page: -1 none, -2 bad
     const int key = first_key(i) + pc * piece;
-    if (i >= mine || !copies || key >= sp.L) return -1;
+    if (i >= mine || !copies || key >= sp.L || !tl.near(p, key, piece)) return -1;
     const int slot = key >> p.c.log_page;
     const int page = slot < p.max_pages ? trow[slot] : -2;
     return page < 0 || page >= p.c.pages ? -2 : page;
@@ -173,13 +180,14 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
   uint32_t qb[NQ][kSteps][2];
   float fac[NQ][2];                 // of rows 8 n + 2 c, + 1
   int node[NQ][2];
+  int at_pos[NQ][2];                // (window) the rows' positions
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const bool on = 8 * n + rr < live;
     const int q = on ? q0 + 8 * n + rr : 0, nd = q / p.g;
     uint32_t w[DH / 8];
     const uint4* src = reinterpret_cast<const uint4*>(
-        p.Q + (static_cast<size_t>(r) * (p.B + 1) + nd) * p.q_stride +
+        p.Q + cache_row<kWin>(p, sp, r, nd) * p.q_stride +
         static_cast<size_t>(hk * p.g + (on ? q - nd * p.g : 0)) * DH + c * (DH / 4));
 #pragma unroll
     for (int k = 0; k < DH / 32; ++k) {
@@ -197,10 +205,14 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
     top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
     float down;
     const float f = row_exponent(p, top, &down);
+    int pos = 0;
+    if constexpr (kWin) pos = row_position(p, sp, r, nd);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       fac[n][i] = __shfl_sync(kFullMask, f, (2 * c + i) * 4);
       node[n][i] = __shfl_sync(kFullMask, nd, (2 * c + i) * 4);
+      at_pos[n][i] = 0;
+      if constexpr (kWin) at_pos[n][i] = __shfl_sync(kFullMask, pos, (2 * c + i) * 4);
     }
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
@@ -219,6 +231,26 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
   }
+
+  // (window) whether a row sees tree node j: one of its mask row within the window
+  auto node_seen = [&](int j, int nd, int pos) {
+    if (nd == 0 || !((__ldg(p.mask + (static_cast<size_t>(r) * p.B + nd - 1) * p.words + (j >> 5)) >> (j & 31)) & 1u))
+      return false;
+    if (pos - sp.base < p.window) return true;  // (no node is that far away)
+    const int key = sp.base + node_depth(p, r, j);
+    return key < p.sinks || pos - key < p.window;
+  };
+  // (window) the tiles of 64 keys that every row sees whole: before `all_end`,
+  // and among the sinks or from `all_beg` on
+  int all_end = sp.Lp, all_beg = 0;
+  if constexpr (kWin) {
+    if (p.chain) all_end = sp.base + q0 / p.g + 1;
+    all_beg = sp.base + (p.chain ? (q0 + max(live, 1) - 1) / p.g : sp.n) - p.window + 1;
+  }
+  auto seen_whole = [&](int key0) {
+    if constexpr (!kWin) return key0 + kTileKeys <= sp.Lp;
+    return key0 + kTileKeys <= all_end && (key0 >= all_beg || key0 + kTileKeys <= p.sinks);
+  };
 
   // One step of 32 keys: `at` their first in the tile, key0 its position,
   // valid their bits.  kAll: every row sees every key.
@@ -279,7 +311,11 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
           for (int x = 0; x < 4; ++x) {
             const int i2 = x & 1, kk = 16 * h + 8 * (x >> 1) + (rr >> 1) + 4 * (rr & 1), pos = key0 + kk;
             bool seen = (valid >> kk) & 1u;
-            if (seen && pos >= sp.Lp) {
+            if constexpr (kWin) {
+              seen = seen && (pos < sp.Lp || p.chain
+                                  ? pos <= at_pos[n][i2] && (pos < p.sinks || at_pos[n][i2] - pos < p.window)
+                                  : node_seen(pos - sp.Lp, node[n][i2], at_pos[n][i2]));
+            } else if (seen && pos >= sp.Lp) {
               const int j = pos - sp.Lp;
               seen = node[n][i2] > 0 &&
                      ((__ldg(p.mask + (static_cast<size_t>(r) * p.B + node[n][i2] - 1) * p.words + (j >> 5)) >>
@@ -399,7 +435,7 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
     const uint8_t* tile = sm.stage[warp][st];
     const int key0 = first_key(i);
     const uint64_t valid = sm.valid[warp][st];
-    if (valid == ~0ull && key0 + kTileKeys <= sp.Lp) {
+    if (valid == ~0ull && seen_whole(key0)) {
 #pragma unroll 1
       for (int at = 0; at < kTileKeys; at += kStep) step(IntC<1>{}, tile, at, key0 + at, ~0u);
     } else {
@@ -469,7 +505,7 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
       if (lane == 0) *reinterpret_cast<float2*>(dst) = make_float2(M, L);
     } else {
       const float inv = L > 0.f ? p.c.v_scale / L : 0.f;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row(p, r, hk, q0 + row) + lane * kE);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row<kWin>(p, sp, r, hk, q0 + row) + lane * kE);
 #pragma unroll
       for (int e = 0; e < kE; e += 2) dst[e / 2] = pack_bf16(v[e] * inv, v[e + 1] * inv);
     }
@@ -494,20 +530,20 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
       for (int e = 0; e < kE; ++e) v[e] += sm.recv[k * each + at][lane * kE + e] * f;
     }
     const float inv = L > 0.f ? p.c.v_scale / L : 0.f;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row(p, r, hk, q0 + row) + lane * kE);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row<kWin>(p, sp, r, hk, q0 + row) + lane * kE);
 #pragma unroll
     for (int e = 0; e < kE; e += 2) dst[e / 2] = pack_bf16(v[e] * inv, v[e + 1] * inv);
   }
 }
 
-template <int DH, int NQ>
+template <int DH, int NQ, bool kWin>
 __global__ void __launch_bounds__(kThreads, 3) k_cache_attention(const CacheAttnParams p) {
   if (!p.tail) {
     pdl_wait();
     // (not ahead of a join: its blocks would take the place of these)
     if (p.cluster || p.n_split == 1) pdl_trigger();
   }
-  attend_rows<DH, NQ>(p);
+  attend_rows<DH, NQ, kWin>(p);
   // The rows left over by the tensor-core kernel: launched while that one
   // runs, whose outputs these are not; one CTA sees it complete, so that what
   // follows this launch follows both.
@@ -517,20 +553,20 @@ __global__ void __launch_bounds__(kThreads, 3) k_cache_attention(const CacheAttn
 template <int DH, int NQ>
 cudaError_t launch_rows(const CacheAttnParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = opt_in_smem(k_cache_attention<DH, NQ>, &done);
+  const cudaError_t e = opt_in_smem(k_cache_attention<DH, NQ, kWin>, &done);
   if (e != cudaSuccess) return e;
   const dim3 grid(p.n_split, p.c.Hkv, p.R);
   if (p.cluster)
-    return launch_kernel_cluster(k_cache_attention<DH, NQ>, grid, dim3(kThreads), sizeof(AttnSmem<DH, NQ>), st,
+    return launch_kernel_cluster(k_cache_attention<DH, NQ, kWin>, grid, dim3(kThreads), sizeof(AttnSmem<DH, NQ>), st,
                                  true, p.n_split, p);
-  return launch_kernel(k_cache_attention<DH, NQ>, grid, dim3(kThreads), sizeof(AttnSmem<DH, NQ>), st, true, p);
+  return launch_kernel(k_cache_attention<DH, NQ, kWin>, grid, dim3(kThreads), sizeof(AttnSmem<DH, NQ>), st, true, p);
 }
 
 // The shares of each row over the key splits, joined in a fixed order: M =
 // max m_s, O = sum O_s 2^(m_s - M) / sum l_s 2^(m_s - M).  W warps per row
 // take every W-th split and meet in shared memory; grid (rows / (8 / W), Hkv,
 // R).
-template <int DH, int W>
+template <int DH, int W, bool kWin>
 __global__ void __launch_bounds__(256) k_cache_attention_join(const CacheAttnParams p) {
   constexpr int kE = DH / 32, kPerBlock = 8 / W;
   __shared__ float s_v[W > 1 ? 8 : 1][DH];
@@ -539,10 +575,10 @@ __global__ void __launch_bounds__(256) k_cache_attention_join(const CacheAttnPar
   const int q = blockIdx.x * kPerBlock + warp / W, hk = blockIdx.y, r = blockIdx.z;
   pdl_wait();
   Span sp;
-  bool on = request_span(p, r, &sp);
+  bool on = request_span<kWin>(p, r, &sp);
   int q0 = 0;  // the launch's first row
   if (on) {
-    const int all = (sp.n + 1) * p.g, tail = p.tile_rows == kTreeRowsCta || p.tail ? tail_rows(all) : 0;
+    const int all = (sp.n + 1) * p.g, tail = p.tile_rows == kTreeRowsCta || p.tail ? tail_rows<kWin>(p, all) : 0;
     q0 = p.tail ? all - tail : 0;
     on = q < (p.tail ? tail : all - tail);
   }
@@ -552,7 +588,8 @@ __global__ void __launch_bounds__(256) k_cache_attention_join(const CacheAttnPar
   for (int e = 0; e < kE; ++e) v[e] = 0.f;
   if (on) {
     const int mt = q / p.tile_rows;
-    const int ns = (row_tile_keys(p, sp, mt) + p.split_tiles - 1) / p.split_tiles;  // splits that had keys
+    // splits that had keys
+    const int ns = (row_key_tiles<kWin>(p, sp, mt, q0 + mt * p.tile_rows).n + p.split_tiles - 1) / p.split_tiles;
     const size_t step = static_cast<size_t>(p.tile_rows) * (DH + kPartHead);
     const float* src = cache_part_row(p, r, hk, mt, 0, q - mt * p.tile_rows);
     for (int s = w + lane * W; s < ns; s += 32 * W) M = fmaxf(M, src[s * step]);
@@ -593,7 +630,7 @@ __global__ void __launch_bounds__(256) k_cache_attention_join(const CacheAttnPar
     }
   }
   const float inv = L > 0.f ? p.c.v_scale / L : 0.f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row(p, r, hk, q0 + q) + lane * kE);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.O + cache_out_row<kWin>(p, sp, r, hk, q0 + q) + lane * kE);
 #pragma unroll
   for (int e = 0; e < kE; e += 2) dst[e / 2] = pack_bf16(v[e] * inv, v[e + 1] * inv);
 }
@@ -603,22 +640,47 @@ cudaError_t launch_join(const CacheAttnParams& p, cudaStream_t st) {
   // eight warps per row where a row has many shares and few rows would leave
   // the GPU to a handful of blocks
   if (p.n_split > 8 && static_cast<long long>(p.R) * p.c.Hkv * p.rows < 152 * 16)
-    return launch_kernel(k_cache_attention_join<DH, 8>, dim3(p.rows, p.c.Hkv, p.R), dim3(256), 0, st, true, p);
-  return launch_kernel(k_cache_attention_join<DH, 1>, dim3((p.rows + 7) / 8, p.c.Hkv, p.R), dim3(256), 0, st, true, p);
+    return launch_kernel(k_cache_attention_join<DH, 8, kWin>, dim3(p.rows, p.c.Hkv, p.R), dim3(256), 0, st, true, p);
+  return launch_kernel(k_cache_attention_join<DH, 1, kWin>, dim3((p.rows + 7) / 8, p.c.Hkv, p.R), dim3(256), 0, st, true, p);
 }
 
 // Zeros in the rows that a call leaves as they were: those behind a request's
-// tree, all of a skipped one.  Grid (R).  (Where it is asked for, a launch of
+// tree, all of a skipped one.  Grid (R, pieces); packed rows (R + 1, pieces).  (Where it is asked for, a launch of
 // its own, 0.6 to 3 us: in the attention kernels its code made 32 trees 5% slower.)
+template <bool kWin>
 __global__ void __launch_bounds__(256) k_cache_zero_rest(const CacheAttnParams p) {
   pdl_wait();
   pdl_trigger();
   const int r = blockIdx.x;
   Span sp;
-  const int first = request_span(p, r, &sp) ? sp.n + 1 : 0;
   const size_t per = static_cast<size_t>(p.Hq) * p.c.dh / 8;  // 16-byte units of a node
+  if (kWin && p.start) {
+    // block r: from the end of the rows that are computed before it on to the
+    // next that are (block R: to the end)
+    auto bound = [&](int k) {
+      const long long at = k < 0 ? 0 : p.start[k];
+      return max(0ll, min(at, p.q_rows));
+    };
+    long long beg = r == 0 ? 0 : bound(r), end = r < p.R ? bound(r + 1) : p.q_rows;
+    if (r < p.R) {
+      if (r == 0 && bound(0) > 0) {  // rows before the first request's
+        uint4* o = reinterpret_cast<uint4*>(p.O);
+        for (long long i = blockIdx.y * 256 + threadIdx.x; i < bound(0) * static_cast<long long>(per); i += gridDim.y * 256)
+          o[i] = make_uint4(0, 0, 0, 0);
+      }
+      beg = bound(r);
+      if (request_span<kWin>(p, r, &sp)) beg = min(end, sp.row0 + sp.n + 1);
+    }
+    uint4* o = reinterpret_cast<uint4*>(p.O);
+    for (long long i = beg * static_cast<long long>(per) + blockIdx.y * 256 + threadIdx.x;
+         i < end * static_cast<long long>(per); i += gridDim.y * 256)
+      o[i] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const int first = request_span<kWin>(p, r, &sp) ? sp.n + 1 : 0;
   uint4* o = reinterpret_cast<uint4*>(p.O) + static_cast<size_t>(r) * (p.B + 1) * per;
-  for (size_t i = first * per + threadIdx.x; i < (p.B + 1) * per; i += 256) o[i] = make_uint4(0, 0, 0, 0);
+  for (size_t i = first * per + blockIdx.y * 256 + threadIdx.x; i < (p.B + 1) * per; i += gridDim.y * 256)
+    o[i] = make_uint4(0, 0, 0, 0);
 }
 
 // How a call is cut: up to kTreeRows rows per key/value head by the kernel
@@ -644,7 +706,25 @@ struct Plan {
   size_t work;
 };
 
-Plan plan_rows(bool tree, long long rows, int R, int max_len, int Hkv, int dh, int most_splits, int sms) {
+// The keys that a row tile can see at most: all, or with a window the sinks and
+// what lies between its first row's window and its last row (of `rows` rows: a
+// chain's positions, a tree's root and nodes).  small: requests may have few
+// rows, which the few-rows kernel takes in the launch of the rows left over (a
+// prompt's 2001 rows among 32 single tokens: 380 us all by the tensor cores, 288 so).
+struct Reach {
+  int max_len, window, sinks, g;
+  bool all, chain, small;
+  int B;
+  long long tiles(int tile_rows, int tile_keys) const {
+    const long long whole = max_len < 1 ? 1 : (max_len - 1) / tile_keys + 1;
+    if (all) return whole;
+    const long long span = chain ? (tile_rows + g - 1) / g + 1 : B + 1;
+    const long long seen = (sinks + tile_keys - 1) / tile_keys + (window + span - 2) / tile_keys + 2;
+    return seen < whole ? seen : whole;
+  }
+};
+
+Plan plan_rows(bool tree, long long rows, int R, const Reach& reach, int Hkv, int dh, int most_splits, int sms) {
   Plan pl;
   pl.rows = static_cast<int>(rows);
   pl.tile_rows = tree ? kTreeRowsCta : rows > 8 ? 16 : 8;
@@ -653,7 +733,7 @@ Plan plan_rows(bool tree, long long rows, int R, int max_len, int Hkv, int dh, i
   const int odd = static_cast<int>(rows % kTreeTile);
   const long long mine = tree && rows > kTreeTile && odd <= kTreeTail ? rows - odd : rows;
   pl.m_tiles = static_cast<int>((mine + pl.tile_rows - 1) / pl.tile_rows);
-  const int tiles = max_len < 1 ? 1 : (max_len - 1) / pl.tile_keys + 1;
+  const int tiles = static_cast<int>(reach.tiles(pl.tile_rows, pl.tile_keys));
   const long long ctas = static_cast<long long>(R) * Hkv * pl.m_tiles;
   long long n = tree ? sms / ctas : (sms * 3 + ctas - 1) / ctas;
   if (!tree && R > 1 && n < (tiles + kSplitTiles - 1) / kSplitTiles) n = (tiles + kSplitTiles - 1) / kSplitTiles;
@@ -674,93 +754,88 @@ Plan plan_rows(bool tree, long long rows, int R, int max_len, int Hkv, int dh, i
 
 // The launches of a call: [0] all rows, or those of whole tiles; [1] (tree
 // only) the rows behind them, where a request may have some.
-int plan_of(int R, int B, int max_len, int Hq, int Hkv, int dh, Plan (&pl)[2]) {
+int plan_of(int R, int B, const Reach& reach, int Hq, int Hkv, int dh, Plan (&pl)[2]) {
   const long long rows = static_cast<long long>(B + 1) * (Hq / Hkv);
-  const bool tree = rows > kTreeRows, left = tree && rows > kTreeTile;
+  const bool tree = rows > kTreeRows, left = tree && (rows > kTreeTile || reach.small);
   int sms = 152;
   if (left) {
     // the rows left over: up to a cluster's splits (they run beside the others
     // and need no launch more), three CTAs to an SM, which the splits of the
     // others leave free (40 SMs at most: half of them cost one tree of 129 rows
     // 42 us, 32 with these)
-    pl[1] = plan_rows(false, kTreeTail, R, max_len, Hkv, dh, kMaxCluster, sms);
+    pl[1] = plan_rows(false, kTreeTail, R, reach, Hkv, dh, kMaxCluster, sms);
     const long long theirs = (static_cast<long long>(R) * Hkv * pl[1].n_split + 2) / 3;
     sms -= static_cast<int>(theirs < 40 ? theirs : 40);
   }
-  pl[0] = plan_rows(tree, rows, R, max_len, Hkv, dh, 1 << 30, sms);
+  pl[0] = plan_rows(tree, rows, R, reach, Hkv, dh, 1 << 30, sms);
   return left ? 2 : 1;
 }
 
-}  // namespace
-}  // namespace dt
-
-extern "C" size_t dartree_cache_attention_workspace(int32_t R, int32_t B, int32_t max_len, int32_t Hq,
-                                                    int32_t Hkv, int32_t dh) {
-  if (R < 1 || B < 0 || B > DARTREE_MAX_B || max_len < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 ||
-      (dh != 64 && dh != 128))
-    return 0;
-  dt::Plan pl[2];
-  dt::plan_of(R, B, max_len, Hq, Hkv, dh, pl);
+// What both entries share: the checks, the parameters, the launches.
+size_t attention_work(int R, int B, const Reach& reach, int Hq, int Hkv, int dh) {
+  Plan pl[2];
+  plan_of(R, B, reach, Hq, Hkv, dh, pl);
   return pl[0].work;
 }
 
-extern "C" dartree_status dartree_cache_attention_ex(const dartree_cache* cache, int32_t layer, const void* Q,
-                                                     int64_t q_token_stride, const uint32_t* mask,
-                                                     const int32_t* n_nodes, const int32_t* table,
-                                                     int32_t max_pages, const int32_t* lens, int32_t R,
-                                                     int32_t B, int32_t max_len, int32_t Hq, float scale,
-                                                     int32_t zero_rest, void* O, void* work, size_t work_bytes,
-                                                     int32_t* err, void* stream) {
-  using namespace dt;
-  CacheAttnParams p{};
-  if (const char* why = cache_view(cache, &p.c)) return cache_fail(DARTREE_ERR_INVALID_ARG, why);
-  if (!Q || !table || !lens || !O || (B > 0 && !mask))
-    return cache_fail(DARTREE_ERR_INVALID_ARG, "null pointer argument");
-  if (layer < 0 || layer >= cache->layers) return cache_fail(DARTREE_ERR_INVALID_ARG, "no such layer");
-  if (R < 1 || B < 0 || B > DARTREE_MAX_B || max_pages < 1 || max_len < 0 || Hq < 1 || Hq % p.c.Hkv != 0 ||
-      !(scale > 0.f) || !(scale <= 3.0e38f))
-    return cache_fail(DARTREE_ERR_INVALID_ARG, "bad R, B, max_pages, max_len, Hq or scale");
-  const int dh = p.c.dh;
-  if (q_token_stride % 8 != 0 || q_token_stride < static_cast<int64_t>(Hq) * dh)
-    return cache_fail(DARTREE_ERR_INVALID_ARG, "q_token_stride must be a multiple of 8, at least Hq * dh");
+const char* attention_check(const dartree_cache* cache, int32_t layer, const void* Q, int64_t q_token_stride,
+                            const int32_t* table, int32_t max_pages, const int32_t* lens, int32_t R, int32_t B,
+                            int32_t max_len, int32_t Hq, float scale, const void* O, const void* work,
+                            CacheAttnParams* p) {
+  if (const char* why = cache_view(cache, &p->c)) return why;
+  if (!Q || !table || !lens || !O) return "null pointer argument";
+  if (layer < 0 || layer >= cache->layers) return "no such layer";
+  if (R < 1 || B < 0 || max_pages < 1 || max_len < 0 || Hq < 1 || Hq % p->c.Hkv != 0 || !(scale > 0.f) ||
+      !(scale <= 3.0e38f))
+    return "bad R, B, max_pages, max_len, Hq or scale";
+  if (q_token_stride % 8 != 0 || q_token_stride < static_cast<int64_t>(Hq) * p->c.dh)
+    return "q_token_stride must be a multiple of 8, at least Hq * dh";
   if ((reinterpret_cast<uintptr_t>(Q) | reinterpret_cast<uintptr_t>(O) | reinterpret_cast<uintptr_t>(work)) & 15)
-    return cache_fail(DARTREE_ERR_INVALID_ARG, "Q, O and work must be 16-byte aligned");
-  Plan pl[2];
-  const int launches = plan_of(R, B, max_len, Hq, p.c.Hkv, dh, pl);
-  if (pl[0].work > 0 && (!work || work_bytes < pl[0].work))
-    return cache_fail(DARTREE_ERR_INVALID_ARG, "work is smaller than dartree_cache_attention_workspace()");
-  p.g = Hq / p.c.Hkv;
-  if (R > 65535 || static_cast<long long>(p.c.Hkv) * pl[0].m_tiles > 65535 || max_len > (1 << 30))
-    return cache_fail(DARTREE_ERR_UNSUPPORTED, "too many requests, heads or keys");
-  p.c.pool += static_cast<size_t>(layer) * p.c.layer_bytes;
-  p.Q = static_cast<const uint16_t*>(Q);
-  p.q_stride = q_token_stride;
-  p.mask = mask;
-  p.n_nodes = n_nodes;
-  p.table = table;
-  p.lens = lens;
-  p.max_pages = max_pages;
-  p.R = R;
-  p.B = B;
-  p.max_len = max_len;
-  p.Hq = Hq;
-  p.words = (B + 31) / 32;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.O = static_cast<uint16_t*>(O);
-  p.err = err;
-  p.wait_limit = kWaitLimitCycles;
+    return "Q, O and work must be 16-byte aligned";
+  p->c.pool += static_cast<size_t>(layer) * p->c.layer_bytes;
+  p->Q = static_cast<const uint16_t*>(Q);
+  p->q_stride = q_token_stride;
+  p->table = table;
+  p->lens = lens;
+  p->max_pages = max_pages;
+  p->R = R;
+  p->B = B;
+  p->max_len = max_len;
+  p->Hq = Hq;
+  p->g = Hq / p->c.Hkv;
+  p->words = (B + 31) / 32;
+  p->scale_log2 = scale * 1.4426950408889634f;
+  p->O = static_cast<uint16_t*>(const_cast<void*>(O));
+  p->wait_limit = kWaitLimitCycles;
   // test knob (as for contexts): shorten the pipeline waits to provoke TIMEOUT
   if (const char* v = getenv("DARTREE_WAIT_LIMIT_CYCLES"))
-    if (const long long c = atoll(v); c > 0) p.wait_limit = c;
+    if (const long long c = atoll(v); c > 0) p->wait_limit = c;
+  return nullptr;
+}
+
+dartree_status attention_run(CacheAttnParams p, const Reach& reach, bool odd_known, bool zero_rest, void* work,
+                             size_t work_bytes, void* stream) {
+  const int dh = p.c.dh;
+  Plan pl[2];
+  const int launches = plan_of(p.R, p.B, reach, p.Hq, p.c.Hkv, dh, pl);
+  if (pl[0].work > 0 && (!work || work_bytes < pl[0].work))
+    return cache_fail(DARTREE_ERR_INVALID_ARG, "work is smaller than the attention's workspace size");
+  if (p.R > 65535 || (!kWin && static_cast<long long>(p.c.Hkv) * pl[0].m_tiles > 65535) || p.max_len > (1 << 30))
+    return cache_fail(DARTREE_ERR_UNSUPPORTED, "too many requests, heads or keys");
   if (!(p.scale_log2 * p.c.k_scale <= 3.0e38f)) return cache_fail(DARTREE_ERR_INVALID_ARG, "scale times k_scale is too large");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (!p.err) e = cudaGetSymbolAddress(reinterpret_cast<void**>(&p.err), g_cache_err);
   if (e != cudaSuccess) return cache_launched(e);
-  if (zero_rest) e = launch_kernel(k_cache_zero_rest, dim3(R), dim3(256), 0, st, true, p);
-  // (without n_nodes it is known here whether rows are left over)
+  if (zero_rest) {
+    // (a request's rows in pieces of about 256 KB)
+    const size_t bytes = static_cast<size_t>(p.B + 1) * p.Hq * dh * 2;
+    const size_t pieces = kWin ? (bytes >> 18) + 1 : 1;
+    e = launch_kernel(k_cache_zero_rest<kWin>, dim3(p.R + (kWin && p.start ? 1 : 0), pieces < 64 ? pieces : 64), dim3(256),
+                      0, st, true, p);
+  }
   const int odd = pl[0].rows % kTreeTile;
-  const int run = launches > 1 && !n_nodes && (odd == 0 || odd > kTreeTail) ? 1 : launches;
+  const int run = launches > 1 && odd_known && (odd == 0 || odd > kTreeTail) ? 1 : launches;
   CacheAttnParams first = p;
   for (int k = 0; k < run && e == cudaSuccess; ++k) {
     p.rows = pl[k].rows;
@@ -773,7 +848,7 @@ extern "C" dartree_status dartree_cache_attention_ex(const dartree_cache* cache,
     p.tail = k;
     p.part = static_cast<float*>(work);
     if (k == 0) first = p;
-    if (p.tile_rows == kTreeRowsCta) e = launch_cache_tree(p, st);
+    if (p.tile_rows == kTreeRowsCta) e = kWin ? launch_cache_window_tree(p, st) : launch_cache_tree(p, st);
     else if (p.tile_rows == 8) e = dh == 128 ? launch_rows<128, 1>(p, st) : launch_rows<64, 1>(p, st);
     else e = dh == 128 ? launch_rows<128, 2>(p, st) : launch_rows<64, 2>(p, st);
   }
@@ -783,13 +858,105 @@ extern "C" dartree_status dartree_cache_attention_ex(const dartree_cache* cache,
   return cache_launched(e);
 }
 
+constexpr int kFar = 1 << 30;  // no window; as far as positions go
+
+// max_len, window, sinks as a call's Reach (window < 1: none).
+Reach reach_of(int32_t B, int32_t max_len, int32_t window, int32_t sinks, bool chain, bool small, int32_t g) {
+  const int w = window < 1 || window > kFar ? kFar : window, s = sinks > kFar ? kFar : sinks;
+  return Reach{max_len, w, s, g, w == kFar, chain, small, B};
+}
+
+}  // namespace
+}  // namespace dt
+
+#if DT_WINDOW
+
+extern "C" size_t dartree_cache_window_attention_workspace(int32_t R, int32_t B, int32_t max_len, int32_t window,
+                                                           int32_t sinks, int32_t chain, int32_t Hq, int32_t Hkv,
+                                                           int32_t dh) {
+  if (R < 1 || B < 0 || (!chain && B > DARTREE_MAX_B) || max_len < 0 || sinks < 0 || Hkv < 1 || Hq < Hkv ||
+      Hq % Hkv != 0 || (dh != 64 && dh != 128) || static_cast<long long>(B + 1ll) * (Hq / Hkv) > dt::kFar)
+    return 0;
+  // (the larger one: the size does not depend on whether the requests' rows differ)
+  size_t most = 0;
+  for (bool small : {false, true}) {
+    const size_t n = dt::attention_work(R, B, dt::reach_of(B, max_len, window, sinks, chain != 0, small, Hq / Hkv), Hq, Hkv, dh);
+    most = n > most ? n : most;
+  }
+  return most;
+}
+
+extern "C" dartree_status dartree_cache_window_attention(
+    const dartree_cache* cache, int32_t layer, const void* Q, int64_t q_token_stride, int64_t q_rows,
+    const int32_t* start, const uint32_t* mask, const int32_t* n_nodes, const int32_t* table, int32_t max_pages,
+    const int32_t* lens, int32_t R, int32_t B, int32_t max_len, int32_t offset, int32_t window, int32_t sinks,
+    int32_t Hq, float scale, int32_t zero_rest, void* O, void* work, size_t work_bytes, int32_t* err, void* stream) {
+  using namespace dt;
+  CacheAttnParams p{};
+  if (const char* why = attention_check(cache, layer, Q, q_token_stride, table, max_pages, lens, R, B, max_len, Hq,
+                                        scale, O, work, &p))
+    return cache_fail(DARTREE_ERR_INVALID_ARG, why);
+  if (window < 0 || sinks < 0) return cache_fail(DARTREE_ERR_INVALID_ARG, "bad window or sinks");
+  if (mask && B > DARTREE_MAX_B) return cache_fail(DARTREE_ERR_INVALID_ARG, "a tree has at most 1024 nodes");
+  if (start && n_nodes) return cache_fail(DARTREE_ERR_INVALID_ARG, "packed rows have their numbers in start");
+  if (q_rows < 1 || (!start && q_rows < (B + 1ll) * R))
+    return cache_fail(DARTREE_ERR_INVALID_ARG, "q_rows is smaller than R (B + 1)");
+  if (static_cast<long long>(B + 1ll) * p.g > kFar)
+    return cache_fail(DARTREE_ERR_UNSUPPORTED, "too many rows per key/value head");
+  p.chain = mask == nullptr || B == 0;
+  const bool small = start || n_nodes;
+  const Reach reach = reach_of(B, max_len, window, sinks, p.chain, small, p.g);
+  p.mask = mask;
+  p.n_nodes = n_nodes;
+  p.start = start;
+  p.q_rows = q_rows;
+  p.window = reach.window;
+  p.sinks = reach.sinks;
+  p.offset = offset;
+  p.small = small;
+  p.err = err;
+  return attention_run(p, reach, !n_nodes && !start, zero_rest != 0, work, work_bytes, stream);
+}
+
+#else
+
+extern "C" size_t dartree_cache_attention_workspace(int32_t R, int32_t B, int32_t max_len, int32_t Hq,
+                                                    int32_t Hkv, int32_t dh) {
+  if (R < 1 || B < 0 || B > DARTREE_MAX_B || max_len < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 ||
+      (dh != 64 && dh != 128))
+    return 0;
+  return dt::attention_work(R, B, dt::reach_of(B, max_len, 0, 0, false, false, Hq / Hkv), Hq, Hkv, dh);
+}
+
+extern "C" dartree_status dartree_cache_attention_ex(const dartree_cache* cache, int32_t layer, const void* Q,
+                                                     int64_t q_token_stride, const uint32_t* mask,
+                                                     const int32_t* n_nodes, const int32_t* table,
+                                                     int32_t max_pages, const int32_t* lens, int32_t R,
+                                                     int32_t B, int32_t max_len, int32_t Hq, float scale,
+                                                     int32_t zero_rest, void* O, void* work, size_t work_bytes,
+                                                     int32_t* err, void* stream) {
+  using namespace dt;
+  CacheAttnParams p{};
+  if (const char* why = attention_check(cache, layer, Q, q_token_stride, table, max_pages, lens, R, B, max_len, Hq,
+                                        scale, O, work, &p))
+    return cache_fail(DARTREE_ERR_INVALID_ARG, why);
+  if (B > 0 && !mask) return cache_fail(DARTREE_ERR_INVALID_ARG, "null pointer argument");
+  if (B > DARTREE_MAX_B) return cache_fail(DARTREE_ERR_INVALID_ARG, "bad R, B, max_pages, max_len, Hq or scale");
+  p.mask = mask;
+  p.n_nodes = n_nodes;
+  p.err = err;
+  // (without n_nodes it is known here whether rows are left over)
+  return attention_run(p, reach_of(B, max_len, 0, 0, false, false, p.g), !n_nodes, zero_rest != 0, work, work_bytes, stream);
+}
+
 extern "C" dartree_status dartree_cache_attention(const dartree_cache* cache, int32_t layer, const void* Q,
                                                   int64_t q_token_stride, const uint32_t* mask,
                                                   const int32_t* n_nodes, const int32_t* table,
-                                                  int32_t max_pages, const int32_t* lens, int32_t R,
-                                                  int32_t B, int32_t max_len, int32_t Hq, float scale,
-                                                  void* O, void* work, size_t work_bytes, int32_t* err,
-                                                  void* stream) {
+                                                  int32_t max_pages, const int32_t* lens, int32_t R, int32_t B,
+                                                  int32_t max_len, int32_t Hq, float scale, void* O,
+                                                  void* work, size_t work_bytes, int32_t* err, void* stream) {
   return dartree_cache_attention_ex(cache, layer, Q, q_token_stride, mask, n_nodes, table, max_pages, lens, R, B,
                                     max_len, Hq, scale, 0, O, work, work_bytes, err, stream);
 }
+
+#endif

@@ -33,15 +33,46 @@ struct CacheAttnParams {
   float* part;               // [R][Hkv][m_tiles][n_split][tile_rows][dh + kPartHead] (n_split > 1)
   int* err;
   long long wait_limit;      // cycles that a pipeline wait may take
+  // the forms with a sliding window (dartree_cache_window_attention)
+  const int32_t* start;      // packed rows: request r has start[r] .. start[r + 1] - 1 (null: B + 1 each)
+  long long q_rows;          // rows of Q and O in all
+  int window, sinks;         // 2^30 at most
+  int offset;                // row 0 is at position lens[r] + offset
+  int chain;                 // row i is at row 0's position + i and sees what is not behind it (no mask)
+  int small;                 // requests of up to kTreeTail rows are all the few-rows kernel's
 };
 
 // A request's keys: its prefix and nodes, cut at max_len.
 struct Span {
-  int Lp, n, L;  // prefix, nodes, keys
+  int Lp, n, L;     // prefix, nodes, keys
+  int base;         // row 0's position
+  long long row0;   // its row in Q and O
 };
 
+// kWin: the forms with a sliding window.  The prefix ends with row 0's token,
+// at position lens + offset; rows come padded or packed.
+template <bool kWin = false>
 __device__ __forceinline__ bool request_span(const CacheAttnParams& p, int r, Span* s) {
   const int len = p.lens[r];
+  if constexpr (kWin) {
+    const long long base = static_cast<long long>(len) + p.offset;
+    long long n = p.start ? p.B : p.n_nodes ? min(p.n_nodes[r], p.B) : p.B, row0 = static_cast<long long>(r) * (p.B + 1);
+    if (p.start) {
+      row0 = p.start[r];
+      const long long end = p.start[r + 1];
+      // (rows that the buffers do not have, or behind B: skipped, and flagged by
+      // span_flag)
+      if (row0 < 0 || end > p.q_rows) return false;
+      n = min(n, end - row0 - 1);
+    }
+    if (len < 0 || base < -1 || n < 0 || base + n >= 0x7FFFFFFFll) return false;
+    s->base = static_cast<int>(base);
+    s->row0 = row0;
+    s->n = static_cast<int>(n);
+    s->Lp = static_cast<int>(min(base + 1, static_cast<long long>(p.max_len)));
+    s->L = static_cast<int>(min(base + 1 + n, static_cast<long long>(p.max_len)));
+    return true;
+  }
   int n = p.n_nodes ? min(p.n_nodes[r], p.B) : p.B;
   if (len < 0 || n < 0) return false;
   s->Lp = min(len, p.max_len);
@@ -50,10 +81,29 @@ __device__ __forceinline__ bool request_span(const CacheAttnParams& p, int r, Sp
   return true;
 }
 
+// What a request is flagged for: tokens behind max_len; with a window also rows
+// that its packed ones name and the buffers do not have, or behind B.
+template <bool kWin>
+__device__ __forceinline__ bool span_flag(const CacheAttnParams& p, int r) {
+  const long long len = p.lens[r];
+  if constexpr (kWin) {
+    long long n = p.n_nodes ? min(p.n_nodes[r], p.B) : p.B;
+    if (p.start) {
+      const long long row0 = p.start[r], end = p.start[r + 1];
+      if (row0 < 0 || end < row0 || end > p.q_rows || end - row0 - 1 > p.B) return true;
+      n = end - row0 - 1;
+    }
+    return len >= 0 && len + p.offset >= -1 && n >= 0 && len + p.offset + 1 + n > p.max_len;
+  }
+  const int n = p.n_nodes ? min(p.n_nodes[r], p.B) : p.B;
+  return len + n > p.max_len;
+}
 
 // The rows behind a request's whole tiles of 128 that are the few-rows
 // kernel's (of `rows` in all).
-__device__ __forceinline__ int tail_rows(int rows) {
+template <bool kWin>
+__device__ __forceinline__ int tail_rows(const CacheAttnParams& p, int rows) {
+  if (kWin && p.small && rows <= kTreeTail) return rows;
   const int odd = rows % kTreeTile;
   return rows > kTreeTile && odd <= kTreeTail ? odd : 0;
 }
@@ -64,6 +114,53 @@ __device__ __forceinline__ int row_tile_keys(const CacheAttnParams& p, const Spa
   const int last = p.tail ? s.n : min(s.n, (mt * p.tile_rows + p.tile_rows - 1) / p.g);
   const int keys = min(s.L, s.Lp + last);
   return (keys + p.tile_keys - 1) / p.tile_keys;
+}
+
+// The same as a list: n tiles, the t-th is tile at(t).  With a window those
+// between the sinks and the first key that any of the rows sees, `lo`, are
+// passed over (a draft tree's rows: by the root's window).
+template <bool kWin>
+struct KeyTiles {
+  int n, sinks, gap, lo;
+  __device__ __forceinline__ int at(int t) const {
+    if constexpr (!kWin) return t;
+    return t < sinks ? t : t + gap;
+  }
+  // whether any row may see one of the keys [k, k + many)
+  __device__ __forceinline__ bool near(const CacheAttnParams& p, int k, int many) const {
+    if constexpr (!kWin) return true;
+    return k < p.sinks || k + many > lo;
+  }
+};
+
+template <bool kWin>
+__device__ __forceinline__ KeyTiles<kWin> row_key_tiles(const CacheAttnParams& p, const Span& s, int mt, int first_row) {
+  KeyTiles<kWin> t;
+  t.n = row_tile_keys(p, s, mt);
+  if constexpr (kWin) {
+    const int first = p.chain ? first_row / p.g : 0;
+    t.lo = max(0, s.base + first - p.window + 1);
+    t.sinks = min(t.n, (min(p.sinks, s.L) + p.tile_keys - 1) / p.tile_keys);
+    t.gap = max(0, min(t.n, t.lo / p.tile_keys) - t.sinks);
+    t.n -= t.gap;
+  }
+  return t;
+}
+
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// A tree node's depth: the number of nodes that its mask row names.
+__device__ __forceinline__ int node_depth(const CacheAttnParams& p, int r, int node) {
+  const uint32_t* row = p.mask + (static_cast<size_t>(r) * p.B + node) * p.words;
+  int d = 0;
+  for (int w = 0; w < p.words; ++w) d += __popc(__ldg(row + w));
+  return d;
+}
+
+// A row's position: row 0 is the root.
+__device__ __forceinline__ int row_position(const CacheAttnParams& p, const Span& s, int r, int node) {
+  return s.base + (node == 0 ? 0 : p.chain ? node : node_depth(p, r, node - 1));
 }
 
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -146,10 +243,18 @@ __device__ __forceinline__ float row_exponent(const CacheAttnParams& p, float to
 // (rounded down: no weight passes 2^(kBias + kRaise) and fp16's range).
 __device__ __forceinline__ float rise_limit(float m, float fac) { return __fadd_rd(m, __fdividef(kRaise, fac)); }
 
+// Node nd of request r among the rows of Q and O.
+template <bool kWin>
+__device__ __forceinline__ size_t cache_row(const CacheAttnParams& p, const Span& s, int r, int nd) {
+  if constexpr (kWin) return static_cast<size_t>(s.row0) + nd;
+  return static_cast<size_t>(r) * (p.B + 1) + nd;
+}
+
 // Row q of a key/value head in the output (node q / g, query head hk g + q % g).
-__device__ __forceinline__ size_t cache_out_row(const CacheAttnParams& p, int r, int hk, int q) {
+template <bool kWin>
+__device__ __forceinline__ size_t cache_out_row(const CacheAttnParams& p, const Span& s, int r, int hk, int q) {
   const int nd = q / p.g;
-  return ((static_cast<size_t>(r) * (p.B + 1) + nd) * p.Hq + hk * p.g + (q - nd * p.g)) * p.c.dh;
+  return (cache_row<kWin>(p, s, r, nd) * p.Hq + hk * p.g + (q - nd * p.g)) * p.c.dh;
 }
 
 // Row `row` of row tile mt and one split in the workspace: (m, l), and behind
@@ -160,7 +265,9 @@ __device__ __forceinline__ float* cache_part_row(const CacheAttnParams& p, int r
   return p.part + (tile * p.tile_rows + row) * (p.c.dh + kPartHead);
 }
 
-// The tensor-core kernel of many rows (cache_tree.cu).
+// The tensor-core kernel of many rows (cache_tree.cu; with a window
+// cache_window_tree.cu).
 cudaError_t launch_cache_tree(const CacheAttnParams& p, cudaStream_t st);
+cudaError_t launch_cache_window_tree(const CacheAttnParams& p, cudaStream_t st);
 
 }  // namespace dt

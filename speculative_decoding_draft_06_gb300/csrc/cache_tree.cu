@@ -40,8 +40,14 @@
 
 #include "cache_attn.cuh"
 
+#ifndef DT_WINDOW
+#define DT_WINDOW 0  // 1: the forms with a sliding window (an object of their own)
+#endif
+
 namespace dt {
 namespace {
+
+constexpr bool kWin = DT_WINDOW != 0;
 
 constexpr int kMRows = 128, kKeys = 128, kStepKeys = 64;
 constexpr int kExpandWarp0 = 16, kExpandWarps = 8, kMmaWarp0 = 24;
@@ -192,8 +198,29 @@ __device__ __forceinline__ uint32_t row_sees(int pos, int Lp, const uint32_t* mr
   return (nodes << np) | ((1u << np) - 1u);
 }
 
+// With a window: which of the 32 keys from position pos on a row at position
+// `at` sees (ls: keys before it that it may see at most: all up to itself in a
+// chain, the prefix in a tree, whose nodes are named by its mask row, and
+// counted one by one if any may lie outside the window).
+__device__ __forceinline__ uint32_t window_sees(const CacheAttnParams& p, const Span& sp, int r, int pos, int at,
+                                                const uint32_t* mrow) {
+  const int end = p.chain ? at + 1 : sp.Lp;
+  const uint32_t near = low_bits(p.sinks - pos) | ~low_bits(at - p.window + 1 - pos);
+  uint32_t see = low_bits(end - pos) & near;
+  if (!p.chain && mrow && pos + 32 > sp.Lp) {
+    uint32_t nodes = row_sees(pos, sp.Lp, mrow, p.words) & ~low_bits(sp.Lp - pos);
+    if (at - sp.base >= p.window)
+      for (uint32_t left = nodes; left; left &= left - 1) {
+        const int k = __ffs(left) - 1, key = sp.base + node_depth(p, r, pos + k - sp.Lp);
+        if (!(key < p.sinks || at - key < p.window)) nodes &= ~(1u << k);
+      }
+    see |= nodes;
+  }
+  return see;
+}
+
 // SHORT: with a limit of the waits (the form that a wait that runs out is tested with).
-template <int DH, bool SHORT>
+template <int DH, bool SHORT, bool kWin>
 __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnParams p) {
   using L = TreeSmem<DH>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -236,18 +263,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   }
   const int r = p.R > 1 && p.R <= kTreeSorted ? s_r : blockIdx.z;
   Span sp;
-  if (!request_span(p, r, &sp)) return;
+  if (kWin && threadIdx.x == 0 && split == 0 && hk == 0 && mt == 0 && span_flag<kWin>(p, r))
+    atomicOr(p.err, DT_ERR_BAD_INDEX);
+  if (!request_span<kWin>(p, r, &sp)) return;
   const int q0 = mt * kTreeRowsCta;
   // rows of this CTA, without the few behind the request's last whole tile
   const int all = (sp.n + 1) * p.g;
-  const int rows = min(all - tail_rows(all) - q0, kTreeRowsCta);
+  const int rows = min(all - tail_rows<kWin>(p, all) - q0, kTreeRowsCta);
   if (rows <= 0) return;
-  const int t_all = row_tile_keys(p, sp, mt);
+  const KeyTiles<kWin> tl = row_key_tiles<kWin>(p, sp, mt, q0);
   const int t_beg = split * p.split_tiles;
-  const int nt = min(t_all, t_beg + p.split_tiles) - t_beg;
+  const int nt = min(tl.n, t_beg + p.split_tiles) - t_beg;
   if (nt <= 0 && !(split == 0 && p.n_split == 1)) return;
   // steps of 64 keys (the last tile may need one only)
-  const int steps = nt > 0 ? min(2 * nt, (sp.L - t_beg * kKeys + kStepKeys - 1) / kStepKeys) : 0;
+  const int steps = nt > 0 ? min(2 * nt, (sp.L - (tl.at(t_beg + nt - 1) - (nt - 1)) * kKeys + kStepKeys - 1) / kStepKeys) : 0;
   const int two = rows > kMRows ? 2 : 1;
 
   if (warp == kMmaWarp0) tmem_alloc<kTmemCols>(tmem_slot);
@@ -300,7 +329,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
       w[j] = make_uint4(0, 0, 0, 0);
       if (row < rows)
         w[j] = __ldg(reinterpret_cast<const uint4*>(
-                         p.Q + (static_cast<size_t>(r) * (p.B + 1) + node) * p.q_stride +
+                         p.Q + cache_row<kWin>(p, sp, r, node) * p.q_stride +
                          static_cast<size_t>(hk * p.g + (q - node * p.g)) * DH) + k);
     }
     uint8_t* dst = smem + (warp / kLoadWarps) * L::kQTile + (k >> 3) * (kMRows * 128);
@@ -348,7 +377,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     using Codes = typename std::conditional<DH == 128, uint4, uint2>::type;
     Codes code[kIt];
     uint32_t scl[kIt];
-    auto group = [&](int f, int it) { return (t_beg + f) * kKeys + (it * kSub + sub) * 8; };  // its first token
+    auto group = [&](int f, int it) { return tl.at(t_beg + f) * kKeys + (it * kSub + sub) * 8; };  // its first token
     // lane it's page of tile f (not looked at before the next tile)
     auto look_up = [&](int f) {
       const int slot = group(f, lane) >> p.c.log_page;
@@ -358,7 +387,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     auto check = [&](int f, int raw, uint32_t* bits) {
       const int left = sp.L - group(f, lane);
       *bits = 0;
-      if (lane >= kIt || f >= nt || left <= 0) return -1;
+      if (lane >= kIt || f >= nt || left <= 0 || !tl.near(p, group(f, lane), 8)) return -1;
       if (raw < 0 || raw >= p.c.pages) {
         atomicOr(p.err, DT_ERR_BAD_INDEX);
         return -1;
@@ -494,7 +523,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     const uint32_t o_addr = tmem_base + lane_base + kColO + static_cast<uint32_t>(i * 128 + half * (DH / 2));
     const int pair = 1 + i * 4 + quarter;  // the barrier of the two warps that share rows
     const int node = row < rows ? q / p.g : 0;
-    const uint32_t* mrow = node >= 1 ? p.mask + (static_cast<size_t>(r) * p.B + node - 1) * p.words : nullptr;
+    const uint32_t* mrow = node >= 1 && !(kWin && p.chain) ? p.mask + (static_cast<size_t>(r) * p.B + node - 1) * p.words : nullptr;
+    int at = 0;  // (window) the row's position
+    if constexpr (kWin) at = row_position(p, sp, r, node);
     bool go = wait_w(&q_full[i], 0);  // (the same in both warps after every barrier)
     float fac = s_fac[row];
     float m = -INFINITY, l = 0.f;  // the row's reference (the same in both threads), this half's sum
@@ -502,12 +533,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     float limit = -INFINITY;       // the score above which the reference rises
     ref = -INFINITY;
     for (int u = 0; u < steps; ++u) {
-      const int f = u >> 1, b = u & 1, key0 = t_beg * kKeys + u * kStepKeys + half * (kStepKeys / 2);
+      const int f = u >> 1, b = u & 1, key0 = tl.at(t_beg + f) * kKeys + b * kStepKeys + half * (kStepKeys / 2);
       go = go && wait_w(&s_full[2 * i + b], static_cast<uint32_t>(f) & 1u);
       tc_fence_after();
       const uint32_t there = *reinterpret_cast<const uint32_t*>(&s_valid[f % kValid][(2 * b + half) * 4]);
       uint32_t see = ~0u;
-      if (key0 + 32 > sp.Lp || there != ~0u) see = row_sees(key0, sp.Lp, mrow, p.words) & there;
+      if constexpr (kWin) {
+        see = there;
+        if (key0 + 32 > (p.chain ? at + 1 : sp.Lp) || (key0 + 32 > p.sinks && key0 <= at - p.window))
+          see &= window_sees(p, sp, r, key0, at, mrow);
+      } else if (key0 + 32 > sp.Lp || there != ~0u) {
+        see = row_sees(key0, sp.Lp, mrow, p.words) & there;
+      }
       // the weights with the reference as it is; where a score passes the
       // limit the reference rises and they are computed once more
       uint32_t pk[16];
@@ -625,7 +662,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
       to[j] = nullptr;
       if (rr < rows)
         to[j] = p.n_split > 1 ? reinterpret_cast<uint8_t*>(cache_part_row(p, r, hk, mt, split, rr) + kPartHead + d)
-                              : reinterpret_cast<uint8_t*>(p.O + cache_out_row(p, r, hk, q0 + rr) + d);
+                              : reinterpret_cast<uint8_t*>(p.O + cache_out_row<kWin>(p, sp, r, hk, q0 + rr) + d);
     }
 #pragma unroll 1
     for (int ch = 0; ch < 4; ++ch) {
@@ -658,7 +695,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
       __syncwarp();
     }
   }
-  if (threadIdx.x == kMmaWarp0 * 32 && split == 0 && hk == 0 && mt == 0 &&
+  if (!kWin && threadIdx.x == kMmaWarp0 * 32 && split == 0 && hk == 0 && mt == 0 &&
       static_cast<long long>(p.lens[r]) + sp.n > p.max_len)
     atomicOr(p.err, DT_ERR_BAD_INDEX);
   tc_fence_before();
@@ -672,15 +709,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
 template <int DH, bool SHORT>
 cudaError_t launch_tree(const CacheAttnParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = opt_in_smem(k_cache_tree<DH, SHORT>, &done);
+  const cudaError_t e = opt_in_smem(k_cache_tree<DH, SHORT, kWin>, &done);
   if (e != cudaSuccess) return e;
-  return launch_kernel(k_cache_tree<DH, SHORT>, dim3(p.m_tiles * p.n_split, p.c.Hkv, p.R), dim3(kTreeThreads),
+  return launch_kernel(k_cache_tree<DH, SHORT, kWin>, dim3(p.m_tiles * p.n_split, p.c.Hkv, p.R), dim3(kTreeThreads),
                        TreeSmem<DH>::kTotal + 1024, st, true, p);
 }
 
 }  // namespace
 
+#if DT_WINDOW
+cudaError_t launch_cache_window_tree(const CacheAttnParams& p, cudaStream_t st) {
+#else
 cudaError_t launch_cache_tree(const CacheAttnParams& p, cudaStream_t st) {
+#endif
   if (p.wait_limit < kWaitLimitCycles) return p.c.dh == 128 ? launch_tree<128, true>(p, st) : launch_tree<64, true>(p, st);
   return p.c.dh == 128 ? launch_tree<128, false>(p, st) : launch_tree<64, false>(p, st);
 }

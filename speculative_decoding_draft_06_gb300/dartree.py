@@ -136,6 +136,10 @@ def load():
                                             _i32, _i32, _i32, ctypes.c_float, _i32, _vp, _vp,
                                             ctypes.c_size_t, _vp, _vp]),
         "dartree_cache_attention_workspace": (ctypes.c_size_t, [_i32] * 6),
+        "dartree_cache_window_attention": (st, [cache, _i32, _vp, i64, i64, _vp, _vp, _vp, _vp, _i32,
+                                                _vp] + [_i32] * 7 + [ctypes.c_float, _i32, _vp, _vp,
+                                                                     ctypes.c_size_t, _vp, _vp]),
+        "dartree_cache_window_attention_workspace": (ctypes.c_size_t, [_i32] * 9),
         "dartree_cache_reserve": (st, [cache, _vp, _i32, _vp, _vp, _i32, _vp, _vp]),
         "dartree_cache_reserve_ex": (st, [cache, _vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp]),
         "dartree_cache_fork": (st, [cache, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp]),
@@ -715,6 +719,88 @@ class KVCache:
         _launch(self._lib.dartree_cache_attention_ex, idx, stream, self._ref, layer, Q.data_ptr(), sq, m,
                 nn, t, width, ln, R, B, max_len, Hq, dh ** -0.5 if scale is None else scale,
                 new, out.data_ptr(), wp, wb, self._err)
+        return out
+
+    def window_attention(self, layer: int, Q: torch.Tensor, table, lens, *, max_len: int,
+                         window: int | None = None, sinks: int = 0, offset: int = -1,
+                         mask: torch.Tensor | None = None, n_nodes: torch.Tensor | None = None,
+                         start: torch.Tensor | None = None, max_rows: int | None = None,
+                         scale: float | None = None, out: torch.Tensor | None = None,
+                         work: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Attention over the cache in which a row at position q sees the tokens
+        k < ``sinks`` and k > q - ``window`` (None: all) of those it sees otherwise
+        (dartree_cache_window_attention) -> O bf16, shaped as Q.  Row i of request r
+        is at place lens[r] + ``offset`` + i: a chain (single tokens, drafted chains,
+        a prompt's tokens), or with ``mask`` a draft tree behind its root.  Q [R,
+        B+1, Hq, dh] (n_nodes[r] + 1 rows of request r count), or packed [T, Hq, dh]
+        with ``start`` [R+1] (:meth:`plan`'s) and ``max_rows``, a bound of a request's
+        rows.  ``max_len`` bounds the place behind a request's last row.  Rows that
+        belong to no request keep what ``out`` holds (zeros in a new one)."""
+        t, width, ln, R = self._seqs(table, lens)
+        idx, dh = self._idx, self.dh
+        if Q.dtype not in _BF16 or Q.get_device() != idx:
+            raise TypeError(f"Q must be a bf16 tensor on {self.dev}")
+        packed = start is not None
+        if Q.dim() != (3 if packed else 4) or Q.shape[-1] != dh or Q.shape[0] < 1:
+            raise ValueError(f"Q {tuple(Q.shape)} is not {'[T' if packed else '[R, B+1'}, Hq, {dh}]")
+        Hq = Q.shape[-2]
+        if packed:
+            if max_rows is None or max_rows < 1:
+                raise ValueError("packed rows need max_rows")
+            if n_nodes is not None:
+                raise ValueError("packed rows have their numbers in start")
+            total, B = Q.shape[0], max_rows - 1
+        else:
+            if Q.shape[0] != R or Q.shape[1] < 1:
+                raise ValueError(f"Q {tuple(Q.shape)} does not match R={R}")
+            total, B = R * Q.shape[1], Q.shape[1] - 1
+        if Hq < 1 or Hq % self.Hkv:
+            raise ValueError(f"{Hq} query heads are not a multiple of {self.Hkv}")
+        if window is not None and window < 1:
+            raise ValueError("window must be at least 1")
+        sq = Hq * dh
+        if not Q.is_contiguous():
+            *lead, sh, sd = Q.stride()
+            if packed or R == 1 or B == 0:  # (a dimension of one has no stride)
+                n = Q.shape[0] if packed or B == 0 else Q.shape[1]
+                sq = (lead[0] if packed or B == 0 else lead[1]) if n > 1 else sq
+            else:
+                sq = lead[1]
+                if lead[0] != (B + 1) * sq:
+                    raise ValueError("Q needs one stride between rows")
+            if (sh != dh and Hq > 1) or sd != 1:
+                raise ValueError("Q must be dense in heads and dims")
+        m = None
+        if mask is not None and B > 0:
+            m = _ints("mask", mask, idx, R * B * ((B + 31) // 32))
+        nn = None if n_nodes is None else _ints("n_nodes", n_nodes, idx, R)
+        s = None if start is None else _ints("start", start, idx, R + 1)
+        new = out is None
+        if new:
+            out = _alloc(stream, Q.shape, torch.bfloat16, self.dev)
+        elif out.dtype not in _BF16 or out.get_device() != idx or not out.is_contiguous():
+            raise TypeError(f"out must be a contiguous bf16 tensor on {self.dev}")
+        elif out.shape != Q.shape:
+            raise ValueError(f"out has shape {tuple(out.shape)}")
+        w = 0 if window is None else window
+        key = (R, B, max_len, w, sinks, m is None, Hq)
+        need = self._work_bytes.get(key)
+        if need is None:
+            if len(self._work_bytes) > 4096:
+                self._work_bytes.clear()
+            need = self._work_bytes[key] = int(self._lib.dartree_cache_window_attention_workspace(
+                R, B, max_len, w, sinks, m is None, Hq, self.Hkv, dh))
+        wp, wb = None, 0
+        if work is not None:
+            if not work.is_contiguous() or work.get_device() != idx:
+                raise TypeError(f"work must be a contiguous tensor on {self.dev}")
+            wp, wb = work.data_ptr(), work.numel() * work.element_size()
+        elif need:
+            work = _alloc(stream, (need,), torch.uint8, self.dev)
+            wp, wb = work.data_ptr(), need
+        _launch(self._lib.dartree_cache_window_attention, idx, stream, self._ref, layer, Q.data_ptr(), sq,
+                total, s, m, nn, t, width, ln, R, B, max_len, offset, w, sinks, Hq,
+                dh ** -0.5 if scale is None else scale, new, out.data_ptr(), wp, wb, self._err)
         return out
 
     # ------------------------------------------------------ page operations
