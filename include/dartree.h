@@ -481,6 +481,15 @@ dartree_status dartree_cache_append(const dartree_cache *cache, int32_t layer, c
                                     int32_t offset, const int32_t *count, int32_t R, int32_t n,
                                     int32_t *err, void *stream);
 
+/* The same for n packed tokens with slots of their own (dartree_cache_plan's):
+ * token i goes to token slot[i] % page_tokens of page slot[i] / page_tokens,
+ * nowhere if slot[i] < 0.  K, V bf16 [n][Hkv][dh], token_stride elements between
+ * tokens (as above).  A page outside the pool, or that several rows hold, is not
+ * written, and flagged; of two tokens with one slot either may remain. */
+dartree_status dartree_cache_append_slots(const dartree_cache *cache, int32_t layer, const void *K,
+                                          const void *V, int64_t token_stride, const int32_t *slot,
+                                          int32_t n, int32_t *err, void *stream);
+
 /* The values of the tokens lens[r] + offset + i, i < min(n, count[r]), as
  * bf16: K, V [R][n][Hkv][dh], dense, 16-byte aligned.  A token without a page
  * reads as 0; tokens behind count[r] and rows with lens[r] < 0 are left as
@@ -591,6 +600,34 @@ dartree_status dartree_cache_reserve_ex(const dartree_cache *cache, int32_t *tab
                                         int32_t max_pages, const int32_t *lens,
                                         const int32_t *want, int32_t R, int32_t pending,
                                         int32_t *ok, void *stream);
+
+/* Page tables and slot maps of a step's packed tokens: count[r] tokens of row r
+ * go to the positions from f = lens[r] + offset on (offset -1: the first of them
+ * is the last that lens counts, as commit's extra leaves it).
+ * - window > 0: pages that no row at position f or behind it sees through a
+ *   sliding window (dartree_cache_window_attention) are let go: those whose tokens
+ *   t all have sinks <= t <= f - window.  Their table entries become -1, in the
+ *   midst of the row's; such a row is planned with this call from then on, not
+ *   with dartree_cache_reserve, and released before it is forked to.
+ * - Row r comes to hold the pages of its tokens (free ones, the lowest first, to
+ *   the rows in order); lens is not changed.  ok[r] = 0, and the row gets none,
+ *   when lens[r], count[r] or f is negative, a position passes 2^31 - 2, the tokens
+ *   end behind max_tokens (so do all later rows that have some), or the page
+ *   table; when a page that they go to is held by another row too, has a bad
+ *   number, or lies behind one that is not held; for the first row whose pages
+ *   are not there and every later one that needs some.
+ * - start [R + 1]: row r's tokens are the packed ones start[r] .. start[r + 1] - 1
+ *   (none for a row that is refused for its numbers or max_tokens; the others keep
+ *   their places).  row, pos, slot [max_tokens]: a packed token's row, its position
+ *   and its slot page * page_tokens + position % page_tokens (-1: its row has no
+ *   pages); -1 each behind the last token.
+ * R <= 4096, R * max_pages < 2^31, pages * page_tokens < 2^31.  Entries that are
+ * let go and hold bad numbers are flagged in err. */
+dartree_status dartree_cache_plan(const dartree_cache *cache, int32_t *table, int32_t max_pages,
+                                  const int32_t *lens, const int32_t *count, int32_t R,
+                                  int32_t offset, int32_t window, int32_t sinks,
+                                  int32_t max_tokens, int32_t *ok, int32_t *start, int32_t *row,
+                                  int32_t *pos, int32_t *slot, int32_t *err, void *stream);
 
 /* Continues sequences in several ways: for i < n, row dst[i] becomes a copy
  * of row src[i].  Complete pages are shared; the last, partly filled page is

@@ -20,6 +20,7 @@ SOURCES = ([("api.cu", [], "api.o"), ("select.cu", [], "select.o"),
             ("cache.cu", [], "cache.o"), ("cache_attention.cu", [], "cache_attention.o"), ("cache_tree.cu", [], "cache_tree.o"),
             ("cache_attention.cu", ["-DDT_WINDOW=1"], "cache_window.o"),
             ("cache_tree.cu", ["-DDT_WINDOW=1"], "cache_window_tree.o"),
+            ("cache_plan.cu", [], "cache_plan.o"),
             ("sample.cu", [], "sample.o")]
            + [("head_tc.cu", [f"-DDT_N={n}"], f"head_tc_{n}.o") for n in _NS]
            + [("head_simt.cu", [f"-DDT_N={n}"], f"head_simt_{n}.o") for n in _NS])

@@ -2,7 +2,7 @@
 // operations (reserve, fork, commit, release, copy).
 #include <cuda_bf16.h>
 
-#include "cache.cuh"
+#include "cache_pages.cuh"
 
 namespace dt {
 namespace {
@@ -152,6 +152,40 @@ __global__ void __launch_bounds__(256) k_cache_append(const TokenParams p) {
   base[half + codes + s.t * (DH / 16) + s.blk] = static_cast<uint8_t>(sv);
 }
 
+// The same for packed tokens with slots of their own: token i goes to token
+// slot[i] % page_tokens of page slot[i] / page_tokens (negative: nowhere).
+// Bound as the above by memory: 24000 packed tokens of 8 heads of 128 written and read back 54 us.
+template <int DH>
+__global__ void __launch_bounds__(256) k_cache_append_slots(const TokenParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const TokenSlot s = token_of<DH>(p);
+  if (s.r >= 1 || s.i >= p.n) return;
+  const size_t at = static_cast<size_t>(s.i) * p.token_stride + s.h * DH + s.blk * 16;
+  const uint4* k = reinterpret_cast<const uint4*>(p.K + at);
+  const uint4* v = reinterpret_cast<const uint4*>(p.V + at);
+  const uint4 kin[2] = {load_once(k), load_once(k + 1)};
+  const uint4 vin[2] = {load_once(v), load_once(v + 1)};
+  const int slot = __ldg(p.table + s.i);
+  if (slot < 0) return;
+  const int page = slot >> p.c.log_page, t = slot & ((1 << p.c.log_page) - 1);
+  const bool there = page < p.c.pages;
+  const int holders = p.refs && there ? p.refs[page] : 1;
+  uint32_t sk, sv;
+  const uint2 ck = quantise16(kin, 1.f / p.c.k_scale, &sk);
+  const uint2 cv = quantise16(vin, 1.f / p.c.v_scale, &sv);
+  if (!there || holders > 1) {  // (other rows read it)
+    if (s.blk == 0 && s.h == 0 && p.err) atomicOr(p.err, DT_ERR_BAD_INDEX);
+    return;
+  }
+  uint8_t* base = p.c.pool + static_cast<size_t>(page) * p.c.page_bytes + static_cast<size_t>(s.h) * p.c.chunk;
+  const int codes = (DH / 2) << p.c.log_page, half = p.c.chunk >> 1;
+  *reinterpret_cast<uint2*>(base + t * (DH / 2) + s.blk * 8) = ck;
+  base[codes + t * (DH / 16) + s.blk] = static_cast<uint8_t>(sk);
+  *reinterpret_cast<uint2*>(base + half + t * (DH / 2) + s.blk * 8) = cv;
+  base[half + codes + t * (DH / 16) + s.blk] = static_cast<uint8_t>(sv);
+}
+
 // 8 bytes of codes and a scale byte -> 16 bf16 (exact).
 __device__ __forceinline__ void values16(uint2 codes, uint32_t scale, float mul, uint4 (&out)[2]) {
   const uint32_t s2 = e4m3x2_to_f16x2(scale | (scale << 8));
@@ -198,39 +232,7 @@ __global__ void __launch_bounds__(256) k_cache_read(const TokenParams p) {
 }
 
 // --------------------------------------------------------- page operations
-constexpr int kPlanThreads = 1024;
-constexpr int kMaxReserveRows = 4096;
 constexpr int kMaxForks = 1024;
-
-// Exclusive prefix sum of one value per thread over the block (1024
-// threads); *total is the block's sum.  sh: 33 ints.
-__device__ __forceinline__ int block_exclusive(int v, int* sh, int* total) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int inc = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kFullMask, inc, o);
-    if (lane >= o) inc += y;
-  }
-  if (lane == 31) sh[warp] = inc;
-  __syncthreads();
-  if (warp == 0) {
-    const int w = sh[lane];
-    int wi = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kFullMask, wi, o);
-      if (lane >= o) wi += y;
-    }
-    sh[lane] = wi - w;
-    if (lane == 31) sh[32] = wi;
-  }
-  __syncthreads();
-  const int out = sh[warp] + inc - v;
-  *total = sh[32];
-  __syncthreads();
-  return out;
-}
 
 // Calls give(rank, page) for the first `need` free pages (refs == 0) in
 // ascending order of their numbers; returns how many there were (at most
@@ -743,6 +745,24 @@ extern "C" dartree_status dartree_cache_append(const dartree_cache* cache, int32
   p.req_stride = req_stride;
   p.token_stride = token_stride;
   return cache_launched(launch_kernel(p.c.dh == 128 ? k_cache_append<128> : k_cache_append<64>, dim3(blocks),
+                                      dim3(256), 0, static_cast<cudaStream_t>(stream), true, p));
+}
+
+extern "C" dartree_status dartree_cache_append_slots(const dartree_cache* cache, int32_t layer, const void* K,
+                                                     const void* V, int64_t token_stride, const int32_t* slot,
+                                                     int32_t n, int32_t* err, void* stream) {
+  using namespace dt;
+  TokenParams p{};
+  unsigned blocks = 0;
+  const dartree_status s = token_params(cache, layer, K, V, slot, 1, slot, 0, nullptr, 1, n, err, &p, &blocks);
+  if (s != DARTREE_OK) return s;
+  if (token_stride % 8 != 0 || token_stride < static_cast<int64_t>(p.c.Hkv) * p.c.dh)
+    return cache_fail(DARTREE_ERR_INVALID_ARG, "strides must be multiples of 8 elements, tokens not overlapping");
+  p.K = static_cast<const uint16_t*>(K);
+  p.V = static_cast<const uint16_t*>(V);
+  p.refs = cache->refs;
+  p.token_stride = token_stride;
+  return cache_launched(launch_kernel(p.c.dh == 128 ? k_cache_append_slots<128> : k_cache_append_slots<64>, dim3(blocks),
                                       dim3(256), 0, static_cast<cudaStream_t>(stream), true, p));
 }
 

@@ -125,6 +125,8 @@ def load():
         "dartree_cache_page_bytes": (ctypes.c_size_t, [_i32, _i32, _i32]),
         "dartree_cache_append": (st, [cache, _i32, _vp, _vp, i64, i64, _vp, _i32, _vp, _i32, _vp,
                                       _i32, _i32, _vp, _vp]),
+        "dartree_cache_append_slots": (st, [cache, _i32, _vp, _vp, i64, _vp, _i32, _vp, _vp]),
+        "dartree_cache_plan": (st, [cache, _vp, _i32, _vp, _vp] + [_i32] * 5 + [_vp] * 7),
         "dartree_cache_read": (st, [cache, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32,
                                     _vp, _vp]),
         "dartree_cache_read_ex": (st, [cache, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32,
@@ -641,6 +643,29 @@ class KVCache:
                 V.data_ptr(), sr, sn, t, width, ln, offset,
                 None if count is None else _ints("count", count, idx, R), R, n, self._err)
 
+    def append_slots(self, layer: int, K: torch.Tensor, V: torch.Tensor, slot: torch.Tensor, *,
+                     stream=None) -> None:
+        """Quantise packed K, V [T, Hkv, dh] bf16 into the slots [T] int32 of
+        :meth:`plan` (dartree_cache_append_slots); the token stride is a multiple
+        of 8, the same in both."""
+        idx, Hkv, dh = self._idx, self.Hkv, self.dh
+        if K.dtype not in _BF16 or K.get_device() != idx:
+            raise TypeError(f"K must be a bf16 tensor on {self.dev}")
+        if V.dtype not in _BF16 or V.get_device() != idx:
+            raise TypeError(f"V must be a bf16 tensor on {self.dev}")
+        n = K.shape[0]
+        if K.shape != (n, Hkv, dh) or V.shape != K.shape or n < 1:
+            raise ValueError(f"K {tuple(K.shape)} / V {tuple(V.shape)} are not [T, {Hkv}, {dh}]")
+        (sn, sh, sd), (vn, vh, vd) = K.stride(), V.stride()
+        if n == 1:  # (a dimension of one has no stride)
+            sn = vn = Hkv * dh
+        if Hkv == 1:
+            sh = vh = dh
+        if (sn, sh, sd) != (vn, vh, vd) or sd != 1 or sh != dh:
+            raise ValueError("K and V need equal strides, dense in heads and dims")
+        _launch(self._lib.dartree_cache_append_slots, idx, stream, self._ref, layer, K.data_ptr(),
+                V.data_ptr(), sn, _ints("slot", slot, idx, n), n, self._err)
+
     def read(self, layer: int, table, lens, n: int, *, offset: int = 0,
              count: torch.Tensor | None = None, out: tuple | None = None, stream=None) -> tuple:
         """The values of the tokens lens[r] + offset + i, i < n, as bf16 (K,
@@ -813,6 +838,27 @@ class KVCache:
         _launch(self._lib.dartree_cache_reserve_ex, self._idx, stream, self._ref, t, width, ln,
                 _ints("want", want, self._idx, R), R, pending, ok.data_ptr())
         return ok
+
+    def plan(self, table, lens, count, *, max_tokens: int, offset: int = -1,
+             window: int | None = None, sinks: int = 0, stream=None) -> dict:
+        """Pages for count[r] packed tokens per row from position lens[r] +
+        ``offset`` on, and their maps (dartree_cache_plan) -> {"ok" [R], "start"
+        [R+1], "row", "pos", "slot" [max_tokens]} int32.  With ``window``, pages that
+        it has left behind (but for the first ``sinks`` tokens') are let go."""
+        t, width, ln, R = self._seqs(table, lens)
+        if max_tokens < 0 or (window is not None and window < 1):
+            raise ValueError("max_tokens must not be negative, window at least 1")
+        c = _ints("count", count, self._idx, R)
+        # (one allocation: five cost 4 us more)
+        pad = -(-max_tokens // 4) * 4
+        sizes = (R, R + 1, max_tokens, max_tokens, max_tokens)
+        at = [0, -(-R // 4) * 4]
+        at += [at[1] + -(-(R + 1) // 4) * 4 + k * pad for k in range(3)]
+        buf = _alloc(stream, (at[4] + max(pad, 4),), _I32, self.dev)
+        base = buf.data_ptr()
+        _launch(self._lib.dartree_cache_plan, self._idx, stream, self._ref, t, width, ln, c, R, offset,
+                window or 0, sinks, max_tokens, *[base + 4 * a for a in at], self._err)
+        return {k: buf[a:a + n] for k, a, n in zip(("ok", "start", "row", "pos", "slot"), at, sizes)}
 
     def fork(self, table, lens, src, dst, *, pending: int = 0, stream=None) -> torch.Tensor:
         """Rows dst become copies of rows src -> ok [n] int32
