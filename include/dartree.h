@@ -704,6 +704,48 @@ dartree_status dartree_sample(const void *logits, int32_t bf16, int64_t row_stri
                               const int32_t *top_k, const float *top_p, const float *min_p,
                               const float *u, int32_t *token, float *prob, void *stream);
 
+/* Verification of drafted tokens that were drawn from a drafter's distribution:
+ * which of them the target accepts, and a token of its own behind them.  The
+ * result is distributed as the target's own tokens (dartree_sample's) whatever
+ * the drafter's distribution is.  (Of tokens that were not drawn, a top-k's, take
+ * dartree_sample's for pred of dartree_accept.)
+ *   parent, token [R][B], n_out [R]  the drafted trees, parents first; parent
+ *        NULL: chains, node i the child of node i - 1;
+ *   logits  the target's, row 0 behind the root, row i + 1 behind node i: row i of
+ *        request r at element r req_stride + i row_stride, fp32 or bf16 (`bf16`);
+ *   draft  the drafter's logits, laid out alike with strides and type of its own:
+ *        from row i's distribution the children of row i were drawn, one after the
+ *        other without replacement, in the order of their numbers.  draft_rows: a
+ *        request's rows (B are enough for chains; a row behind them has no
+ *        children);
+ *   temperature, top_k, top_p, min_p [R] the target's settings as
+ *        dartree_sample's, draft_temperature [R] the drafter's (NULL or not above
+ *        0: 1);
+ *   u [R][B + 1] in [0, 1): u[i + 1] tests node i, u[0] draws the last token.
+ * At a node with the target's probabilities p (after the cuts) and the drafter's q,
+ * with A = 0, N = Z = 1: the children x with q(x) > 0 are tried in order (of two
+ * with one token the first).  With a = N / Z, x is accepted if u a q(x) < p(x) - A
+ * q(x); otherwise A += a, Z -= q(x), N = sum_i max(p_i - A q_i, 0) (below 2^-40: 0,
+ * and no other is accepted).  An accepted node is the next; at the last one the
+ * token is the one with the lowest index whose running sum of max(p_i - A q_i, 0)
+ * (of p_i where N = 0) exceeds u[0] times their total, prob its share of it.
+ * temperature <= 0 (or NaN): the child that has the largest logit's token (lowest
+ * index) is accepted.  NaN logits count as -inf, +inf as in dartree_sample; a
+ * target's row of -inf ends the path with token -1, prob 0.
+ * Out: accept_len [R], accept_nodes [R][max_len], bonus [R] as dartree_accept
+ * writes them, prob [R] fp32.  Weights are whole numbers in units of 2^-44 of a
+ * row's largest wherever their sums decide; only rows of the path are read.
+ * Context-free, asynchronous, no allocation.  V <= 2^18, B <= 1024. */
+dartree_status dartree_verify(const int32_t *parent, const int32_t *token, const int32_t *n_out,
+                              const void *logits, int32_t bf16, int64_t req_stride,
+                              int64_t row_stride, const void *draft, int32_t draft_bf16,
+                              int64_t draft_req_stride, int64_t draft_row_stride,
+                              int32_t draft_rows, int32_t V, int32_t R, int32_t B,
+                              const float *temperature, const int32_t *top_k, const float *top_p,
+                              const float *min_p, const float *draft_temperature, const float *u,
+                              int32_t max_len, int32_t *accept_len, int32_t *accept_nodes,
+                              int32_t *bonus, float *prob, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -39,54 +39,19 @@
 // (monotone in the logit) gives the class in which it falls; the class is
 // gathered (refined by digits of the key while it is large), sorted, and the
 // cut's token found in it.
-#include <cuda_bf16.h>
-
-#include "block.cuh"
-#include "cache.cuh"
-#include "ptx.cuh"
+#include "row_cuts.cuh"
 
 namespace dt {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 1024;
-constexpr float kBinsPer2 = 20.f;    // classes per power of two
 constexpr float kMassUnit = 16000.f; // 2^18 2^(1/40) units fit 32 bits
 constexpr int kTable = 768;          // bf16 logits of a sign whose weights are tabled
 constexpr int kList = 2944;          // candidates
 constexpr float kWant = 1800.f;      // candidates aimed at
-constexpr int kClass = 1024;         // members of a class that are sorted
-constexpr int kRanked = 128;         // members of a class that are ranked by comparisons
 constexpr int kUnits = 4096;         // 16-byte units of a CTA that may hold candidates
 constexpr int kMaxCl = 8;
-constexpr int kIdxBits = 18;
-constexpr float kZeroBelow = -46.f;  // 2^-46 rounds to 0 in units of 2^-44
-constexpr int kExpBits = 10;
-
-// 2^(j / 1024) as the sum of two floats.
-struct alignas(16) ExpTable {
-  float v[2 << kExpBits];  // hi, lo
-};
-constexpr double exp2_fraction(double x) {  // x in [0, 1): the exponential series of x ln 2
-  const double t = x * 0.69314718055994530941723212145818;
-  double sum = 1.0, term = 1.0;
-  for (int k = 1; k < 24; ++k) {
-    term *= t / k;
-    sum += term;
-  }
-  return sum;
-}
-constexpr ExpTable make_exp_table() {
-  ExpTable t{};
-  for (int j = 0; j < (1 << kExpBits); ++j) {
-    const double x = exp2_fraction(static_cast<double>(j) / (1 << kExpBits));
-    t.v[2 * j] = static_cast<float>(x);
-    t.v[2 * j + 1] = static_cast<float>(x - static_cast<double>(t.v[2 * j]));
-  }
-  return t;
-}
-__device__ constexpr ExpTable g_exp = make_exp_table();
 
 struct SampleParams {
   const void* logits;
@@ -99,23 +64,13 @@ struct SampleParams {
   float* prob;
 };
 
-struct Ctl {             // the leader's decisions, read by the whole cluster
-  unsigned long long prefix, mask;  // class within the bin
-  unsigned long long keep;          // threshold key
-  unsigned long long left, total;   // draw: mass before the token in the warp's share, whole mass
-  float top;                        // the row's largest logit
-  int bin, last;
-  int refine;            // 1: another digit, 0: gather
-  int warp;              // draw: the warp (of the cluster)
-  int done;              // the list decided the row
-};
-
 struct Part {            // a CTA's share of the pass, for the leader
   float top, sum, off;
   int lost;              // more units than kUnits
 };
 
 struct Smem {
+  static constexpr int kThreads = kWarps * 32;
   __align__(16) float2 exp[1 << kExpBits];
   union {
     struct {
@@ -144,524 +99,8 @@ struct Smem {
   Ctl ctl;
 };
 
-// One row's weights.
-struct Weights {
-  float top;      // the largest logit
-  float ch, cl;   // log2(e) / T as a sum of two floats
-  const float2* exp;
-
-  // log2 of the weight, rounded to fp32 (monotone in x; x finite or -inf)
-  __device__ __forceinline__ float log2w(float x) const { return x == top ? 0.f : (x - top) * ch; }
-
-  // The weight in units of 2^-44, to about 2^-45.  l - top and its product
-  // with log2(e) / T are carried as sums of two floats, the fraction is split
-  // into a table entry 2^(j/1024) and |t| <= 2^-11, and 2^t - 1 =
-  // t ln2 + t^2 (ln2^2/2 + t ln2^3/6) needs the low parts of its first term
-  // only.
-  __device__ __forceinline__ unsigned long long weight44(float x) const {
-    if (x == top) return 1ull << 44;
-    const float s = x - top;
-    const float p = s * ch;
-    if (!(p >= kZeroBelow)) return 0ull;  // (also -inf)
-    const float bb = s - x;               // x - top = s + err exactly
-    const float err = (x - (s - bb)) - (top + bb);
-    float e = fmaf(s, ch, -p);
-    e = fmaf(s, cl, e);
-    e = fmaf(err, ch, e);
-    // n = the nearest multiple of 1/1024 to p, by adding 1.5 2^13 (ulp 2^-10)
-    const float big = p + 12288.f;
-    const float t0 = p - (big - 12288.f);  // exact, |t0| <= 2^-11
-    const float t = t0 + e;
-    e -= t - t0;                          // t + e unchanged, |e| < 2^-35
-    const int n = __float_as_int(big) - __float_as_int(12288.f);  // 1024 n
-    const float2 T = exp[n & 1023];
-    constexpr float kL1 = 0.693147182464599609375f;  // ln 2 = kL1 + kL1lo
-    constexpr float kL1lo = -1.904654299957768e-9f;
-    const float a = t * kL1;
-    float b = fmaf(t, kL1, -a);
-    b = fmaf(t, kL1lo, b);
-    b = fmaf(e, kL1, b);
-    b = fmaf(t * t, fmaf(t, 0.05550410866f, 0.24022650696f), b);  // 2^(t+e) - 1 = a + b
-    const float m = T.x * a;              // |m| < 2^-10
-    float lo = fmaf(T.x, a, -m);
-    lo = fmaf(T.x, b, lo);
-    lo = fmaf(T.y, a, lo);
-    lo += T.y;                            // T (1 + a + b) = T.x + m + lo, |lo| < 2^-22
-    // in units of 2^-45: T.x's mantissa, m in multiples of 2^-32 (the low bits
-    // of m + 1.5 2^-9, whose ulp that is), what m has left and lo (ulp 2^-44
-    // at 1.5 2^-21)
-    constexpr float kC1 = 1.5f / 512.f, kC2 = 1.5f / 2097152.f;
-    const float m1 = m + kC1;
-    const float rest = (m - (m1 - kC1)) + lo;
-    const float m2 = rest + kC2;
-    const int i1 = __float_as_int(m1) - __float_as_int(kC1), i2 = __float_as_int(m2) - __float_as_int(kC2);
-    const long long w45 = (static_cast<long long>((__float_as_int(T.x) & 0x7FFFFF) | 0x800000) << 22) +
-                          (static_cast<long long>(i1) << 13) + 2 * i2;
-    const int down = 1 - (n >> 10);       // 1 .. 47
-    return static_cast<unsigned long long>((w45 + (1ll << (down - 1))) >> down);
-  }
-};
-
-// (-0 + 0 = 0: the two zeros are one logit)
-__device__ __forceinline__ unsigned long long key50(float x, int idx) {
-  return (static_cast<unsigned long long>(float_order(x + 0.f)) << kIdxBits) |
-         static_cast<unsigned>((1 << kIdxBits) - 1 - idx);
-}
-__device__ __forceinline__ float key50_value(unsigned long long k) {
-  return order_float(static_cast<uint32_t>(k >> kIdxBits));
-}
-
-// Inclusive scan of (count, mass) over the block's threads.
-__device__ __forceinline__ void block_scan(Smem& sm, unsigned& c, unsigned long long& m) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned cy = __shfl_up_sync(kFullMask, c, o);
-    const unsigned long long my = __shfl_up_sync(kFullMask, m, o);
-    if (lane >= o) {
-      c += cy;
-      m += my;
-    }
-  }
-  if (lane == 31) {
-    sm.scan_c[warp] = c;
-    sm.scan_m[warp] = m;
-  }
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) {
-    c += sm.scan_c[w];
-    m += sm.scan_m[w];
-  }
-  __syncthreads();
-}
-
-template <typename E>
-__device__ __forceinline__ float logit(const E* row, int i);
-template <>
-__device__ __forceinline__ float logit<float>(const float* row, int i) {
-  const float x = __ldg(row + i);
-  return x == x ? x : -INFINITY;
-}
-template <>
-__device__ __forceinline__ float logit<uint16_t>(const uint16_t* row, int i) {
-  const float x = bf16_bits_to_float(__ldg(row + i));
-  return x == x ? x : -INFINITY;
-}
-
-// floor(x 2^64) for x in (0, 1).
-__device__ __forceinline__ unsigned long long fraction64(float x) {
-  const unsigned b = __float_as_uint(x);
-  const int e = static_cast<int>(b >> 23);  // x = m 2^(e - 150), subnormals as if e were 1
-  const unsigned long long m = (b & 0x7FFFFFu) | (e ? 0x800000u : 0u);
-  const int up = max(e, 1) - 86;
-  return up >= 0 ? m << up : up > -24 ? m >> -up : 0ull;
-}
-
-// w / z to fp32, for w <= z: both as sums of two floats (49 bits or more), the
-// quotient of the upper ones corrected once.  (An fp64 division: 0.7 us.)
-__device__ __forceinline__ float share_of(unsigned long long w, unsigned long long z) {
-  const float wh = __ull2float_rn(w), zh = __ull2float_rn(z);
-  const float wl = __ll2float_rn(static_cast<long long>(w - __float2ull_rn(wh)));
-  const float zl = __ll2float_rn(static_cast<long long>(z - __float2ull_rn(zh)));
-  const float q = __fdiv_rn(wh, zh);
-  return q + __fdiv_rn(fmaf(-q, zh, wh) + fmaf(-q, zl, wl), zh);
-}
-
-// ceil(p z) for p in (0, 1) (fp32) and z < 2^63, at least 1.
-__device__ __forceinline__ unsigned long long ceil_share(float p, unsigned long long z) {
-  const unsigned long long f = fraction64(p) >> 1;
-  const unsigned long long hi = __umul64hi(f, z), lo = f * z;
-  const unsigned long long q = (hi << 1) | (lo >> 63);
-  const unsigned long long c = q + ((lo << 1) != 0ull ? 1ull : 0ull);
-  return c > 0ull ? c : 1ull;
-}
-
-// A row in 16-byte units: `head` logits before the first aligned address,
-// `units` units, the rest behind them.  Warp w of the cluster's n has the
-// units [w share, (w + 1) share), warp 0 the head too and warp n - 1 the
-// rest: the shares follow the index order.
-template <typename E>
-struct Row {
-  static constexpr int kPer = 16 / static_cast<int>(sizeof(E));
-  const E* src;
-  int V, head, units;
-  __device__ __forceinline__ Row(const E* p, int v) : src(p), V(v) {
-    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15);
-    head = off == 0 ? 0 : (16 - off) / static_cast<int>(sizeof(E));
-    head = head < v ? head : v;
-    units = (v - head) / kPer;
-  }
-  __device__ __forceinline__ uint4 load(int u) const {
-    return __ldg(reinterpret_cast<const uint4*>(src + head) + u);
-  }
-  __device__ __forceinline__ int index(int u) const { return head + u * kPer; }
-};
-
-template <typename E>
-__device__ __forceinline__ void unpack(uint4 v, float (&x)[16 / sizeof(E)]);
-template <>
-__device__ __forceinline__ void unpack<float>(uint4 v, float (&x)[4]) {
-  x[0] = __uint_as_float(v.x);
-  x[1] = __uint_as_float(v.y);
-  x[2] = __uint_as_float(v.z);
-  x[3] = __uint_as_float(v.w);
-}
-template <>
-__device__ __forceinline__ void unpack<uint16_t>(uint4 v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    x[2 * k] = __uint_as_float(w[k] << 16);
-    x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-  }
-}
-
-// The largest of a unit's logits (fmaxf drops NaN; all NaN: NaN, which no
-// comparison takes).
-template <int N>
-__device__ __forceinline__ float max_of(const float (&x)[N]) {
-  float m = x[0];
-#pragma unroll
-  for (int k = 1; k < N; ++k) m = fmaxf(m, x[k]);
-  return m;
-}
-
-// f(unit, its number) for the lane's units of a warp's [ub, ue), with a load
-// in flight ahead (three: 4% to 7% slower by their moves).
-template <typename E, typename F>
-__device__ __forceinline__ void each_unit(const Row<E>& row, int ub, int ue, F f) {
-  int u = ub + (threadIdx.x & 31);
-  auto at = [&](int q) { return q < ue ? row.load(q) : make_uint4(0, 0, 0, 0); };
-  uint4 next = at(u);
-#pragma unroll 1
-  for (; u < ue; u += 32) {
-    const uint4 v = next;
-    next = at(u + 32);
-    f(v, u);
-  }
-}
-
-// What the cuts work on.  LIST: the leader's list of candidates, by the
-// leader's block alone; otherwise the whole row, by the cluster.
 template <bool LIST, typename E>
-struct Source {
-  Smem& sm;
-  Smem& ls;
-  Row<E> row;
-  int ub, ue;      // the warp's units (row)
-  int first, last; // 1: the warp has the head, the rest
-  int n;           // list entries
-  int cl;
-  bool lead;
-  int gw, share;   // the warp in the cluster, units per warp (row)
-  using Elem = E;
-  __device__ __forceinline__ void sync() const {
-    if constexpr (LIST) __syncthreads();
-    else cluster_sync();
-  }
-  // f(logit, index) for the row's logits above -inf, in no particular order
-  template <typename F>
-  __device__ __forceinline__ void each_value(F f) const {
-    const int lane = threadIdx.x & 31;
-    auto one = [&](float x, int i) {
-      if (x > -INFINITY) f(x, i);  // (not NaN either)
-    };
-    if (first && lane < row.head) one(logit<E>(row.src, lane), lane);
-    const int rest = row.index(row.units);
-    if (last && lane < row.V - rest) one(logit<E>(row.src, rest + lane), rest + lane);
-    each_unit(row, ub, ue, [&](uint4 v, int u) {
-      float x[Row<E>::kPer];
-      unpack<E>(v, x);
-#pragma unroll
-      for (int k = 0; k < Row<E>::kPer; ++k) one(x[k], row.index(u) + k);
-    });
-  }
-  template <typename F>
-  __device__ __forceinline__ void each(F f) const {  // f(logit, key)
-    if constexpr (LIST) {
-      for (int i = threadIdx.x; i < n; i += kThreads) {
-        const unsigned long long k = sm.list[i];
-        f(key50_value(k), k);
-      }
-    } else {
-      each_value([&](float x, int i) { f(x, key50(x, i)); });
-    }
-  }
-  // class b's sums over the cluster (leader)
-  __device__ __forceinline__ void sums(int b, unsigned* c, unsigned long long* m) const {
-    *c = 0;
-    *m = 0;
-    for (int q = 0; q < (LIST ? 1 : cl); ++q) {
-      const Smem* o = LIST ? &sm : at_rank(&sm, q);
-      *c += o->count[b];
-      *m += (static_cast<unsigned long long>(o->mass_hi[b]) << 32) + o->mass_lo[b];
-    }
-  }
-};
-
-// A 64-bit sum in shared memory from two 32-bit atomics (shared memory has
-// no 64-bit add): the low word's add that wraps carries.
-__device__ __forceinline__ void add_mass(Smem& sm, int b, unsigned long long w) {
-  const unsigned lo = static_cast<unsigned>(w);
-  const unsigned old = atomicAdd(&sm.mass_lo[b], lo);
-  const unsigned hi = static_cast<unsigned>(w >> 32) + (old + lo < old ? 1u : 0u);
-  if (hi) atomicAdd(&sm.mass_hi[b], hi);
-}
-
-__device__ __forceinline__ void clear_classes(Smem& sm) {
-  for (int i = threadIdx.x; i < kBins; i += kThreads) {
-    sm.mass_lo[i] = 0;
-    sm.mass_hi[i] = 0;
-    sm.count[i] = 0;
-  }
-}
-
-// Among the classes (ascending class = descending order) finds the one in
-// which the running count or mass reaches `target`; the leader's block.
-// c_before, m_before: what lies before the first class, then before the one
-// found.  Returns the class; *members: its count.
-template <typename S>
-__device__ __forceinline__ int pick_class(const S& s, bool by_count, unsigned long long target, unsigned& c_before,
-                                          unsigned long long& m_before, unsigned* members) {
-  constexpr int kPer = kBins / kThreads;
-  Smem& sm = s.sm;
-  unsigned cs[kPer], c = 0;
-  unsigned long long ms[kPer], m = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    s.sums(threadIdx.x * kPer + j, &cs[j], &ms[j]);
-    c += cs[j];
-    m += ms[j];
-  }
-  unsigned bc = c_before - c;
-  unsigned long long bm = m_before - m;
-  block_scan(sm, c, m);
-  bc += c;
-  bm += m;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    if (by_count ? (bc < target && target <= bc + cs[j]) : (bm < target && target <= bm + ms[j])) {
-      sm.picked = threadIdx.x * kPer + j;
-      sm.picked_n = cs[j];
-      sm.picked_c = bc;
-      sm.picked_m = bm;
-    }
-    bc += cs[j];
-    bm += ms[j];
-  }
-  __syncthreads();
-  c_before = sm.picked_c;
-  m_before = sm.picked_m;
-  *members = sm.picked_n;
-  const int k = sm.picked;
-  __syncthreads();
-  return k;
-}
-
-constexpr float kBinBig = 12582912.f;
-
-// The classes of the cuts: -log2 w in steps of 1 / kBinsPer2, to the nearest
-// (by adding 1.5 2^23, whose ulp is 1).
-__device__ __forceinline__ int bin_of_log2(float y) {
-  return min(kBins - 1, __float_as_int(fmaf(y, -kBinsPer2, kBinBig)) - __float_as_int(kBinBig));
-}
-__device__ __forceinline__ int bin_of(const Weights& wt, float x) { return bin_of_log2(wt.log2w(x)); }
-
-// The element at which the running count (by_count) or mass in the order
-// reaches `target`: its key becomes `keep`; the mass up to and with it is
-// left in the leader's *upto.  The bins' sums are in place.  All threads of
-// the source call it.  Returns whether the bins' sums were used for digits
-// (else those before the cut's bin still hold).
-template <typename S>
-__device__ bool cut(const S& s, const Weights& wt, bool by_count, unsigned long long target,
-                    unsigned long long& keep, unsigned long long* upto) {
-  Smem& sm = s.sm;
-  Ctl& ctl = s.ls.ctl;
-  unsigned c_before = 0, members = 0;
-  unsigned long long m_before = 0;
-  if (s.lead) {
-    const int b = pick_class(s, by_count, target, c_before, m_before, &members);
-    if (threadIdx.x == 0) {
-      ctl.bin = b;
-      ctl.prefix = ctl.mask = 0;
-      ctl.refine = members > kClass;
-    }
-  }
-  s.sync();
-  // a class too large to be gathered: by digits of its keys, 10 bits each
-  bool refined = false;
-  for (int shift = 40; ctl.refine; shift -= 10) {
-    refined = true;
-    const int bin = ctl.bin;
-    const unsigned long long pre = ctl.prefix, msk = ctl.mask;
-    clear_classes(sm);
-    __syncthreads();
-    s.each([&](float x, unsigned long long key) {
-      if (key < keep || (key & msk) != pre || bin_of(wt, x) != bin) return;
-      const unsigned long long w = wt.weight44(x);
-      if (w == 0) return;
-      const int d = 1023 - static_cast<int>((key >> shift) & 1023);
-      atomicAdd(&sm.count[d], 1u);
-      add_mass(sm, d, w);
-    });
-    s.sync();
-    if (s.lead) {
-      const int d = pick_class(s, by_count, target, c_before, m_before, &members);
-      if (threadIdx.x == 0) {
-        ctl.prefix |= static_cast<unsigned long long>(1023 - d) << shift;
-        ctl.mask |= 1023ull << shift;
-        ctl.refine = members > kClass;
-      }
-    }
-    s.sync();
-  }
-  {
-    const int bin = ctl.bin;
-    const unsigned long long pre = ctl.prefix, msk = ctl.mask;
-    s.each([&](float x, unsigned long long key) {
-      if (key < keep || (key & msk) != pre || bin_of(wt, x) != bin || wt.weight44(x) == 0) return;
-      const unsigned at = atomicAdd(&s.ls.cls_n, 1u);
-      if (at < kClass) s.ls.cls[at] = key;
-    });
-  }
-  s.sync();
-  if (s.lead) {
-    const int n = min(static_cast<int>(sm.cls_n), kClass);
-    if (n <= kRanked) {
-      // few: each thread adds up what precedes its member
-      const int i = threadIdx.x;
-      unsigned long long key = 0, w = 0;
-      if (i < n) {
-        key = sm.cls[i];
-        w = wt.weight44(key50_value(key));
-        sm.cls[kRanked + i] = w;
-      }
-      __syncthreads();
-      if (i < n) {
-        unsigned bc = c_before;
-        unsigned long long bm = m_before;
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) {
-          const bool before = sm.cls[j] > key;
-          bc += before;
-          bm += before ? sm.cls[kRanked + j] : 0ull;
-        }
-        if (by_count ? bc + 1 == target : (bm < target && target <= bm + w)) {
-          ctl.keep = key;
-          sm.picked_m = bm + w;
-        }
-      }
-    } else {
-      const int n2 = pow2_at_least(n);
-      for (int i = n + threadIdx.x; i < n2; i += kThreads) sm.cls[i] = 0;
-      __syncthreads();
-      block_sort_desc(reinterpret_cast<uint64_t*>(sm.cls), n2);
-      constexpr int kQ = kClass / kThreads;
-      unsigned long long ms[kQ], m = 0;
-      unsigned c = 0;
-#pragma unroll
-      for (int j = 0; j < kQ; ++j) {
-        const int i = threadIdx.x * kQ + j;
-        ms[j] = i < n ? wt.weight44(key50_value(sm.cls[i])) : 0ull;
-        c += i < n ? 1u : 0u;
-        m += ms[j];
-      }
-      unsigned bc = c_before - c;
-      unsigned long long bm = m_before - m;
-      block_scan(sm, c, m);
-      bc += c;
-      bm += m;
-#pragma unroll
-      for (int j = 0; j < kQ; ++j) {
-        const int i = threadIdx.x * kQ + j;
-        if (i < n && (by_count ? bc + 1 == target : (bm < target && target <= bm + ms[j]))) {
-          ctl.keep = sm.cls[i];
-          sm.picked_m = bm + ms[j];
-        }
-        bc += i < n ? 1u : 0u;
-        bm += ms[j];
-      }
-    }
-    if (threadIdx.x == 0) sm.cls_n = 0;
-    __syncthreads();
-    *upto = sm.picked_m;
-  }
-  s.sync();
-  keep = ctl.keep;
-  return refined;
-}
-
-// A request's settings for a row.
-struct Rule {
-  float tp, mp;
-  int k;
-  bool use_k, use_p;
-};
-
-// Smallest key whose weight is at least min_p: 32 probes a round over the
-// ordered logits (every warp finds the same).
-__device__ unsigned long long min_p_key(const Weights& wt, float mp) {
-  const int lane = threadIdx.x & 31;
-  const unsigned long long need = static_cast<unsigned long long>(ceil(ldexp(static_cast<double>(mp), 44)));
-  unsigned lo = 0, hi = float_order(wt.top);  // the answer lies in (lo, hi]
-  while (hi - lo > 1) {
-    const unsigned step = (hi - lo + 31) / 32;
-    const unsigned long long at = static_cast<unsigned long long>(lo) + static_cast<unsigned long long>(lane + 1) * step;
-    const bool in = at >= hi || wt.weight44(order_float(static_cast<unsigned>(at))) >= need;
-    const int f = __ffs(__ballot_sync(kFullMask, in)) - 1;  // (the last probe is at or behind hi)
-    const unsigned long long nhi = static_cast<unsigned long long>(lo) + static_cast<unsigned long long>(f + 1) * step;
-    lo += static_cast<unsigned>(f) * step;
-    hi = nhi < hi ? static_cast<unsigned>(nhi) : hi;
-  }
-  return static_cast<unsigned long long>(hi) << kIdxBits;
-}
-
-// floor(u total) for the draw, below total.
-__device__ __forceinline__ unsigned long long draw_mark(float u, unsigned long long total) {
-  unsigned long long t = 0;
-  if (u > 0.f)
-    t = u >= 1.f ? total : __umul64hi(fraction64(u), total);
-  return t < total ? t : total - 1;
-}
-
-// The row's classes: counts and masses of what is above `keep`.
-template <typename S>
-__device__ void fill_bins(const S& s, const Weights& wt, unsigned long long keep) {
-  clear_classes(s.sm);
-  __syncthreads();
-  s.each([&](float x, unsigned long long key) {
-    if (key < keep) return;
-    const unsigned long long w = wt.weight44(x);
-    if (w == 0) return;
-    const int b = bin_of(wt, x);
-    atomicAdd(&s.sm.count[b], 1u);
-    add_mass(s.sm, b, w);
-  });
-  s.sync();
-}
-
-// Count and mass over all classes (leader's block).
-template <typename S>
-__device__ void all_classes(const S& s, unsigned* count, unsigned long long* mass) {
-  constexpr int kPer = kBins / kThreads;
-  unsigned c = 0, cj;
-  unsigned long long m = 0, mj;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    s.sums(threadIdx.x * kPer + j, &cj, &mj);
-    c += cj;
-    m += mj;
-  }
-  block_scan(s.sm, c, m);
-  if (threadIdx.x == kThreads - 1) {
-    s.sm.picked_c = c;
-    s.sm.picked_m = m;
-  }
-  __syncthreads();
-  *count = s.sm.picked_c;
-  *mass = s.sm.picked_m;
-  __syncthreads();
-}
+using Source = RowSource<LIST, E, Smem>;
 
 // bf16 logits near the largest are few different values: kTable codes downward
 // from it and kTable negative ones from -1/4 (or from it, if that is lower)

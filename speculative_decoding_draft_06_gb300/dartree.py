@@ -152,6 +152,8 @@ def load():
         "dartree_sample": (st, [_vp, _i32, i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
                                 _vp, _vp]),
     })
+    sig["dartree_verify"] = (st, [_vp, _vp, _vp, _vp, _i32, i64, i64, _vp, _i32, i64, i64] + [_i32] * 4
+                             + [_vp] * 6 + [_i32] + [_vp] * 5)
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -928,3 +930,55 @@ def sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: torch.Tensor |
             logits.stride(0) if rows > 1 else max(V, logits.stride(0)), V, rows, rows_per_req, T, k,
             p, m, up, token.data_ptr(), prob.data_ptr())
     return {"token": token, "prob": prob}
+
+
+def _logit_rows(name: str, x: torch.Tensor, R: int, rows, idx: int) -> tuple:
+    """(address, is bf16, request stride, row stride, rows) of logits [R, rows,
+    V], dense in V."""
+    if x.get_device() != idx or x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} must be an fp32 or bf16 tensor on cuda:{idx}")
+    if x.dim() != 3 or x.shape[0] != R or x.shape[1] not in rows or x.shape[2] < 1:
+        raise ValueError(f"{name} {tuple(x.shape)} does not match R={R}, rows={rows}")
+    n, V = x.shape[1:]
+    if V > 1 and x.stride(2) != 1:
+        raise ValueError(f"{name} must be dense in V")
+    per = x.stride(1) if n > 1 else max(V, x.stride(1))  # (a dimension of one has no stride)
+    return x.data_ptr(), int(x.dtype is torch.bfloat16), x.stride(0) if R > 1 else 0, per, n
+
+
+def verify(parent: torch.Tensor | None, token: torch.Tensor, n_out: torch.Tensor, logits: torch.Tensor,
+           draft: torch.Tensor, u: torch.Tensor, *, max_len: int,
+           temperature: torch.Tensor | None = None, top_k: torch.Tensor | None = None,
+           top_p: torch.Tensor | None = None, min_p: torch.Tensor | None = None,
+           draft_temperature: torch.Tensor | None = None, stream=None) -> dict:
+    """Which drafted tokens the target accepts, and its own token behind them
+    (dartree_verify) -> {"len" [R], "nodes" [R, max_len], "bonus" [R], "prob" [R]},
+    the first three as :func:`accept` gives them.  parent (None: chains), token [R, B],
+    n_out [R]; the target's logits [R, B+1, V] and the drafter's, from which the
+    tokens were drawn, draft [R, B or B+1, V] (fp32 or bf16, dense in V); u [R,
+    B+1] in [0, 1): u[:, i+1] tests node i, u[:, 0] draws the last token."""
+    if not isinstance(token, torch.Tensor) or token.dim() != 2 or not token.is_cuda:
+        raise TypeError("token must be a CUDA tensor [R, B]")
+    R, B = token.shape
+    if R < 1 or B < 1 or max_len < 1:
+        raise ValueError("token and max_len must not be empty")
+    idx, dev = token.get_device(), token.device
+    par = None if parent is None else _ints("parent", parent, idx, R * B)
+    tok, n = _ints("token", token, idx, R * B), _ints("n_out", n_out, idx, R)
+    t = _logit_rows("logits", logits, R, (B + 1,), idx)
+    d = _logit_rows("draft", draft, R, (B, B + 1), idx)
+    V = logits.shape[2]
+    if draft.shape[2] != V:
+        raise ValueError(f"logits have {V} tokens, draft {draft.shape[2]}")
+    T = None if temperature is None else _floats("temperature", temperature, idx, R)
+    k = None if top_k is None else _ints("top_k", top_k, idx, R)
+    p = None if top_p is None else _floats("top_p", top_p, idx, R)
+    m = None if min_p is None else _floats("min_p", min_p, idx, R)
+    dt = None if draft_temperature is None else _floats("draft_temperature", draft_temperature, idx, R)
+    up = _floats("u", u, idx, R * (B + 1))
+    out = _alloc(stream, (R * (max_len + 3),), _I32, dev)  # (one allocation: four cost 3 us more)
+    o = {"len": out[:R], "nodes": out[3 * R:].view(R, max_len), "bonus": out[R:2 * R],
+         "prob": out[2 * R:3 * R].view(torch.float32)}
+    _launch(load().dartree_verify, idx, stream, par, tok, n, *t[:4], *d, V, R, B, T, k, p, m, dt, up, max_len,
+            *[o[x].data_ptr() for x in ("len", "nodes", "bonus", "prob")])
+    return o

@@ -89,3 +89,39 @@ def test_workspace(lib):
     assert far == lib.dartree_cache_attention_workspace(1, 0, 1 << 20, 32, 8, 128) > 0
     assert work(1, 0, 1 << 20, 1 << 30, 0, 1, 32, 8, 128) == far
     assert work(1, 0, 1 << 20, 100, 4, 1, 32, 8, 128) < far
+
+
+VERIFY = dict(parent=A, token=A, n_out=A, logits=A, bf16=0, rs=4000, ws=1000, draft=A, dbf16=1, drs=3000, dws=1000, rows=3, V=1000,
+              R=2, B=3, T=A, k=A, p=A, m=A, Td=A, u=A, max_len=4, len=A, nodes=A, bonus=A, prob=A)
+
+
+@pytest.mark.parametrize("over, status", [
+    (dict(token=None), INVALID), (dict(n_out=None), INVALID), (dict(logits=None), INVALID), (dict(draft=None), INVALID),
+    (dict(u=None), INVALID), (dict(len=None), INVALID), (dict(nodes=None), INVALID), (dict(bonus=None), INVALID),
+    (dict(prob=None), INVALID), (dict(V=0), INVALID), (dict(R=0), INVALID), (dict(B=0), INVALID), (dict(rows=0), INVALID),
+    (dict(max_len=0), INVALID), (dict(ws=999), INVALID), (dict(dws=999), INVALID), (dict(rs=-1), INVALID),
+    (dict(drs=-1), INVALID), (dict(logits=A + 2), INVALID), (dict(draft=A + 1), INVALID),
+    (dict(V=(1 << 18) + 1, ws=1 << 19, dws=1 << 19), UNSUPPORTED), (dict(B=1025), UNSUPPORTED),
+    (dict(R=(1 << 24) + 1), UNSUPPORTED)])
+def test_verify_refusals(lib, over, status):
+    assert lib.dartree_verify(*{**VERIFY, **over}.values(), None) == status
+    assert lib.dartree_last_error(None)
+
+
+def test_verification_reference():
+    """The reference's own arithmetic on a case by hand: p = (1/2, 1/2, 0), q = (1/4, 0, 3/4)."""
+    import numpy as np
+
+    from tests import verify_ref as ref
+    with np.errstate(divide="ignore"):
+        z, d = np.log([[0.5, 0.5, 0.0]] * 3), np.log([[0.25, 0.0, 0.75]] * 3)
+    par = [-1, -1]
+    # token 2: p = 0, never accepted; then max(p - q, 0) = (1/4, 1/2, 0): token 0 is left of q, with
+    # certainty, and accepted with probability 1/3
+    for u, nodes in ((0.33, [1]), (0.34, [])):
+        got = ref.verify(par, [2, 0], 2, z, d, [0.5, 0.0, u])
+        assert got[0] == nodes
+    # rejected as well: max((1/3, 2/3, 0) - (1, 0, 0), 0): token 1
+    assert got[1] == 1 and abs(got[2] - 1.0) < 1e-12
+    # token 0 first: accepted (p > q)
+    assert ref.verify(par, [0, 2], 2, z, d, [0.5, 0.99, 0.0])[0] == [0]
