@@ -21,7 +21,7 @@ SOURCES = ([("api.cu", [], "api.o"), ("select.cu", [], "select.o"),
             ("cache_attention.cu", ["-DDT_WINDOW=1"], "cache_window.o"),
             ("cache_tree.cu", ["-DDT_WINDOW=1"], "cache_window_tree.o"),
             ("cache_plan.cu", [], "cache_plan.o"),
-            ("sample.cu", [], "sample.o"), ("verify_draft.cu", [], "verify_draft.o")]
+            ("sample.cu", [], "sample.o"), *(("verify_draft.cu", [f"-DDT_E={e}", f"-DDT_F={f}"], f"verify_draft_{e}{f}.o") for e in (0, 1) for f in (0, 1))]
            + [("head_tc.cu", [f"-DDT_N={n}"], f"head_tc_{n}.o") for n in _NS]
            + [("head_simt.cu", [f"-DDT_N={n}"], f"head_simt_{n}.o") for n in _NS])
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

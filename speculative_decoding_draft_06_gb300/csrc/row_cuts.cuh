@@ -4,8 +4,9 @@
 //
 // The functions take the including kernel's shared memory as Mem: the classes
 // (mass_lo, mass_hi, count [kBins]), a class's members (cls [kClass], cls_n), the
-// scans (scan_m, scan_c [warps]), picked, picked_n, picked_c, picked_m, ctl, and
-// kThreads, the block's threads.
+// codes' counts (codes [2 kTable]), a list, the scans (scan_m, scan_c [warps]),
+// picked, picked_n, picked_c, picked_m, ctl, kThreads, the block's threads, and
+// kWideSums, whether sums over the cluster's CTAs take all their loads together.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -22,6 +23,7 @@ constexpr int kRanked = 128;         // members of a class that are ranked by co
 constexpr int kIdxBits = 18;
 constexpr float kZeroBelow = -46.f;  // 2^-46 rounds to 0 in units of 2^-44
 constexpr int kExpBits = 10;
+constexpr int kTable = 768;          // bf16 logits of a sign whose weights are tabled
 
 // 2^(j / 1024) as the sum of two floats.
 struct alignas(16) ExpTable {
@@ -114,6 +116,18 @@ struct Weights {
     const int down = 1 - (n >> 10);       // 1 .. 47
     return static_cast<unsigned long long>((w45 + (1ll << (down - 1))) >> down);
   }
+};
+
+// weight44 as a call, where it is rare or not what takes the time (its code is some
+// 70 instructions, and kernels that have it in a dozen places take minutes to
+// compile).
+static __device__ __noinline__ unsigned long long weight44_call(float x, float top, float ch, float cl,
+                                                                const float2* exp) {
+  return Weights{top, ch, cl, exp}.weight44(x);
+}
+struct CalledWeights : Weights {
+  __device__ __forceinline__ explicit CalledWeights(const Weights& w) : Weights(w) {}
+  __device__ __forceinline__ unsigned long long weight44(float x) const { return weight44_call(x, top, ch, cl, exp); }
 };
 
 // (-0 + 0 = 0: the two zeros are one logit)
@@ -307,10 +321,17 @@ struct RowSource {
   __device__ __forceinline__ void sums(int b, unsigned* c, unsigned long long* m) const {
     *c = 0;
     *m = 0;
-    for (int q = 0; q < (LIST ? 1 : cl); ++q) {
-      const Mem* o = LIST ? &sm : at_rank(&sm, q);
-      *c += o->count[b];
-      *m += (static_cast<unsigned long long>(o->mass_hi[b]) << 32) + o->mass_lo[b];
+    // (all CTAs' loads together, where the kernel has the registers: one after the
+    // other 8 CTAs' take 3 us)
+    constexpr int kAhead = !LIST && Mem::kWideSums ? 8 : 1;
+    for (int q0 = 0; q0 < (LIST ? 1 : cl); q0 += kAhead) {
+#pragma unroll
+      for (int q = q0; q < q0 + kAhead; ++q) {
+        if (q >= (LIST ? 1 : cl)) continue;
+        const Mem* o = LIST ? &sm : at_rank(&sm, q);
+        *c += o->count[b];
+        *m += (static_cast<unsigned long long>(o->mass_hi[b]) << 32) + o->mass_lo[b];
+      }
     }
   }
 };
@@ -390,8 +411,8 @@ __device__ __forceinline__ int bin_of(const Weights& wt, float x) { return bin_o
 // left in the leader's *upto.  The bins' sums are in place.  All threads of
 // the source call it.  Returns whether the bins' sums were used for digits
 // (else those before the cut's bin still hold).
-template <typename S>
-__device__ bool cut(const S& s, const Weights& wt, bool by_count, unsigned long long target,
+template <typename S, typename W>
+__device__ bool cut(const S& s, const W& wt, bool by_count, unsigned long long target,
                     unsigned long long& keep, unsigned long long* upto) {
   constexpr int kThreads = S::Mem::kThreads;
   auto& sm = s.sm;
@@ -519,7 +540,8 @@ struct Rule {
 
 // Smallest key whose weight is at least min_p: 32 probes a round over the
 // ordered logits (every warp finds the same).
-static __device__ unsigned long long min_p_key(const Weights& wt, float mp) {
+template <typename W>
+__device__ unsigned long long min_p_key(const W& wt, float mp) {
   const int lane = threadIdx.x & 31;
   const unsigned long long need = static_cast<unsigned long long>(ceil(ldexp(static_cast<double>(mp), 44)));
   unsigned lo = 0, hi = float_order(wt.top);  // the answer lies in (lo, hi]
@@ -544,8 +566,8 @@ __device__ __forceinline__ unsigned long long draw_mark(float u, unsigned long l
 }
 
 // The row's classes: counts and masses of what is above `keep`.
-template <typename S>
-__device__ void fill_bins(const S& s, const Weights& wt, unsigned long long keep) {
+template <typename S, typename W>
+__device__ void fill_bins(const S& s, const W& wt, unsigned long long keep) {
   clear_classes(s.sm);
   __syncthreads();
   s.each([&](float x, unsigned long long key) {
@@ -580,6 +602,231 @@ __device__ void all_classes(const S& s, unsigned* count, unsigned long long* mas
   *count = s.sm.picked_c;
   *mass = s.sm.picked_m;
   __syncthreads();
+}
+
+// bf16 logits near the largest are few different values: kTable codes downward
+// from it and kTable negative ones from -1/4 (or from it, if that is lower)
+// have places, in descending order.  What lies between the two and what lies
+// below them has none.
+// (Behind the last place of an extreme largest logit lies -inf: weight 0.)
+struct Codes {
+  int top, neg0;
+  __device__ __forceinline__ explicit Codes(float t) {
+    top = __float_as_int(t) >> 16;
+    neg0 = max(0x3E80, top < 0 ? top & 0x7FFF : 0);
+  }
+  // the place or -1
+  __device__ __forceinline__ int place(float x) const {
+    const int b = __float_as_int(x) >> 16;
+    const int j = b < 0 ? (b & 0x7FFF) - neg0 : top - b;
+    return static_cast<unsigned>(j) < kTable ? j + (b < 0 ? kTable : 0) : -1;
+  }
+  // x without a place: whether it lies below them all
+  __device__ __forceinline__ bool below(float x) const {
+    const int b = __float_as_int(x) >> 16;
+    return b < 0 && (b & 0x7FFF) >= neg0;
+  }
+  // whether zero has no place (its two codes would be two logits)
+  __device__ __forceinline__ bool sound() const { return top >= kTable || top < 0; }
+  __device__ __forceinline__ float value(int j) const {  // (-inf behind the last)
+    const int code = j < kTable ? max(top - j, 0) : 0x8000 | min(neg0 + j - kTable, 0x7F80);
+    return bf16_bits_to_float(static_cast<uint16_t>(code));
+  }
+  template <typename W>
+  __device__ __forceinline__ unsigned long long weight(const W& wt, int j) const {
+    const float x = value(j);
+    return x > -INFINITY && x <= wt.top ? wt.weight44(x) : 0ull;
+  }
+};
+
+// coded(x, index, place) and other(x, index) for the row's bf16 logits, in no
+// particular order, but for -inf and NaN without a place.
+template <typename S, typename F, typename G>
+__device__ __forceinline__ void each_code(const S& s, const Codes& c, F coded, G other) {
+  using E = typename S::Elem;
+  constexpr int kPer = Row<E>::kPer;
+  const int lane = threadIdx.x & 31;
+  auto one = [&](float x, int i) {
+    const int j = c.place(x);
+    if (j >= 0) coded(x, i, j);
+    else if (x > -INFINITY) other(x, i);
+  };
+  if (s.first && lane < s.row.head) one(logit<E>(s.row.src, lane), lane);
+  const int rest = s.row.index(s.row.units);
+  if (s.last && lane < s.row.V - rest) one(logit<E>(s.row.src, rest + lane), rest + lane);
+  each_unit(s.row, s.ub, s.ue, [&](uint4 v, int u) {
+    float x[kPer];
+    unpack<E>(v, x);
+    unsigned others = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int j = c.place(x[k]);
+      if (j >= 0) coded(x[k], s.row.index(u) + k, j);
+      else others |= 1u << k;
+    }
+    for (; others; others &= others - 1) {
+      const int k = __ffs(others) - 1;
+      const uint32_t pair = k < 4 ? (k < 2 ? v.x : v.y) : (k < 6 ? v.z : v.w);
+      const float y = __uint_as_float(k & 1 ? pair & 0xFFFF0000u : pair << 16);
+      if (y > -INFINITY) other(y, s.row.index(u) + k);
+    }
+  });
+}
+
+// top-k and top-p of a bf16 row by counts of its codes: they and the codes'
+// weights give the running counts and masses exactly, so a cut falls on a code
+// and a number of its ties, the first in index order.  Left for the cluster: the
+// code's place ctl.bin (-1: nothing is cut), its ties that are kept ctl.left, all
+// of them ctl.last, and the kept mass ctl.total.  False where a cut falls on a
+// logit without a place.  The leader's list is used (4 numbers per warp).
+// kLeast: tokens below `least` are out (min-p's).
+template <bool kLeast = false, typename S, typename W>
+__device__ __forceinline__ bool code_cut(const S& s, const W& wt, const Rule& rule, const Codes& code,
+                                         float least = -INFINITY) {
+  auto& sm = s.sm;
+  Ctl& ctl = s.ls.ctl;
+  constexpr int kThreads = S::Mem::kThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warps = s.cl * (kThreads / 32);
+  constexpr int kN = 2 * kTable + 2, kPer = (kN + kThreads - 1) / kThreads;
+  for (int j = tid; j < 2 * kTable; j += kThreads) sm.codes[j] = 0;
+  __syncthreads();
+  unsigned between = 0, below = 0;
+  unsigned long long between_m = 0, below_m = 0;
+  auto other = [&](float x, int) {
+    const unsigned long long w = wt.weight44(x);
+    const bool low = code.below(x);
+    between += !low;
+    below += low;
+    between_m += low ? 0ull : w;
+    below_m += low ? w : 0ull;
+  };
+  each_code(s, code,
+            [&](float x, int, int j) {
+              if (!kLeast || x >= least) atomicAdd(&sm.codes[j], 1u);
+            },
+            [&](float x, int i) {
+              if (!kLeast || x >= least) other(x, i);
+            });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    between += __shfl_xor_sync(kFullMask, between, o);
+    below += __shfl_xor_sync(kFullMask, below, o);
+    between_m += __shfl_xor_sync(kFullMask, between_m, o);
+    below_m += __shfl_xor_sync(kFullMask, below_m, o);
+  }
+  if (lane == 0) {  // (the list is not in use)
+    unsigned long long* to = &s.ls.list[4 * s.gw];
+    to[0] = between;
+    to[1] = between_m;
+    to[2] = below;
+    to[3] = below_m;
+  }
+  s.sync();
+  if (s.lead) {
+    // entries in order: the positive codes, what lies between, the negative
+    // codes, what lies below
+    unsigned cs[kPer], c = 0;
+    unsigned long long ms[kPer], m = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) cs[q] = 0;
+    // (what lies between and below: warp v adds up the warps' v-th number)
+    if constexpr (S::Mem::kWideSums) {
+      const int v = tid >> 5;
+      if (v < 4) {
+        unsigned long long x = 0;
+        for (int w = lane; w < warps; w += 32) x += sm.list[4 * w + v];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFullMask, x, o);
+        if (lane == 0) sm.list[4 * warps + v] = x;
+      }
+    }
+    constexpr int kAhead = S::Mem::kWideSums ? 8 : 1;
+    for (int r0 = 0; r0 < s.cl; r0 += kAhead) {
+#pragma unroll
+      for (int r = r0; r < r0 + kAhead; ++r) {
+        if (r >= s.cl) continue;
+        const unsigned* from = at_rank(&sm, r)->codes;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+          const int e = tid * kPer + q;
+          if (e < kN - 1 && e != kTable) cs[q] += from[e < kTable ? e : e - 1];
+        }
+      }
+    }
+    if constexpr (S::Mem::kWideSums) __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int e = tid * kPer + q;
+      ms[q] = 0;
+      if (e == kTable || e == kN - 1) {
+        const int v = e == kN - 1 ? 2 : 0;
+        if constexpr (S::Mem::kWideSums) {
+          cs[q] = static_cast<unsigned>(sm.list[4 * warps + v]);
+          ms[q] = sm.list[4 * warps + v + 1];
+        } else {
+#pragma unroll 8
+          for (int w = 0; w < warps; ++w) {
+            cs[q] += static_cast<unsigned>(sm.list[4 * w + v]);
+            ms[q] += sm.list[4 * w + v + 1];
+          }
+        }
+      } else if (cs[q]) {
+        ms[q] = cs[q] * code.weight(wt, e < kTable ? e : e - 1);
+      }
+      c += cs[q];
+      m += ms[q];
+    }
+    unsigned c0 = 0u - c;
+    unsigned long long m0 = 0ull - m;
+    block_scan(sm, c, m);
+    c0 += c;
+    m0 += m;  // what lies before the thread's entries
+    if (tid == kThreads - 1) {
+      sm.picked = -1;
+      sm.picked_c = c;
+      sm.picked_m = m;
+    }
+    __syncthreads();
+    unsigned long long Z = sm.picked_m;
+    bool ok = true;
+    // the entry that a cut falls on, and how many of its tokens are kept
+    auto fall = [&](bool by_count, unsigned long long target) {
+      unsigned bc = c0;
+      unsigned long long bm = m0;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        if (by_count ? (bc < target && target <= bc + cs[q]) : (bm < target && target <= bm + ms[q])) {
+          const int e = tid * kPer + q;
+          const unsigned long long w = max(ms[q] / cs[q], 1ull);
+          const unsigned n = by_count ? static_cast<unsigned>(target - bc)
+                                      : static_cast<unsigned>((target - bm + w - 1) / w);
+          sm.picked = e == kTable || e == kN - 1 ? -2 : e < kTable ? e : e - 1;
+          sm.picked_n = n;
+          sm.picked_c = cs[q];
+          sm.picked_m = ms[q] ? bm + n * w : bm;  // (an entry without a place: not used)
+        }
+        bc += cs[q];
+        bm += ms[q];
+      }
+      __syncthreads();
+      if (sm.picked == -2) ok = false;
+      Z = sm.picked_m;
+      __syncthreads();
+    };
+    const unsigned all = sm.picked_c;
+    __syncthreads();
+    if (rule.use_k && all > static_cast<unsigned>(rule.k)) fall(true, static_cast<unsigned long long>(rule.k));
+    if (rule.use_p && ok && Z > 0) fall(false, rule.tp > 0.f ? ceil_share(rule.tp, Z) : 1ull);
+    if (tid == 0) {
+      ctl.bin = sm.picked;
+      ctl.left = sm.picked < 0 ? 0 : sm.picked_n;
+      ctl.last = static_cast<int>(sm.picked_c);
+      ctl.total = Z;
+      ctl.refine = ok ? 0 : 1;
+    }
+  }
+  s.sync();
+  return ctl.refine == 0;
 }
 
 }  // namespace dt

@@ -47,7 +47,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr float kMassUnit = 16000.f; // 2^18 2^(1/40) units fit 32 bits
-constexpr int kTable = 768;          // bf16 logits of a sign whose weights are tabled
 constexpr int kList = 2944;          // candidates
 constexpr float kWant = 1800.f;      // candidates aimed at
 constexpr int kUnits = 4096;         // 16-byte units of a CTA that may hold candidates
@@ -71,6 +70,7 @@ struct Part {            // a CTA's share of the pass, for the leader
 
 struct Smem {
   static constexpr int kThreads = kWarps * 32;
+  static constexpr bool kWideSums = false;
   __align__(16) float2 exp[1 << kExpBits];
   union {
     struct {
@@ -102,74 +102,6 @@ struct Smem {
 template <bool LIST, typename E>
 using Source = RowSource<LIST, E, Smem>;
 
-// bf16 logits near the largest are few different values: kTable codes downward
-// from it and kTable negative ones from -1/4 (or from it, if that is lower)
-// have places, in descending order.  What lies between the two and what lies
-// below them has none.
-// (Behind the last place of an extreme largest logit lies -inf: weight 0.)
-struct Codes {
-  int top, neg0;
-  __device__ __forceinline__ explicit Codes(float t) {
-    top = __float_as_int(t) >> 16;
-    neg0 = max(0x3E80, top < 0 ? top & 0x7FFF : 0);
-  }
-  // the place or -1
-  __device__ __forceinline__ int place(float x) const {
-    const int b = __float_as_int(x) >> 16;
-    const int j = b < 0 ? (b & 0x7FFF) - neg0 : top - b;
-    return static_cast<unsigned>(j) < kTable ? j + (b < 0 ? kTable : 0) : -1;
-  }
-  // x without a place: whether it lies below them all
-  __device__ __forceinline__ bool below(float x) const {
-    const int b = __float_as_int(x) >> 16;
-    return b < 0 && (b & 0x7FFF) >= neg0;
-  }
-  // whether zero has no place (its two codes would be two logits)
-  __device__ __forceinline__ bool sound() const { return top >= kTable || top < 0; }
-  __device__ __forceinline__ float value(int j) const {  // (-inf behind the last)
-    const int code = j < kTable ? max(top - j, 0) : 0x8000 | min(neg0 + j - kTable, 0x7F80);
-    return bf16_bits_to_float(static_cast<uint16_t>(code));
-  }
-  __device__ __forceinline__ unsigned long long weight(const Weights& wt, int j) const {
-    const float x = value(j);
-    return x > -INFINITY && x <= wt.top ? wt.weight44(x) : 0ull;
-  }
-};
-
-// coded(x, index, place) and other(x, index) for the row's bf16 logits, in no
-// particular order, but for -inf and NaN without a place.
-template <typename S, typename F, typename G>
-__device__ __forceinline__ void each_code(const S& s, const Codes& c, F coded, G other) {
-  using E = typename S::Elem;
-  constexpr int kPer = Row<E>::kPer;
-  const int lane = threadIdx.x & 31;
-  auto one = [&](float x, int i) {
-    const int j = c.place(x);
-    if (j >= 0) coded(x, i, j);
-    else if (x > -INFINITY) other(x, i);
-  };
-  if (s.first && lane < s.row.head) one(logit<E>(s.row.src, lane), lane);
-  const int rest = s.row.index(s.row.units);
-  if (s.last && lane < s.row.V - rest) one(logit<E>(s.row.src, rest + lane), rest + lane);
-  each_unit(s.row, s.ub, s.ue, [&](uint4 v, int u) {
-    float x[kPer];
-    unpack<E>(v, x);
-    unsigned others = 0;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int j = c.place(x[k]);
-      if (j >= 0) coded(x[k], s.row.index(u) + k, j);
-      else others |= 1u << k;
-    }
-    for (; others; others &= others - 1) {
-      const int k = __ffs(others) - 1;
-      const uint32_t pair = k < 4 ? (k < 2 ? v.x : v.y) : (k < 6 ? v.z : v.w);
-      const float y = __uint_as_float(k & 1 ? pair & 0xFFFF0000u : pair << 16);
-      if (y > -INFINITY) other(y, s.row.index(u) + k);
-    }
-  });
-}
-
 // f(logit, index, weight) for the row's logits that have a weight (and some
 // without), in no particular order; the classes' memory is used.  The weights of the codes that have
 // places come from a table (weight44 is some 70 instructions: 2064 rows of
@@ -200,120 +132,10 @@ __device__ bool code_cuts(const S& s, const Weights& wt, const Rule& rule, float
   Smem& sm = s.sm;
   Ctl& ctl = s.ls.ctl;
   const int tid = threadIdx.x, lane = tid & 31, warps = s.cl * kWarps;
-  constexpr int kN = 2 * kTable + 2, kPer = (kN + kThreads - 1) / kThreads;
   const Codes code(wt.top);
   if (!code.sound()) return false;
-  float v = -INFINITY;
-  {
-    for (int j = tid; j < 2 * kTable; j += kThreads) sm.codes[j] = 0;
-    __syncthreads();
-    unsigned between = 0, below = 0;
-    unsigned long long between_m = 0, below_m = 0;
-    each_code(s, code, [&](float, int, int j) { atomicAdd(&sm.codes[j], 1u); },
-              [&](float x, int) {
-                const unsigned long long w = wt.weight44(x);
-                const bool low = code.below(x);
-                between += !low;
-                below += low;
-                between_m += low ? 0ull : w;
-                below_m += low ? w : 0ull;
-              });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      between += __shfl_xor_sync(kFullMask, between, o);
-      below += __shfl_xor_sync(kFullMask, below, o);
-      between_m += __shfl_xor_sync(kFullMask, between_m, o);
-      below_m += __shfl_xor_sync(kFullMask, below_m, o);
-    }
-    if (lane == 0) {  // (the list is not in use)
-      unsigned long long* to = &s.ls.list[4 * s.gw];
-      to[0] = between;
-      to[1] = between_m;
-      to[2] = below;
-      to[3] = below_m;
-    }
-    s.sync();
-    if (s.lead) {
-      // entries in order: the positive codes, what lies between, the negative
-      // codes, what lies below
-      unsigned cs[kPer], c = 0;
-      unsigned long long ms[kPer], m = 0;
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) cs[q] = 0;
-      for (int r = 0; r < s.cl; ++r) {
-        const unsigned* from = at_rank(&sm, r)->codes;
-#pragma unroll
-        for (int q = 0; q < kPer; ++q) {
-          const int e = tid * kPer + q;
-          if (e < kN - 1 && e != kTable) cs[q] += from[e < kTable ? e : e - 1];
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) {
-        const int e = tid * kPer + q;
-        ms[q] = 0;
-        if (e == kTable || e == kN - 1) {
-#pragma unroll 8
-          for (int w = 0; w < warps; ++w) {
-            cs[q] += static_cast<unsigned>(sm.list[4 * w + (e == kN - 1 ? 2 : 0)]);
-            ms[q] += sm.list[4 * w + (e == kN - 1 ? 3 : 1)];
-          }
-        } else if (cs[q]) {
-          ms[q] = cs[q] * code.weight(wt, e < kTable ? e : e - 1);
-        }
-        c += cs[q];
-        m += ms[q];
-      }
-      unsigned c0 = 0u - c;
-      unsigned long long m0 = 0ull - m;
-      block_scan(sm, c, m);
-      c0 += c;
-      m0 += m;  // what lies before the thread's entries
-      if (tid == kThreads - 1) {
-        sm.picked = -1;
-        sm.picked_c = c;
-        sm.picked_m = m;
-      }
-      __syncthreads();
-      unsigned long long Z = sm.picked_m;
-      bool ok = true;
-      // the entry that a cut falls on, and how many of its tokens are kept
-      auto fall = [&](bool by_count, unsigned long long target) {
-        unsigned bc = c0;
-        unsigned long long bm = m0;
-#pragma unroll
-        for (int q = 0; q < kPer; ++q) {
-          if (by_count ? (bc < target && target <= bc + cs[q]) : (bm < target && target <= bm + ms[q])) {
-            const int e = tid * kPer + q;
-            const unsigned long long w = max(ms[q] / cs[q], 1ull);
-            const unsigned n = by_count ? static_cast<unsigned>(target - bc)
-                                        : static_cast<unsigned>((target - bm + w - 1) / w);
-            sm.picked = e == kTable || e == kN - 1 ? -2 : e < kTable ? e : e - 1;
-            sm.picked_n = n;
-            sm.picked_m = ms[q] ? bm + n * w : bm;  // (an entry without a place: not used)
-          }
-          bc += cs[q];
-          bm += ms[q];
-        }
-        __syncthreads();
-        if (sm.picked == -2) ok = false;
-        Z = sm.picked_m;
-        __syncthreads();
-      };
-      const unsigned all = sm.picked_c;
-      __syncthreads();
-      if (rule.use_k && all > static_cast<unsigned>(rule.k)) fall(true, static_cast<unsigned long long>(rule.k));
-      if (rule.use_p && ok && Z > 0) fall(false, rule.tp > 0.f ? ceil_share(rule.tp, Z) : 1ull);
-      if (tid == 0) {
-        ctl.bin = sm.picked;
-        ctl.left = sm.picked < 0 ? 0 : sm.picked_n;
-        ctl.refine = ok ? 0 : 1;
-      }
-    }
-    s.sync();
-    if (ctl.refine) return false;
-    if (ctl.bin >= 0) v = code.value(ctl.bin);
-  }
+  if (!code_cut(s, wt, rule, code)) return false;
+  const float v = ctl.bin >= 0 ? code.value(ctl.bin) : -INFINITY;
   // the weights of what is above the cut's code, and its ties
   for (int j = tid; j < 2 * kTable; j += kThreads) sm.weight[j] = code.value(j) > v ? code.weight(wt, j) : 0ull;
   __syncthreads();

@@ -174,6 +174,21 @@ def test_tokens_that_cannot_have_been_drawn():
     assert (lens[6::8] > 0).all()
 
 
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16)])
+@pytest.mark.parametrize("rules", [dict(k=500), dict(k=40, p=0.9), dict(p=0.6), dict(p=0.97, mp=0.01), dict(k=1024, mp=0.001),
+                                   dict(k=3000, p=0.9)])
+def test_cuts_among_ties(types, rules):
+    """Few different logits: a cut falls on one that thousands of tokens share, of
+    which the first are kept; rows over several CTAs."""
+    g = np.random.default_rng(13)
+    R, B, V = 3, 5, 40000
+    par, tok, n, z, d = problem(g, R, B, V, 2, 4)
+    z = (np.round(z / 2) * 2).astype(np.float32)
+    n[:] = B
+    u = g.random((R, B + 1)).astype(np.float32)
+    check(par, tok, n, z, d, u, types=types, **{k: np.full(R, v) for k, v in rules.items()})
+
+
 def test_infinite_logits():
     g = np.random.default_rng(6)
     R, B, V = 24, 6, 300
