@@ -142,15 +142,21 @@ __global__ void __launch_bounds__(kPlanThreads) k_cache_plan(const PlanParams p)
       const int beg = (p.sinks >> p.log_page) + ((p.sinks & (P - 1)) != 0);
       const int end = min(p.max_pages, f >= p.window ? (f - p.window + 1) >> p.log_page : 0);
       int32_t* row = p.table + static_cast<size_t>(r) * p.max_pages;
-      for (int b = beg + part * 128; b < end; b += per * 128) {
-        int page[4];
+      // (most are gone already: what takes the time is to look, all loads together)
+      constexpr int kLooks = 8;
+      for (int b = beg + part * 32 * kLooks; b < end; b += per * 32 * kLooks) {
+        int page[kLooks];
+        bool some = false;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kLooks; ++k) {
           const int j = b + 32 * k + lane;
           page[k] = j < end ? row[j] : -1;
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kLooks; ++k) some |= page[k] != -1;
+        if (!some) continue;
+#pragma unroll
+        for (int k = 0; k < kLooks; ++k) {
           if (page[k] == -1) continue;
           row[b + 32 * k + lane] = -1;
           bool bad = page[k] < 0 || page[k] >= p.pages;

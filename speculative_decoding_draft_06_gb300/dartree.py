@@ -842,25 +842,32 @@ class KVCache:
         return ok
 
     def plan(self, table, lens, count, *, max_tokens: int, offset: int = -1,
-             window: int | None = None, sinks: int = 0, stream=None) -> dict:
+             window: int | None = None, sinks: int = 0, out: dict | None = None, stream=None) -> dict:
         """Pages for count[r] packed tokens per row from position lens[r] +
         ``offset`` on, and their maps (dartree_cache_plan) -> {"ok" [R], "start"
-        [R+1], "row", "pos", "slot" [max_tokens]} int32.  With ``window``, pages that
-        it has left behind (but for the first ``sinks`` tokens') are let go."""
+        [R+1], "row", "pos", "slot" [max_tokens]} int32 (``out``: an earlier call's, to
+        be written again).  With ``window``, pages that it has left behind (but for
+        the first ``sinks`` tokens') are let go."""
         t, width, ln, R = self._seqs(table, lens)
         if max_tokens < 0 or (window is not None and window < 1):
             raise ValueError("max_tokens must not be negative, window at least 1")
         c = _ints("count", count, self._idx, R)
-        # (one allocation: five cost 4 us more)
-        pad = -(-max_tokens // 4) * 4
-        sizes = (R, R + 1, max_tokens, max_tokens, max_tokens)
-        at = [0, -(-R // 4) * 4]
-        at += [at[1] + -(-(R + 1) // 4) * 4 + k * pad for k in range(3)]
-        buf = _alloc(stream, (at[4] + max(pad, 4),), _I32, self.dev)
-        base = buf.data_ptr()
+        T = max_tokens
+        if out is None:  # (an allocation each: views of one cost 4 to 7 us more)
+            if stream is None:
+                ok, start = torch.empty(R, dtype=_I32, device=self.dev), torch.empty(R + 1, dtype=_I32, device=self.dev)
+                row, pos, slot = (torch.empty(T, dtype=_I32, device=self.dev), torch.empty(T, dtype=_I32, device=self.dev),
+                                  torch.empty(T, dtype=_I32, device=self.dev))
+            else:
+                ok, start, row, pos, slot = (_alloc(stream, (n,), _I32, self.dev) for n in (R, R + 1, T, T, T))
+            out = {"ok": ok, "start": start, "row": row, "pos": pos, "slot": slot}
+            at = ok.data_ptr(), start.data_ptr(), row.data_ptr(), pos.data_ptr(), slot.data_ptr()
+        else:
+            at = [_ints(k, out[k], self._idx, n)
+                  for k, n in (("ok", R), ("start", R + 1), ("row", T), ("pos", T), ("slot", T))]
         _launch(self._lib.dartree_cache_plan, self._idx, stream, self._ref, t, width, ln, c, R, offset,
-                window or 0, sinks, max_tokens, *[base + 4 * a for a in at], self._err)
-        return {k: buf[a:a + n] for k, a, n in zip(("ok", "start", "row", "pos", "slot"), at, sizes)}
+                window or 0, sinks, T, *at, self._err)
+        return out
 
     def fork(self, table, lens, src, dst, *, pending: int = 0, stream=None) -> torch.Tensor:
         """Rows dst become copies of rows src -> ok [n] int32
@@ -976,9 +983,8 @@ def verify(parent: torch.Tensor | None, token: torch.Tensor, n_out: torch.Tensor
     m = None if min_p is None else _floats("min_p", min_p, idx, R)
     dt = None if draft_temperature is None else _floats("draft_temperature", draft_temperature, idx, R)
     up = _floats("u", u, idx, R * (B + 1))
-    out = _alloc(stream, (R * (max_len + 3),), _I32, dev)  # (one allocation: four cost 3 us more)
-    o = {"len": out[:R], "nodes": out[3 * R:].view(R, max_len), "bonus": out[R:2 * R],
-         "prob": out[2 * R:3 * R].view(torch.float32)}
+    o = {"len": _alloc(stream, (R,), _I32, dev), "nodes": _alloc(stream, (R, max_len), _I32, dev),
+         "bonus": _alloc(stream, (R,), _I32, dev), "prob": _alloc(stream, (R,), torch.float32, dev)}
     _launch(load().dartree_verify, idx, stream, par, tok, n, *t[:4], *d, V, R, B, T, k, p, m, dt, up, max_len,
             *[o[x].data_ptr() for x in ("len", "nodes", "bonus", "prob")])
     return o

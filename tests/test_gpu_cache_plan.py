@@ -126,7 +126,9 @@ def test_plan(case):
     cache.err.zero_()
     # once more: the same maps, nothing taken (rows that were refused for pages may fare better or not, so only then)
     if (want[0] == 1).all():
-        again = cache.plan(t, ln, cu(count), max_tokens=T, offset=offset, window=window, sinks=sinks)
+        reused = {k: torch.full_like(v, 99) for k, v in out.items()}
+        again = cache.plan(t, ln, cu(count), max_tokens=T, offset=offset, window=window, sinks=sinks, out=reused)
+        assert again is reused
         assert all(np.array_equal(host(again[k]), host(out[k])) for k in out)
         assert np.array_equal(host(t), want_table) and np.array_equal(host(cache.refs), want_refs)
 
@@ -200,6 +202,8 @@ def test_refusals():
             cache.plan(t, ln, n, **k)
     with pytest.raises(ValueError):
         cache.plan(t, ln, cu([1]), max_tokens=4)
+    with pytest.raises(ValueError):
+        cache.plan(t, ln, n, max_tokens=4, out=cache.plan(t, ln, cu([0, 0]), max_tokens=5))
     x = torch.zeros(5, 2, 64, dtype=torch.bfloat16, device="cuda")
     s = cu([0, 1, 2, 3, 4])
     for K, V, sl in ((x.float(), x, s), (x, x.cpu(), s), (x[:, :1], x[:, :1], s), (x, x[:4], s), (x, x, s[:4]), (x, x, s.long()),
