@@ -249,7 +249,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   pdl_wait();
   pdl_trigger();  // (the launch of the rows left over may fill the SMs that come free)
   __shared__ int s_r;
-  if (p.R > 1 && p.R <= kTreeSorted) {  // the z-th longest request
+  // (where a request's CTAs are a wave of their own the order does not matter)
+  const bool sorted = p.R > 1 && p.R <= kTreeSorted && gridDim.x * gridDim.y < 152;
+  if (sorted) {  // the z-th longest request
     for (int a = threadIdx.x; a < p.R; a += kTreeThreads) {
       const int len = p.lens[a];
       int before = 0;
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     }
     __syncthreads();
   }
-  const int r = p.R > 1 && p.R <= kTreeSorted ? s_r : blockIdx.z;
+  const int r = sorted ? s_r : blockIdx.z;
   Span sp;
   if (kWin && threadIdx.x == 0 && split == 0 && hk == 0 && mt == 0 && span_flag<kWin>(p, r))
     atomicOr(p.err, DT_ERR_BAD_INDEX);
@@ -295,10 +297,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     }
     if (lane == 0) *abort_flag = 0;
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  // (the roles come to this barrier with their first loads on their way: 2000
+  // cycles of a CTA's 15000 before its first scores)
+  uint32_t tmem_base = 0;
+  auto ready = [&]() {
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    tmem_base = *tmem_slot;
+  };
+  // a row's node, and its query head in the group (a row is less than 256 behind
+  // q0: the quotient is exact in fp32)
+  const int node0 = q0 / p.g, rem0 = q0 - node0 * p.g;
+  const float inv_g = 1.f / static_cast<float>(p.g);
+  auto node_of = [&](int row, int* head) {
+    const int t = rem0 + row, n = static_cast<int>((static_cast<float>(t) + 0.5f) * inv_g);
+    *head = t - n * p.g;
+    return node0 + n;
+  };
 
   // a bounded wait of the whole warp; false: give up (another warp has, or
   // the time is over)
@@ -325,13 +341,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     uint4 w[kIts];
 #pragma unroll
     for (int j = 0; j < kIts; ++j) {
-      const int row = first + j * kRowsIt, q = q0 + row, node = row < rows ? q / p.g : 0;
+      const int row = first + j * kRowsIt;
       w[j] = make_uint4(0, 0, 0, 0);
-      if (row < rows)
-        w[j] = __ldg(reinterpret_cast<const uint4*>(
-                         p.Q + cache_row<kWin>(p, sp, r, node) * p.q_stride +
-                         static_cast<size_t>(hk * p.g + (q - node * p.g)) * DH) + k);
+      if (row < rows) {
+        int head;
+        const int node = node_of(row, &head);
+        w[j] = __ldg(reinterpret_cast<const uint4*>(p.Q + cache_row<kWin>(p, sp, r, node) * p.q_stride +
+                                                    static_cast<size_t>(hk * p.g + head) * DH) + k);
+      }
     }
+    ready();
     uint8_t* dst = smem + (warp / kLoadWarps) * L::kQTile + (k >> 3) * (kMRows * 128);
 #pragma unroll
     for (int j = 0; j < kIts; ++j) {
@@ -355,6 +374,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     fence_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&q_full[warp / kLoadWarps]);
+  } else if (warp < kExpandWarp0 || warp >= kMmaWarp0) {
+    ready();
   }
 
   if (warp >= kExpandWarp0 && warp < kMmaWarp0) {
@@ -417,6 +438,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
 #pragma unroll
     for (int it = 0; it < kIt; ++it) load(0, page, it);
     int raw = look_up(1);
+    ready();
     uint64_t* full = kv ? v_full : k_full;
     uint64_t* empty = kv ? v_empty : k_empty;
     bool go = true;
@@ -517,12 +539,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   } else if (warp < kExpandWarp0 && (warp >> 3) * kMRows + (warp & 3) * 32 < rows) {
     // ------------------------------------------------------------- softmax
     const int i = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
-    const int row = i * kMRows + quarter * 32 + lane, q = q0 + row;
+    const int row = i * kMRows + quarter * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_addr = tmem_base + lane_base + static_cast<uint32_t>(i * kKeys);
     const uint32_t o_addr = tmem_base + lane_base + kColO + static_cast<uint32_t>(i * 128 + half * (DH / 2));
     const int pair = 1 + i * 4 + quarter;  // the barrier of the two warps that share rows
-    const int node = row < rows ? q / p.g : 0;
+    int row_head = 0;
+    const int node = row < rows ? node_of(row, &row_head) : 0;
     const uint32_t* mrow = node >= 1 && !(kWin && p.chain) ? p.mask + (static_cast<size_t>(r) * p.B + node - 1) * p.words : nullptr;
     int at = 0;  // (window) the row's position
     if constexpr (kWin) at = row_position(p, sp, r, node);
@@ -660,9 +683,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
       const int rr = i * kMRows + quarter * 32 + lane / kLanes + j * (32 / kLanes);
       const int d = half * (DH / 2) + (lane % kLanes) * 4;
       to[j] = nullptr;
-      if (rr < rows)
+      if (rr < rows) {
+        int h;
+        const int nd = node_of(rr, &h);
         to[j] = p.n_split > 1 ? reinterpret_cast<uint8_t*>(cache_part_row(p, r, hk, mt, split, rr) + kPartHead + d)
-                              : reinterpret_cast<uint8_t*>(p.O + cache_out_row<kWin>(p, sp, r, hk, q0 + rr) + d);
+                              : reinterpret_cast<uint8_t*>(
+                                    p.O + (cache_row<kWin>(p, sp, r, nd) * p.Hq + hk * p.g + h) * DH + d);
+      }
     }
 #pragma unroll 1
     for (int ch = 0; ch < 4; ++ch) {
