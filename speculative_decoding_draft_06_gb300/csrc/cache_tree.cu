@@ -27,14 +27,19 @@
 //
 // Bound by the latency of a step's chain (scores, maximum, weights, product)
 // at two row tiles per SM: 32 trees of 65 rows over up to 2500 tokens, 32 heads
-// over 8 of 128: 73 us (76 in a graph), 730 TFLOP/s, the tensor pipe active 37% of the time,
+// over 8 of 128: 68 us, 780 TFLOP/s, the tensor pipe active 37% of the time,
 // issue 0.62 (the exponentials and the conversions of the codes alone would
 // take 29 us); one of 129 rows over 4099 tokens: 28 us.  Steps for the 32 (the
 // one): one row tile 181 us (41); two, and codes expanded from registers 121
 // (53); scores a step of 64 keys ahead and two issuers 85 (47); leftover rows in
 // a launch beside 89 (43); two threads per row 83 (35); queries loaded by the
 // softmax warps beside the first codes, output addresses out of the loop 77
-// (31).  A polynomial for part of the exponentials and row tiles that take
+// (31); first loads ahead of the set-up barrier 70, whole rows staged as bf16 68.
+// With a window a row tile begins at the first tile that one of its rows sees,
+// and only tiles that reach past the end of a range or the start of a window
+// compare positions: prompts of 2 x 4096 tokens behind a window of 2048 540 us, 890
+// TFLOP/s of the pairs that are seen, 190 us behind a window of 1 (the CTAs' fixed
+// cost: 30 thousand cycles each).  A polynomial for part of the exponentials and row tiles that take
 // turns were slower (no figures kept).
 #include <type_traits>
 
@@ -669,57 +674,81 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     if (half == 0 && p.n_split > 1 && row < rows)
       *reinterpret_cast<float2*>(cache_part_row(p, r, hk, mt, split, row)) = make_float2(have ? ref * s_fac[row] : -INFINITY, l);
     // O by way of the row tile's queries' place in shared memory (the scores
-    // are done), an eighth of the dims at a time, so that a warp's accesses are
-    // whole pieces of rows: kC dims of a row by kC / 4 lanes
-    constexpr int kC = DH / 8, kPitch = kC + 4, kLanes = kC / 4;
-    float* stage = reinterpret_cast<float*>(smem + i * L::kQTile) + (warp & 7) * 32 * kPitch;
-    static_assert(8 * 32 * kPitch * 4 <= L::kQTile, "the staged rows fit");
-    const float mul = p.n_split > 1 ? 1.f : inv;
-    // the lane's pieces of rows k = lane / kLanes, + 32 / kLanes, ..: where they
-    // go, a chunk's step on (looked up once: in the loop 3000 cycles)
-    uint8_t* to[kLanes];
+    // are done), so that a warp's accesses are whole pieces of rows: as bf16, 32
+    // dims at a time, four lanes a row; a pair of rows' pieces is turned by
+    // the pair's number, which keeps both accesses free of conflicts
+    uint8_t* const place = smem + i * L::kQTile;
+    if (p.n_split == 1) {
+      constexpr int kPieces = 4;
+      static_assert(8 * 32 * kPieces * 16 <= L::kQTile, "the staged rows fit");
+      uint4* stage = reinterpret_cast<uint4*>(place) + (warp & 7) * 32 * kPieces;
+      uint16_t* to[4];
 #pragma unroll
-    for (int j = 0; j < kLanes; ++j) {
-      const int rr = i * kMRows + quarter * 32 + lane / kLanes + j * (32 / kLanes);
-      const int d = half * (DH / 2) + (lane % kLanes) * 4;
-      to[j] = nullptr;
-      if (rr < rows) {
-        int h;
-        const int nd = node_of(rr, &h);
-        to[j] = p.n_split > 1 ? reinterpret_cast<uint8_t*>(cache_part_row(p, r, hk, mt, split, rr) + kPartHead + d)
-                              : reinterpret_cast<uint8_t*>(
-                                    p.O + (cache_row<kWin>(p, sp, r, nd) * p.Hq + hk * p.g + h) * DH + d);
-      }
-    }
-#pragma unroll 1
-    for (int ch = 0; ch < 4; ++ch) {
-      float x[kC];
-      if (have) {
-        if constexpr (kC == 16) tmem_ld16(o_addr + ch * kC, x);
-        else tmem_ld8(o_addr + ch * kC, x);
-      } else {
-#pragma unroll
-        for (int k = 0; k < kC; ++k) x[k] = 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < kC; k += 4)
-        *reinterpret_cast<float4*>(stage + lane * kPitch + k) =
-            make_float4(x[k] * mul, x[k + 1] * mul, x[k + 2] * mul, x[k + 3] * mul);
-      __syncwarp();
-#pragma unroll
-      for (int j = 0; j < kLanes; ++j) {
-        const float4 v = *reinterpret_cast<const float4*>(stage + (lane / kLanes + j * (32 / kLanes)) * kPitch +
-                                                          (lane % kLanes) * 4);
-        if (!to[j]) continue;
-        if (p.n_split > 1) {
-          *reinterpret_cast<float4*>(to[j]) = v;
-          to[j] += kC * 4;
-        } else {
-          *reinterpret_cast<uint2*>(to[j]) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-          to[j] += kC * 2;
+      for (int j = 0; j < 4; ++j) {
+        const int rr = i * kMRows + quarter * 32 + lane / kPieces + j * 8;
+        to[j] = nullptr;
+        if (rr < rows) {
+          int h;
+          const int nd = node_of(rr, &h);
+          to[j] = p.O + (cache_row<kWin>(p, sp, r, nd) * p.Hq + hk * p.g + h) * DH + half * (DH / 2) + (lane % kPieces) * 8;
         }
       }
-      __syncwarp();
+#pragma unroll 1
+      for (int ch = 0; ch < DH / 64; ++ch) {
+        uint32_t x[32];
+        if (have) {
+          tmem_ld32(o_addr + ch * 32, x);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[k] = 0u;
+        }
+        auto two = [&](int k) { return pack_bf16(__uint_as_float(x[k]) * inv, __uint_as_float(x[k + 1]) * inv); };
+#pragma unroll
+        for (int k = 0; k < 32; k += 8)
+          stage[lane * kPieces + (k / 8 ^ (lane >> 1 & 3))] = make_uint4(two(k), two(k + 2), two(k + 4), two(k + 6));
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = lane / kPieces + j * 8;
+          const uint4 v = stage[row * kPieces + (lane % kPieces ^ (row >> 1 & 3))];
+          if (to[j]) *reinterpret_cast<uint4*>(to[j] + ch * 32) = v;
+        }
+        __syncwarp();
+      }
+    } else {
+      // a share in fp32: an eighth of the dims at a time, kC dims of a row by kC / 4 lanes
+      constexpr int kC = DH / 8, kPitch = kC + 4, kLanes = kC / 4;
+      float* stage = reinterpret_cast<float*>(place) + (warp & 7) * 32 * kPitch;
+      static_assert(8 * 32 * kPitch * 4 <= L::kQTile, "the staged rows fit");
+      float* to[kLanes];
+#pragma unroll
+      for (int j = 0; j < kLanes; ++j) {
+        const int rr = i * kMRows + quarter * 32 + lane / kLanes + j * (32 / kLanes);
+        const int d = half * (DH / 2) + (lane % kLanes) * 4;
+        to[j] = rr < rows ? cache_part_row(p, r, hk, mt, split, rr) + kPartHead + d : nullptr;
+      }
+#pragma unroll 1
+      for (int ch = 0; ch < 4; ++ch) {
+        float x[kC];
+        if (have) {
+          if constexpr (kC == 16) tmem_ld16(o_addr + ch * kC, x);
+          else tmem_ld8(o_addr + ch * kC, x);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kC; ++k) x[k] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kC; k += 4)
+          *reinterpret_cast<float4*>(stage + lane * kPitch + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kLanes; ++j) {
+          const float4 v = *reinterpret_cast<const float4*>(stage + (lane / kLanes + j * (32 / kLanes)) * kPitch +
+                                                            (lane % kLanes) * 4);
+          if (to[j]) *reinterpret_cast<float4*>(to[j] + ch * kC) = v;
+        }
+        __syncwarp();
+      }
     }
   }
   if (!kWin && threadIdx.x == kMmaWarp0 * 32 && split == 0 && hk == 0 && mt == 0 &&
