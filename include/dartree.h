@@ -568,7 +568,8 @@ size_t dartree_cache_attention_workspace(int32_t R, int32_t B, int32_t max_len, 
  * rows: within the root's window); others may have been let go.  Arithmetic,
  * alignment, work, zero_rest, err and rows without a visible token are those of
  * dartree_cache_attention_ex.  A request with lens[r] < 0 or lens[r] + offset <
- * -1 is skipped (at -1 row 0 stands before the first token), and one whose rows lie outside [0, q_rows) is, too, and flagged.
+ * -1 is skipped (at -1 row 0 stands before the first token), and one whose rows
+ * lie outside [0, q_rows) is, too, and flagged.
  * work: dartree_cache_window_attention_workspace() bytes (chain: whether mask is
  * NULL). */
 dartree_status dartree_cache_window_attention(

@@ -514,6 +514,7 @@ def accept(parent, token, n_out, pred, *, max_len: int, stream=None) -> dict:
 # ------------------------------------------------------- paged 4-bit cache
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _I32 = torch.int32
+_TOP = 1 << 31
 
 
 def _ints(name: str, t: torch.Tensor, idx: int, n: int) -> int:
@@ -748,6 +749,16 @@ class KVCache:
                 new, out.data_ptr(), wp, wb, self._err)
         return out
 
+    @staticmethod
+    def _window(window, sinks, offset) -> tuple:
+        """window (0: none) and sinks as the calls take them: no position passes
+        2^31 - 2, so larger ones are as good as that."""
+        if window is not None and window < 1:
+            raise ValueError("window must be at least 1")
+        if sinks < 0 or not -_TOP <= offset < _TOP:
+            raise ValueError("sinks must not be negative, offset fit 32 bits")
+        return 0 if window is None else min(window, _TOP - 1), min(sinks, _TOP - 1)
+
     def window_attention(self, layer: int, Q: torch.Tensor, table, lens, *, max_len: int,
                          window: int | None = None, sinks: int = 0, offset: int = -1,
                          mask: torch.Tensor | None = None, n_nodes: torch.Tensor | None = None,
@@ -783,8 +794,9 @@ class KVCache:
             total, B = R * Q.shape[1], Q.shape[1] - 1
         if Hq < 1 or Hq % self.Hkv:
             raise ValueError(f"{Hq} query heads are not a multiple of {self.Hkv}")
-        if window is not None and window < 1:
-            raise ValueError("window must be at least 1")
+        w, sinks = self._window(window, sinks, offset)
+        if not 0 <= max_len < _TOP or B >= _TOP:
+            raise ValueError("max_len and max_rows must fit 31 bits")
         sq = Hq * dh
         if not Q.is_contiguous():
             *lead, sh, sd = Q.stride()
@@ -809,7 +821,6 @@ class KVCache:
             raise TypeError(f"out must be a contiguous bf16 tensor on {self.dev}")
         elif out.shape != Q.shape:
             raise ValueError(f"out has shape {tuple(out.shape)}")
-        w = 0 if window is None else window
         key = (R, B, max_len, w, sinks, m is None, Hq)
         need = self._work_bytes.get(key)
         if need is None:
@@ -849,8 +860,9 @@ class KVCache:
         be written again).  With ``window``, pages that it has left behind (but for
         the first ``sinks`` tokens') are let go."""
         t, width, ln, R = self._seqs(table, lens)
-        if max_tokens < 0 or (window is not None and window < 1):
-            raise ValueError("max_tokens must not be negative, window at least 1")
+        w, sinks = self._window(window, sinks, offset)
+        if not 0 <= max_tokens < _TOP:
+            raise ValueError("max_tokens must not be negative, and fit 31 bits")
         c = _ints("count", count, self._idx, R)
         T = max_tokens
         if out is None:  # (an allocation each: views of one cost 4 to 7 us more)
@@ -866,7 +878,7 @@ class KVCache:
             at = [_ints(k, out[k], self._idx, n)
                   for k, n in (("ok", R), ("start", R + 1), ("row", T), ("pos", T), ("slot", T))]
         _launch(self._lib.dartree_cache_plan, self._idx, stream, self._ref, t, width, ln, c, R, offset,
-                window or 0, sinks, T, *at, self._err)
+                w, sinks, T, *at, self._err)
         return out
 
     def fork(self, table, lens, src, dst, *, pending: int = 0, stream=None) -> torch.Tensor:
