@@ -227,11 +227,11 @@ __device__ __forceinline__ void warp_stats(float& m, float& s, float& m2, float&
 }
 
 // The largest of a unit's logits (NaN counts as nothing).
-__device__ __forceinline__ float unit_max(uint4 v, float) {
+[[maybe_unused]] __device__ __forceinline__ float unit_max(uint4 v, float) {
   return fmaxf(fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w))),
                -INFINITY);
 }
-__device__ __forceinline__ float unit_max(uint4 v, uint16_t) {
+[[maybe_unused]] __device__ __forceinline__ float unit_max(uint4 v, uint16_t) {
   const auto pair = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
   const __nv_bfloat162 m = __hmax2(__hmax2(pair(v.x), pair(v.y)), __hmax2(pair(v.z), pair(v.w)));
   return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
@@ -589,6 +589,83 @@ __device__ __noinline__ bool class_cut(const S& src, const Weights& wp, const Ru
   return ctl.done != 0;
 }
 
+// A bit per token of a bf16 unit whose logit is both halves of v, in index order.
+[[maybe_unused]] __device__ __forceinline__ unsigned tie_bits(uint4 u, __nv_bfloat162 v) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  unsigned bits = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const unsigned m = __heq2_mask(*reinterpret_cast<const __nv_bfloat162*>(&w[k]), v);
+    bits |= (m & (1u << 2 * k)) | (m >> 16 & (2u << 2 * k));
+  }
+  return bits;
+}
+
+// The key of the want-th token, in index order, whose bf16 logit is v (not zero): the
+// warps' numbers of them, then the warp in whose share it lies.  Written to ctl.keep;
+// a barrier of the cluster has to follow.
+template <typename S>
+__device__ __noinline__ void nth_tie(const S& src, float v, unsigned want) {
+  auto& sm = src.sm;
+  const auto& row = src.row;
+  const int lane = threadIdx.x & 31, rest = row.index(row.units);
+  const unsigned before_lane = (1u << lane) - 1u;
+  const __nv_bfloat162 vv = __float2bfloat162_rn(v);
+  const bool head = src.first && lane < row.head && logit<uint16_t>(row.src, lane) == v;
+  const bool tail = src.last && lane < row.V - rest && logit<uint16_t>(row.src, rest + lane) == v;
+  const unsigned heads = __ballot_sync(kFullMask, head), tails = __ballot_sync(kFullMask, tail);
+  constexpr int kAhead = 4;
+  unsigned mine = 0;
+#pragma unroll 1
+  for (int a = src.ub + lane; a < src.ue; a += 32 * kAhead) {
+    uint4 u[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (a + 32 * k < src.ue) u[k] = row.load(a + 32 * k);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (a + 32 * k < src.ue) mine += __popc(tie_bits(u[k], vv));
+  }
+  mine = __reduce_add_sync(kFullMask, mine) + __popc(heads) + __popc(tails);
+  if (lane < src.cl) at_rank(&sm, lane)->list[src.gw] = mine;
+  cluster_sync();
+  unsigned before = 0;
+  for (int w = lane; w < src.gw; w += 32) before += static_cast<unsigned>(sm.list[w]);
+  before = __reduce_add_sync(kFullMask, before);
+  if (want <= before || want > before + mine) return;
+  unsigned left = want - before;  // of the warp's own
+  auto emit = [&](int i) { src.ls.ctl.keep = key50(v, i); };
+  if (left <= static_cast<unsigned>(__popc(heads))) {
+    if (head && __popc(heads & before_lane) == left - 1) emit(lane);
+    return;
+  }
+  left -= __popc(heads);
+  auto load = [&](int q) { return q < src.ue ? row.load(q) : make_uint4(0, 0, 0, 0); };
+  uint4 next = load(src.ub + lane);
+#pragma unroll 1
+  for (int b = src.ub + lane; b - lane < src.ue; b += 32) {
+    unsigned bits = b < src.ue ? tie_bits(next, vv) : 0u;
+    next = load(b + 32);
+    const unsigned n = __popc(bits);
+    unsigned upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned x = __shfl_up_sync(kFullMask, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const unsigned all = __shfl_sync(kFullMask, upto, 31);
+    if (left <= all) {
+      if (upto - n < left && left <= upto) {
+        for (unsigned k = left - (upto - n); k > 1; --k) bits &= bits - 1;
+        emit(row.index(b) + __ffs(bits) - 1);
+      }
+      return;
+    }
+    left -= all;
+  }
+  if (tail && __popc(tails & before_lane) == left - 1) emit(rest + lane);
+}
+
 // The cuts of a row -> the key that the kept tokens reach (0: all are), their mass
 // in *mass (0: not known).  sum: the row's sum in fp32; half: which slots have the
 // warps' largest logits.
@@ -629,8 +706,8 @@ __device__ __noinline__ unsigned long long cut_row(const S& src, const Weights& 
         const float v = code.value(bin);
         keep = static_cast<unsigned long long>(float_order(v + 0.f)) << kIdxBits;
         if (want < ties) {  // the first of them in index order
-          done = ties <= Mem::kListMost;
-          if (done) {
+          // (few: by a list, a barrier less, 3 to 5 us at 150 thousand tokens)
+          if (ties <= kFew) {
             FloorSource<E, Mem>(src, v).each_value([&](float x, int i) {
               if (x == v) ls.list[atomicAdd(&ls.list_n, 1u)] = key50(x, i);
             });
@@ -645,9 +722,11 @@ __device__ __noinline__ unsigned long long cut_row(const S& src, const Weights& 
               }
               if (tid == 0) sm.list_n = 0;
             }
-            cluster_sync();
-            keep = ls.ctl.keep;
+          } else {
+            nth_tie(src, v, want);
           }
+          cluster_sync();
+          keep = ls.ctl.keep;
         }
       }
     }

@@ -189,6 +189,24 @@ def test_cuts_among_ties(types, rules):
     check(par, tok, n, z, d, u, types=types, **{k: np.full(R, v) for k, v in rules.items()})
 
 
+@pytest.mark.parametrize("V, first", [(5003, 300), (5003, 5), (40007, 301), (40001, 7)])
+def test_cut_within_one_logit(V, first):
+    """All tokens but a few share a logit, and top-k keeps the first of them: from
+    one to all but one, in rows that begin and end at odd places.  u close to 1
+    draws the last one kept."""
+    R = 8
+    g = np.random.default_rng(V + first)
+    z = np.full((R, 2, V), 6.5, np.float32)
+    for r in range(R):
+        z[r][:, g.permutation(V)[:first] if r % 2 else np.arange(first)] = 7.0
+    d = np.zeros_like(z)
+    k = first + np.array([1, 2, 700, V // 3, V // 2, V - first - 9, V - first - 2, V - first - 1])
+    u = np.full((R, 2), 1 - 2.0 ** -24, np.float32)
+    for types in ((BF16, BF16), (F32, BF16)):
+        out = check(np.full((R, 1), -1), np.zeros((R, 1)), np.zeros(R, int), z, d, u, types=types, k=k)
+        assert (host(out["bonus"])[::2] == k[::2] - 1).all()
+
+
 def test_infinite_logits():
     g = np.random.default_rng(6)
     R, B, V = 24, 6, 300
