@@ -1524,9 +1524,16 @@ extern "C" dartree_status dartree_verify(const int32_t* parent, const int32_t* t
   const uintptr_t odd = (reinterpret_cast<uintptr_t>(logits) & (bf16 ? 1 : 3)) |
                         (reinterpret_cast<uintptr_t>(draft) & (draft_bf16 ? 1 : 3));
   if (odd) return cache_fail(DARTREE_ERR_INVALID_ARG, "logits and draft must be aligned to their type");
-  // a request's rows over as many CTAs as the SMs hold at once
+  // A request's rows over several CTAs.  15 clusters of 8, 36 of 4 and 76 of 2 find
+  // room at once; paths differ in length, so a few more than that still gain (those
+  // that wait start long before the longest ends).  Chains of 7 over 151936 bf16
+  // logits without cuts (with settings of their own), us: 16 of them by 8 CTAs 106
+  // (149), by 4 113 (176); 24 147 (209), 113 (186); 40 by 4 156 (204), by 2 177 (277);
+  // 64 205 (283), 176 (322); 100 by 2 248 (335), by 1 291 (529); 150 342 (472), 306
+  // (623).
+  const int most = R <= 16 ? kMaxCl : R <= 40 ? 4 : R <= 152 ? 2 : 1;
   int cl = 1;
-  while (cl < kMaxCl && static_cast<long long>(R) * cl * 2 <= 152 && V / cl > 4096) cl *= 2;
+  while (cl < most && V / cl > 4096) cl *= 2;
   const VerifyParams p{parent, token, n_out, logits, draft, req_stride, row_stride, draft_req_stride, draft_row_stride,
                        V, R, B, draft_rows, temperature, top_k, top_p, min_p, draft_temperature, u,
                        max_len, accept_len, accept_nodes, bonus, prob};
