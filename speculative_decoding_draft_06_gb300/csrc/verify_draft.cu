@@ -26,10 +26,10 @@
 // Bound by latency: a path's nodes wait for one another, and each is a chain of
 // passes, barriers of the cluster and scalar steps, 5 us at the least; the pass in
 // whole numbers by issue and by its table's bank conflicts (two look-ups a token).
-// One chain of 8 over 32000 fp32 logits 47 us (5 nodes); 16 trees of 128 nodes over
-// 151936 in bf16 140 us, 64 chains of 7 with settings of their own 365 us (both to
-// the end of their longest paths; the rows of all paths read once would take 10 and
-// 20 us).  Steps for the trees (the chains): every sum in whole numbers 210 us (837);
+// One chain of 8 over 32000 fp32 logits 36 to 56 us (by its path); 16 trees of 128 nodes
+// over 151936 in bf16 137 to 157 us, 64 chains of 7 with settings of their own 300 to
+// 390 us (both to the end of their longest paths; the rows of all paths read once would
+// take 10 and 20 us).  Steps for the trees (the chains): every sum in whole numbers 210 us (837);
 // tests in fp32, one pass in whole numbers per path, its fp64 in one warp 147 (440,
 // top-p); floors and lists for top-k, the pass at the draw in line 137 (385);
 // acceptance before the cut 140 (318).  The passes as calls cost 7%, two CTAs of 512
