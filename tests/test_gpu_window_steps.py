@@ -187,3 +187,73 @@ def test_numbers_past_32_bits():
         with pytest.raises(ValueError):
             plan(**a)
     cache.check()
+
+
+def test_fork_of_a_row_behind_its_window():
+    """A row whose window has left pages behind is forked: both see the same, and
+    what they held goes back."""
+    Hq, Hkv, dh, P, window, sinks, L = 4, 2, 64, 16, 30, 0, 133
+    g = np.random.default_rng(21)
+    cache = dtl.KVCache(1, 30, page_tokens=P, Hkv=Hkv, dh=dh)
+    table, lens = cu(np.full((2, 12), -1)), cu([0, 0])
+    K, V = (torch.from_numpy(g.standard_normal((L, Hkv, dh))).to(torch.bfloat16) for _ in range(2))
+    for a, n in ((0, 120), (120, L - 120)):
+        out = cache.plan(table, lens, cu([n, 0]), max_tokens=n, offset=0, window=window, sinks=sinks)
+        cache.append_slots(0, K[a:a + n].cuda(), V[a:a + n].cuda(), out["slot"])
+        lens[0] += n
+    assert (table[0, :5] == -1).all() and (table[0, 6:9] >= 0).all()
+    assert host(cache.fork(table, lens, cu([0]), cu([1]))).tolist() == [1]
+    q = torch.from_numpy(g.standard_normal((1, 1, Hq, dh))).to(torch.bfloat16)
+    O = host(cache.window_attention(0, q.expand(2, -1, -1, -1).contiguous().cuda(), table, lens, max_len=L, window=window).double())
+    k, v = (ref.values(*ref.quantise(x.double().numpy())) for x in (K, V))
+    for r in range(2):
+        check_request(O[r], q[0].double().numpy(), k, v, visible(L - 1, 1, window, sinks), dh ** -0.5)
+    cache.release(table, lens, cu([0, 1]), cu([0, 0]))
+    cache.check()
+    assert not host(cache.refs).any() and (host(table) == -1).all()
+
+
+def test_far_pages_and_rows():
+    """Pages and query rows that lie more than 2^32 bytes apart."""
+    Hq, Hkv, dh, P, pages, window, L, n = 8, 8, 128, 128, 30000, 200, 300, 40
+    g = np.random.default_rng(22)
+    cache = dtl.KVCache(1, pages, page_tokens=P, Hkv=Hkv, dh=dh)
+    assert pages * cache.page_bytes > 1 << 32
+    cache.refs[:pages - 4] = 1
+    table, lens = cu(np.full((1, 5), -1)), cu([0])
+    K, V = (torch.from_numpy(g.standard_normal((L, Hkv, dh))).to(torch.bfloat16) for _ in range(2))
+    out = cache.plan(table, lens, cu([L]), max_tokens=L, offset=0)
+    assert host(table).tolist() == [[pages - 4, pages - 3, pages - 2, -1, -1]]
+    cache.append_slots(0, K.cuda(), V.cuda(), out["slot"])
+    step = 1 << 26                                          # elements between rows: 40 of them pass 2^32 bytes
+    q = torch.from_numpy(g.standard_normal((n, Hq, dh))).to(torch.bfloat16)
+    far = torch.empty(n * step, dtype=torch.bfloat16, device="cuda").as_strided((n, Hq, dh), (step, dh, 1))
+    far.copy_(q)
+    k, v = (ref.values(*ref.quantise(x.double().numpy())) for x in (K, V))
+    for rows in (n, 3):                                     # the tensor cores' kernel, the few rows'
+        O = host(cache.window_attention(0, far[n - rows:], table, cu([L - rows]), start=cu([0, rows]), max_rows=rows, max_len=L,
+                                        window=window, offset=0).double())
+        check_request(O, q[n - rows:].double().numpy(), k, v, visible(L - rows, rows, window, 0), dh ** -0.5)
+    cache.check()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_far_logits(dtype):
+    """Requests' and nodes' logits that lie more than 2^32 bytes apart."""
+    g = np.random.default_rng(23)
+    R, B, V, row, req = 2, 3, 700, 1 << 29, (1 << 31) + (1 << 20)
+    z = torch.from_numpy(g.standard_normal((R, B + 1, V)) * 2).to(dtype)
+    d = torch.from_numpy(z.float().numpy() + g.standard_normal(z.shape) * 0.2).to(dtype)
+    far = torch.empty(req + B * row + V, dtype=dtype, device="cuda").as_strided((R, B + 1, V), (req, row, 1))
+    near = torch.empty(R, B + 1, V, dtype=dtype, device="cuda")
+    u = f32(g.random((R, B + 1)) * 0.2)
+    tok = cu([draw_tokens(g, np.arange(B) - 1, np.zeros(B, int), d[r].float().numpy(), 1.0) for r in range(R)])
+    got = []
+    for logits, draft in ((far, near), (near, far)):
+        logits.copy_(z)
+        draft.copy_(d)
+        got.append(dtl.verify(None, tok, cu([B] * R), logits, draft, u, max_len=B, top_p=f32([0.99] * R)))
+    want = dtl.verify(None, tok, cu([B] * R), z.cuda(), d.cuda(), u, max_len=B, top_p=f32([0.99] * R))
+    assert host(want["len"]).sum() > 0
+    for x in got:
+        assert all(np.array_equal(host(x[k]), host(want[k])) for k in want)
