@@ -778,20 +778,23 @@ class KVCache:
         idx, dh = self._idx, self.dh
         if Q.dtype not in _BF16 or Q.get_device() != idx:
             raise TypeError(f"Q must be a bf16 tensor on {self.dev}")
-        packed = start is not None
-        if Q.dim() != (3 if packed else 4) or Q.shape[-1] != dh or Q.shape[0] < 1:
-            raise ValueError(f"Q {tuple(Q.shape)} is not {'[T' if packed else '[R, B+1'}, Hq, {dh}]")
-        Hq = Q.shape[-2]
-        if packed:
+        shape = Q.shape
+        if start is None:
+            if len(shape) != 4:
+                raise ValueError(f"Q {tuple(shape)} is not [R, B+1, Hq, {dh}]")
+            r, rows, Hq, d = shape
+            if r != R or rows < 1 or d != dh:
+                raise ValueError(f"Q {tuple(shape)} does not match R={R}, dh={dh}")
+            total, B, s = R * rows, rows - 1, None
+        else:
             if max_rows is None or max_rows < 1:
                 raise ValueError("packed rows need max_rows")
             if n_nodes is not None:
                 raise ValueError("packed rows have their numbers in start")
-            total, B = Q.shape[0], max_rows - 1
-        else:
-            if Q.shape[0] != R or Q.shape[1] < 1:
-                raise ValueError(f"Q {tuple(Q.shape)} does not match R={R}")
-            total, B = R * Q.shape[1], Q.shape[1] - 1
+            if len(shape) != 3 or shape[0] < 1 or shape[2] != dh:
+                raise ValueError(f"Q {tuple(shape)} is not [T, Hq, {dh}]")
+            total, Hq, d = shape
+            rows, B, s = total, max_rows - 1, _ints("start", start, idx, R + 1)
         if Hq < 1 or Hq % self.Hkv:
             raise ValueError(f"{Hq} query heads are not a multiple of {self.Hkv}")
         w, sinks = self._window(window, sinks, offset)
@@ -800,12 +803,11 @@ class KVCache:
         sq = Hq * dh
         if not Q.is_contiguous():
             *lead, sh, sd = Q.stride()
-            if packed or R == 1 or B == 0:  # (a dimension of one has no stride)
-                n = Q.shape[0] if packed or B == 0 else Q.shape[1]
-                sq = (lead[0] if packed or B == 0 else lead[1]) if n > 1 else sq
+            if s is None and rows == 1:  # (a dimension of one has no stride)
+                sq = lead[0] if R > 1 else sq
             else:
-                sq = lead[1]
-                if lead[0] != (B + 1) * sq:
+                sq = lead[-1] if rows > 1 else sq
+                if s is None and R > 1 and lead[0] != rows * sq:
                     raise ValueError("Q needs one stride between rows")
             if (sh != dh and Hq > 1) or sd != 1:
                 raise ValueError("Q must be dense in heads and dims")
@@ -813,13 +815,12 @@ class KVCache:
         if mask is not None and B > 0:
             m = _ints("mask", mask, idx, R * B * ((B + 31) // 32))
         nn = None if n_nodes is None else _ints("n_nodes", n_nodes, idx, R)
-        s = None if start is None else _ints("start", start, idx, R + 1)
         new = out is None
         if new:
-            out = _alloc(stream, Q.shape, torch.bfloat16, self.dev)
+            out = _alloc(stream, shape, torch.bfloat16, self.dev)
         elif out.dtype not in _BF16 or out.get_device() != idx or not out.is_contiguous():
             raise TypeError(f"out must be a contiguous bf16 tensor on {self.dev}")
-        elif out.shape != Q.shape:
+        elif out.shape != shape:
             raise ValueError(f"out has shape {tuple(out.shape)}")
         key = (R, B, max_len, w, sinks, m is None, Hq)
         need = self._work_bytes.get(key)
