@@ -30,12 +30,14 @@
 // transposed within the warp (movmatrix).
 //
 // Bound by memory where there are many keys: 64 single tokens over 1 to 16001
-// tokens, 32 heads over 8 of 128: 144 us, 5.1 TB/s, 77% of a copy's rate; one
+// tokens, 32 heads over 8 of 128: 139 us, 5.3 TB/s, 79% of a copy's rate; one
 // over 131072 tokens 36 us, 4.2 TB/s (the join and the ramp: a warp has 9
-// tiles); over 1000 tokens 6.9 us, latency.  Steps:
+// tiles); over 1000 tokens 6.4 us, latency.  Behind a window of 4096 the 64 take 76
+// us (4.0 TB/s), behind one of 512 the single one 7.2.  Steps:
 // a producer warp and rows as the 16-row operand 315 us for the 64; warps with
 // rings of their own and keys as that operand 246; four code bytes to a
-// conversion 198; stages of 64 keys and no scaling in front 145.
+// conversion 198; stages of 64 keys and no scaling in front 145; no divisions ahead of
+// the first loads 139 (the single one 6.7 to 6.4).
 #include <cstdlib>
 
 #include "cache_attn.cuh"
@@ -43,7 +45,7 @@
 namespace dt {
 namespace {
 
-constexpr int kTileKeys = 64;   // keys of a stage
+constexpr int kLogTileKeys = 6, kTileKeys = 1 << kLogTileKeys;  // keys of a stage
 constexpr int kStep = 32;       // keys between two looks at the maximum
 constexpr int kStages = 2;
 constexpr int kMaxCluster = 8;  // splits that join in a cluster's shared memory
@@ -126,9 +128,9 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
   // piece: min(page, 64) tokens; segments: key codes, key scales, values', or
   // all of a 64-token page at once)
   const int P = 1 << p.c.log_page;
-  const int piece = P < kTileKeys ? P : kTileKeys;
-  const int pieces = kTileKeys / piece, segs = P == kTileKeys ? 1 : 4;
-  const int pc = lane / segs, seg = lane % segs;
+  const int log_piece = min(p.c.log_page, kLogTileKeys), piece = 1 << log_piece;
+  const int pieces = kTileKeys >> log_piece, log_segs = P == kTileKeys ? 0 : 2, segs = 1 << log_segs;
+  const int pc = lane >> log_segs, seg = lane & (segs - 1);
   const bool copies = pc < pieces;
   const int32_t* trow = p.table + static_cast<size_t>(r) * p.max_pages;
   const int unit = (seg & 1) ? DH / 16 : DH / 2;  // bytes of a token in the segment
@@ -159,7 +161,7 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
       const int left = sp.L - key0;
       if (left < kTileKeys) v &= (1ull << left) - 1ull;
       sm.valid[warp][st] = v;
-      mbar_arrive_expect_tx(&sm.full[warp][st], static_cast<uint32_t>(__popc(got) / segs * piece * (DH / 8 * 9)));
+      mbar_arrive_expect_tx(&sm.full[warp][st], static_cast<uint32_t>((__popc(got) >> log_segs << log_piece) * (DH / 8 * 9)));
     }
     __syncwarp();
     if (page >= 0) {
@@ -184,7 +186,7 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const bool on = 8 * n + rr < live;
-    const int q = on ? q0 + 8 * n + rr : 0, nd = q / p.g;
+    const int q = on ? q0 + 8 * n + rr : 0, nd = row_node(p, sp, q);
     uint32_t w[DH / 8];
     const uint4* src = reinterpret_cast<const uint4*>(
         p.Q + cache_row<kWin>(p, sp, r, nd) * p.q_stride +
@@ -244,8 +246,9 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
   // and among the sinks or from `all_beg` on
   int all_end = sp.Lp, all_beg = 0;
   if constexpr (kWin) {
-    if (p.chain) all_end = sp.base + q0 / p.g + 1;
-    all_beg = sp.base + (p.chain ? (q0 + max(live, 1) - 1) / p.g : sp.n) - p.window + 1;
+    // (these rows are a request's last)
+    if (p.chain) all_end = sp.base + row_node(p, sp, q0) + 1;
+    all_beg = sp.base + sp.n - p.window + 1;
   }
   auto seen_whole = [&](int key0) {
     if constexpr (!kWin) return key0 + kTileKeys <= sp.Lp;
@@ -469,6 +472,9 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
         *reinterpret_cast<float4*>(dst + 2 * j) =
             make_float4(o[n][j][x], o[n][j][x + 2], o[n][j + 1][x], o[n][j + 1][x + 2]);
     }
+  // (a cluster's rows and splits are few: their quotients are exact so)
+  const float inv_split = __fdividef(1.f, static_cast<float>(p.n_split));
+  const int each = static_cast<int>((static_cast<float>(kRows + p.n_split - 1) + 0.5f) * inv_split);
   if (p.cluster) cluster_sync();  // (every CTA's stages are free: the rows may be sent)
   else __syncthreads();
   // ---- the four warps' shares of each row, joined in warp order
@@ -492,7 +498,8 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
     }
     if (p.cluster) {
       // row i is the (i / n)-th that CTA i % n joins
-      const int owner = row % p.n_split, at = split * ((kRows + p.n_split - 1) / p.n_split) + row / p.n_split;
+      const int turn = static_cast<int>((static_cast<float>(row) + 0.5f) * inv_split);
+      const int owner = row - turn * p.n_split, at = split * each + turn;
       float* dst = at_rank(&sm.recv[at][0], owner);
 #pragma unroll
       for (int e = 0; e < kE; ++e) dst[lane * kE + e] = v[e];
@@ -513,9 +520,8 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
   if (!p.cluster) return;
   cluster_sync();
   // ---- the rows this CTA joins, in split order
-  const int each = (kRows + p.n_split - 1) / p.n_split;
   for (int row = split + warp * p.n_split; row < min(live, kRows); row += kWarps * p.n_split) {
-    const int at = row / p.n_split;
+    const int at = static_cast<int>((static_cast<float>(row) + 0.5f) * inv_split);
     float M = -INFINITY, L = 0.f;
     for (int k = 0; k < p.n_split; ++k) M = fmaxf(M, sm.recv_ml[k * each + at].x);
     constexpr int kE = DH / 32;

@@ -108,12 +108,20 @@ __device__ __forceinline__ int tail_rows(const CacheAttnParams& p, int rows) {
   return rows > kTreeTile && odd <= kTreeTail ? odd : 0;
 }
 
+// The node of query row q of a request.  (Divisions by what is known at the launch only
+// take 150 cycles each, one after the other ahead of a single token's first loads:
+// none where a request has one row.)
+__device__ __forceinline__ int row_node(const CacheAttnParams& p, const Span& s, int q) { return s.n == 0 ? 0 : q / p.g; }
+
+// n keys in whole tiles (a power of two).
+__device__ __forceinline__ int whole_tiles(const CacheAttnParams& p, int keys) { return keys >> (31 - __clz(p.tile_keys)); }
+
 // Key tiles that the rows of row tile mt can see: the prefix
 // and the nodes up to the tile's last row's.
 __device__ __forceinline__ int row_tile_keys(const CacheAttnParams& p, const Span& s, int mt) {
-  const int last = p.tail ? s.n : min(s.n, (mt * p.tile_rows + p.tile_rows - 1) / p.g);
+  const int last = p.tail ? s.n : min(s.n, row_node(p, s, mt * p.tile_rows + p.tile_rows - 1));
   const int keys = min(s.L, s.Lp + last);
-  return (keys + p.tile_keys - 1) / p.tile_keys;
+  return whole_tiles(p, keys + p.tile_keys - 1);
 }
 
 // The same as a list: n tiles, the t-th is tile at(t).  With a window those
@@ -138,10 +146,10 @@ __device__ __forceinline__ KeyTiles<kWin> row_key_tiles(const CacheAttnParams& p
   KeyTiles<kWin> t;
   t.n = row_tile_keys(p, s, mt);
   if constexpr (kWin) {
-    const int first = p.chain ? first_row / p.g : 0;
+    const int first = p.chain ? row_node(p, s, first_row) : 0;
     t.lo = max(0, s.base + first - p.window + 1);
-    t.sinks = min(t.n, (min(p.sinks, s.L) + p.tile_keys - 1) / p.tile_keys);
-    t.gap = max(0, min(t.n, t.lo / p.tile_keys) - t.sinks);
+    t.sinks = min(t.n, whole_tiles(p, min(p.sinks, s.L) + p.tile_keys - 1));
+    t.gap = max(0, min(t.n, whole_tiles(p, t.lo)) - t.sinks);
     t.n -= t.gap;
   }
   return t;
@@ -253,7 +261,7 @@ __device__ __forceinline__ size_t cache_row(const CacheAttnParams& p, const Span
 // Row q of a key/value head in the output (node q / g, query head hk g + q % g).
 template <bool kWin>
 __device__ __forceinline__ size_t cache_out_row(const CacheAttnParams& p, const Span& s, int r, int hk, int q) {
-  const int nd = q / p.g;
+  const int nd = row_node(p, s, q);
   return (cache_row<kWin>(p, s, r, nd) * p.Hq + hk * p.g + (q - nd * p.g)) * p.c.dh;
 }
 
