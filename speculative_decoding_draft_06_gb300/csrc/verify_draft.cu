@@ -761,8 +761,9 @@ __device__ __noinline__ unsigned long long cut_row(const S& src, const Weights& 
   return keep;
 }
 
-// A node's rows and what the cluster's threads know of them.  The passes over both
-// rows are calls: the kernel has them in many places.
+// A node's rows and what the cluster's threads know of them.  The seldom steps are
+// calls, with a copy of it: an object whose address a call is given lies in memory, and
+// 512 threads' of them do not stay in L1.
 template <typename E, typename F>
 struct Node {
   VerifySmem& sm;
@@ -898,7 +899,13 @@ struct Node {
   }
 
   // The kept tokens' sum.
-  __device__ __noinline__ float near_kept() { return near_pass(0.f); }
+  __device__ __forceinline__ float near_kept() {
+    Node n = *this;
+    const float sum = kept_call(&n);
+    par = n.par;
+    return sum;
+  }
+  static __device__ __noinline__ float kept_call(Node* n) { return n->near_pass(0.f); }
 
   template <int kMost>
   __device__ __forceinline__ void sum_up(const float (&lc)[kLevels], Sums& t) {
@@ -1044,18 +1051,34 @@ struct Node {
     exact = true;
   }
 
-  // sm.ex behind all rejected children (a call: seldom before the draw).
-  __device__ __noinline__ void settle() {
-    bool totals = !exact && tried == 0;
-    begin_exact();
-    for (int done = sm.ex.settled; done < tried || totals; done = sm.ex.settled) {
-      exact_pass(tried - done > 1 ? kLevels : 1, done);
+  // sm.ex behind all rejected children (seldom before the draw).
+  __device__ __forceinline__ void settle() {
+    Node n = *this;
+    settle_call(&n);
+    par = n.par;
+    total_p = n.total_p;
+    total_q = n.total_q;
+    tables = n.tables;
+    exact = n.exact;
+  }
+  static __device__ __noinline__ void settle_call(Node* n) {
+    bool totals = !n->exact && n->tried == 0;
+    n->begin_exact();
+    for (int done = n->sm.ex.settled; done < n->tried || totals; done = n->sm.ex.settled) {
+      n->exact_pass(n->tried - done > 1 ? kLevels : 1, done);
       totals = false;
     }
   }
 
   // A test in whole numbers: child `tried`'s logits, p's only if it is kept.
-  __device__ __noinline__ void exact_test(float xp, float xq, bool in, float u) {
+  __device__ __forceinline__ void exact_test(float xp, float xq, bool in, float u) const {
+    const Node n = *this;
+    test_call(&n, xp, xq, in, u);
+  }
+  static __device__ __noinline__ void test_call(const Node* n, float xp, float xq, bool in, float u) {
+    n->test(xp, xq, in, u);
+  }
+  __device__ __forceinline__ void test(float xp, float xq, bool in, float u) const {
     __syncthreads();  // (the test before has been read)
     if (threadIdx.x < 32) {
       const double np = static_cast<double>(total_p), nq = static_cast<double>(total_q), z = sm.ex.Z;
@@ -1075,7 +1098,7 @@ struct Node {
 };
 
 template <typename E, typename F>
-__global__ void __launch_bounds__(kThr) k_verify(const VerifyParams p) {
+__global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
   using Mem = VerifySmem;
   constexpr int kWarps = Mem::kWarps;
   extern __shared__ __align__(16) uint8_t raw[];
@@ -1254,7 +1277,12 @@ __global__ void __launch_bounds__(kThr) k_verify(const VerifyParams p) {
       }
     }
     if (rule.use_k || rule.use_p || rule.mp > 0.f) {
-      node.keep = cut_row(src, wp, rule, lane_top, sum_p, par ^ 1, &node.total_p);
+      const auto its_src = src;  // (copies, as Node's)
+      const Weights its_wp = wp;
+      const Rule its_rule = rule;
+      unsigned long long mass = 0;
+      node.keep = cut_row(its_src, its_wp, its_rule, lane_top, sum_p, par ^ 1, &mass);
+      node.total_p = mass;
       node.keep_x = node.keep ? key50_value(node.keep) : -INFINITY;
       if (node.keep && node.total_p == 0) node.sum_p = node.near_kept();  // (min-p alone)
     }
