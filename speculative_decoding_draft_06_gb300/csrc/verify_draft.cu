@@ -392,7 +392,9 @@ struct FloorSource : RowSource<false, E, Mem> {
 // largest, or a little below the k-th largest of the lanes' (by classes, with two
 // barriers of the cluster).
 template <typename S>
-__device__ __noinline__ float kth_floor(const S& src, const Weights& wp, int k, float lane_top, int half) {
+__device__ __noinline__ float kth_floor(const S& given, const Weights& its_wp, int k, float lane_top, int half) {
+  const S src(given);
+  const Weights wp(its_wp);
   using Mem = typename S::Mem;
   Mem& sm = src.sm;
   const int warps = src.cl * Mem::kWarps, tid = threadIdx.x;
@@ -431,7 +433,10 @@ __device__ __noinline__ float kth_floor(const S& src, const Weights& wp, int k, 
 // The cuts of the few tokens in the leader's list (its block; every token that
 // reaches the list's least is in it, k of them at least): each against all.
 template <typename S>
-__device__ __noinline__ void list_cut(const S& src, const Weights& wp, const Rule& rule, unsigned long long least, int n) {
+__device__ __noinline__ void list_cut(const S& given, const Weights& its_wp, const Rule& its_rule, unsigned long long least, int n) {
+  const S src(given);
+  const Weights wp(its_wp);
+  const Rule rule(its_rule);
   auto& sm = src.sm;
   const CalledWeights called(wp);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -517,8 +522,11 @@ __device__ __forceinline__ void share_between(float p, unsigned long long z, flo
 // ctl.total.  With `rest` the tokens below the source's floor are part of what
 // top-p's share is of, and the cut may stay open.
 template <typename S>
-__device__ __noinline__ bool class_cut(const S& src, const Weights& wp, const Rule& rule, bool rest,
+__device__ __noinline__ bool class_cut(const S& given, const Weights& its_wp, const Rule& its_rule, bool rest,
                                        unsigned long long* keep_io) {
+  const S src(given);
+  const Weights wp(its_wp);
+  const Rule rule(its_rule);
   auto& sm = src.sm;
   const CalledWeights called(wp);
   unsigned long long keep = *keep_io;
@@ -605,7 +613,8 @@ __device__ __noinline__ bool class_cut(const S& src, const Weights& wp, const Ru
 // warps' numbers of them, then the warp in whose share it lies.  Written to ctl.keep;
 // a barrier of the cluster has to follow.
 template <typename S>
-__device__ __noinline__ void nth_tie(const S& src, float v, unsigned want) {
+__device__ __noinline__ void nth_tie(const S& given, float v, unsigned want) {
+  const S src(given);
   auto& sm = src.sm;
   const auto& row = src.row;
   const int lane = threadIdx.x & 31, rest = row.index(row.units);
@@ -670,8 +679,11 @@ __device__ __noinline__ void nth_tie(const S& src, float v, unsigned want) {
 // in *mass (0: not known).  sum: the row's sum in fp32; half: which slots have the
 // warps' largest logits.
 template <typename S>
-__device__ __noinline__ unsigned long long cut_row(const S& src, const Weights& wp, const Rule& rule, float lane_top,
+__device__ __noinline__ unsigned long long cut_row(const S& given, const Weights& its_wp, const Rule& its_rule, float lane_top,
                                                    float sum, int half, unsigned long long* mass) {
+  const S src(given);
+  const Weights wp(its_wp);
+  const Rule rule(its_rule);
   using E = typename S::Elem;
   using Mem = typename S::Mem;
   Mem &sm = src.sm, &ls = src.ls;
@@ -683,7 +695,7 @@ __device__ __noinline__ unsigned long long cut_row(const S& src, const Weights& 
   unsigned long long keep = least;
   bool done = false;
   if (rule.use_k && rule.k <= kFew / 2) {  // few: by a list of those above the k-th's floor
-    const float floor = fmaxf(least_x, kth_floor(src, wp, rule.k, lane_top, half));
+    const float floor = fmaxf(least_x, kth_floor(S(src), Weights(wp), rule.k, lane_top, half));
     FloorSource<E, Mem>(src, floor).each_value([&](float x, int i) {
       const unsigned at = atomicAdd(&ls.list_n, 1u);
       if (at < kFew) ls.list[at] = key50(x, i);
@@ -691,7 +703,7 @@ __device__ __noinline__ unsigned long long cut_row(const S& src, const Weights& 
     cluster_sync();
     const int n = static_cast<int>(ls.list_n);
     done = n <= kFew;
-    if (done && src.lead) list_cut(src, wp, rule, least, n);
+    if (done && src.lead) list_cut(S(src), Weights(wp), Rule(rule), least, n);
     cluster_sync();
     if (src.lead && tid == 0) sm.list_n = 0;  // (the next to add to it comes behind another barrier)
     if (done) keep = ls.ctl.keep;
@@ -723,7 +735,7 @@ __device__ __noinline__ unsigned long long cut_row(const S& src, const Weights& 
               if (tid == 0) sm.list_n = 0;
             }
           } else {
-            nth_tie(src, v, want);
+            nth_tie(S(src), v, want);
           }
           cluster_sync();
           keep = ls.ctl.keep;
@@ -740,7 +752,7 @@ __device__ __noinline__ unsigned long long cut_row(const S& src, const Weights& 
     keep = least;
     if (rule.use_k && rule.k <= 1024) {
       cluster_sync();  // (ctl may be written again)
-      floor = fmaxf(floor, kth_floor(src, wp, rule.k, lane_top, half));
+      floor = fmaxf(floor, kth_floor(S(src), Weights(wp), rule.k, lane_top, half));
       // (what lies below it is out, also where k tokens are left)
       if (floor > -INFINITY) keep = max(keep, static_cast<unsigned long long>(float_order(floor + 0.f)) << kIdxBits);
     } else if (!rule.use_k && least == 0 && rule.tp > 0.f) {
@@ -751,8 +763,9 @@ __device__ __noinline__ unsigned long long cut_row(const S& src, const Weights& 
   }
   for (int round = 0; round < 2 && !done; ++round) {
     cluster_sync();  // (ctl and the classes' memory may be written again)
-    done = class_cut(FloorSource<E, Mem>(src, floor), wp, rule, rest, &keep);
-    if (!done) keep = least;
+    unsigned long long kept = keep;
+    done = class_cut(FloorSource<E, Mem>(src, floor), Weights(wp), Rule(rule), rest, &kept);
+    keep = done ? kept : least;
     floor = -INFINITY;
     rest = false;
   }
