@@ -124,25 +124,19 @@ struct VerifySmem {
 
 // Behind it, B + 1 entries each.
 struct TreeSmem {
-  int *parent, *token;        // the request's tree and random numbers
-  float* u;
-  int* kids;                  // the node's children
-  float *kid_p, *kid_q;       // their logits (q -inf: passed over)
-  float *reject_a, *reject_q; // the rejected ones: A behind them, about, and their logits under q
+  int* at;
+  int n;
   static constexpr int kArrays = 8;
-  __device__ __forceinline__ TreeSmem(void* at, int B) {
-    float* f = static_cast<float*>(at);
-    int* i = static_cast<int*>(at);
-    const int n = B + 1;
-    parent = i;
-    token = i + n;
-    kids = i + 2 * n;
-    u = f + 3 * n;
-    kid_p = f + 4 * n;
-    kid_q = f + 5 * n;
-    reject_a = f + 6 * n;
-    reject_q = f + 7 * n;
-  }
+  __device__ __forceinline__ TreeSmem(void* from, int B) : at(static_cast<int*>(from)), n(B + 1) {}
+  __device__ __forceinline__ float* floats(int k) const { return reinterpret_cast<float*>(at + k * n); }
+  __device__ __forceinline__ int* parent() const { return at; }  // the request's tree and random numbers
+  __device__ __forceinline__ int* token() const { return at + n; }
+  __device__ __forceinline__ float* u() const { return floats(2); }
+  __device__ __forceinline__ int* kids() const { return at + 3 * n; }  // the node's children
+  __device__ __forceinline__ float* kid_p() const { return floats(4); }  // their logits (q -inf: passed over)
+  __device__ __forceinline__ float* kid_q() const { return floats(5); }
+  __device__ __forceinline__ float* reject_a() const { return floats(6); }  // the rejected ones: A behind them,
+  __device__ __forceinline__ float* reject_q() const { return floats(7); }  // about, and their logits under q
 };
 
 // Weights of a row's tokens: bf16's codes from a table.
@@ -1002,7 +996,7 @@ struct Node {
     const int m = min(levels, tried - done);
     float lc[kLevels];
 #pragma unroll
-    for (int k = 0; k < kLevels; ++k) lc[k] = k < m ? log2_c(tree.reject_a[done + k]) : INFINITY;
+    for (int k = 0; k < kLevels; ++k) lc[k] = k < m ? log2_c(tree.reject_a()[done + k]) : INFINITY;
     Sums t;
     if (levels == 0) sum_up<0>(lc, t);
     else if (levels == 1) sum_up<1>(lc, t);
@@ -1011,7 +1005,7 @@ struct Node {
     if (threadIdx.x < 32) {
       int at = 0;
       if (m > 0) {
-        const unsigned long long weight = lane < m ? CalledWeights(wq).weight44(tree.reject_q[done + lane]) : 0ull;
+        const unsigned long long weight = lane < m ? CalledWeights(wq).weight44(tree.reject_q()[done + lane]) : 0ull;
         const double inv_np = 1. / static_cast<double>(t.p), inv_nq = 1. / static_cast<double>(t.q);
         double a = sm.ex.A, n = sm.ex.N, z = sm.ex.Z;
         unsigned long long gone = sm.ex.gone;
@@ -1019,9 +1013,9 @@ struct Node {
         for (int k = 0; k < kLevels; ++k) {
           if (k >= m || at < k) continue;
           const double next_a = a == 0. ? 1. : z > 0. ? a + n / z : a;
-          if (fabs(next_a - static_cast<double>(tree.reject_a[done + k])) > 0x1p-17 * next_a) {
+          if (fabs(next_a - static_cast<double>(tree.reject_a()[done + k])) > 0x1p-17 * next_a) {
             __syncwarp();
-            if (lane == 0) tree.reject_a[done + k] = static_cast<float>(next_a);
+            if (lane == 0) tree.reject_a()[done + k] = static_cast<float>(next_a);
             continue;
           }
           a = next_a;
@@ -1103,7 +1097,7 @@ struct Node {
       if (threadIdx.x == 0) {
         sm.ex.yes = ok;
         sm.ex.drawn = left;
-        tree.reject_a[tried] = static_cast<float>(sm.ex.A + a);
+        tree.reject_a()[tried] = static_cast<float>(sm.ex.A + a);
       }
     }
     __syncthreads();
@@ -1147,10 +1141,10 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
   if (tid == 0) sm.cls_n = sm.list_n = 0;
   const int n = max(0, min(p.n_out[r], p.B));
   for (int i = tid; i < n; i += kThr) {
-    tree.parent[i] = p.parent ? p.parent[static_cast<size_t>(r) * p.B + i] : i - 1;
-    tree.token[i] = p.token[static_cast<size_t>(r) * p.B + i];
+    tree.parent()[i] = p.parent ? p.parent[static_cast<size_t>(r) * p.B + i] : i - 1;
+    tree.token()[i] = p.token[static_cast<size_t>(r) * p.B + i];
   }
-  for (int i = tid; i <= n; i += kThr) tree.u[i] = p.u[static_cast<size_t>(r) * (p.B + 1) + i];
+  for (int i = tid; i <= n; i += kThr) tree.u()[i] = p.u[static_cast<size_t>(r) * (p.B + 1) + i];
   int par = 0, cur = 0, len = 0;
   cluster_sync();  // (every CTA's memory is there)
 
@@ -1164,7 +1158,7 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
     if (cur < p.draft_rows)  // (else no draft distribution: nothing was drawn there)
       for (int b = cur; b < n; b += kThr) {
         const int i = b + tid;
-        const bool mine = i < n && tree.parent[i] == cur - 1;
+        const bool mine = i < n && tree.parent()[i] == cur - 1;
         const unsigned in = __ballot_sync(kFullMask, mine);
         if (lane == 0) sm.kid_count[warp] = __popc(in);
         __syncthreads();
@@ -1173,12 +1167,12 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
           if (w < warp) at += sm.kid_count[w];
           kids += sm.kid_count[w];
         }
-        if (mine) tree.kids[at + __popc(in & ((1u << lane) - 1u))] = i;
+        if (mine) tree.kids()[at + __popc(in & ((1u << lane) - 1u))] = i;
         __syncthreads();
       }
     // a thread per child: its logits (on their way during the pass below)
     auto kid_logits = [&](int k, float* lp, float* lq) {
-      const int x = tree.token[tree.kids[k]];
+      const int x = tree.token()[tree.kids()[k]];
       *lp = *lq = -INFINITY;
       if (x >= 0 && x < p.V) {
         *lp = logit<E>(prow, x);
@@ -1206,11 +1200,11 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
       for (int k = tid; k < kids; k += kThr) {
         if (k != tid) kid_logits(k, &lp, &lq);
         // (of several with one token the first counts)
-        const int x = tree.token[tree.kids[k]];
+        const int x = tree.token()[tree.kids()[k]];
         bool twice = false;
-        for (int j = 0; j < k; ++j) twice |= tree.token[tree.kids[j]] == x;
-        tree.kid_p[k] = lp;
-        tree.kid_q[k] = twice ? -INFINITY : lq;
+        for (int j = 0; j < k; ++j) twice |= tree.token()[tree.kids()[j]] == x;
+        tree.kid_p()[k] = lp;
+        tree.kid_q()[k] = twice ? -INFINITY : lq;
       }
       cluster_sync();
       top_p = top_q = -INFINITY;
@@ -1260,7 +1254,7 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
       const int x = (1 << kIdxBits) - 1 - static_cast<int>(best & ((1u << kIdxBits) - 1));
       int next = -1;
       for (int k = kids - 1; k >= 0; --k)
-        if (tree.token[tree.kids[k]] == x) next = tree.kids[k];
+        if (tree.token()[tree.kids()[k]] == x) next = tree.kids()[k];
       if (next < 0) {
         if (lead && tid == 0) {
           p.bonus[r] = x;
@@ -1278,11 +1272,11 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
     // cuts off, at a quarter of its cost)
     if (rule.use_p && !rule.use_k && !(rule.mp > 0.f) && rule.tp > 0.f) {
       int k = 0;
-      while (k < kids && !(tree.kid_q[k] > -INFINITY && wq.log2w(tree.kid_q[k]) >= kZeroBelow + 2.f)) ++k;
-      if (k < kids && isfinite(sum_p) && isfinite(sum_q) && tree.kid_p[k] > -INFINITY) {
-        const int kid = tree.kids[k];
-        const float need = tree.u[kid + 1] * ex2(wq.log2w(tree.kid_q[k])) / sum_q;
-        if (node.surely_kept(tree.kid_p[k], tree.token[kid], rule.tp, need)) {
+      while (k < kids && !(tree.kid_q()[k] > -INFINITY && wq.log2w(tree.kid_q()[k]) >= kZeroBelow + 2.f)) ++k;
+      if (k < kids && isfinite(sum_p) && isfinite(sum_q) && tree.kid_p()[k] > -INFINITY) {
+        const int kid = tree.kids()[k];
+        const float need = tree.u()[kid + 1] * ex2(wq.log2w(tree.kid_q()[k])) / sum_q;
+        if (node.surely_kept(tree.kid_p()[k], tree.token()[kid], rule.tp, need)) {
           par = node.par;
           accept(kid);
           continue;
@@ -1307,13 +1301,13 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
     const float near_p = node.near_p(), inv_p = 1.f / near_p, inv_q = 1.f / sum_q;
     for (int k = 0; k < kids; ++k) {
       if (node.exact && !(sm.ex.N > 0.)) break;
-      const int kid = tree.kids[k];
-      const float xq = tree.kid_q[k], xp = tree.kid_p[k], yq = wq.log2w(xq);
+      const int kid = tree.kids()[k];
+      const float xq = tree.kid_q()[k], xp = tree.kid_p()[k], yq = wq.log2w(xq);
       // (it cannot have been drawn)
       if (!(xq > -INFINITY) || !(yq >= kZeroBelow)) continue;
       if (yq < kZeroBelow + 2.f && CalledWeights(wq).weight44(xq) == 0) continue;
-      const bool in = node.kept(xp, tree.token[kid]);
-      const float ux = tree.u[kid + 1], qx = ex2(yq) * inv_q;
+      const bool in = node.kept(xp, tree.token()[kid]);
+      const float ux = tree.u()[kid + 1], qx = ex2(yq) * inv_q;
       bool yes = false, drawn = true;
       if (!node.exact) {
         const float px = in ? ex2(wp.log2w(xp)) * inv_p : 0.f, a = N / Z;
@@ -1338,8 +1332,8 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
       Z -= qx;
       off_z += kSumError * qx;
       if (tid == 0) {
-        if (!node.exact) tree.reject_a[node.tried] = A;
-        tree.reject_q[node.tried] = xq;
+        if (!node.exact) tree.reject_a()[node.tried] = A;
+        tree.reject_q()[node.tried] = xq;
       }
       ++node.tried;
       __syncthreads();
@@ -1347,7 +1341,7 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
         node.settle();
       } else {
         bool more = false;  // another child to be tested (the draw takes whole numbers)
-        for (int j = k + 1; j < kids; ++j) more |= tree.kid_q[j] > -INFINITY;
+        for (int j = k + 1; j < kids; ++j) more |= tree.kid_q()[j] > -INFINITY;
         if (!more) break;
         N = node.near_pass(A) * inv_p;
         off_n = kSumError * (1.f + A) + off_a;
@@ -1398,7 +1392,7 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
         if (lane >= o) inc += y;
       }
       const double total = __shfl_sync(kFullMask, inc, 31);
-      const double u0 = static_cast<double>(tree.u[0]);
+      const double u0 = static_cast<double>(tree.u()[0]);
       const double mark = u0 > 0. ? fmin(u0, 1.) * total : 0.;
       double before = inc - sum, left = 0.;
       int owner = -1, last = -1;
