@@ -24,16 +24,18 @@
 // row by counts of its codes.
 //
 // Bound by latency: a path's nodes wait for one another, and each is a chain of
-// passes, barriers of the cluster and scalar steps, 5 us at the least; the pass in
+// passes, barriers of the cluster and scalar steps, 4 us at the least; the pass in
 // whole numbers by issue and by its table's bank conflicts (two look-ups a token).
-// One chain of 8 over 32000 fp32 logits 36 to 56 us (by its path); 16 trees of 128 nodes
-// over 151936 in bf16 137 to 157 us, 64 chains of 7 with settings of their own 300 to
-// 390 us (both to the end of their longest paths; the rows of all paths read once would
-// take 10 and 20 us).  Steps for the trees (the chains): every sum in whole numbers 210 us (837);
-// tests in fp32, one pass in whole numbers per path, its fp64 in one warp 147 (440,
-// top-p); floors and lists for top-k, the pass at the draw in line 137 (385);
-// acceptance before the cut 140 (318).  The passes as calls cost 7%, two CTAs of 512
-// threads to an SM (64 registers) 20 to 40%.
+// One chain of 8 over 32000 fp32 logits 31 to 40 us (by its path); 16 trees of 128 nodes
+// over 151936 in bf16 104 to 121 us, 64 chains of 7 with settings of their own 266 to
+// 320 us (both to the end of their longest paths; the rows of all paths read once would
+// take 10 and 20 us).  Steps for the trees (the chains; by other draws than these):
+// every sum in whole numbers 210 us (837); tests in fp32, one pass in whole numbers per
+// path, its fp64 in one warp 147 (440, top-p); floors and lists for top-k, the pass at
+// the draw in line 137 (385); acceptance before the cut 140 (318); a node's state and
+// the cuts' arguments in registers, copies of them for the calls, 136 to 104 (301 to
+// 266).  The passes as calls cost 7%, two CTAs of 512 threads to an SM (64 registers) 20
+// to 40%, copies in registers inside the calls of a Node too 3 to 10%.
 #include "row_cuts.cuh"
 
 namespace dt {
@@ -1562,10 +1564,10 @@ extern "C" dartree_status dartree_verify(const int32_t* parent, const int32_t* t
   // A request's rows over several CTAs.  15 clusters of 8, 36 of 4 and 76 of 2 find
   // room at once; paths differ in length, so a few more than that still gain (those
   // that wait start long before the longest ends).  Chains of 7 over 151936 bf16
-  // logits without cuts (with settings of their own), us: 16 of them by 8 CTAs 106
-  // (149), by 4 113 (176); 24 147 (209), 113 (186); 40 by 4 156 (204), by 2 177 (277);
-  // 64 205 (283), 176 (322); 100 by 2 248 (335), by 1 291 (529); 150 342 (472), 306
-  // (623).
+  // logits without cuts (with settings of their own), us: 16 of them by 8 CTAs 82
+  // (128), by 4 93 (153); 24 110 (178), 89 (160); 40 by 4 127 (174), by 2 151 (243);
+  // 64 168 (238), 152 (283); 100 by 2 216 (296), by 1 264 (487); 150 294 (416), 276
+  // (581).
   const int most = R <= 16 ? kMaxCl : R <= 40 ? 4 : R <= 152 ? 2 : 1;
   int cl = 1;
   while (cl < most && V / cl > 4096) cl *= 2;
