@@ -59,7 +59,7 @@ def problem(g, R, B, V, kids, depth, spread=2.0, noise=0.7, Td=None):
     return par, tok, n, z, d
 
 
-def check(par, tok, n, z, d, u, *, max_len=40, chain=False, types=(F32, F32), out=None, **rules):
+def check(par, tok, n, z, d, u, *, max_len=40, chain=False, types=(F32, F32), out=None, open_=0, **rules):
     """One call against the reference; rules: T, k, p, mp, Td [R] each."""
     R = len(n)
     if out is None:
@@ -78,7 +78,7 @@ def check(par, tok, n, z, d, u, *, max_len=40, chain=False, types=(F32, F32), ou
         assert got["nodes"][r].tolist() == want, (r, got["nodes"][r], want)
         assert got["bonus"][r] == t, (r, got["bonus"][r], t)
         assert abs(got["prob"][r] - prob) <= tol, (r, got["prob"][r], prob, tol)
-    assert near <= 1 + 0.05 * R, near
+    assert near <= open_ + 1 + 0.05 * R, near
     return out
 
 
@@ -205,6 +205,22 @@ def test_cut_within_one_logit(V, first):
     for types in ((BF16, BF16), (F32, BF16)):
         out = check(np.full((R, 1), -1), np.zeros((R, 1)), np.zeros(R, int), z, d, u, types=types, k=k)
         assert (host(out["bonus"])[::2] == k[::2] - 1).all()
+
+
+@pytest.mark.parametrize("V", [7, 900, 20011])
+def test_smallest_random_numbers(V):
+    """u[0] down to the smallest fp32.  Weights off by 2^-44 of the largest leave the
+    first tokens' running sums open by e = V 2^-43 (p_max + q_max) / N, 1e-9 at V = 20011:
+    a mark u[0] below that may fall on any of the leading tokens that are together
+    less, so the six draws up to 1e-9 may each be undecided."""
+    g = np.random.default_rng(V)
+    draws = np.array([2.0 ** -149, 1e-40, 1e-30, 1e-20, 2.0 ** -45, 1e-9, 2.0 ** -25, 2.0 ** -24, 3e-5, 1 - 2.0 ** -24], np.float32)
+    R, B = len(draws), 3
+    par, tok, n, z, d = problem(g, R, B, V, 1, 3)
+    u = g.random((R, B + 1)).astype(np.float32)
+    u[:, 0] = draws
+    check(par, tok, n, z, d, u, chain=True, open_=6)
+    check(par, tok, n, z, d, u, chain=True, types=(BF16, BF16), p=np.full(R, 0.9), open_=6)
 
 
 def test_infinite_logits():
