@@ -716,7 +716,8 @@ struct Plan {
 // what lies between its first row's window and its last row (of `rows` rows: a
 // chain's positions, a tree's root and nodes).  small: requests may have few
 // rows, which the few-rows kernel takes in the launch of the rows left over (a
-// prompt's 2001 rows among 32 single tokens: 380 us all by the tensor cores, 251 so).
+// prompt's 2001 rows among 32 single tokens: 380 us all by the tensor cores, 288 so; 250
+// with the steps since).
 struct Reach {
   int max_len, window, sinks, g;
   bool all, chain, small;
