@@ -699,7 +699,7 @@ dartree_status token_params(const dartree_cache* cache, int32_t layer, const voi
   p->R = R;
   p->n = n;
   const int tok = 512 / p->c.dh;  // tokens per warp
-  p->groups = (n + tok - 1) / tok;
+  p->groups = (n - 1) / tok + 1;
   p->err = err;
   const long long warps = static_cast<long long>(R) * p->groups * p->c.Hkv;
   if (warps > 0x7FFFFFF0ll) return cache_fail(DARTREE_ERR_UNSUPPORTED, "too many tokens in one call");
