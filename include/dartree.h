@@ -522,7 +522,7 @@ dartree_status dartree_cache_read_ex(const dartree_cache *cache, int32_t layer, 
  * row sees need not be written.  A row with
  * lens[r] < 0 is skipped (with n_nodes[r] < 0, too): left as it was.  _ex:
  * with zero_rest != 0 the rows that are left otherwise are written as 0.
- * B <= 1024, Hq % Hkv == 0; Q, O 16-byte aligned.
+ * B <= 1024, Hq % Hkv == 0, (B + 1) Hq / Hkv <= 2^30; Q, O 16-byte aligned.
  * work: dartree_cache_attention_workspace() bytes of scratch, 16-byte
  * aligned, that overlapping calls must not share (its contents need no
  * preparation; NULL when the size is 0). */

@@ -865,7 +865,7 @@ dartree_status attention_run(CacheAttnParams p, const Reach& reach, bool odd_kno
   return cache_launched(e);
 }
 
-constexpr int kFar = 1 << 30;  // no window; as far as positions go
+constexpr int kFar = 1 << 30;  // no window; as far as positions go; rows of a key/value head at most
 
 // max_len, window, sinks as a call's Reach (window < 1: none).
 Reach reach_of(int32_t B, int32_t max_len, int32_t window, int32_t sinks, bool chain, bool small, int32_t g) {
@@ -930,7 +930,7 @@ extern "C" dartree_status dartree_cache_window_attention(
 extern "C" size_t dartree_cache_attention_workspace(int32_t R, int32_t B, int32_t max_len, int32_t Hq,
                                                     int32_t Hkv, int32_t dh) {
   if (R < 1 || B < 0 || B > DARTREE_MAX_B || max_len < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 ||
-      (dh != 64 && dh != 128))
+      (dh != 64 && dh != 128) || static_cast<long long>(B + 1ll) * (Hq / Hkv) > dt::kFar)
     return 0;
   return dt::attention_work(R, B, dt::reach_of(B, max_len, 0, 0, false, false, Hq / Hkv), Hq, Hkv, dh);
 }
@@ -949,6 +949,8 @@ extern "C" dartree_status dartree_cache_attention_ex(const dartree_cache* cache,
     return cache_fail(DARTREE_ERR_INVALID_ARG, why);
   if (B > 0 && !mask) return cache_fail(DARTREE_ERR_INVALID_ARG, "null pointer argument");
   if (B > DARTREE_MAX_B) return cache_fail(DARTREE_ERR_INVALID_ARG, "bad R, B, max_pages, max_len, Hq or scale");
+  if (static_cast<long long>(B + 1ll) * p.g > kFar)
+    return cache_fail(DARTREE_ERR_UNSUPPORTED, "too many rows per key/value head");
   p.mask = mask;
   p.n_nodes = n_nodes;
   p.err = err;

@@ -17,3 +17,12 @@ def test_tokens_of_one_write(lib, n, dh):  # noqa: F811
     assert window_call(lib, "append_slots", desc(**c), n=n, ts=64 * dh) == UNSUPPORTED
     assert call(lib, "append", desc(**c), R=1, n=n, ts=64 * dh) == UNSUPPORTED
     assert call(lib, "read", desc(**c), R=1, n=n) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("B, Hq", [(1023, 1 << 30), (1024, MOST), (1023, MOST), (1, 1 << 30)])
+def test_rows_of_one_head(lib, B, Hq):  # noqa: F811
+    """More than 2^30 rows per key/value head."""
+    assert lib.dartree_cache_attention_workspace(1, B, 100, Hq, 1, 64) == 0
+    c = dict(Hkv=1, dh=64)
+    assert call(lib, "attention", desc(**c), R=1, B=B, Hq=Hq, qs=64 * Hq) == UNSUPPORTED
+    assert window_call(lib, "window_attention", desc(**c), R=1, B=B, Hq=Hq, qs=64 * Hq, q_rows=B + 1) == UNSUPPORTED
