@@ -328,6 +328,6 @@ extern "C" dartree_status dartree_cache_plan(const dartree_cache* cache, int32_t
   if (e == cudaSuccess)
     e = launch_kernel_cluster(k_cache_plan, dim3(kMaxCl), dim3(kPlanThreads), sizeof(PlanSmem), st, true, kMaxCl, p);
   if (e == cudaSuccess && !p.own_maps)
-    e = launch_kernel(k_cache_maps, dim3((max_tokens + 1023) / 1024), dim3(256), 0, st, true, p);
+    e = launch_kernel(k_cache_maps, dim3((max_tokens - 1) / 1024 + 1), dim3(256), 0, st, true, p);
   return cache_launched(e);
 }
