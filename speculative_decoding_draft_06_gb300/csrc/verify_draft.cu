@@ -1289,9 +1289,11 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
     // ---- the cuts (top-p alone: often the first child is accepted whatever it
     // cuts off, at a quarter of its cost)
     if (rule.use_p && !rule.use_k && !(rule.mp > 0.f) && rule.tp > 0.f) {
+      // (the first that may have been drawn; one of a weight near zero is left to the tests)
       int k = 0;
-      while (k < kids && !(tree.kid_q()[k] > -INFINITY && wq.log2w(tree.kid_q()[k]) >= kZeroBelow + 2.f)) ++k;
-      if (k < kids && isfinite(sum_p) && isfinite(sum_q) && tree.kid_p()[k] > -INFINITY) {
+      while (k < kids && !(tree.kid_q()[k] > -INFINITY && wq.log2w(tree.kid_q()[k]) >= kZeroBelow)) ++k;
+      if (k < kids && wq.log2w(tree.kid_q()[k]) >= kZeroBelow + 2.f && isfinite(sum_p) && isfinite(sum_q) &&
+          tree.kid_p()[k] > -INFINITY) {
         const int kid = tree.kids()[k];
         const float need = tree.u()[kid + 1] * ex2(wq.log2w(tree.kid_q()[k])) / sum_q;
         if (node.surely_kept(tree.kid_p()[k], tree.token()[kid], rule.tp, need)) {
