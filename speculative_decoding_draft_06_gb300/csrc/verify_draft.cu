@@ -188,10 +188,11 @@ __device__ __forceinline__ void load_logits(const E* src, int at, bool wide, flo
   for (int k = 0; k < kN; ++k) x[k] = fmaxf(x[k], -INFINITY);
 }
 
-// log2(e) / T as a sum of two floats.
+// log2(e) / T as a sum of two floats (of an infinite T the smallest float: 0 times the
+// distance of a logit of -inf would be NaN).
 __device__ __forceinline__ void set_temperature(Weights& wt, float T) {
   constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLo = 1.9259629911266175e-8f;
-  wt.ch = __fdiv_rn(kLog2e, T);
+  wt.ch = T == INFINITY ? 0x1p-149f : __fdiv_rn(kLog2e, T);
   wt.cl = isfinite(wt.ch) && isfinite(T) ? __fdiv_rn(fmaf(-wt.ch, T, kLog2e) + kLog2eLo, T) : 0.f;
 }
 

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from tests.test_gpu_cache import host
-from tests.test_gpu_verify_draft import BF16, F32, check
+from tests.test_gpu_verify_draft import BF16, F32, check, run
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +36,29 @@ def test_the_first_child_has_the_smallest_weight(bits, types):
     for rules in (dict(p=np.full(R, 0.98)), dict(), dict(p=np.full(R, 0.98), k=np.full(R, 30)), dict(p=np.full(R, 0.98), mp=np.full(R, 1e-3))):
         out = check(par, tok, np.full(R, 2), z, d, u, types=types, **rules)
         assert (host(out["nodes"])[:, 0] == (0 if drawn else 1)).all(), rules
+
+
+@pytest.mark.parametrize("V", [7, 300, 5003])
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16), (F32, BF16), (BF16, F32)])
+def test_infinite_temperatures(V, types):
+    """A draft (or a target) of infinite temperature is uniform over its tokens above
+    -inf: the same as equal logits there."""
+    g = np.random.default_rng(V)
+    R, B = 20, 3
+    par, n = np.tile([-1, -1, 0], (R, 1)), np.full(R, B)
+    z = torch.from_numpy((2 * g.standard_normal((R, B + 1, V))).astype(np.float32)).to(BF16).float().numpy()
+    d = torch.from_numpy((2 * g.standard_normal((R, B + 1, V))).astype(np.float32)).to(BF16).float().numpy()
+    gone = g.random((R, B + 1, V)) < 0.4
+    gone[:, :, 0] = False
+    flat = np.where(gone, -np.inf, 0.0).astype(np.float32)
+    tok = np.stack([g.choice(np.flatnonzero(~gone[r, 0]), 3, replace=V < 8) for r in range(R)])
+    u = g.random((R, B + 1)).astype(np.float32)
+    inf = np.full(R, np.inf)
+
+    def dev(x, t):
+        return torch.from_numpy(x.astype(np.float32)).to(t).cuda()
+
+    out = run(par, tok, n, dev(z, types[0]), dev(np.where(gone, -np.inf, d), types[1]), u, Td=inf)
+    check(par, tok, n, z, flat, u, out=out)
+    out = run(par, tok, n, dev(np.where(gone, -np.inf, z), types[0]), dev(d, types[1]), u, T=inf)
+    check(par, tok, n, flat, d, u, out=out)
