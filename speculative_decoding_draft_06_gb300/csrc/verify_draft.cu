@@ -18,8 +18,10 @@
 // where a test lies within the bound, and the draw at the path's end: there 32-bit
 // sums would not do, a row has as many borders as tokens.  One pass gives them for
 // up to kLevels rejections: what enters N_k are the sums of p and of q over the
-// tokens with p > A_k q, which the approximate A_k tells apart (a token on the
-// wrong side adds the square of A_k's error); the exact A_k follow from them.
+// tokens with p > A_k q, which the logarithms and the approximate A_k tell apart to
+// 2^-14 (kBorder); the exact A_k follow from them.  Where the tokens that lie nearer
+// to the border could matter to N_k (a target that is its draft but for a few tokens),
+// one more pass takes those in whole numbers, by the exact A_k.
 // top-k, min-p and top-p cut the target's row first, as dartree_sample does; a bf16
 // row by counts of its codes.
 //
@@ -60,6 +62,8 @@ constexpr int kMaxCl = 8;
 constexpr int kLevels = 4;           // rejections of a pass in whole numbers
 constexpr int kNotes = 256;           // tokens that a warp notes in a scan
 constexpr int kFew = 512;            // tokens of a list on which top-k is decided by comparing all
+constexpr float kBorder = 0x1p-14f;  // what log2 p - log2 A q may be off by: two logarithms below 46, three
+                                     // roundings each, 2^-15.9; A by 2^-17 and the rows' sums by 2^-18, 2^-15.5
 constexpr float kSumError = 0x1p-16f;  // relative error of a sum in fp32 (logits' differences times
                                        // log2(e) / T below 46: 2^-19 each; the additions' 2^-18)
 
@@ -97,6 +101,7 @@ struct VerifySmem {
     unsigned long long best;
   };
   __align__(16) Slot slot[2][kMaxCl * kWarps];
+  unsigned long long near[2];      // p over the tokens within kBorder of a level's border (as slot; 0 between its uses)
   uint16_t notes[kWarps][kNotes];  // of a scan
   unsigned long long scan_m[kWarps];
   unsigned scan_c[kWarps];
@@ -121,6 +126,7 @@ struct VerifySmem {
     int owner;                   // the warp that has it
     unsigned long long scale_m;  // A sum_p / sum_q
     int scale_s;
+    int border;                  // the next pass takes the tokens at the border in whole numbers, by it
   } ex;
 };
 
@@ -289,7 +295,8 @@ __device__ __forceinline__ void row_stats(const Row<E>& row, int ub, int ue, boo
   if (last && lane < row.V - rest) one(rest + lane);
 }
 
-// c q^ in whole units for the tokens with p^ > c q^ (about: at most p^): c = m 2^-s.
+// floor(c q), or `most` where that is less, for c = m 2^-s > 0.  Exact: where the sum of some
+// tokens' p is above that of their q, one of them is above its own.
 struct Scale {
   unsigned long long m;
   int s;
@@ -298,17 +305,11 @@ struct Scale {
     return Scale{c > 0. ? static_cast<unsigned long long>(scalbn(c, 62 - e)) : 0ull, 62 - e};  // [2^62, 2^63)
   }
   __device__ __forceinline__ unsigned long long of(unsigned long long q, unsigned long long most) const {
-    // q < 2^45: (q 2^18) m / 2^64 = c q 2^(s - 46)
-    const unsigned long long h = __umul64hi(q << 18, m);
-    const int down = s - 46;
-    const unsigned long long x = down >= 64 ? 0ull : down >= 0 ? h >> down : down > -64 ? h << -down : most;
-    return min(x, most);
-  }
-  // the same of sums (below 2^63)
-  __device__ __forceinline__ unsigned long long of_sum(unsigned long long q, unsigned long long most) const {
-    const unsigned long long h = __umul64hi(q, m);  // c q 2^(s - 64)
-    const int up = 64 - s;
-    const unsigned long long x = up <= -64 ? 0ull : up <= 0 ? h >> -up : up < 64 && h >> (64 - up) == 0 ? h << up : h ? most : 0ull;
+    const unsigned long long hi = __umul64hi(q, m), lo = q * m;
+    unsigned long long x;
+    if (s >= 64) x = s >= 128 ? 0ull : hi >> (s - 64);
+    else if (s > 0) x = hi >> s ? most : hi << (64 - s) | lo >> s;
+    else x = s == 0 && !hi ? lo : q ? most : 0ull;
     return min(x, most);
   }
 };
@@ -933,12 +934,13 @@ struct Node {
   }
   static __device__ __noinline__ float kept_call(Node* n) { return n->near_pass(0.f); }
 
-  template <int kMost>
+  template <int kMost, bool kExactBorder = false>
   __device__ __forceinline__ void sum_up(const float (&lc)[kLevels], Sums& t) {
     const int lane = threadIdx.x & 31;
     const Weigh<E, Weights> weigh_p(wp, sm.table_p);
     const Weigh<F, Weights> weigh_q(wq, sm.table_q);
     t = Sums{};
+    float near = 0.f;
     each_pair<(kMost > 0)>([&](float x, float y, int i) {
       const unsigned long long v = kept(x, i) ? weigh_p(x) : 0ull;
       t.p += v;
@@ -947,11 +949,18 @@ struct Node {
         t.q += w;
         const float gap = v ? wp.log2w(x) - wq.log2w(y) : -INFINITY;
 #pragma unroll
-        for (int k = 0; k < kMost; ++k)
-          if (gap > lc[k]) {
+        for (int k = 0; k < kMost; ++k) {
+          const float by = gap - lc[k];
+          bool over = by > 0.f;
+          if (fabsf(by) < kBorder) {
+            if constexpr (kExactBorder) over = Scale{sm.ex.scale_m, sm.ex.scale_s}.of(w, v) < v;
+            else near += __ull2float_rn(v);
+          }
+          if (over) {
             t.over_p[k] += v;
             t.over_q[k] += w;
           }
+        }
       }
     });
     auto reduce = [&]() {
@@ -968,6 +977,13 @@ struct Node {
     };
     reduce();
     if (kMost == 0) t.over_p[0] = t.p;
+    if (kMost > 0 && !kExactBorder && __any_sync(kFullMask, near > 0.f)) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) near += __shfl_xor_sync(kFullMask, near, o);
+      // (a whole number: the same in every CTA, in whatever order the warps come)
+      const unsigned long long mine = __float2ull_rn(__shfl_sync(kFullMask, near, 0));
+      if (lane < cl) atomicAdd(&at_rank(&sm, lane)->near[par], mine);
+    }
     if (lane < cl) {
       Sums& to = at_rank(&sm, lane)->slot[par][gw].sums;
       to.p = t.p;
@@ -997,8 +1013,11 @@ struct Node {
 
   // The sums in whole numbers.  levels 0: p's alone; above: for the rejected
   // children from `done` on (or, behind all of them, only the rows' totals), whose As
-  // in reject_a tell the tokens' sides.  Where one turns out too far off, it is
-  // corrected, and settled with the next pass.  The warps' sums are left in slot[par ^ 1].
+  // in reject_a tell the tokens' sides.  Where one of them or the rows' sums turn out
+  // too far off, or the tokens at the border too many, it is settled with the next
+  // pass (kExactBorder: one level, whose scale is known).  The warps' sums are left in
+  // slot[par ^ 1].
+  template <bool kExactBorder = false>
   __device__ __forceinline__ void exact_pass(int levels, int done) {
     const int lane = threadIdx.x & 31;
     if (!tables && sizeof(E) + sizeof(F) < 8) {
@@ -1017,35 +1036,51 @@ struct Node {
 #pragma unroll
     for (int k = 0; k < kLevels; ++k) lc[k] = k < m ? log2_c(tree.reject_a()[done + k]) : INFINITY;
     Sums t;
-    if (levels == 0) sum_up<0>(lc, t);
+    if constexpr (kExactBorder) sum_up<1, true>(lc, t);
+    else if (levels == 0) sum_up<0>(lc, t);
     else if (levels == 1) sum_up<1>(lc, t);
     else sum_up<kLevels>(lc, t);
     par ^= 1;
     if (threadIdx.x < 32) {
       int at = 0;
+      bool border = false;
       if (m > 0) {
         const unsigned long long weight = lane < m ? CalledWeights(wq).weight44(tree.reject_q()[done + lane]) : 0ull;
         const double inv_np = 1. / static_cast<double>(t.p), inv_nq = 1. / static_cast<double>(t.q);
         double a = sm.ex.A, n = sm.ex.N, z = sm.ex.Z;
         unsigned long long gone = sm.ex.gone;
+        // (the sums that the sides were told by: exact ones from the next pass on)
+        const float p44 = __ull2float_rn(t.p), q44 = __ull2float_rn(t.q), near = __ull2float_rn(sm.near[par ^ 1]);
+        const bool sound = fabsf(near_p() * 0x1p44f - p44) <= 0x1p-18f * p44 && fabsf(near_q() * 0x1p44f - q44) <= 0x1p-18f * q44;
 #pragma unroll
         for (int k = 0; k < kLevels; ++k) {
-          if (k >= m || at < k) continue;
+          if (k >= m || at < k || !sound || border) continue;
           const double next_a = a == 0. ? 1. : z > 0. ? a + n / z : a;
           if (fabs(next_a - static_cast<double>(tree.reject_a()[done + k])) > 0x1p-17 * next_a) {
             __syncwarp();
             if (lane == 0) tree.reject_a()[done + k] = static_cast<float>(next_a);
             continue;
           }
+          const double next_n = static_cast<double>(t.over_p[k]) * inv_np - next_a * (static_cast<double>(t.over_q[k]) * inv_nq);
+          // (a token on the wrong side takes less than 2^-14 of its p from the sum: more than 2^-25 of it all?)
+          if (!kExactBorder && near > 0x1p-11f * static_cast<float>(next_n) * p44) {
+            border = true;
+            const Scale c = Scale::from(next_a * static_cast<double>(t.p) * inv_nq);
+            if (lane == 0) {
+              sm.ex.scale_m = c.m;
+              sm.ex.scale_s = c.s;
+            }
+            continue;
+          }
           a = next_a;
           gone += __shfl_sync(kFullMask, weight, k);
           z = t.q > gone ? static_cast<double>(t.q - gone) * inv_nq : 0.;
-          n = static_cast<double>(t.over_p[k]) * inv_np - a * (static_cast<double>(t.over_q[k]) * inv_nq);
-          if (!(n > 0x1p-40)) n = 0.;  // (nothing but rounding)
+          n = next_n > 0x1p-40 ? next_n : 0.;  // (below: nothing but rounding)
           at = k + 1;
         }
         __syncwarp();
         if (lane == 0) {
+          sm.near[par ^ 1] = 0;
           sm.ex.A = a;
           sm.ex.N = n;
           sm.ex.Z = z;
@@ -1055,6 +1090,7 @@ struct Node {
       }
       if (lane == 0) {
         sm.ex.level = levels == 0 ? 0 : at - 1;
+        sm.ex.border = border;
         sm.ex.p = t.p;
         sm.ex.q = t.q;
       }
@@ -1072,6 +1108,7 @@ struct Node {
       sm.ex.gone = 0;
       sm.ex.settled = 0;
       sm.ex.level = -1;
+      sm.ex.border = 0;
     }
     __syncthreads();
     exact = true;
@@ -1091,7 +1128,8 @@ struct Node {
     bool totals = !n->exact && n->tried == 0;
     n->begin_exact();
     for (int done = n->sm.ex.settled; done < n->tried || totals; done = n->sm.ex.settled) {
-      n->exact_pass(n->tried - done > 1 ? kLevels : 1, done);
+      if (n->sm.ex.border) n->template exact_pass<true>(1, done);
+      else n->exact_pass(n->tried - done > 1 ? kLevels : 1, done);
       totals = false;
     }
   }
@@ -1157,7 +1195,7 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
   set_temperature(wq, Td);
   for (int i = tid; i < (1 << kExpBits); i += kThr)
     sm.exp[i] = make_float2(__ldg(g_exp.v + 2 * i), __ldg(g_exp.v + 2 * i + 1));
-  if (tid == 0) sm.cls_n = sm.list_n = 0;
+  if (tid == 0) sm.cls_n = sm.list_n = 0, sm.near[0] = sm.near[1] = 0;
   const int n = max(0, min(p.n_out[r], p.B));
   for (int i = tid; i < n; i += kThr) {
     tree.parent()[i] = p.parent ? p.parent[static_cast<size_t>(r) * p.B + i] : i - 1;
@@ -1387,6 +1425,7 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
       }
       node.exact_pass(more > 1 ? kLevels : more, done);
       if (!with_q) break;
+      if (sm.ex.border) node.settle();
     }
     // the warp in whose share the running sum passes the mark; behind all of
     // them, the last that has any
@@ -1404,7 +1443,7 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
         if (w < gn) {
           const Sums& x = sm.slot[from][w].sums;
           mine[k] = x.over_p[level];
-          if (with_q) mine[k] -= sc.of_sum(x.over_q[level], mine[k]);
+          if (with_q) mine[k] -= sc.of(x.over_q[level], mine[k]);
         }
         sum += mine[k];
       }
@@ -1461,7 +1500,8 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
         const float x = logit<E>(prow, i);
         if (!node.kept(x, i)) return 0ull;
         const float y = with_q ? logit<F>(qrow, i) : -INFINITY;
-        if (with_q && !(wp.log2w(x) - wq.log2w(y) > lc)) return 0ull;
+        // (at the border in whole numbers, whatever the pass took it for)
+        if (with_q && wp.log2w(x) - wq.log2w(y) < lc - 2.f * kBorder) return 0ull;
         const unsigned long long v = weigh_p(x);
         return with_q ? v - sc.of(weigh_q(y), v) : v;
       };
@@ -1485,7 +1525,8 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
         if (w == warp) upto += all;
         all += sm.part[w];
       }
-      if (t >= all) t = all ? all - 1 : 0;  // (the mark lies behind the share by its rounding)
+      // (the share's sum is above 0, so one of its tokens is; the mark may lie behind them by rounding)
+      t = min(t, all - 1);
       auto emit = [&](int i, unsigned long long z) {
         p.bonus[r] = i;
         p.prob[r] = static_cast<float>(static_cast<double>(z) / sm.ex.total);
@@ -1509,16 +1550,6 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
           if (found && lane == __ffs(at) - 1) emit(i, z);
           run += __shfl_sync(kFullMask, sum, 31);
         }
-      }
-      if (all == 0 && warp == 0) {  // (the share's residual is nothing but rounding: the kept token with the largest p)
-        unsigned long long best = 0;
-        for (int i = lane; i < p.V; i += 32) {
-          const float x = logit<E>(prow, i);
-          if (node.kept(x, i)) best = max(best, key50(x, i));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(kFullMask, best, o));
-        if (lane == 0) emit((1 << kIdxBits) - 1 - static_cast<int>(best & ((1u << kIdxBits) - 1)), 0);
       }
     }
     break;

@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from tests import verify_ref as ref
 from tests.test_gpu_cache import host
 from tests.test_gpu_verify_draft import BF16, F32, check, run
 
@@ -62,3 +63,86 @@ def test_infinite_temperatures(V, types):
     check(par, tok, n, z, flat, u, out=out)
     out = run(par, tok, n, dev(np.where(gone, -np.inf, z), types[0]), dev(d, types[1]), u, T=inf)
     check(par, tok, n, flat, d, u, out=out)
+
+
+def agreeing(g, R, V, bits, rows):
+    """A target that is its draft but for one token x, whose weight under the draft
+    is 2^-bits of the largest.  (z, d, x, the draft's second)"""
+    z = np.repeat((g.standard_normal((R, 1, V)) * 2).astype(np.float32), rows, 1)
+    order = np.argsort(-z[:, 0], axis=1)
+    x, y = order[:, V // 2], order[:, 1]
+    for r in range(R):
+        z[r, :, x[r]] = z[r, 0].max() - np.float32(bits * LN2)
+    return z, z.copy(), x, y
+
+
+def undecided(R, V, bits):
+    """How many of R results may be undecided: a partial sum of a residual of N = 2^-bits
+    p_max or more is off by e = V 2^-43 (p_max + q_max) (1 + A) / N <= V 2^(bits - 41), and V of
+    them have a mark within 2 e on either side."""
+    return int(R * min(1.0, 4 * V * V * 2.0 ** (bits - 41)))
+
+
+def second(z, x2, bits):
+    """The bits of N behind two rejections: p is q (1 + N) but for the first child, so
+    max(p - A q, 0) sums up to N q(x2), x2 the second."""
+    p = np.array([ref.softmax(row[0], 1.0)[x] / ref.softmax(row[0], 1.0).max() for row, x in zip(z, x2)])
+    return bits - float(np.log2(p.min()))
+
+
+AGREE = [(64, 12), (64, 16), (64, 19), (64, 22), (500, 12), (500, 15), (500, 18), (3000, 12), (3000, 14)]
+
+
+@pytest.mark.parametrize("V, bits", AGREE)
+@pytest.mark.parametrize("types", [(F32, F32), (F32, BF16)])
+def test_a_sibling_after_a_small_residual(V, bits, types):
+    """x is rejected and N = sum max(p - q, 0), half of q(x), is spread over all other
+    tokens in proportion: the next child's p - q is N q of it, accepted at any u
+    below about 1."""
+    g = np.random.default_rng(1000 * V + bits)
+    R = 100
+    z, d, x, y = agreeing(g, R, V, bits, 3)
+    if types[1] is BF16:
+        z, d = (torch.from_numpy(a).to(BF16).float().numpy() for a in (z, d))
+    for r in range(R):
+        z[r, :, x[r]] -= np.float32(0.75)
+    u = np.stack([g.random(R), np.full(R, 0.9), g.random(R)], 1).astype(np.float32)
+    out = check(np.full((R, 2), -1), np.stack([x, y], 1), np.full(R, 2), z, d, u, types=types, open_=undecided(R, V, bits))
+    assert (host(out["nodes"])[:, 0] == 1).mean() > 0.9
+
+
+@pytest.mark.parametrize("V, bits", AGREE + [(64, 24)])
+@pytest.mark.parametrize("child", [1, 2])
+def test_a_draw_from_a_small_residual(V, bits, child):
+    """The target cannot say x, the only drafted token: its own is drawn from the other
+    tokens in proportion to p.  With a second child that it cannot say either, from
+    what is left behind two rejections."""
+    g = np.random.default_rng(2000 * V + 10 * bits + child)
+    R = 100
+    z, d, x, y = agreeing(g, R, V, bits, 3)
+    tok = np.stack([x, np.argsort(-z[:, 0], axis=1)[:, V // 2 + 1]], 1)
+    for r in range(R):
+        z[r, :, tok[r, :child]] = -np.inf
+    u = np.stack([g.random(R), g.random(R), g.random(R)], 1).astype(np.float32)
+    if child == 2:
+        bits = second(d, tok[:, 1], bits)
+    check(np.full((R, 2), -1), tok, np.full(R, child), z, d, u, open_=undecided(R, V, bits))
+
+
+@pytest.mark.parametrize("V", [12, 300, 20011])
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16)])
+def test_two_logits_changed_places(V, types):
+    """The target has the draft's logits with those of x and y exchanged: p = A q for
+    all other tokens, exactly, and nothing but y is left behind a rejected x."""
+    g = np.random.default_rng(V)
+    R = 30
+    d = torch.from_numpy((g.standard_normal((R, 1, V)) * 2).astype(np.float32)).to(types[0]).float().numpy().repeat(2, 1)
+    z, x, y = d.copy(), np.zeros(R, int), np.zeros(R, int)
+    for r in range(R):
+        order = np.argsort(-d[r, 0])
+        x[r], y[r] = order[g.integers(0, 3)], order[g.integers(3, min(V, 40))]
+        z[r, :, x[r]], z[r, :, y[r]] = d[r, 0, y[r]], d[r, 0, x[r]]
+    u = np.stack([g.random(R), np.full(R, 1 - 2.0 ** -24)], 1).astype(np.float32)
+    out = check(np.full((R, 1), -1), x[:, None], np.ones(R, int), z, d, u, types=types)
+    rejected = host(out["len"]) == 0
+    assert rejected.sum() > R // 2 and (host(out["bonus"])[rejected] == y[rejected]).all()
