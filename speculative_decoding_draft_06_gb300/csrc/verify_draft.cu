@@ -64,8 +64,10 @@ constexpr int kNotes = 256;           // tokens that a warp notes in a scan
 constexpr int kFew = 512;            // tokens of a list on which top-k is decided by comparing all
 constexpr float kBorder = 0x1p-14f;  // what log2 p - log2 A q may be off by: two logarithms below 46, three
                                      // roundings each, 2^-15.9; A by 2^-17 and the rows' sums by 2^-18, 2^-15.5
-constexpr float kSumError = 0x1p-16f;  // relative error of a sum in fp32 (logits' differences times
-                                       // log2(e) / T below 46: 2^-19 each; the additions' 2^-18)
+constexpr float kSumError = 0x1p-15f;  // relative error of a sum in fp32: a lane's 130 additions one after the
+                                       // other (2^18 tokens, one CTA) 2^-17; logits' differences times log2(e) / T
+                                       // below 46, three roundings, 2^-17.4; 128 new largest logits, each an ex2
+                                       // (2^-22) for half of the sum, 2^-16
 
 // A warp's sums of a pass, in units of 2^-44 of the rows' largest weights: p and
 // q over all tokens, and over those with p > A_k q.
@@ -513,8 +515,8 @@ __device__ __noinline__ void list_cut(const S& given, const Weights& its_wp, con
 }
 
 // ceil(p (z + rest)), at least 1, for z and a mass that is known in fp32 only (in units of the largest
-// weight; its terms' arguments are off by 2^-19 each, its sum by 2^-18 of itself):
-// the least and the largest that it may be.
+// weight; off by 2^-17.4 for its terms' arguments and 2^-17 for a lane's 140 additions, together below
+// 2^-16): the least and the largest that it may be.
 __device__ __forceinline__ void share_between(float p, unsigned long long z, float rest, int tokens,
                                               unsigned long long* lo, unsigned long long* hi) {
   if (!(p > 0.f)) {
@@ -817,13 +819,13 @@ struct Node {
     return A > 0.f ? __log2f(A) + __log2f(near_p()) - __log2f(near_q()) : -INFINITY;
   }
 
-  // f(p's logit, q's, index) for the warp's tokens
+  // f(p's logit, q's, index, place in its unit) for the warp's tokens
   template <bool kQ, typename G>
   __device__ __forceinline__ void each_pair(G f) const {
     constexpr int kPer = Row<E>::kPer;
     const int lane = threadIdx.x & 31;
     const bool wide = (reinterpret_cast<uintptr_t>(qrow + row.head) & (sizeof(F) < sizeof(E) ? 7 : 15)) == 0;
-    auto one = [&](int i) { f(logit<E>(row.src, i), kQ ? logit<F>(qrow, i) : -INFINITY, i); };
+    auto one = [&](int i) { f(logit<E>(row.src, i), kQ ? logit<F>(qrow, i) : -INFINITY, i, 0); };
     if (gw == 0 && lane < row.head) one(lane);
     const int rest = row.index(row.units);
     if (gw == gn - 1 && lane < row.V - rest) one(rest + lane);
@@ -850,25 +852,26 @@ struct Node {
         if constexpr (kQ) load_logits<F, kPer>(qrow, row.index(a), wide, y);
       }
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) f(fmaxf(x[k], -INFINITY), z[k], i + k);
+      for (int k = 0; k < kPer; ++k) f(fmaxf(x[k], -INFINITY), z[k], i + k, k);
     }
   }
 
-  // sum max(p - A q, 0) in fp32, in units of p's largest weight
+  // sum max(p - A q, 0) in fp32, in units of p's largest weight (four sums a lane)
   __device__ __forceinline__ float near_pass(float A) {
     const int lane = threadIdx.x & 31;
-    float sum = 0.f;
+    float part[4] = {0.f, 0.f, 0.f, 0.f};
     if (A > 0.f) {
       const float lc = log2_c(A);
-      each_pair<true>([&](float x, float y, int i) {
+      each_pair<true>([&](float x, float y, int i, int k) {
         const float a = wp.log2w(x), b = wq.log2w(y) + lc;
-        if (kept(x, i)) sum += fmaxf(ex2(a) - ex2(b), 0.f);
+        if (kept(x, i)) part[k & 3] += fmaxf(ex2(a) - ex2(b), 0.f);
       });
     } else {
-      each_pair<false>([&](float x, float, int i) {
-        if (kept(x, i)) sum += ex2(wp.log2w(x));
+      each_pair<false>([&](float x, float, int i, int k) {
+        if (kept(x, i)) part[k & 3] += ex2(wp.log2w(x));
       });
     }
+    float sum = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
     if (lane < cl) at_rank(&sm, lane)->slot[par][gw].stats = make_float4(sum, 0.f, 0.f, 0.f);
@@ -890,7 +893,7 @@ struct Node {
     const int lane = threadIdx.x & 31;
     const float yx = wp.log2w(xp);
     float s0 = 0.f, s1 = 0.f, s2 = 0.f;
-    each_pair<false>([&](float x, float, int i) {
+    each_pair<false>([&](float x, float, int i, int) {
       const float y = wp.log2w(x), w = ex2(y);
       s0 += x > xp || (x == xp && i < xi) ? w : 0.f;
       s1 += y >= yx - 4.f ? w : 0.f;
@@ -918,6 +921,7 @@ struct Node {
       s2 += __shfl_xor_sync(kFullMask, s2, o);
     }
     par ^= 1;
+    // (512 additions a lane, 2^-15, and the arguments: below 2 kSumError)
     constexpr float kLow = 1.f - 4.f * kSumError, kHigh = 1.f + 4.f * kSumError;
     const float target = top_p * sum_p, below = target * kLow, w = ex2(yx);
     const float last = s2 < below ? w * (1.f / 256.f) : s1 < below ? w * (1.f / 16.f) : w;
@@ -941,7 +945,7 @@ struct Node {
     const Weigh<F, Weights> weigh_q(wq, sm.table_q);
     t = Sums{};
     float near = 0.f;
-    each_pair<(kMost > 0)>([&](float x, float y, int i) {
+    each_pair<(kMost > 0)>([&](float x, float y, int i, int) {
       const unsigned long long v = kept(x, i) ? weigh_p(x) : 0ull;
       t.p += v;
       if constexpr (kMost > 0) {

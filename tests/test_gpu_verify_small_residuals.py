@@ -146,3 +146,38 @@ def test_two_logits_changed_places(V, types):
     out = check(np.full((R, 1), -1), x[:, None], np.ones(R, int), z, d, u, types=types)
     rejected = host(out["len"]) == 0
     assert rejected.sum() > R // 2 and (host(out["bonus"])[rejected] == y[rejected]).all()
+
+
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16)])
+def test_one_large_logit_per_thread_and_a_flat_tail(types):
+    """More requests than share a row between CTAs, at the largest vocabulary: a thread
+    sums 512 tokens, a large one and 511 below half a unit of its last place.  The
+    second child's u lies around what p, q and N = sum max(p - q, 0) accept, down
+    to 2^-20 of it."""
+    R, V = 160, 1 << 18
+    g = np.random.default_rng(1)
+    z = np.full(V, np.float32(-24.25 * LN2), np.float32)
+    first = (np.arange(16)[:, None] * (V // 16) + np.arange(32)[None, :] * (4 if types[0] is F32 else 8)).ravel()
+    z[first] = 0.0
+    d = np.full(V, np.float32(-18 * LN2), np.float32)
+    x, y = int(first[77]), int(first[300])
+    z[x] = -20.0                     # the draft's likeliest, hardly the target's
+    d[x], d[y] = 0.0, -6.4
+    z, d = (torch.from_numpy(a).to(BF16).float().numpy() for a in (z, d))
+    p, q = ref.target(z, 1.0, 0, 1.0, 0.0), ref.softmax(d, 1.0)
+    N, Z = np.maximum(p - q, 0.0).sum(), 1.0 - q[x]
+    edge = (p[y] - q[y]) / (N / Z * q[y])
+    assert 0.3 < edge < 0.9
+    off = np.concatenate([2.0 ** -np.arange(8, 21), -2.0 ** -np.arange(8, 21)])
+    u = np.zeros((R, 3), np.float32)
+    u[:, 1] = 0.9
+    u[:, 2] = edge * (1 + np.resize(off, R))
+    u[:, 0] = g.random(R)
+    # (one request's three rows, the same for all requests)
+    rows = [torch.from_numpy(np.tile(a, (1, 3, 1))).to(t).cuda().expand(R, 3, V) for a, t in ((z, types[0]), (d, types[1]))]
+    par, tok, n = np.full((R, 2), -1), np.tile([x, y], (R, 1)), np.full(R, 2)
+    out = run(par, tok, n, rows[0], rows[1], u)
+    accepted = host(out["nodes"])[:, 0] == 1
+    want = u[:, 2].astype(np.float64) * (N / Z) * q[y] < p[y] - q[y]
+    assert (accepted == want).all(), np.flatnonzero(accepted != want)
+    assert want.any() and not want.all()
