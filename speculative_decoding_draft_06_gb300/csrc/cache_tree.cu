@@ -315,12 +315,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
     tc_fence_after();
     tmem_base = *tmem_slot;
   };
-  // a row's node, and its query head in the group (a row is less than 256 behind
-  // q0: the quotient is exact in fp32 for smaller groups, 0 or 1 for larger ones)
-  const int node0 = q0 / p.g, rem0 = q0 - node0 * p.g;
+  // a row's node, and its query head in the group: by the distance t of the row from
+  // the end of the node that q0 belongs to (-g to 254: floor((t + 1/2) / g) is exact in
+  // fp32, where from t >= 0 on a quotient is one of small numbers)
+  const int node0 = q0 / p.g + 1, rem0 = q0 - node0 * p.g;
   const float inv_g = 1.f / static_cast<float>(p.g);
   auto node_of = [&](int row, int* head) {
-    const int t = rem0 + row, n = p.g >= 256 ? t >= p.g : static_cast<int>((static_cast<float>(t) + 0.5f) * inv_g);
+    const int t = rem0 + row, n = __float2int_rd((static_cast<float>(t) + 0.5f) * inv_g);
     *head = t - n * p.g;
     return node0 + n;
   };
