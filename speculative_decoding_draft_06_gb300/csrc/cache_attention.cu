@@ -100,7 +100,7 @@ __device__ __forceinline__ void attend_rows(const CacheAttnParams& p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x, hk = blockIdx.y, r = blockIdx.z;
   Span sp;
-  if (kWin && threadIdx.x == 0 && split == 0 && hk == 0 && !p.tail && span_flag<kWin>(p, r))
+  if (kWin && threadIdx.x == 0 && split == 0 && hk == 0 && !p.tail && window_flag(p, r))
     atomicOr(p.err, DT_ERR_BAD_INDEX);
   if (!request_span<kWin>(p, r, &sp)) return;
   // rows q0 .. q0 + live - 1

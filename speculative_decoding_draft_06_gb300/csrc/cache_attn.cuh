@@ -61,7 +61,7 @@ __device__ __forceinline__ bool request_span(const CacheAttnParams& p, int r, Sp
       row0 = p.start[r];
       const long long end = p.start[r + 1];
       // (rows that the buffers do not have, or behind B: skipped, and flagged by
-      // span_flag)
+      // window_flag)
       if (row0 < 0 || end > p.q_rows) return false;
       n = min(n, end - row0 - 1);
     }
@@ -81,22 +81,17 @@ __device__ __forceinline__ bool request_span(const CacheAttnParams& p, int r, Sp
   return true;
 }
 
-// What a request is flagged for: tokens behind max_len; with a window also rows
-// that its packed ones name and the buffers do not have, or behind B.
-template <bool kWin>
-__device__ __forceinline__ bool span_flag(const CacheAttnParams& p, int r) {
+// What a request is flagged for in the forms with a window: tokens behind max_len,
+// rows that its packed ones name and the buffers do not have, or behind B.
+__device__ __forceinline__ bool window_flag(const CacheAttnParams& p, int r) {
   const long long len = p.lens[r];
-  if constexpr (kWin) {
-    long long n = p.n_nodes ? min(p.n_nodes[r], p.B) : p.B;
-    if (p.start) {
-      const long long row0 = p.start[r], end = p.start[r + 1];
-      if (row0 < 0 || end < row0 || end > p.q_rows || end - row0 - 1 > p.B) return true;
-      n = end - row0 - 1;
-    }
-    return len >= 0 && len + p.offset >= -1 && n >= 0 && len + p.offset + 1 + n > p.max_len;
+  long long n = p.n_nodes ? min(p.n_nodes[r], p.B) : p.B;
+  if (p.start) {
+    const long long row0 = p.start[r], end = p.start[r + 1];
+    if (row0 < 0 || end < row0 || end > p.q_rows || end - row0 - 1 > p.B) return true;
+    n = end - row0 - 1;
   }
-  const int n = p.n_nodes ? min(p.n_nodes[r], p.B) : p.B;
-  return len + n > p.max_len;
+  return len >= 0 && len + p.offset >= -1 && n >= 0 && len + p.offset + 1 + n > p.max_len;
 }
 
 // The rows behind a request's whole tiles of 128 that are the few-rows
@@ -273,8 +268,8 @@ __device__ __forceinline__ float* cache_part_row(const CacheAttnParams& p, int r
   return p.part + (tile * p.tile_rows + row) * (p.c.dh + kPartHead);
 }
 
-// The tensor-core kernel of many rows (cache_tree.cu; with a window
-// cache_window_tree.cu).
+// The tensor-core kernel of many rows (cache_tree.cu; with a window the same file,
+// compiled with DT_WINDOW).
 cudaError_t launch_cache_tree(const CacheAttnParams& p, cudaStream_t st);
 cudaError_t launch_cache_window_tree(const CacheAttnParams& p, cudaStream_t st);
 

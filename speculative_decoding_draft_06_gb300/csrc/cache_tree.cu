@@ -37,9 +37,9 @@
 // (31); first loads ahead of the set-up barrier 70, whole rows staged as bf16 68.
 // With a window a row tile begins at the first tile that one of its rows sees,
 // and only tiles that reach past the end of a range or the start of a window
-// compare positions: prompts of 2 x 4096 tokens behind a window of 2048 540 us, 890
-// TFLOP/s of the pairs that are seen, 190 us behind a window of 1 (the CTAs' fixed
-// cost: 30 thousand cycles each).  A polynomial for part of the exponentials and row tiles that take
+// compare positions: two prompts, of 8192 tokens and of 6144 to 8192, behind a window
+// of 2048 552 us, 810 TFLOP/s of the pairs that are seen, 190 us behind a window of 1
+// (the CTAs' fixed cost: 30 thousand cycles each).  A polynomial for part of the exponentials and row tiles that take
 // turns were slower (no figures kept).
 #include <type_traits>
 
@@ -204,9 +204,9 @@ __device__ __forceinline__ uint32_t row_sees(int pos, int Lp, const uint32_t* mr
 }
 
 // With a window: which of the 32 keys from position pos on a row at position
-// `at` sees (ls: keys before it that it may see at most: all up to itself in a
-// chain, the prefix in a tree, whose nodes are named by its mask row, and
-// counted one by one if any may lie outside the window).
+// `at` sees (in a chain all up to itself, in a tree the prefix and the nodes that
+// its mask row names, whose depths are looked at one by one if any may lie outside
+// the window).
 __device__ __forceinline__ uint32_t window_sees(const CacheAttnParams& p, const Span& sp, int r, int pos, int at,
                                                 const uint32_t* mrow) {
   const int end = p.chain ? at + 1 : sp.Lp;
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   }
   const int r = sorted ? s_r : blockIdx.z;
   Span sp;
-  if (kWin && threadIdx.x == 0 && split == 0 && hk == 0 && mt == 0 && span_flag<kWin>(p, r))
+  if (kWin && threadIdx.x == 0 && split == 0 && hk == 0 && mt == 0 && window_flag(p, r))
     atomicOr(p.err, DT_ERR_BAD_INDEX);
   if (!request_span<kWin>(p, r, &sp)) return;
   const int q0 = mt * kTreeRowsCta;
