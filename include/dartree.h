@@ -708,13 +708,16 @@ dartree_status dartree_sample(const void *logits, int32_t bf16, int64_t row_stri
 /* Verification of drafted tokens that were drawn from a drafter's distribution:
  * which of them the target accepts, and a token of its own behind them.  The
  * result is distributed as the target's own tokens (dartree_sample's) whatever
- * the drafter's distribution is.  (Of tokens that were not drawn, a top-k's, take
- * dartree_sample's for pred of dartree_accept.)
+ * the drafter's distribution is.  (dartree_sample draws one token of a row; siblings are
+ * drawn one after the other, with the logits of those before at -inf.  Of tokens that
+ * were not drawn, a top-k's or dartree_build's, take dartree_sample's for pred of
+ * dartree_accept.)
  *   parent, token [R][B], n_out [R]  the drafted trees, parents first; parent
  *        NULL: chains, node i the child of node i - 1;
  *   logits  the target's, row 0 behind the root, row i + 1 behind node i: row i of
  *        request r at element r req_stride + i row_stride, fp32 or bf16 (`bf16`);
- *   draft  the drafter's logits, laid out alike with strides and type of its own:
+ *   draft  the drafter's logits (-inf where a drafter with cuts of its own left a token
+ *        out), laid out alike with strides and type of its own:
  *        from row i's distribution the children of row i were drawn, one after the
  *        other without replacement, in the order of their numbers.  draft_rows: a
  *        request's rows (B are enough for chains; a row behind them has no

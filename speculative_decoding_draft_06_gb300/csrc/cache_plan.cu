@@ -13,10 +13,11 @@
 //      the row their rank falls in;
 //   5. ok, starts and, for few tokens, the maps (many: a launch of their own).
 // Bound by latency: each step is a few dependent reads and a barrier of the
-// cluster.  32 rows of 65 tokens at 9000 in pages of 16 behind a window: 14 us on
-// the GPU (a caller takes 20 to 25 us to launch it, five outputs' allocations among
-// them); 1024 rows with prompts of 2000 tokens among them, maps of 265 thousand: 27
-// us, 8 of them the maps' launch.
+// cluster.  32 rows of 65 tokens at 9000 in pages of 16 behind a window: 14.3 us on
+// the GPU with the release before it that makes the pages be taken again, 7.7 where
+// all are held (a caller takes 20 to 25 us to launch it, five outputs' allocations
+// among them); 1024 rows with prompts of 2000 tokens among them, maps of 265 thousand:
+// 26.8 and 17.5 us, 8 of them the maps' launch.
 #include "cache_pages.cuh"
 
 namespace dt {

@@ -38,7 +38,7 @@
 // With a window a row tile begins at the first tile that one of its rows sees,
 // and only tiles that reach past the end of a range or the start of a window
 // compare positions: two prompts, of 8192 tokens and of 6144 to 8192, behind a window
-// of 2048 552 us, 810 TFLOP/s of the pairs that are seen, 190 us behind a window of 1
+// of 2048 552 us, about 800 TFLOP/s of the pairs that are seen, 190 us behind a window of 1
 // (the CTAs' fixed cost: 30 thousand cycles each).  A polynomial for part of the exponentials and row tiles that take
 // turns were slower (no figures kept).
 #include <type_traits>
@@ -254,11 +254,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_cache_tree(const CacheAttnP
   pdl_wait();
   pdl_trigger();  // (the launch of the rows left over may fill the SMs that come free)
   __shared__ int s_r;
-  // The longest first: 8 trees of 1025 rows over up to 16000 keys, 8 heads to each of
-  // 8, by their lengths 2147 to 3240 us, as they come 2160 to 3405.  With a window not
+  // The longest first: 8 trees of 1025 rows over up to 16000 keys, 64 heads over
+  // 8, by their lengths 2145 to 3240 us, as they come 2160 to 3405.  With a window not
   // where a request has CTAs for every SM: packed rows have up to 30 empty CTAs there
   // to one with work, which all rank the requests (one request of 2001 rows among 33:
-  // 328 us, 359 ranked; 8 unequal prompts without a window gain 2% to 6% by it).
+  // 320 us, 350 ranked; 8 unequal prompts without a window gain 2% to 6% by it).
   const bool sorted = p.R > 1 && p.R <= kTreeSorted && (!kWin || gridDim.x * gridDim.y < 152);
   if (sorted) {  // the z-th longest request
     for (int a = threadIdx.x; a < p.R; a += kTreeThreads) {

@@ -186,16 +186,6 @@ __device__ __forceinline__ unsigned long long fraction64(float x) {
   return up >= 0 ? m << up : up > -24 ? m >> -up : 0ull;
 }
 
-// w / z to fp32, for w <= z: both as sums of two floats (49 bits or more), the
-// quotient of the upper ones corrected once.  (An fp64 division: 0.7 us.)
-__device__ __forceinline__ float share_of(unsigned long long w, unsigned long long z) {
-  const float wh = __ull2float_rn(w), zh = __ull2float_rn(z);
-  const float wl = __ll2float_rn(static_cast<long long>(w - __float2ull_rn(wh)));
-  const float zl = __ll2float_rn(static_cast<long long>(z - __float2ull_rn(zh)));
-  const float q = __fdiv_rn(wh, zh);
-  return q + __fdiv_rn(fmaf(-q, zh, wh) + fmaf(-q, zl, wl), zh);
-}
-
 // ceil(p z) for p in (0, 1) (fp32) and z < 2^63, at least 1.
 __device__ __forceinline__ unsigned long long ceil_share(float p, unsigned long long z) {
   const unsigned long long f = fraction64(p) >> 1;
@@ -243,16 +233,6 @@ __device__ __forceinline__ void unpack<uint16_t>(uint4 v, float (&x)[8]) {
     x[2 * k] = __uint_as_float(w[k] << 16);
     x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
   }
-}
-
-// The largest of a unit's logits (fmaxf drops NaN; all NaN: NaN, which no
-// comparison takes).
-template <int N>
-__device__ __forceinline__ float max_of(const float (&x)[N]) {
-  float m = x[0];
-#pragma unroll
-  for (int k = 1; k < N; ++k) m = fmaxf(m, x[k]);
-  return m;
 }
 
 // f(unit, its number) for the lane's units of a warp's [ub, ue), with a load
@@ -555,30 +535,6 @@ __device__ unsigned long long min_p_key(const W& wt, float mp) {
     hi = nhi < hi ? static_cast<unsigned>(nhi) : hi;
   }
   return static_cast<unsigned long long>(hi) << kIdxBits;
-}
-
-// floor(u total) for the draw, below total.
-__device__ __forceinline__ unsigned long long draw_mark(float u, unsigned long long total) {
-  unsigned long long t = 0;
-  if (u > 0.f)
-    t = u >= 1.f ? total : __umul64hi(fraction64(u), total);
-  return t < total ? t : total - 1;
-}
-
-// The row's classes: counts and masses of what is above `keep`.
-template <typename S, typename W>
-__device__ void fill_bins(const S& s, const W& wt, unsigned long long keep) {
-  clear_classes(s.sm);
-  __syncthreads();
-  s.each([&](float x, unsigned long long key) {
-    if (key < keep) return;
-    const unsigned long long w = wt.weight44(x);
-    if (w == 0) return;
-    const int b = bin_of(wt, x);
-    atomicAdd(&s.sm.count[b], 1u);
-    add_mass(s.sm, b, w);
-  });
-  s.sync();
 }
 
 // Count and mass over all classes (leader's block).

@@ -102,6 +102,50 @@ struct Smem {
 template <bool LIST, typename E>
 using Source = RowSource<LIST, E, Smem>;
 
+// w / z to fp32, for w <= z: both as sums of two floats (49 bits or more), the
+// quotient of the upper ones corrected once.  (An fp64 division: 0.7 us.)
+__device__ __forceinline__ float share_of(unsigned long long w, unsigned long long z) {
+  const float wh = __ull2float_rn(w), zh = __ull2float_rn(z);
+  const float wl = __ll2float_rn(static_cast<long long>(w - __float2ull_rn(wh)));
+  const float zl = __ll2float_rn(static_cast<long long>(z - __float2ull_rn(zh)));
+  const float q = __fdiv_rn(wh, zh);
+  return q + __fdiv_rn(fmaf(-q, zh, wh) + fmaf(-q, zl, wl), zh);
+}
+
+// The largest of a unit's logits (fmaxf drops NaN; all NaN: NaN, which no
+// comparison takes).
+template <int N>
+__device__ __forceinline__ float max_of(const float (&x)[N]) {
+  float m = x[0];
+#pragma unroll
+  for (int k = 1; k < N; ++k) m = fmaxf(m, x[k]);
+  return m;
+}
+
+// floor(u total) for the draw, below total.
+__device__ __forceinline__ unsigned long long draw_mark(float u, unsigned long long total) {
+  unsigned long long t = 0;
+  if (u > 0.f)
+    t = u >= 1.f ? total : __umul64hi(fraction64(u), total);
+  return t < total ? t : total - 1;
+}
+
+// The row's classes: counts and masses of what is above `keep`.
+template <typename S, typename W>
+__device__ void fill_bins(const S& s, const W& wt, unsigned long long keep) {
+  clear_classes(s.sm);
+  __syncthreads();
+  s.each([&](float x, unsigned long long key) {
+    if (key < keep) return;
+    const unsigned long long w = wt.weight44(x);
+    if (w == 0) return;
+    const int b = bin_of(wt, x);
+    atomicAdd(&s.sm.count[b], 1u);
+    add_mass(s.sm, b, w);
+  });
+  s.sync();
+}
+
 // f(logit, index, weight) for the row's logits that have a weight (and some
 // without), in no particular order; the classes' memory is used.  The weights of the codes that have
 // places come from a table (weight44 is some 70 instructions: 2064 rows of

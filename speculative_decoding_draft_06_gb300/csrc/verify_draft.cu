@@ -29,15 +29,16 @@
 // passes, barriers of the cluster and scalar steps, 4 us at the least; the pass in
 // whole numbers by issue and by its table's bank conflicts (two look-ups a token).
 // One chain of 8 over 32000 fp32 logits 30 to 38 us (by its path); 16 trees of 128 nodes
-// over 151936 in bf16 102 to 119 us, 64 chains of 7 with settings of their own 266 to
-// 320 us (both to the end of their longest paths; the rows of all paths read once would
+// over 151936 in bf16 101 to 117 us, 64 chains of 7 with settings of their own 268 to
+// 302 us (both to the end of their longest paths; the rows of all paths read once would
 // take 10 and 20 us).  Steps for the trees (the chains; by other draws than these):
 // every sum in whole numbers 210 us (837); tests in fp32, one pass in whole numbers per
 // path, its fp64 in one warp 147 (440, top-p); floors and lists for top-k, the pass at
 // the draw in line 137 (385); acceptance before the cut 140 (318); a node's state and
 // the cuts' arguments in registers, copies of them for the calls, 136 to 104 (301 to
 // 266).  The passes as calls cost 7%, two CTAs of 512 threads to an SM (64 registers) 20
-// to 40%, copies in registers inside the calls of a Node too 3 to 10%.
+// to 40%, copies in registers inside the calls of a Node too 3 to 10%.  The tokens at the
+// border p = A q in whole numbers cost 1%.
 #include "row_cuts.cuh"
 
 namespace dt {
@@ -317,7 +318,7 @@ struct Scale {
 };
 
 // floor(u z) for u in (0, 1), z below 2^63.
-__device__ __forceinline__ unsigned long long share_of(float u, unsigned long long z) {
+__device__ __forceinline__ unsigned long long floor_share(float u, unsigned long long z) {
   const unsigned bits = __float_as_uint(u);
   const int exponent = static_cast<int>(bits >> 23), down = 150 - max(exponent, 1);  // u = factor 2^-down
   const unsigned long long factor = (bits & 0x7FFFFFu) | (exponent ? 0x800000u : 0u);
@@ -1459,7 +1460,7 @@ __global__ void __launch_bounds__(kThr, 1) k_verify(const VerifyParams p) {
       }
       const unsigned long long total = __shfl_sync(kFullMask, inc, 31);
       const float u0 = tree.u()[0];
-      const unsigned long long mark = !(u0 > 0.f) ? 0ull : u0 < 1.f ? share_of(u0, total) : total;
+      const unsigned long long mark = !(u0 > 0.f) ? 0ull : u0 < 1.f ? floor_share(u0, total) : total;
       unsigned long long before = inc - sum, left = 0;
       int owner = -1, last = -1;
 #pragma unroll

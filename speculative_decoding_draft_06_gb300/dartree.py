@@ -975,8 +975,10 @@ def verify(parent: torch.Tensor | None, token: torch.Tensor, n_out: torch.Tensor
     (dartree_verify) -> {"len" [R], "nodes" [R, max_len], "bonus" [R], "prob" [R]},
     the first three as :func:`accept` gives them.  parent (None: chains), token [R, B],
     n_out [R]; the target's logits [R, B+1, V] and the drafter's, from which the
-    tokens were drawn, draft [R, B or B+1, V] (fp32 or bf16, dense in V); u [R,
-    B+1] in [0, 1): u[:, i+1] tests node i, u[:, 0] draws the last token."""
+    tokens were drawn, draft [R, B or B+1, V] (fp32 or bf16, dense in V; -inf where
+    the drafter's own cuts left a token out); u [R, B+1] in [0, 1): u[:, i+1] tests
+    node i, u[:, 0] draws the last token.  :func:`sample` draws a chain's tokens; a
+    tree's siblings one after the other, those before at -inf."""
     if not isinstance(token, torch.Tensor) or token.dim() != 2 or not token.is_cuda:
         raise TypeError("token must be a CUDA tensor [R, B]")
     R, B = token.shape
