@@ -29,8 +29,8 @@
 // passes, barriers of the cluster and scalar steps, 4 us at the least; the pass in
 // whole numbers by issue and by its table's bank conflicts (two look-ups a token).
 // One chain of 8 over 32000 fp32 logits 30 to 38 us (by its path); 16 trees of 128 nodes
-// over 151936 in bf16 101 to 117 us, 64 chains of 7 with settings of their own 268 to
-// 302 us (both to the end of their longest paths; the rows of all paths read once would
+// over 151936 in bf16 101 to 117 us, 64 chains of 7 with settings of their own 258 to
+// 351 us (both to the end of their longest paths; the rows of all paths read once would
 // take 10 and 20 us).  Steps for the trees (the chains; by other draws than these):
 // every sum in whole numbers 210 us (837); tests in fp32, one pass in whole numbers per
 // path, its fp64 in one warp 147 (440, top-p); floors and lists for top-k, the pass at
